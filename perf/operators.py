@@ -199,12 +199,11 @@ def _sequence_of(s):
 
 def _balance(s):
     B, E, K = s["seqs"], s["experts"], s["topk"]
-    seq = _sequence_of(s)
-    p = s["scores"] / s["scores"].sum(1, keepdim=True)
-    total = torch.zeros((B + 1, E), dtype=torch.float64, device="cuda").index_add_(0, seq, p.double())[:B]
-    counts = torch.zeros((B + 1) * E, dtype=torch.int32, device="cuda")
-    counts.index_add_(0, (seq[:, None] * E + s["ids"]).view(-1), torch.ones_like(s["ids"]).view(-1))
-    counts = counts.view(B + 1, E)[:B].contiguous()
+    at = torch.arange(B, device="cuda")[:, None]
+    member = (_sequence_of(s) == at).double()  # [B, T]: which tokens are a sequence's
+    total = member @ (s["scores"] / s["scores"].sum(1, keepdim=True)).double()
+    picks = torch.zeros_like(s["scores"]).scatter_add_(1, s["ids"].long(), torch.ones_like(s["ids"]).float())
+    counts = (member @ picks.double()).to(torch.int32)
     n = (s["off"][1:] - s["off"][:-1]).double()[:, None].clamp_min(1)
     prob = total / n
     loss = ALPHA * E * (counts / (K * n) * prob).sum(1)
