@@ -30,10 +30,17 @@ EXPORTED = ("beam_moe_workspace_bytes", "beam_moe_route_workspace_bytes", "beam_
             "beam_moe_route", "beam_moe_select", "beam_moe_dispatch",
             "beam_moe_forward", "beam_moe_forward_noalloc", "beam_moe_pack_weights", "beam_moe_forward_packed",
             "beam_moe_forward_fp8", "beam_moe_residual_forward",
-            "beam_moe_residual_forward_fp8", "beam_moe_stream_rows", "beam_moe_timing_enable",
+            "beam_moe_residual_forward_fp8", "beam_moe_layer_norm", "beam_moe_layer_norm_backward_workspace_bytes",
+            "beam_moe_layer_norm_backward", "beam_moe_balance_loss_workspace_bytes", "beam_moe_balance_loss",
+            "beam_moe_route_backward", "beam_moe_linear_workspace_bytes", "beam_moe_linear_backward_workspace_bytes",
+            "beam_moe_linear", "beam_moe_linear_backward", "beam_moe_stream_rows", "beam_moe_timing_enable",
             "beam_moe_timing_read", "beam_moe_stage_name", "beam_moe_status_str")
 
 SIZE_MAX = 2 ** 64 - 1
+
+BEAM_MOE_BF16, BEAM_MOE_F16, BEAM_MOE_F32 = 0, 1, 2
+ELEM_TYPES = {torch.bfloat16: BEAM_MOE_BF16, torch.float16: BEAM_MOE_F16, torch.float32: BEAM_MOE_F32}
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 
 
 class BeamMoeError(RuntimeError):
@@ -87,6 +94,23 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.beam_moe_residual_forward.restype = ctypes.c_int
     lib.beam_moe_residual_forward_fp8.argtypes = [pd, i32, vp, i32, vp, vp, ctypes.c_float] + [vp] * 16 + [sz, vp]
     lib.beam_moe_residual_forward_fp8.restype = ctypes.c_int
+    ci, i64, f32 = ctypes.c_int, ctypes.c_int64, ctypes.c_float
+    for fn, res, args in (
+            ("beam_moe_layer_norm", ci, [i32, i32, vp, ci, i64, vp, vp, f32, vp, ci, i64, vp, vp, vp]),
+            ("beam_moe_layer_norm_backward_workspace_bytes", sz, [i32, i32]),
+            ("beam_moe_layer_norm_backward", ci,
+             [i32, i32, vp, ci, i64, vp, ci, i64, vp, vp, vp, vp, i64, vp, vp, vp, sz, vp]),
+            ("beam_moe_balance_loss_workspace_bytes", sz, [pd, i32, i32]),
+            ("beam_moe_balance_loss", ci, [pd, i32, vp, vp, i32, vp, f32, vp, vp, vp, vp, sz, vp]),
+            ("beam_moe_route_backward", ci, [pd, i32, vp, vp, vp, i32, vp, f32, vp, vp, vp, vp]),
+            ("beam_moe_linear_workspace_bytes", sz, [i32, i32, i32, i64, i64]),
+            ("beam_moe_linear_backward_workspace_bytes", sz, [i32, i32, i32, i64, i64]),
+            ("beam_moe_linear", ci, [i32, i32, i32, ci, vp, i64, vp, i64, vp, ci, vp, i64, f32, f32, vp, ci, i64, vp,
+                                     i64, vp, sz, vp]),
+            ("beam_moe_linear_backward", ci, [i32, i32, i32, ci, vp, ci, i64, vp, i64, vp, i64, vp, i64, ci, f32, f32,
+                                              vp, i64, vp, i64, vp, vp, i64, vp, sz, vp])):
+        getattr(lib, fn).argtypes = args
+        getattr(lib, fn).restype = res
     lib.beam_moe_stream_rows.argtypes = [pd, i32, ctypes.c_int]
     lib.beam_moe_stream_rows.restype = ctypes.c_int
     lib.beam_moe_timing_enable.argtypes = [ctypes.c_int]
@@ -429,6 +453,257 @@ def beam_moe_residual_forward_fp8(dims: Dims, stream_in: torch.Tensor, step: int
         _ptr(w_up_fp8), _ptr(up_scale), _ptr(w_down_fp8), _ptr(down_scale), *_outputs(bufs, out), _stream(stream))
     _check(st, "beam_moe_residual_forward_fp8")
     return bufs
+
+
+# --------------------------------------------------------------------------
+# operators around the block: layer norm, the router's training side, linear
+# --------------------------------------------------------------------------
+class _On:
+    """Where a call runs: the tensors' device made current, and the given stream, or that device's
+    current one.  Outputs and workspaces allocated inside belong to that stream."""
+    __slots__ = ("dev", "stream", "ctx")
+
+    def __init__(self, dev: torch.device, stream):
+        self.dev, self.stream, self.ctx = dev, stream, None
+
+    def __enter__(self) -> int:
+        dev, stream = self.dev, self.stream
+        if stream is None:
+            if torch.cuda.current_device() != dev.index:
+                self.ctx = torch.cuda.device(dev)
+                self.ctx.__enter__()
+            return torch.cuda.current_stream().cuda_stream
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        elif stream.device != dev:
+            raise ValueError(f"the stream belongs to {stream.device}, the tensors to {dev}")
+        self.ctx = torch.cuda.stream(stream)
+        self.ctx.__enter__()
+        return stream.cuda_stream
+
+    def __exit__(self, *exc) -> None:
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _rows(t: torch.Tensor, name: str, dtypes, shape, dev) -> int:
+    """Checks a matrix whose rows may be strided; returns its row stride."""
+    if t.device != dev or not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor on {dev}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be one of {tuple(dtypes)}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    r, c = shape
+    ld, one = t.stride()
+    if c > 1 and one != 1:
+        raise ValueError(f"{name} must have consecutive columns")
+    if r > 1 and ld < c:
+        raise ValueError(f"{name} must have rows that do not overlap")
+    return ld if r > 1 and ld > c else c
+
+
+def _vec(t: Optional[torch.Tensor], name: str, dtype, shape, dev) -> Optional[int]:
+    """Checks an optional contiguous tensor; returns its address."""
+    if t is None:
+        return None
+    if t.device != dev or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _mat(t: torch.Tensor, name: str) -> tuple:
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix")
+    return t.shape[0], t.shape[1], t.device
+
+
+def _scratch(n: int, ws: Optional[torch.Tensor], dev, fn: str):
+    """(address, bytes, keeper) of a workspace of n bytes: the caller's, or a new one."""
+    if n == SIZE_MAX:
+        raise BeamMoeError(BEAM_MOE_ERR_UNSUPPORTED, fn)
+    if ws is None:
+        if n == 0:
+            return None, 0, None
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    elif ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous on {dev}")
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
+
+
+_FLOATS = tuple(ELEM_TYPES)
+_F32 = torch.float32
+
+
+def beam_moe_layer_norm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Optional[torch.Tensor] = None, *,
+                        eps: float = 1e-5, out_dtype: Optional[torch.dtype] = None,
+                        out: Optional[torch.Tensor] = None, want_stats: bool = True, stream=None):
+    """Layer norm of the rows of x [T, H] (bf16, fp16 or fp32; rows may be strided). Returns (y, mean, rstd):
+    y of out_dtype (default x's), mean and rstd [T] fp32 for the backward pass, or None without want_stats."""
+    T, H, dev = _mat(x, "x")
+    ldx = _rows(x, "x", _FLOATS, (T, H), dev)
+    g, b = _vec(gamma, "gamma", _F32, (H,), dev), _vec(beta, "beta", _F32, (H,), dev)
+    with _On(dev, stream) as st:
+        if out is None:
+            out = torch.empty((T, H), dtype=out_dtype or x.dtype, device=dev)
+        elif out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError("out is not of out_dtype")
+        ldy = _rows(out, "out", _FLOATS, (T, H), dev)
+        mean = torch.empty((T,), dtype=_F32, device=dev) if want_stats else None
+        rstd = torch.empty((T,), dtype=_F32, device=dev) if want_stats else None
+        _check(load_library().beam_moe_layer_norm(
+            T, H, x.data_ptr(), ELEM_TYPES[x.dtype], ldx, g, b, eps, out.data_ptr(), ELEM_TYPES[out.dtype], ldy,
+            mean.data_ptr() if want_stats else None, rstd.data_ptr() if want_stats else None, st),
+            "beam_moe_layer_norm")
+    return out, mean, rstd
+
+
+def beam_moe_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                                 gamma: Optional[torch.Tensor] = None, *, want_dx: bool = True,
+                                 want_params: bool = True, ws: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of beam_moe_layer_norm. Returns (dx of x's type, dgamma [H] fp32, dbeta [H] fp32); dx is None
+    without want_dx, the other two without want_params."""
+    T, H, dev = _mat(x, "x")
+    ldx, lddy = _rows(x, "x", _FLOATS, (T, H), dev), _rows(dy, "dy", _FLOATS, (T, H), dev)
+    m, r = _vec(mean, "mean", _F32, (T,), dev), _vec(rstd, "rstd", _F32, (T,), dev)
+    g = _vec(gamma, "gamma", _F32, (H,), dev)
+    lib = load_library()
+    with _On(dev, stream) as st:
+        dx = torch.empty((T, H), dtype=x.dtype, device=dev) if want_dx else None
+        dg = torch.empty((H,), dtype=_F32, device=dev) if want_params else None
+        db = torch.empty((H,), dtype=_F32, device=dev) if want_params else None
+        need = lib.beam_moe_layer_norm_backward_workspace_bytes(T, H) if want_params else 0
+        wp, wn, _keep = _scratch(need, ws, dev, "beam_moe_layer_norm_backward")
+        _check(lib.beam_moe_layer_norm_backward(
+            T, H, dy.data_ptr(), ELEM_TYPES[dy.dtype], lddy, x.data_ptr(), ELEM_TYPES[x.dtype], ldx, m, r, g,
+            dx.data_ptr() if want_dx else None, H, dg.data_ptr() if want_params else None,
+            db.data_ptr() if want_params else None, wp, wn, st), "beam_moe_layer_norm_backward")
+    return dx, dg, db
+
+
+def _routed(dims: Dims, scores: torch.Tensor, topk_ids: torch.Tensor, seq_offsets: Optional[torch.Tensor]):
+    T, E, dev = _mat(scores, "scores")
+    if not scores.is_cuda:
+        raise ValueError("scores must be a device tensor")
+    s = _vec(scores, "scores", _F32, (T, dims.num_experts), dev)
+    i = _vec(topk_ids, "topk_ids", torch.int32, (T, dims.topk), dev)
+    B = 1
+    if seq_offsets is not None:
+        B = seq_offsets.numel() - 1
+        if B < 1:
+            raise ValueError("seq_offsets must hold at least two offsets")
+    return T, E, dev, s, i, B, _vec(seq_offsets, "seq_offsets", torch.int32, (B + 1,), dev)
+
+
+def beam_moe_balance_loss(dims: Dims, scores: torch.Tensor, topk_ids: torch.Tensor, *, alpha: float,
+                          seq_offsets: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None):
+    """Load-balance loss and per-expert counts of each packed sequence (one sequence without seq_offsets
+    [B+1] int32). Returns (loss [B] fp32, counts [B,E] int32, prob [B,E] fp32)."""
+    T, E, dev, s, i, B, off = _routed(dims, scores, topk_ids, seq_offsets)
+    lib, cd = load_library(), _cdims(dims)
+    with _On(dev, stream) as st:
+        loss = torch.empty((B,), dtype=_F32, device=dev)
+        counts = torch.empty((B, E), dtype=torch.int32, device=dev)
+        prob = torch.empty((B, E), dtype=_F32, device=dev)
+        wp, wn, _keep = _scratch(lib.beam_moe_balance_loss_workspace_bytes(ctypes.byref(cd), T, B), ws, dev,
+                                 "beam_moe_balance_loss")
+        _check(lib.beam_moe_balance_loss(ctypes.byref(cd), T, s, i, B, off, alpha, loss.data_ptr(), counts.data_ptr(),
+                                         prob.data_ptr(), wp, wn, st), "beam_moe_balance_loss")
+    return loss, counts, prob
+
+
+def beam_moe_route_backward(dims: Dims, scores: torch.Tensor, topk_ids: torch.Tensor, *,
+                            dw: Optional[torch.Tensor] = None, dloss: Optional[torch.Tensor] = None,
+                            counts: Optional[torch.Tensor] = None, alpha: float = 0.0,
+                            seq_offsets: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Gradient with respect to the router's logits, [T,E] fp32, of the routing weights (given dw [T,K]) and of
+    beam_moe_balance_loss (given dloss [B] and its counts, alpha and seq_offsets)."""
+    T, E, dev, s, i, B, off = _routed(dims, scores, topk_ids, seq_offsets)
+    d = _vec(dw, "dw", _F32, (T, dims.topk), dev)
+    dl, c = _vec(dloss, "dloss", _F32, (B,), dev), _vec(counts, "counts", torch.int32, (B, E), dev)
+    cd = _cdims(dims)
+    with _On(dev, stream) as st:
+        out = torch.empty((T, E), dtype=_F32, device=dev)
+        if T == 0 and (dw is not None or dloss is not None):
+            return out
+        _check(load_library().beam_moe_route_backward(ctypes.byref(cd), T, s, i, d, B, off, alpha, dl, c,
+                                                      out.data_ptr(), st), "beam_moe_route_backward")
+    return out
+
+
+_HALF = (torch.bfloat16, torch.float16)
+
+
+def _act(act: str) -> int:
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {tuple(ACTIVATIONS)}, got {act!r}")
+    return ACTIVATIONS[act]
+
+
+def beam_moe_linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None, *, act: str = "none",
+                    residual: Optional[torch.Tensor] = None, keep: float = 1.0, add: float = 1.0,
+                    out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None,
+                    want_pre: bool = False, ws: Optional[torch.Tensor] = None, stream=None):
+    """y = keep * residual + add * act(x w^T + bias) for x [M, K], w [N, K] in bf16 or fp16 (rows may be strided),
+    bias [N] fp32. y is of out_dtype (x's type, or fp32), as residual is; out may be residual itself. Returns y,
+    or (y, pre) with want_pre: pre [M, N] of x's type is what the backward pass reads."""
+    M, K, dev = _mat(x, "x")
+    N = _mat(w, "w")[0]
+    ldx, ldw = _rows(x, "x", _HALF, (M, K), dev), _rows(w, "w", (x.dtype,), (N, K), dev)
+    b, a = _vec(bias, "bias", _F32, (N,), dev), _act(act)
+    lib = load_library()
+    with _On(dev, stream) as st:
+        if out is None:
+            out = torch.empty((M, N), dtype=out_dtype or x.dtype, device=dev)
+        elif out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError("out is not of out_dtype")
+        ldy = _rows(out, "out", (x.dtype, _F32), (M, N), dev)
+        ldr = 0 if residual is None else _rows(residual, "residual", (out.dtype,), (M, N), dev)
+        pre = torch.empty((M, N), dtype=x.dtype, device=dev) if want_pre else None
+        wp, wn, _keep = _scratch(lib.beam_moe_linear_workspace_bytes(M, N, K, ldx, ldw), ws, dev, "beam_moe_linear")
+        _check(lib.beam_moe_linear(
+            M, N, K, ELEM_TYPES[x.dtype], x.data_ptr(), ldx, w.data_ptr(), ldw, b, a,
+            None if residual is None else residual.data_ptr(), ldr, keep, add, out.data_ptr(), ELEM_TYPES[out.dtype],
+            ldy, pre.data_ptr() if want_pre else None, N, wp, wn, st), "beam_moe_linear")
+    return (out, pre) if want_pre else out
+
+
+def beam_moe_linear_backward(dy: torch.Tensor, x: Optional[torch.Tensor], w: Optional[torch.Tensor],
+                             pre: Optional[torch.Tensor] = None, *, act: str = "none", keep: float = 1.0,
+                             add: float = 1.0, want_dx: bool = True, want_dw: bool = True, want_dbias: bool = True,
+                             want_dres: bool = False, ws: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of beam_moe_linear from dy [M, N] (x's type or fp32) and, with an activation, pre. Returns
+    (dx, dw, dbias), with want_dres (dx, dw, dbias, dres); those not wanted are None. x may be None without
+    want_dw, w without want_dx; one of them is needed for the type."""
+    M, N, dev = _mat(dy, "dy")
+    if x is None and w is None or want_dw and x is None or want_dx and w is None:
+        raise ValueError("x is needed for dw, w for dx, and one of them for the type")
+    K, dt = (x if x is not None else w).shape[-1], (x if x is not None else w).dtype
+    ldx = K if x is None else _rows(x, "x", _HALF, (M, K), dev)
+    ldw = K if w is None else _rows(w, "w", (dt,) if dt in _HALF else _HALF, (N, K), dev)
+    lddy = _rows(dy, "dy", (dt, _F32), (M, N), dev)
+    a = _act(act)
+    ldp = N
+    if a:
+        if pre is None:
+            raise ValueError("pre is needed with an activation")
+        ldp = _rows(pre, "pre", (dt,), (M, N), dev)
+    lib = load_library()
+    with _On(dev, stream) as st:
+        dx = torch.empty((M, K), dtype=dt, device=dev) if want_dx else None
+        dw = torch.empty((N, K), dtype=dt, device=dev) if want_dw else None
+        db = torch.empty((N,), dtype=_F32, device=dev) if want_dbias else None
+        dres = torch.empty((M, N), dtype=dy.dtype, device=dev) if want_dres else None
+        wp, wn, _keep = _scratch(lib.beam_moe_linear_backward_workspace_bytes(M, N, K, ldx, ldw), ws, dev,
+                                 "beam_moe_linear_backward")
+        _check(lib.beam_moe_linear_backward(
+            M, N, K, ELEM_TYPES[dt], dy.data_ptr(), ELEM_TYPES[dy.dtype], lddy, None if x is None else x.data_ptr(),
+            ldx, None if w is None else w.data_ptr(), ldw, pre.data_ptr() if a else None, ldp, a, keep, add,
+            dx.data_ptr() if want_dx else None, K, dw.data_ptr() if want_dw else None, K,
+            db.data_ptr() if want_dbias else None, dres.data_ptr() if want_dres else None, N, wp, wn, st),
+            "beam_moe_linear_backward")
+    return (dx, dw, db, dres) if want_dres else (dx, dw, db)
 
 
 # --------------------------------------------------------------------------

@@ -8,9 +8,10 @@
 #include <array>
 #include <cmath>
 #include <cstdint>
-#include <initializer_list>
 #include <mutex>
 #include <vector>
+
+#include "abi_util.h"
 
 namespace beam {
 struct Tile;
@@ -65,11 +66,14 @@ hipError_t launch_down_grouped(const uint16_t* h, const uint8_t* hscale, const i
 
 namespace {
 
-constexpr size_t kAlign = 256;
+using beam::align_up;
+using beam::aligned16;
+using beam::at;
+using beam::check_ptrs;
+using beam::hip_status;
+
 constexpr int kTileBytes = 32;          // sizeof(beam::Tile)
 constexpr int64_t kMaxPairs = 1 << 28;  // T * K limit
-
-size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
 bool dims_ok(const beam_moe_dims* d) {
   if (!d) return false;
@@ -174,13 +178,6 @@ void make_plan(const beam_moe_dims* d, int T, Plan* p, bool fp8 = false) {
 size_t route_ws_bytes(const Plan& p) { return (size_t)p.splits * p.T * p.E * sizeof(float); }
 size_t dispatch_ws_bytes(const Plan& p) { return (size_t)p.units * p.E * sizeof(int32_t); }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-template <typename Tp>
-Tp* at(void* ws, size_t off) {
-  return reinterpret_cast<Tp*>(static_cast<char*>(ws) + off);
-}
-
 int check_common(const beam_moe_dims* d, int32_t T) {
   if (!d) return BEAM_MOE_ERR_INVALID_ARG;
   if (!dims_ok(d)) return BEAM_MOE_ERR_UNSUPPORTED;
@@ -188,14 +185,6 @@ int check_common(const beam_moe_dims* d, int32_t T) {
   if ((int64_t)T * d->topk > kMaxPairs) return BEAM_MOE_ERR_UNSUPPORTED;
   return BEAM_MOE_OK;
 }
-
-int check_ptrs(std::initializer_list<const void*> ptrs) {
-  for (const void* p : ptrs)
-    if (!p || !aligned16(p)) return BEAM_MOE_ERR_INVALID_ARG;
-  return BEAM_MOE_OK;
-}
-
-int hip_status(hipError_t e) { return e == hipSuccess ? BEAM_MOE_OK : BEAM_MOE_ERR_HIP; }
 
 // ---------------------------------------------------------------------------
 // stage timing (diagnostics)
@@ -418,6 +407,8 @@ int forward_bf16(const beam_moe_dims* d, const Plan& p, const void* x_bf16, cons
 }
 
 }  // namespace
+
+int beam::check_block(const beam_moe_dims* d, int32_t T) { return check_common(d, T); }
 
 // ---------------------------------------------------------------------------
 // scratch of beam_moe_forward_noalloc

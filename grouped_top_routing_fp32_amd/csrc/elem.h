@@ -1,0 +1,73 @@
+// Element types of the operators around the block (layer norm, linear and their
+// backward passes): storage, loads and stores of 1 or 8 consecutive elements as
+// FP32, and wave reductions.
+#pragma once
+
+#include "common.h"
+
+namespace beam {
+
+// Values of the ABI's element type arguments (BEAM_MOE_BF16, _F16, _F32).
+enum ElemType { kElemBF16 = 0, kElemF16 = 1, kElemF32 = 2 };
+
+// Stores round once, to nearest even, in the hardware converters (NaN stays NaN).
+struct BF16 {
+  using S = uint16_t;
+  __device__ static float up(S v) { return __uint_as_float((uint32_t)v << 16); }
+  __device__ static S down(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
+};
+struct F16 {
+  using S = uint16_t;
+  __device__ static float up(S v) { return (float)__builtin_bit_cast(_Float16, v); }
+  __device__ static S down(float f) { return __builtin_bit_cast(uint16_t, (_Float16)f); }
+};
+struct F32 {
+  using S = float;
+  __device__ static float up(S v) { return v; }
+  __device__ static S down(float f) { return f; }
+};
+
+// N = 1, or 8 elements from an address aligned to 16 bytes.
+template <class T, int N>
+__device__ __forceinline__ void load_n(const typename T::S* p, float* v) {
+  if constexpr (N == 1) {
+    v[0] = T::up(*p);
+  } else if constexpr (sizeof(typename T::S) == 4) {
+    const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      v[q] = a[q];
+      v[q + 4] = b[q];
+    }
+  } else {
+    const u32x4 r = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      v[2 * q] = T::up((uint16_t)(r[q] & 0xFFFFu));
+      v[2 * q + 1] = T::up((uint16_t)(r[q] >> 16));
+    }
+  }
+}
+
+template <class T, int N>
+__device__ __forceinline__ void store_n(typename T::S* p, const float* v) {
+  if constexpr (N == 1) {
+    *p = T::down(v[0]);
+  } else if constexpr (sizeof(typename T::S) == 4) {
+    *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<f32x4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+  } else {
+    u32x4 r;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) r[q] = T::down(v[2 * q]) | ((uint32_t)T::down(v[2 * q + 1]) << 16);
+    *reinterpret_cast<u32x4*>(p) = r;
+  }
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);
+  return v;
+}
+
+}  // namespace beam

@@ -1,0 +1,329 @@
+// Layer norm and its backward pass (gfx950).
+//
+//   y  = (x - mean) rstd gamma + beta,  mean = sum x / H,  rstd = 1 / sqrt(sum (x - mean)^2 / H + eps)
+//   with xh = (x - mean) rstd and g = dy gamma:
+//   dx = rstd (g - sum g / H - xh sum(g xh) / H),  dgamma = sum_t dy xh,  dbeta = sum_t dy
+//
+// Both are bound by HBM: a row is read once and kept in registers between its
+// sums and its result.  A row belongs to a team of `team` threads (whole waves;
+// one wave per row up to 512 columns, several such rows in a workgroup); thread
+// i of it holds chunks i, i + team, ... of VEC consecutive columns.
+#include <initializer_list>
+#include <type_traits>
+
+#include "elem.h"
+
+namespace beam {
+
+constexpr int kLnMaxThreads = 1024;
+constexpr int kLnMaxWaves = kLnMaxThreads / 64;
+
+// Forward.  Statistics: each wave takes the mean of its own columns, then the sum
+// of squares about it (two passes over registers), and the waves' means and
+// squares are joined about the common mean in FP64, in wave order: one barrier,
+// and a mean far from zero cancels nothing.
+template <class XT, class YT, int VEC, int NCH>
+__global__ __launch_bounds__(kLnMaxThreads) void layer_norm_kernel(
+    const typename XT::S* __restrict__ x, int64_t ldx, const float* __restrict__ gamma,
+    const float* __restrict__ beta, typename YT::S* __restrict__ y, int64_t ldy, float* __restrict__ mean_out,
+    float* __restrict__ rstd_out, int T, int H, float eps) {
+  __shared__ double smean[kLnMaxWaves], sm2[kLnMaxWaves];
+  const int tid = threadIdx.x, team = blockDim.x, wave = tid >> 6, nw = team >> 6;
+  const int t = blockIdx.x * blockDim.y + threadIdx.y;
+  if (t >= T) return;  // blockDim.y > 1 only for one-wave teams, which meet no barrier
+  const int nch = H / VEC;
+  const typename XT::S* xr = x + (int64_t)t * ldx;
+  float v[NCH][VEC];
+  float s = 0.f;
+#pragma unroll
+  for (int c = 0; c < NCH; ++c) {
+    const int ch = tid + c * team;
+    if (ch < nch) {
+      load_n<XT, VEC>(xr + (int64_t)ch * VEC, v[c]);
+#pragma unroll
+      for (int q = 0; q < VEC; ++q) s += v[c][q];
+    }
+  }
+  auto wave_cols = [&](int w) {
+    int n = 0;
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) n += min(64, max(0, nch - (c * team + 64 * w)));
+    return n * VEC;
+  };
+  const int n = wave_cols(wave);
+  const float m = n ? wave_sum(s) / n : 0.f;
+  float r = 0.f, q2 = 0.f;
+#pragma unroll
+  for (int c = 0; c < NCH; ++c)
+    if (tid + c * team < nch) {
+#pragma unroll
+      for (int q = 0; q < VEC; ++q) {
+        const float d = v[c][q] - m;
+        r += d;
+        q2 += d * d;
+      }
+    }
+  r = wave_sum(r);
+  q2 = wave_sum(q2);
+  // m is rounded: the rest r / n belongs to the mean, and r^2 / n off the squares
+  double mean = n ? (double)m + (double)r / n : 0.0;
+  double m2 = n ? (double)q2 - (double)r * r / n : 0.0;
+  if (nw > 1) {
+    if ((tid & 63) == 0) {
+      smean[wave] = mean;
+      sm2[wave] = m2;
+    }
+    __syncthreads();
+    mean = 0.0;
+    m2 = 0.0;
+    for (int w = 0; w < nw; ++w) mean += smean[w] * wave_cols(w);
+    mean /= H;
+    for (int w = 0; w < nw; ++w) {
+      const double d = smean[w] - mean;
+      m2 += sm2[w] + d * d * wave_cols(w);
+    }
+  }
+  const float rs = 1.f / sqrtf((float)(m2 / H) + eps);
+  const float mh = (float)mean, ml = (float)(mean - (double)mh);
+  if (tid == 0) {
+    if (mean_out) mean_out[t] = mh;
+    if (rstd_out) rstd_out[t] = rs;
+  }
+  typename YT::S* yr = y + (int64_t)t * ldy;
+#pragma unroll
+  for (int c = 0; c < NCH; ++c) {
+    const int ch = tid + c * team;
+    if (ch < nch) {
+      float g[VEC], b[VEC], o[VEC];
+      if (gamma) load_n<F32, VEC>(gamma + ch * VEC, g);
+      if (beta) load_n<F32, VEC>(beta + ch * VEC, b);
+#pragma unroll
+      for (int q = 0; q < VEC; ++q) {
+        o[q] = ((v[c][q] - mh) - ml) * rs;
+        if (gamma) o[q] *= g[q];
+        if (beta) o[q] += b[q];
+      }
+      store_n<YT, VEC>(yr + (int64_t)ch * VEC, o);
+    }
+  }
+}
+
+// Backward.  Unit u (one team) takes rows u, u + units, ...; a thread's columns
+// stay the same from row to row, so it sums their dgamma and dbeta in registers
+// and writes them once, as row u of part [2][units][H], which
+// column_sums_kernel adds up: no atomics, so the sums' order is fixed.
+template <class DT, class XT, int VEC, int NCH>
+__global__ __launch_bounds__(kLnMaxThreads) void layer_norm_backward_kernel(
+    const typename DT::S* __restrict__ dy, int64_t lddy, const typename XT::S* __restrict__ x, int64_t ldx,
+    const float* __restrict__ mean, const float* __restrict__ rstd, const float* __restrict__ gamma,
+    typename XT::S* __restrict__ dx, int64_t lddx, float* __restrict__ part, int T, int H, int units) {
+  __shared__ float red[2][kLnMaxWaves][2];
+  const int tid = threadIdx.x, team = blockDim.x, wave = tid >> 6, nw = team >> 6;
+  const int unit = blockIdx.x * blockDim.y + threadIdx.y;
+  if (unit >= units) return;
+  const int nch = H / VEC;
+  float g[NCH][VEC], dg[NCH][VEC], db[NCH][VEC];
+#pragma unroll
+  for (int c = 0; c < NCH; ++c) {
+#pragma unroll
+    for (int q = 0; q < VEC; ++q) {
+      g[c][q] = 1.f;
+      dg[c][q] = db[c][q] = 0.f;
+    }
+    if (gamma && tid + c * team < nch) load_n<F32, VEC>(gamma + (tid + c * team) * VEC, g[c]);
+  }
+  int buf = 0;
+  for (int t = unit; t < T; t += units, buf ^= 1) {
+    const float mu = mean[t], rs = rstd[t];
+    float xh[NCH][VEC], gy[NCH][VEC];
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+      const int ch = tid + c * team;
+      if (ch < nch) {
+        load_n<XT, VEC>(x + (int64_t)t * ldx + (int64_t)ch * VEC, xh[c]);
+        load_n<DT, VEC>(dy + (int64_t)t * lddy + (int64_t)ch * VEC, gy[c]);
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) {
+          xh[c][q] = (xh[c][q] - mu) * rs;
+          dg[c][q] += gy[c][q] * xh[c][q];
+          db[c][q] += gy[c][q];
+          gy[c][q] *= g[c][q];
+          s1 += gy[c][q];
+          s2 += gy[c][q] * xh[c][q];
+        }
+      }
+    }
+    s1 = wave_sum(s1);
+    s2 = wave_sum(s2);
+    if (nw > 1) {  // two buffers: the next row's sums do not wait for this row's readers
+      if ((tid & 63) == 0) {
+        red[buf][wave][0] = s1;
+        red[buf][wave][1] = s2;
+      }
+      __syncthreads();
+      s1 = s2 = 0.f;
+      for (int w = 0; w < nw; ++w) {
+        s1 += red[buf][w][0];
+        s2 += red[buf][w][1];
+      }
+    }
+    if (dx) {
+      const float c1 = s1 / H, c2 = s2 / H;
+#pragma unroll
+      for (int c = 0; c < NCH; ++c) {
+        const int ch = tid + c * team;
+        if (ch < nch) {
+          float o[VEC];
+#pragma unroll
+          for (int q = 0; q < VEC; ++q) o[q] = rs * (gy[c][q] - c1 - xh[c][q] * c2);
+          store_n<XT, VEC>(dx + (int64_t)t * lddx + (int64_t)ch * VEC, o);
+        }
+      }
+    }
+  }
+  if (part) {
+    float* pg = part + (int64_t)unit * H;
+    float* pb = part + ((int64_t)units + unit) * H;
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+      const int ch = tid + c * team;
+      if (ch < nch) {
+        store_n<F32, VEC>(pg + (int64_t)ch * VEC, dg[c]);
+        store_n<F32, VEC>(pb + (int64_t)ch * VEC, db[c]);
+      }
+    }
+  }
+}
+
+// out0[h] = sum_u part[0][u][h], out1[h] = sum_u part[1][u][h] (either may be null).
+// grid (ceil(H / 64), 2), block (64, 16): thread (c, g) adds rows g, g + 16, ...;
+// the 16 sums of a column are added in order, in FP64.
+__global__ __launch_bounds__(1024) void column_sums_kernel(const float* __restrict__ part, float* __restrict__ out0,
+                                                           float* __restrict__ out1, int units, int H) {
+  __shared__ float s[16][64];
+  float* out = blockIdx.y ? out1 : out0;
+  if (!out) return;
+  const float* p = part + (int64_t)blockIdx.y * units * H;
+  const int h = blockIdx.x * 64 + threadIdx.x;
+  float v = 0.f;
+  if (h < H)
+    for (int u = threadIdx.y; u < units; u += 16) v += p[(int64_t)u * H + h];
+  s[threadIdx.y][threadIdx.x] = v;
+  __syncthreads();
+  if (threadIdx.y == 0 && h < H) {
+    double a = 0.0;
+#pragma unroll
+    for (int g = 0; g < 16; ++g) a += s[g][threadIdx.x];
+    out[h] = (float)a;
+  }
+}
+
+hipError_t launch_column_sums(const float* part, float* out0, float* out1, int units, int H, hipStream_t st) {
+  hipLaunchKernelGGL(column_sums_kernel, dim3((H + 63) / 64, out1 ? 2 : 1), dim3(64, 16), 0, st, part, out0, out1,
+                     units, H);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// launch shapes
+// ---------------------------------------------------------------------------
+int layer_norm_max_cols() { return 16384; }
+
+namespace {
+
+// 8 columns to a chunk where every row of every operand starts on 16 bytes and
+// holds whole chunks, else 1.
+bool wide(int H, std::initializer_list<int64_t> lds) {
+  if (H % 8) return false;
+  for (int64_t ld : lds)
+    if (ld % 8) return false;
+  return true;
+}
+
+struct Shape {
+  int nch;   // chunks per thread
+  int team;  // threads per row
+  int rows;  // rows per workgroup (one-wave teams only)
+};
+
+Shape shape(int H, bool vec) {
+  const int chunks = vec ? H / 8 : H;
+  const int nch = vec ? (chunks <= 1024 ? 1 : 2) : (chunks <= 4096 ? 4 : 16);
+  Shape s;
+  s.nch = nch;
+  s.team = ((chunks + nch - 1) / nch + 63) / 64 * 64;
+  s.rows = s.team == 64 ? 4 : 1;
+  return s;
+}
+
+template <class F>
+hipError_t by_type(int type, F f) {
+  return type == kElemBF16 ? f(BF16{}) : type == kElemF16 ? f(F16{}) : f(F32{});
+}
+
+template <class F>
+hipError_t by_chunks(bool vec, int nch, F f) {
+  using std::integral_constant;
+  if (vec)
+    return nch == 1 ? f(integral_constant<int, 8>{}, integral_constant<int, 1>{})
+                    : f(integral_constant<int, 8>{}, integral_constant<int, 2>{});
+  return nch == 4 ? f(integral_constant<int, 1>{}, integral_constant<int, 4>{})
+                  : f(integral_constant<int, 1>{}, integral_constant<int, 16>{});
+}
+
+}  // namespace
+
+hipError_t launch_layer_norm(const void* x, int x_type, int64_t ldx, const float* gamma, const float* beta, void* y,
+                             int y_type, int64_t ldy, float* mean, float* rstd, int T, int H, float eps,
+                             hipStream_t st) {
+  const bool vec = wide(H, {ldx, ldy});
+  const Shape s = shape(H, vec);
+  return by_type(x_type, [&](auto xt) {
+    return by_type(y_type, [&](auto yt) {
+      return by_chunks(vec, s.nch, [&](auto v, auto n) {
+        using XT = decltype(xt);
+        using YT = decltype(yt);
+        hipLaunchKernelGGL((layer_norm_kernel<XT, YT, decltype(v)::value, decltype(n)::value>),
+                           dim3((T + s.rows - 1) / s.rows), dim3(s.team, s.rows), 0, st,
+                           static_cast<const typename XT::S*>(x), ldx, gamma, beta, static_cast<typename YT::S*>(y),
+                           ldy, mean, rstd, T, H, eps);
+        return hipGetLastError();
+      });
+    });
+  });
+}
+
+// Rows of partial column sums the backward kernel writes.
+int layer_norm_backward_units(int T, int H) {
+  (void)H;
+  return T < 512 ? T : 512;
+}
+
+hipError_t launch_layer_norm_backward(const void* dy, int dy_type, int64_t lddy, const void* x, int x_type,
+                                      int64_t ldx, const float* mean, const float* rstd, const float* gamma, void* dx,
+                                      int64_t lddx, float* dgamma, float* dbeta, float* part, int T, int H,
+                                      hipStream_t st) {
+  const bool vec = wide(H, {lddy, ldx, dx ? lddx : 0});
+  const Shape s = shape(H, vec);
+  const int units = layer_norm_backward_units(T, H);
+  const bool sums = dgamma || dbeta;
+  hipError_t e = by_type(dy_type, [&](auto dt) {
+    return by_type(x_type, [&](auto xt) {
+      return by_chunks(vec, s.nch, [&](auto v, auto n) {
+        using DT = decltype(dt);
+        using XT = decltype(xt);
+        hipLaunchKernelGGL((layer_norm_backward_kernel<DT, XT, decltype(v)::value, decltype(n)::value>),
+                           dim3((units + s.rows - 1) / s.rows), dim3(s.team, s.rows), 0, st,
+                           static_cast<const typename DT::S*>(dy), lddy, static_cast<const typename XT::S*>(x), ldx,
+                           mean, rstd, gamma, static_cast<typename XT::S*>(dx), lddx, sums ? part : nullptr, T, H,
+                           units);
+        return hipGetLastError();
+      });
+    });
+  });
+  if (e != hipSuccess || !sums) return e;
+  return launch_column_sums(part, dgamma, dbeta, units, H, st);
+}
+
+}  // namespace beam

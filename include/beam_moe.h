@@ -304,6 +304,146 @@ const char* beam_moe_stage_name(int32_t stage);
  * fp8 != 0 asks about beam_moe_forward_fp8. */
 int beam_moe_stream_rows(const beam_moe_dims* dims, int32_t T, int fp8);
 
+/* ---------------------------------------------------------------------------
+ * Operators around the block: what a training step of a sublayer, or one of
+ * the model's dense sublayers, needs next to it.  The conventions above hold;
+ * in addition
+ * - matrices are given with a row stride in elements (ld... >= the number of
+ *   columns), so a matrix may be the first columns of a wider buffer.  Any
+ *   strides and sizes work; the fastest kernels run where rows start on 16
+ *   bytes and hold whole groups of 8 elements;
+ * - element types are given as BEAM_MOE_BF16, _F16 or _F32;
+ * - every sum is held in FP32 or FP64 and every result is rounded once, to
+ *   nearest even, when it is stored;
+ * - infinities and NaN go through as the formulas send them: a row of layer
+ *   norm, a token of the router's gradient or a row of a product that holds
+ *   one does not touch the others (column sums hold all rows).
+ * ------------------------------------------------------------------------- */
+enum { BEAM_MOE_BF16 = 0, BEAM_MOE_F16 = 1, BEAM_MOE_F32 = 2 };
+enum {
+  BEAM_MOE_ACT_NONE = 0,
+  BEAM_MOE_ACT_RELU = 1, /* z < 0 ? 0 : z, slope 0 at 0 */
+  BEAM_MOE_ACT_SILU = 2, /* z / (1 + e^-z)              */
+  BEAM_MOE_ACT_GELU = 3  /* z (1 + erf(z / sqrt 2)) / 2 */
+};
+
+/* Layer norm of the rows of x [rows, cols]:
+ *   mean = sum x / cols,  rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps),
+ *   y = (x - mean) * rstd * gamma + beta
+ *   gamma, beta  [cols] fp32, NULL = ones, zeros
+ *   eps          >= 0, finite
+ *   y            [rows, cols] out, of any element type
+ *   mean, rstd   [rows] fp32 out, what the backward pass reads; NULL = not written
+ * 1 <= cols <= 16384, 0 <= rows <= 2^21 (0: nothing is written).  The statistics
+ * do not cancel where the mean is far from zero. */
+int beam_moe_layer_norm(int32_t rows, int32_t cols, const void* x, int x_type, int64_t ldx, const float* gamma,
+                        const float* beta, float eps, void* y, int y_type, int64_t ldy, float* mean, float* rstd,
+                        void* stream);
+
+/* Workspace of beam_moe_layer_norm_backward (partial column sums, at most
+ * 8 * 512 * cols bytes).  Returns SIZE_MAX for unsupported sizes. */
+size_t beam_moe_layer_norm_backward_workspace_bytes(int32_t rows, int32_t cols);
+
+/* Its gradients: with xh = (x - mean) * rstd and g = dy * gamma,
+ *   dx = rstd * (g - sum g / cols - xh * sum(g xh) / cols),
+ *   dgamma = sum over rows of dy * xh,  dbeta = sum over rows of dy
+ *   dy          [rows, cols] of any element type
+ *   mean, rstd  [rows] as beam_moe_layer_norm wrote them
+ *   gamma       as there
+ *   dx          [rows, cols] out, of x's type; NULL = not wanted
+ *   dgamma, dbeta  [cols] fp32 out, either may be NULL; zeros when rows = 0
+ *   ws          needed when dgamma or dbeta is wanted and rows > 0
+ * At least one output must be wanted. */
+int beam_moe_layer_norm_backward(int32_t rows, int32_t cols, const void* dy, int dy_type, int64_t lddy, const void* x,
+                                 int x_type, int64_t ldx, const float* mean, const float* rstd, const float* gamma,
+                                 void* dx, int64_t lddx, float* dgamma, float* dbeta, void* ws, size_t ws_bytes,
+                                 void* stream);
+
+/* Workspace of beam_moe_balance_loss (per-unit counts and sums; 0 up to 512
+ * tokens).  Returns SIZE_MAX for invalid or unsupported arguments. */
+size_t beam_moe_balance_loss_workspace_bytes(const beam_moe_dims* dims, int32_t T, int32_t num_seqs);
+
+/* Load-balance loss and per-expert counts of a routed batch, for each packed
+ * sequence b of n tokens, with p[t,e] = s[t,e] / sum_j s[t,j]:
+ *   counts[b,e] = slots of the sequence's tokens that chose e,
+ *   prob[b,e]   = mean over its tokens of p[t,e],
+ *   loss[b]     = alpha * sum_e (E * counts[b,e] / (K * n)) * prob[b,e]
+ *   scores       [T, E] fp32 post-sigmoid scores (beam_moe_route's scores_out)
+ *   topk_ids     [T, K] int32; a slot outside [0, E) (a dropped one) counts for no expert
+ *   num_seqs     B, 1 .. 2^20
+ *   seq_offsets  [B+1] int32 on the device, ascending, in [0, T]: sequence b holds the
+ *                tokens [seq_offsets[b], seq_offsets[b+1]), tokens outside are padding
+ *                and count for nothing; NULL = one sequence of all T tokens (B = 1).
+ *                Offsets that descend or lie outside leave the outputs undefined,
+ *                without faulting.
+ *   alpha        finite
+ *   loss [B] fp32 out;  counts [B, E] int32 out;  prob [B, E] fp32 out
+ * An empty sequence (n = 0; every one when T = 0) has loss, counts and prob 0.  A
+ * token whose scores sum to 0 adds nothing to prob. */
+int beam_moe_balance_loss(const beam_moe_dims* dims, int32_t T, const float* scores, const int32_t* topk_ids,
+                          int32_t num_seqs, const int32_t* seq_offsets, float alpha, float* loss, int32_t* counts,
+                          float* prob, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of the routing weights and of the balance loss with respect to the
+ * router's logits (the sigmoid's argument), in one pass; the choice of experts
+ * itself has no gradient:
+ *   w_k = routed_scaling * s_k / sum_j s_j over the K chosen experts, given dw;
+ *   loss[b] as in beam_moe_balance_loss, given dloss, its counts and its alpha;
+ *   dlogits[t,e] = (d/ds of both) * s * (1 - s)
+ *   scores, topk_ids, num_seqs, seq_offsets, alpha: as in beam_moe_balance_loss; a slot
+ *                outside [0, E) has no weight and no gradient, an id chosen twice adds twice
+ *   dw           [T, K] fp32, NULL = no gradient from the weights
+ *   dloss        [B] fp32, NULL = none from the loss (counts is then not read)
+ *   counts       [B, E] int32, needed with dloss
+ *   dlogits      [T, E] fp32 out; padding tokens have the weights' part alone
+ * At least one of dw and dloss must be given.  T <= 2^25. */
+int beam_moe_route_backward(const beam_moe_dims* dims, int32_t T, const float* scores, const int32_t* topk_ids,
+                            const float* dw, int32_t num_seqs, const int32_t* seq_offsets, float alpha,
+                            const float* dloss, const int32_t* counts, float* dlogits, void* stream);
+
+/* Workspace of beam_moe_linear and beam_moe_linear_backward; the leading
+ * dimensions are those of the call (the operands whose rows do not start on 16
+ * bytes or do not hold whole groups of 8 elements are laid out anew there).
+ * Return SIZE_MAX for unsupported sizes. */
+size_t beam_moe_linear_workspace_bytes(int32_t rows, int32_t cols, int32_t inner, int64_t ldx, int64_t ldw);
+size_t beam_moe_linear_backward_workspace_bytes(int32_t rows, int32_t cols, int32_t inner, int64_t ldx, int64_t ldw);
+
+/* A matrix product with bias, activation and residual in its epilogue:
+ *   z = x w^T + bias,  y = keep * res + add * act(z)
+ *   x      [rows, inner], w [cols, inner], both of `type` (BEAM_MOE_BF16 or _F16)
+ *   bias   [cols] fp32, NULL = none
+ *   act    BEAM_MOE_ACT_*
+ *   res    [rows, cols] of y_type, NULL = none (keep is then not used); with
+ *          keep = sqrt((k-1)/k), add = sqrt(1/k) this is the residual update of a
+ *          sublayer at step k
+ *   y      [rows, cols] out, of y_type: `type` or BEAM_MOE_F32; may be res itself
+ *          (in-place update, ldy = ldr)
+ *   pre    [rows, cols] out, of `type`: z, what the backward pass reads; NULL = not written
+ *   keep, add   finite
+ * Products are exact and summed in FP32.
+ * 0 <= rows <= 2^20, 1 <= cols, inner <= 2^18. */
+int beam_moe_linear(int32_t rows, int32_t cols, int32_t inner, int type, const void* x, int64_t ldx, const void* w,
+                    int64_t ldw, const float* bias, int act, const void* res, int64_t ldr, float keep, float add,
+                    void* y, int y_type, int64_t ldy, void* pre, int64_t ldpre, void* ws, size_t ws_bytes,
+                    void* stream);
+
+/* Its gradients:
+ *   dz = add * dy * act'(pre),  dx = dz w,  dw = dz^T x,
+ *   dbias = sum over rows of dz,  dres = keep * dy
+ *   dy     [rows, cols] of dy_type: `type` or BEAM_MOE_F32
+ *   pre    [rows, cols] of `type` as beam_moe_linear wrote it; not read (and may be NULL)
+ *          when act is BEAM_MOE_ACT_NONE
+ *   dx     [rows, inner] of `type`, dw [cols, inner] of `type`, dbias [cols] fp32,
+ *          dres [rows, cols] of dy_type: each NULL = not wanted, one at least wanted;
+ *          x is needed for dw and w for dx (else NULL)
+ * dz enters the two products rounded to `type` (dbias sums it unrounded).  When
+ * rows = 0, dw and dbias are zeros. */
+int beam_moe_linear_backward(int32_t rows, int32_t cols, int32_t inner, int type, const void* dy, int dy_type,
+                             int64_t lddy, const void* x, int64_t ldx, const void* w, int64_t ldw, const void* pre,
+                             int64_t ldpre, int act, float keep, float add, void* dx, int64_t lddx, void* dw,
+                             int64_t lddw, float* dbias, void* dres, int64_t lddres, void* ws, size_t ws_bytes,
+                             void* stream);
+
 /* Static string for a status code. */
 const char* beam_moe_status_str(int status);
 
