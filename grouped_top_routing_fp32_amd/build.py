@@ -19,7 +19,7 @@ BUILD_DIR = os.path.join(HERE, "_build")
 ARCH = "gfx950"
 
 SOURCES = ["route.hip", "dispatch.hip", "experts.hip", "grouped_gemm.hip", "residual.hip", "layer_norm.hip",
-           "balance.hip", "linear.hip", "abi.cpp", "ops_abi.cpp"]
+           "balance.hip", "linear.hip", "gemm_bf16.hip", "gemm_f16.hip", "abi.cpp", "ops_abi.cpp"]
 
 # Packed FP32 instructions (v_pk_*_f32) are kept out of every kernel.
 DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]

@@ -1,0 +1,10 @@
+// The tiled product on fp16 operands (gfx950).
+#include "gemm_tiles.h"
+
+namespace beam {
+
+hipError_t launch_gemm_f16(const GemmArgs& g, const GemmPlan& p, float* part, int64_t ldpart, hipStream_t st) {
+  return launch_gemm_tiles<true>(g, p, part, ldpart, st);
+}
+
+}  // namespace beam

@@ -1,0 +1,222 @@
+// The tiled MFMA product of linear.hip, instantiated once for each 16-bit type.
+#pragma once
+
+#include <type_traits>
+
+#include "linear.h"
+
+namespace beam {
+
+namespace {
+
+constexpr int kBK = 64;  // K per stage
+
+typedef __attribute__((address_space(3))) uint16_t lds_u16;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// Source of the chunks of an operand past its K, so that they add nothing.
+__device__ const u32x4 zero_chunk = {0u, 0u, 0u, 0u};
+
+// One operand's side of a tile: R rows of the output (M or N) by kBK of K per stage.
+//
+// K contiguous: LDS rows of 64 K (128 bytes), chunk c (8 elements) of row r at position
+// c ^ ((r >> 1) & 7), so the 16 rows of a fragment read cover all banks once; a copy of
+// 1 KB fills 8 rows from 128 contiguous bytes each.
+// Transposed (TR): LDS rows of one k, R elements.  A fragment needs 8 consecutive k of a
+// column; the transposing LDS read delivers 4 of them, taking 16 columns (32 bytes) of 4
+// rows per 16 lanes.  The 32-byte granule g of row k sits at g ^ ((k & 3) | (k >> 1 & 4)):
+// the 8 rows that 32 lanes read together fall on distinct banks.
+template <bool TR, int R, int NW>
+struct Side {
+  static constexpr int kCopies = R / 8 / NW;     // per wave and stage
+  static constexpr int kRowChunks = TR ? R / 8 : 8;
+  static constexpr int kCopyRows = 64 / kRowChunks;  // LDS rows per copy
+  const uint16_t* src[kCopies];
+  int64_t step;
+
+  static __device__ __forceinline__ int swz(int r) { return TR ? ((r & 3) | ((r >> 1) & 4)) << 1 : (r >> 1) & 7; }
+  // LDS row and source chunk of this lane in copy q
+  static __device__ __forceinline__ int row(int q, int wave, int lane) {
+    return (wave * kCopies + q) * kCopyRows + lane / kRowChunks;
+  }
+  static __device__ __forceinline__ int chunk(int r, int lane) { return (lane % kRowChunks) ^ swz(r); }
+
+  // Rows i0 .. i0 + R - 1 of ni; K from k0.  Rows past the end repeat the last one (K
+  // contiguous) or the last chunk of 8 (transposed): their results are never stored.
+  __device__ __forceinline__ void init(const void* base, int64_t ld, int i0, int ni, int k0, int wave, int lane) {
+#pragma unroll
+    for (int q = 0; q < kCopies; ++q) {
+      const int r = row(q, wave, lane), c = chunk(r, lane);
+      if constexpr (TR)
+        src[q] = static_cast<const uint16_t*>(base) + (int64_t)(k0 + r) * ld + min(i0 + 8 * c, (ni - 1) & ~7);
+      else
+        src[q] = static_cast<const uint16_t*>(base) + (int64_t)min(i0 + r, ni - 1) * ld + k0 + 8 * c;
+    }
+    step = TR ? kBK * ld : kBK;
+  }
+
+  // Copies a stage of which `left` K remain and moves on to the next.
+  __device__ __forceinline__ void issue(lds_u16* slot, int left, int wave, int lane) {
+#pragma unroll
+    for (int q = 0; q < kCopies; ++q) {
+      const void* p = src[q];
+      if (left < kBK) {  // uniform; the last stage alone
+        const int r = row(q, wave, lane);
+        if ((TR ? r : 8 * chunk(r, lane)) >= left) p = &zero_chunk;
+      }
+      lds_copy16(p, __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(slot + (wave * kCopies + q) * 512)));
+      src[q] += step;
+    }
+  }
+
+  // The 16 rows from `r0` (a multiple of 16) of K 32 s .. 32 s + 31: lane l holds row
+  // l % 16, K 8 (l / 16) .. + 7.
+  static __device__ __forceinline__ u32x4 frag(const lds_u16* slot, int r0, int s, int lane) {
+    const int l16 = lane & 15, g = lane >> 4;
+    if constexpr (TR) {
+      uint2 h[2];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int k = 32 * s + 8 * g + 4 * half + (l16 >> 2);
+        const int c = ((r0 >> 3) + ((lane & 3) >> 1)) ^ swz(k);
+        const lds_u16* p = slot + k * R + 8 * c + 4 * (lane & 1);
+        h[half] = __builtin_bit_cast(
+            uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p));
+      }
+      return u32x4{h[0].x, h[0].y, h[1].x, h[1].y};
+    } else {
+      return *(const __attribute__((address_space(3))) u32x4*)(slot + (r0 + l16) * 64 + (((4 * s + g) ^ swz(l16)) << 3));
+    }
+  }
+};
+
+// XCD-aware order: workgroup b runs on XCD b % 8; each XCD takes a contiguous range.
+__device__ __forceinline__ int xcd_lin(int b, int total) {
+  const int full = total & ~7;
+  return b >= full ? b : (b & 7) * (full >> 3) + (b >> 3);
+}
+
+}  // namespace
+
+// Tiles of BM x BN outputs, one workgroup each, WM x WN waves; grid tiles * splits.
+// Consecutive workgroups of an XCD take 8 row tiles of one column before the next, so
+// the 32 that run at once share both operands in its L2.
+// Two stages of both operands in LDS: the copies of stage t + 1 are requested at the
+// start of step t and waited for at its end; they are issued and waited for by hand
+// (the compiler's own tracking drains them at every loop head).
+// The mfma's first operand is B's: a lane then holds four consecutive columns of a row.
+template <bool HALF, bool AT, bool BT, int BM, int BN, int WM, int WN, bool EPI>
+__global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(GemmArgs g, int mt, int nt, int k_per_split,
+                                                            float* __restrict__ part, int64_t ldpart) {
+  constexpr int NW = WM * WN, FI = BM / WM / 16, FJ = BN / WN / 16;
+  constexpr int kSlot = (BM + BN) * kBK;
+  __shared__ __align__(1024) uint16_t ring[2 * kSlot];
+  lds_u16* lds = (lds_u16*)ring;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const int tiles = mt * nt;
+  const int lin = xcd_lin(blockIdx.x, gridDim.x);
+  const int split = lin / tiles, t = lin % tiles;
+  const int group = t / (8 * nt), in = t % (8 * nt), rows = min(8, mt - 8 * group);
+  const int m0 = (8 * group + in % rows) * BM, n0 = in / rows * BN;
+  const int k0 = split * k_per_split, k1 = min(g.K, k0 + k_per_split);
+
+  Side<AT, BM, NW> sa;
+  Side<BT, BN, NW> sb;
+  sa.init(g.a, g.lda, m0, g.M, k0, wave, lane);
+  sb.init(g.b, g.ldb, n0, g.N, k0, wave, lane);
+  f32x4 acc[FI][FJ] = {};
+  auto issue = [&](int slot, int left) {
+    sa.issue(lds + slot * kSlot, left, wave, lane);
+    sb.issue(lds + slot * kSlot + BM * kBK, left, wave, lane);
+  };
+  const int stages = (k1 - k0 + kBK - 1) / kBK;  // 0 when K is 0
+  if (stages > 0) issue(0, k1 - k0);
+  for (int st = 0; st < stages; ++st) {
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+    __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (st + 1 < stages) issue((st + 1) & 1, k1 - k0 - (st + 1) * kBK);
+    const lds_u16* A = lds + (st & 1) * kSlot;
+    const lds_u16* B = A + BM * kBK;
+    u32x4 fa[2][FI], fb[2][FJ];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+#pragma unroll
+      for (int j = 0; j < FJ; ++j) fb[s][j] = Side<BT, BN, NW>::frag(B, wn * (BN / WN) + 16 * j, s, lane);
+#pragma unroll
+      for (int i = 0; i < FI; ++i) fa[s][i] = Side<AT, BM, NW>::frag(A, wm * (BM / WM) + 16 * i, s, lane);
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int i = 0; i < FI; ++i)
+#pragma unroll
+        for (int j = 0; j < FJ; ++j) acc[i][j] = mfma<HALF>(fb[s][j], fa[s][i], acc[i][j]);
+  }
+
+  // Epilogue through LDS: FP32 sums in the ring (WM / kPasses wave rows at a time), then
+  // every wave takes whole rows of the tile, four columns to a lane, so memory sees full
+  // lines.  16-byte chunk c of row r sits at c ^ (r & 15): the 16 rows that a wave writes
+  // at once fall on distinct banks.
+  constexpr int kPasses = BM * BN * 4 / (2 * kSlot * 2), kPassRows = BM / kPasses;
+  static_assert(kPasses * 2 * kSlot * 2 == BM * BN * 4 && WM % kPasses == 0, "a pass fills the ring");
+  f32x4* sums = reinterpret_cast<f32x4*>(ring);
+  constexpr int kQuads = BN / 4, kRowsAtOnce = 64 * NW / kQuads;
+  const int qn = tid % kQuads, qr = tid / kQuads;
+  const int n = n0 + 4 * qn;
+  const bool wide = epilogue_wide(g);
+#pragma unroll
+  for (int pass = 0; pass < kPasses; ++pass) {
+    __syncthreads();  // everyone is done with the stages, or with the last pass
+    if (wm / (WM / kPasses) == pass) {
+#pragma unroll
+      for (int i = 0; i < FI; ++i)
+#pragma unroll
+        for (int j = 0; j < FJ; ++j) {
+          const int r = wm * (BM / WM) - pass * kPassRows + 16 * i + (lane & 15);
+          const int c = wn * (BN / WN) / 4 + 4 * j + (lane >> 4);
+          sums[r * kQuads + (c ^ (r & 15))] = acc[i][j];
+        }
+    }
+    __syncthreads();
+    const int mp = m0 + pass * kPassRows, rmax = n < g.N ? min(kPassRows, g.M - mp) : 0;
+    auto rows_of = [&](auto f) {
+#pragma unroll 4
+      for (int r = qr; r < rmax; r += kRowsAtOnce) f(mp + r, sums[r * kQuads + (qn ^ (r & 15))]);
+    };
+    if (part) {  // ldpart is a multiple of four and holds the columns past N
+      float* p = part + (int64_t)split * g.M * ldpart + n;
+      rows_of([&](int m, f32x4 v) { *reinterpret_cast<f32x4*>(p + (int64_t)m * ldpart) = v; });
+    } else if constexpr (EPI) {
+      by_act(g.act, [&](auto act) {
+        rows_of([&](int m, f32x4 v) { epilogue4<decltype(act)::value>(g, wide, m, n, v); });
+      });
+    } else {
+      rows_of([&](int m, f32x4 v) { epilogue4<kActNone>(g, wide, m, n, v); });
+    }
+  }
+}
+
+// Launches the tiles of g's layout (A transposed implies B transposed).
+template <bool HALF>
+hipError_t launch_gemm_tiles(const GemmArgs& g, const GemmPlan& p, float* part, int64_t ldpart, hipStream_t st) {
+  const int mt = (g.M + p.tile - 1) / p.tile, nt = (g.N + p.tile - 1) / p.tile;
+  const dim3 grid(mt * nt * p.splits);
+  auto go = [&](auto kernel, int threads) {
+    hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, st, g, mt, nt, p.k_per_split, part, ldpart);
+    return hipGetLastError();
+  };
+  if (p.tile == 256) {
+    if (!g.at && !g.bt) return go(gemm_kernel<HALF, false, false, 256, 256, 4, 2, true>, 512);
+    if (!g.at) return go(gemm_kernel<HALF, false, true, 256, 256, 4, 2, false>, 512);
+    return go(gemm_kernel<HALF, true, true, 256, 256, 4, 2, false>, 512);
+  }
+  if (!g.at && !g.bt) return go(gemm_kernel<HALF, false, false, 128, 128, 2, 2, true>, 256);
+  if (!g.at) return go(gemm_kernel<HALF, false, true, 128, 128, 2, 2, false>, 256);
+  return go(gemm_kernel<HALF, true, true, 128, 128, 2, 2, false>, 256);
+}
+
+}  // namespace beam

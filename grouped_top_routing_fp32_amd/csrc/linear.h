@@ -2,6 +2,8 @@
 // and its epilogue.
 #pragma once
 
+#include <type_traits>
+
 #include "elem.h"
 
 namespace beam {
@@ -10,8 +12,8 @@ namespace beam {
 enum Act { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3 };
 
 // out[m, n] = keep res[m, n] + add act(sum_k a(m, k) b(n, k) + bias[n]), pre[m, n] = the
-// activation's argument.  a(m, k) is at a + m * lda + k, or with at at a + k * lda + m;
-// b the same with n.  Types are ElemType; a, b and pre share one of two bytes.
+// activation's argument.  a(m, k) is at a + m * lda + k, or with at (A transposed) at
+// a + k * lda + m; b the same with n.  Types are ElemType; a, b and pre share one of two bytes.
 struct GemmArgs {
   const void* a;
   const void* b;
@@ -31,26 +33,56 @@ struct GemmArgs {
   int64_t ldp;
 };
 
-__device__ __forceinline__ float act_f32(float z, int act) {
-  switch (act) {
-    case kActRelu: return z < 0.f ? 0.f : z;  // NaN stays NaN
-    case kActSilu: return z / (1.f + expf(-z));
-    case kActGelu: return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
-    default: return z;
-  }
+// How a product runs: which kernel, and the workspace it needs (bytes from its start).
+struct GemmPlan {
+  enum Kind { kSkinny, kTiles } kind;
+  int tile;            // kTiles: 256 or 128, rows and columns of an output tile
+  int splits;          // of K; above 1 the partial sums go through the workspace
+  int k_per_split;     // multiple of 64
+  bool copy_a, copy_b; // the operand is laid out anew in the workspace
+  size_t off_a, off_b, off_part, total;
+};
+// Operand shapes and leading dimensions decide alone, so a size query and its call agree.
+// padded_a: A's rows are whole chunks of 8 elements (zeros past the end), whatever M and K are.
+GemmPlan plan_gemm(int M, int N, int K, bool at, bool bt, int64_t lda, int64_t ldb, bool padded_a = false);
+hipError_t launch_gemm(const GemmArgs& g, const GemmPlan& p, void* ws, hipStream_t st);
+hipError_t launch_gemm_bf16(const GemmArgs& g, const GemmPlan& p, float* part, int64_t ldpart, hipStream_t st);
+hipError_t launch_gemm_f16(const GemmArgs& g, const GemmPlan& p, float* part, int64_t ldpart, hipStream_t st);
+
+template <bool HALF>
+__device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+  return HALF ? mfma16x16x32_f16(a, b, c) : mfma16x16x32(a, b, c);
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_f32(float z) {
+  if constexpr (ACT == kActRelu) return z < 0.f ? 0.f : z;  // NaN stays NaN
+  if constexpr (ACT == kActSilu) return z / (1.f + expf(-z));
+  if constexpr (ACT == kActGelu) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+  return z;
 }
 
 // d act / dz
-__device__ __forceinline__ float act_slope_f32(float z, int act) {
+template <int ACT>
+__device__ __forceinline__ float act_slope_f32(float z) {
+  if constexpr (ACT == kActRelu) return z > 0.f ? 1.f : 0.f;
+  if constexpr (ACT == kActSilu) {
+    const float s = 1.f / (1.f + expf(-z));
+    return s * (1.f + z * (1.f - s));
+  }
+  if constexpr (ACT == kActGelu)
+    return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * 0.39894228040143268f * expf(-0.5f * z * z);
+  return 1.f;
+}
+
+// f(integral_constant<int, act>) for a run-time activation.
+template <class F>
+__device__ __forceinline__ void by_act(int act, F f) {
   switch (act) {
-    case kActRelu: return z > 0.f ? 1.f : 0.f;
-    case kActSilu: {
-      const float s = 1.f / (1.f + expf(-z));
-      return s * (1.f + z * (1.f - s));
-    }
-    case kActGelu:
-      return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * 0.39894228040143268f * expf(-0.5f * z * z);
-    default: return 1.f;
+    case kActRelu: f(std::integral_constant<int, kActRelu>{}); break;
+    case kActSilu: f(std::integral_constant<int, kActSilu>{}); break;
+    case kActGelu: f(std::integral_constant<int, kActGelu>{}); break;
+    default: f(std::integral_constant<int, kActNone>{});
   }
 }
 
@@ -67,13 +99,67 @@ __device__ __forceinline__ void store_elem(void* p, int64_t i, int type, float f
     static_cast<uint16_t*>(p)[i] = type == kElemBF16 ? BF16::down(f) : F16::down(f);
 }
 
+// Four consecutive elements, the first a multiple of four elements from an aligned row start.
+__device__ __forceinline__ f32x4 load_elem4(const void* p, int64_t i, int type) {
+  if (type == kElemF32) return *reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + i);
+  const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
+  const uint16_t h[4] = {(uint16_t)r.x, (uint16_t)(r.x >> 16), (uint16_t)r.y, (uint16_t)(r.y >> 16)};
+  f32x4 v;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) v[q] = type == kElemBF16 ? BF16::up(h[q]) : F16::up(h[q]);
+  return v;
+}
+
+__device__ __forceinline__ void store_elem4(void* p, int64_t i, int type, f32x4 v) {
+  if (type == kElemF32) {
+    *reinterpret_cast<f32x4*>(static_cast<float*>(p) + i) = v;
+    return;
+  }
+  uint32_t h[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) h[q] = type == kElemBF16 ? BF16::down(v[q]) : F16::down(v[q]);
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) = uint2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
+}
+
 // One element of the result from its sum over k.
-__device__ __forceinline__ void epilogue(const GemmArgs& g, int m, int n, float z) {
+template <int ACT>
+__device__ __forceinline__ void epilogue1(const GemmArgs& g, int m, int n, float z) {
   if (g.bias) z += g.bias[n];
   if (g.pre) store_elem(g.pre, (int64_t)m * g.ldp + n, g.type, z);
-  float v = g.add * act_f32(z, g.act);
+  float v = g.add * act_f32<ACT>(z);
   if (g.res) v += g.keep * load_elem(g.res, (int64_t)m * g.ldr + n, g.out_type);
   store_elem(g.out, (int64_t)m * g.ldo + n, g.out_type, v);
+}
+
+// Whether rows of the result and of what goes with it start where four elements can be moved at once.
+__device__ __forceinline__ bool epilogue_wide(const GemmArgs& g) {
+  return g.ldo % 4 == 0 && (!g.res || g.ldr % 4 == 0) && (!g.pre || g.ldp % 4 == 0);
+}
+
+// Columns n .. n + 3 (n a multiple of four) of row m, those past N left alone.
+template <int ACT>
+__device__ __forceinline__ void epilogue4(const GemmArgs& g, bool wide, int m, int n, f32x4 z) {
+  if (wide && n + 4 <= g.N) {
+    if (g.bias) {
+      const f32x4 b = *reinterpret_cast<const f32x4*>(g.bias + n);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) z[q] += b[q];
+    }
+    if (g.pre) store_elem4(g.pre, (int64_t)m * g.ldp + n, g.type, z);
+    f32x4 v;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = g.add * act_f32<ACT>(z[q]);
+    if (g.res) {
+      const f32x4 r = load_elem4(g.res, (int64_t)m * g.ldr + n, g.out_type);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] += g.keep * r[q];
+    }
+    store_elem4(g.out, (int64_t)m * g.ldo + n, g.out_type, v);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (n + q < g.N) epilogue1<ACT>(g, m, n + q, z[q]);
+  }
 }
 
 }  // namespace beam

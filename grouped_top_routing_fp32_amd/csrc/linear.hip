@@ -4,85 +4,289 @@
 //   y  = keep res + add act(x w^T + bias)
 //   dz = add dy act'(z),  dx = dz w,  dw = dz^T x,  dbias = sum_m dz,  dres = keep dy
 //
-// Products run on 16-bit MFMA with FP32 accumulation; the epilogue is FP32 and
-// rounds once to the output's type.
+// All three products are one kernel over operands whose contiguous axis is K (x and w
+// of the forward product, dz in dx) or the output's (w in dx, both in dw); products
+// run on 16-bit MFMA with FP32 accumulation; the epilogue is FP32 and rounds once to
+// the output's type.
+#include <type_traits>
+
 #include "linear.h"
 
 namespace beam {
 
-constexpr int kLinTile = 64;  // rows and columns of an output tile
-constexpr int kLinK = 32;     // K per step
-constexpr int kLinPad = 8;    // LDS rows of 80 bytes: 16-byte reads of 16 rows fall on distinct banks
-
-// Element (i, k) of an operand, 0 past its ends.
-__device__ __forceinline__ uint16_t operand_at(const void* p, int64_t ld, bool trans, int i, int k, int ni, int nk) {
-  if (i >= ni || k >= nk) return 0;
-  return static_cast<const uint16_t*>(p)[trans ? (int64_t)k * ld + i : (int64_t)i * ld + k];
+// out from the partial sums of the splits, added in order: four columns to a thread.
+__global__ __launch_bounds__(256) void gemm_join_kernel(GemmArgs g, const float* __restrict__ part, int64_t ldpart,
+                                                        int splits) {
+  const int quads = (int)(ldpart / 4);
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= (int64_t)g.M * quads) return;
+  const int m = (int)(i / quads), n = (int)(i % quads) * 4;
+  f32x4 z = {0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < splits; ++s) {
+    const f32x4 v = *reinterpret_cast<const f32x4*>(part + ((int64_t)s * g.M + m) * ldpart + n);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) z[q] += v[q];
+  }
+  const bool wide = epilogue_wide(g);
+  by_act(g.act, [&](auto act) { epilogue4<decltype(act)::value>(g, wide, m, n, z); });
 }
 
-// grid (ceil(N / 64), ceil(M / 64)), 4 waves as 2 x 2, each 32 x 32 of the tile.
-__global__ __launch_bounds__(256) void gemm_simple_kernel(GemmArgs g) {
-  __shared__ __align__(16) uint16_t sa[kLinTile][kLinK + kLinPad], sb[kLinTile][kLinK + kLinPad];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int m0 = blockIdx.y * kLinTile, n0 = blockIdx.x * kLinTile;
-  const int wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
-  f32x4 acc[2][2] = {};
-  for (int k0 = 0; k0 < g.K; k0 += kLinK) {
-    __syncthreads();
-    for (int i = tid; i < kLinTile * kLinK; i += 256) {
-      // consecutive threads along the operand's contiguous axis
-      const int ar = g.at ? i % kLinTile : i / kLinK, ak = g.at ? i / kLinTile : i % kLinK;
-      sa[ar][ak] = operand_at(g.a, g.lda, g.at, m0 + ar, k0 + ak, g.M, g.K);
-      const int br = g.bt ? i % kLinTile : i / kLinK, bk = g.bt ? i / kLinTile : i % kLinK;
-      sb[br][bk] = operand_at(g.b, g.ldb, g.bt, n0 + br, k0 + bk, g.N, g.K);
+// Few rows (M <= 64, both operands K contiguous): bound by reading w once.  A workgroup
+// takes 16 columns; its 8 waves share K in pieces of 128, straight from memory into
+// MFMA operands (a wave reads 256 contiguous bytes of 16 rows of w), and their sums are
+// joined in LDS in wave order.  MT fragments of 16 rows.
+constexpr int kSkinnyWaves = 8;
+
+template <bool HALF, int MT, bool WIDE>
+__global__ __launch_bounds__(64 * kSkinnyWaves) void gemm_skinny_kernel(GemmArgs g) {
+  __shared__ f32x4 sum[kSkinnyWaves][MT][64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, gr = lane >> 4;
+  const int n0 = blockIdx.x * 16;
+  const uint16_t* wrow = static_cast<const uint16_t*>(g.b) + (int64_t)min(n0 + l16, g.N - 1) * g.ldb;
+  const uint16_t* xrow[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+    xrow[i] = static_cast<const uint16_t*>(g.a) + (int64_t)min(16 * i + l16, g.M - 1) * g.lda;
+  auto chunk = [&](const uint16_t* row, int k) {  // 8 elements from k, 0 past K
+    if constexpr (WIDE) {
+      u32x4 v = {0u, 0u, 0u, 0u};
+      if (k < g.K) v = ldg16(row + k);
+      return v;
+    } else {
+      uint16_t e[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) e[q] = k + q < g.K ? row[k + q] : 0;
+      u32x4 v;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = e[2 * q] | ((uint32_t)e[2 * q + 1] << 16);
+      return v;
     }
-    __syncthreads();
+  };
+  f32x4 acc[MT] = {};
+  for (int k = 128 * wave; k < g.K; k += 128 * kSkinnyWaves) {
+    u32x4 fw[4], fx[4][MT];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int s = 0; s < 4; ++s) {
+      fw[s] = chunk(wrow, k + 32 * s + 8 * gr);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const u32x4 fa = *reinterpret_cast<const u32x4*>(&sa[wm + 16 * i + (lane & 15)][8 * (lane >> 4)]);
-        const u32x4 fb = *reinterpret_cast<const u32x4*>(&sb[wn + 16 * j + (lane & 15)][8 * (lane >> 4)]);
-        acc[i][j] = g.type == kElemBF16 ? mfma16x16x32(fa, fb, acc[i][j]) : mfma16x16x32_f16(fa, fb, acc[i][j]);
-      }
+      for (int i = 0; i < MT; ++i) fx[s][i] = chunk(xrow[i], k + 32 * s + 8 * gr);
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int i = 0; i < MT; ++i) acc[i] = mfma<HALF>(fw[s], fx[s][i], acc[i]);
   }
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < MT; ++i) sum[wave][i][lane] = acc[i];
+  __syncthreads();
+  if (wave >= MT) return;
+  f32x4 z = sum[0][wave][lane];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+  for (int w = 1; w < kSkinnyWaves; ++w) {
+    const f32x4 v = sum[w][wave][lane];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int m = m0 + wm + 16 * i + 4 * (lane >> 4) + r, n = n0 + wn + 16 * j + (lane & 15);
-        if (m < g.M && n < g.N) epilogue(g, m, n, acc[i][j][r]);
-      }
+    for (int q = 0; q < 4; ++q) z[q] += v[q];
+  }
+  const int m = 16 * wave + l16, n = n0 + 4 * gr;
+  if (m >= g.M || n >= g.N) return;
+  const bool wide = epilogue_wide(g);
+  by_act(g.act, [&](auto act) { epilogue4<decltype(act)::value>(g, wide, m, n, z); });
+}
+
+// Lays an operand out anew: dst [rows, ld], ld a multiple of 8, zeros past cols.
+__global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* __restrict__ src, int64_t lds, int rows, int cols,
+                                                       uint16_t* __restrict__ dst, int ld) {
+  const int chunks = ld / 8;
+  const int64_t n = (int64_t)rows * chunks;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int r = (int)(i / chunks), c = (int)(i % chunks) * 8;
+    const uint16_t* s = src + (int64_t)r * lds;
+    u32x4 v;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t lo = c + 2 * q < cols ? s[c + 2 * q] : 0, hi = c + 2 * q + 1 < cols ? s[c + 2 * q + 1] : 0;
+      v[q] = lo | (hi << 16);
+    }
+    *reinterpret_cast<u32x4*>(dst + (int64_t)r * ld + c) = v;
+  }
 }
 
 // dz[m, n] = add dy act'(z), rounded to the products' 16-bit type (the rounding that a
 // gradient kept between two layers has anyway); part[u][n] = the unit's sum of the
-// unrounded dz; dres = keep dy.  grid (ceil(N / 256), units), one column to a thread.
+// unrounded dz; dres = keep dy.  grid (ceil(N / VEC / 64), units), block (64, 4): thread
+// (c, r) takes chunk c of VEC columns in rows r, r + 4, ... of the unit.  dz rows are
+// lddz long, a multiple of 8, with zeros past N.
+template <int VEC>
 __global__ __launch_bounds__(256) void linear_dz_kernel(const void* __restrict__ dy, int dy_type, int64_t lddy,
                                                         const void* __restrict__ z, int64_t ldz, int act, float keep,
                                                         float add, uint16_t* __restrict__ dz, int64_t lddz, int type,
                                                         float* __restrict__ part, void* __restrict__ dres,
                                                         int64_t lddres, int M, int N, int rows) {
-  const int n = blockIdx.x * 256 + threadIdx.x;
-  if (n >= N) return;
-  const int m0 = blockIdx.y * rows, m1 = min(M, m0 + rows);
-  float s = 0.f;
-  for (int m = m0; m < m1; ++m) {
-    const float d = load_elem(dy, (int64_t)m * lddy + n, dy_type);
-    float v = add * d;
-    if (act != kActNone) v *= act_slope_f32(load_elem(z, (int64_t)m * ldz + n, type), act);
-    if (dz) store_elem(dz, (int64_t)m * lddz + n, type, v);
-    if (dres) store_elem(dres, (int64_t)m * lddres + n, dy_type, keep * d);
-    s += v;
+  __shared__ float sums[4][64][VEC];
+  const int n = (blockIdx.x * 64 + threadIdx.x) * VEC, y = threadIdx.y;
+  const int m1 = min(M, (int)(blockIdx.y + 1) * rows);
+  float s[VEC] = {};
+  if (n < (dz ? lddz : N)) {
+    auto load = [&](const void* p, int64_t i, int ty, float* v) {
+      if constexpr (VEC == 1) {
+        v[0] = load_elem(p, i, ty);
+      } else if (ty == kElemF32) {
+        load_n<F32, VEC>(static_cast<const float*>(p) + i, v);
+      } else if (ty == kElemBF16) {
+        load_n<BF16, VEC>(static_cast<const uint16_t*>(p) + i, v);
+      } else {
+        load_n<F16, VEC>(static_cast<const uint16_t*>(p) + i, v);
+      }
+    };
+    auto store = [&](void* p, int64_t i, int ty, const float* v) {
+      if constexpr (VEC == 1) {
+        store_elem(p, i, ty, v[0]);
+      } else if (ty == kElemF32) {
+        store_n<F32, VEC>(static_cast<float*>(p) + i, v);
+      } else if (ty == kElemBF16) {
+        store_n<BF16, VEC>(static_cast<uint16_t*>(p) + i, v);
+      } else {
+        store_n<F16, VEC>(static_cast<uint16_t*>(p) + i, v);
+      }
+    };
+    by_act(act, [&](auto a) {
+      constexpr int ACT = decltype(a)::value;
+      for (int m = blockIdx.y * rows + y; m < m1; m += 4) {
+        float d[VEC] = {}, v[VEC] = {}, zz[VEC] = {};
+        if (n < N) {  // VEC = 8 only where N holds whole chunks
+          load(dy, (int64_t)m * lddy + n, dy_type, d);
+          if constexpr (ACT != kActNone) load(z, (int64_t)m * ldz + n, type, zz);
+#pragma unroll
+          for (int q = 0; q < VEC; ++q) {
+            v[q] = add * d[q] * act_slope_f32<ACT>(zz[q]);
+            s[q] += v[q];
+            d[q] *= keep;
+          }
+          if (dres) store(dres, (int64_t)m * lddres + n, dy_type, d);
+        }
+        if (dz) store(dz, (int64_t)m * lddz + n, type, v);
+      }
+    });
   }
-  if (part) part[(int64_t)blockIdx.y * N + n] = s;
+  if (!part) return;
+#pragma unroll
+  for (int q = 0; q < VEC; ++q) sums[y][threadIdx.x][q] = s[q];
+  __syncthreads();
+  for (int i = y * 64 + threadIdx.x; i < 64 * VEC; i += 256) {
+    const int c = i / VEC, q = i % VEC, col = (blockIdx.x * 64 + c) * VEC + q;
+    if (col < N) part[(int64_t)blockIdx.y * N + col] = (sums[0][c][q] + sums[1][c][q]) + (sums[2][c][q] + sums[3][c][q]);
+  }
 }
 
-hipError_t launch_gemm(const GemmArgs& g, hipStream_t st) {
-  hipLaunchKernelGGL(gemm_simple_kernel, dim3((g.N + kLinTile - 1) / kLinTile, (g.M + kLinTile - 1) / kLinTile),
-                     dim3(256), 0, st, g);
+// ---------------------------------------------------------------------------
+// plans and launches
+// ---------------------------------------------------------------------------
+namespace {
+
+constexpr int kBK = 64;  // K per stage of the tiled kernel
+constexpr int kCUs = 256;
+constexpr int kSkinnyRows = 64;
+
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+int ceil_div(int a, int b) { return (a + b - 1) / b; }
+int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
+
+// Whether the copies can take the operand as it is: whole chunks of 8 elements on 16 bytes.
+bool regular(int64_t ld, int contiguous) { return ld % 8 == 0 && contiguous % 8 == 0; }
+
+}  // namespace
+
+GemmPlan plan_gemm(int M, int N, int K, bool at, bool bt, int64_t lda, int64_t ldb, bool padded_a) {
+  GemmPlan p{};
+  p.splits = 1;
+  p.k_per_split = K > 0 ? ceil_div(K, kBK) * kBK : kBK;
+  if (!at && !bt && M <= kSkinnyRows) {
+    p.kind = GemmPlan::kSkinny;
+    return p;
+  }
+  p.kind = GemmPlan::kTiles;
+  p.copy_a = !padded_a && !regular(lda, at ? M : K);
+  p.copy_b = !regular(ldb, bt ? N : K);
+  const int big = ceil_div(M, 256) * ceil_div(N, 256);
+  p.tile = big >= 160 ? 256 : 128;
+  if (p.tile == 128 && M > 0) {
+    const int tiles = ceil_div(M, 128) * ceil_div(N, 128), stages = ceil_div(K, kBK);
+    int s = 2 * kCUs / tiles;               // two workgroups of 128 x 128 fit a CU
+    s = s < stages / 8 ? s : stages / 8;    // at least 8 stages each
+    s = s < 16 ? s : 16;
+    if (s > 1) {
+      p.k_per_split = ceil_div(stages, s) * kBK;
+      p.splits = ceil_div(K, p.k_per_split);
+    }
+  }
+  size_t off = 0;
+  p.off_a = off;
+  if (p.copy_a) off = up256(off + (size_t)(at ? K : M) * up8(at ? M : K) * 2);
+  p.off_b = off;
+  if (p.copy_b) off = up256(off + (size_t)(bt ? K : N) * up8(bt ? N : K) * 2);
+  p.off_part = off;
+  if (p.splits > 1) off = up256(off + (size_t)p.splits * M * ((N + 3) / 4 * 4) * sizeof(float));
+  p.total = off;
+  return p;
+}
+
+namespace {
+
+template <bool HALF, int MT>
+void skinny(const GemmArgs& g, bool wide, hipStream_t st) {
+  const dim3 grid(ceil_div(g.N, 16)), block(64 * kSkinnyWaves);
+  if (wide)
+    hipLaunchKernelGGL((gemm_skinny_kernel<HALF, MT, true>), grid, block, 0, st, g);
+  else
+    hipLaunchKernelGGL((gemm_skinny_kernel<HALF, MT, false>), grid, block, 0, st, g);
+}
+
+template <bool HALF>
+hipError_t launch_skinny(const GemmArgs& g, hipStream_t st) {
+  const bool wide = regular(g.lda, g.K) && regular(g.ldb, g.K);
+  if (g.M <= 16)
+    skinny<HALF, 1>(g, wide, st);
+  else if (g.M <= 32)
+    skinny<HALF, 2>(g, wide, st);
+  else
+    skinny<HALF, 4>(g, wide, st);
+  return hipGetLastError();
+}
+
+hipError_t pad_rows(const void* src, int64_t ld, int rows, int cols, void* dst, hipStream_t st) {
+  const int64_t blocks = (rows * (up8(cols) / 8) + 255) / 256;
+  hipLaunchKernelGGL(pad_rows_kernel, dim3((uint32_t)(blocks < (1 << 20) ? blocks : 1 << 20)), dim3(256), 0, st,
+                     static_cast<const uint16_t*>(src), ld, rows, cols, static_cast<uint16_t*>(dst), (int)up8(cols));
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_gemm(const GemmArgs& args, const GemmPlan& p, void* ws, hipStream_t st) {
+  GemmArgs g = args;
+  char* base = static_cast<char*>(ws);
+  hipError_t e;
+  if (p.copy_a && g.K > 0) {
+    const int rows = g.at ? g.K : g.M, cols = g.at ? g.M : g.K;
+    if ((e = pad_rows(g.a, g.lda, rows, cols, base + p.off_a, st)) != hipSuccess) return e;
+    g.a = base + p.off_a;
+    g.lda = up8(cols);
+  }
+  if (p.copy_b && g.K > 0) {
+    const int rows = g.bt ? g.K : g.N, cols = g.bt ? g.N : g.K;
+    if ((e = pad_rows(g.b, g.ldb, rows, cols, base + p.off_b, st)) != hipSuccess) return e;
+    g.b = base + p.off_b;
+    g.ldb = up8(cols);
+  }
+  const int64_t ldpart = (g.N + 3) / 4 * 4;
+  float* part = p.splits > 1 ? reinterpret_cast<float*>(base + p.off_part) : nullptr;
+  const bool half = g.type == kElemF16;
+  if (p.kind == GemmPlan::kSkinny) return half ? launch_skinny<true>(g, st) : launch_skinny<false>(g, st);
+  e = half ? launch_gemm_f16(g, p, part, ldpart, st) : launch_gemm_bf16(g, p, part, ldpart, st);
+  if (e != hipSuccess || !part) return e;
+  const int64_t quads = (int64_t)g.M * (ldpart / 4);
+  hipLaunchKernelGGL(gemm_join_kernel, dim3((uint32_t)((quads + 255) / 256)), dim3(256), 0, st, g, part, ldpart,
+                     p.splits);
   return hipGetLastError();
 }
 
@@ -91,9 +295,17 @@ int linear_dz_units(int M) { return M < 128 ? M : 128; }
 hipError_t launch_linear_dz(const void* dy, int dy_type, int64_t lddy, const void* z, int64_t ldz, int act, float keep,
                             float add, uint16_t* dz, int64_t lddz, int type, float* part, void* dres, int64_t lddres,
                             int M, int N, hipStream_t st) {
-  const int units = linear_dz_units(M), rows = (M + units - 1) / units;
-  hipLaunchKernelGGL(linear_dz_kernel, dim3((N + 255) / 256, units), dim3(256), 0, st, dy, dy_type, lddy, z, ldz, act,
-                     keep, add, dz, lddz, type, part, dres, lddres, M, N, rows);
+  const int units = linear_dz_units(M), rows = ceil_div(M, units);
+  const bool wide = N % 8 == 0 && lddy % 8 == 0 && (act == kActNone || ldz % 8 == 0) && (!dres || lddres % 8 == 0);
+  const int cols = dz ? (int)lddz : N;
+  auto go = [&](auto kernel, int vec) {
+    hipLaunchKernelGGL(kernel, dim3(ceil_div(ceil_div(cols, vec), 64), units), dim3(64, 4), 0, st, dy, dy_type, lddy,
+                       z, ldz, act, keep, add, dz, lddz, type, part, dres, lddres, M, N, rows);
+  };
+  if (wide)
+    go(linear_dz_kernel<8>, 8);
+  else
+    go(linear_dz_kernel<1>, 1);
   return hipGetLastError();
 }
 

@@ -25,7 +25,6 @@ hipError_t launch_balance(const float* scores, const int32_t* ids, int B, const 
 hipError_t launch_route_backward(const float* scores, const int32_t* ids, const float* dw, float scale, int B,
                                  const int32_t* off, float alpha, const float* dloss, const int32_t* counts,
                                  float* dlogits, int T, int E, int K, hipStream_t st);
-hipError_t launch_gemm(const GemmArgs& g, hipStream_t st);
 int linear_dz_units(int M);
 hipError_t launch_linear_dz(const void* dy, int dy_type, int64_t lddy, const void* z, int64_t ldz, int act, float keep,
                             float add, uint16_t* dz, int64_t lddz, int type, float* part, void* dres, int64_t lddres,
@@ -72,17 +71,25 @@ int check_linear(int32_t rows, int32_t cols, int32_t inner) {
 
 bool act_ok(int act) { return act >= BEAM_MOE_ACT_NONE && act <= BEAM_MOE_ACT_GELU; }
 
+// Workspace of the backward pass: dz, the partial sums of dbias, then what the two
+// products need, one after the other in the same place.  Where dz is dy itself its
+// place stays unused; the size does not depend on it.
 struct BackwardPlan {
-  size_t off_dz, off_part, total;
+  size_t off_dz, off_part, off_gemm, total;
   int64_t lddz;
+  beam::GemmPlan dx, dw;
 };
 
-BackwardPlan backward_plan(int32_t rows, int32_t cols) {
+BackwardPlan backward_plan(int32_t rows, int32_t cols, int32_t inner, int64_t ldx, int64_t ldw) {
   BackwardPlan p;
   p.lddz = (cols + 7) / 8 * 8;
+  // dz rows are whole chunks with zeros past cols, so the products take them as they are
+  p.dx = beam::plan_gemm(rows, inner, cols, false, true, p.lddz, ldw, true);
+  p.dw = beam::plan_gemm(cols, inner, rows, true, true, p.lddz, ldx, true);
   p.off_dz = 0;
   p.off_part = align_up((size_t)rows * p.lddz * 2);
-  p.total = p.off_part + align_up((size_t)beam::linear_dz_units(rows) * cols * sizeof(float));
+  p.off_gemm = p.off_part + align_up((size_t)beam::linear_dz_units(rows) * cols * sizeof(float));
+  p.total = p.off_gemm + (p.dx.total > p.dw.total ? p.dx.total : p.dw.total);
   return p;
 }
 
@@ -167,7 +174,7 @@ int beam_moe_route_backward(const beam_moe_dims* d, int32_t T, const float* scor
 
 size_t beam_moe_linear_workspace_bytes(int32_t rows, int32_t cols, int32_t inner, int64_t ldx, int64_t ldw) {
   if (check_linear(rows, cols, inner) != BEAM_MOE_OK || !ld_ok(ldx, inner) || !ld_ok(ldw, inner)) return SIZE_MAX;
-  return 0;
+  return beam::plan_gemm(rows, cols, inner, false, false, ldx, ldw).total;
 }
 
 int beam_moe_linear(int32_t rows, int32_t cols, int32_t inner, int type, const void* x, int64_t ldx, const void* w,
@@ -185,8 +192,8 @@ int beam_moe_linear(int32_t rows, int32_t cols, int32_t inner, int type, const v
     return BEAM_MOE_ERR_INVALID_ARG;
   if ((rc = check_ptrs({x, w, y})) != BEAM_MOE_OK) return rc;
   if ((rc = check_optional({bias, res, pre})) != BEAM_MOE_OK) return rc;
-  const size_t need = beam_moe_linear_workspace_bytes(rows, cols, inner, ldx, ldw);
-  if (need && (!ws || !aligned16(ws) || ws_bytes < need)) return BEAM_MOE_ERR_WORKSPACE;
+  const beam::GemmPlan plan = beam::plan_gemm(rows, cols, inner, false, false, ldx, ldw);
+  if (plan.total && (!ws || !aligned16(ws) || ws_bytes < plan.total)) return BEAM_MOE_ERR_WORKSPACE;
   beam::GemmArgs g{};
   g.a = x;
   g.lda = ldx;
@@ -207,12 +214,12 @@ int beam_moe_linear(int32_t rows, int32_t cols, int32_t inner, int type, const v
   g.ldo = ldy;
   g.pre = pre;
   g.ldp = ldpre;
-  return hip_status(beam::launch_gemm(g, static_cast<hipStream_t>(stream)));
+  return hip_status(beam::launch_gemm(g, plan, ws, static_cast<hipStream_t>(stream)));
 }
 
 size_t beam_moe_linear_backward_workspace_bytes(int32_t rows, int32_t cols, int32_t inner, int64_t ldx, int64_t ldw) {
   if (check_linear(rows, cols, inner) != BEAM_MOE_OK || !ld_ok(ldx, inner) || !ld_ok(ldw, inner)) return SIZE_MAX;
-  return backward_plan(rows, cols).total;
+  return backward_plan(rows, cols, inner, ldx, ldw).total;
 }
 
 int beam_moe_linear_backward(int32_t rows, int32_t cols, int32_t inner, int type, const void* dy, int dy_type,
@@ -235,13 +242,16 @@ int beam_moe_linear_backward(int32_t rows, int32_t cols, int32_t inner, int type
         (pre && !ld_ok(ldpre, cols)) || (x && !ld_ok(ldx, inner)) || (w && !ld_ok(ldw, inner)))
       return BEAM_MOE_ERR_INVALID_ARG;
   }
-  const BackwardPlan p = backward_plan(rows, cols);
+  const BackwardPlan p = backward_plan(rows, cols, inner, x ? ldx : inner, w ? ldw : inner);
   if (rows > 0 && (!ws || !aligned16(ws) || ws_bytes < p.total)) return BEAM_MOE_ERR_WORKSPACE;
-  uint16_t* dz = at<uint16_t>(ws, p.off_dz);
   float* part = dbias ? at<float>(ws, p.off_part) : nullptr;
-  if (rows > 0)
-    if ((rc = hip_status(beam::launch_linear_dz(dy, dy_type, lddy, pre, ldpre, act, keep, add, dx || dw ? dz : nullptr,
-                                                p.lddz, type, part, dres, lddres, rows, cols, st))) != BEAM_MOE_OK)
+  void* gemm_ws = at<void*>(ws, p.off_gemm);
+  // dz is dy itself where nothing changes it and its rows are whole chunks
+  const bool same = act == BEAM_MOE_ACT_NONE && add == 1.f && dy_type == type && lddy % 8 == 0 && cols % 8 == 0;
+  uint16_t* dz = same || !(dx || dw) ? nullptr : at<uint16_t>(ws, p.off_dz);
+  if (rows > 0 && (dz || part || dres))
+    if ((rc = hip_status(beam::launch_linear_dz(dy, dy_type, lddy, pre, ldpre, act, keep, add, dz, p.lddz, type, part,
+                                                dres, lddres, rows, cols, st))) != BEAM_MOE_OK)
       return rc;
   if (dbias)
     if ((rc = hip_status(beam::launch_column_sums(part, dbias, nullptr, rows > 0 ? beam::linear_dz_units(rows) : 0,
@@ -251,8 +261,8 @@ int beam_moe_linear_backward(int32_t rows, int32_t cols, int32_t inner, int type
   g.type = type;
   g.out_type = type;
   g.add = 1.f;
-  g.a = dz;
-  g.lda = p.lddz;
+  g.a = same ? dy : dz;
+  g.lda = same ? lddy : p.lddz;
   if (dx && rows > 0) {
     g.b = w;
     g.ldb = ldw;
@@ -262,7 +272,7 @@ int beam_moe_linear_backward(int32_t rows, int32_t cols, int32_t inner, int type
     g.K = cols;
     g.out = dx;
     g.ldo = lddx;
-    if ((rc = hip_status(beam::launch_gemm(g, st))) != BEAM_MOE_OK) return rc;
+    if ((rc = hip_status(beam::launch_gemm(g, p.dx, gemm_ws, st))) != BEAM_MOE_OK) return rc;
   }
   if (dw) {
     g.at = g.bt = true;
@@ -273,7 +283,7 @@ int beam_moe_linear_backward(int32_t rows, int32_t cols, int32_t inner, int type
     g.K = rows;
     g.out = dw;
     g.ldo = lddw;
-    if ((rc = hip_status(beam::launch_gemm(g, st))) != BEAM_MOE_OK) return rc;
+    if ((rc = hip_status(beam::launch_gemm(g, p.dw, gemm_ws, st))) != BEAM_MOE_OK) return rc;
   }
   return BEAM_MOE_OK;
 }
