@@ -19,5 +19,6 @@ _EXPORTS = ("beam_moe_route", "beam_moe_select", "beam_moe_dispatch", "beam_moe_
 def __getattr__(name):
     if name in _EXPORTS:
         from . import binding
-        return getattr(binding, name)
+        globals()[name] = value = getattr(binding, name)  # later uses find it without coming here
+        return value
     raise AttributeError(name)

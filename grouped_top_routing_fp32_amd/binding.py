@@ -8,6 +8,7 @@ is missing or fails to load, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -458,6 +459,11 @@ def beam_moe_residual_forward_fp8(dims: Dims, stream_in: torch.Tensor, step: int
 # --------------------------------------------------------------------------
 # operators around the block: layer norm, the router's training side, linear
 # --------------------------------------------------------------------------
+# the current stream's handle without a Stream object around it, which takes 2.7 us to make
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 class _On:
     """Where a call runs: the tensors' device made current, and the given stream, or that device's
     current one.  Outputs and workspaces allocated inside belong to that stream."""
@@ -472,7 +478,7 @@ class _On:
             if torch.cuda.current_device() != dev.index:
                 self.ctx = torch.cuda.device(dev)
                 self.ctx.__enter__()
-            return torch.cuda.current_stream().cuda_stream
+            return _raw_stream(dev.index)
         if not hasattr(stream, "cuda_stream"):
             stream = torch.cuda.ExternalStream(int(stream), device=dev)
         elif stream.device != dev:
@@ -532,6 +538,7 @@ def _scratch(n: int, ws: Optional[torch.Tensor], dev, fn: str):
     return ws.data_ptr(), ws.numel() * ws.element_size(), ws
 
 
+_cdims_of = functools.lru_cache(maxsize=64)(_cdims)
 _FLOATS = tuple(ELEM_TYPES)
 _F32 = torch.float32
 
@@ -601,7 +608,7 @@ def beam_moe_balance_loss(dims: Dims, scores: torch.Tensor, topk_ids: torch.Tens
     """Load-balance loss and per-expert counts of each packed sequence (one sequence without seq_offsets
     [B+1] int32). Returns (loss [B] fp32, counts [B,E] int32, prob [B,E] fp32)."""
     T, E, dev, s, i, B, off = _routed(dims, scores, topk_ids, seq_offsets)
-    lib, cd = load_library(), _cdims(dims)
+    lib, cd = load_library(), _cdims_of(dims)
     with _On(dev, stream) as st:
         loss = torch.empty((B,), dtype=_F32, device=dev)
         counts = torch.empty((B, E), dtype=torch.int32, device=dev)
@@ -622,7 +629,7 @@ def beam_moe_route_backward(dims: Dims, scores: torch.Tensor, topk_ids: torch.Te
     T, E, dev, s, i, B, off = _routed(dims, scores, topk_ids, seq_offsets)
     d = _vec(dw, "dw", _F32, (T, dims.topk), dev)
     dl, c = _vec(dloss, "dloss", _F32, (B,), dev), _vec(counts, "counts", torch.int32, (B, E), dev)
-    cd = _cdims(dims)
+    cd = _cdims_of(dims)
     with _On(dev, stream) as st:
         out = torch.empty((T, E), dtype=_F32, device=dev)
         if T == 0 and (dw is not None or dloss is not None):

@@ -93,11 +93,8 @@ __device__ void sum_rows(const float* __restrict__ scores, const int32_t* __rest
       s[u] = (v[u][0] + v[u][1]) + (v[u][2] + v[u][3]);
     }
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1)
-#pragma unroll
-      for (int u = 0; u < U; ++u) s[u] += __shfl_xor(s[u], off);
-#pragma unroll
     for (int u = 0; u < U; ++u) {
+      s[u] = wave_sum(s[u]);
       const float inv = s[u] == 0.f ? 0.f : 1.f / s[u];  // a row of zeros (or past the end) adds nothing
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[i] += v[u][i] * inv;

@@ -167,32 +167,94 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(GemmArgs g, int mt, i
   constexpr int kQuads = BN / 4, kRowsAtOnce = 64 * NW / kQuads;
   const int qn = tid % kQuads, qr = tid / kQuads;
   const int n = n0 + 4 * qn;
-  const bool wide = epilogue_wide(g);
-#pragma unroll
-  for (int pass = 0; pass < kPasses; ++pass) {
+  auto fill = [&](int pass) __attribute__((always_inline)) {
     __syncthreads();  // everyone is done with the stages, or with the last pass
     if (wm / (WM / kPasses) == pass) {
 #pragma unroll
       for (int i = 0; i < FI; ++i)
 #pragma unroll
         for (int j = 0; j < FJ; ++j) {
-          const int r = wm * (BM / WM) - pass * kPassRows + 16 * i + (lane & 15);
+          const int r = (wm % (WM / kPasses)) * (BM / WM) + 16 * i + (lane & 15);
           const int c = wn * (BN / WN) / 4 + 4 * j + (lane >> 4);
           sums[r * kQuads + (c ^ (r & 15))] = acc[i][j];
         }
     }
     __syncthreads();
+  };
+  auto sum_at = [&](int r) __attribute__((always_inline)) { return sums[r * kQuads + (qn ^ (r & 15))]; };
+  const bool wide = epilogue_wide(g);
+
+  // Tiles inside the result: batches of kBatch rows to a thread, the residual of the next
+  // batch requested as this one's is used, so its latency shows once per tile.
+  constexpr int kBatch = 8, kBatches = kPassRows / kRowsAtOnce / kBatch;
+  static_assert(kBatches * kBatch * kRowsAtOnce == kPassRows, "whole batches");
+  if (EPI && wide && !part && m0 + BM <= g.M && n0 + BN <= g.N) {
+    auto inside = [&](auto out_type, auto act) __attribute__((always_inline)) {
+      using OT = decltype(out_type);
+      using Raw = std::conditional_t<sizeof(typename OT::S) == 4, f32x4, uint2>;
+      const typename OT::S* res = static_cast<const typename OT::S*>(g.res) + (int64_t)(m0 + qr) * g.ldr + n;
+      Raw rv[kBatch] = {};
+      auto request = [&](int u, int row) __attribute__((always_inline)) {
+        if (g.res) rv[u] = *reinterpret_cast<const Raw*>(res + (int64_t)row * g.ldr);
+      };
+      f32x4 bias = {0.f, 0.f, 0.f, 0.f};
+      if (g.bias) bias = *reinterpret_cast<const f32x4*>(g.bias + n);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) request(u, u * kRowsAtOnce);
+#pragma unroll 1
+      for (int b = 0; b < kPasses * kBatches; ++b) {
+        if (b % kBatches == 0) fill(b / kBatches);
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const int row = (b * kBatch + u) * kRowsAtOnce;  // of the tile, before qr
+          f32x4 z = sum_at(row % kPassRows + qr);
+          const int m = m0 + qr + row;
+          f32x4 r;
+          if constexpr (sizeof(typename OT::S) == 4) {
+            r = rv[u];
+          } else {
+            const uint32_t h[2] = {rv[u].x, rv[u].y};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) r[q] = OT::up((uint16_t)(h[q / 2] >> (16 * (q % 2))));
+          }
+          if (b + 1 < kPasses * kBatches) request(u, row + kBatch * kRowsAtOnce);
+          f32x4 v;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            z[q] += bias[q];
+            v[q] = g.add * act_f32<decltype(act)::value>(z[q]);
+          }
+          if (g.res) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] += g.keep * r[q];
+          }
+          if (g.pre) store_elem4(g.pre, (int64_t)m * g.ldp + n, g.type, z);
+          store_elem4(g.out, (int64_t)m * g.ldo + n, sizeof(typename OT::S) == 4 ? kElemF32 : g.type, v);
+        }
+      }
+    };
+    by_act(g.act, [&](auto act) {
+      if (g.out_type == kElemF32)
+        inside(F32{}, act);
+      else
+        inside(std::conditional_t<HALF, F16, BF16>{}, act);
+    });
+    return;
+  }
+#pragma unroll
+  for (int pass = 0; pass < kPasses; ++pass) {
+    fill(pass);
     const int mp = m0 + pass * kPassRows, rmax = n < g.N ? min(kPassRows, g.M - mp) : 0;
-    auto rows_of = [&](auto f) {
+    auto rows_of = [&](auto f) __attribute__((always_inline)) {
 #pragma unroll 4
-      for (int r = qr; r < rmax; r += kRowsAtOnce) f(mp + r, sums[r * kQuads + (qn ^ (r & 15))]);
+      for (int r = qr; r < rmax; r += kRowsAtOnce) f(mp + r, sum_at(r));
     };
     if (part) {  // ldpart is a multiple of four and holds the columns past N
       float* p = part + (int64_t)split * g.M * ldpart + n;
       rows_of([&](int m, f32x4 v) { *reinterpret_cast<f32x4*>(p + (int64_t)m * ldpart) = v; });
     } else if constexpr (EPI) {
       by_act(g.act, [&](auto act) {
-        rows_of([&](int m, f32x4 v) { epilogue4<decltype(act)::value>(g, wide, m, n, v); });
+        for (int r = qr; r < rmax; r += kRowsAtOnce) epilogue4<decltype(act)::value>(g, wide, mp + r, n, sum_at(r));
       });
     } else {
       rows_of([&](int m, f32x4 v) { epilogue4<kActNone>(g, wide, m, n, v); });

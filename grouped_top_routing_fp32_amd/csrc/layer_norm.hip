@@ -17,17 +17,20 @@ namespace beam {
 
 constexpr int kLnMaxThreads = 1024;
 constexpr int kLnMaxWaves = kLnMaxThreads / 64;
+static_assert(kLnMaxWaves == 16, "16 lanes join the waves' sums");
 
-// Forward.  Statistics: each wave takes the mean of its own columns, then the sum
-// of squares about it (two passes over registers), and the waves' means and
-// squares are joined about the common mean in FP64, in wave order: one barrier,
-// and a mean far from zero cancels nothing.
+// Forward.  Statistics: each wave takes the mean m of its own columns, then the sum of
+// squares about it (two passes over registers) and the rest c of its mean that m's
+// rounding left.  The waves are joined about the first one's m, P: wave w's mean is
+// P + d_w, d_w = (m_w - P) + c_w, the row's P + D, D = sum n_w d_w / H, and the squares
+// add up to sum M2_w + n_w (d_w - D)^2.  One barrier; a mean far from zero cancels
+// nothing, since only P holds its size, and y is taken from (x - P) - D.
 template <class XT, class YT, int VEC, int NCH>
 __global__ __launch_bounds__(kLnMaxThreads) void layer_norm_kernel(
     const typename XT::S* __restrict__ x, int64_t ldx, const float* __restrict__ gamma,
     const float* __restrict__ beta, typename YT::S* __restrict__ y, int64_t ldy, float* __restrict__ mean_out,
     float* __restrict__ rstd_out, int T, int H, float eps) {
-  __shared__ double smean[kLnMaxWaves], sm2[kLnMaxWaves];
+  __shared__ f32x4 parts[kLnMaxWaves];
   const int tid = threadIdx.x, team = blockDim.x, wave = tid >> 6, nw = team >> 6;
   const int t = blockIdx.x * blockDim.y + threadIdx.y;
   if (t >= T) return;  // blockDim.y > 1 only for one-wave teams, which meet no barrier
@@ -35,58 +38,46 @@ __global__ __launch_bounds__(kLnMaxThreads) void layer_norm_kernel(
   const typename XT::S* xr = x + (int64_t)t * ldx;
   float v[NCH][VEC];
   float s = 0.f;
+  int cols = 0;  // the wave's
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
     const int ch = tid + c * team;
+    cols += min(64, max(0, nch - (c * team + 64 * wave))) * VEC;
     if (ch < nch) {
       load_n<XT, VEC>(xr + (int64_t)ch * VEC, v[c]);
 #pragma unroll
       for (int q = 0; q < VEC; ++q) s += v[c][q];
     }
   }
-  auto wave_cols = [&](int w) {
-    int n = 0;
-#pragma unroll
-    for (int c = 0; c < NCH; ++c) n += min(64, max(0, nch - (c * team + 64 * w)));
-    return n * VEC;
-  };
-  const int n = wave_cols(wave);
-  const float m = n ? wave_sum(s) / n : 0.f;
-  float r = 0.f, q2 = 0.f;
+  float P = cols ? wave_sum(s) / cols : 0.f;
+  float r = 0.f, m2 = 0.f;
 #pragma unroll
   for (int c = 0; c < NCH; ++c)
     if (tid + c * team < nch) {
 #pragma unroll
       for (int q = 0; q < VEC; ++q) {
-        const float d = v[c][q] - m;
+        const float d = v[c][q] - P;
         r += d;
-        q2 += d * d;
+        m2 += d * d;
       }
     }
   r = wave_sum(r);
-  q2 = wave_sum(q2);
-  // m is rounded: the rest r / n belongs to the mean, and r^2 / n off the squares
-  double mean = n ? (double)m + (double)r / n : 0.0;
-  double m2 = n ? (double)q2 - (double)r * r / n : 0.0;
+  float D = cols ? r / cols : 0.f;
+  m2 = wave_sum(m2) - r * D;
   if (nw > 1) {
-    if ((tid & 63) == 0) {
-      smean[wave] = mean;
-      sm2[wave] = m2;
-    }
+    if ((tid & 63) == 0) parts[wave] = f32x4{P, D, m2, (float)cols};
     __syncthreads();
-    mean = 0.0;
-    m2 = 0.0;
-    for (int w = 0; w < nw; ++w) mean += smean[w] * wave_cols(w);
-    mean /= H;
-    for (int w = 0; w < nw; ++w) {
-      const double d = smean[w] - mean;
-      m2 += sm2[w] + d * d * wave_cols(w);
-    }
+    // every 16 lanes join the waves' parts among themselves
+    const int w = tid & 15;
+    const f32x4 mine = w < nw ? parts[w] : f32x4{0.f, 0.f, 0.f, 0.f};
+    P = parts[0][0];
+    const float d = mine[3] > 0.f ? (mine[0] - P) + mine[1] : 0.f;
+    D = row16_sum(mine[3] * d) / H;
+    m2 = row16_sum(mine[2] + mine[3] * (d - D) * (d - D));
   }
-  const float rs = 1.f / sqrtf((float)(m2 / H) + eps);
-  const float mh = (float)mean, ml = (float)(mean - (double)mh);
+  const float rs = 1.f / sqrtf(m2 / H + eps);
   if (tid == 0) {
-    if (mean_out) mean_out[t] = mh;
+    if (mean_out) mean_out[t] = P + D;
     if (rstd_out) rstd_out[t] = rs;
   }
   typename YT::S* yr = y + (int64_t)t * ldy;
@@ -99,7 +90,7 @@ __global__ __launch_bounds__(kLnMaxThreads) void layer_norm_kernel(
       if (beta) load_n<F32, VEC>(beta + ch * VEC, b);
 #pragma unroll
       for (int q = 0; q < VEC; ++q) {
-        o[q] = ((v[c][q] - mh) - ml) * rs;
+        o[q] = ((v[c][q] - P) - D) * rs;
         if (gamma) o[q] *= g[q];
         if (beta) o[q] += b[q];
       }
@@ -162,11 +153,9 @@ __global__ __launch_bounds__(kLnMaxThreads) void layer_norm_backward_kernel(
         red[buf][wave][1] = s2;
       }
       __syncthreads();
-      s1 = s2 = 0.f;
-      for (int w = 0; w < nw; ++w) {
-        s1 += red[buf][w][0];
-        s2 += red[buf][w][1];
-      }
+      const int w = tid & 15;  // every 16 lanes add the waves' sums among themselves
+      s1 = row16_sum(w < nw ? red[buf][w][0] : 0.f);
+      s2 = row16_sum(w < nw ? red[buf][w][1] : 0.f);
     }
     if (dx) {
       const float c1 = s1 / H, c2 = s2 / H;

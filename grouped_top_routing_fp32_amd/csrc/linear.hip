@@ -151,6 +151,7 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(const void* __restrict__
     };
     by_act(act, [&](auto a) {
       constexpr int ACT = decltype(a)::value;
+#pragma unroll 4
       for (int m = blockIdx.y * rows + y; m < m1; m += 4) {
         float d[VEC] = {}, v[VEC] = {}, zz[VEC] = {};
         if (n < N) {  // VEC = 8 only where N holds whole chunks
@@ -290,7 +291,7 @@ hipError_t launch_gemm(const GemmArgs& args, const GemmPlan& p, void* ws, hipStr
   return hipGetLastError();
 }
 
-int linear_dz_units(int M) { return M < 128 ? M : 128; }
+int linear_dz_units(int M) { return M < 256 ? M : 256; }
 
 hipError_t launch_linear_dz(const void* dy, int dy_type, int64_t lddy, const void* z, int64_t ldz, int act, float keep,
                             float add, uint16_t* dz, int64_t lddz, int type, float* part, void* dres, int64_t lddres,

@@ -422,12 +422,15 @@ def _linear_check(x, w, bias, act, res, keep, add, y, pre=None):
     _near(y, ry, abs(add) * (1.13 * dz + 8 * U * (rz.abs() + (act != "none"))) + 2 * U * ry.abs() + extra, "y")
 
 
+# the last of each list are large enough for 256-row tiles: the forward product's, dx's and dw's
+LARGE = [(1000, 1032, 2048), (2100, 2560, 1280), (3300, 3336, 136)]
+LARGE_BACK = LARGE + [(3300, 200, 3336), (200, 3300, 3336), (136, 3584, 3584)]
 LINEAR_SHAPES = [(1, 1, 1), (1, 64, 64), (1, 100, 1000), (2, 2560, 512), (3, 17, 5), (7, 33, 2049), (16, 256, 128),
                  (17, 48, 96), (33, 1000, 136), (64, 512, 2560), (65, 130, 72), (100, 64, 7), (129, 257, 65),
                  (255, 96, 520), (256, 256, 64), (300, 513, 1024), (257, 264, 192), (520, 1040, 328)]
 
 
-@pytest.mark.parametrize("M,N,K", LINEAR_SHAPES + [(1000, 1032, 2048), (2100, 2560, 1280)])
+@pytest.mark.parametrize("M,N,K", LINEAR_SHAPES + LARGE)
 @pytest.mark.parametrize("dt", [BF16, F16])
 def test_linear(M, N, K, dt):
     g = _gen(M * 3 + N * 5 + K)
@@ -497,7 +500,7 @@ def _linear_back_check(dy, x, w, pre, act, keep, add, out):
         _near(dres, keep * dy.double(), 2 * U * (keep * dy.double()).abs(), "dres")
 
 
-@pytest.mark.parametrize("M,N,K", LINEAR_SHAPES + [(1000, 1032, 2048), (2100, 2560, 1280)])
+@pytest.mark.parametrize("M,N,K", LINEAR_SHAPES + LARGE_BACK)
 @pytest.mark.parametrize("dt", [BF16, F16])
 def test_linear_backward(M, N, K, dt):
     g = _gen(M * 3 + N * 5 + K + 1)
