@@ -18,7 +18,7 @@ namespace beam {
 constexpr int kBalMaxE = 256;
 constexpr int kBalSmallT = 512;    // up to here one workgroup per sequence does everything
 constexpr int kBalSmallThreads = 1024;
-constexpr int kBalUnitThreads = 256;
+constexpr int kBalUnitThreads = 512;
 constexpr int kBalFinishThreads = 1024;
 
 // Offset i of the packed sequences; without offsets, one sequence of T rows.  Values
@@ -222,68 +222,125 @@ __global__ __launch_bounds__(kBalFinishThreads) void balance_finish_kernel(Units
 //     ds_e = (g_e - sum_j g_j s_j / S) / S
 // A constant added to every g_e changes nothing, so g is taken from the exact integers
 // E count - K n: with near-even counts the difference would lose most of its digits.
-// One wave per token; a slot whose id lies outside [0, E) is skipped.
+// One wave per token; a slot whose id lies outside [0, E) is skipped.  Bound by vector
+// instructions next to the memory (16 waves to a SIMD at 16384 tokens): what the slots
+// need of the row goes through the wave's own LDS row instead of compares over all
+// experts, and up to 64 sequences a token's is found in one load.  Everything that
+// does not hang on another load is requested at the start.
+constexpr int kGradWaves = 4;
+
 template <bool V4>
-__global__ __launch_bounds__(256) void route_backward_kernel(
+__global__ __launch_bounds__(64 * kGradWaves) void route_backward_kernel(
     const float* __restrict__ scores, const int32_t* __restrict__ ids, const float* __restrict__ dw, float scale,
     Sequences q, float alpha, const float* __restrict__ dloss, const int32_t* __restrict__ counts,
     float* __restrict__ dlogits, int E, int K) {
-  const int lane = threadIdx.x & 63;
-  const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (t >= q.T) return;
+  // experts of lane l at 4 l .. 4 l + 3 with V4, else at place(e) = 4 (e % 64) + e / 64
+  __shared__ f32x4 rows[kGradWaves][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int t = __builtin_amdgcn_readfirstlane(blockIdx.x * kGradWaves + wave);
+  if (t >= q.T) return;  // no barrier follows
   float s[4], ds[4] = {0.f, 0.f, 0.f, 0.f};
-  const float* row = scores + (int64_t)t * E;
-  load_row<V4>(row, E, lane, s);
+  load_row<V4>(scores + (int64_t)t * E, E, lane, s);
+  int id = -1;
+  float d = 0.f;
+  if (dw && lane < K) {
+    id = ids[(int64_t)t * K + lane];
+    d = dw[(int64_t)t * K + lane];
+  }
   if (dloss) {
-    const int b = q.off ? wave_prefix_count(q.B, [&](int i) { return q.at(i + 1) <= t; }) : 0;
-    const int lo = b < q.B ? q.at(b) : 0, n = b < q.B ? q.at(b + 1) - lo : 0;
-    if (n > 0 && t >= lo) {
-      // a double's range: n^2 may pass the 24 bits of a float
-      const float c = (float)((double)dloss[b] * alpha / ((double)K * n * n));
+    int b, lo, hi;
+    if (!q.off) {
+      b = lo = 0;
+      hi = q.T;
+    } else if (q.B <= 64) {
+      const int first = q.at(0);
+      const int end = q.at(lane < q.B ? lane + 1 : q.B);
+      b = __popcll(__ballot(lane < q.B && end <= t));
+      lo = b ? __builtin_amdgcn_readlane(end, b - 1) : first;
+      hi = __builtin_amdgcn_readlane(end, min(b, 63));
+    } else {
+      b = wave_prefix_count(q.B, [&](int i) { return q.at(i + 1) <= t; });
+      lo = q.at(min(b, q.B - 1));
+      hi = q.at(min(b, q.B - 1) + 1);
+    }
+    const int n = hi - lo;
+    if (b < q.B && n > 0 && t >= lo) {  // else padding
       const int32_t* cb = counts + (int64_t)b * E;
-      float g[4], tot = 0.f, dot = 0.f;
+      int cnt[4];
+      if constexpr (V4) {
+        int4 c4 = {0, 0, 0, 0};
+        if (4 * lane < E) c4 = *reinterpret_cast<const int4*>(cb + 4 * lane);
+        cnt[0] = c4.x;
+        cnt[1] = c4.y;
+        cnt[2] = c4.z;
+        cnt[3] = c4.w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) cnt[i] = lane + 64 * i < E ? cb[lane + 64 * i] : 0;
+      }
+      const float c = dloss[b] * alpha / ((float)K * n * n);
+      float g[4];
+      // E count - K n, exact: in 24-bit products while K n (>= count) fits one, else in FP64.
+      // Past E the score is 0 and the result is not stored.
+      if ((int64_t)K * n < (1 << 23)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) g[i] = (float)(__mul24(cnt[i], E) - K * n);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) g[i] = (float)((double)cnt[i] * E - (double)K * n);
+      }
+      float tot = 0.f, dot = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int e = expert_of<V4>(lane, i);
-        g[i] = e < E ? (float)((int64_t)cb[e] * E - (int64_t)K * n) : 0.f;
         tot += s[i];
         dot += g[i] * s[i];
       }
       tot = wave_sum(tot);
       dot = wave_sum(dot);
       const float inv = tot == 0.f ? 0.f : 1.f / tot;
-      const float m = dot * inv;
+      const float m = dot * inv, ci = c * inv;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) ds[i] = c * ((g[i] - m) * inv);
+      for (int i = 0; i < 4; ++i) ds[i] = ci * (g[i] - m);
     }
   }
   if (dw) {
-    int id = -1;
-    float d = 0.f, sk = 0.f;
-    if (lane < K) {
-      id = ids[(int64_t)t * K + lane];
-      d = dw[(int64_t)t * K + lane];
-      if (id < 0 || id >= E)
-        id = -1;
-      else
-        sk = row[id];
-    }
-    if (id < 0) d = 0.f;
-    const float tot = wave_sum(sk), dot = wave_sum(d * sk);
+    float* row = reinterpret_cast<float*>(rows[wave]);
+    auto in_order = [] {  // LDS operations of one wave execute in order; this keeps the compiler to it
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    };
+    const bool ok = id >= 0 && id < E;
+    const int place = V4 ? id : 4 * (id & 63) + (id >> 6);
+    rows[wave][lane] = f32x4{s[0], s[1], s[2], s[3]};
+    in_order();
+    const float sk = ok ? row[place] : 0.f;
+    in_order();
+    rows[wave][lane] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (!ok) d = 0.f;
+    // K <= 16: the slots all lie in the first 16 lanes
+    const float tot = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(row16_sum(sk)), 0));
+    const float dot = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(row16_sum(d * sk)), 0));
     const float inv = tot == 0.f ? 0.f : 1.f / tot;
     const float a = scale * inv * (d - dot * inv);
+    // slots of one expert: each holds the sum over all of them, in slot order
+    float all = 0.f;
     for (int k = 0; k < K; ++k) {
       const int ik = __builtin_amdgcn_readlane(id, k);
       const float ak = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(a), k));
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (expert_of<V4>(lane, i) == ik) ds[i] += ak;
+      all += id == ik ? ak : 0.f;
     }
+    in_order();
+    if (ok) row[place] = all;
+    in_order();
+    const f32x4 add = rows[wave][lane];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ds[i] += add[i];
   }
   float* out = dlogits + (int64_t)t * E;
   float o[4];
+  // an expert without any gradient has 0 whatever its score holds (padding may hold anything)
 #pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = ds[i] * s[i] * (1.f - s[i]);
+  for (int i = 0; i < 4; ++i) o[i] = ds[i] == 0.f ? 0.f : ds[i] * s[i] * (1.f - s[i]);
   if constexpr (V4) {
     if (4 * lane < E) *reinterpret_cast<f32x4*>(out + 4 * lane) = f32x4{o[0], o[1], o[2], o[3]};
   } else {
@@ -331,8 +388,9 @@ hipError_t launch_route_backward(const float* scores, const int32_t* ids, const 
                                  const int32_t* off, float alpha, const float* dloss, const int32_t* counts,
                                  float* dlogits, int T, int E, int K, hipStream_t st) {
   const Sequences q{off, B, T};
-  hipLaunchKernelGGL(balance_v4(E) ? route_backward_kernel<true> : route_backward_kernel<false>, dim3((T + 3) / 4),
-                     dim3(256), 0, st, scores, ids, dw, scale, q, alpha, dloss, counts, dlogits, E, K);
+  hipLaunchKernelGGL(balance_v4(E) ? route_backward_kernel<true> : route_backward_kernel<false>,
+                     dim3((T + kGradWaves - 1) / kGradWaves), dim3(64 * kGradWaves), 0, st, scores, ids, dw, scale, q,
+                     alpha, dloss, counts, dlogits, E, K);
   return hipGetLastError();
 }
 

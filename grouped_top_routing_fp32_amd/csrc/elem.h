@@ -27,26 +27,36 @@ struct F32 {
   __device__ static S down(float f) { return f; }
 };
 
-// N = 1, or 8 elements from an address aligned to 16 bytes.
+// N = 1, or 8 elements from an address aligned to 16 bytes: as they lie in memory
+// (so that a load can be requested before its values are wanted), and as FP32.
+template <class T, int N>
+struct Raw {
+  static constexpr int kWords = N * sizeof(typename T::S) / 16;  // N = 8: 1 or 2
+  u32x4 w[kWords];
+  __device__ __forceinline__ void load(const typename T::S* p) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = reinterpret_cast<const u32x4*>(p)[i];
+  }
+  __device__ __forceinline__ float operator[](int i) const {
+    if constexpr (sizeof(typename T::S) == 4)
+      return __uint_as_float(w[i / 4][i % 4]);
+    else
+      return T::up((uint16_t)(w[0][i / 2] >> (16 * (i % 2))));
+  }
+};
+template <class T>
+struct Raw<T, 1> {
+  typename T::S s;
+  __device__ __forceinline__ void load(const typename T::S* p) { s = *p; }
+  __device__ __forceinline__ float operator[](int) const { return T::up(s); }
+};
+
 template <class T, int N>
 __device__ __forceinline__ void load_n(const typename T::S* p, float* v) {
-  if constexpr (N == 1) {
-    v[0] = T::up(*p);
-  } else if constexpr (sizeof(typename T::S) == 4) {
-    const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+  Raw<T, N> r;
+  r.load(p);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      v[q] = a[q];
-      v[q + 4] = b[q];
-    }
-  } else {
-    const u32x4 r = *reinterpret_cast<const u32x4*>(p);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      v[2 * q] = T::up((uint16_t)(r[q] & 0xFFFFu));
-      v[2 * q + 1] = T::up((uint16_t)(r[q] >> 16));
-    }
-  }
+  for (int i = 0; i < N; ++i) v[i] = r[i];
 }
 
 template <class T, int N>

@@ -17,6 +17,7 @@ namespace beam {
 
 constexpr int kLnMaxThreads = 1024;
 constexpr int kLnMaxWaves = kLnMaxThreads / 64;
+constexpr int kLnMaxJoin = 4096;  // columns of rows that share a workgroup with others
 static_assert(kLnMaxWaves == 16, "16 lanes join the waves' sums");
 
 // Forward.  Statistics: each wave takes the mean m of its own columns, then the sum of
@@ -99,52 +100,79 @@ __global__ __launch_bounds__(kLnMaxThreads) void layer_norm_kernel(
   }
 }
 
-// Backward.  Unit u (one team) takes rows u, u + units, ...; a thread's columns
-// stay the same from row to row, so it sums their dgamma and dbeta in registers
-// and writes them once, as row u of part [2][units][H], which
+// Backward.  A workgroup of blockDim.y teams takes rows blockIdx.x * blockDim.y + team,
+// then those gridDim.x * blockDim.y further on; a thread's columns stay the same from
+// row to row, so it sums their dgamma and dbeta in registers.  At the end the teams add
+// up in LDS, in order, and the workgroup writes one row of part [2][gridDim.x][H], which
 // column_sums_kernel adds up: no atomics, so the sums' order is fixed.
 template <class DT, class XT, int VEC, int NCH>
 __global__ __launch_bounds__(kLnMaxThreads) void layer_norm_backward_kernel(
     const typename DT::S* __restrict__ dy, int64_t lddy, const typename XT::S* __restrict__ x, int64_t ldx,
     const float* __restrict__ mean, const float* __restrict__ rstd, const float* __restrict__ gamma,
-    typename XT::S* __restrict__ dx, int64_t lddx, float* __restrict__ part, int T, int H, int units) {
+    typename XT::S* __restrict__ dx, int64_t lddx, float* __restrict__ part, int T, int H) {
   __shared__ float red[2][kLnMaxWaves][2];
-  const int tid = threadIdx.x, team = blockDim.x, wave = tid >> 6, nw = team >> 6;
-  const int unit = blockIdx.x * blockDim.y + threadIdx.y;
-  if (unit >= units) return;
+  __shared__ __align__(16) float joined[2][kLnMaxJoin];
+  const int tid = threadIdx.x, team = blockDim.x, nw = team >> 6;
+  const int wave0 = threadIdx.y * nw, wave = wave0 + (tid >> 6);
+  const int teams = blockDim.y, stride = gridDim.x * teams;
   const int nch = H / VEC;
-  float g[NCH][VEC], dg[NCH][VEC], db[NCH][VEC];
+  // few columns to a thread: gamma stays in registers, and rows are requested one ahead
+  constexpr bool kAhead = NCH * VEC <= 8;
+  float g[NCH][VEC], dg[NCH][VEC] = {}, db[NCH][VEC] = {};
+  auto load_gamma = [&](int c) __attribute__((always_inline)) {
 #pragma unroll
-  for (int c = 0; c < NCH; ++c) {
-#pragma unroll
-    for (int q = 0; q < VEC; ++q) {
-      g[c][q] = 1.f;
-      dg[c][q] = db[c][q] = 0.f;
-    }
+    for (int q = 0; q < VEC; ++q) g[c][q] = 1.f;
     if (gamma && tid + c * team < nch) load_n<F32, VEC>(gamma + (tid + c * team) * VEC, g[c]);
+  };
+  if (kAhead) {
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) load_gamma(c);
   }
-  int buf = 0;
-  for (int t = unit; t < T; t += units, buf ^= 1) {
-    const float mu = mean[t], rs = rstd[t];
-    float xh[NCH][VEC], gy[NCH][VEC];
-    float s1 = 0.f, s2 = 0.f;
+  Raw<XT, VEC> xr[NCH];
+  Raw<DT, VEC> yr[NCH];
+  float mu = 0.f, rs = 0.f;
+  auto request = [&](int t) __attribute__((always_inline)) {
+    if (t >= T) return;
+    mu = mean[t];
+    rs = rstd[t];
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
       const int ch = tid + c * team;
       if (ch < nch) {
-        load_n<XT, VEC>(x + (int64_t)t * ldx + (int64_t)ch * VEC, xh[c]);
-        load_n<DT, VEC>(dy + (int64_t)t * lddy + (int64_t)ch * VEC, gy[c]);
+        xr[c].load(x + (int64_t)t * ldx + (int64_t)ch * VEC);
+        yr[c].load(dy + (int64_t)t * lddy + (int64_t)ch * VEC);
+      }
+    }
+  };
+  if (kAhead) request(blockIdx.x * teams + threadIdx.y);
+  int buf = 0;
+  // every team makes the same number of rounds; one past the end has no row in the last
+  for (int t0 = blockIdx.x * teams; t0 < T; t0 += stride, buf ^= 1) {
+    const int t = t0 + threadIdx.y;
+    const bool live = t < T;
+    float xh[NCH][VEC], gy[NCH][VEC];
+    float s1 = 0.f, s2 = 0.f;
+    if (!kAhead) request(t);
+    const float r = rs;
+    if (live) {
 #pragma unroll
-        for (int q = 0; q < VEC; ++q) {
-          xh[c][q] = (xh[c][q] - mu) * rs;
-          dg[c][q] += gy[c][q] * xh[c][q];
-          db[c][q] += gy[c][q];
-          gy[c][q] *= g[c][q];
-          s1 += gy[c][q];
-          s2 += gy[c][q] * xh[c][q];
+      for (int c = 0; c < NCH; ++c) {
+        if (!kAhead) load_gamma(c);
+        if (tid + c * team < nch) {
+#pragma unroll
+          for (int q = 0; q < VEC; ++q) {
+            xh[c][q] = (xr[c][q] - mu) * r;
+            gy[c][q] = yr[c][q];
+            dg[c][q] += gy[c][q] * xh[c][q];
+            db[c][q] += gy[c][q];
+            gy[c][q] *= g[c][q];
+            s1 += gy[c][q];
+            s2 += gy[c][q] * xh[c][q];
+          }
         }
       }
     }
+    if (kAhead) request(t + stride);  // the next row comes in while this one is reduced and written
     s1 = wave_sum(s1);
     s2 = wave_sum(s2);
     if (nw > 1) {  // two buffers: the next row's sums do not wait for this row's readers
@@ -154,10 +182,10 @@ __global__ __launch_bounds__(kLnMaxThreads) void layer_norm_backward_kernel(
       }
       __syncthreads();
       const int w = tid & 15;  // every 16 lanes add the waves' sums among themselves
-      s1 = row16_sum(w < nw ? red[buf][w][0] : 0.f);
-      s2 = row16_sum(w < nw ? red[buf][w][1] : 0.f);
+      s1 = row16_sum(w < nw ? red[buf][wave0 + w][0] : 0.f);
+      s2 = row16_sum(w < nw ? red[buf][wave0 + w][1] : 0.f);
     }
-    if (dx) {
+    if (dx && live) {
       const float c1 = s1 / H, c2 = s2 / H;
 #pragma unroll
       for (int c = 0; c < NCH; ++c) {
@@ -165,23 +193,39 @@ __global__ __launch_bounds__(kLnMaxThreads) void layer_norm_backward_kernel(
         if (ch < nch) {
           float o[VEC];
 #pragma unroll
-          for (int q = 0; q < VEC; ++q) o[q] = rs * (gy[c][q] - c1 - xh[c][q] * c2);
+          for (int q = 0; q < VEC; ++q) o[q] = r * (gy[c][q] - c1 - xh[c][q] * c2);
           store_n<XT, VEC>(dx + (int64_t)t * lddx + (int64_t)ch * VEC, o);
         }
       }
     }
   }
-  if (part) {
-    float* pg = part + (int64_t)unit * H;
-    float* pb = part + ((int64_t)units + unit) * H;
+  if (!part) return;
+  float* pg = part + (int64_t)blockIdx.x * H;
+  float* pb = part + ((int64_t)gridDim.x + blockIdx.x) * H;
+  for (int y = 0; y < teams; ++y) {
+    if ((int)threadIdx.y == y) {
 #pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-      const int ch = tid + c * team;
-      if (ch < nch) {
-        store_n<F32, VEC>(pg + (int64_t)ch * VEC, dg[c]);
-        store_n<F32, VEC>(pb + (int64_t)ch * VEC, db[c]);
+      for (int c = 0; c < NCH; ++c) {
+        const int col = (tid + c * team) * VEC;
+        if (col < H) {
+          if (y > 0) {  // teams > 1: H <= kLnMaxJoin
+#pragma unroll
+            for (int q = 0; q < VEC; ++q) {
+              dg[c][q] += joined[0][col + q];
+              db[c][q] += joined[1][col + q];
+            }
+          }
+          if (y + 1 < teams) {
+            store_n<F32, VEC>(&joined[0][col], dg[c]);
+            store_n<F32, VEC>(&joined[1][col], db[c]);
+          } else {
+            store_n<F32, VEC>(pg + col, dg[c]);
+            store_n<F32, VEC>(pb + col, db[c]);
+          }
+        }
       }
     }
+    if (y + 1 < teams) __syncthreads();
   }
 }
 
@@ -238,7 +282,7 @@ struct Shape {
 
 Shape shape(int H, bool vec) {
   const int chunks = vec ? H / 8 : H;
-  const int nch = vec ? (chunks <= 1024 ? 1 : 2) : (chunks <= 4096 ? 4 : 16);
+  const int nch = vec ? (chunks <= 1024 ? 1 : 2) : (chunks <= 4096 ? 4 : chunks <= 8192 ? 8 : 16);
   Shape s;
   s.nch = nch;
   s.team = ((chunks + nch - 1) / nch + 63) / 64 * 64;
@@ -257,8 +301,9 @@ hipError_t by_chunks(bool vec, int nch, F f) {
   if (vec)
     return nch == 1 ? f(integral_constant<int, 8>{}, integral_constant<int, 1>{})
                     : f(integral_constant<int, 8>{}, integral_constant<int, 2>{});
-  return nch == 4 ? f(integral_constant<int, 1>{}, integral_constant<int, 4>{})
-                  : f(integral_constant<int, 1>{}, integral_constant<int, 16>{});
+  return nch == 4   ? f(integral_constant<int, 1>{}, integral_constant<int, 4>{})
+         : nch == 8 ? f(integral_constant<int, 1>{}, integral_constant<int, 8>{})
+                    : f(integral_constant<int, 1>{}, integral_constant<int, 16>{});
 }
 
 }  // namespace
@@ -283,10 +328,20 @@ hipError_t launch_layer_norm(const void* x, int x_type, int64_t ldx, const float
   });
 }
 
-// Rows of partial column sums the backward kernel writes.
+// Teams of a backward workgroup, and workgroups (rows of partial column sums): as many
+// teams as 1024 threads hold, one workgroup to a CU.  More of either costs more in
+// partial sums than it gains: [8192, 5120] fp32 / bf16 82 us with 256 workgroups, 84
+// with 192, 93 with 512; [1021, 2561] fp16 16, 16 and 22 us.
+static int backward_teams(int H, bool vec) { return H <= kLnMaxJoin ? kLnMaxThreads / shape(H, vec).team : 1; }
+static int backward_groups(int T, int teams) {
+  const int n = (T + teams - 1) / teams;
+  return n < 256 ? n : 256;
+}
+
+// The most rows of partial sums of a call on rows of H columns, whatever their strides.
 int layer_norm_backward_units(int T, int H) {
   (void)H;
-  return T < 512 ? T : 512;
+  return T < 256 ? T : 256;
 }
 
 hipError_t launch_layer_norm_backward(const void* dy, int dy_type, int64_t lddy, const void* x, int x_type,
@@ -295,7 +350,7 @@ hipError_t launch_layer_norm_backward(const void* dy, int dy_type, int64_t lddy,
                                       hipStream_t st) {
   const bool vec = wide(H, {lddy, ldx, dx ? lddx : 0});
   const Shape s = shape(H, vec);
-  const int units = layer_norm_backward_units(T, H);
+  const int teams = backward_teams(H, vec), units = backward_groups(T, teams);
   const bool sums = dgamma || dbeta;
   hipError_t e = by_type(dy_type, [&](auto dt) {
     return by_type(x_type, [&](auto xt) {
@@ -303,10 +358,9 @@ hipError_t launch_layer_norm_backward(const void* dy, int dy_type, int64_t lddy,
         using DT = decltype(dt);
         using XT = decltype(xt);
         hipLaunchKernelGGL((layer_norm_backward_kernel<DT, XT, decltype(v)::value, decltype(n)::value>),
-                           dim3((units + s.rows - 1) / s.rows), dim3(s.team, s.rows), 0, st,
-                           static_cast<const typename DT::S*>(dy), lddy, static_cast<const typename XT::S*>(x), ldx,
-                           mean, rstd, gamma, static_cast<typename XT::S*>(dx), lddx, sums ? part : nullptr, T, H,
-                           units);
+                           dim3(units), dim3(s.team, teams), 0, st, static_cast<const typename DT::S*>(dy), lddy,
+                           static_cast<const typename XT::S*>(x), ldx, mean, rstd, gamma,
+                           static_cast<typename XT::S*>(dx), lddx, sums ? part : nullptr, T, H);
         return hipGetLastError();
       });
     });

@@ -341,7 +341,7 @@ int beam_moe_layer_norm(int32_t rows, int32_t cols, const void* x, int x_type, i
                         void* stream);
 
 /* Workspace of beam_moe_layer_norm_backward (partial column sums, at most
- * 8 * 512 * cols bytes).  Returns SIZE_MAX for unsupported sizes. */
+ * 8 * 256 * cols bytes).  Returns SIZE_MAX for unsupported sizes. */
 size_t beam_moe_layer_norm_backward_workspace_bytes(int32_t rows, int32_t cols);
 
 /* Its gradients: with xh = (x - mean) * rstd and g = dy * gamma,

@@ -141,14 +141,14 @@ def _norm_back_ref(dy, x, mean, rstd, gamma):
 
 def _norm_back_check(dy, x, mean, rstd, gamma, out):
     """dx: two row sums of depth <= 64 of g and g xh, whose factors carry a few steps each.
-    Column sums: T / 512 rows in a unit (of <= 4 rows a workgroup), 32 units a thread, 16 joined."""
+    Column sums: a team's rows, up to 16 teams of a workgroup, 16 of at most 256 workgroups a thread, 16 joined."""
     T = x.shape[0]
     rdx, rdg, rdb, hat, g = _norm_back_ref(dy, x, mean, rstd, gamma)
     dx, dg, db = out
     rs = rstd.double()[:, None]
     a, b = g.abs().mean(1, keepdim=True), (g * hat).abs().mean(1, keepdim=True)
     _near(dx, rdx, U * rs * (6 * g.abs() + 70 * a + hat.abs() * 76 * b), "dx")
-    depth = math.ceil(T / 512) + 512 / 16 + 24
+    depth = math.ceil(T / 256) + 16 + 16 + 24
     _near(dg, rdg, depth * U * (dy.double() * hat).abs().sum(0), "dgamma")
     _near(db, rdb, depth * U * dy.double().abs().sum(0), "dbeta")
 
@@ -343,6 +343,29 @@ def test_route_backward(T, E, K, lens, lead):
                                          counts=counts if l is not None else None)
         want, mag = _route_back_ref(scores, ids, w, 2.5, off, 0.5, l, counts, K)
         _near(got, want, 40 * U * mag, (w is None, l is None))
+
+
+@pytest.mark.parametrize("E", [100, 256])
+def test_route_backward_keeps_nan_in_its_token(E):
+    """A token's NaN stays in its row; padding has zeros whatever its scores hold, and where it has weights,
+    their part alone."""
+    _say("route_backward nan", E)
+    T, K, lens = 90, 4, [20, 30, 20]
+    scores, ids, off = _problem(T, E, K, lens, 3)
+    o = torch.tensor(off, dtype=torch.int32, device=DEV)
+    dw, dloss = torch.ones((T, K), device=DEV), torch.ones(3, device=DEV)
+    counts = _balance_ref(scores, ids, off, 1.0, K)[1].int()
+    args = dict(dloss=dloss, counts=counts, alpha=1.0, seq_offsets=o)
+    clean, loss_only = (fw.beam_moe_route_backward(_dims(E, K), scores, ids, dw=w, **args) for w in (dw, None))
+    assert not loss_only[70:].any()
+    scores[25, 7] = float("nan")
+    scores[80:] = float("nan")
+    got, got_loss = (fw.beam_moe_route_backward(_dims(E, K), scores, ids, dw=w, **args) for w in (dw, None))
+    rows = torch.arange(T, device=DEV)
+    keep = (rows != 25) & (rows < 80)
+    assert torch.equal(got[keep], clean[keep]) and torch.equal(got_loss[keep], loss_only[keep])
+    assert got_loss[25].isnan().all() and not got_loss[80:].any()
+    assert fw.beam_moe_route_backward(_dims(E, K), scores, ids, dw=dw)[:20].isfinite().all()
 
 
 def test_route_gradient_against_differences():
