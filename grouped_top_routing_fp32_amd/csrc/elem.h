@@ -7,6 +7,8 @@
 
 namespace beam {
 
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
 // Values of the ABI's element type arguments (BEAM_MOE_BF16, _F16, _F32).
 enum ElemType { kElemBF16 = 0, kElemF16 = 1, kElemF32 = 2 };
 

@@ -24,8 +24,9 @@ __device__ const u32x4 zero_chunk = {0u, 0u, 0u, 0u};
 // 1 KB fills 8 rows from 128 contiguous bytes each.
 // Transposed (TR): LDS rows of one k, R elements.  A fragment needs 8 consecutive k of a
 // column; the transposing LDS read delivers 4 of them, taking 16 columns (32 bytes) of 4
-// rows per 16 lanes.  The 32-byte granule g of row k sits at g ^ ((k & 3) | (k >> 1 & 4)):
-// the 8 rows that 32 lanes read together fall on distinct banks.
+// rows per 16 lanes.  The 32-byte granule g of row k sits at g ^ ((k & 3) | (k >> 1 & 4))
+// (R = 64, where two rows make up all banks: g ^ (k >> 1 & 1 | k >> 2 & 2)): the 8 rows
+// that 32 lanes read together fall on distinct banks.
 template <bool TR, int R, int NW>
 struct Side {
   static constexpr int kCopies = R / 8 / NW;     // per wave and stage
@@ -34,7 +35,10 @@ struct Side {
   const uint16_t* src[kCopies];
   int64_t step;
 
-  static __device__ __forceinline__ int swz(int r) { return TR ? ((r & 3) | ((r >> 1) & 4)) << 1 : (r >> 1) & 7; }
+  static __device__ __forceinline__ int swz(int r) {
+    if (!TR) return (r >> 1) & 7;
+    return (R == 64 ? ((r >> 1) & 1) | ((r >> 2) & 2) : (r & 3) | ((r >> 1) & 4)) << 1;
+  }
   // LDS row and source chunk of this lane in copy q
   static __device__ __forceinline__ int row(int q, int wave, int lane) {
     return (wave * kCopies + q) * kCopyRows + lane / kRowChunks;
@@ -136,7 +140,7 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(GemmArgs g, int mt, i
     __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
     __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_s_barrier();  // the stage is there for every wave, and all are done with the other slot
     asm volatile("" ::: "memory");
     if (st + 1 < stages) issue((st + 1) & 1, k1 - k0 - (st + 1) * kBK);
     const lds_u16* A = lds + (st & 1) * kSlot;
@@ -161,8 +165,8 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(GemmArgs g, int mt, i
   // every wave takes whole rows of the tile, four columns to a lane, so memory sees full
   // lines.  16-byte chunk c of row r sits at c ^ (r & 15): the 16 rows that a wave writes
   // at once fall on distinct banks.
-  constexpr int kPasses = BM * BN * 4 / (2 * kSlot * 2), kPassRows = BM / kPasses;
-  static_assert(kPasses * 2 * kSlot * 2 == BM * BN * 4 && WM % kPasses == 0, "a pass fills the ring");
+  constexpr int kPasses = (BM * BN * 4 + 2 * kSlot * 2 - 1) / (2 * kSlot * 2), kPassRows = BM / kPasses;
+  static_assert(BM % kPasses == 0 && WM % kPasses == 0, "whole wave rows in a pass");
   f32x4* sums = reinterpret_cast<f32x4*>(ring);
   constexpr int kQuads = BN / 4, kRowsAtOnce = 64 * NW / kQuads;
   const int qn = tid % kQuads, qr = tid / kQuads;
@@ -185,17 +189,19 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(GemmArgs g, int mt, i
   const bool wide = epilogue_wide(g);
 
   // Tiles inside the result: batches of kBatch rows to a thread, the residual of the next
-  // batch requested as this one's is used, so its latency shows once per tile.
-  constexpr int kBatch = 8, kBatches = kPassRows / kRowsAtOnce / kBatch;
+  // batch requested as this one's is used, so its latency shows once per tile.  A residual and
+  // an FP32 result pass the caches by, which keep the operands: 500 -> 479 us at
+  // [16384, 2560] x [5120, 2560] onto an FP32 stream.
+  constexpr int kIters = kPassRows / kRowsAtOnce, kBatch = kIters < 8 ? kIters : 8, kBatches = kIters / kBatch;
   static_assert(kBatches * kBatch * kRowsAtOnce == kPassRows, "whole batches");
   if (EPI && wide && !part && m0 + BM <= g.M && n0 + BN <= g.N) {
     auto inside = [&](auto out_type, auto act) __attribute__((always_inline)) {
       using OT = decltype(out_type);
-      using Raw = std::conditional_t<sizeof(typename OT::S) == 4, f32x4, uint2>;
+      using Raw = std::conditional_t<sizeof(typename OT::S) == 4, f32x4, u32x2>;
       const typename OT::S* res = static_cast<const typename OT::S*>(g.res) + (int64_t)(m0 + qr) * g.ldr + n;
       Raw rv[kBatch] = {};
       auto request = [&](int u, int row) __attribute__((always_inline)) {
-        if (g.res) rv[u] = *reinterpret_cast<const Raw*>(res + (int64_t)row * g.ldr);
+        if (g.res) rv[u] = __builtin_nontemporal_load(reinterpret_cast<const Raw*>(res + (int64_t)row * g.ldr));
       };
       f32x4 bias = {0.f, 0.f, 0.f, 0.f};
       if (g.bias) bias = *reinterpret_cast<const f32x4*>(g.bias + n);
@@ -213,7 +219,7 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(GemmArgs g, int mt, i
           if constexpr (sizeof(typename OT::S) == 4) {
             r = rv[u];
           } else {
-            const uint32_t h[2] = {rv[u].x, rv[u].y};
+            const uint32_t h[2] = {rv[u][0], rv[u][1]};
 #pragma unroll
             for (int q = 0; q < 4; ++q) r[q] = OT::up((uint16_t)(h[q / 2] >> (16 * (q % 2))));
           }
@@ -229,7 +235,10 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(GemmArgs g, int mt, i
             for (int q = 0; q < 4; ++q) v[q] += g.keep * r[q];
           }
           if (g.pre) store_elem4(g.pre, (int64_t)m * g.ldp + n, g.type, z);
-          store_elem4(g.out, (int64_t)m * g.ldo + n, sizeof(typename OT::S) == 4 ? kElemF32 : g.type, v);
+          if constexpr (sizeof(typename OT::S) == 4)
+            __builtin_nontemporal_store(v, reinterpret_cast<f32x4*>(static_cast<float*>(g.out) + (int64_t)m * g.ldo + n));
+          else
+            store_elem4(g.out, (int64_t)m * g.ldo + n, g.type, v);
         }
       }
     };
@@ -276,9 +285,14 @@ hipError_t launch_gemm_tiles(const GemmArgs& g, const GemmPlan& p, float* part, 
     if (!g.at) return go(gemm_kernel<HALF, false, true, 256, 256, 4, 2, false>, 512);
     return go(gemm_kernel<HALF, true, true, 256, 256, 4, 2, false>, 512);
   }
-  if (!g.at && !g.bt) return go(gemm_kernel<HALF, false, false, 128, 128, 2, 2, true>, 256);
-  if (!g.at) return go(gemm_kernel<HALF, false, true, 128, 128, 2, 2, false>, 256);
-  return go(gemm_kernel<HALF, true, true, 128, 128, 2, 2, false>, 256);
+  if (p.tile == 128) {
+    if (!g.at && !g.bt) return go(gemm_kernel<HALF, false, false, 128, 128, 2, 2, true>, 256);
+    if (!g.at) return go(gemm_kernel<HALF, false, true, 128, 128, 2, 2, false>, 256);
+    return go(gemm_kernel<HALF, true, true, 128, 128, 2, 2, false>, 256);
+  }
+  if (!g.at && !g.bt) return go(gemm_kernel<HALF, false, false, 64, 64, 2, 2, true>, 256);
+  if (!g.at) return go(gemm_kernel<HALF, false, true, 64, 64, 2, 2, false>, 256);
+  return go(gemm_kernel<HALF, true, true, 64, 64, 2, 2, false>, 256);
 }
 
 }  // namespace beam

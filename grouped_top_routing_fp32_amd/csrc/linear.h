@@ -36,16 +36,29 @@ struct GemmArgs {
 // How a product runs: which kernel, and the workspace it needs (bytes from its start).
 struct GemmPlan {
   enum Kind { kSkinny, kTiles } kind;
-  int tile;            // kTiles: 256 or 128, rows and columns of an output tile
+  int tile;            // kTiles: 256, 128 or 64, rows and columns of an output tile
   int splits;          // of K; above 1 the partial sums go through the workspace
   int k_per_split;     // multiple of 64
   bool copy_a, copy_b; // the operand is laid out anew in the workspace
   size_t off_a, off_b, off_part, total;
 };
 // Operand shapes and leading dimensions decide alone, so a size query and its call agree.
-// padded_a: A's rows are whole chunks of 8 elements (zeros past the end), whatever M and K are.
-GemmPlan plan_gemm(int M, int N, int K, bool at, bool bt, int64_t lda, int64_t ldb, bool padded_a = false);
+// padded: both operands' rows are whole chunks of 8 elements (zeros past the end of K), whatever the sizes.
+GemmPlan plan_gemm(int M, int N, int K, bool at, bool bt, int64_t lda, int64_t ldb, bool padded = false);
 hipError_t launch_gemm(const GemmArgs& g, const GemmPlan& p, void* ws, hipStream_t st);
+
+// A matrix to be laid out anew: dst rows of up8(cols) elements, zeros past cols.
+struct PadJob {
+  const void* src;
+  int64_t ld;
+  int rows, cols;  // rows 0: nothing to do
+  void* dst;
+};
+inline int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
+// Whether the tiled kernel's copies can take rows as they are: whole chunks of 8 elements on 16 bytes.
+inline bool regular_rows(int64_t ld, int cols) { return ld % 8 == 0 && cols % 8 == 0; }
+inline size_t padded_bytes(int rows, int cols) { return (size_t)rows * up8(cols) * 2; }
+hipError_t launch_pad(const PadJob& first, const PadJob& second, hipStream_t st);
 hipError_t launch_gemm_bf16(const GemmArgs& g, const GemmPlan& p, float* part, int64_t ldpart, hipStream_t st);
 hipError_t launch_gemm_f16(const GemmArgs& g, const GemmPlan& p, float* part, int64_t ldpart, hipStream_t st);
 

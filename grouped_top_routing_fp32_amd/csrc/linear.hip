@@ -31,22 +31,19 @@ __global__ __launch_bounds__(256) void gemm_join_kernel(GemmArgs g, const float*
   by_act(g.act, [&](auto act) { epilogue4<decltype(act)::value>(g, wide, m, n, z); });
 }
 
-// Few rows (M <= 64, both operands K contiguous): bound by reading w once.  A workgroup
+// Few rows (M <= 16, both operands K contiguous): bound by reading w once.  A workgroup
 // takes 16 columns; its 8 waves share K in pieces of 128, straight from memory into
 // MFMA operands (a wave reads 256 contiguous bytes of 16 rows of w), and their sums are
-// joined in LDS in wave order.  MT fragments of 16 rows.
+// joined in LDS in wave order.
 constexpr int kSkinnyWaves = 8;
 
-template <bool HALF, int MT, bool WIDE>
+template <bool HALF, bool WIDE>
 __global__ __launch_bounds__(64 * kSkinnyWaves) void gemm_skinny_kernel(GemmArgs g) {
-  __shared__ f32x4 sum[kSkinnyWaves][MT][64];
+  __shared__ f32x4 sum[kSkinnyWaves][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, gr = lane >> 4;
   const int n0 = blockIdx.x * 16;
   const uint16_t* wrow = static_cast<const uint16_t*>(g.b) + (int64_t)min(n0 + l16, g.N - 1) * g.ldb;
-  const uint16_t* xrow[MT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-    xrow[i] = static_cast<const uint16_t*>(g.a) + (int64_t)min(16 * i + l16, g.M - 1) * g.lda;
+  const uint16_t* xrow = static_cast<const uint16_t*>(g.a) + (int64_t)min(l16, g.M - 1) * g.lda;
   auto chunk = [&](const uint16_t* row, int k) {  // 8 elements from k, 0 past K
     if constexpr (WIDE) {
       u32x4 v = {0u, 0u, 0u, 0u};
@@ -62,52 +59,51 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void gemm_skinny_kernel(GemmArgs
       return v;
     }
   };
-  f32x4 acc[MT] = {};
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
   for (int k = 128 * wave; k < g.K; k += 128 * kSkinnyWaves) {
-    u32x4 fw[4], fx[4][MT];
+    u32x4 fw[4], fx[4];
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       fw[s] = chunk(wrow, k + 32 * s + 8 * gr);
-#pragma unroll
-      for (int i = 0; i < MT; ++i) fx[s][i] = chunk(xrow[i], k + 32 * s + 8 * gr);
+      fx[s] = chunk(xrow, k + 32 * s + 8 * gr);
     }
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
-#pragma unroll
-      for (int i = 0; i < MT; ++i) acc[i] = mfma<HALF>(fw[s], fx[s][i], acc[i]);
+    for (int s = 0; s < 4; ++s) acc = mfma<HALF>(fw[s], fx[s], acc);
   }
-#pragma unroll
-  for (int i = 0; i < MT; ++i) sum[wave][i][lane] = acc[i];
+  sum[wave][lane] = acc;
   __syncthreads();
-  if (wave >= MT) return;
-  f32x4 z = sum[0][wave][lane];
+  if (wave > 0) return;
+  f32x4 z = acc;
 #pragma unroll
   for (int w = 1; w < kSkinnyWaves; ++w) {
-    const f32x4 v = sum[w][wave][lane];
+    const f32x4 v = sum[w][lane];
 #pragma unroll
     for (int q = 0; q < 4; ++q) z[q] += v[q];
   }
-  const int m = 16 * wave + l16, n = n0 + 4 * gr;
-  if (m >= g.M || n >= g.N) return;
+  const int n = n0 + 4 * gr;
+  if (l16 >= g.M || n >= g.N) return;
   const bool wide = epilogue_wide(g);
-  by_act(g.act, [&](auto act) { epilogue4<decltype(act)::value>(g, wide, m, n, z); });
+  by_act(g.act, [&](auto act) { epilogue4<decltype(act)::value>(g, wide, l16, n, z); });
 }
 
-// Lays an operand out anew: dst [rows, ld], ld a multiple of 8, zeros past cols.
-__global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* __restrict__ src, int64_t lds, int rows, int cols,
-                                                       uint16_t* __restrict__ dst, int ld) {
-  const int chunks = ld / 8;
-  const int64_t n = (int64_t)rows * chunks;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+// Lays one or two operands out anew, the first with blocks workgroups and the second with
+// the rest: one launch for what a product or both gradients need.
+__global__ __launch_bounds__(256) void pad_rows_kernel(PadJob first, PadJob second, int blocks) {
+  const bool other = (int)blockIdx.x >= blocks;
+  const PadJob j = other ? second : first;
+  const int64_t threads = 256 * (int64_t)(other ? gridDim.x - blocks : blocks);
+  const int chunks = (j.cols + 7) / 8;
+  const int64_t n = (int64_t)j.rows * chunks;
+  for (int64_t i = (int64_t)(blockIdx.x - (other ? blocks : 0)) * 256 + threadIdx.x; i < n; i += threads) {
     const int r = (int)(i / chunks), c = (int)(i % chunks) * 8;
-    const uint16_t* s = src + (int64_t)r * lds;
+    const uint16_t* s = static_cast<const uint16_t*>(j.src) + (int64_t)r * j.ld;
     u32x4 v;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const uint32_t lo = c + 2 * q < cols ? s[c + 2 * q] : 0, hi = c + 2 * q + 1 < cols ? s[c + 2 * q + 1] : 0;
+      const uint32_t lo = c + 2 * q < j.cols ? s[c + 2 * q] : 0, hi = c + 2 * q + 1 < j.cols ? s[c + 2 * q + 1] : 0;
       v[q] = lo | (hi << 16);
     }
-    *reinterpret_cast<u32x4*>(dst + (int64_t)r * ld + c) = v;
+    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(j.dst) + ((int64_t)r * chunks + c / 8) * 8) = v;
   }
 }
 
@@ -186,18 +182,14 @@ namespace {
 
 constexpr int kBK = 64;  // K per stage of the tiled kernel
 constexpr int kCUs = 256;
-constexpr int kSkinnyRows = 64;
-
+// Up to here the skinny kernel: 2560 columns, K 5120: 11.3 us at 16 rows against 12.8 in
+// tiles; its form for 32 rows took 15.9 against 12.8.
+constexpr int kSkinnyRows = 16;
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
-int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
-
-// Whether the copies can take the operand as it is: whole chunks of 8 elements on 16 bytes.
-bool regular(int64_t ld, int contiguous) { return ld % 8 == 0 && contiguous % 8 == 0; }
-
 }  // namespace
 
-GemmPlan plan_gemm(int M, int N, int K, bool at, bool bt, int64_t lda, int64_t ldb, bool padded_a) {
+GemmPlan plan_gemm(int M, int N, int K, bool at, bool bt, int64_t lda, int64_t ldb, bool padded) {
   GemmPlan p{};
   p.splits = 1;
   p.k_per_split = K > 0 ? ceil_div(K, kBK) * kBK : kBK;
@@ -206,25 +198,37 @@ GemmPlan plan_gemm(int M, int N, int K, bool at, bool bt, int64_t lda, int64_t l
     return p;
   }
   p.kind = GemmPlan::kTiles;
-  p.copy_a = !padded_a && !regular(lda, at ? M : K);
-  p.copy_b = !regular(ldb, bt ? N : K);
-  const int big = ceil_div(M, 256) * ceil_div(N, 256);
-  p.tile = big >= 160 ? 256 : 128;
-  if (p.tile == 128 && M > 0) {
-    const int tiles = ceil_div(M, 128) * ceil_div(N, 128), stages = ceil_div(K, kBK);
-    int s = 2 * kCUs / tiles;               // two workgroups of 128 x 128 fit a CU
-    s = s < stages / 8 ? s : stages / 8;    // at least 8 stages each
+  p.copy_a = !padded && !regular_rows(lda, at ? M : K);
+  p.copy_b = !padded && !regular_rows(ldb, bt ? N : K);
+  // 256-row tiles from 160 of them on ([4096, 5120] x [2560, 5120], 160 tiles: 125 us, 134
+  // in 128-row tiles; [3000, ...], 120 tiles: 91 and 90).  Below, 128-row tiles with K
+  // split until two workgroups a CU (what LDS holds) have work, in at least 8 stages each;
+  // under 24 stages the join costs what a split gains.  64-row tiles where even split
+  // 128-row tiles would leave CUs without work: [1000, 1000] x [1000, 1000] forward and
+  // back 32 us, 41 in 128-row tiles; but [512, 5120] x [2560, 5120] 42 us, 28 in those.
+  const int stages = ceil_div(K, kBK);
+  int tiles = ceil_div(M, 256) * ceil_div(N, 256);
+  p.tile = 256;
+  if (tiles < 160) {
+    p.tile = 128;
+    tiles = ceil_div(M, 128) * ceil_div(N, 128);
+    if (tiles * (stages / 8 + 1) < kCUs) {
+      p.tile = 64;
+      tiles = ceil_div(M, 64) * ceil_div(N, 64);
+    }
+    int s = tiles > 0 ? 2 * kCUs / tiles : 1;
+    s = s < stages / 8 ? s : stages / 8;
     s = s < 16 ? s : 16;
-    if (s > 1) {
+    if (s > 1 && stages >= 24) {
       p.k_per_split = ceil_div(stages, s) * kBK;
       p.splits = ceil_div(K, p.k_per_split);
     }
   }
   size_t off = 0;
   p.off_a = off;
-  if (p.copy_a) off = up256(off + (size_t)(at ? K : M) * up8(at ? M : K) * 2);
+  if (p.copy_a) off = up256(off + padded_bytes(at ? K : M, at ? M : K));
   p.off_b = off;
-  if (p.copy_b) off = up256(off + (size_t)(bt ? K : N) * up8(bt ? N : K) * 2);
+  if (p.copy_b) off = up256(off + padded_bytes(bt ? K : N, bt ? N : K));
   p.off_part = off;
   if (p.splits > 1) off = up256(off + (size_t)p.splits * M * ((N + 3) / 4 * 4) * sizeof(float));
   p.total = off;
@@ -233,52 +237,46 @@ GemmPlan plan_gemm(int M, int N, int K, bool at, bool bt, int64_t lda, int64_t l
 
 namespace {
 
-template <bool HALF, int MT>
-void skinny(const GemmArgs& g, bool wide, hipStream_t st) {
-  const dim3 grid(ceil_div(g.N, 16)), block(64 * kSkinnyWaves);
-  if (wide)
-    hipLaunchKernelGGL((gemm_skinny_kernel<HALF, MT, true>), grid, block, 0, st, g);
-  else
-    hipLaunchKernelGGL((gemm_skinny_kernel<HALF, MT, false>), grid, block, 0, st, g);
-}
-
 template <bool HALF>
 hipError_t launch_skinny(const GemmArgs& g, hipStream_t st) {
-  const bool wide = regular(g.lda, g.K) && regular(g.ldb, g.K);
-  if (g.M <= 16)
-    skinny<HALF, 1>(g, wide, st);
-  else if (g.M <= 32)
-    skinny<HALF, 2>(g, wide, st);
+  const bool wide = regular_rows(g.lda, g.K) && regular_rows(g.ldb, g.K);
+  const dim3 grid(ceil_div(g.N, 16)), block(64 * kSkinnyWaves);
+  if (wide)
+    hipLaunchKernelGGL((gemm_skinny_kernel<HALF, true>), grid, block, 0, st, g);
   else
-    skinny<HALF, 4>(g, wide, st);
-  return hipGetLastError();
-}
-
-hipError_t pad_rows(const void* src, int64_t ld, int rows, int cols, void* dst, hipStream_t st) {
-  const int64_t blocks = (rows * (up8(cols) / 8) + 255) / 256;
-  hipLaunchKernelGGL(pad_rows_kernel, dim3((uint32_t)(blocks < (1 << 20) ? blocks : 1 << 20)), dim3(256), 0, st,
-                     static_cast<const uint16_t*>(src), ld, rows, cols, static_cast<uint16_t*>(dst), (int)up8(cols));
+    hipLaunchKernelGGL((gemm_skinny_kernel<HALF, false>), grid, block, 0, st, g);
   return hipGetLastError();
 }
 
 }  // namespace
 
+hipError_t launch_pad(const PadJob& first, const PadJob& second, hipStream_t st) {
+  auto blocks = [](const PadJob& j) {
+    const int64_t n = (j.rows * (up8(j.cols) / 8) + 255) / 256;
+    return (int)(n < (1 << 20) ? n : 1 << 20);
+  };
+  const int a = blocks(first), b = blocks(second);
+  if (a + b == 0) return hipSuccess;
+  hipLaunchKernelGGL(pad_rows_kernel, dim3(a + b), dim3(256), 0, st, first, second, a);
+  return hipGetLastError();
+}
+
 hipError_t launch_gemm(const GemmArgs& args, const GemmPlan& p, void* ws, hipStream_t st) {
   GemmArgs g = args;
   char* base = static_cast<char*>(ws);
   hipError_t e;
-  if (p.copy_a && g.K > 0) {
-    const int rows = g.at ? g.K : g.M, cols = g.at ? g.M : g.K;
-    if ((e = pad_rows(g.a, g.lda, rows, cols, base + p.off_a, st)) != hipSuccess) return e;
-    g.a = base + p.off_a;
-    g.lda = up8(cols);
+  PadJob ja{}, jb{};
+  if (p.copy_a) {
+    ja = {g.a, g.lda, g.at ? g.K : g.M, g.at ? g.M : g.K, base + p.off_a};
+    g.a = ja.dst;
+    g.lda = up8(ja.cols);
   }
-  if (p.copy_b && g.K > 0) {
-    const int rows = g.bt ? g.K : g.N, cols = g.bt ? g.N : g.K;
-    if ((e = pad_rows(g.b, g.ldb, rows, cols, base + p.off_b, st)) != hipSuccess) return e;
-    g.b = base + p.off_b;
-    g.ldb = up8(cols);
+  if (p.copy_b) {
+    jb = {g.b, g.ldb, g.bt ? g.K : g.N, g.bt ? g.N : g.K, base + p.off_b};
+    g.b = jb.dst;
+    g.ldb = up8(jb.cols);
   }
+  if ((e = launch_pad(ja, jb, st)) != hipSuccess) return e;
   const int64_t ldpart = (g.N + 3) / 4 * 4;
   float* part = p.splits > 1 ? reinterpret_cast<float*>(base + p.off_part) : nullptr;
   const bool half = g.type == kElemF16;
@@ -291,7 +289,8 @@ hipError_t launch_gemm(const GemmArgs& args, const GemmPlan& p, void* ws, hipStr
   return hipGetLastError();
 }
 
-int linear_dz_units(int M) { return M < 256 ? M : 256; }
+// Rows of partial sums of dbias: 16 rows or more to each.
+int linear_dz_units(int M) { return M < 32 ? 1 : M / 16 < 256 ? M / 16 : 256; }
 
 hipError_t launch_linear_dz(const void* dy, int dy_type, int64_t lddy, const void* z, int64_t ldz, int act, float keep,
                             float add, uint16_t* dz, int64_t lddz, int type, float* part, void* dres, int64_t lddres,

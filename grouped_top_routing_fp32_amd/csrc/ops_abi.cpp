@@ -71,24 +71,29 @@ int check_linear(int32_t rows, int32_t cols, int32_t inner) {
 
 bool act_ok(int act) { return act >= BEAM_MOE_ACT_NONE && act <= BEAM_MOE_ACT_GELU; }
 
-// Workspace of the backward pass: dz, the partial sums of dbias, then what the two
-// products need, one after the other in the same place.  Where dz is dy itself its
-// place stays unused; the size does not depend on it.
+// Workspace of the backward pass: dz, the partial sums of dbias, w and x where they are
+// laid out anew, then the partial sums of the two products, one after the other in the
+// same place.  Where dz is dy itself its place stays unused; the size does not depend on it.
 struct BackwardPlan {
-  size_t off_dz, off_part, off_gemm, total;
+  size_t off_dz, off_part, off_w, off_x, off_gemm, total;
   int64_t lddz;
+  bool copy_w, copy_x;
   beam::GemmPlan dx, dw;
 };
 
 BackwardPlan backward_plan(int32_t rows, int32_t cols, int32_t inner, int64_t ldx, int64_t ldw) {
   BackwardPlan p;
-  p.lddz = (cols + 7) / 8 * 8;
-  // dz rows are whole chunks with zeros past cols, so the products take them as they are
+  p.lddz = beam::up8(cols);
+  p.copy_w = !beam::regular_rows(ldw, inner);
+  p.copy_x = !beam::regular_rows(ldx, inner);
+  // dz rows are whole chunks with zeros past cols, and the other operands' are made so
   p.dx = beam::plan_gemm(rows, inner, cols, false, true, p.lddz, ldw, true);
   p.dw = beam::plan_gemm(cols, inner, rows, true, true, p.lddz, ldx, true);
   p.off_dz = 0;
-  p.off_part = align_up((size_t)rows * p.lddz * 2);
-  p.off_gemm = p.off_part + align_up((size_t)beam::linear_dz_units(rows) * cols * sizeof(float));
+  p.off_part = align_up(beam::padded_bytes(rows, cols));
+  p.off_w = p.off_part + align_up((size_t)beam::linear_dz_units(rows) * cols * sizeof(float));
+  p.off_x = p.off_w + align_up(p.copy_w ? beam::padded_bytes(cols, inner) : 0);
+  p.off_gemm = p.off_x + align_up(p.copy_x ? beam::padded_bytes(rows, inner) : 0);
   p.total = p.off_gemm + (p.dx.total > p.dw.total ? p.dx.total : p.dw.total);
   return p;
 }
@@ -257,6 +262,18 @@ int beam_moe_linear_backward(int32_t rows, int32_t cols, int32_t inner, int type
     if ((rc = hip_status(beam::launch_column_sums(part, dbias, nullptr, rows > 0 ? beam::linear_dz_units(rows) : 0,
                                                   cols, st))) != BEAM_MOE_OK)
       return rc;
+  beam::PadJob jw{}, jx{};
+  if (dx && p.copy_w && rows > 0) {
+    jw = {w, ldw, cols, inner, at<void*>(ws, p.off_w)};
+    w = jw.dst;
+    ldw = beam::up8(inner);
+  }
+  if (dw && p.copy_x && rows > 0) {
+    jx = {x, ldx, rows, inner, at<void*>(ws, p.off_x)};
+    x = jx.dst;
+    ldx = beam::up8(inner);
+  }
+  if ((rc = hip_status(beam::launch_pad(jw, jx, st))) != BEAM_MOE_OK) return rc;
   beam::GemmArgs g{};
   g.type = type;
   g.out_type = type;
