@@ -492,37 +492,54 @@ class _On:
             self.ctx.__exit__(*exc)
 
 
-def _rows(t: torch.Tensor, name: str, dtypes, shape, dev) -> int:
+def _rows(t: torch.Tensor, name: str, dtypes, shape: tuple, dev) -> int:
     """Checks a matrix whose rows may be strided; returns its row stride."""
-    if t.device != dev or not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor on {dev}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, as the first tensor is")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be one of {tuple(dtypes)}, got {t.dtype}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     r, c = shape
     ld, one = t.stride()
-    if c > 1 and one != 1:
+    if one != 1 and c > 1:
         raise ValueError(f"{name} must have consecutive columns")
-    if r > 1 and ld < c:
+    if ld >= c:
+        return ld
+    if r > 1:
         raise ValueError(f"{name} must have rows that do not overlap")
-    return ld if r > 1 and ld > c else c
+    return c
 
 
 def _vec(t: Optional[torch.Tensor], name: str, dtype, shape, dev) -> Optional[int]:
     """Checks an optional contiguous tensor; returns its address."""
     if t is None:
         return None
-    if t.device != dev or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
 def _mat(t: torch.Tensor, name: str) -> tuple:
+    """Rows, columns and device of the matrix that the others are checked against."""
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise ValueError(f"{name} must be a matrix")
-    return t.shape[0], t.shape[1], t.device
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    return *t.shape, t.device
+
+
+def _result(out: Optional[torch.Tensor], out_dtype, default, dtypes, shape: tuple, dev):
+    """The output and its row stride: the caller's, checked, or a new one."""
+    if out is None:
+        dtype = out_dtype or default
+        if dtype not in dtypes:
+            raise ValueError(f"out_dtype must be one of {tuple(dtypes)}, got {dtype}")
+        return torch.empty(*shape, dtype=dtype, device=dev), shape[1]
+    if out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError("out is not of out_dtype")
+    return out, _rows(out, "out", dtypes, shape, dev)
 
 
 def _scratch(n: int, ws: Optional[torch.Tensor], dev, fn: str):
@@ -552,13 +569,9 @@ def beam_moe_layer_norm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, b
     ldx = _rows(x, "x", _FLOATS, (T, H), dev)
     g, b = _vec(gamma, "gamma", _F32, (H,), dev), _vec(beta, "beta", _F32, (H,), dev)
     with _On(dev, stream) as st:
-        if out is None:
-            out = torch.empty((T, H), dtype=out_dtype or x.dtype, device=dev)
-        elif out_dtype is not None and out.dtype != out_dtype:
-            raise ValueError("out is not of out_dtype")
-        ldy = _rows(out, "out", _FLOATS, (T, H), dev)
-        mean = torch.empty((T,), dtype=_F32, device=dev) if want_stats else None
-        rstd = torch.empty((T,), dtype=_F32, device=dev) if want_stats else None
+        out, ldy = _result(out, out_dtype, x.dtype, _FLOATS, (T, H), dev)
+        mean = torch.empty(T, dtype=_F32, device=dev) if want_stats else None
+        rstd = torch.empty_like(mean) if want_stats else None
         _check(load_library().beam_moe_layer_norm(
             T, H, x.data_ptr(), ELEM_TYPES[x.dtype], ldx, g, b, eps, out.data_ptr(), ELEM_TYPES[out.dtype], ldy,
             mean.data_ptr() if want_stats else None, rstd.data_ptr() if want_stats else None, st),
@@ -577,9 +590,9 @@ def beam_moe_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.
     g = _vec(gamma, "gamma", _F32, (H,), dev)
     lib = load_library()
     with _On(dev, stream) as st:
-        dx = torch.empty((T, H), dtype=x.dtype, device=dev) if want_dx else None
-        dg = torch.empty((H,), dtype=_F32, device=dev) if want_params else None
-        db = torch.empty((H,), dtype=_F32, device=dev) if want_params else None
+        dx = torch.empty(T, H, dtype=x.dtype, device=dev) if want_dx else None
+        dg = torch.empty(H, dtype=_F32, device=dev) if want_params else None
+        db = torch.empty_like(dg) if want_params else None
         need = lib.beam_moe_layer_norm_backward_workspace_bytes(T, H) if want_params else 0
         wp, wn, _keep = _scratch(need, ws, dev, "beam_moe_layer_norm_backward")
         _check(lib.beam_moe_layer_norm_backward(
@@ -591,8 +604,6 @@ def beam_moe_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.
 
 def _routed(dims: Dims, scores: torch.Tensor, topk_ids: torch.Tensor, seq_offsets: Optional[torch.Tensor]):
     T, E, dev = _mat(scores, "scores")
-    if not scores.is_cuda:
-        raise ValueError("scores must be a device tensor")
     s = _vec(scores, "scores", _F32, (T, dims.num_experts), dev)
     i = _vec(topk_ids, "topk_ids", torch.int32, (T, dims.topk), dev)
     B = 1
@@ -610,9 +621,9 @@ def beam_moe_balance_loss(dims: Dims, scores: torch.Tensor, topk_ids: torch.Tens
     T, E, dev, s, i, B, off = _routed(dims, scores, topk_ids, seq_offsets)
     lib, cd = load_library(), _cdims_of(dims)
     with _On(dev, stream) as st:
-        loss = torch.empty((B,), dtype=_F32, device=dev)
-        counts = torch.empty((B, E), dtype=torch.int32, device=dev)
-        prob = torch.empty((B, E), dtype=_F32, device=dev)
+        loss = torch.empty(B, dtype=_F32, device=dev)
+        prob = torch.empty(B, E, dtype=_F32, device=dev)
+        counts = torch.empty_like(prob, dtype=torch.int32)
         wp, wn, _keep = _scratch(lib.beam_moe_balance_loss_workspace_bytes(ctypes.byref(cd), T, B), ws, dev,
                                  "beam_moe_balance_loss")
         _check(lib.beam_moe_balance_loss(ctypes.byref(cd), T, s, i, B, off, alpha, loss.data_ptr(), counts.data_ptr(),
@@ -631,7 +642,7 @@ def beam_moe_route_backward(dims: Dims, scores: torch.Tensor, topk_ids: torch.Te
     dl, c = _vec(dloss, "dloss", _F32, (B,), dev), _vec(counts, "counts", torch.int32, (B, E), dev)
     cd = _cdims_of(dims)
     with _On(dev, stream) as st:
-        out = torch.empty((T, E), dtype=_F32, device=dev)
+        out = torch.empty_like(scores)
         if T == 0 and (dw is not None or dloss is not None):
             return out
         _check(load_library().beam_moe_route_backward(ctypes.byref(cd), T, s, i, d, B, off, alpha, dl, c,
@@ -656,18 +667,16 @@ def beam_moe_linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tenso
     bias [N] fp32. y is of out_dtype (x's type, or fp32), as residual is; out may be residual itself. Returns y,
     or (y, pre) with want_pre: pre [M, N] of x's type is what the backward pass reads."""
     M, K, dev = _mat(x, "x")
-    N = _mat(w, "w")[0]
+    if w.dim() != 2:
+        raise ValueError("w must be a matrix")
+    N = w.shape[0]
     ldx, ldw = _rows(x, "x", _HALF, (M, K), dev), _rows(w, "w", (x.dtype,), (N, K), dev)
     b, a = _vec(bias, "bias", _F32, (N,), dev), _act(act)
     lib = load_library()
     with _On(dev, stream) as st:
-        if out is None:
-            out = torch.empty((M, N), dtype=out_dtype or x.dtype, device=dev)
-        elif out_dtype is not None and out.dtype != out_dtype:
-            raise ValueError("out is not of out_dtype")
-        ldy = _rows(out, "out", (x.dtype, _F32), (M, N), dev)
+        out, ldy = _result(out, out_dtype, x.dtype, (x.dtype, _F32), (M, N), dev)
         ldr = 0 if residual is None else _rows(residual, "residual", (out.dtype,), (M, N), dev)
-        pre = torch.empty((M, N), dtype=x.dtype, device=dev) if want_pre else None
+        pre = torch.empty(M, N, dtype=x.dtype, device=dev) if want_pre else None
         wp, wn, _keep = _scratch(lib.beam_moe_linear_workspace_bytes(M, N, K, ldx, ldw), ws, dev, "beam_moe_linear")
         _check(lib.beam_moe_linear(
             M, N, K, ELEM_TYPES[x.dtype], x.data_ptr(), ldx, w.data_ptr(), ldw, b, a,
@@ -683,12 +692,14 @@ def beam_moe_linear_backward(dy: torch.Tensor, x: Optional[torch.Tensor], w: Opt
     """Gradients of beam_moe_linear from dy [M, N] (x's type or fp32) and, with an activation, pre. Returns
     (dx, dw, dbias), with want_dres (dx, dw, dbias, dres); those not wanted are None. x may be None without
     want_dw, w without want_dx; one of them is needed for the type."""
-    M, N, dev = _mat(dy, "dy")
     if x is None and w is None or want_dw and x is None or want_dx and w is None:
         raise ValueError("x is needed for dw, w for dx, and one of them for the type")
+    M, N, dev = _mat(dy, "dy")
     K, dt = (x if x is not None else w).shape[-1], (x if x is not None else w).dtype
+    if dt not in _HALF:
+        raise ValueError(f"x and w must be one of {_HALF}, got {dt}")
     ldx = K if x is None else _rows(x, "x", _HALF, (M, K), dev)
-    ldw = K if w is None else _rows(w, "w", (dt,) if dt in _HALF else _HALF, (N, K), dev)
+    ldw = K if w is None else _rows(w, "w", (dt,), (N, K), dev)
     lddy = _rows(dy, "dy", (dt, _F32), (M, N), dev)
     a = _act(act)
     ldp = N
@@ -698,10 +709,10 @@ def beam_moe_linear_backward(dy: torch.Tensor, x: Optional[torch.Tensor], w: Opt
         ldp = _rows(pre, "pre", (dt,), (M, N), dev)
     lib = load_library()
     with _On(dev, stream) as st:
-        dx = torch.empty((M, K), dtype=dt, device=dev) if want_dx else None
-        dw = torch.empty((N, K), dtype=dt, device=dev) if want_dw else None
-        db = torch.empty((N,), dtype=_F32, device=dev) if want_dbias else None
-        dres = torch.empty((M, N), dtype=dy.dtype, device=dev) if want_dres else None
+        dx = torch.empty(M, K, dtype=dt, device=dev) if want_dx else None
+        dw = torch.empty(N, K, dtype=dt, device=dev) if want_dw else None
+        db = torch.empty(N, dtype=_F32, device=dev) if want_dbias else None
+        dres = torch.empty(M, N, dtype=dy.dtype, device=dev) if want_dres else None
         wp, wn, _keep = _scratch(lib.beam_moe_linear_backward_workspace_bytes(M, N, K, ldx, ldw), ws, dev,
                                  "beam_moe_linear_backward")
         _check(lib.beam_moe_linear_backward(

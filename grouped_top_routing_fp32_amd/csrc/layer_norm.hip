@@ -241,6 +241,7 @@ __global__ __launch_bounds__(1024) void column_sums_kernel(const float* __restri
   const int h = blockIdx.x * 64 + threadIdx.x;
   float v = 0.f;
   if (h < H)
+#pragma unroll 8
     for (int u = threadIdx.y; u < units; u += 16) v += p[(int64_t)u * H + h];
   s[threadIdx.y][threadIdx.x] = v;
   __syncthreads();

@@ -67,10 +67,17 @@ __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
   return HALF ? mfma16x16x32_f16(a, b, c) : mfma16x16x32(a, b, c);
 }
 
+// 1 / (1 + e^-z) from the hardware base-2 exponential and reciprocal, about 1 ulp each.
+// The rounded exponent -z log2 e makes e^-z up to |z| half steps off; the result moves by
+// s (1 - s) of that, and z s by at most 0.6 half steps of 1.
+__device__ __forceinline__ float sigmoid_f32(float z) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * z));
+}
+
 template <int ACT>
 __device__ __forceinline__ float act_f32(float z) {
   if constexpr (ACT == kActRelu) return z < 0.f ? 0.f : z;  // NaN stays NaN
-  if constexpr (ACT == kActSilu) return z / (1.f + expf(-z));
+  if constexpr (ACT == kActSilu) return z * sigmoid_f32(z);
   if constexpr (ACT == kActGelu) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
   return z;
 }
@@ -80,7 +87,7 @@ template <int ACT>
 __device__ __forceinline__ float act_slope_f32(float z) {
   if constexpr (ACT == kActRelu) return z > 0.f ? 1.f : 0.f;
   if constexpr (ACT == kActSilu) {
-    const float s = 1.f / (1.f + expf(-z));
+    const float s = sigmoid_f32(z);
     return s * (1.f + z * (1.f - s));
   }
   if constexpr (ACT == kActGelu)
