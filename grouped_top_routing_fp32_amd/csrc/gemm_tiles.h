@@ -109,17 +109,20 @@ __device__ __forceinline__ int xcd_lin(int b, int total) {
 // start of step t and waited for at its end; they are issued and waited for by hand
 // (the compiler's own tracking drains them at every loop head).
 // The mfma's first operand is B's: a lane then holds four consecutive columns of a row.
+// lin is the tile's place in the order of all of them, split after split; ring holds
+// kRing<BM, BN> elements of LDS.
+template <int BM, int BN>
+constexpr int kRing = 2 * (BM + BN) * kBK;
+
 template <bool HALF, bool AT, bool BT, int BM, int BN, int WM, int WN, bool EPI>
-__global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(GemmArgs g, int mt, int nt, int k_per_split,
-                                                            float* __restrict__ part, int64_t ldpart) {
+__device__ __forceinline__ void gemm_tile(uint16_t* ring, GemmArgs g, int mt, int nt, int lin, int k_per_split,
+                                          float* __restrict__ part, int64_t ldpart) {
   constexpr int NW = WM * WN, FI = BM / WM / 16, FJ = BN / WN / 16;
   constexpr int kSlot = (BM + BN) * kBK;
-  __shared__ __align__(1024) uint16_t ring[2 * kSlot];
   lds_u16* lds = (lds_u16*)ring;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
   const int tiles = mt * nt;
-  const int lin = xcd_lin(blockIdx.x, gridDim.x);
   const int split = lin / tiles, t = lin % tiles;
   const int group = t / (8 * nt), in = t % (8 * nt), rows = min(8, mt - 8 * group);
   const int m0 = (8 * group + in % rows) * BM, n0 = in / rows * BN;
@@ -269,6 +272,36 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(GemmArgs g, int mt, i
       rows_of([&](int m, f32x4 v) { epilogue4<kActNone>(g, wide, m, n, v); });
     }
   }
+}
+
+template <bool HALF, bool AT, bool BT, int BM, int BN, int WM, int WN, bool EPI>
+__global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(GemmArgs g, int mt, int nt, int k_per_split,
+                                                            float* __restrict__ part, int64_t ldpart) {
+  __shared__ __align__(1024) uint16_t ring[kRing<BM, BN>];
+  gemm_tile<HALF, AT, BT, BM, BN, WM, WN, EPI>(ring, g, mt, nt, xcd_lin(blockIdx.x, gridDim.x), k_per_split, part,
+                                               ldpart);
+}
+
+// dx = dz w and dw = dz^T x of small sizes, both in whole 64-row tiles, in one launch: neither
+// fills the card alone, and each launch costs more than a stage or two of K.  dx's tiles
+// come first.  (Large ones gain nothing: 429 us either way at [8192, 5120] x [2560, 5120],
+// where the matrix cores' power is the bound and idle CUs leave the others more of it.)
+template <bool HALF>
+__global__ __launch_bounds__(256) void gemm_pair_kernel(GemmArgs dx, GemmArgs dw) {
+  __shared__ __align__(1024) uint16_t ring[kRing<64, 64>];
+  const int mx = (dx.M + 63) / 64, nx = (dx.N + 63) / 64, mw = (dw.M + 63) / 64, nw = (dw.N + 63) / 64;
+  const int b = blockIdx.x, first = mx * nx;
+  if (b < first)
+    gemm_tile<HALF, false, true, 64, 64, 2, 2, false>(ring, dx, mx, nx, xcd_lin(b, first), dx.K, nullptr, 0);
+  else
+    gemm_tile<HALF, true, true, 64, 64, 2, 2, false>(ring, dw, mw, nw, xcd_lin(b - first, mw * nw), dw.K, nullptr, 0);
+}
+
+template <bool HALF>
+hipError_t launch_gemm_pair(const GemmArgs& dx, const GemmArgs& dw, hipStream_t st) {
+  auto tiles = [](const GemmArgs& g) { return ((g.M + 63) / 64) * ((g.N + 63) / 64); };
+  hipLaunchKernelGGL(gemm_pair_kernel<HALF>, dim3(tiles(dx) + tiles(dw)), dim3(256), 0, st, dx, dw);
+  return hipGetLastError();
 }
 
 // Launches the tiles of g's layout (A transposed implies B transposed).

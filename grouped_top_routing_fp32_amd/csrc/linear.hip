@@ -289,6 +289,18 @@ hipError_t launch_gemm(const GemmArgs& args, const GemmPlan& p, void* ws, hipStr
   return hipGetLastError();
 }
 
+hipError_t launch_gemm_pair(const GemmArgs& dx, const GemmPlan& px, const GemmArgs& dw, const GemmPlan& pw, void* ws,
+                            hipStream_t st) {
+  auto whole = [](const GemmPlan& p) { return p.kind == GemmPlan::kTiles && p.tile == 64 && p.splits == 1; };
+  if (dx.M > 0 && whole(px) && whole(pw))
+    return dx.type == kElemF16 ? launch_gemm_pair_f16(dx, dw, st) : launch_gemm_pair_bf16(dx, dw, st);
+  if (dx.M > 0) {
+    const hipError_t e = launch_gemm(dx, px, ws, st);
+    if (e != hipSuccess) return e;
+  }
+  return launch_gemm(dw, pw, ws, st);
+}
+
 // Rows of partial sums of dbias: 16 rows or more to each.
 int linear_dz_units(int M) { return M < 32 ? 1 : M / 16 < 256 ? M / 16 : 256; }
 

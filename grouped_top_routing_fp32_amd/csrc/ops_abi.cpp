@@ -274,34 +274,30 @@ int beam_moe_linear_backward(int32_t rows, int32_t cols, int32_t inner, int type
     ldx = beam::up8(inner);
   }
   if ((rc = hip_status(beam::launch_pad(jw, jx, st))) != BEAM_MOE_OK) return rc;
-  beam::GemmArgs g{};
-  g.type = type;
-  g.out_type = type;
-  g.add = 1.f;
-  g.a = same ? dy : dz;
-  g.lda = same ? lddy : p.lddz;
-  if (dx && rows > 0) {
-    g.b = w;
-    g.ldb = ldw;
-    g.bt = true;
-    g.M = rows;
-    g.N = inner;
-    g.K = cols;
-    g.out = dx;
-    g.ldo = lddx;
-    if ((rc = hip_status(beam::launch_gemm(g, p.dx, gemm_ws, st))) != BEAM_MOE_OK) return rc;
-  }
-  if (dw) {
-    g.at = g.bt = true;
-    g.b = x;
-    g.ldb = ldx;
-    g.M = cols;
-    g.N = inner;
-    g.K = rows;
-    g.out = dw;
-    g.ldo = lddw;
-    if ((rc = hip_status(beam::launch_gemm(g, p.dw, gemm_ws, st))) != BEAM_MOE_OK) return rc;
-  }
+  beam::GemmArgs gx{}, gw{};
+  gx.type = gx.out_type = gw.type = gw.out_type = type;
+  gx.add = gw.add = 1.f;
+  gx.a = gw.a = same ? dy : dz;
+  gx.lda = gw.lda = same ? lddy : p.lddz;
+  gx.b = w;
+  gx.ldb = ldw;
+  gx.bt = true;
+  gx.M = rows;
+  gx.N = inner;
+  gx.K = cols;
+  gx.out = dx;
+  gx.ldo = lddx;
+  gw.b = x;
+  gw.ldb = ldx;
+  gw.at = gw.bt = true;
+  gw.M = cols;
+  gw.N = inner;
+  gw.K = rows;
+  gw.out = dw;
+  gw.ldo = lddw;
+  if (dx && dw) return hip_status(beam::launch_gemm_pair(gx, p.dx, gw, p.dw, gemm_ws, st));
+  if (dx && rows > 0) return hip_status(beam::launch_gemm(gx, p.dx, gemm_ws, st));
+  if (dw) return hip_status(beam::launch_gemm(gw, p.dw, gemm_ws, st));
   return BEAM_MOE_OK;
 }
 
