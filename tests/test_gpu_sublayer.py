@@ -131,6 +131,22 @@ def test_layer_norm_zero_eps_and_padding_untouched():
     assert y.shape == (0, 40) and mean.numel() == 0 and rstd.numel() == 0
 
 
+def test_layer_norm_offsets_past_32_bits():
+    """Rows of a buffer so wide that the last ones start past 2^32 elements."""
+    _say("layer_norm wide rows")
+    g = _gen(12)
+    rows, ld, cols = 66000, 65600, 72
+    buf = torch.empty((rows, ld), dtype=BF16, device=DEV)
+    x = buf[:, :cols]
+    x.copy_(torch.randn((rows, cols), generator=g, device=DEV))
+    y, mean, rstd = fw.beam_moe_layer_norm(x, out=buf[:, 128: 128 + cols])
+    want = fw.beam_moe_layer_norm(x.contiguous())
+    assert torch.equal(y, want[0]) and torch.equal(mean, want[1]) and torch.equal(rstd, want[2])
+    a = fw.beam_moe_layer_norm_backward(y, x, mean, rstd)
+    b = fw.beam_moe_layer_norm_backward(y.contiguous(), x.contiguous(), mean, rstd)
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
 def _norm_back_ref(dy, x, mean, rstd, gamma):
     dy, x, rs = dy.double(), x.double(), rstd.double()[:, None]
     hat = (x - mean.double()[:, None]) * rs
@@ -411,6 +427,47 @@ def test_bad_offsets_do_not_fault():
         assert out.shape == scores.shape
 
 
+def test_many_and_long_sequences():
+    """70,000 sequences of one or two tokens; and one so long that its counts times E pass 24 bits."""
+    _say("many sequences")
+    lens = [1 + (i % 2) for i in range(70000)]
+    scores, ids, off = _problem(105001, 8, 2, lens, 4)
+    o = torch.tensor(off, dtype=torch.int32, device=DEV)
+    loss, counts, prob = fw.beam_moe_balance_loss(_dims(8, 2), scores, ids, alpha=0.01, seq_offsets=o)
+    p = scores.double() / scores.double().sum(1, keepdim=True)
+    total = torch.cat([torch.zeros_like(p[:1]), p.cumsum(0)])
+    n = (o[1:] - o[:-1])[:, None]
+    want = (total[o[1:].long()] - total[o[:-1].long()]) / n
+    # the running 64-bit sums hold 1e5 terms of at most 1
+    _near(prob, want, 100 * U * want + 1e-10)
+    seq = torch.bucketize(torch.arange(105001, device=DEV), o[1:].long(), right=True)[:, None]
+    ok = (ids >= 0) & (ids < 8) & (seq < 70000)
+    c = torch.bincount((seq * 8 + ids)[ok], minlength=70000 * 8).view(70000, 8)
+    assert torch.equal(counts.long(), c)
+    _near(loss, 0.01 * 8 / (2 * n[:, 0]) * (c * want).sum(1), 100 * U * 0.01 * 8 + 0 * loss.double())
+    dl = fw.beam_moe_route_backward(_dims(8, 2), scores, ids, dloss=torch.ones_like(loss), counts=counts, alpha=1.0,
+                                    seq_offsets=o)
+    g = (counts * 8.0 - 2 * n)[seq[:-1, 0]].double() / (2 * n * n)[seq[:-1, 0]]
+    ref = (g - (g * p[:-1]).sum(1, keepdim=True)) / scores[:-1].double().sum(1, keepdim=True)
+    mag = (g.abs() + (g.abs() * p[:-1]).sum(1, keepdim=True)) / scores[:-1].double().sum(1, keepdim=True)
+    s = scores[:-1].double()
+    _near(dl[:-1], ref * s * (1 - s), 40 * U * mag * s * (1 - s))
+    assert not dl[-1].any()
+
+    _say("a long sequence")
+    T, E, K = 1_100_000, 8, 8
+    scores, ids, off = _problem(T, E, K, [T], 5)
+    loss, counts, prob = fw.beam_moe_balance_loss(_dims(E, K), scores, ids, alpha=1.0)
+    rl, rc, rp = _balance_ref(scores, ids, off, 1.0, K)
+    assert torch.equal(counts.long(), rc)
+    # 4096 rows to a unit, 512 to each of its 8 waves, one after the other in FP32: depth 540, then FP64
+    _near(prob, rp, 600 * U * rp)
+    _near(loss, rl, 600 * U * rl)
+    dl = fw.beam_moe_route_backward(_dims(E, K), scores, ids, dloss=loss, counts=counts, alpha=1.0)
+    want, mag = _route_back_ref(scores, ids, None, 2.5, off, 1.0, loss, counts, K)
+    _near(dl, want, 40 * U * mag)
+
+
 # --------------------------------------------------------------------------
 # linear
 # --------------------------------------------------------------------------
@@ -550,6 +607,22 @@ def test_linear_backward_parts():
     assert torch.equal(b[1], dw) and torch.equal(c[2], db)
     dx, dw, db = fw.beam_moe_linear_backward(dy[:0], x[:0], w, pre[:0], act="silu")
     assert dx.shape == (0, K) and not dw.any() and not db.any() and dw.shape == (N, K)
+
+
+def test_linear_offsets_past_32_bits():
+    _say("linear wide rows")
+    g = _gen(13)
+    M, K, N, ld = 66000, 64, 40, 65600
+    buf = torch.empty((M, ld), dtype=BF16, device=DEV)
+    x, res, y = buf[:, :K], buf[:, 128: 128 + N], buf[:, 256: 256 + N]
+    x.copy_(torch.randn((M, K), generator=g, device=DEV))
+    res.copy_(torch.randn((M, N), generator=g, device=DEV))
+    w = _randn(g, (N, K), BF16, 0.1)
+    fw.beam_moe_linear(x, w, act="relu", residual=res, out=y)
+    assert torch.equal(y, fw.beam_moe_linear(x.contiguous(), w, act="relu", residual=res.contiguous()))
+    a = fw.beam_moe_linear_backward(y, x, w, res, act="silu")
+    b = fw.beam_moe_linear_backward(y.contiguous(), x.contiguous(), w, res.contiguous(), act="silu")
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
 
 
 def test_linear_gradient_against_differences():
