@@ -9,6 +9,12 @@ namespace beam {
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
+// Vectors in global memory that start at any element: this target's wide loads and
+// stores need no more than that, so rows of any stride are moved 16 bytes at a time.
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef u32x2 u32x2_any __attribute__((aligned(2)));
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+
 // Values of the ABI's element type arguments (BEAM_MOE_BF16, _F16, _F32).
 enum ElemType { kElemBF16 = 0, kElemF16 = 1, kElemF32 = 2 };
 
@@ -29,15 +35,28 @@ struct F32 {
   __device__ static S down(float f) { return f; }
 };
 
-// N = 1, or 8 elements from an address aligned to 16 bytes: as they lie in memory
-// (so that a load can be requested before its values are wanted), and as FP32.
-template <class T, int N>
-struct Raw {
-  static constexpr int kWords = N * sizeof(typename T::S) / 16;  // N = 8: 1 or 2
+// Eight consecutive elements as they lie in memory (so that a load can be requested
+// before its values are wanted), read as FP32.
+template <class T>
+struct Raw8 {
+  static constexpr int kWords = sizeof(typename T::S) / 2;  // of 16 bytes: 1 or 2
   u32x4 w[kWords];
   __device__ __forceinline__ void load(const typename T::S* p) {
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) w[i] = reinterpret_cast<const u32x4*>(p)[i];
+    for (int i = 0; i < kWords; ++i) w[i] = reinterpret_cast<const u32x4_any*>(p)[i];
+  }
+  // n < 8 elements, zeros after them
+  __device__ __forceinline__ void load_part(const typename T::S* p, int n) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) {
+        if constexpr (sizeof(typename T::S) == 4)
+          w[i / 4][i % 4] = __float_as_uint(p[i]);
+        else
+          w[0][i / 2] |= (uint32_t)p[i] << (16 * (i % 2));
+      }
   }
   __device__ __forceinline__ float operator[](int i) const {
     if constexpr (sizeof(typename T::S) == 4)
@@ -46,33 +65,35 @@ struct Raw {
       return T::up((uint16_t)(w[0][i / 2] >> (16 * (i % 2))));
   }
 };
-template <class T>
-struct Raw<T, 1> {
-  typename T::S s;
-  __device__ __forceinline__ void load(const typename T::S* p) { s = *p; }
-  __device__ __forceinline__ float operator[](int) const { return T::up(s); }
-};
 
-template <class T, int N>
-__device__ __forceinline__ void load_n(const typename T::S* p, float* v) {
-  Raw<T, N> r;
-  r.load(p);
+// n >= 8: eight elements, else the first n, and zeros.
+template <class T>
+__device__ __forceinline__ void load8(const typename T::S* p, int n, float* v) {
+  Raw8<T> r;
+  if (n >= 8)
+    r.load(p);
+  else
+    r.load_part(p, n);
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = r[i];
+  for (int i = 0; i < 8; ++i) v[i] = r[i];
 }
 
-template <class T, int N>
-__device__ __forceinline__ void store_n(typename T::S* p, const float* v) {
-  if constexpr (N == 1) {
-    *p = T::down(v[0]);
-  } else if constexpr (sizeof(typename T::S) == 4) {
-    *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
-    *reinterpret_cast<f32x4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
-  } else {
-    u32x4 r;
+template <class T>
+__device__ __forceinline__ void store8(typename T::S* p, int n, const float* v) {
+  if (n >= 8) {
+    if constexpr (sizeof(typename T::S) == 4) {
+      reinterpret_cast<f32x4_any*>(p)[0] = f32x4{v[0], v[1], v[2], v[3]};
+      reinterpret_cast<f32x4_any*>(p)[1] = f32x4{v[4], v[5], v[6], v[7]};
+    } else {
+      u32x4 r;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) r[q] = T::down(v[2 * q]) | ((uint32_t)T::down(v[2 * q + 1]) << 16);
-    *reinterpret_cast<u32x4*>(p) = r;
+      for (int q = 0; q < 4; ++q) r[q] = T::down(v[2 * q]) | ((uint32_t)T::down(v[2 * q + 1]) << 16);
+      *reinterpret_cast<u32x4_any*>(p) = r;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = T::down(v[i]);
   }
 }
 

@@ -189,7 +189,6 @@ __device__ __forceinline__ void gemm_tile(uint16_t* ring, GemmArgs g, int mt, in
     __syncthreads();
   };
   auto sum_at = [&](int r) __attribute__((always_inline)) { return sums[r * kQuads + (qn ^ (r & 15))]; };
-  const bool wide = epilogue_wide(g);
 
   // Tiles inside the result: batches of kBatch rows to a thread, the residual of the next
   // batch requested as this one's is used, so its latency shows once per tile.  A residual and
@@ -197,14 +196,15 @@ __device__ __forceinline__ void gemm_tile(uint16_t* ring, GemmArgs g, int mt, in
   // [16384, 2560] x [5120, 2560] onto an FP32 stream.
   constexpr int kIters = kPassRows / kRowsAtOnce, kBatch = kIters < 8 ? kIters : 8, kBatches = kIters / kBatch;
   static_assert(kBatches * kBatch * kRowsAtOnce == kPassRows, "whole batches");
-  if (EPI && wide && !part && m0 + BM <= g.M && n0 + BN <= g.N) {
+  if (EPI && !part && m0 + BM <= g.M && n0 + BN <= g.N) {
     auto inside = [&](auto out_type, auto act) __attribute__((always_inline)) {
       using OT = decltype(out_type);
       using Raw = std::conditional_t<sizeof(typename OT::S) == 4, f32x4, u32x2>;
+      using RawAny = std::conditional_t<sizeof(typename OT::S) == 4, f32x4_any, u32x2_any>;
       const typename OT::S* res = static_cast<const typename OT::S*>(g.res) + (int64_t)(m0 + qr) * g.ldr + n;
       Raw rv[kBatch] = {};
       auto request = [&](int u, int row) __attribute__((always_inline)) {
-        if (g.res) rv[u] = __builtin_nontemporal_load(reinterpret_cast<const Raw*>(res + (int64_t)row * g.ldr));
+        if (g.res) rv[u] = __builtin_nontemporal_load(reinterpret_cast<const RawAny*>(res + (int64_t)row * g.ldr));
       };
       f32x4 bias = {0.f, 0.f, 0.f, 0.f};
       if (g.bias) bias = *reinterpret_cast<const f32x4*>(g.bias + n);
@@ -239,7 +239,7 @@ __device__ __forceinline__ void gemm_tile(uint16_t* ring, GemmArgs g, int mt, in
           }
           if (g.pre) store_elem4(g.pre, (int64_t)m * g.ldp + n, g.type, z);
           if constexpr (sizeof(typename OT::S) == 4)
-            __builtin_nontemporal_store(v, reinterpret_cast<f32x4*>(static_cast<float*>(g.out) + (int64_t)m * g.ldo + n));
+            __builtin_nontemporal_store(v, reinterpret_cast<f32x4_any*>(static_cast<float*>(g.out) + (int64_t)m * g.ldo + n));
           else
             store_elem4(g.out, (int64_t)m * g.ldo + n, g.type, v);
         }
@@ -266,10 +266,10 @@ __device__ __forceinline__ void gemm_tile(uint16_t* ring, GemmArgs g, int mt, in
       rows_of([&](int m, f32x4 v) { *reinterpret_cast<f32x4*>(p + (int64_t)m * ldpart) = v; });
     } else if constexpr (EPI) {
       by_act(g.act, [&](auto act) {
-        for (int r = qr; r < rmax; r += kRowsAtOnce) epilogue4<decltype(act)::value>(g, wide, mp + r, n, sum_at(r));
+        for (int r = qr; r < rmax; r += kRowsAtOnce) epilogue4<decltype(act)::value>(g, mp + r, n, sum_at(r));
       });
     } else {
-      rows_of([&](int m, f32x4 v) { epilogue4<kActNone>(g, wide, m, n, v); });
+      rows_of([&](int m, f32x4 v) { epilogue4<kActNone>(g, m, n, v); });
     }
   }
 }

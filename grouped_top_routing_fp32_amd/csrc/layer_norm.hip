@@ -7,8 +7,9 @@
 // Both are bound by HBM: a row is read once and kept in registers between its
 // sums and its result.  A row belongs to a team of `team` threads (whole waves;
 // one wave per row up to 512 columns, several such rows in a workgroup); thread
-// i of it holds chunks i, i + team, ... of VEC consecutive columns.
-#include <initializer_list>
+// i of it holds chunks i, i + team, ... of 8 consecutive columns, moved 16 bytes at
+// a time wherever the row starts.  TAIL: H is no multiple of 8, so a row's last chunk
+// holds fewer columns.
 #include <type_traits>
 
 #include "elem.h"
@@ -20,13 +21,19 @@ constexpr int kLnMaxWaves = kLnMaxThreads / 64;
 constexpr int kLnMaxJoin = 4096;  // columns of rows that share a workgroup with others
 static_assert(kLnMaxWaves == 16, "16 lanes join the waves' sums");
 
+// Columns in chunk ch of a row: a constant where every chunk is whole.
+template <bool TAIL>
+__device__ __forceinline__ int chunk_cols(int H, int ch) {
+  return TAIL ? min(8, H - 8 * ch) : 8;
+}
+
 // Forward.  Statistics: each wave takes the mean m of its own columns, then the sum of
 // squares about it (two passes over registers) and the rest c of its mean that m's
 // rounding left.  The waves are joined about the first one's m, P: wave w's mean is
 // P + d_w, d_w = (m_w - P) + c_w, the row's P + D, D = sum n_w d_w / H, and the squares
 // add up to sum M2_w + n_w (d_w - D)^2.  One barrier; a mean far from zero cancels
 // nothing, since only P holds its size, and y is taken from (x - P) - D.
-template <class XT, class YT, int VEC, int NCH>
+template <class XT, class YT, int NCH, bool TAIL>
 __global__ __launch_bounds__(kLnMaxThreads) void layer_norm_kernel(
     const typename XT::S* __restrict__ x, int64_t ldx, const float* __restrict__ gamma,
     const float* __restrict__ beta, typename YT::S* __restrict__ y, int64_t ldy, float* __restrict__ mean_out,
@@ -35,19 +42,19 @@ __global__ __launch_bounds__(kLnMaxThreads) void layer_norm_kernel(
   const int tid = threadIdx.x, team = blockDim.x, wave = tid >> 6, nw = team >> 6;
   const int t = blockIdx.x * blockDim.y + threadIdx.y;
   if (t >= T) return;  // blockDim.y > 1 only for one-wave teams, which meet no barrier
-  const int nch = H / VEC;
+  const int nch = (H + 7) / 8;
   const typename XT::S* xr = x + (int64_t)t * ldx;
-  float v[NCH][VEC];
+  float v[NCH][8];
   float s = 0.f;
   int cols = 0;  // the wave's
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
-    const int ch = tid + c * team;
-    cols += min(64, max(0, nch - (c * team + 64 * wave))) * VEC;
+    const int ch = tid + c * team, w0 = 8 * (c * team + 64 * wave);
+    cols += min(H, w0 + 512) - min(H, w0);
     if (ch < nch) {
-      load_n<XT, VEC>(xr + (int64_t)ch * VEC, v[c]);
+      load8<XT>(xr + 8 * ch, chunk_cols<TAIL>(H, ch), v[c]);
 #pragma unroll
-      for (int q = 0; q < VEC; ++q) s += v[c][q];
+      for (int q = 0; q < 8; ++q) s += v[c][q];
     }
   }
   float P = cols ? wave_sum(s) / cols : 0.f;
@@ -56,8 +63,8 @@ __global__ __launch_bounds__(kLnMaxThreads) void layer_norm_kernel(
   for (int c = 0; c < NCH; ++c)
     if (tid + c * team < nch) {
 #pragma unroll
-      for (int q = 0; q < VEC; ++q) {
-        const float d = v[c][q] - P;
+      for (int q = 0; q < 8; ++q) {
+        const float d = !TAIL || q < chunk_cols<TAIL>(H, tid + c * team) ? v[c][q] - P : 0.f;
         r += d;
         m2 += d * d;
       }
@@ -86,16 +93,17 @@ __global__ __launch_bounds__(kLnMaxThreads) void layer_norm_kernel(
   for (int c = 0; c < NCH; ++c) {
     const int ch = tid + c * team;
     if (ch < nch) {
-      float g[VEC], b[VEC], o[VEC];
-      if (gamma) load_n<F32, VEC>(gamma + ch * VEC, g);
-      if (beta) load_n<F32, VEC>(beta + ch * VEC, b);
+      const int n = chunk_cols<TAIL>(H, ch);
+      float g[8], b[8], o[8];
+      if (gamma) load8<F32>(gamma + 8 * ch, n, g);
+      if (beta) load8<F32>(beta + 8 * ch, n, b);
 #pragma unroll
-      for (int q = 0; q < VEC; ++q) {
+      for (int q = 0; q < 8; ++q) {
         o[q] = ((v[c][q] - P) - D) * rs;
         if (gamma) o[q] *= g[q];
         if (beta) o[q] += b[q];
       }
-      store_n<YT, VEC>(yr + (int64_t)ch * VEC, o);
+      store8<YT>(yr + 8 * ch, n, o);
     }
   }
 }
@@ -105,7 +113,7 @@ __global__ __launch_bounds__(kLnMaxThreads) void layer_norm_kernel(
 // row to row, so it sums their dgamma and dbeta in registers.  At the end the teams add
 // up in LDS, in order, and the workgroup writes one row of part [2][gridDim.x][H], which
 // column_sums_kernel adds up: no atomics, so the sums' order is fixed.
-template <class DT, class XT, int VEC, int NCH>
+template <class DT, class XT, int NCH, bool TAIL>
 __global__ __launch_bounds__(kLnMaxThreads) void layer_norm_backward_kernel(
     const typename DT::S* __restrict__ dy, int64_t lddy, const typename XT::S* __restrict__ x, int64_t ldx,
     const float* __restrict__ mean, const float* __restrict__ rstd, const float* __restrict__ gamma,
@@ -115,21 +123,22 @@ __global__ __launch_bounds__(kLnMaxThreads) void layer_norm_backward_kernel(
   const int tid = threadIdx.x, team = blockDim.x, nw = team >> 6;
   const int wave0 = threadIdx.y * nw, wave = wave0 + (tid >> 6);
   const int teams = blockDim.y, stride = gridDim.x * teams;
-  const int nch = H / VEC;
+  const int nch = (H + 7) / 8;
   // few columns to a thread: gamma stays in registers, and rows are requested one ahead
-  constexpr bool kAhead = NCH * VEC <= 8;
-  float g[NCH][VEC], dg[NCH][VEC] = {}, db[NCH][VEC] = {};
+  constexpr bool kAhead = NCH == 1;
+  float g[NCH][8], dg[NCH][8] = {}, db[NCH][8] = {};
   auto load_gamma = [&](int c) __attribute__((always_inline)) {
+    const int ch = tid + c * team;
 #pragma unroll
-    for (int q = 0; q < VEC; ++q) g[c][q] = 1.f;
-    if (gamma && tid + c * team < nch) load_n<F32, VEC>(gamma + (tid + c * team) * VEC, g[c]);
+    for (int q = 0; q < 8; ++q) g[c][q] = 1.f;
+    if (gamma && ch < nch) load8<F32>(gamma + 8 * ch, chunk_cols<TAIL>(H, ch), g[c]);
   };
   if (kAhead) {
 #pragma unroll
     for (int c = 0; c < NCH; ++c) load_gamma(c);
   }
-  Raw<XT, VEC> xr[NCH];
-  Raw<DT, VEC> yr[NCH];
+  Raw8<XT> xr[NCH];
+  Raw8<DT> yr[NCH];
   float mu = 0.f, rs = 0.f;
   auto request = [&](int t) __attribute__((always_inline)) {
     if (t >= T) return;
@@ -139,8 +148,16 @@ __global__ __launch_bounds__(kLnMaxThreads) void layer_norm_backward_kernel(
     for (int c = 0; c < NCH; ++c) {
       const int ch = tid + c * team;
       if (ch < nch) {
-        xr[c].load(x + (int64_t)t * ldx + (int64_t)ch * VEC);
-        yr[c].load(dy + (int64_t)t * lddy + (int64_t)ch * VEC);
+        const typename XT::S* xp = x + (int64_t)t * ldx + 8 * ch;
+        const typename DT::S* yp = dy + (int64_t)t * lddy + 8 * ch;
+        const int n = chunk_cols<TAIL>(H, ch);
+        if (!TAIL || n == 8) {
+          xr[c].load(xp);
+          yr[c].load(yp);
+        } else {  // dy is 0 past the row's end, which leaves the sums alone
+          xr[c].load_part(xp, n);
+          yr[c].load_part(yp, n);
+        }
       }
     }
   };
@@ -150,7 +167,7 @@ __global__ __launch_bounds__(kLnMaxThreads) void layer_norm_backward_kernel(
   for (int t0 = blockIdx.x * teams; t0 < T; t0 += stride, buf ^= 1) {
     const int t = t0 + threadIdx.y;
     const bool live = t < T;
-    float xh[NCH][VEC], gy[NCH][VEC];
+    float xh[NCH][8], gy[NCH][8];
     float s1 = 0.f, s2 = 0.f;
     if (!kAhead) request(t);
     const float r = rs;
@@ -160,7 +177,7 @@ __global__ __launch_bounds__(kLnMaxThreads) void layer_norm_backward_kernel(
         if (!kAhead) load_gamma(c);
         if (tid + c * team < nch) {
 #pragma unroll
-          for (int q = 0; q < VEC; ++q) {
+          for (int q = 0; q < 8; ++q) {
             xh[c][q] = (xr[c][q] - mu) * r;
             gy[c][q] = yr[c][q];
             dg[c][q] += gy[c][q] * xh[c][q];
@@ -191,10 +208,10 @@ __global__ __launch_bounds__(kLnMaxThreads) void layer_norm_backward_kernel(
       for (int c = 0; c < NCH; ++c) {
         const int ch = tid + c * team;
         if (ch < nch) {
-          float o[VEC];
+          float o[8];
 #pragma unroll
-          for (int q = 0; q < VEC; ++q) o[q] = r * (gy[c][q] - c1 - xh[c][q] * c2);
-          store_n<XT, VEC>(dx + (int64_t)t * lddx + (int64_t)ch * VEC, o);
+          for (int q = 0; q < 8; ++q) o[q] = r * (gy[c][q] - c1 - xh[c][q] * c2);
+          store8<XT>(dx + (int64_t)t * lddx + 8 * ch, chunk_cols<TAIL>(H, ch), o);
         }
       }
     }
@@ -206,21 +223,24 @@ __global__ __launch_bounds__(kLnMaxThreads) void layer_norm_backward_kernel(
     if ((int)threadIdx.y == y) {
 #pragma unroll
       for (int c = 0; c < NCH; ++c) {
-        const int col = (tid + c * team) * VEC;
-        if (col < H) {
-          if (y > 0) {  // teams > 1: H <= kLnMaxJoin
+        const int ch = tid + c * team;
+        if (ch < nch) {
+          if (y > 0) {  // teams > 1: H <= kLnMaxJoin, a multiple of 8
 #pragma unroll
-            for (int q = 0; q < VEC; ++q) {
-              dg[c][q] += joined[0][col + q];
-              db[c][q] += joined[1][col + q];
+            for (int q = 0; q < 8; ++q) {
+              dg[c][q] += joined[0][8 * ch + q];
+              db[c][q] += joined[1][8 * ch + q];
             }
           }
           if (y + 1 < teams) {
-            store_n<F32, VEC>(&joined[0][col], dg[c]);
-            store_n<F32, VEC>(&joined[1][col], db[c]);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              joined[0][8 * ch + q] = dg[c][q];
+              joined[1][8 * ch + q] = db[c][q];
+            }
           } else {
-            store_n<F32, VEC>(pg + col, dg[c]);
-            store_n<F32, VEC>(pb + col, db[c]);
+            store8<F32>(pg + 8 * ch, chunk_cols<TAIL>(H, ch), dg[c]);
+            store8<F32>(pb + 8 * ch, chunk_cols<TAIL>(H, ch), db[c]);
           }
         }
       }
@@ -266,27 +286,17 @@ int layer_norm_max_cols() { return 16384; }
 
 namespace {
 
-// 8 columns to a chunk where every row of every operand starts on 16 bytes and
-// holds whole chunks, else 1.
-bool wide(int H, std::initializer_list<int64_t> lds) {
-  if (H % 8) return false;
-  for (int64_t ld : lds)
-    if (ld % 8) return false;
-  return true;
-}
-
 struct Shape {
   int nch;   // chunks per thread
   int team;  // threads per row
-  int rows;  // rows per workgroup (one-wave teams only)
+  int rows;  // rows per workgroup of the forward kernel (one-wave teams only)
 };
 
-Shape shape(int H, bool vec) {
-  const int chunks = vec ? H / 8 : H;
-  const int nch = vec ? (chunks <= 1024 ? 1 : 2) : (chunks <= 4096 ? 4 : chunks <= 8192 ? 8 : 16);
+Shape shape(int H) {
+  const int chunks = (H + 7) / 8;
   Shape s;
-  s.nch = nch;
-  s.team = ((chunks + nch - 1) / nch + 63) / 64 * 64;
+  s.nch = chunks <= 1024 ? 1 : 2;
+  s.team = ((chunks + s.nch - 1) / s.nch + 63) / 64 * 64;
   s.rows = s.team == 64 ? 4 : 1;
   return s;
 }
@@ -297,14 +307,14 @@ hipError_t by_type(int type, F f) {
 }
 
 template <class F>
-hipError_t by_chunks(bool vec, int nch, F f) {
+hipError_t by_chunks(int H, int nch, F f) {
   using std::integral_constant;
-  if (vec)
-    return nch == 1 ? f(integral_constant<int, 8>{}, integral_constant<int, 1>{})
-                    : f(integral_constant<int, 8>{}, integral_constant<int, 2>{});
-  return nch == 4   ? f(integral_constant<int, 1>{}, integral_constant<int, 4>{})
-         : nch == 8 ? f(integral_constant<int, 1>{}, integral_constant<int, 8>{})
-                    : f(integral_constant<int, 1>{}, integral_constant<int, 16>{});
+  using std::bool_constant;
+  if (H % 8 == 0)
+    return nch == 1 ? f(integral_constant<int, 1>{}, bool_constant<false>{})
+                    : f(integral_constant<int, 2>{}, bool_constant<false>{});
+  return nch == 1 ? f(integral_constant<int, 1>{}, bool_constant<true>{})
+                  : f(integral_constant<int, 2>{}, bool_constant<true>{});
 }
 
 }  // namespace
@@ -312,14 +322,13 @@ hipError_t by_chunks(bool vec, int nch, F f) {
 hipError_t launch_layer_norm(const void* x, int x_type, int64_t ldx, const float* gamma, const float* beta, void* y,
                              int y_type, int64_t ldy, float* mean, float* rstd, int T, int H, float eps,
                              hipStream_t st) {
-  const bool vec = wide(H, {ldx, ldy});
-  const Shape s = shape(H, vec);
+  const Shape s = shape(H);
   return by_type(x_type, [&](auto xt) {
     return by_type(y_type, [&](auto yt) {
-      return by_chunks(vec, s.nch, [&](auto v, auto n) {
+      return by_chunks(H, s.nch, [&](auto n, auto tail) {
         using XT = decltype(xt);
         using YT = decltype(yt);
-        hipLaunchKernelGGL((layer_norm_kernel<XT, YT, decltype(v)::value, decltype(n)::value>),
+        hipLaunchKernelGGL((layer_norm_kernel<XT, YT, decltype(n)::value, decltype(tail)::value>),
                            dim3((T + s.rows - 1) / s.rows), dim3(s.team, s.rows), 0, st,
                            static_cast<const typename XT::S*>(x), ldx, gamma, beta, static_cast<typename YT::S*>(y),
                            ldy, mean, rstd, T, H, eps);
@@ -333,7 +342,7 @@ hipError_t launch_layer_norm(const void* x, int x_type, int64_t ldx, const float
 // teams as 1024 threads hold, one workgroup to a CU.  More of either costs more in
 // partial sums than it gains: [8192, 5120] fp32 / bf16 82 us with 256 workgroups, 84
 // with 192, 93 with 512; [1021, 2561] fp16 16, 16 and 22 us.
-static int backward_teams(int H, bool vec) { return H <= kLnMaxJoin ? kLnMaxThreads / shape(H, vec).team : 1; }
+static int backward_teams(int H) { return H <= kLnMaxJoin ? kLnMaxThreads / shape(H).team : 1; }
 static int backward_groups(int T, int teams) {
   const int n = (T + teams - 1) / teams;
   return n < 256 ? n : 256;
@@ -349,16 +358,15 @@ hipError_t launch_layer_norm_backward(const void* dy, int dy_type, int64_t lddy,
                                       int64_t ldx, const float* mean, const float* rstd, const float* gamma, void* dx,
                                       int64_t lddx, float* dgamma, float* dbeta, float* part, int T, int H,
                                       hipStream_t st) {
-  const bool vec = wide(H, {lddy, ldx, dx ? lddx : 0});
-  const Shape s = shape(H, vec);
-  const int teams = backward_teams(H, vec), units = backward_groups(T, teams);
+  const Shape s = shape(H);
+  const int teams = backward_teams(H), units = backward_groups(T, teams);
   const bool sums = dgamma || dbeta;
   hipError_t e = by_type(dy_type, [&](auto dt) {
     return by_type(x_type, [&](auto xt) {
-      return by_chunks(vec, s.nch, [&](auto v, auto n) {
+      return by_chunks(H, s.nch, [&](auto n, auto tail) {
         using DT = decltype(dt);
         using XT = decltype(xt);
-        hipLaunchKernelGGL((layer_norm_backward_kernel<DT, XT, decltype(v)::value, decltype(n)::value>),
+        hipLaunchKernelGGL((layer_norm_backward_kernel<DT, XT, decltype(n)::value, decltype(tail)::value>),
                            dim3(units), dim3(s.team, teams), 0, st, static_cast<const typename DT::S*>(dy), lddy,
                            static_cast<const typename XT::S*>(x), ldx, mean, rstd, gamma,
                            static_cast<typename XT::S*>(dx), lddx, sums ? part : nullptr, T, H);

@@ -124,26 +124,28 @@ __device__ __forceinline__ void store_elem(void* p, int64_t i, int type, float f
     static_cast<uint16_t*>(p)[i] = type == kElemBF16 ? BF16::down(f) : F16::down(f);
 }
 
-// Four consecutive elements, the first a multiple of four elements from an aligned row start.
+// Four consecutive elements from any one.
 __device__ __forceinline__ f32x4 load_elem4(const void* p, int64_t i, int type) {
-  if (type == kElemF32) return *reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + i);
-  const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
-  const uint16_t h[4] = {(uint16_t)r.x, (uint16_t)(r.x >> 16), (uint16_t)r.y, (uint16_t)(r.y >> 16)};
+  if (type == kElemF32) return *reinterpret_cast<const f32x4_any*>(static_cast<const float*>(p) + i);
+  const u32x2 r = *reinterpret_cast<const u32x2_any*>(static_cast<const uint16_t*>(p) + i);
   f32x4 v;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) v[q] = type == kElemBF16 ? BF16::up(h[q]) : F16::up(h[q]);
+  for (int q = 0; q < 4; ++q) {
+    const uint16_t h = (uint16_t)(r[q / 2] >> (16 * (q % 2)));
+    v[q] = type == kElemBF16 ? BF16::up(h) : F16::up(h);
+  }
   return v;
 }
 
 __device__ __forceinline__ void store_elem4(void* p, int64_t i, int type, f32x4 v) {
   if (type == kElemF32) {
-    *reinterpret_cast<f32x4*>(static_cast<float*>(p) + i) = v;
+    *reinterpret_cast<f32x4_any*>(static_cast<float*>(p) + i) = v;
     return;
   }
   uint32_t h[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) h[q] = type == kElemBF16 ? BF16::down(v[q]) : F16::down(v[q]);
-  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) = uint2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
+  *reinterpret_cast<u32x2_any*>(static_cast<uint16_t*>(p) + i) = u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
 }
 
 // One element of the result from its sum over k.
@@ -156,15 +158,10 @@ __device__ __forceinline__ void epilogue1(const GemmArgs& g, int m, int n, float
   store_elem(g.out, (int64_t)m * g.ldo + n, g.out_type, v);
 }
 
-// Whether rows of the result and of what goes with it start where four elements can be moved at once.
-__device__ __forceinline__ bool epilogue_wide(const GemmArgs& g) {
-  return g.ldo % 4 == 0 && (!g.res || g.ldr % 4 == 0) && (!g.pre || g.ldp % 4 == 0);
-}
-
 // Columns n .. n + 3 (n a multiple of four) of row m, those past N left alone.
 template <int ACT>
-__device__ __forceinline__ void epilogue4(const GemmArgs& g, bool wide, int m, int n, f32x4 z) {
-  if (wide && n + 4 <= g.N) {
+__device__ __forceinline__ void epilogue4(const GemmArgs& g, int m, int n, f32x4 z) {
+  if (n + 4 <= g.N) {
     if (g.bias) {
       const f32x4 b = *reinterpret_cast<const f32x4*>(g.bias + n);
 #pragma unroll

@@ -27,8 +27,7 @@ __global__ __launch_bounds__(256) void gemm_join_kernel(GemmArgs g, const float*
 #pragma unroll
     for (int q = 0; q < 4; ++q) z[q] += v[q];
   }
-  const bool wide = epilogue_wide(g);
-  by_act(g.act, [&](auto act) { epilogue4<decltype(act)::value>(g, wide, m, n, z); });
+  by_act(g.act, [&](auto act) { epilogue4<decltype(act)::value>(g, m, n, z); });
 }
 
 // Few rows (M <= 16, both operands K contiguous): bound by reading w once.  A workgroup
@@ -37,7 +36,7 @@ __global__ __launch_bounds__(256) void gemm_join_kernel(GemmArgs g, const float*
 // joined in LDS in wave order.
 constexpr int kSkinnyWaves = 8;
 
-template <bool HALF, bool WIDE>
+template <bool HALF>
 __global__ __launch_bounds__(64 * kSkinnyWaves) void gemm_skinny_kernel(GemmArgs g) {
   __shared__ f32x4 sum[kSkinnyWaves][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, gr = lane >> 4;
@@ -45,19 +44,15 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void gemm_skinny_kernel(GemmArgs
   const uint16_t* wrow = static_cast<const uint16_t*>(g.b) + (int64_t)min(n0 + l16, g.N - 1) * g.ldb;
   const uint16_t* xrow = static_cast<const uint16_t*>(g.a) + (int64_t)min(l16, g.M - 1) * g.lda;
   auto chunk = [&](const uint16_t* row, int k) {  // 8 elements from k, 0 past K
-    if constexpr (WIDE) {
-      u32x4 v = {0u, 0u, 0u, 0u};
-      if (k < g.K) v = ldg16(row + k);
-      return v;
-    } else {
-      uint16_t e[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) e[q] = k + q < g.K ? row[k + q] : 0;
-      u32x4 v;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) v[q] = e[2 * q] | ((uint32_t)e[2 * q + 1] << 16);
-      return v;
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (k + 8 <= g.K) {
+      v = *reinterpret_cast<const u32x4_any*>(row + k);
+    } else if (k < g.K) {
+      Raw8<F16> part;  // the bits alone matter
+      part.load_part(row + k, g.K - k);
+      v = part.w[0];
     }
+    return v;
   };
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
   for (int k = 128 * wave; k < g.K; k += 128 * kSkinnyWaves) {
@@ -82,8 +77,7 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void gemm_skinny_kernel(GemmArgs
   }
   const int n = n0 + 4 * gr;
   if (l16 >= g.M || n >= g.N) return;
-  const bool wide = epilogue_wide(g);
-  by_act(g.act, [&](auto act) { epilogue4<decltype(act)::value>(g, wide, l16, n, z); });
+  by_act(g.act, [&](auto act) { epilogue4<decltype(act)::value>(g, l16, n, z); });
 }
 
 // Lays one or two operands out anew, the first with blocks workgroups and the second with
@@ -96,81 +90,59 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(PadJob first, PadJob seco
   const int64_t n = (int64_t)j.rows * chunks;
   for (int64_t i = (int64_t)(blockIdx.x - (other ? blocks : 0)) * 256 + threadIdx.x; i < n; i += threads) {
     const int r = (int)(i / chunks), c = (int)(i % chunks) * 8;
-    const uint16_t* s = static_cast<const uint16_t*>(j.src) + (int64_t)r * j.ld;
-    u32x4 v;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint32_t lo = c + 2 * q < j.cols ? s[c + 2 * q] : 0, hi = c + 2 * q + 1 < j.cols ? s[c + 2 * q + 1] : 0;
-      v[q] = lo | (hi << 16);
-    }
-    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(j.dst) + ((int64_t)r * chunks + c / 8) * 8) = v;
+    const uint16_t* s = static_cast<const uint16_t*>(j.src) + (int64_t)r * j.ld + c;
+    Raw8<F16> v;  // the bits alone matter
+    if (c + 8 <= j.cols)
+      v.load(s);
+    else
+      v.load_part(s, j.cols - c);
+    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(j.dst) + 8 * i) = v.w[0];
   }
 }
 
 // dz[m, n] = add dy act'(z), rounded to the products' 16-bit type (the rounding that a
 // gradient kept between two layers has anyway); part[u][n] = the unit's sum of the
-// unrounded dz; dres = keep dy.  grid (ceil(N / VEC / 64), units), block (64, 4): thread
-// (c, r) takes chunk c of VEC columns in rows r, r + 4, ... of the unit.  dz rows are
-// lddz long, a multiple of 8, with zeros past N.
-template <int VEC>
-__global__ __launch_bounds__(256) void linear_dz_kernel(const void* __restrict__ dy, int dy_type, int64_t lddy,
-                                                        const void* __restrict__ z, int64_t ldz, int act, float keep,
-                                                        float add, uint16_t* __restrict__ dz, int64_t lddz, int type,
-                                                        float* __restrict__ part, void* __restrict__ dres,
-                                                        int64_t lddres, int M, int N, int rows) {
-  __shared__ float sums[4][64][VEC];
-  const int n = (blockIdx.x * 64 + threadIdx.x) * VEC, y = threadIdx.y;
+// unrounded dz; dres = keep dy.  grid (ceil(N / 512), units), block (64, 4): thread (c, r)
+// takes 8 columns in rows r, r + 4, ... of the unit.  dz rows are lddz long, a multiple of
+// 8, with zeros past N.  Bound by HBM and, with a smooth activation, its arithmetic:
+// [8192, 2560] bf16 SiLU 26 us for 126 MB.
+template <class DT, class T>
+__global__ __launch_bounds__(256) void linear_dz_kernel(const typename DT::S* __restrict__ dy, int64_t lddy,
+                                                        const typename T::S* __restrict__ z, int64_t ldz, int act,
+                                                        float keep, float add, typename T::S* __restrict__ dz,
+                                                        int64_t lddz, float* __restrict__ part,
+                                                        typename DT::S* __restrict__ dres, int64_t lddres, int M, int N,
+                                                        int rows) {
+  __shared__ float sums[4][64][8];
+  const int n = (blockIdx.x * 64 + threadIdx.x) * 8, y = threadIdx.y;
+  const int cols = min(8, N - n);  // <= 0: none
   const int m1 = min(M, (int)(blockIdx.y + 1) * rows);
-  float s[VEC] = {};
-  if (n < (dz ? lddz : N)) {
-    auto load = [&](const void* p, int64_t i, int ty, float* v) {
-      if constexpr (VEC == 1) {
-        v[0] = load_elem(p, i, ty);
-      } else if (ty == kElemF32) {
-        load_n<F32, VEC>(static_cast<const float*>(p) + i, v);
-      } else if (ty == kElemBF16) {
-        load_n<BF16, VEC>(static_cast<const uint16_t*>(p) + i, v);
-      } else {
-        load_n<F16, VEC>(static_cast<const uint16_t*>(p) + i, v);
-      }
-    };
-    auto store = [&](void* p, int64_t i, int ty, const float* v) {
-      if constexpr (VEC == 1) {
-        store_elem(p, i, ty, v[0]);
-      } else if (ty == kElemF32) {
-        store_n<F32, VEC>(static_cast<float*>(p) + i, v);
-      } else if (ty == kElemBF16) {
-        store_n<BF16, VEC>(static_cast<uint16_t*>(p) + i, v);
-      } else {
-        store_n<F16, VEC>(static_cast<uint16_t*>(p) + i, v);
-      }
-    };
+  float s[8] = {};
+  if (cols > 0) {
     by_act(act, [&](auto a) {
       constexpr int ACT = decltype(a)::value;
 #pragma unroll 4
       for (int m = blockIdx.y * rows + y; m < m1; m += 4) {
-        float d[VEC] = {}, v[VEC] = {}, zz[VEC] = {};
-        if (n < N) {  // VEC = 8 only where N holds whole chunks
-          load(dy, (int64_t)m * lddy + n, dy_type, d);
-          if constexpr (ACT != kActNone) load(z, (int64_t)m * ldz + n, type, zz);
+        float d[8], v[8], zz[8] = {};
+        load8<DT>(dy + (int64_t)m * lddy + n, cols, d);  // zeros past N
+        if constexpr (ACT != kActNone) load8<T>(z + (int64_t)m * ldz + n, cols, zz);
 #pragma unroll
-          for (int q = 0; q < VEC; ++q) {
-            v[q] = add * d[q] * act_slope_f32<ACT>(zz[q]);
-            s[q] += v[q];
-            d[q] *= keep;
-          }
-          if (dres) store(dres, (int64_t)m * lddres + n, dy_type, d);
+        for (int q = 0; q < 8; ++q) {
+          v[q] = add * d[q] * act_slope_f32<ACT>(zz[q]);
+          s[q] += v[q];
+          d[q] *= keep;
         }
-        if (dz) store(dz, (int64_t)m * lddz + n, type, v);
+        if (dres) store8<DT>(dres + (int64_t)m * lddres + n, cols, d);
+        if (dz) store8<T>(dz + (int64_t)m * lddz + n, 8, v);
       }
     });
   }
   if (!part) return;
 #pragma unroll
-  for (int q = 0; q < VEC; ++q) sums[y][threadIdx.x][q] = s[q];
+  for (int q = 0; q < 8; ++q) sums[y][threadIdx.x][q] = s[q];
   __syncthreads();
-  for (int i = y * 64 + threadIdx.x; i < 64 * VEC; i += 256) {
-    const int c = i / VEC, q = i % VEC, col = (blockIdx.x * 64 + c) * VEC + q;
+  for (int i = y * 64 + threadIdx.x; i < 512; i += 256) {
+    const int c = i / 8, q = i % 8, col = blockIdx.x * 512 + i;
     if (col < N) part[(int64_t)blockIdx.y * N + col] = (sums[0][c][q] + sums[1][c][q]) + (sums[2][c][q] + sums[3][c][q]);
   }
 }
@@ -200,26 +172,32 @@ GemmPlan plan_gemm(int M, int N, int K, bool at, bool bt, int64_t lda, int64_t l
   p.kind = GemmPlan::kTiles;
   p.copy_a = !padded && !regular_rows(lda, at ? M : K);
   p.copy_b = !padded && !regular_rows(ldb, bt ? N : K);
-  // 256-row tiles from 160 of them on ([4096, 5120] x [2560, 5120], 160 tiles: 125 us, 134
-  // in 128-row tiles; [3000, ...], 120 tiles: 91 and 90).  Below, 128-row tiles with K
-  // split until two workgroups a CU (what LDS holds) have work, in at least 8 stages each;
-  // under 24 stages the join costs what a split gains.  64-row tiles where even split
-  // 128-row tiles would leave CUs without work: [1000, 1000] x [1000, 1000] forward and
-  // back 32 us, 41 in 128-row tiles; but [512, 5120] x [2560, 5120] 42 us, 28 in those.
+  // The tile is chosen by how full the card's rounds are: a round is 256 workgroups of
+  // 256-row tiles (one a CU) or 512 of 128-row ones (two, each filling the other's gaps),
+  // and full rounds of the smaller reach 0.85 of the larger's rate ([16384, 2560] x [5120,
+  // 2560], full rounds of both: 391 us, 465 in 128-row tiles; [8192, 2560] x [2560, 2560],
+  // 1.25 rounds and 2.5: 137 and 118).  128-row tiles split K until two workgroups a CU
+  // have work, in at least 8 stages each; under 24 stages the join costs what a split
+  // gains.  64-row tiles where even split 128-row tiles would leave CUs without work ([1000,
+  // 1000] x [1000, 1000] forward and back 32 us, 41 in 128-row tiles; but [512, 5120] x
+  // [2560, 5120] 42 us, 28 in those), and for one or two stages, where the result's
+  // stores are most of the work ([3000, 128] x [3000, 128] 12.7 us against 15.7).
   const int stages = ceil_div(K, kBK);
-  int tiles = ceil_div(M, 256) * ceil_div(N, 256);
-  p.tile = 256;
-  if (tiles < 160) {
-    p.tile = 128;
-    tiles = ceil_div(M, 128) * ceil_div(N, 128);
-    if (tiles * (stages / 8 + 1) < kCUs) {
-      p.tile = 64;
-      tiles = ceil_div(M, 64) * ceil_div(N, 64);
-    }
-    int s = tiles > 0 ? 2 * kCUs / tiles : 1;
+  const int t256 = ceil_div(M, 256) * ceil_div(N, 256), t128 = ceil_div(M, 128) * ceil_div(N, 128);
+  auto fill = [](int64_t n, int round) { return (double)n / (double)((n + round - 1) / round * round); };
+  auto splits = [&](int tiles) {
+    int s = tiles > 0 && stages >= 24 ? 2 * kCUs / tiles : 1;
     s = s < stages / 8 ? s : stages / 8;
     s = s < 16 ? s : 16;
-    if (s > 1 && stages >= 24) {
+    return s > 1 ? s : 1;
+  };
+  if (stages <= 2 || t128 * (stages / 8 + 1) < kCUs)
+    p.tile = 64;
+  else
+    p.tile = fill(t256, kCUs) >= 0.85 * fill((int64_t)t128 * splits(t128), 2 * kCUs) ? 256 : 128;
+  if (p.tile < 256) {
+    const int s = splits(p.tile == 128 ? t128 : ceil_div(M, 64) * ceil_div(N, 64));
+    if (s > 1) {
       p.k_per_split = ceil_div(stages, s) * kBK;
       p.splits = ceil_div(K, p.k_per_split);
     }
@@ -237,14 +215,9 @@ GemmPlan plan_gemm(int M, int N, int K, bool at, bool bt, int64_t lda, int64_t l
 
 namespace {
 
-template <bool HALF>
 hipError_t launch_skinny(const GemmArgs& g, hipStream_t st) {
-  const bool wide = regular_rows(g.lda, g.K) && regular_rows(g.ldb, g.K);
-  const dim3 grid(ceil_div(g.N, 16)), block(64 * kSkinnyWaves);
-  if (wide)
-    hipLaunchKernelGGL((gemm_skinny_kernel<HALF, true>), grid, block, 0, st, g);
-  else
-    hipLaunchKernelGGL((gemm_skinny_kernel<HALF, false>), grid, block, 0, st, g);
+  hipLaunchKernelGGL(g.type == kElemF16 ? gemm_skinny_kernel<true> : gemm_skinny_kernel<false>,
+                     dim3(ceil_div(g.N, 16)), dim3(64 * kSkinnyWaves), 0, st, g);
   return hipGetLastError();
 }
 
@@ -280,7 +253,7 @@ hipError_t launch_gemm(const GemmArgs& args, const GemmPlan& p, void* ws, hipStr
   const int64_t ldpart = (g.N + 3) / 4 * 4;
   float* part = p.splits > 1 ? reinterpret_cast<float*>(base + p.off_part) : nullptr;
   const bool half = g.type == kElemF16;
-  if (p.kind == GemmPlan::kSkinny) return half ? launch_skinny<true>(g, st) : launch_skinny<false>(g, st);
+  if (p.kind == GemmPlan::kSkinny) return launch_skinny(g, st);
   e = half ? launch_gemm_f16(g, p, part, ldpart, st) : launch_gemm_bf16(g, p, part, ldpart, st);
   if (e != hipSuccess || !part) return e;
   const int64_t quads = (int64_t)g.M * (ldpart / 4);
@@ -301,23 +274,26 @@ hipError_t launch_gemm_pair(const GemmArgs& dx, const GemmPlan& px, const GemmAr
   return launch_gemm(dw, pw, ws, st);
 }
 
-// Rows of partial sums of dbias: 16 rows or more to each.
-int linear_dz_units(int M) { return M < 32 ? 1 : M / 16 < 256 ? M / 16 : 256; }
+// Rows of partial sums of dbias: a unit of linear_dz_kernel has 4 rows (one to each row of
+// its threads) until there are 256 units.  At 16 rows GELU's arithmetic alone took 10 us
+// of [517, 1003].
+int linear_dz_units(int M) { return M < 8 ? 1 : M / 4 < 256 ? M / 4 : 256; }
 
 hipError_t launch_linear_dz(const void* dy, int dy_type, int64_t lddy, const void* z, int64_t ldz, int act, float keep,
                             float add, uint16_t* dz, int64_t lddz, int type, float* part, void* dres, int64_t lddres,
                             int M, int N, hipStream_t st) {
   const int units = linear_dz_units(M), rows = ceil_div(M, units);
-  const bool wide = N % 8 == 0 && lddy % 8 == 0 && (act == kActNone || ldz % 8 == 0) && (!dres || lddres % 8 == 0);
-  const int cols = dz ? (int)lddz : N;
-  auto go = [&](auto kernel, int vec) {
-    hipLaunchKernelGGL(kernel, dim3(ceil_div(ceil_div(cols, vec), 64), units), dim3(64, 4), 0, st, dy, dy_type, lddy,
-                       z, ldz, act, keep, add, dz, lddz, type, part, dres, lddres, M, N, rows);
+  auto go = [&](auto dt, auto t) {
+    using DT = decltype(dt);
+    using T = decltype(t);
+    hipLaunchKernelGGL((linear_dz_kernel<DT, T>), dim3(ceil_div(N, 512), units), dim3(64, 4), 0, st,
+                       static_cast<const typename DT::S*>(dy), lddy, static_cast<const typename T::S*>(z), ldz, act,
+                       keep, add, dz, lddz, part, static_cast<typename DT::S*>(dres), lddres, M, N, rows);
   };
-  if (wide)
-    go(linear_dz_kernel<8>, 8);
+  if (type == kElemF16)
+    dy_type == kElemF32 ? go(F32{}, F16{}) : go(F16{}, F16{});
   else
-    go(linear_dz_kernel<1>, 1);
+    dy_type == kElemF32 ? go(F32{}, BF16{}) : go(BF16{}, BF16{});
   return hipGetLastError();
 }
 
