@@ -89,7 +89,8 @@ struct Side {
       }
       return u32x4{h[0].x, h[0].y, h[1].x, h[1].y};
     } else {
-      return *(const __attribute__((address_space(3))) u32x4*)(slot + (r0 + l16) * 64 + (((4 * s + g) ^ swz(l16)) << 3));
+      const lds_u16* p = slot + (r0 + l16) * 64 + (((4 * s + g) ^ swz(l16)) << 3);
+      return *(const __attribute__((address_space(3))) u32x4*)p;
     }
   }
 };
@@ -239,7 +240,8 @@ __device__ __forceinline__ void gemm_tile(uint16_t* ring, GemmArgs g, int mt, in
           }
           if (g.pre) store_elem4(g.pre, (int64_t)m * g.ldp + n, g.type, z);
           if constexpr (sizeof(typename OT::S) == 4)
-            __builtin_nontemporal_store(v, reinterpret_cast<f32x4_any*>(static_cast<float*>(g.out) + (int64_t)m * g.ldo + n));
+            __builtin_nontemporal_store(
+                v, reinterpret_cast<f32x4_any*>(static_cast<float*>(g.out) + (int64_t)m * g.ldo + n));
           else
             store_elem4(g.out, (int64_t)m * g.ldo + n, g.type, v);
         }

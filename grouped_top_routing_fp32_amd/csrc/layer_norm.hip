@@ -340,8 +340,8 @@ hipError_t launch_layer_norm(const void* x, int x_type, int64_t ldx, const float
 
 // Teams of a backward workgroup, and workgroups (rows of partial column sums): as many
 // teams as 1024 threads hold, one workgroup to a CU.  More of either costs more in
-// partial sums than it gains: [8192, 5120] fp32 / bf16 82 us with 256 workgroups, 84
-// with 192, 93 with 512; [1021, 2561] fp16 16, 16 and 22 us.
+// partial sums than it gains: [8192, 5120] fp32 / bf16 80 us with 256 workgroups, 84
+// with 192, 86 with 512; [1021, 2561] fp16 12.6, 13.8 and 16.9 us.
 static int backward_teams(int H) { return H <= kLnMaxJoin ? kLnMaxThreads / shape(H).team : 1; }
 static int backward_groups(int T, int teams) {
   const int n = (T + teams - 1) / teams;

@@ -143,7 +143,8 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(const typename DT::S* __
   __syncthreads();
   for (int i = y * 64 + threadIdx.x; i < 512; i += 256) {
     const int c = i / 8, q = i % 8, col = blockIdx.x * 512 + i;
-    if (col < N) part[(int64_t)blockIdx.y * N + col] = (sums[0][c][q] + sums[1][c][q]) + (sums[2][c][q] + sums[3][c][q]);
+    if (col < N)
+      part[(int64_t)blockIdx.y * N + col] = (sums[0][c][q] + sums[1][c][q]) + (sums[2][c][q] + sums[3][c][q]);
   }
 }
 
@@ -174,9 +175,10 @@ GemmPlan plan_gemm(int M, int N, int K, bool at, bool bt, int64_t lda, int64_t l
   p.copy_b = !padded && !regular_rows(ldb, bt ? N : K);
   // The tile is chosen by how full the card's rounds are: a round is 256 workgroups of
   // 256-row tiles (one a CU) or 512 of 128-row ones (two, each filling the other's gaps),
-  // and full rounds of the smaller reach 0.85 of the larger's rate ([16384, 2560] x [5120,
-  // 2560], full rounds of both: 391 us, 465 in 128-row tiles; [8192, 2560] x [2560, 2560],
-  // 1.25 rounds and 2.5: 137 and 118).  128-row tiles split K until two workgroups a CU
+  // and full rounds of the smaller reach 0.85 of the larger's rate up to 24 stages, then
+  // 0.8 ([16384, 2560] x [5120, 2560], full rounds of both: 391 us, 465 in 128-row tiles;
+  // [8192, 2560] x [2560, 2560], 1.25 rounds and 2.5: 137 and 118; [8192, 1024] x [5120,
+  // 1024], 2.5 and 5: 112 and 106, but 220 and 240 with K 2560).  128-row tiles split K until two workgroups a CU
   // have work, in at least 8 stages each; under 24 stages the join costs what a split
   // gains.  64-row tiles where even split 128-row tiles would leave CUs without work ([1000,
   // 1000] x [1000, 1000] forward and back 32 us, 41 in 128-row tiles; but [512, 5120] x
@@ -194,7 +196,7 @@ GemmPlan plan_gemm(int M, int N, int K, bool at, bool bt, int64_t lda, int64_t l
   if (stages <= 2 || t128 * (stages / 8 + 1) < kCUs)
     p.tile = 64;
   else
-    p.tile = fill(t256, kCUs) >= 0.85 * fill((int64_t)t128 * splits(t128), 2 * kCUs) ? 256 : 128;
+    p.tile = fill(t256, kCUs) >= (stages <= 24 ? 0.85 : 0.8) * fill((int64_t)t128 * splits(t128), 2 * kCUs) ? 256 : 128;
   if (p.tile < 256) {
     const int s = splits(p.tile == 128 ? t128 : ceil_div(M, 64) * ceil_div(N, 64));
     if (s > 1) {
