@@ -309,9 +309,9 @@ int beam_moe_stream_rows(const beam_moe_dims* dims, int32_t T, int fp8);
  * the model's dense sublayers, needs next to it.  The conventions above hold;
  * in addition
  * - matrices are given with a row stride in elements (ld... >= the number of
- *   columns), so a matrix may be the first columns of a wider buffer.  Any
- *   strides and sizes work; the fastest kernels run where rows start on 16
- *   bytes and hold whole groups of 8 elements;
+ *   columns), so a matrix may be the first columns of a wider buffer; rows may
+ *   start at any element (a product of more than 16 rows first lays out operands
+ *   anew whose rows do not start on 16 bytes or hold whole groups of 8 elements);
  * - element types are given as BEAM_MOE_BF16, _F16 or _F32;
  * - every sum is held in FP32 or FP64 and every result is rounded once, to
  *   nearest even, when it is stored;
@@ -436,8 +436,8 @@ int beam_moe_linear(int32_t rows, int32_t cols, int32_t inner, int type, const v
  *   dx     [rows, inner] of `type`, dw [cols, inner] of `type`, dbias [cols] fp32,
  *          dres [rows, cols] of dy_type: each NULL = not wanted, one at least wanted;
  *          x is needed for dw and w for dx (else NULL)
- * dz enters the two products rounded to `type` (dbias sums it unrounded).  When
- * rows = 0, dw and dbias are zeros. */
+ * dz enters the two products rounded to `type` (dbias sums it unrounded), so in fp16
+ * a dz past 65504 becomes an infinity there.  When rows = 0, dw and dbias are zeros. */
 int beam_moe_linear_backward(int32_t rows, int32_t cols, int32_t inner, int type, const void* dy, int dy_type,
                              int64_t lddy, const void* x, int64_t ldx, const void* w, int64_t ldw, const void* pre,
                              int64_t ldpre, int act, float keep, float add, void* dx, int64_t lddx, void* dw,
