@@ -264,7 +264,7 @@ BALANCE = [  # T, E, K, lengths, tokens before the first sequence
     (1, 256, 8, [1], 0), (4, 16, 4, [4], 0), (64, 256, 8, [64], 0), (64, 60, 3, [10, 0, 1, 50], 0),
     (500, 256, 8, [0, 0, 499], 1), (513, 256, 8, [513], 0), (700, 129, 16, [64, 64, 1, 0, 63, 400], 5),
     (3000, 200, 8, [1] * 100 + [0] * 30 + [2500], 11), (5000, 256, 8, [129, 4000, 0, 800], 64),
-    (4096, 7, 2, [4096], 0), (40000, 32, 1, [39999], 0), (2048, 256, 8, [2] * 1000, 0),
+    (4096, 7, 2, [4096], 0), (50, 1, 1, [20, 30], 0), (600, 1, 1, [600], 0), (40000, 32, 1, [39999], 0), (2048, 256, 8, [2] * 1000, 0),
 ]
 
 
@@ -548,6 +548,24 @@ def test_linear_in_place_padding_and_nan(M, N, K):
     z = fw.beam_moe_linear(x, w, act="silu")
     assert torch.equal(z[keep][:, : N - 1], y[keep][:, : N - 1])
     assert fw.beam_moe_linear(x[:0], w).shape == (0, N)
+
+
+def test_activations_far_from_zero():
+    """Arguments at which exponentials over- and underflow: finite values and slopes, at their limits."""
+    _say("activations")
+    z = torch.tensor([0.0, -0.0, 1e-30, -1e-30, 20.0, -20.0, 90.0, -90.0, 200.0, -200.0, 3e4, -3e4], device=DEV)
+    w = torch.zeros((z.numel(), 8), dtype=BF16, device=DEV)
+    x = torch.zeros((3, 8), dtype=BF16, device=DEV)
+    for act, fn in ACTS.items():
+        y = fw.beam_moe_linear(x, w, z, act=act, out_dtype=F32)
+        want = fn(z.double())
+        # sigmoid moves by |z| half steps of e^-z: 0.6 u of 1 in z s; erf and the rest to a few steps
+        _near(y, want.expand(3, -1), 8 * U * (want.abs() + 1) * z.abs().clamp(max=1) + 2.0 ** -149, act)
+        pre = z.to(BF16).expand(3, -1).contiguous()
+        dy = torch.ones((3, z.numel()), device=DEV)
+        _, _, db = fw.beam_moe_linear_backward(dy, x, w, pre, act=act)
+        slope = _slope(pre[0], act) if act != "none" else torch.ones_like(z)
+        _near(db, 3 * slope.double(), 3 * 8 * U * (slope.double().abs() + 1), act)
 
 
 def _slope(z, act):
