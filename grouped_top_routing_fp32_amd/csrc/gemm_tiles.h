@@ -268,10 +268,10 @@ __device__ __forceinline__ void gemm_tile(uint16_t* ring, GemmArgs g, int mt, in
       rows_of([&](int m, f32x4 v) { *reinterpret_cast<f32x4*>(p + (int64_t)m * ldpart) = v; });
     } else if constexpr (EPI) {
       by_act(g.act, [&](auto act) {
-        for (int r = qr; r < rmax; r += kRowsAtOnce) epilogue4<decltype(act)::value>(g, mp + r, n, sum_at(r));
+        for (int r = qr; r < rmax; r += kRowsAtOnce) epilogue4<decltype(act)::value>(g, mp + r, n, g.N, sum_at(r));
       });
     } else {
-      rows_of([&](int m, f32x4 v) { epilogue4<kActNone>(g, m, n, v); });
+      rows_of([&](int m, f32x4 v) { epilogue4<kActNone>(g, m, n, g.N, v); });
     }
   }
 }

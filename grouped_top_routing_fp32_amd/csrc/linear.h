@@ -158,12 +158,12 @@ __device__ __forceinline__ void epilogue1(const GemmArgs& g, int m, int n, float
   store_elem(g.out, (int64_t)m * g.ldo + n, g.out_type, v);
 }
 
-// Columns n .. n + 3 (n a multiple of four) of row m, those past N left alone.
+// Columns n .. n + 3 of row m, those from `end` on left alone.
 template <int ACT>
-__device__ __forceinline__ void epilogue4(const GemmArgs& g, int m, int n, f32x4 z) {
-  if (n + 4 <= g.N) {
+__device__ __forceinline__ void epilogue4(const GemmArgs& g, int m, int n, int end, f32x4 z) {
+  if (n + 4 <= end) {
     if (g.bias) {
-      const f32x4 b = *reinterpret_cast<const f32x4*>(g.bias + n);
+      const f32x4 b = *reinterpret_cast<const f32x4_any*>(g.bias + n);
 #pragma unroll
       for (int q = 0; q < 4; ++q) z[q] += b[q];
     }
@@ -180,7 +180,7 @@ __device__ __forceinline__ void epilogue4(const GemmArgs& g, int m, int n, f32x4
   } else {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      if (n + q < g.N) epilogue1<ACT>(g, m, n + q, z[q]);
+      if (n + q < end) epilogue1<ACT>(g, m, n + q, z[q]);
   }
 }
 

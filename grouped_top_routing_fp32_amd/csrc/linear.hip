@@ -27,21 +27,23 @@ __global__ __launch_bounds__(256) void gemm_join_kernel(GemmArgs g, const float*
 #pragma unroll
     for (int q = 0; q < 4; ++q) z[q] += v[q];
   }
-  by_act(g.act, [&](auto act) { epilogue4<decltype(act)::value>(g, m, n, z); });
+  by_act(g.act, [&](auto act) { epilogue4<decltype(act)::value>(g, m, n, g.N, z); });
 }
 
-// Few rows (M <= 16, both operands K contiguous): bound by reading w once.  A workgroup
-// takes 16 columns; its 8 waves share K in pieces of 128, straight from memory into
-// MFMA operands (a wave reads 256 contiguous bytes of 16 rows of w), and their sums are
-// joined in LDS in wave order.
-constexpr int kSkinnyWaves = 8;
+// Few rows (M <= 16, both operands K contiguous): bound by reading w once, and one CU
+// takes no more than some 22 bytes a nanosecond from beyond its L2.  So a workgroup takes
+// `cols` <= 16 columns, as many as share w evenly among the CUs; its 16 waves share K in
+// pieces of 128, straight from memory into MFMA operands (a wave reads 256 contiguous
+// bytes of a row of w; operand rows past cols repeat the last), and their sums are joined
+// in LDS in wave order.
+constexpr int kSkinnyWaves = 16;
 
 template <bool HALF>
-__global__ __launch_bounds__(64 * kSkinnyWaves) void gemm_skinny_kernel(GemmArgs g) {
+__global__ __launch_bounds__(64 * kSkinnyWaves) void gemm_skinny_kernel(GemmArgs g, int cols) {
   __shared__ f32x4 sum[kSkinnyWaves][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, gr = lane >> 4;
-  const int n0 = blockIdx.x * 16;
-  const uint16_t* wrow = static_cast<const uint16_t*>(g.b) + (int64_t)min(n0 + l16, g.N - 1) * g.ldb;
+  const int n0 = blockIdx.x * cols, n1 = min(g.N, n0 + cols);
+  const uint16_t* wrow = static_cast<const uint16_t*>(g.b) + (int64_t)min(n0 + l16, n1 - 1) * g.ldb;
   const uint16_t* xrow = static_cast<const uint16_t*>(g.a) + (int64_t)min(l16, g.M - 1) * g.lda;
   auto chunk = [&](const uint16_t* row, int k) {  // 8 elements from k, 0 past K
     u32x4 v = {0u, 0u, 0u, 0u};
@@ -55,15 +57,24 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void gemm_skinny_kernel(GemmArgs
     return v;
   };
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  for (int k = 128 * wave; k < g.K; k += 128 * kSkinnyWaves) {
+  // whole pieces without a test, so that all of their loads are in flight together
+  int k = 128 * wave;
+  for (; k + 128 <= g.K; k += 128 * kSkinnyWaves) {
     u32x4 fw[4], fx[4];
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      fw[s] = chunk(wrow, k + 32 * s + 8 * gr);
-      fx[s] = chunk(xrow, k + 32 * s + 8 * gr);
+      fw[s] = *reinterpret_cast<const u32x4_any*>(wrow + k + 32 * s + 8 * gr);
+      fx[s] = *reinterpret_cast<const u32x4_any*>(xrow + k + 32 * s + 8 * gr);
     }
 #pragma unroll
     for (int s = 0; s < 4; ++s) acc = mfma<HALF>(fw[s], fx[s], acc);
+  }
+  if (k < g.K) {  // K's last piece, one wave's
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int ks = k + 32 * s + 8 * gr;
+      acc = mfma<HALF>(chunk(wrow, ks), chunk(xrow, ks), acc);
+    }
   }
   sum[wave][lane] = acc;
   __syncthreads();
@@ -76,8 +87,8 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void gemm_skinny_kernel(GemmArgs
     for (int q = 0; q < 4; ++q) z[q] += v[q];
   }
   const int n = n0 + 4 * gr;
-  if (l16 >= g.M || n >= g.N) return;
-  by_act(g.act, [&](auto act) { epilogue4<decltype(act)::value>(g, l16, n, z); });
+  if (l16 >= g.M || n >= n1) return;
+  by_act(g.act, [&](auto act) { epilogue4<decltype(act)::value>(g, l16, n, n1, z); });
 }
 
 // Lays one or two operands out anew, the first with blocks workgroups and the second with
@@ -155,8 +166,8 @@ namespace {
 
 constexpr int kBK = 64;  // K per stage of the tiled kernel
 constexpr int kCUs = 256;
-// Up to here the skinny kernel: 2560 columns, K 5120: 11.3 us at 16 rows against 12.8 in
-// tiles; its form for 32 rows took 15.9 against 12.8.
+// Up to here the skinny kernel: 2560 columns, K 5120: 10.4 us at 16 rows against 12.7 in
+// tiles; a form of it for 32 rows took 15.9 against 12.8.
 constexpr int kSkinnyRows = 16;
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
@@ -220,8 +231,13 @@ GemmPlan plan_gemm(int M, int N, int K, bool at, bool bt, int64_t lda, int64_t l
 namespace {
 
 hipError_t launch_skinny(const GemmArgs& g, hipStream_t st) {
+  // [1, 5120] x [5120, 5120], 320 workgroups of 16 columns 16.5 us, 512 of 10 13.1 us; below
+  // 4 columns x is read more often than w
+  const int rounds = ceil_div(g.N, 16 * kCUs);
+  int cols = ceil_div(g.N, rounds * kCUs);
+  cols = cols < 4 ? 4 : cols;
   hipLaunchKernelGGL(g.type == kElemF16 ? gemm_skinny_kernel<true> : gemm_skinny_kernel<false>,
-                     dim3(ceil_div(g.N, 16)), dim3(64 * kSkinnyWaves), 0, st, g);
+                     dim3(ceil_div(g.N, cols)), dim3(64 * kSkinnyWaves), 0, st, g, cols);
   return hipGetLastError();
 }
 
