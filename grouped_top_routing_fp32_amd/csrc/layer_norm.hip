@@ -348,11 +348,8 @@ static int backward_groups(int T, int teams) {
   return n < 256 ? n : 256;
 }
 
-// The most rows of partial sums of a call on rows of H columns, whatever their strides.
-int layer_norm_backward_units(int T, int H) {
-  (void)H;
-  return T < 256 ? T : 256;
-}
+// The most rows of partial sums of a call.
+int layer_norm_backward_units(int T) { return T < 256 ? T : 256; }
 
 hipError_t launch_layer_norm_backward(const void* dy, int dy_type, int64_t lddy, const void* x, int x_type,
                                       int64_t ldx, const float* mean, const float* rstd, const float* gamma, void* dx,

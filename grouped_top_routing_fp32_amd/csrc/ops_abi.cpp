@@ -9,7 +9,7 @@
 
 namespace beam {
 int layer_norm_max_cols();
-int layer_norm_backward_units(int T, int H);
+int layer_norm_backward_units(int T);
 hipError_t launch_layer_norm(const void* x, int x_type, int64_t ldx, const float* gamma, const float* beta, void* y,
                              int y_type, int64_t ldy, float* mean, float* rstd, int T, int H, float eps,
                              hipStream_t st);
@@ -118,7 +118,7 @@ int beam_moe_layer_norm(int32_t rows, int32_t cols, const void* x, int x_type, i
 
 size_t beam_moe_layer_norm_backward_workspace_bytes(int32_t rows, int32_t cols) {
   if (check_norm(rows, cols) != BEAM_MOE_OK) return SIZE_MAX;
-  return (size_t)beam::layer_norm_backward_units(rows, cols) * cols * 2 * sizeof(float);
+  return (size_t)beam::layer_norm_backward_units(rows) * cols * 2 * sizeof(float);
 }
 
 int beam_moe_layer_norm_backward(int32_t rows, int32_t cols, const void* dy, int dy_type, int64_t lddy, const void* x,
