@@ -68,6 +68,10 @@ __device__ __forceinline__ void load_row(const float* __restrict__ row, int E, i
   }
 }
 
+// Scores that sum to less than kTiny are taken kUp times as large (exactly, so their shares
+// of the sum stay the same): the reciprocal of a sum near 2^-128 or below is infinite.
+constexpr float kTiny = 0x1p-100f, kUp = 0x1p64f;
+
 // Adds rows [r0, r1) of p and their slots' experts: sp[e] (this workgroup's sums,
 // one plane per wave, added in wave order at the end) and the integer counts sc[e].
 // Both are complete for every thread on return.
@@ -98,6 +102,11 @@ __device__ void sum_rows(const float* __restrict__ scores, const int32_t* __rest
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       s[u] = wave_sum(s[u]);
+      if (s[u] < kTiny) {  // uniform, as the sum is
+        s[u] *= kUp;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[u][i] *= kUp;
+      }
       const float inv = s[u] == 0.f ? 0.f : 1.f / s[u];  // a row of zeros (or past the end) adds nothing
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[i] += v[u][i] * inv;
@@ -218,11 +227,11 @@ __global__ __launch_bounds__(kBalFinishThreads) void balance_finish_kernel(Units
 // ---------------------------------------------------------------------------
 // gradient with respect to the logits
 // ---------------------------------------------------------------------------
-// dlogit = ds s (1 - s), ds the sum of two parts:
-//   routing weights w_k = scale s_k / S_K over the K chosen experts, S_K = sum_k s_k:
-//     ds_k = scale / S_K (dw_k - sum_j dw_j s_j / S_K)
+// dlogit = ds s (1 - s); ds s is the sum of two parts, in shares p = s / S of a sum:
+//   routing weights w_k = scale p_k over the K chosen experts, S = sum_k s_k:
+//     scale p_k (dw_k - sum_j dw_j p_j)
 //   balance loss, g_e = dloss[b] alpha E count[b,e] / (K n^2), S = sum_e s_e:
-//     ds_e = (g_e - sum_j g_j s_j / S) / S
+//     p_e (g_e - sum_j g_j p_j)
 // A constant added to every g_e changes nothing, so g is taken from the exact integers
 // E count - K n: with near-even counts the difference would lose most of its digits.
 // One wave per token; a slot whose id lies outside [0, E) is skipped.  Bound by vector
@@ -301,10 +310,20 @@ __global__ __launch_bounds__(64 * kGradWaves) void route_backward_kernel(
       }
       tot = wave_sum(tot);
       dot = wave_sum(dot);
+      if (tot < kTiny) {  // uniform; 1 - s is 1 for these either way
+        tot *= kUp;
+        dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s[i] *= kUp;
+          dot += g[i] * s[i];
+        }
+        dot = wave_sum(dot);
+      }
       const float inv = tot == 0.f ? 0.f : 1.f / tot;
       const float m = dot * inv, ci = c * inv;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) ds[i] = ci * (g[i] - m);
+      for (int i = 0; i < 4; ++i) ds[i] = ci * s[i] * (g[i] - m);
     }
   }
   if (dw) {
@@ -317,15 +336,22 @@ __global__ __launch_bounds__(64 * kGradWaves) void route_backward_kernel(
     const int place = V4 ? id : 4 * (id & 63) + (id >> 6);
     rows[wave][lane] = f32x4{s[0], s[1], s[2], s[3]};
     in_order();
-    const float sk = ok ? row[place] : 0.f;
+    float sk = ok ? row[place] : 0.f;
     in_order();
     rows[wave][lane] = f32x4{0.f, 0.f, 0.f, 0.f};
     if (!ok) d = 0.f;
     // K <= 16: the slots all lie in the first 16 lanes
-    const float tot = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(row16_sum(sk)), 0));
-    const float dot = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(row16_sum(d * sk)), 0));
+    auto slot_sum = [](float v) {
+      return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(row16_sum(v)), 0));
+    };
+    float tot = slot_sum(sk), dot = slot_sum(d * sk);
+    if (tot < kTiny) {  // uniform
+      tot *= kUp;
+      sk *= kUp;
+      dot = slot_sum(d * sk);
+    }
     const float inv = tot == 0.f ? 0.f : 1.f / tot;
-    const float a = scale * inv * (d - dot * inv);
+    const float a = scale * inv * sk * (d - dot * inv);
     // slots of one expert: each holds the sum over all of them, in slot order
     float all = 0.f;
     for (int k = 0; k < K; ++k) {
@@ -344,7 +370,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void route_backward_kernel(
   float o[4];
   // an expert without any gradient has 0 whatever its score holds (padding may hold anything)
 #pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = ds[i] == 0.f ? 0.f : ds[i] * s[i] * (1.f - s[i]);
+  for (int i = 0; i < 4; ++i) o[i] = ds[i] == 0.f ? 0.f : ds[i] * (1.f - s[i]);
   if constexpr (V4) {
     if (4 * lane < E) *reinterpret_cast<f32x4*>(out + 4 * lane) = f32x4{o[0], o[1], o[2], o[3]};
   } else {

@@ -206,7 +206,7 @@ GemmPlan plan_gemm(int M, int N, int K, bool at, bool bt, int64_t lda, int64_t l
   };
   if (t128 > 1 << 20)  // so large a grid of smaller tiles would pass 2^32 threads
     p.tile = 256;
-  else if (stages <= 2 || t128 * (stages / 8 + 1) < kCUs)
+  else if (stages <= 2 || (int64_t)t128 * (stages / 8 + 1) < kCUs)
     p.tile = 64;
   else
     p.tile = fill(t256, kCUs) >= (stages <= 24 ? 0.85 : 0.8) * fill((int64_t)t128 * splits(t128), 2 * kCUs) ? 256 : 128;

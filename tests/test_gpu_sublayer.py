@@ -117,6 +117,22 @@ def test_layer_norm_far_mean_constant_rows_and_nan(cols):
     assert z[2].isnan().all() and z[5].isnan().any()
 
 
+@pytest.mark.parametrize("cols", [96, 2561, 5120, 16383])
+def test_layer_norm_large_constant_rows(cols):
+    """Equal columns of any size have variance 0, never a negative one.  A wave's mean P is off by e <= 64 u |x|,
+    the rest D by 64 u e, so the variance comes out within 64 u e^2 and y within 64 u e rstd."""
+    _say("layer_norm large constants", cols)
+    g = _gen(cols)
+    c = torch.rand((200,), generator=g, device=DEV) * 10.0 ** torch.linspace(0, 12, 200, device=DEV)
+    y, mean, rstd = fw.beam_moe_layer_norm(c[:, None].expand(200, cols).contiguous(), eps=1e-5)
+    e = 64 * U * c.double()
+    assert y.isfinite().all() and rstd.isfinite().all()
+    assert ((mean.double() - c.double()).abs() <= 64 * U * e + U * c.double()).all()
+    assert (rstd.double() <= 1e-5 ** -0.5 * (1 + 8 * U)).all()
+    assert (rstd.double() >= (1e-5 + 64 * U * e * e) ** -0.5 * (1 - 8 * U)).all()
+    assert (y.double().abs() <= (64 * U * e * 1e-5 ** -0.5)[:, None]).all()
+
+
 def test_layer_norm_zero_eps_and_padding_untouched():
     _say("layer_norm padding")
     g = _gen(3)
@@ -300,6 +316,36 @@ def test_balance_loss_keeps_nan_in_its_sequence(T):
     assert loss[1].isnan() and prob[1].isnan().all()
     assert loss[[0, 2]].isfinite().all() and prob[[0, 2]].isfinite().all()
     assert torch.equal(counts.long(), _balance_ref(scores, ids, off, 1.0, 8)[1])
+
+
+def _faint(T, E, K, seed):
+    """Scores of logits near -95, below the smallest normal number, but for the first row."""
+    g = _gen(seed)
+    scores = (0.1 + 0.9 * torch.rand((T, E), generator=g, device=DEV)) * 2.0 ** -132
+    scores[0] = torch.rand((E,), generator=g, device=DEV)
+    assert (scores[1:] > 0).all() and float(scores[1:].max()) < torch.finfo(F32).tiny
+    ids = torch.rand((T, E), generator=g, device=DEV).topk(K, dim=1).indices.int()
+    return scores, ids
+
+
+@pytest.mark.parametrize("T,E,K", [(40, 100, 4), (33, 101, 4), (700, 256, 8), (600, 9, 2)])
+def test_faint_scores(T, E, K):
+    """The shares of scores whose sum has no finite reciprocal in FP32 are as good as any others'.  Bounds as in
+    the tests of ordinary scores."""
+    _say("faint scores", T, E, K)
+    scores, ids = _faint(T, E, K, T + E)
+    loss, counts, prob = fw.beam_moe_balance_loss(_dims(E, K), scores, ids, alpha=0.3)
+    rl, rc, rp = _balance_ref(scores, ids, [0, T], 0.3, K)
+    assert torch.equal(counts.long(), rc)
+    _near(prob, rp, 100 * U * rp, "prob")
+    _near(loss, rl, 100 * U * rl, "loss")
+    g = _gen(T)
+    dw, dloss = torch.randn((T, K), generator=g, device=DEV), torch.randn((1,), generator=g, device=DEV)
+    for w, l in ((dw, dloss), (dw, None), (None, dloss)):
+        got = fw.beam_moe_route_backward(_dims(E, K), scores, ids, dw=w, dloss=l, alpha=0.5,
+                                         counts=counts if l is not None else None)
+        want, mag = _route_back_ref(scores, ids, w, 2.5, [0, T], 0.5, l, counts, K)
+        _near(got, want, 40 * U * mag, (w is None, l is None))
 
 
 def test_balance_loss_of_no_tokens_is_zero():
