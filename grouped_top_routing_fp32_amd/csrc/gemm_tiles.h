@@ -284,25 +284,44 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(GemmArgs g, int mt, i
                                                ldpart);
 }
 
-// dx = dz w and dw = dz^T x of small sizes, both in whole 64-row tiles, in one launch: neither
-// fills the card alone, and each launch costs more than a stage or two of K.  dx's tiles
-// come first.  (Large ones gain nothing: 429 us either way at [8192, 5120] x [2560, 5120],
+// dx = dz w and dw = dz^T x of small sizes, both in whole 64-row tiles, and the column sums
+// of dbias in one launch: none fills the card alone, and each launch costs more than a
+// stage or two of K.  dx's tiles come first, then dw's; a workgroup of the sums takes 16
+// columns, thread (c, g) the rows g, g + 16, ... of column c, and adds a column's 16 sums
+// in order, in FP64.  (Large ones gain nothing: 429 us either way at [8192, 5120] x [2560, 5120],
 // where the matrix cores' power is the bound and idle CUs leave the others more of it.)
 template <bool HALF>
-__global__ __launch_bounds__(256) void gemm_pair_kernel(GemmArgs dx, GemmArgs dw) {
+__global__ __launch_bounds__(256) void gemm_pair_kernel(GemmArgs dx, GemmArgs dw, SumJob sums) {
   __shared__ __align__(1024) uint16_t ring[kRing<64, 64>];
   const int mx = (dx.M + 63) / 64, nx = (dx.N + 63) / 64, mw = (dw.M + 63) / 64, nw = (dw.N + 63) / 64;
-  const int b = blockIdx.x, first = mx * nx;
-  if (b < first)
+  const int b = blockIdx.x, first = mx * nx, both = first + mw * nw;
+  if (b < first) {
     gemm_tile<HALF, false, true, 64, 64, 2, 2, false>(ring, dx, mx, nx, xcd_lin(b, first), dx.K, nullptr, 0);
-  else
+  } else if (b < both) {
     gemm_tile<HALF, true, true, 64, 64, 2, 2, false>(ring, dw, mw, nw, xcd_lin(b - first, mw * nw), dw.K, nullptr, 0);
+  } else {
+    float* s = reinterpret_cast<float*>(ring);
+    const int c = threadIdx.x & 15, h = (b - both) * 16 + c;
+    float v = 0.f;
+    if (h < sums.cols)
+#pragma unroll 16
+      for (int u = threadIdx.x >> 4; u < sums.units; u += 16) v += sums.part[(int64_t)u * sums.cols + h];
+    s[threadIdx.x] = v;
+    __syncthreads();
+    if (threadIdx.x < 16 && h < sums.cols) {
+      double a = 0.0;
+#pragma unroll
+      for (int g = 0; g < 16; ++g) a += s[16 * g + c];
+      sums.out[h] = (float)a;
+    }
+  }
 }
 
 template <bool HALF>
-hipError_t launch_gemm_pair(const GemmArgs& dx, const GemmArgs& dw, hipStream_t st) {
+hipError_t launch_gemm_pair(const GemmArgs& dx, const GemmArgs& dw, const SumJob& sums, hipStream_t st) {
   auto tiles = [](const GemmArgs& g) { return ((g.M + 63) / 64) * ((g.N + 63) / 64); };
-  hipLaunchKernelGGL(gemm_pair_kernel<HALF>, dim3(tiles(dx) + tiles(dw)), dim3(256), 0, st, dx, dw);
+  hipLaunchKernelGGL(gemm_pair_kernel<HALF>, dim3(tiles(dx) + tiles(dw) + (sums.out ? (sums.cols + 15) / 16 : 0)),
+                     dim3(256), 0, st, dx, dw, sums);
   return hipGetLastError();
 }
 

@@ -46,9 +46,17 @@ struct GemmPlan {
 // padded: both operands' rows are whole chunks of 8 elements (zeros past the end of K), whatever the sizes.
 GemmPlan plan_gemm(int M, int N, int K, bool at, bool bt, int64_t lda, int64_t ldb, bool padded = false);
 hipError_t launch_gemm(const GemmArgs& g, const GemmPlan& p, void* ws, hipStream_t st);
-// Both gradients' products, one after the other or, where both take 64-row tiles whole, in one launch.
-hipError_t launch_gemm_pair(const GemmArgs& dx, const GemmPlan& px, const GemmArgs& dw, const GemmPlan& pw, void* ws,
-                            hipStream_t st);
+// out[h] = sum_u part[u][h]; out null: nothing to do.
+struct SumJob {
+  const float* part;
+  float* out;
+  int units, cols;
+};
+// Both gradients' products and the column sums of dbias, one after the other or, where both products take
+// 64-row tiles whole, in one launch.
+hipError_t launch_gemm_pair(const GemmArgs& dx, const GemmPlan& px, const GemmArgs& dw, const GemmPlan& pw,
+                            const SumJob& sums, void* ws, hipStream_t st);
+hipError_t launch_column_sums(const float* part, float* out0, float* out1, int units, int H, hipStream_t st);
 
 // A matrix to be laid out anew: dst rows of up8(cols) elements, zeros past cols.
 struct PadJob {
@@ -64,8 +72,8 @@ inline size_t padded_bytes(int rows, int cols) { return (size_t)rows * up8(cols)
 hipError_t launch_pad(const PadJob& first, const PadJob& second, hipStream_t st);
 hipError_t launch_gemm_bf16(const GemmArgs& g, const GemmPlan& p, float* part, int64_t ldpart, hipStream_t st);
 hipError_t launch_gemm_f16(const GemmArgs& g, const GemmPlan& p, float* part, int64_t ldpart, hipStream_t st);
-hipError_t launch_gemm_pair_bf16(const GemmArgs& dx, const GemmArgs& dw, hipStream_t st);
-hipError_t launch_gemm_pair_f16(const GemmArgs& dx, const GemmArgs& dw, hipStream_t st);
+hipError_t launch_gemm_pair_bf16(const GemmArgs& dx, const GemmArgs& dw, const SumJob& sums, hipStream_t st);
+hipError_t launch_gemm_pair_f16(const GemmArgs& dx, const GemmArgs& dw, const SumJob& sums, hipStream_t st);
 
 template <bool HALF>
 __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {

@@ -91,15 +91,20 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void gemm_skinny_kernel(GemmArgs
   by_act(g.act, [&](auto act) { epilogue4<decltype(act)::value>(g, l16, n, n1, z); });
 }
 
-// Lays one or two operands out anew, the first with blocks workgroups and the second with
-// the rest: one launch for what a product or both gradients need.
-__global__ __launch_bounds__(256) void pad_rows_kernel(PadJob first, PadJob second, int blocks) {
-  const bool other = (int)blockIdx.x >= blocks;
-  const PadJob j = other ? second : first;
-  const int64_t threads = 256 * (int64_t)(other ? gridDim.x - blocks : blocks);
+// Lays one or two operands out anew, the first with `blocks` workgroups of 256 threads and the
+// second with the rest: one launch for what a product or both gradients need.  b is the
+// workgroup's place among `total`.
+struct PadJobs {
+  PadJob first, second;
+  int blocks, total;
+};
+__device__ __forceinline__ void pad_rows(const PadJobs& p, int b, int tid) {
+  const bool other = b >= p.blocks;
+  const PadJob j = other ? p.second : p.first;
+  const int64_t threads = 256 * (int64_t)(other ? p.total - p.blocks : p.blocks);
   const int chunks = (j.cols + 7) / 8;
   const int64_t n = (int64_t)j.rows * chunks;
-  for (int64_t i = (int64_t)(blockIdx.x - (other ? blocks : 0)) * 256 + threadIdx.x; i < n; i += threads) {
+  for (int64_t i = (int64_t)(b - (other ? p.blocks : 0)) * 256 + tid; i < n; i += threads) {
     const int r = (int)(i / chunks), c = (int)(i % chunks) * 8;
     const uint16_t* s = static_cast<const uint16_t*>(j.src) + (int64_t)r * j.ld + c;
     Raw8<F16> v;  // the bits alone matter
@@ -111,10 +116,14 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(PadJob first, PadJob seco
   }
 }
 
+__global__ __launch_bounds__(256) void pad_rows_kernel(PadJobs p) { pad_rows(p, blockIdx.x, threadIdx.x); }
+
 // dz[m, n] = add dy act'(z), rounded to the products' 16-bit type (the rounding that a
 // gradient kept between two layers has anyway); part[u][n] = the unit's sum of the
-// unrounded dz; dres = keep dy.  grid (ceil(N / 512), units), block (64, 4): thread (c, r)
-// takes 8 columns in rows r, r + 4, ... of the unit.  dz rows are lddz long, a multiple of
+// unrounded dz; dres = keep dy.  grid ceil(N / 512) * units, block (64, 4): thread (c, r)
+// takes 8 columns in rows r, r + 4, ... of the unit.  Behind them the workgroups that lay the
+// products' other operands out anew, which would leave most of the card idle in a launch of
+// their own.  dz rows are lddz long, a multiple of
 // 8, with zeros past N.  Bound by HBM and, with a smooth activation, its arithmetic:
 // [8192, 2560] bf16 SiLU 26 us for 126 MB.
 template <class DT, class T>
@@ -123,17 +132,19 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(const typename DT::S* __
                                                         float keep, float add, typename T::S* __restrict__ dz,
                                                         int64_t lddz, float* __restrict__ part,
                                                         typename DT::S* __restrict__ dres, int64_t lddres, int M, int N,
-                                                        int rows) {
+                                                        int units, int rows, PadJobs pad) {
   __shared__ float sums[4][64][8];
-  const int n = (blockIdx.x * 64 + threadIdx.x) * 8, y = threadIdx.y;
+  const int wide = (N + 511) / 512, bx = blockIdx.x % wide, unit = blockIdx.x / wide;
+  if (unit >= units) return pad_rows(pad, blockIdx.x - wide * units, threadIdx.y * 64 + threadIdx.x);
+  const int n = (bx * 64 + threadIdx.x) * 8, y = threadIdx.y;
   const int cols = min(8, N - n);  // <= 0: none
-  const int m1 = min(M, (int)(blockIdx.y + 1) * rows);
+  const int m1 = min(M, (unit + 1) * rows);
   float s[8] = {};
   if (cols > 0) {
     by_act(act, [&](auto a) {
       constexpr int ACT = decltype(a)::value;
 #pragma unroll 4
-      for (int m = blockIdx.y * rows + y; m < m1; m += 4) {
+      for (int m = unit * rows + y; m < m1; m += 4) {
         float d[8], v[8], zz[8] = {};
         load8<DT>(dy + (int64_t)m * lddy + n, cols, d);  // zeros past N
         if constexpr (ACT != kActNone) load8<T>(z + (int64_t)m * ldz + n, cols, zz);
@@ -153,9 +164,9 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(const typename DT::S* __
   for (int q = 0; q < 8; ++q) sums[y][threadIdx.x][q] = s[q];
   __syncthreads();
   for (int i = y * 64 + threadIdx.x; i < 512; i += 256) {
-    const int c = i / 8, q = i % 8, col = blockIdx.x * 512 + i;
+    const int c = i / 8, q = i % 8, col = bx * 512 + i;
     if (col < N)
-      part[(int64_t)blockIdx.y * N + col] = (sums[0][c][q] + sums[1][c][q]) + (sums[2][c][q] + sums[3][c][q]);
+      part[(int64_t)unit * N + col] = (sums[0][c][q] + sums[1][c][q]) + (sums[2][c][q] + sums[3][c][q]);
   }
 }
 
@@ -243,14 +254,19 @@ hipError_t launch_skinny(const GemmArgs& g, hipStream_t st) {
 
 }  // namespace
 
-hipError_t launch_pad(const PadJob& first, const PadJob& second, hipStream_t st) {
+static PadJobs pad_jobs(const PadJob& first, const PadJob& second) {
   auto blocks = [](const PadJob& j) {
     const int64_t n = (j.rows * (up8(j.cols) / 8) + 255) / 256;
     return (int)(n < (1 << 20) ? n : 1 << 20);
   };
   const int a = blocks(first), b = blocks(second);
-  if (a + b == 0) return hipSuccess;
-  hipLaunchKernelGGL(pad_rows_kernel, dim3(a + b), dim3(256), 0, st, first, second, a);
+  return {first, second, a, a + b};
+}
+
+hipError_t launch_pad(const PadJob& first, const PadJob& second, hipStream_t st) {
+  const PadJobs p = pad_jobs(first, second);
+  if (p.total == 0) return hipSuccess;
+  hipLaunchKernelGGL(pad_rows_kernel, dim3(p.total), dim3(256), 0, st, p);
   return hipGetLastError();
 }
 
@@ -282,15 +298,14 @@ hipError_t launch_gemm(const GemmArgs& args, const GemmPlan& p, void* ws, hipStr
   return hipGetLastError();
 }
 
-hipError_t launch_gemm_pair(const GemmArgs& dx, const GemmPlan& px, const GemmArgs& dw, const GemmPlan& pw, void* ws,
-                            hipStream_t st) {
+hipError_t launch_gemm_pair(const GemmArgs& dx, const GemmPlan& px, const GemmArgs& dw, const GemmPlan& pw,
+                            const SumJob& sums, void* ws, hipStream_t st) {
   auto whole = [](const GemmPlan& p) { return p.kind == GemmPlan::kTiles && p.tile == 64 && p.splits == 1; };
   if (dx.M > 0 && whole(px) && whole(pw))
-    return dx.type == kElemF16 ? launch_gemm_pair_f16(dx, dw, st) : launch_gemm_pair_bf16(dx, dw, st);
-  if (dx.M > 0) {
-    const hipError_t e = launch_gemm(dx, px, ws, st);
-    if (e != hipSuccess) return e;
-  }
+    return dx.type == kElemF16 ? launch_gemm_pair_f16(dx, dw, sums, st) : launch_gemm_pair_bf16(dx, dw, sums, st);
+  hipError_t e = sums.out ? launch_column_sums(sums.part, sums.out, nullptr, sums.units, sums.cols, st) : hipSuccess;
+  if (e == hipSuccess && dx.M > 0) e = launch_gemm(dx, px, ws, st);
+  if (e != hipSuccess) return e;
   return launch_gemm(dw, pw, ws, st);
 }
 
@@ -301,14 +316,16 @@ int linear_dz_units(int M) { return M < 8 ? 1 : M / 4 < 256 ? M / 4 : 256; }
 
 hipError_t launch_linear_dz(const void* dy, int dy_type, int64_t lddy, const void* z, int64_t ldz, int act, float keep,
                             float add, uint16_t* dz, int64_t lddz, int type, float* part, void* dres, int64_t lddres,
-                            int M, int N, hipStream_t st) {
+                            int M, int N, const PadJob& first, const PadJob& second, hipStream_t st) {
   const int units = linear_dz_units(M), rows = ceil_div(M, units);
+  const PadJobs pad = pad_jobs(first, second);
   auto go = [&](auto dt, auto t) {
     using DT = decltype(dt);
     using T = decltype(t);
-    hipLaunchKernelGGL((linear_dz_kernel<DT, T>), dim3(ceil_div(N, 512), units), dim3(64, 4), 0, st,
+    hipLaunchKernelGGL((linear_dz_kernel<DT, T>), dim3(ceil_div(N, 512) * units + pad.total), dim3(64, 4), 0, st,
                        static_cast<const typename DT::S*>(dy), lddy, static_cast<const typename T::S*>(z), ldz, act,
-                       keep, add, dz, lddz, part, static_cast<typename DT::S*>(dres), lddres, M, N, rows);
+                       keep, add, dz, lddz, part, static_cast<typename DT::S*>(dres), lddres, M, N, units, rows,
+                       pad);
   };
   if (type == kElemF16)
     dy_type == kElemF32 ? go(F32{}, F16{}) : go(F16{}, F16{});

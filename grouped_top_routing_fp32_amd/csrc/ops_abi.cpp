@@ -17,7 +17,6 @@ hipError_t launch_layer_norm_backward(const void* dy, int dy_type, int64_t lddy,
                                       int64_t ldx, const float* mean, const float* rstd, const float* gamma, void* dx,
                                       int64_t lddx, float* dgamma, float* dbeta, float* part, int T, int H,
                                       hipStream_t st);
-hipError_t launch_column_sums(const float* part, float* out0, float* out1, int units, int H, hipStream_t st);
 int balance_units(int T, int B);
 hipError_t launch_balance(const float* scores, const int32_t* ids, int B, const int32_t* off, int T, int E, int K,
                           float alpha, float* loss, int32_t* counts, float* prob, int32_t* part_count, float* part_sum,
@@ -28,7 +27,7 @@ hipError_t launch_route_backward(const float* scores, const int32_t* ids, const 
 int linear_dz_units(int M);
 hipError_t launch_linear_dz(const void* dy, int dy_type, int64_t lddy, const void* z, int64_t ldz, int act, float keep,
                             float add, uint16_t* dz, int64_t lddz, int type, float* part, void* dres, int64_t lddres,
-                            int M, int N, hipStream_t st);
+                            int M, int N, const PadJob& first, const PadJob& second, hipStream_t st);
 }  // namespace beam
 
 namespace {
@@ -254,14 +253,6 @@ int beam_moe_linear_backward(int32_t rows, int32_t cols, int32_t inner, int type
   // dz is dy itself where nothing changes it and its rows are whole chunks
   const bool same = act == BEAM_MOE_ACT_NONE && add == 1.f && dy_type == type && lddy % 8 == 0 && cols % 8 == 0;
   uint16_t* dz = same || !(dx || dw) ? nullptr : at<uint16_t>(ws, p.off_dz);
-  if (rows > 0 && (dz || part || dres))
-    if ((rc = hip_status(beam::launch_linear_dz(dy, dy_type, lddy, pre, ldpre, act, keep, add, dz, p.lddz, type, part,
-                                                dres, lddres, rows, cols, st))) != BEAM_MOE_OK)
-      return rc;
-  if (dbias)
-    if ((rc = hip_status(beam::launch_column_sums(part, dbias, nullptr, rows > 0 ? beam::linear_dz_units(rows) : 0,
-                                                  cols, st))) != BEAM_MOE_OK)
-      return rc;
   beam::PadJob jw{}, jx{};
   if (dx && p.copy_w && rows > 0) {
     jw = {w, ldw, cols, inner, at<void*>(ws, p.off_w)};
@@ -273,7 +264,11 @@ int beam_moe_linear_backward(int32_t rows, int32_t cols, int32_t inner, int type
     x = jx.dst;
     ldx = beam::up8(inner);
   }
-  if ((rc = hip_status(beam::launch_pad(jw, jx, st))) != BEAM_MOE_OK) return rc;
+  rc = hip_status(rows > 0 && (dz || part || dres)
+                      ? beam::launch_linear_dz(dy, dy_type, lddy, pre, ldpre, act, keep, add, dz, p.lddz, type, part,
+                                               dres, lddres, rows, cols, jw, jx, st)
+                      : beam::launch_pad(jw, jx, st));
+  if (rc != BEAM_MOE_OK) return rc;
   beam::GemmArgs gx{}, gw{};
   gx.type = gx.out_type = gw.type = gw.out_type = type;
   gx.add = gw.add = 1.f;
@@ -295,7 +290,12 @@ int beam_moe_linear_backward(int32_t rows, int32_t cols, int32_t inner, int type
   gw.K = rows;
   gw.out = dw;
   gw.ldo = lddw;
-  if (dx && dw) return hip_status(beam::launch_gemm_pair(gx, p.dx, gw, p.dw, gemm_ws, st));
+  const beam::SumJob sums{part, dbias, rows > 0 ? beam::linear_dz_units(rows) : 0, cols};
+  if (dx && dw) return hip_status(beam::launch_gemm_pair(gx, p.dx, gw, p.dw, sums, gemm_ws, st));
+  if (dbias) {
+    rc = hip_status(beam::launch_column_sums(part, dbias, nullptr, sums.units, cols, st));
+    if (rc != BEAM_MOE_OK) return rc;
+  }
   if (dx && rows > 0) return hip_status(beam::launch_gemm(gx, p.dx, gemm_ws, st));
   if (dw) return hip_status(beam::launch_gemm(gw, p.dw, gemm_ws, st));
   return BEAM_MOE_OK;
