@@ -7,8 +7,8 @@ hipError_t launch_gemm_bf16(const GemmArgs& g, const GemmPlan& p, float* part, i
   return launch_gemm_tiles<false>(g, p, part, ldpart, st);
 }
 
-hipError_t launch_gemm_pair_bf16(const GemmArgs& dx, const GemmArgs& dw, const SumJob& sums, hipStream_t st) {
-  return launch_gemm_pair<false>(dx, dw, sums, st);
+hipError_t launch_gemm_pair_bf16(const GemmArgs& dx, const GemmArgs& dw, hipStream_t st) {
+  return launch_gemm_pair<false>(dx, dw, st);
 }
 
 }  // namespace beam

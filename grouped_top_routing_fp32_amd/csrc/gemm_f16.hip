@@ -7,8 +7,8 @@ hipError_t launch_gemm_f16(const GemmArgs& g, const GemmPlan& p, float* part, in
   return launch_gemm_tiles<true>(g, p, part, ldpart, st);
 }
 
-hipError_t launch_gemm_pair_f16(const GemmArgs& dx, const GemmArgs& dw, const SumJob& sums, hipStream_t st) {
-  return launch_gemm_pair<true>(dx, dw, sums, st);
+hipError_t launch_gemm_pair_f16(const GemmArgs& dx, const GemmArgs& dw, hipStream_t st) {
+  return launch_gemm_pair<true>(dx, dw, st);
 }
 
 }  // namespace beam

@@ -276,52 +276,58 @@ __device__ __forceinline__ void gemm_tile(uint16_t* ring, GemmArgs g, int mt, in
   }
 }
 
+// The column sums that run beside dx's product, in workgroups behind its tiles: b's are those
+// of 16 columns, thread (c, g) adds the rows g, g + 16, ... of column c, and a column's 16
+// sums are added in order, in FP64.  As a launch of their own they take 3 to 5 us, mostly
+// latency.
+__device__ __forceinline__ void sum_columns(float* s, const SumJob& j, int b) {
+  const int tid = threadIdx.x, c = tid & 15, h = b * 16 + c;
+  float v = 0.f;
+  if (tid < 256 && h < j.cols)
+#pragma unroll 16
+    for (int u = tid >> 4; u < j.units; u += 16) v += j.part[(int64_t)u * j.cols + h];
+  s[tid] = v;
+  __syncthreads();
+  if (tid < 16 && h < j.cols) {
+    double a = 0.0;
+#pragma unroll
+    for (int g = 0; g < 16; ++g) a += s[16 * g + c];
+    j.out[h] = (float)a;
+  }
+}
+inline int sum_groups(const SumJob& j) { return j.out ? (j.cols + 15) / 16 : 0; }
+
 template <bool HALF, bool AT, bool BT, int BM, int BN, int WM, int WN, bool EPI>
-__global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(GemmArgs g, int mt, int nt, int k_per_split,
+__global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(GemmArgs g, int mt, int nt, int total, int k_per_split,
                                                             float* __restrict__ part, int64_t ldpart) {
   __shared__ __align__(1024) uint16_t ring[kRing<BM, BN>];
-  gemm_tile<HALF, AT, BT, BM, BN, WM, WN, EPI>(ring, g, mt, nt, xcd_lin(blockIdx.x, gridDim.x), k_per_split, part,
-                                               ldpart);
+  if constexpr (BT && !AT)
+    if ((int)blockIdx.x >= total) return sum_columns(reinterpret_cast<float*>(ring), g.sums, blockIdx.x - total);
+  gemm_tile<HALF, AT, BT, BM, BN, WM, WN, EPI>(ring, g, mt, nt, xcd_lin(blockIdx.x, total), k_per_split, part, ldpart);
 }
 
-// dx = dz w and dw = dz^T x of small sizes, both in whole 64-row tiles, and the column sums
-// of dbias in one launch: none fills the card alone, and each launch costs more than a
-// stage or two of K.  dx's tiles come first, then dw's; a workgroup of the sums takes 16
-// columns, thread (c, g) the rows g, g + 16, ... of column c, and adds a column's 16 sums
-// in order, in FP64.  (Large ones gain nothing: 429 us either way at [8192, 5120] x [2560, 5120],
+// dx = dz w and dw = dz^T x of small sizes, both in whole 64-row tiles, in one launch: neither
+// fills the card alone, and each launch costs more than a stage or two of K.  dx's tiles
+// come first.  (Large ones gain nothing: 429 us either way at [8192, 5120] x [2560, 5120],
 // where the matrix cores' power is the bound and idle CUs leave the others more of it.)
 template <bool HALF>
-__global__ __launch_bounds__(256) void gemm_pair_kernel(GemmArgs dx, GemmArgs dw, SumJob sums) {
+__global__ __launch_bounds__(256) void gemm_pair_kernel(GemmArgs dx, GemmArgs dw) {
   __shared__ __align__(1024) uint16_t ring[kRing<64, 64>];
   const int mx = (dx.M + 63) / 64, nx = (dx.N + 63) / 64, mw = (dw.M + 63) / 64, nw = (dw.N + 63) / 64;
   const int b = blockIdx.x, first = mx * nx, both = first + mw * nw;
-  if (b < first) {
+  if (b < first)
     gemm_tile<HALF, false, true, 64, 64, 2, 2, false>(ring, dx, mx, nx, xcd_lin(b, first), dx.K, nullptr, 0);
-  } else if (b < both) {
+  else if (b < both)
     gemm_tile<HALF, true, true, 64, 64, 2, 2, false>(ring, dw, mw, nw, xcd_lin(b - first, mw * nw), dw.K, nullptr, 0);
-  } else {
-    float* s = reinterpret_cast<float*>(ring);
-    const int c = threadIdx.x & 15, h = (b - both) * 16 + c;
-    float v = 0.f;
-    if (h < sums.cols)
-#pragma unroll 16
-      for (int u = threadIdx.x >> 4; u < sums.units; u += 16) v += sums.part[(int64_t)u * sums.cols + h];
-    s[threadIdx.x] = v;
-    __syncthreads();
-    if (threadIdx.x < 16 && h < sums.cols) {
-      double a = 0.0;
-#pragma unroll
-      for (int g = 0; g < 16; ++g) a += s[16 * g + c];
-      sums.out[h] = (float)a;
-    }
-  }
+  else
+    sum_columns(reinterpret_cast<float*>(ring), dx.sums, b - both);
 }
 
 template <bool HALF>
-hipError_t launch_gemm_pair(const GemmArgs& dx, const GemmArgs& dw, const SumJob& sums, hipStream_t st) {
+hipError_t launch_gemm_pair(const GemmArgs& dx, const GemmArgs& dw, hipStream_t st) {
   auto tiles = [](const GemmArgs& g) { return ((g.M + 63) / 64) * ((g.N + 63) / 64); };
-  hipLaunchKernelGGL(gemm_pair_kernel<HALF>, dim3(tiles(dx) + tiles(dw) + (sums.out ? (sums.cols + 15) / 16 : 0)),
-                     dim3(256), 0, st, dx, dw, sums);
+  hipLaunchKernelGGL(gemm_pair_kernel<HALF>, dim3(tiles(dx) + tiles(dw) + sum_groups(dx.sums)), dim3(256), 0, st,
+                     dx, dw);
   return hipGetLastError();
 }
 
@@ -329,9 +335,10 @@ hipError_t launch_gemm_pair(const GemmArgs& dx, const GemmArgs& dw, const SumJob
 template <bool HALF>
 hipError_t launch_gemm_tiles(const GemmArgs& g, const GemmPlan& p, float* part, int64_t ldpart, hipStream_t st) {
   const int mt = (g.M + p.tile - 1) / p.tile, nt = (g.N + p.tile - 1) / p.tile;
-  const dim3 grid(mt * nt * p.splits);
+  const int total = mt * nt * p.splits;
+  const dim3 grid(total + sum_groups(g.sums));
   auto go = [&](auto kernel, int threads) {
-    hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, st, g, mt, nt, p.k_per_split, part, ldpart);
+    hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, st, g, mt, nt, total, p.k_per_split, part, ldpart);
     return hipGetLastError();
   };
   if (p.tile == 256) {

@@ -11,6 +11,13 @@ namespace beam {
 // Values of the ABI's activation argument (BEAM_MOE_ACT_*).
 enum Act { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3 };
 
+// out[h] = sum_u part[u][h]; out null: nothing to do.
+struct SumJob {
+  const float* part;
+  float* out;
+  int units, cols;
+};
+
 // out[m, n] = keep res[m, n] + add act(sum_k a(m, k) b(n, k) + bias[n]), pre[m, n] = the
 // activation's argument.  a(m, k) is at a + m * lda + k, or with at (A transposed) at
 // a + k * lda + m; b the same with n.  Types are ElemType; a, b and pre share one of two bytes.
@@ -31,6 +38,7 @@ struct GemmArgs {
   int64_t ldo;
   void* pre;  // null: not written
   int64_t ldp;
+  SumJob sums;  // runs beside a product of transposed b alone (dx)
 };
 
 // How a product runs: which kernel, and the workspace it needs (bytes from its start).
@@ -46,16 +54,9 @@ struct GemmPlan {
 // padded: both operands' rows are whole chunks of 8 elements (zeros past the end of K), whatever the sizes.
 GemmPlan plan_gemm(int M, int N, int K, bool at, bool bt, int64_t lda, int64_t ldb, bool padded = false);
 hipError_t launch_gemm(const GemmArgs& g, const GemmPlan& p, void* ws, hipStream_t st);
-// out[h] = sum_u part[u][h]; out null: nothing to do.
-struct SumJob {
-  const float* part;
-  float* out;
-  int units, cols;
-};
-// Both gradients' products and the column sums of dbias, one after the other or, where both products take
-// 64-row tiles whole, in one launch.
-hipError_t launch_gemm_pair(const GemmArgs& dx, const GemmPlan& px, const GemmArgs& dw, const GemmPlan& pw,
-                            const SumJob& sums, void* ws, hipStream_t st);
+// Both gradients' products, one after the other or, where both take 64-row tiles whole, in one launch.
+hipError_t launch_gemm_pair(const GemmArgs& dx, const GemmPlan& px, const GemmArgs& dw, const GemmPlan& pw, void* ws,
+                            hipStream_t st);
 hipError_t launch_column_sums(const float* part, float* out0, float* out1, int units, int H, hipStream_t st);
 
 // A matrix to be laid out anew: dst rows of up8(cols) elements, zeros past cols.
@@ -72,8 +73,8 @@ inline size_t padded_bytes(int rows, int cols) { return (size_t)rows * up8(cols)
 hipError_t launch_pad(const PadJob& first, const PadJob& second, hipStream_t st);
 hipError_t launch_gemm_bf16(const GemmArgs& g, const GemmPlan& p, float* part, int64_t ldpart, hipStream_t st);
 hipError_t launch_gemm_f16(const GemmArgs& g, const GemmPlan& p, float* part, int64_t ldpart, hipStream_t st);
-hipError_t launch_gemm_pair_bf16(const GemmArgs& dx, const GemmArgs& dw, const SumJob& sums, hipStream_t st);
-hipError_t launch_gemm_pair_f16(const GemmArgs& dx, const GemmArgs& dw, const SumJob& sums, hipStream_t st);
+hipError_t launch_gemm_pair_bf16(const GemmArgs& dx, const GemmArgs& dw, hipStream_t st);
+hipError_t launch_gemm_pair_f16(const GemmArgs& dx, const GemmArgs& dw, hipStream_t st);
 
 template <bool HALF>
 __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {

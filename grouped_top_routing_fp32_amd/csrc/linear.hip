@@ -298,15 +298,13 @@ hipError_t launch_gemm(const GemmArgs& args, const GemmPlan& p, void* ws, hipStr
   return hipGetLastError();
 }
 
-hipError_t launch_gemm_pair(const GemmArgs& dx, const GemmPlan& px, const GemmArgs& dw, const GemmPlan& pw,
-                            const SumJob& sums, void* ws, hipStream_t st) {
+hipError_t launch_gemm_pair(const GemmArgs& dx, const GemmPlan& px, const GemmArgs& dw, const GemmPlan& pw, void* ws,
+                            hipStream_t st) {
   auto whole = [](const GemmPlan& p) { return p.kind == GemmPlan::kTiles && p.tile == 64 && p.splits == 1; };
-  if (dx.M > 0 && whole(px) && whole(pw))
-    return dx.type == kElemF16 ? launch_gemm_pair_f16(dx, dw, sums, st) : launch_gemm_pair_bf16(dx, dw, sums, st);
-  hipError_t e = sums.out ? launch_column_sums(sums.part, sums.out, nullptr, sums.units, sums.cols, st) : hipSuccess;
-  if (e == hipSuccess && dx.M > 0) e = launch_gemm(dx, px, ws, st);
-  if (e != hipSuccess) return e;
-  return launch_gemm(dw, pw, ws, st);
+  if (whole(px) && whole(pw))
+    return dx.type == kElemF16 ? launch_gemm_pair_f16(dx, dw, st) : launch_gemm_pair_bf16(dx, dw, st);
+  const hipError_t e = launch_gemm(dx, px, ws, st);
+  return e != hipSuccess ? e : launch_gemm(dw, pw, ws, st);
 }
 
 // Rows of partial sums of dbias: a unit of linear_dz_kernel has 4 rows (one to each row of

@@ -290,13 +290,16 @@ int beam_moe_linear_backward(int32_t rows, int32_t cols, int32_t inner, int type
   gw.K = rows;
   gw.out = dw;
   gw.ldo = lddw;
-  const beam::SumJob sums{part, dbias, rows > 0 ? beam::linear_dz_units(rows) : 0, cols};
-  if (dx && dw) return hip_status(beam::launch_gemm_pair(gx, p.dx, gw, p.dw, sums, gemm_ws, st));
+  const int units = rows > 0 ? beam::linear_dz_units(rows) : 0;
+  if (dx && rows > 0) {
+    gx.sums = {part, dbias, units, cols};
+    return hip_status(dw ? beam::launch_gemm_pair(gx, p.dx, gw, p.dw, gemm_ws, st)
+                         : beam::launch_gemm(gx, p.dx, gemm_ws, st));
+  }
   if (dbias) {
-    rc = hip_status(beam::launch_column_sums(part, dbias, nullptr, sums.units, cols, st));
+    rc = hip_status(beam::launch_column_sums(part, dbias, nullptr, units, cols, st));
     if (rc != BEAM_MOE_OK) return rc;
   }
-  if (dx && rows > 0) return hip_status(beam::launch_gemm(gx, p.dx, gemm_ws, st));
   if (dw) return hip_status(beam::launch_gemm(gw, p.dw, gemm_ws, st));
   return BEAM_MOE_OK;
 }
