@@ -202,10 +202,12 @@ GemmPlan plan_gemm(int M, int N, int K, bool at, bool bt, int64_t lda, int64_t l
   // [8192, 2560] x [2560, 2560], 1.25 rounds and 2.5: 137 and 118; [8192, 1024] x [5120,
   // 1024], 2.5 and 5: 112 and 106, but 220 and 240 with K 2560).  128-row tiles split K until two workgroups a CU
   // have work, in at least 8 stages each; under 24 stages the join costs what a split
-  // gains.  64-row tiles where even split 128-row tiles would leave CUs without work ([1000,
-  // 1000] x [1000, 1000] forward and back 32 us, 41 in 128-row tiles; but [512, 5120] x
-  // [2560, 5120] 42 us, 28 in those), and for one or two stages, where the result's
-  // stores are most of the work ([3000, 128] x [3000, 128] 12.7 us against 15.7).
+  // gains.  64-row tiles where 128-row ones, split or not, make no more than a workgroup a CU
+  // ([2048, 1472] x [1024, 1472], 128 of those, 15.2 us against 21.4; [4096, 1024] x [1024,
+  // 1024], 256, 16.1 against 17.3; but [2048, 1024] x [2560, 1024], 320, 23.7 against 20.3,
+  // and [512, 5120] x [2560, 5120], 80 split nine times, 42 against 28), and for one or two
+  // stages, where the result's stores are most of the work ([3000, 128] x [3000, 128] 12.7
+  // us against 15.7).
   const int stages = ceil_div(K, kBK);
   const int t256 = ceil_div(M, 256) * ceil_div(N, 256), t128 = ceil_div(M, 128) * ceil_div(N, 128);
   auto fill = [](int64_t n, int round) { return (double)n / (double)((n + round - 1) / round * round); };
@@ -217,7 +219,7 @@ GemmPlan plan_gemm(int M, int N, int K, bool at, bool bt, int64_t lda, int64_t l
   };
   if (t128 > 1 << 20)  // so large a grid of smaller tiles would pass 2^32 threads
     p.tile = 256;
-  else if (stages <= 2 || (int64_t)t128 * (stages / 8 + 1) < kCUs)
+  else if (stages <= 2 || (int64_t)t128 * (stages >= 24 ? stages / 8 + 1 : 1) <= kCUs)
     p.tile = 64;
   else
     p.tile = fill(t256, kCUs) >= (stages <= 24 ? 0.85 : 0.8) * fill((int64_t)t128 * splits(t128), 2 * kCUs) ? 256 : 128;
