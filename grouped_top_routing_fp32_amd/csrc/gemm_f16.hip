@@ -3,12 +3,13 @@
 
 namespace beam {
 
-hipError_t launch_gemm_f16(const GemmArgs& g, const GemmPlan& p, float* part, int64_t ldpart, hipStream_t st) {
-  return launch_gemm_tiles<true>(g, p, part, ldpart, st);
+hipError_t launch_gemm_f16(const GemmArgs& g, const GemmSplit& s, int tile, hipStream_t st) {
+  return launch_gemm_tiles<true>(g, s, tile, st);
 }
 
-hipError_t launch_gemm_pair_f16(const GemmArgs& dx, const GemmArgs& dw, hipStream_t st) {
-  return launch_gemm_pair<true>(dx, dw, st);
+hipError_t launch_gemm_pair_f16(const GemmArgs& dx, const GemmSplit& sx, const GemmArgs& dw, const GemmSplit& sw,
+                                int tile, hipStream_t st) {
+  return tile == 128 ? launch_gemm_pair<true, 128>(dx, sx, dw, sw, st) : launch_gemm_pair<true, 64>(dx, sx, dw, sw, st);
 }
 
 }  // namespace beam

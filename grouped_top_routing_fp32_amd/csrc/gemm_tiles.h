@@ -306,47 +306,52 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(GemmArgs g, int mt, i
   gemm_tile<HALF, AT, BT, BM, BN, WM, WN, EPI>(ring, g, mt, nt, xcd_lin(blockIdx.x, total), k_per_split, part, ldpart);
 }
 
-// dx = dz w and dw = dz^T x of small sizes, both in whole 64-row tiles, in one launch: neither
-// fills the card alone, and each launch costs more than a stage or two of K.  dx's tiles
-// come first.  (Large ones gain nothing: 429 us either way at [8192, 5120] x [2560, 5120],
-// where the matrix cores' power is the bound and idle CUs leave the others more of it.)
-template <bool HALF>
-__global__ __launch_bounds__(256) void gemm_pair_kernel(GemmArgs dx, GemmArgs dw) {
-  __shared__ __align__(1024) uint16_t ring[kRing<64, 64>];
-  const int mx = (dx.M + 63) / 64, nx = (dx.N + 63) / 64, mw = (dw.M + 63) / 64, nw = (dw.N + 63) / 64;
-  const int b = blockIdx.x, first = mx * nx, both = first + mw * nw;
+// dx = dz w and dw = dz^T x in one launch, where neither fills the card alone.  dx's tiles
+// come first.  (In 256-row tiles nothing is gained: 429 us either way at [8192, 5120] x
+// [2560, 5120], where the matrix cores' power is the bound and idle CUs leave the others more
+// of it.)
+template <bool HALF, int TILE>
+__global__ __launch_bounds__(256) void gemm_pair_kernel(GemmArgs dx, GemmSplit sx, GemmArgs dw, GemmSplit sw) {
+  __shared__ __align__(1024) uint16_t ring[kRing<TILE, TILE>];
+  const int mx = (dx.M + TILE - 1) / TILE, nx = (dx.N + TILE - 1) / TILE;
+  const int mw = (dw.M + TILE - 1) / TILE, nw = (dw.N + TILE - 1) / TILE;
+  const int b = blockIdx.x, first = mx * nx * sx.splits, second = mw * nw * sw.splits;
   if (b < first)
-    gemm_tile<HALF, false, true, 64, 64, 2, 2, false>(ring, dx, mx, nx, xcd_lin(b, first), dx.K, nullptr, 0);
-  else if (b < both)
-    gemm_tile<HALF, true, true, 64, 64, 2, 2, false>(ring, dw, mw, nw, xcd_lin(b - first, mw * nw), dw.K, nullptr, 0);
+    gemm_tile<HALF, false, true, TILE, TILE, 2, 2, false>(ring, dx, mx, nx, xcd_lin(b, first), sx.k_per_split,
+                                                          sx.part, sx.ld);
+  else if (b < first + second)
+    gemm_tile<HALF, true, true, TILE, TILE, 2, 2, false>(ring, dw, mw, nw, xcd_lin(b - first, second),
+                                                         sw.k_per_split, sw.part, sw.ld);
   else
-    sum_columns(reinterpret_cast<float*>(ring), dx.sums, b - both);
+    sum_columns(reinterpret_cast<float*>(ring), dx.sums, b - first - second);
 }
 
-template <bool HALF>
-hipError_t launch_gemm_pair(const GemmArgs& dx, const GemmArgs& dw, hipStream_t st) {
-  auto tiles = [](const GemmArgs& g) { return ((g.M + 63) / 64) * ((g.N + 63) / 64); };
-  hipLaunchKernelGGL(gemm_pair_kernel<HALF>, dim3(tiles(dx) + tiles(dw) + sum_groups(dx.sums)), dim3(256), 0, st,
-                     dx, dw);
+template <bool HALF, int TILE>
+hipError_t launch_gemm_pair(const GemmArgs& dx, const GemmSplit& sx, const GemmArgs& dw, const GemmSplit& sw,
+                            hipStream_t st) {
+  auto tiles = [](const GemmArgs& g) { return ((g.M + TILE - 1) / TILE) * ((g.N + TILE - 1) / TILE); };
+  hipLaunchKernelGGL((gemm_pair_kernel<HALF, TILE>),
+                     dim3(tiles(dx) * sx.splits + tiles(dw) * sw.splits + sum_groups(dx.sums)), dim3(256), 0, st, dx,
+                     sx, dw, sw);
   return hipGetLastError();
 }
 
 // Launches the tiles of g's layout (A transposed implies B transposed).
 template <bool HALF>
-hipError_t launch_gemm_tiles(const GemmArgs& g, const GemmPlan& p, float* part, int64_t ldpart, hipStream_t st) {
-  const int mt = (g.M + p.tile - 1) / p.tile, nt = (g.N + p.tile - 1) / p.tile;
-  const int total = mt * nt * p.splits;
+hipError_t launch_gemm_tiles(const GemmArgs& g, const GemmSplit& s, int tile, hipStream_t st) {
+  const int mt = (g.M + tile - 1) / tile, nt = (g.N + tile - 1) / tile;
+  const int total = mt * nt * s.splits;
   const dim3 grid(total + sum_groups(g.sums));
   auto go = [&](auto kernel, int threads) {
-    hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, st, g, mt, nt, total, p.k_per_split, part, ldpart);
+    hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, st, g, mt, nt, total, s.k_per_split, s.part, s.ld);
     return hipGetLastError();
   };
-  if (p.tile == 256) {
+  if (tile == 256) {
     if (!g.at && !g.bt) return go(gemm_kernel<HALF, false, false, 256, 256, 4, 2, true>, 512);
     if (!g.at) return go(gemm_kernel<HALF, false, true, 256, 256, 4, 2, false>, 512);
     return go(gemm_kernel<HALF, true, true, 256, 256, 4, 2, false>, 512);
   }
-  if (p.tile == 128) {
+  if (tile == 128) {
     if (!g.at && !g.bt) return go(gemm_kernel<HALF, false, false, 128, 128, 2, 2, true>, 256);
     if (!g.at) return go(gemm_kernel<HALF, false, true, 128, 128, 2, 2, false>, 256);
     return go(gemm_kernel<HALF, true, true, 128, 128, 2, 2, false>, 256);

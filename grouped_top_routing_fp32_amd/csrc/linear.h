@@ -50,11 +50,19 @@ struct GemmPlan {
   bool copy_a, copy_b; // the operand is laid out anew in the workspace
   size_t off_a, off_b, off_part, total;
 };
+// Where the partial sums of a product's splits go: [splits][M][ld] (null: one split, the result itself).
+struct GemmSplit {
+  float* part;
+  int64_t ld;  // a multiple of four
+  int splits, k_per_split;
+};
 // Operand shapes and leading dimensions decide alone, so a size query and its call agree.
 // padded: both operands' rows are whole chunks of 8 elements (zeros past the end of K), whatever the sizes.
 GemmPlan plan_gemm(int M, int N, int K, bool at, bool bt, int64_t lda, int64_t ldb, bool padded = false);
 hipError_t launch_gemm(const GemmArgs& g, const GemmPlan& p, void* ws, hipStream_t st);
-// Both gradients' products, one after the other or, where both take 64-row tiles whole, in one launch.
+// Whether both gradients' products run in one launch; their workspaces then lie one behind the other (dx's first),
+// else in the same place.
+bool gemm_pairs(const GemmPlan& dx, const GemmPlan& dw);
 hipError_t launch_gemm_pair(const GemmArgs& dx, const GemmPlan& px, const GemmArgs& dw, const GemmPlan& pw, void* ws,
                             hipStream_t st);
 hipError_t launch_column_sums(const float* part, float* out0, float* out1, int units, int H, hipStream_t st);
@@ -71,10 +79,12 @@ inline int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
 inline bool regular_rows(int64_t ld, int cols) { return ld % 8 == 0 && cols % 8 == 0; }
 inline size_t padded_bytes(int rows, int cols) { return (size_t)rows * up8(cols) * 2; }
 hipError_t launch_pad(const PadJob& first, const PadJob& second, hipStream_t st);
-hipError_t launch_gemm_bf16(const GemmArgs& g, const GemmPlan& p, float* part, int64_t ldpart, hipStream_t st);
-hipError_t launch_gemm_f16(const GemmArgs& g, const GemmPlan& p, float* part, int64_t ldpart, hipStream_t st);
-hipError_t launch_gemm_pair_bf16(const GemmArgs& dx, const GemmArgs& dw, hipStream_t st);
-hipError_t launch_gemm_pair_f16(const GemmArgs& dx, const GemmArgs& dw, hipStream_t st);
+hipError_t launch_gemm_bf16(const GemmArgs& g, const GemmSplit& s, int tile, hipStream_t st);
+hipError_t launch_gemm_f16(const GemmArgs& g, const GemmSplit& s, int tile, hipStream_t st);
+hipError_t launch_gemm_pair_bf16(const GemmArgs& dx, const GemmSplit& sx, const GemmArgs& dw, const GemmSplit& sw,
+                                 int tile, hipStream_t st);
+hipError_t launch_gemm_pair_f16(const GemmArgs& dx, const GemmSplit& sx, const GemmArgs& dw, const GemmSplit& sw,
+                                int tile, hipStream_t st);
 
 template <bool HALF>
 __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {

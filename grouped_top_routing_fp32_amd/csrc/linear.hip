@@ -14,16 +14,23 @@
 
 namespace beam {
 
-// out from the partial sums of the splits, added in order: four columns to a thread.
-__global__ __launch_bounds__(256) void gemm_join_kernel(GemmArgs g, const float* __restrict__ part, int64_t ldpart,
-                                                        int splits) {
-  const int quads = (int)(ldpart / 4);
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+// out from the partial sums of the splits, added in order: four columns to a thread; of one
+// product or of two, the first with `blocks` workgroups.
+struct JoinJob {
+  GemmArgs g;
+  GemmSplit s;
+};
+__global__ __launch_bounds__(256) void gemm_join_kernel(JoinJob first, JoinJob second, int blocks) {
+  const bool other = (int)blockIdx.x >= blocks;
+  const GemmArgs& g = other ? second.g : first.g;
+  const GemmSplit& sp = other ? second.s : first.s;
+  const int quads = (int)(sp.ld / 4);
+  const int64_t i = (int64_t)(blockIdx.x - (other ? blocks : 0)) * 256 + threadIdx.x;
   if (i >= (int64_t)g.M * quads) return;
   const int m = (int)(i / quads), n = (int)(i % quads) * 4;
   f32x4 z = {0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < splits; ++s) {
-    const f32x4 v = *reinterpret_cast<const f32x4*>(part + ((int64_t)s * g.M + m) * ldpart + n);
+  for (int s = 0; s < sp.splits; ++s) {
+    const f32x4 v = *reinterpret_cast<const f32x4*>(sp.part + ((int64_t)s * g.M + m) * sp.ld + n);
 #pragma unroll
     for (int q = 0; q < 4; ++q) z[q] += v[q];
   }
@@ -256,6 +263,20 @@ hipError_t launch_skinny(const GemmArgs& g, hipStream_t st) {
 
 }  // namespace
 
+static GemmSplit split_of(const GemmArgs& g, const GemmPlan& p, char* base) {
+  return {p.splits > 1 ? reinterpret_cast<float*>(base + p.off_part) : nullptr, (g.N + 3) / 4 * 4, p.splits,
+          p.k_per_split};
+}
+
+// The results of those that were split.
+static hipError_t launch_join(const JoinJob& first, const JoinJob& second, hipStream_t st) {
+  auto blocks = [](const JoinJob& j) { return j.s.part ? (int)((j.g.M * (j.s.ld / 4) + 255) / 256) : 0; };
+  const int a = blocks(first), b = blocks(second);
+  if (a + b == 0) return hipSuccess;
+  hipLaunchKernelGGL(gemm_join_kernel, dim3(a + b), dim3(256), 0, st, first, second, a);
+  return hipGetLastError();
+}
+
 static PadJobs pad_jobs(const PadJob& first, const PadJob& second) {
   auto blocks = [](const PadJob& j) {
     const int64_t n = (j.rows * (up8(j.cols) / 8) + 255) / 256;
@@ -288,25 +309,25 @@ hipError_t launch_gemm(const GemmArgs& args, const GemmPlan& p, void* ws, hipStr
     g.ldb = up8(jb.cols);
   }
   if ((e = launch_pad(ja, jb, st)) != hipSuccess) return e;
-  const int64_t ldpart = (g.N + 3) / 4 * 4;
-  float* part = p.splits > 1 ? reinterpret_cast<float*>(base + p.off_part) : nullptr;
-  const bool half = g.type == kElemF16;
   if (p.kind == GemmPlan::kSkinny) return launch_skinny(g, st);
-  e = half ? launch_gemm_f16(g, p, part, ldpart, st) : launch_gemm_bf16(g, p, part, ldpart, st);
-  if (e != hipSuccess || !part) return e;
-  const int64_t quads = (int64_t)g.M * (ldpart / 4);
-  hipLaunchKernelGGL(gemm_join_kernel, dim3((uint32_t)((quads + 255) / 256)), dim3(256), 0, st, g, part, ldpart,
-                     p.splits);
-  return hipGetLastError();
+  const GemmSplit s = split_of(g, p, base);
+  e = g.type == kElemF16 ? launch_gemm_f16(g, s, p.tile, st) : launch_gemm_bf16(g, s, p.tile, st);
+  return e != hipSuccess ? e : launch_join({g, s}, {}, st);
 }
+
+bool gemm_pairs(const GemmPlan& dx, const GemmPlan& dw) { return dx.tile == dw.tile && dx.tile < 256; }
 
 hipError_t launch_gemm_pair(const GemmArgs& dx, const GemmPlan& px, const GemmArgs& dw, const GemmPlan& pw, void* ws,
                             hipStream_t st) {
-  auto whole = [](const GemmPlan& p) { return p.kind == GemmPlan::kTiles && p.tile == 64 && p.splits == 1; };
-  if (whole(px) && whole(pw))
-    return dx.type == kElemF16 ? launch_gemm_pair_f16(dx, dw, st) : launch_gemm_pair_bf16(dx, dw, st);
-  const hipError_t e = launch_gemm(dx, px, ws, st);
-  return e != hipSuccess ? e : launch_gemm(dw, pw, ws, st);
+  if (!gemm_pairs(px, pw)) {
+    const hipError_t e = launch_gemm(dx, px, ws, st);
+    return e != hipSuccess ? e : launch_gemm(dw, pw, ws, st);
+  }
+  char* base = static_cast<char*>(ws);
+  const GemmSplit sx = split_of(dx, px, base), sw = split_of(dw, pw, base + px.total);
+  const hipError_t e = dx.type == kElemF16 ? launch_gemm_pair_f16(dx, sx, dw, sw, px.tile, st)
+                                           : launch_gemm_pair_bf16(dx, sx, dw, sw, px.tile, st);
+  return e != hipSuccess ? e : launch_join({dx, sx}, {dw, sw}, st);
 }
 
 // Rows of partial sums of dbias: a unit of linear_dz_kernel has 4 rows (one to each row of

@@ -71,8 +71,8 @@ int check_linear(int32_t rows, int32_t cols, int32_t inner) {
 bool act_ok(int act) { return act >= BEAM_MOE_ACT_NONE && act <= BEAM_MOE_ACT_GELU; }
 
 // Workspace of the backward pass: dz, the partial sums of dbias, w and x where they are
-// laid out anew, then the partial sums of the two products, one after the other in the
-// same place.  Where dz is dy itself its place stays unused; the size does not depend on it.
+// laid out anew, then the partial sums of the two products, in the same place unless they
+// run in one launch.  Where dz is dy itself its place stays unused; the size does not depend on it.
 struct BackwardPlan {
   size_t off_dz, off_part, off_w, off_x, off_gemm, total;
   int64_t lddz;
@@ -93,7 +93,9 @@ BackwardPlan backward_plan(int32_t rows, int32_t cols, int32_t inner, int64_t ld
   p.off_w = p.off_part + align_up((size_t)beam::linear_dz_units(rows) * cols * sizeof(float));
   p.off_x = p.off_w + align_up(p.copy_w ? beam::padded_bytes(cols, inner) : 0);
   p.off_gemm = p.off_x + align_up(p.copy_x ? beam::padded_bytes(rows, inner) : 0);
-  p.total = p.off_gemm + (p.dx.total > p.dw.total ? p.dx.total : p.dw.total);
+  p.total = p.off_gemm + (beam::gemm_pairs(p.dx, p.dw)          ? p.dx.total + p.dw.total
+                          : p.dx.total > p.dw.total ? p.dx.total
+                                                    : p.dw.total);
   return p;
 }
 
