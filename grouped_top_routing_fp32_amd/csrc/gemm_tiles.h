@@ -306,8 +306,8 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(GemmArgs g, int mt, i
   gemm_tile<HALF, AT, BT, BM, BN, WM, WN, EPI>(ring, g, mt, nt, xcd_lin(blockIdx.x, total), k_per_split, part, ldpart);
 }
 
-// dx = dz w and dw = dz^T x in one launch, where neither fills the card alone.  dx's tiles
-// come first.  (In 256-row tiles nothing is gained: 429 us either way at [8192, 5120] x
+// dx = dz w and dw = dz^T x in one launch, where neither fills the card alone.  Those
+// with the longer K come first.  (In 256-row tiles nothing is gained: 429 us either way at [8192, 5120] x
 // [2560, 5120], where the matrix cores' power is the bound and idle CUs leave the others more
 // of it.)
 template <bool HALF, int TILE>
@@ -315,7 +315,9 @@ __global__ __launch_bounds__(256) void gemm_pair_kernel(GemmArgs dx, GemmSplit s
   __shared__ __align__(1024) uint16_t ring[kRing<TILE, TILE>];
   const int mx = (dx.M + TILE - 1) / TILE, nx = (dx.N + TILE - 1) / TILE;
   const int mw = (dw.M + TILE - 1) / TILE, nw = (dw.N + TILE - 1) / TILE;
-  const int b = blockIdx.x, first = mx * nx * sx.splits, second = mw * nw * sw.splits;
+  const int first = mx * nx * sx.splits, second = mw * nw * sw.splits;
+  int b = blockIdx.x;  // in the order dx, dw, sums
+  if (b < first + second && sw.k_per_split > sx.k_per_split) b = b < second ? b + first : b - second;
   if (b < first)
     gemm_tile<HALF, false, true, TILE, TILE, 2, 2, false>(ring, dx, mx, nx, xcd_lin(b, first), sx.k_per_split,
                                                           sx.part, sx.ld);

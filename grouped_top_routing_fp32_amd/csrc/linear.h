@@ -48,6 +48,7 @@ struct GemmPlan {
   int splits;          // of K; above 1 the partial sums go through the workspace
   int k_per_split;     // multiple of 64
   bool copy_a, copy_b; // the operand is laid out anew in the workspace
+  bool paired;         // runs with the other gradient's product
   size_t off_a, off_b, off_part, total;
 };
 // Where the partial sums of a product's splits go: [splits][M][ld] (null: one split, the result itself).
@@ -60,9 +61,10 @@ struct GemmSplit {
 // padded: both operands' rows are whole chunks of 8 elements (zeros past the end of K), whatever the sizes.
 GemmPlan plan_gemm(int M, int N, int K, bool at, bool bt, int64_t lda, int64_t ldb, bool padded = false);
 hipError_t launch_gemm(const GemmArgs& g, const GemmPlan& p, void* ws, hipStream_t st);
-// Whether both gradients' products run in one launch; their workspaces then lie one behind the other (dx's first),
-// else in the same place.
-bool gemm_pairs(const GemmPlan& dx, const GemmPlan& dw);
+// Both gradients' products, planned together.  Where they are paired (run in one launch) their workspaces lie one
+// behind the other, dx's first, else in the same place.
+void plan_gradients(int rows, int cols, int inner, int64_t lddz, int64_t ldw, int64_t ldx, GemmPlan* dx,
+                    GemmPlan* dw);
 hipError_t launch_gemm_pair(const GemmArgs& dx, const GemmPlan& px, const GemmArgs& dw, const GemmPlan& pw, void* ws,
                             hipStream_t st);
 hipError_t launch_column_sums(const float* part, float* out0, float* out1, int units, int H, hipStream_t st);

@@ -189,6 +189,23 @@ constexpr int kCUs = 256;
 constexpr int kSkinnyRows = 16;
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// Splits of a K of `stages` for `tiles` workgroups where `room` of them run at once.
+int splits_of(int tiles, int stages, int room) {
+  int s = tiles > 0 && stages >= 24 ? room / tiles : 1;
+  s = s < stages / 8 ? s : stages / 8;
+  s = s < 16 ? s : 16;
+  return s > 1 ? s : 1;
+}
+
+void split_plan(GemmPlan& p, int s, int K) {
+  p.splits = 1;
+  p.k_per_split = K > 0 ? ceil_div(K, kBK) * kBK : kBK;
+  if (s > 1) {
+    p.k_per_split = ceil_div(ceil_div(K, kBK), s) * kBK;
+    p.splits = ceil_div(K, p.k_per_split);
+  }
+}
 }  // namespace
 
 GemmPlan plan_gemm(int M, int N, int K, bool at, bool bt, int64_t lda, int64_t ldb, bool padded) {
@@ -218,12 +235,7 @@ GemmPlan plan_gemm(int M, int N, int K, bool at, bool bt, int64_t lda, int64_t l
   const int stages = ceil_div(K, kBK);
   const int t256 = ceil_div(M, 256) * ceil_div(N, 256), t128 = ceil_div(M, 128) * ceil_div(N, 128);
   auto fill = [](int64_t n, int round) { return (double)n / (double)((n + round - 1) / round * round); };
-  auto splits = [&](int tiles) {
-    int s = tiles > 0 && stages >= 24 ? 2 * kCUs / tiles : 1;
-    s = s < stages / 8 ? s : stages / 8;
-    s = s < 16 ? s : 16;
-    return s > 1 ? s : 1;
-  };
+  auto splits = [&](int tiles) { return splits_of(tiles, stages, 2 * kCUs); };
   if (t128 > 1 << 20)  // so large a grid of smaller tiles would pass 2^32 threads
     p.tile = 256;
   else if (stages <= 2 || (int64_t)t128 * (stages >= 24 ? stages / 8 + 1 : 1) <= kCUs)
@@ -231,11 +243,7 @@ GemmPlan plan_gemm(int M, int N, int K, bool at, bool bt, int64_t lda, int64_t l
   else
     p.tile = fill(t256, kCUs) >= (stages <= 24 ? 0.85 : 0.8) * fill((int64_t)t128 * splits(t128), 2 * kCUs) ? 256 : 128;
   if (p.tile < 256) {
-    const int s = splits(p.tile == 128 ? t128 : ceil_div(M, 64) * ceil_div(N, 64));
-    if (s > 1) {
-      p.k_per_split = ceil_div(stages, s) * kBK;
-      p.splits = ceil_div(K, p.k_per_split);
-    }
+    split_plan(p, splits(p.tile == 128 ? t128 : ceil_div(M, 64) * ceil_div(N, 64)), K);
   }
   size_t off = 0;
   p.off_a = off;
@@ -315,11 +323,73 @@ hipError_t launch_gemm(const GemmArgs& args, const GemmPlan& p, void* ws, hipStr
   return e != hipSuccess ? e : launch_join({g, s}, {}, st);
 }
 
-bool gemm_pairs(const GemmPlan& dx, const GemmPlan& dw) { return dx.tile == dw.tile && dx.tile < 256; }
+// Stages until n workgroups of `len` stages each and, started after them, m of l <= len are
+// done, where `room` run at once.
+static int64_t pair_stages(int64_t n, int64_t len, int64_t m, int64_t l) {
+  constexpr int64_t room = 2 * kCUs;
+  const int64_t rounds = n / room * len, late = n % room, soon = room - late;
+  if (late == 0) return rounds + (m + room - 1) / room * l;
+  // soon places take the m from the start on, the late ones from len on
+  int64_t a = len / l, b = 0, t = len;
+  if (m > soon * a + 8 * room) {  // whole rounds of both
+    b = (m - soon * a) / room - 4;
+    a += b;
+    t += b * l;
+  }
+  while (soon * a + late * b < m) {
+    const bool next_soon = (a + 1) * l <= len + (b + 1) * l;
+    t = next_soon ? ++a * l : len + ++b * l;
+  }
+  return rounds + t;
+}
+
+void plan_gradients(int rows, int cols, int inner, int64_t lddz, int64_t ldw, int64_t ldx, GemmPlan* dx,
+                    GemmPlan* dw) {
+  // dz rows are whole chunks with zeros past cols, and the other operands' are made so
+  *dx = plan_gemm(rows, inner, cols, false, true, lddz, ldw, true);
+  *dw = plan_gemm(cols, inner, rows, true, true, lddz, ldx, true);
+  if (dx->tile == 256 || dw->tile == 256 || rows == 0) return;
+  dx->paired = dw->paired = true;
+  if (dx->tile == 64 && dw->tile == 64) return;
+  auto tiles = [](int m, int n) { return ceil_div(m, 128) * ceil_div(n, 128); };
+  const int tx = tiles(rows, inner), tw = tiles(cols, inner);
+  const int lx = ceil_div(cols, kBK), lw = ceil_div(rows, kBK);
+  // 128-row tiles for both where either takes them, and of the splits of both those that end
+  // first: a stage is about a microsecond where two workgroups share a CU, a join some 3 and
+  // its partial sums' bytes.  Gradients of [1000, 2500] x [1700, 2500] 49.7 us one product
+  // after the other, 40.2 so; [7000, 640] x [900, 640] 43.8 and 40.7; [3600, 640] x [2560,
+  // 640] 46.1 and 37.4; none of 120 sizes lost more than its noise.
+  auto join = [&](int s, int m) { return s > 1 ? (double)s * m * inner * 8 / 4e6 : 0.; };
+  auto cost = [&](int sx, int sw) {
+    const int ax = ceil_div(lx, sx), aw = ceil_div(lw, sw);
+    const int64_t t = ax >= aw ? pair_stages((int64_t)tx * sx, ax, (int64_t)tw * sw, aw)
+                           : pair_stages((int64_t)tw * sw, aw, (int64_t)tx * sx, ax);
+    return t + join(sx, rows) + join(sw, cols) + (sx > 1 || sw > 1 ? 3. : 0.);
+  };
+  constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12};
+  int bx = 1, bw = 1;
+  double best = 1e30;
+  for (int sx : kSplits) {
+    if (sx > 1 && (lx < 24 || sx > lx / 8)) break;
+    for (int sw : kSplits) {
+      if (sw > 1 && (lw < 24 || sw > lw / 8)) break;
+      const double c = cost(sx, sw);
+      if (c < best) best = c, bx = sx, bw = sw;
+    }
+  }
+  dx->tile = dw->tile = 128;
+  split_plan(*dx, bx, cols);
+  split_plan(*dw, bw, rows);
+  auto bytes = [](const GemmPlan& p, int m, int n) {
+    return p.splits > 1 ? up256((size_t)p.splits * m * ((n + 3) / 4 * 4) * sizeof(float)) : 0;
+  };
+  dx->total = bytes(*dx, rows, inner);
+  dw->total = bytes(*dw, cols, inner);
+}
 
 hipError_t launch_gemm_pair(const GemmArgs& dx, const GemmPlan& px, const GemmArgs& dw, const GemmPlan& pw, void* ws,
                             hipStream_t st) {
-  if (!gemm_pairs(px, pw)) {
+  if (!px.paired) {
     const hipError_t e = launch_gemm(dx, px, ws, st);
     return e != hipSuccess ? e : launch_gemm(dw, pw, ws, st);
   }

@@ -85,15 +85,13 @@ BackwardPlan backward_plan(int32_t rows, int32_t cols, int32_t inner, int64_t ld
   p.lddz = beam::up8(cols);
   p.copy_w = !beam::regular_rows(ldw, inner);
   p.copy_x = !beam::regular_rows(ldx, inner);
-  // dz rows are whole chunks with zeros past cols, and the other operands' are made so
-  p.dx = beam::plan_gemm(rows, inner, cols, false, true, p.lddz, ldw, true);
-  p.dw = beam::plan_gemm(cols, inner, rows, true, true, p.lddz, ldx, true);
+  beam::plan_gradients(rows, cols, inner, p.lddz, ldw, ldx, &p.dx, &p.dw);
   p.off_dz = 0;
   p.off_part = align_up(beam::padded_bytes(rows, cols));
   p.off_w = p.off_part + align_up((size_t)beam::linear_dz_units(rows) * cols * sizeof(float));
   p.off_x = p.off_w + align_up(p.copy_w ? beam::padded_bytes(cols, inner) : 0);
   p.off_gemm = p.off_x + align_up(p.copy_x ? beam::padded_bytes(rows, inner) : 0);
-  p.total = p.off_gemm + (beam::gemm_pairs(p.dx, p.dw)          ? p.dx.total + p.dw.total
+  p.total = p.off_gemm + (p.dx.paired                   ? p.dx.total + p.dw.total
                           : p.dx.total > p.dw.total ? p.dx.total
                                                     : p.dw.total);
   return p;

@@ -658,6 +658,24 @@ def test_linear_backward(M, N, K, dt):
         _linear_back_check(dy, x, w, pre, act, 0.75, add, out)
 
 
+# products that run together: in 64-row tiles with K of one or both split, and in 128-row tiles with none, either
+# or both split, where dx's or dw's K is the longer
+@pytest.mark.parametrize("M,N,K", [(181, 1838, 1863), (2000, 1280, 128), (60, 2500, 2505), (1000, 300, 5000),
+                                   (500, 2560, 1400), (3600, 900, 640), (3600, 2560, 192), (1021, 1699, 1401)])
+@pytest.mark.parametrize("act,dt,pad", [("none", BF16, 0), ("gelu", F16, 5)])
+def test_linear_backward_together(M, N, K, act, dt, pad):
+    _say("linear_backward together", M, N, K, act, dt, pad)
+    g = _gen(M + N + K)
+    x, w = _randn(g, (M, K), dt, 1.0, pad), _randn(g, (N, K), dt, K ** -0.5, pad)
+    dy, pre = _randn(g, (M, N), dt, 1.0, pad), _randn(g, (M, N), dt, 1.5, pad)
+    dx, dw, db = fw.beam_moe_linear_backward(dy, x, w, pre, act=act)
+    _linear_back_check(dy, x, w, pre, act, 1.0, 1.0, (dx, dw, db, None))
+    again = fw.beam_moe_linear_backward(dy, x, w, pre, act=act)
+    assert all(torch.equal(p, q) for p, q in zip(again, (dx, dw, db)))
+    assert torch.equal(fw.beam_moe_linear_backward(dy, None, w, pre, act=act, want_dw=False)[0], dx)
+    assert torch.equal(fw.beam_moe_linear_backward(dy, x, None, pre, act=act, want_dx=False)[1], dw)
+
+
 def test_linear_backward_parts():
     _say("linear_backward parts")
     g = _gen(4)
