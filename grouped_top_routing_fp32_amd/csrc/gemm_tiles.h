@@ -73,6 +73,29 @@ struct Side {
     }
   }
 
+  // The same through registers, for rows of K that start at any element and may end inside a
+  // chunk (zeros follow).
+  __device__ __forceinline__ void load(u32x4* regs, int left, int wave, int lane) {
+    static_assert(!TR, "rows of K alone");
+#pragma unroll
+    for (int q = 0; q < kCopies; ++q) {
+      const int n = left < kBK ? left - 8 * chunk(row(q, wave, lane), lane) : 8;
+      if (n >= 8) {
+        regs[q] = *reinterpret_cast<const u32x4_any*>(src[q]);
+      } else {
+        Raw8<F16> part;  // the bits alone matter
+        part.load_part(src[q], n);
+        regs[q] = part.w[0];
+      }
+      src[q] += step;
+    }
+  }
+  static __device__ __forceinline__ void store(lds_u16* slot, const u32x4* regs, int wave, int lane) {
+#pragma unroll
+    for (int q = 0; q < kCopies; ++q)
+      *(__attribute__((address_space(3))) u32x4*)(slot + (wave * kCopies + q) * 512 + lane * 8) = regs[q];
+  }
+
   // The 16 rows from `r0` (a multiple of 16) of K 32 s .. 32 s + 31: lane l holds row
   // l % 16, K 8 (l / 16) .. + 7.
   static __device__ __forceinline__ u32x4 frag(const lds_u16* slot, int r0, int s, int lane) {
@@ -115,7 +138,7 @@ __device__ __forceinline__ int xcd_lin(int b, int total) {
 template <int BM, int BN>
 constexpr int kRing = 2 * (BM + BN) * kBK;
 
-template <bool HALF, bool AT, bool BT, int BM, int BN, int WM, int WN, bool EPI>
+template <bool HALF, bool AT, bool BT, int BM, int BN, int WM, int WN, bool EPI, bool REGS = false>
 __device__ __forceinline__ void gemm_tile(uint16_t* ring, GemmArgs g, int mt, int nt, int lin, int k_per_split,
                                           float* __restrict__ part, int64_t ldpart) {
   constexpr int NW = WM * WN, FI = BM / WM / 16, FJ = BN / WN / 16;
@@ -138,15 +161,40 @@ __device__ __forceinline__ void gemm_tile(uint16_t* ring, GemmArgs g, int mt, in
     sa.issue(lds + slot * kSlot, left, wave, lane);
     sb.issue(lds + slot * kSlot + BM * kBK, left, wave, lane);
   };
+  u32x4 ra[REGS ? Side<AT, BM, NW>::kCopies : 1], rb[REGS ? Side<BT, BN, NW>::kCopies : 1];
+  auto load = [&](int left) {
+    if constexpr (REGS) {
+      sa.load(ra, left, wave, lane);
+      sb.load(rb, left, wave, lane);
+    }
+  };
+  auto store = [&](int slot) {
+    if constexpr (REGS) {
+      Side<AT, BM, NW>::store(lds + slot * kSlot, ra, wave, lane);
+      Side<BT, BN, NW>::store(lds + slot * kSlot + BM * kBK, rb, wave, lane);
+    }
+  };
   const int stages = (k1 - k0 + kBK - 1) / kBK;  // 0 when K is 0
-  if (stages > 0) issue(0, k1 - k0);
+  if (stages > 0) {
+    if constexpr (REGS) {
+      load(k1 - k0);
+      store(0);
+    } else {
+      issue(0, k1 - k0);
+    }
+  }
   for (int st = 0; st < stages; ++st) {
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
-    __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_barrier();  // the stage is there for every wave, and all are done with the other slot
-    asm volatile("" ::: "memory");
-    if (st + 1 < stages) issue((st + 1) & 1, k1 - k0 - (st + 1) * kBK);
+    if constexpr (REGS) {
+      __syncthreads();
+      if (st + 1 < stages) load(k1 - k0 - (st + 1) * kBK);
+    } else {
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+      __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_barrier();  // the stage is there for every wave, and all are done with the other slot
+      asm volatile("" ::: "memory");
+      if (st + 1 < stages) issue((st + 1) & 1, k1 - k0 - (st + 1) * kBK);
+    }
     const lds_u16* A = lds + (st & 1) * kSlot;
     const lds_u16* B = A + BM * kBK;
     u32x4 fa[2][FI], fb[2][FJ];
@@ -163,6 +211,8 @@ __device__ __forceinline__ void gemm_tile(uint16_t* ring, GemmArgs g, int mt, in
       for (int i = 0; i < FI; ++i)
 #pragma unroll
         for (int j = 0; j < FJ; ++j) acc[i][j] = mfma<HALF>(fb[s][j], fa[s][i], acc[i][j]);
+    if constexpr (REGS)
+      if (st + 1 < stages) store((st + 1) & 1);
   }
 
   // Epilogue through LDS: FP32 sums in the ring (WM / kPasses wave rows at a time), then
@@ -297,13 +347,14 @@ __device__ __forceinline__ void sum_columns(float* s, const SumJob& j, int b) {
 }
 inline int sum_groups(const SumJob& j) { return j.out ? (j.cols + 15) / 16 : 0; }
 
-template <bool HALF, bool AT, bool BT, int BM, int BN, int WM, int WN, bool EPI>
+template <bool HALF, bool AT, bool BT, int BM, int BN, int WM, int WN, bool EPI, bool REGS = false>
 __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(GemmArgs g, int mt, int nt, int total, int k_per_split,
                                                             float* __restrict__ part, int64_t ldpart) {
   __shared__ __align__(1024) uint16_t ring[kRing<BM, BN>];
   if constexpr (BT && !AT)
     if ((int)blockIdx.x >= total) return sum_columns(reinterpret_cast<float*>(ring), g.sums, blockIdx.x - total);
-  gemm_tile<HALF, AT, BT, BM, BN, WM, WN, EPI>(ring, g, mt, nt, xcd_lin(blockIdx.x, total), k_per_split, part, ldpart);
+  gemm_tile<HALF, AT, BT, BM, BN, WM, WN, EPI, REGS>(ring, g, mt, nt, xcd_lin(blockIdx.x, total), k_per_split, part,
+                                                     ldpart);
 }
 
 // dx = dz w and dw = dz^T x in one launch, where neither fills the card alone.  Those
@@ -353,6 +404,9 @@ hipError_t launch_gemm_tiles(const GemmArgs& g, const GemmSplit& s, int tile, hi
     if (!g.at) return go(gemm_kernel<HALF, false, true, 256, 256, 4, 2, false>, 512);
     return go(gemm_kernel<HALF, true, true, 256, 256, 4, 2, false>, 512);
   }
+  if (g.regs)  // neither operand transposed
+    return tile == 128 ? go(gemm_kernel<HALF, false, false, 128, 128, 2, 2, true, true>, 256)
+                       : go(gemm_kernel<HALF, false, false, 64, 64, 2, 2, true, true>, 256);
   if (tile == 128) {
     if (!g.at && !g.bt) return go(gemm_kernel<HALF, false, false, 128, 128, 2, 2, true>, 256);
     if (!g.at) return go(gemm_kernel<HALF, false, true, 128, 128, 2, 2, false>, 256);

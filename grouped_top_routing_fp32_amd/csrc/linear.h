@@ -26,6 +26,7 @@ struct GemmArgs {
   const void* b;
   int64_t lda, ldb;
   bool at, bt;
+  bool regs;  // the operands, neither transposed, go through registers: rows start at any element
   int M, N, K;
   int type;
   const float* bias;  // null: none
@@ -48,6 +49,7 @@ struct GemmPlan {
   int splits;          // of K; above 1 the partial sums go through the workspace
   int k_per_split;     // multiple of 64
   bool copy_a, copy_b; // the operand is laid out anew in the workspace
+  bool regs;           // operands go through registers
   bool paired;         // runs with the other gradient's product
   size_t off_a, off_b, off_part, total;
 };

@@ -245,6 +245,18 @@ GemmPlan plan_gemm(int M, int N, int K, bool at, bool bt, int64_t lda, int64_t l
   if (p.tile < 256) {
     split_plan(p, splits(p.tile == 128 ? t128 : ceil_div(M, 64) * ceil_div(N, 64)), K);
   }
+  // Rows that are no whole chunks go through registers where that costs less than laying them
+  // out anew, a launch and their bytes twice: [500, 640] x [1000, 640] 8.0 us against 10.6,
+  // [8000, 1401] x [300, 1401], 625 x 22 stages of 64-row tiles, 26.3 against 30.9, but [4000,
+  // 1401] x [1000, 1401], 1008 x 22, 38.0 against 30.5, and [8000, 100] x [2500, 100], 5000 x
+  // 2, 30.8 against 24.1; [500, 5003] x [2500, 5003], 80 128-row
+  // tiles, 34.6 against 39.7, but [1000, 2560] x [2500, 2560], 160, 33.0 against 31.7.
+  const int64_t t64 = (int64_t)ceil_div(M, 64) * ceil_div(N, 64);
+  if ((p.copy_a || p.copy_b) &&
+      (p.tile == 64 ? t64 <= 4 * kCUs && t64 * stages <= 56 * kCUs : p.tile == 128 && t128 <= kCUs / 2)) {
+    p.copy_a = p.copy_b = false;
+    p.regs = true;
+  }
   size_t off = 0;
   p.off_a = off;
   if (p.copy_a) off = up256(off + padded_bytes(at ? K : M, at ? M : K));
@@ -318,6 +330,7 @@ hipError_t launch_gemm(const GemmArgs& args, const GemmPlan& p, void* ws, hipStr
   }
   if ((e = launch_pad(ja, jb, st)) != hipSuccess) return e;
   if (p.kind == GemmPlan::kSkinny) return launch_skinny(g, st);
+  g.regs = p.regs;
   const GemmSplit s = split_of(g, p, base);
   e = g.type == kElemF16 ? launch_gemm_f16(g, s, p.tile, st) : launch_gemm_bf16(g, s, p.tile, st);
   return e != hipSuccess ? e : launch_join({g, s}, {}, st);

@@ -310,7 +310,7 @@ int beam_moe_stream_rows(const beam_moe_dims* dims, int32_t T, int fp8);
  * in addition
  * - matrices are given with a row stride in elements (ld... >= the number of
  *   columns), so a matrix may be the first columns of a wider buffer; rows may
- *   start at any element (a product of more than 16 rows first lays out operands
+ *   start at any element (a larger product of more than 16 rows first lays out operands
  *   anew whose rows do not start on 16 bytes or hold whole groups of 8 elements);
  * - element types are given as BEAM_MOE_BF16, _F16 or _F32;
  * - every sum is held in FP32 or FP64 and every result is rounded once, to
@@ -403,7 +403,8 @@ int beam_moe_route_backward(const beam_moe_dims* dims, int32_t T, const float* s
 
 /* Workspace of beam_moe_linear and beam_moe_linear_backward; the leading
  * dimensions are those of the call (the operands whose rows do not start on 16
- * bytes or do not hold whole groups of 8 elements are laid out anew there).
+ * bytes or do not hold whole groups of 8 elements are laid out anew there, but
+ * for the smaller forward products).
  * Return SIZE_MAX for unsupported sizes. */
 size_t beam_moe_linear_workspace_bytes(int32_t rows, int32_t cols, int32_t inner, int64_t ldx, int64_t ldw);
 size_t beam_moe_linear_backward_workspace_bytes(int32_t rows, int32_t cols, int32_t inner, int64_t ldx, int64_t ldw);

@@ -572,6 +572,23 @@ def test_linear(M, N, K, dt):
         assert torch.equal(y, fw.beam_moe_linear(x, w, bias, act=act, residual=r, keep=keep, add=add, out_dtype=yt))
 
 
+# rows that are no whole chunks of 16 bytes: through registers in 64- and 128-row tiles, split or not, and laid out
+# anew where that costs less
+@pytest.mark.parametrize("M,N,K,pad", [(17, 33, 71, 2), (200, 300, 1409, 0), (130, 70, 2050, 1), (500, 2505, 2603, 0),
+                                       (513, 1001, 4100, 5), (4000, 1000, 1401, 0), (2100, 1030, 63, 1)])
+@pytest.mark.parametrize("dt", [BF16, F16])
+def test_linear_rows_off_16_bytes(M, N, K, pad, dt):
+    _say("linear rows off 16 bytes", M, N, K, pad, dt)
+    g = _gen(M + K)
+    x, w = _randn(g, (M, K), dt, 1.0, pad), _randn(g, (N, K), dt, K ** -0.5, pad)
+    bias, r = _randn(g, (N,)), _randn(g, (M, N), F32, 1.0, pad)
+    y, pre = fw.beam_moe_linear(x, w, bias, act="silu", residual=r, keep=0.5, add=2.0, out_dtype=F32, want_pre=True)
+    _linear_check(x, w, bias, "silu", r, 0.5, 2.0, y, pre)
+    # one operand's rows whole, the other's not
+    z = fw.beam_moe_linear(x[:, : K // 8 * 8].contiguous(), w[:, : K // 8 * 8])
+    _linear_check(x[:, : K // 8 * 8], w[:, : K // 8 * 8], None, "none", None, 1.0, 1.0, z)
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 40, 64), (5, 70, 65), (70, 70, 65), (300, 264, 128)])
 def test_linear_in_place_padding_and_nan(M, N, K):
     _say("linear in place", M, N, K)
