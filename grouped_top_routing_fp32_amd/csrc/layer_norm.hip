@@ -18,6 +18,11 @@ namespace beam {
 
 constexpr int kLnMaxThreads = 1024;
 constexpr int kLnMaxWaves = kLnMaxThreads / 64;
+// Up to here the backward pass is one launch: with 1021 rows of 2561 columns in bf16 10.6 us
+// on the GPU, 12.8 in two launches, with 256 rows of 5120 6.3 and 12.0, with 1500 rows of 5120
+// in fp32 22.8 and 20.9; the second launch takes the host 4 us besides.
+constexpr int kLnFewRows = 1024;
+constexpr int kLnFewCols = 32;  // of a workgroup that adds columns
 constexpr int kLnMaxJoin = 4096;  // columns of rows that share a workgroup with others
 static_assert(kLnMaxWaves == 16, "16 lanes join the waves' sums");
 
@@ -108,21 +113,21 @@ __global__ __launch_bounds__(kLnMaxThreads) void layer_norm_kernel(
   }
 }
 
-// Backward.  A workgroup of blockDim.y teams takes rows blockIdx.x * blockDim.y + team,
-// then those gridDim.x * blockDim.y further on; a thread's columns stay the same from
+// Backward.  A workgroup of blockDim.y teams takes rows block * blockDim.y + team,
+// then those blocks * blockDim.y further on; a thread's columns stay the same from
 // row to row, so it sums their dgamma and dbeta in registers.  At the end the teams add
-// up in LDS, in order, and the workgroup writes one row of part [2][gridDim.x][H], which
+// up in LDS, in order, and the workgroup writes one row of part [2][blocks][H], which
 // column_sums_kernel adds up: no atomics, so the sums' order is fixed.
-template <class DT, class XT, int NCH, bool TAIL>
-__global__ __launch_bounds__(kLnMaxThreads) void layer_norm_backward_kernel(
+template <class DT, class XT, int NCH, bool TAIL, bool SUMS>
+__device__ __forceinline__ void backward_rows(
     const typename DT::S* __restrict__ dy, int64_t lddy, const typename XT::S* __restrict__ x, int64_t ldx,
     const float* __restrict__ mean, const float* __restrict__ rstd, const float* __restrict__ gamma,
-    typename XT::S* __restrict__ dx, int64_t lddx, float* __restrict__ part, int T, int H) {
+    typename XT::S* __restrict__ dx, int64_t lddx, float* __restrict__ part, int T, int H, int block, int blocks) {
   __shared__ float red[2][kLnMaxWaves][2];
   __shared__ __align__(16) float joined[2][kLnMaxJoin];
   const int tid = threadIdx.x, team = blockDim.x, nw = team >> 6;
   const int wave0 = threadIdx.y * nw, wave = wave0 + (tid >> 6);
-  const int teams = blockDim.y, stride = gridDim.x * teams;
+  const int teams = blockDim.y, stride = blocks * teams;
   const int nch = (H + 7) / 8;
   // few columns to a thread: gamma stays in registers, and rows are requested one ahead
   constexpr bool kAhead = NCH == 1;
@@ -161,10 +166,10 @@ __global__ __launch_bounds__(kLnMaxThreads) void layer_norm_backward_kernel(
       }
     }
   };
-  if (kAhead) request(blockIdx.x * teams + threadIdx.y);
+  if (kAhead) request(block * teams + threadIdx.y);
   int buf = 0;
   // every team makes the same number of rounds; one past the end has no row in the last
-  for (int t0 = blockIdx.x * teams; t0 < T; t0 += stride, buf ^= 1) {
+  for (int t0 = block * teams; t0 < T; t0 += stride, buf ^= 1) {
     const int t = t0 + threadIdx.y;
     const bool live = t < T;
     float xh[NCH][8], gy[NCH][8];
@@ -180,8 +185,10 @@ __global__ __launch_bounds__(kLnMaxThreads) void layer_norm_backward_kernel(
           for (int q = 0; q < 8; ++q) {
             xh[c][q] = (xr[c][q] - mu) * r;
             gy[c][q] = yr[c][q];
-            dg[c][q] += gy[c][q] * xh[c][q];
-            db[c][q] += gy[c][q];
+            if constexpr (SUMS) {
+              dg[c][q] += gy[c][q] * xh[c][q];
+              db[c][q] += gy[c][q];
+            }
             gy[c][q] *= g[c][q];
             s1 += gy[c][q];
             s2 += gy[c][q] * xh[c][q];
@@ -216,9 +223,9 @@ __global__ __launch_bounds__(kLnMaxThreads) void layer_norm_backward_kernel(
       }
     }
   }
-  if (!part) return;
-  float* pg = part + (int64_t)blockIdx.x * H;
-  float* pb = part + ((int64_t)gridDim.x + blockIdx.x) * H;
+  if constexpr (!SUMS) return;
+  float* pg = part + (int64_t)block * H;
+  float* pb = part + ((int64_t)blocks + block) * H;
   for (int y = 0; y < teams; ++y) {
     if ((int)threadIdx.y == y) {
 #pragma unroll
@@ -246,6 +253,75 @@ __global__ __launch_bounds__(kLnMaxThreads) void layer_norm_backward_kernel(
       }
     }
     if (y + 1 < teams) __syncthreads();
+  }
+}
+
+template <class DT, class XT, int NCH, bool TAIL>
+__global__ __launch_bounds__(kLnMaxThreads) void layer_norm_backward_kernel(
+    const typename DT::S* __restrict__ dy, int64_t lddy, const typename XT::S* __restrict__ x, int64_t ldx,
+    const float* __restrict__ mean, const float* __restrict__ rstd, const float* __restrict__ gamma,
+    typename XT::S* __restrict__ dx, int64_t lddx, float* __restrict__ part, int T, int H) {
+  backward_rows<DT, XT, NCH, TAIL, true>(dy, lddy, x, ldx, mean, rstd, gamma, dx, lddx, part, T, H, blockIdx.x,
+                                         gridDim.x);
+}
+
+// Few rows: one launch without partial sums.  Workgroups [0, cgroups) own 32 columns each and
+// add all rows of them (xh needs the row's mean and rstd alone, so nothing waits for dx): thread
+// (c, g) takes chunk c of four in rows g, g + threads / 4, ...; a wave's 16 rows are joined by
+// shuffles, the waves in order, in FP64.  The others take dx's rows, of which x and dy come a
+// second time, from the caches.  Bound by what one CU takes from beyond its L2: 1021 rows of
+// 2561 fp32 12.5 us, with 64 columns a workgroup 15.0, with 16, which share lines, 13.9.
+template <class DT, class XT, int NCH, bool TAIL>
+__global__ __launch_bounds__(kLnMaxThreads) void layer_norm_backward_few_kernel(
+    const typename DT::S* __restrict__ dy, int64_t lddy, const typename XT::S* __restrict__ x, int64_t ldx,
+    const float* __restrict__ mean, const float* __restrict__ rstd, const float* __restrict__ gamma,
+    typename XT::S* __restrict__ dx, int64_t lddx, float* __restrict__ dgamma, float* __restrict__ dbeta, int T, int H,
+    int cgroups) {
+  if ((int)blockIdx.x >= cgroups)
+    return backward_rows<DT, XT, NCH, TAIL, false>(dy, lddy, x, ldx, mean, rstd, gamma, dx, lddx, nullptr, T, H,
+                                                   blockIdx.x - cgroups, gridDim.x - cgroups);
+  constexpr int kChunks = kLnFewCols / 8;
+  __shared__ float sums[kLnMaxWaves][2][kLnFewCols];
+  const int threads = blockDim.x * blockDim.y, tid = threadIdx.y * blockDim.x + threadIdx.x;
+  const int full = cgroups & ~7, b = blockIdx.x;  // neighbours share lines: on one XCD
+  const int h0 = kLnFewCols * (b >= full ? b : (b & 7) * (full >> 3) + (b >> 3));
+  const int h = h0 + 8 * (tid % kChunks), n = min(8, H - h);  // n <= 0: none
+  float dg[8] = {}, db[8] = {};
+  if (n > 0) {
+#pragma unroll 4
+    for (int t = tid / kChunks; t < T; t += threads / kChunks) {
+      float xv[8], yv[8];
+      load8<XT>(x + (int64_t)t * ldx + h, chunk_cols<TAIL>(H, h / 8), xv);
+      load8<DT>(dy + (int64_t)t * lddy + h, chunk_cols<TAIL>(H, h / 8), yv);
+      const float mu = mean[t], r = rstd[t];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        dg[q] += yv[q] * ((xv[q] - mu) * r);
+        db[q] += yv[q];
+      }
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+#pragma unroll
+    for (int off = kChunks; off < 64; off *= 2) {
+      dg[q] += __shfl_xor(dg[q], off);
+      db[q] += __shfl_xor(db[q], off);
+    }
+  if ((tid & 63) < kChunks) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      sums[tid >> 6][0][8 * (tid % kChunks) + q] = dg[q];
+      sums[tid >> 6][1][8 * (tid % kChunks) + q] = db[q];
+    }
+  }
+  __syncthreads();
+  const int c = tid % kLnFewCols;
+  float* out = tid / kLnFewCols ? dbeta : dgamma;
+  if (tid < 2 * kLnFewCols && h0 + c < H && out) {
+    double a = 0.0;
+    for (int w = 0; w < threads >> 6; ++w) a += sums[w][tid / kLnFewCols][c];
+    out[h0 + c] = (float)a;
   }
 }
 
@@ -341,7 +417,7 @@ hipError_t launch_layer_norm(const void* x, int x_type, int64_t ldx, const float
 // Teams of a backward workgroup, and workgroups (rows of partial column sums): as many
 // teams as 1024 threads hold, one workgroup to a CU.  More of either costs more in
 // partial sums than it gains: [8192, 5120] fp32 / bf16 80 us with 256 workgroups, 84
-// with 192, 86 with 512; [1021, 2561] fp16 12.6, 13.8 and 16.9 us.
+// with 192, 86 with 512.
 static int backward_teams(int H) { return H <= kLnMaxJoin ? kLnMaxThreads / shape(H).team : 1; }
 static int backward_groups(int T, int teams) {
   const int n = (T + teams - 1) / teams;
@@ -349,7 +425,7 @@ static int backward_groups(int T, int teams) {
 }
 
 // The most rows of partial sums of a call.
-int layer_norm_backward_units(int T) { return T < 256 ? T : 256; }
+int layer_norm_backward_units(int T) { return T <= kLnFewRows ? 0 : 256; }
 
 hipError_t launch_layer_norm_backward(const void* dy, int dy_type, int64_t lddy, const void* x, int x_type,
                                       int64_t ldx, const float* mean, const float* rstd, const float* gamma, void* dx,
@@ -358,6 +434,22 @@ hipError_t launch_layer_norm_backward(const void* dy, int dy_type, int64_t lddy,
   const Shape s = shape(H);
   const int teams = backward_teams(H), units = backward_groups(T, teams);
   const bool sums = dgamma || dbeta;
+  if (!sums || T <= kLnFewRows) {
+    const int cgroups = sums ? (H + kLnFewCols - 1) / kLnFewCols : 0, rgroups = dx ? (T + teams - 1) / teams : 0;
+    return by_type(dy_type, [&](auto dt) {
+      return by_type(x_type, [&](auto xt) {
+        return by_chunks(H, s.nch, [&](auto n, auto tail) {
+          using DT = decltype(dt);
+          using XT = decltype(xt);
+          hipLaunchKernelGGL((layer_norm_backward_few_kernel<DT, XT, decltype(n)::value, decltype(tail)::value>),
+                             dim3(cgroups + rgroups), dim3(s.team, teams), 0, st,
+                             static_cast<const typename DT::S*>(dy), lddy, static_cast<const typename XT::S*>(x), ldx,
+                             mean, rstd, gamma, static_cast<typename XT::S*>(dx), lddx, dgamma, dbeta, T, H, cgroups);
+          return hipGetLastError();
+        });
+      });
+    });
+  }
   hipError_t e = by_type(dy_type, [&](auto dt) {
     return by_type(x_type, [&](auto xt) {
       return by_chunks(H, s.nch, [&](auto n, auto tail) {

@@ -134,8 +134,8 @@ int beam_moe_layer_norm_backward(int32_t rows, int32_t cols, const void* dy, int
   if (rows == 0) return sums ? hip_status(beam::launch_column_sums(nullptr, dgamma, dbeta, 0, cols, st)) : BEAM_MOE_OK;
   if (!ld_ok(lddy, cols) || !ld_ok(ldx, cols) || (dx && !ld_ok(lddx, cols))) return BEAM_MOE_ERR_INVALID_ARG;
   if ((rc = check_ptrs({dy, x, mean, rstd})) != BEAM_MOE_OK) return rc;
-  if (sums && (!ws || !aligned16(ws) || ws_bytes < beam_moe_layer_norm_backward_workspace_bytes(rows, cols)))
-    return BEAM_MOE_ERR_WORKSPACE;
+  const size_t need = sums ? beam_moe_layer_norm_backward_workspace_bytes(rows, cols) : 0;
+  if (need && (!ws || !aligned16(ws) || ws_bytes < need)) return BEAM_MOE_ERR_WORKSPACE;
   return hip_status(beam::launch_layer_norm_backward(dy, dy_type, lddy, x, x_type, ldx, mean, rstd, gamma, dx, lddx,
                                                      dgamma, dbeta, static_cast<float*>(ws), rows, cols, st));
 }

@@ -340,8 +340,8 @@ int beam_moe_layer_norm(int32_t rows, int32_t cols, const void* x, int x_type, i
                         const float* beta, float eps, void* y, int y_type, int64_t ldy, float* mean, float* rstd,
                         void* stream);
 
-/* Workspace of beam_moe_layer_norm_backward (partial column sums, at most
- * 8 * 256 * cols bytes).  Returns SIZE_MAX for unsupported sizes. */
+/* Workspace of beam_moe_layer_norm_backward (partial column sums, 8 * 256 * cols
+ * bytes; 0 up to 1024 rows).  Returns SIZE_MAX for unsupported sizes. */
 size_t beam_moe_layer_norm_backward_workspace_bytes(int32_t rows, int32_t cols);
 
 /* Its gradients: with xh = (x - mean) * rstd and g = dy * gamma,
@@ -352,7 +352,7 @@ size_t beam_moe_layer_norm_backward_workspace_bytes(int32_t rows, int32_t cols);
  *   gamma       as there
  *   dx          [rows, cols] out, of x's type; NULL = not wanted
  *   dgamma, dbeta  [cols] fp32 out, either may be NULL; zeros when rows = 0
- *   ws          needed when dgamma or dbeta is wanted and rows > 0
+ *   ws          needed when dgamma or dbeta is wanted, of that size
  * At least one output must be wanted. */
 int beam_moe_layer_norm_backward(int32_t rows, int32_t cols, const void* dy, int dy_type, int64_t lddy, const void* x,
                                  int x_type, int64_t ldx, const float* mean, const float* rstd, const float* gamma,

@@ -185,7 +185,8 @@ def _norm_back_check(dy, x, mean, rstd, gamma, out):
     _near(db, rdb, depth * U * dy.double().abs().sum(0), "dbeta")
 
 
-@pytest.mark.parametrize("rows,cols", NORM_SHAPES + [(2100, 640), (1100, 5120)])
+@pytest.mark.parametrize("rows,cols", NORM_SHAPES + [
+    (2100, 640), (1100, 5120), (1024, 520), (1025, 129), (1600, 2561), (1540, 4097), (1100, 8200), (1538, 16383)])
 @pytest.mark.parametrize("xt,dt", [(F32, BF16), (BF16, BF16), (F16, F16), (BF16, F32), (F32, F32)])
 def test_layer_norm_backward(rows, cols, xt, dt):
     _say("layer_norm_backward", rows, cols, xt, dt)
@@ -208,8 +209,29 @@ def test_layer_norm_backward_parts_zero_rows_and_repeat():
     assert torch.equal(only[0], dx) and only[1] is None
     only = fw.beam_moe_layer_norm_backward(dy, x, mean, rstd, gamma, want_dx=False)
     assert only[0] is None and torch.equal(only[1], dg) and torch.equal(only[2], db)
+    x, dy = _randn(g, (1700, 264), BF16), _randn(g, (1700, 264), BF16)
+    _, mean, rstd = fw.beam_moe_layer_norm(x, gamma)
+    both = fw.beam_moe_layer_norm_backward(dy, x, mean, rstd, gamma)
+    only = fw.beam_moe_layer_norm_backward(dy, x, mean, rstd, gamma, want_params=False)
+    assert torch.equal(only[0], both[0])
+    only = fw.beam_moe_layer_norm_backward(dy, x, mean, rstd, gamma, want_dx=False)
+    assert torch.equal(only[1], both[1]) and torch.equal(only[2], both[2])
     dx, dg, db = fw.beam_moe_layer_norm_backward(dy[:0], x[:0], mean[:0], rstd[:0], gamma)
     assert dx.shape == (0, 264) and not dg.any() and not db.any()
+
+
+def test_layer_norm_backward_of_few_rows_past_32_bits():
+    _say("layer_norm_backward few rows far apart")
+    g = _gen(17)
+    T, H, ld = 1024, 100, 5 << 20
+    buf = torch.empty((T, ld), dtype=BF16, device=DEV)
+    x, dy = buf[:, :H], buf[:, 128: 128 + H]
+    x.copy_(torch.randn((T, H), generator=g, device=DEV))
+    dy.copy_(torch.randn((T, H), generator=g, device=DEV))
+    _, mean, rstd = fw.beam_moe_layer_norm(x)
+    a = fw.beam_moe_layer_norm_backward(dy, x, mean, rstd)
+    b = fw.beam_moe_layer_norm_backward(dy.contiguous(), x.contiguous(), mean, rstd)
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
 
 
 def test_layer_norm_gradient_against_differences():

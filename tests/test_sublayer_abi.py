@@ -28,7 +28,7 @@ class Call:
 
 NORM = Call("beam_moe_layer_norm", rows=4, cols=100, x=FAKE, x_type=BF16, ldx=100, gamma=FAKE, beta=FAKE, eps=1e-5,
             y=FAKE, y_type=BF16, ldy=100, mean=FAKE, rstd=FAKE, stream=None)
-NORM_BACK = Call("beam_moe_layer_norm_backward", rows=4, cols=100, dy=FAKE, dy_type=BF16, lddy=100, x=FAKE,
+NORM_BACK = Call("beam_moe_layer_norm_backward", rows=4000, cols=100, dy=FAKE, dy_type=BF16, lddy=100, x=FAKE,
                  x_type=F32, ldx=100, mean=FAKE, rstd=FAKE, gamma=FAKE, dx=FAKE, lddx=100, dgamma=FAKE, dbeta=FAKE,
                  ws=FAKE, ws_bytes=1 << 40, stream=None)
 BALANCE = Call("beam_moe_balance_loss", dims=ctypes.byref(binding._cdims(BEAM)), T=1024, scores=FAKE, ids=FAKE,
@@ -101,7 +101,7 @@ def test_unsupported_sizes(call, bad):
 
 
 @pytest.mark.parametrize("call, need", [
-    (NORM_BACK, lambda lib: lib.beam_moe_layer_norm_backward_workspace_bytes(4, 100)),
+    (NORM_BACK, lambda lib: lib.beam_moe_layer_norm_backward_workspace_bytes(4000, 100)),
     (BALANCE, lambda lib: lib.beam_moe_balance_loss_workspace_bytes(ctypes.byref(binding._cdims(BEAM)), 1024, 3)),
     (LINEAR_BACK, lambda lib: lib.beam_moe_linear_backward_workspace_bytes(4, 10, 12, 12, 12)),
 ], ids=lambda v: v.fn if isinstance(v, Call) else "")
@@ -118,6 +118,8 @@ def test_workspace_queries_refuse_what_the_calls_refuse():
     none = binding.SIZE_MAX
     assert lib.beam_moe_layer_norm_backward_workspace_bytes(4, 16385) == none
     assert lib.beam_moe_layer_norm_backward_workspace_bytes(-1, 16) == none
+    assert lib.beam_moe_layer_norm_backward_workspace_bytes(1024, 16) == 0
+    assert lib.beam_moe_layer_norm_backward_workspace_bytes(1025, 16) == 8 * 256 * 16
     beam = ctypes.byref(binding._cdims(BEAM))
     assert lib.beam_moe_balance_loss_workspace_bytes(beam, 8, 0) == none
     assert lib.beam_moe_balance_loss_workspace_bytes(beam, -1, 1) == none
