@@ -102,11 +102,36 @@ __device__ __forceinline__ float sigmoid_f32(float z) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * z));
 }
 
+// The normal distribution function at z, and e^(-z^2 / 2) with it.  At -|z| it is that
+// exponential times a polynomial in t = 1 / (1 + 0.35 |z|) (Hastings' form), fitted in 64 bits to
+// the scaled complementary error function on |z| <= 14.5, where the exponential vanishes:
+// relative error 3e-8 of the fit, 3.3e-7 at most in FP32, far below zero too, where 1 + erf(z / sqrt 2)
+// cancels; the exponent's rounding adds z^2 / 2 half steps.  Fewer instructions than erff and
+// expf: [8192, 1024] x [2560, 1024] with GELU 62 us, 68.5 with those, its gradients 135 and 144.
+__device__ __forceinline__ float normal_cdf(float z, float& e) {
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.35f, fabsf(z), 1.f));
+  e = __builtin_amdgcn_exp2f(-0.72134752044448170f * z * z);
+  float p = -0.029157998f;
+  p = fmaf(p, t, 0.14403148f);
+  p = fmaf(p, t, -0.255840153f);
+  p = fmaf(p, t, 0.159320995f);
+  p = fmaf(p, t, -0.0232132431f);
+  p = fmaf(p, t, 0.105552875f);
+  p = fmaf(p, t, 0.119821198f);
+  p = fmaf(p, t, 0.139863521f);
+  p = fmaf(p, t, 0.139621302f);
+  const float low = p * t * e;
+  return z > 0.f ? 1.f - low : low;
+}
+
 template <int ACT>
 __device__ __forceinline__ float act_f32(float z) {
   if constexpr (ACT == kActRelu) return z < 0.f ? 0.f : z;  // NaN stays NaN
   if constexpr (ACT == kActSilu) return z * sigmoid_f32(z);
-  if constexpr (ACT == kActGelu) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+  if constexpr (ACT == kActGelu) {
+    float e;
+    return z * normal_cdf(z, e);
+  }
   return z;
 }
 
@@ -118,8 +143,11 @@ __device__ __forceinline__ float act_slope_f32(float z) {
     const float s = sigmoid_f32(z);
     return s * (1.f + z * (1.f - s));
   }
-  if constexpr (ACT == kActGelu)
-    return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * 0.39894228040143268f * expf(-0.5f * z * z);
+  if constexpr (ACT == kActGelu) {
+    float e;
+    const float cdf = normal_cdf(z, e);
+    return fmaf(z * 0.39894228040143268f, e, cdf);
+  }
   return 1.f;
 }
 

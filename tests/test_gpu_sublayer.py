@@ -653,6 +653,18 @@ def test_activations_far_from_zero():
         _near(db, 3 * slope.double(), 3 * 8 * U * (slope.double().abs() + 1), act)
 
 
+def test_gelu_keeps_its_digits_below_zero():
+    """z times the normal distribution function, relative to itself: the fit and its evaluation 6 steps, the
+    reciprocal, the exponential and four products 10, the exponent z^2 / 2 three half steps of itself."""
+    _say("gelu below zero")
+    z = torch.linspace(-12.0, 12.0, 24001, device=DEV)
+    w = torch.zeros((z.numel(), 8), dtype=BF16, device=DEV)
+    y = fw.beam_moe_linear(torch.zeros((2, 8), dtype=BF16, device=DEV), w, z, act="gelu", out_dtype=F32)
+    d = z.double()
+    want = d * 0.5 * torch.erfc(-d * math.sqrt(0.5))
+    _near(y, want.expand(2, -1), (16 + 1.5 * d * d) * U * want.abs(), "gelu")
+
+
 def _slope(z, act):
     z = z.double().requires_grad_(True)
     return torch.autograd.grad(ACTS[act](z).sum(), z)[0]
