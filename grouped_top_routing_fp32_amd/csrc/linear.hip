@@ -361,17 +361,18 @@ void plan_gradients(int rows, int cols, int inner, int64_t lddz, int64_t ldw, in
   // dz rows are whole chunks with zeros past cols, and the other operands' are made so
   *dx = plan_gemm(rows, inner, cols, false, true, lddz, ldw, true);
   *dw = plan_gemm(cols, inner, rows, true, true, lddz, ldx, true);
-  if (dx->tile == 256 || dw->tile == 256 || rows == 0) return;
-  dx->paired = dw->paired = true;
-  if (dx->tile == 64 && dw->tile == 64) return;
+  if (rows == 0 || rows > 1 << 17 || cols > 1 << 17 || inner > 1 << 17) return;  // far from the tiles' limits
+  if (dx->tile == 64 && dw->tile == 64) {
+    dx->paired = dw->paired = true;
+    return;
+  }
   auto tiles = [](int m, int n) { return ceil_div(m, 128) * ceil_div(n, 128); };
   const int tx = tiles(rows, inner), tw = tiles(cols, inner);
   const int lx = ceil_div(cols, kBK), lw = ceil_div(rows, kBK);
-  // 128-row tiles for both where either takes them, and of the splits of both those that end
-  // first: a stage is about a microsecond where two workgroups share a CU, a join some 3 and
-  // its partial sums' bytes.  Gradients of [1000, 2500] x [1700, 2500] 49.7 us one product
-  // after the other, 40.2 so; [7000, 640] x [900, 640] 43.8 and 40.7; [3600, 640] x [2560,
-  // 640] 46.1 and 37.4; none of 120 sizes lost more than its noise.
+  // 128-row tiles for both, and of the splits of both those that end first: a stage is about a
+  // microsecond where two workgroups share a CU, a join some 3 and its partial sums' bytes.
+  // Gradients of [1000, 2500] x [1700, 2500] 49.7 us one product after the other, 40.2 so; [7000,
+  // 640] x [900, 640] 43.8 and 40.7; [3600, 640] x [2560, 640] 46.1 and 37.4.
   auto join = [&](int s, int m) { return s > 1 ? (double)s * m * inner * 8 / 4e6 : 0.; };
   auto cost = [&](int sx, int sw) {
     const int ax = ceil_div(lx, sx), aw = ceil_div(lw, sw);
@@ -390,6 +391,19 @@ void plan_gradients(int rows, int cols, int inner, int64_t lddz, int64_t ldw, in
       if (c < best) best = c, bx = sx, bw = sw;
     }
   }
+  // Where one takes 256-row tiles, which run one to a CU for 1.7 of a 128-row tile's stages (see
+  // plan_gemm), both stay as they are unless together they end first by this count: [2000,
+  // 2560] x [4000, 2560] 114.6 us by themselves, 89.3 together, [4096, 5120] x [5120, 5120] 474
+  // and 433 (0.94 of it), but [8192, 5120] x [2560, 5120] 433 and 449 (0.98).
+  if (dx->tile == 256 || dw->tile == 256) {
+    auto alone = [&](const GemmPlan& p, int m) {
+      const int64_t n = (int64_t)ceil_div(m, p.tile) * ceil_div(inner, p.tile) * p.splits;
+      const int64_t room = p.tile == 256 ? kCUs : p.tile == 128 ? 2 * kCUs : 8 * kCUs;
+      return (double)((n + room - 1) / room) * (p.k_per_split / kBK) * (p.tile == 256 ? 1.7 : 1.) + join(p.splits, m);
+    };
+    if (best > 0.97 * (alone(*dx, rows) + alone(*dw, cols) + 4.)) return;
+  }
+  dx->paired = dw->paired = true;
   dx->tile = dw->tile = 128;
   split_plan(*dx, bx, cols);
   split_plan(*dw, bw, rows);

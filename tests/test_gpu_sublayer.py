@@ -712,7 +712,8 @@ def test_linear_backward(M, N, K, dt):
 # products that run together: in 64-row tiles with K of one or both split, and in 128-row tiles with none, either
 # or both split, where dx's or dw's K is the longer
 @pytest.mark.parametrize("M,N,K", [(181, 1838, 1863), (2000, 1280, 128), (60, 2500, 2505), (1000, 300, 5000),
-                                   (500, 2560, 1400), (3600, 900, 640), (3600, 2560, 192), (1021, 1699, 1401)])
+                                   (500, 2560, 1400), (3600, 900, 640), (3600, 2560, 192), (1021, 1699, 1401),
+                                   (2000, 4000, 2560), (6001, 999, 1399)])
 @pytest.mark.parametrize("act,dt,pad", [("none", BF16, 0), ("gelu", F16, 5)])
 def test_linear_backward_together(M, N, K, act, dt, pad):
     _say("linear_backward together", M, N, K, act, dt, pad)
