@@ -51,7 +51,7 @@ struct GemmPlan {
   bool copy_a, copy_b; // the operand is laid out anew in the workspace
   bool regs;           // operands go through registers
   bool paired;         // runs with the other gradient's product
-  size_t off_a, off_b, off_part, total;
+  size_t off_b, off_part, total;  // the first operand lies at the start
 };
 // Where the partial sums of a product's splits go: [splits][M][ld] (null: one split, the result itself).
 struct GemmSplit {
@@ -60,13 +60,11 @@ struct GemmSplit {
   int splits, k_per_split;
 };
 // Operand shapes and leading dimensions decide alone, so a size query and its call agree.
-// padded: both operands' rows are whole chunks of 8 elements (zeros past the end of K), whatever the sizes.
-GemmPlan plan_gemm(int M, int N, int K, bool at, bool bt, int64_t lda, int64_t ldb, bool padded = false);
+GemmPlan plan_linear(int M, int N, int K, int64_t ldx, int64_t ldw);
 hipError_t launch_gemm(const GemmArgs& g, const GemmPlan& p, void* ws, hipStream_t st);
 // Both gradients' products, planned together.  Where they are paired (run in one launch) their workspaces lie one
 // behind the other, dx's first, else in the same place.
-void plan_gradients(int rows, int cols, int inner, int64_t lddz, int64_t ldw, int64_t ldx, GemmPlan* dx,
-                    GemmPlan* dw);
+void plan_gradients(int rows, int cols, int inner, GemmPlan* dx, GemmPlan* dw);
 hipError_t launch_gemm_pair(const GemmArgs& dx, const GemmPlan& px, const GemmArgs& dw, const GemmPlan& pw, void* ws,
                             hipStream_t st);
 hipError_t launch_column_sums(const float* part, float* out0, float* out1, int units, int H, hipStream_t st);

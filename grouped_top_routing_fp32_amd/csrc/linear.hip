@@ -206,27 +206,23 @@ void split_plan(GemmPlan& p, int s, int K) {
     p.splits = ceil_div(K, p.k_per_split);
   }
 }
-}  // namespace
 
-GemmPlan plan_gemm(int M, int N, int K, bool at, bool bt, int64_t lda, int64_t ldb, bool padded) {
+size_t split_bytes(const GemmPlan& p, int M, int N) {
+  return p.splits > 1 ? up256((size_t)p.splits * M * ((N + 3) / 4 * 4) * sizeof(float)) : 0;
+}
+
+// A product of operands whose rows are whole chunks on 16 bytes.
+GemmPlan plan_tiles(int M, int N, int K) {
   GemmPlan p{};
-  p.splits = 1;
-  p.k_per_split = K > 0 ? ceil_div(K, kBK) * kBK : kBK;
-  if (!at && !bt && M <= kSkinnyRows) {
-    p.kind = GemmPlan::kSkinny;
-    return p;
-  }
   p.kind = GemmPlan::kTiles;
-  p.copy_a = !padded && !regular_rows(lda, at ? M : K);
-  p.copy_b = !padded && !regular_rows(ldb, bt ? N : K);
   // The tile is chosen by how full the card's rounds are: a round is 256 workgroups of
   // 256-row tiles (one a CU) or 512 of 128-row ones (two, each filling the other's gaps),
   // and full rounds of the smaller reach 0.85 of the larger's rate up to 24 stages, then
   // 0.8 ([16384, 2560] x [5120, 2560], full rounds of both: 391 us, 465 in 128-row tiles;
   // [8192, 2560] x [2560, 2560], 1.25 rounds and 2.5: 137 and 118; [8192, 1024] x [5120,
-  // 1024], 2.5 and 5: 112 and 106, but 220 and 240 with K 2560).  128-row tiles split K until two workgroups a CU
-  // have work, in at least 8 stages each; under 24 stages the join costs what a split
-  // gains.  64-row tiles where 128-row ones, split or not, make no more than a workgroup a CU
+  // 1024], 2.5 and 5: 112 and 106, but 220 and 240 with K 2560).  128-row tiles split K until
+  // two workgroups a CU have work, in at least 8 stages each; under 24 stages the join costs
+  // what a split gains.  64-row tiles where 128-row ones, split or not, make no more than a workgroup a CU
   // ([2048, 1472] x [1024, 1472], 128 of those, 15.2 us against 21.4; [4096, 1024] x [1024,
   // 1024], 256, 16.1 against 17.3; but [2048, 1024] x [2560, 1024], 320, 23.7 against 20.3,
   // and [512, 5120] x [2560, 5120], 80 split nine times, 42 against 28), and for one or two
@@ -242,29 +238,33 @@ GemmPlan plan_gemm(int M, int N, int K, bool at, bool bt, int64_t lda, int64_t l
     p.tile = 64;
   else
     p.tile = fill(t256, kCUs) >= (stages <= 24 ? 0.85 : 0.8) * fill((int64_t)t128 * splits(t128), 2 * kCUs) ? 256 : 128;
-  if (p.tile < 256) {
-    split_plan(p, splits(p.tile == 128 ? t128 : ceil_div(M, 64) * ceil_div(N, 64)), K);
-  }
+  split_plan(p, p.tile == 256 ? 1 : splits(p.tile == 128 ? t128 : ceil_div(M, 64) * ceil_div(N, 64)), K);
+  p.total = split_bytes(p, M, N);
+  return p;
+}
+}  // namespace
+
+GemmPlan plan_linear(int M, int N, int K, int64_t ldx, int64_t ldw) {
+  if (M <= kSkinnyRows) return GemmPlan{};  // kSkinny
+  GemmPlan p = plan_tiles(M, N, K);
+  p.copy_a = !regular_rows(ldx, K);
+  p.copy_b = !regular_rows(ldw, K);
   // Rows that are no whole chunks go through registers where that costs less than laying them
   // out anew, a launch and their bytes twice: [500, 640] x [1000, 640] 8.0 us against 10.6,
   // [8000, 1401] x [300, 1401], 625 x 22 stages of 64-row tiles, 26.3 against 30.9, but [4000,
   // 1401] x [1000, 1401], 1008 x 22, 38.0 against 30.5, and [8000, 100] x [2500, 100], 5000 x
-  // 2, 30.8 against 24.1; [500, 5003] x [2500, 5003], 80 128-row
-  // tiles, 34.6 against 39.7, but [1000, 2560] x [2500, 2560], 160, 33.0 against 31.7.
-  const int64_t t64 = (int64_t)ceil_div(M, 64) * ceil_div(N, 64);
-  if ((p.copy_a || p.copy_b) &&
-      (p.tile == 64 ? t64 <= 4 * kCUs && t64 * stages <= 56 * kCUs : p.tile == 128 && t128 <= kCUs / 2)) {
+  // 2, 30.8 against 24.1; [500, 5003] x [2500, 5003], 80 128-row tiles, 34.6 against 39.7, but
+  // [1000, 2560] x [2500, 2560], 160, 33.0 against 31.7.
+  const int64_t tiles = (int64_t)ceil_div(M, p.tile) * ceil_div(N, p.tile);
+  const bool few = p.tile == 64 ? tiles <= 4 * kCUs && tiles * ceil_div(K, kBK) <= 56 * kCUs
+                                : p.tile == 128 && tiles <= kCUs / 2;
+  if (few && (p.copy_a || p.copy_b)) {
     p.copy_a = p.copy_b = false;
     p.regs = true;
   }
-  size_t off = 0;
-  p.off_a = off;
-  if (p.copy_a) off = up256(off + padded_bytes(at ? K : M, at ? M : K));
-  p.off_b = off;
-  if (p.copy_b) off = up256(off + padded_bytes(bt ? K : N, bt ? N : K));
-  p.off_part = off;
-  if (p.splits > 1) off = up256(off + (size_t)p.splits * M * ((N + 3) / 4 * 4) * sizeof(float));
-  p.total = off;
+  p.off_b = p.copy_a ? up256(padded_bytes(M, K)) : 0;
+  p.off_part = p.off_b + (p.copy_b ? up256(padded_bytes(N, K)) : 0);
+  p.total += p.off_part;
   return p;
 }
 
@@ -319,14 +319,14 @@ hipError_t launch_gemm(const GemmArgs& args, const GemmPlan& p, void* ws, hipStr
   hipError_t e;
   PadJob ja{}, jb{};
   if (p.copy_a) {
-    ja = {g.a, g.lda, g.at ? g.K : g.M, g.at ? g.M : g.K, base + p.off_a};
+    ja = {g.a, g.lda, g.M, g.K, base};
     g.a = ja.dst;
-    g.lda = up8(ja.cols);
+    g.lda = up8(g.K);
   }
   if (p.copy_b) {
-    jb = {g.b, g.ldb, g.bt ? g.K : g.N, g.bt ? g.N : g.K, base + p.off_b};
+    jb = {g.b, g.ldb, g.N, g.K, base + p.off_b};
     g.b = jb.dst;
-    g.ldb = up8(jb.cols);
+    g.ldb = up8(g.K);
   }
   if ((e = launch_pad(ja, jb, st)) != hipSuccess) return e;
   if (p.kind == GemmPlan::kSkinny) return launch_skinny(g, st);
@@ -356,11 +356,10 @@ static int64_t pair_stages(int64_t n, int64_t len, int64_t m, int64_t l) {
   return rounds + t;
 }
 
-void plan_gradients(int rows, int cols, int inner, int64_t lddz, int64_t ldw, int64_t ldx, GemmPlan* dx,
-                    GemmPlan* dw) {
+void plan_gradients(int rows, int cols, int inner, GemmPlan* dx, GemmPlan* dw) {
   // dz rows are whole chunks with zeros past cols, and the other operands' are made so
-  *dx = plan_gemm(rows, inner, cols, false, true, lddz, ldw, true);
-  *dw = plan_gemm(cols, inner, rows, true, true, lddz, ldx, true);
+  *dx = plan_tiles(rows, inner, cols);
+  *dw = plan_tiles(cols, inner, rows);
   if (rows == 0 || rows > 1 << 17 || cols > 1 << 17 || inner > 1 << 17) return;  // far from the tiles' limits
   if (dx->tile == 64 && dw->tile == 64) {
     dx->paired = dw->paired = true;
@@ -392,7 +391,7 @@ void plan_gradients(int rows, int cols, int inner, int64_t lddz, int64_t ldw, in
     }
   }
   // Where one takes 256-row tiles, which run one to a CU for 1.7 of a 128-row tile's stages (see
-  // plan_gemm), both stay as they are unless together they end first by this count: [2000,
+  // plan_tiles), both stay as they are unless together they end first by this count: [2000,
   // 2560] x [4000, 2560] 114.6 us by themselves, 89.3 together, [4096, 5120] x [5120, 5120] 474
   // and 433 (0.94 of it), but [8192, 5120] x [2560, 5120] 433 and 449 (0.98).
   if (dx->tile == 256 || dw->tile == 256) {
@@ -407,11 +406,8 @@ void plan_gradients(int rows, int cols, int inner, int64_t lddz, int64_t ldw, in
   dx->tile = dw->tile = 128;
   split_plan(*dx, bx, cols);
   split_plan(*dw, bw, rows);
-  auto bytes = [](const GemmPlan& p, int m, int n) {
-    return p.splits > 1 ? up256((size_t)p.splits * m * ((n + 3) / 4 * 4) * sizeof(float)) : 0;
-  };
-  dx->total = bytes(*dx, rows, inner);
-  dw->total = bytes(*dw, cols, inner);
+  dx->total = split_bytes(*dx, rows, inner);
+  dw->total = split_bytes(*dw, cols, inner);
 }
 
 hipError_t launch_gemm_pair(const GemmArgs& dx, const GemmPlan& px, const GemmArgs& dw, const GemmPlan& pw, void* ws,

@@ -85,7 +85,7 @@ BackwardPlan backward_plan(int32_t rows, int32_t cols, int32_t inner, int64_t ld
   p.lddz = beam::up8(cols);
   p.copy_w = !beam::regular_rows(ldw, inner);
   p.copy_x = !beam::regular_rows(ldx, inner);
-  beam::plan_gradients(rows, cols, inner, p.lddz, ldw, ldx, &p.dx, &p.dw);
+  beam::plan_gradients(rows, cols, inner, &p.dx, &p.dw);
   p.off_dz = 0;
   p.off_part = align_up(beam::padded_bytes(rows, cols));
   p.off_w = p.off_part + align_up((size_t)beam::linear_dz_units(rows) * cols * sizeof(float));
@@ -178,7 +178,7 @@ int beam_moe_route_backward(const beam_moe_dims* d, int32_t T, const float* scor
 
 size_t beam_moe_linear_workspace_bytes(int32_t rows, int32_t cols, int32_t inner, int64_t ldx, int64_t ldw) {
   if (check_linear(rows, cols, inner) != BEAM_MOE_OK || !ld_ok(ldx, inner) || !ld_ok(ldw, inner)) return SIZE_MAX;
-  return beam::plan_gemm(rows, cols, inner, false, false, ldx, ldw).total;
+  return beam::plan_linear(rows, cols, inner, ldx, ldw).total;
 }
 
 int beam_moe_linear(int32_t rows, int32_t cols, int32_t inner, int type, const void* x, int64_t ldx, const void* w,
@@ -196,7 +196,7 @@ int beam_moe_linear(int32_t rows, int32_t cols, int32_t inner, int type, const v
     return BEAM_MOE_ERR_INVALID_ARG;
   if ((rc = check_ptrs({x, w, y})) != BEAM_MOE_OK) return rc;
   if ((rc = check_optional({bias, res, pre})) != BEAM_MOE_OK) return rc;
-  const beam::GemmPlan plan = beam::plan_gemm(rows, cols, inner, false, false, ldx, ldw);
+  const beam::GemmPlan plan = beam::plan_linear(rows, cols, inner, ldx, ldw);
   if (plan.total && (!ws || !aligned16(ws) || ws_bytes < plan.total)) return BEAM_MOE_ERR_WORKSPACE;
   beam::GemmArgs g{};
   g.a = x;
