@@ -344,10 +344,11 @@ __device__ __forceinline__ void gemm_tile(uint16_t* ring, GemmArgs g, int mt, in
       rows_of([&](int m, f32x4 v) { *reinterpret_cast<f32x4*>(p + (int64_t)m * ldpart) = v; });
     } else if constexpr (EPI) {
       by_act(g.act, [&](auto act) {
-        for (int r = qr; r < rmax; r += kRowsAtOnce) epilogue4<decltype(act)::value>(g, mp + r, n, g.N, sum_at(r));
+        for (int r = qr; r < rmax; r += kRowsAtOnce) epilogue4<decltype(act)::value>(g, g.add, mp + r, n, g.N, sum_at(r));
       });
     } else {
-      rows_of([&](int m, f32x4 v) { epilogue4<kActNone>(g, m, n, g.N, v); });
+      const float add = add_of(g);
+      rows_of([&](int m, f32x4 v) { gradient4(g, add, m, n, v); });
     }
   }
 }

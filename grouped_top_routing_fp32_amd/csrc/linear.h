@@ -34,6 +34,7 @@ struct GemmArgs {
   const void* res;  // out's type; null: none
   int64_t ldr;
   float keep, add;
+  const float* add_at;  // a gradient's add, on the device; null: add
   void* out;
   int out_type;
   int64_t ldo;
@@ -197,19 +198,22 @@ __device__ __forceinline__ void store_elem4(void* p, int64_t i, int type, f32x4 
   *reinterpret_cast<u32x2_any*>(static_cast<uint16_t*>(p) + i) = u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
 }
 
+// A product's `add`; read once, before its results.
+__device__ __forceinline__ float add_of(const GemmArgs& g) { return g.add_at ? *g.add_at : g.add; }
+
 // One element of the result from its sum over k.
 template <int ACT>
-__device__ __forceinline__ void epilogue1(const GemmArgs& g, int m, int n, float z) {
+__device__ __forceinline__ void epilogue1(const GemmArgs& g, float add, int m, int n, float z) {
   if (g.bias) z += g.bias[n];
   if (g.pre) store_elem(g.pre, (int64_t)m * g.ldp + n, g.type, z);
-  float v = g.add * act_f32<ACT>(z);
+  float v = add * act_f32<ACT>(z);
   if (g.res) v += g.keep * load_elem(g.res, (int64_t)m * g.ldr + n, g.out_type);
   store_elem(g.out, (int64_t)m * g.ldo + n, g.out_type, v);
 }
 
 // Columns n .. n + 3 of row m, those from `end` on left alone.
 template <int ACT>
-__device__ __forceinline__ void epilogue4(const GemmArgs& g, int m, int n, int end, f32x4 z) {
+__device__ __forceinline__ void epilogue4(const GemmArgs& g, float add, int m, int n, int end, f32x4 z) {
   if (n + 4 <= end) {
     if (g.bias) {
       const f32x4 b = *reinterpret_cast<const f32x4_any*>(g.bias + n);
@@ -219,7 +223,7 @@ __device__ __forceinline__ void epilogue4(const GemmArgs& g, int m, int n, int e
     if (g.pre) store_elem4(g.pre, (int64_t)m * g.ldp + n, g.type, z);
     f32x4 v;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) v[q] = g.add * act_f32<ACT>(z[q]);
+    for (int q = 0; q < 4; ++q) v[q] = add * act_f32<ACT>(z[q]);
     if (g.res) {
       const f32x4 r = load_elem4(g.res, (int64_t)m * g.ldr + n, g.out_type);
 #pragma unroll
@@ -229,7 +233,21 @@ __device__ __forceinline__ void epilogue4(const GemmArgs& g, int m, int n, int e
   } else {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      if (n + q < end) epilogue1<ACT>(g, m, n + q, z[q]);
+      if (n + q < end) epilogue1<ACT>(g, add, m, n + q, z[q]);
+  }
+}
+
+// The same of a gradient, which has the sums alone.
+__device__ __forceinline__ void gradient4(const GemmArgs& g, float add, int m, int n, f32x4 z) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) z[q] *= add;
+  const int64_t i = (int64_t)m * g.ldo + n;
+  if (n + 4 <= g.N) {
+    store_elem4(g.out, i, g.type, z);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (n + q < g.N) store_elem(g.out, i + q, g.type, z[q]);
   }
 }
 

@@ -24,6 +24,7 @@ __global__ __launch_bounds__(256) void gemm_join_kernel(JoinJob first, JoinJob s
   const bool other = (int)blockIdx.x >= blocks;
   const GemmArgs& g = other ? second.g : first.g;
   const GemmSplit& sp = other ? second.s : first.s;
+  const float add = add_of(g);  // requested before the sums, which hide it
   const int quads = (int)(sp.ld / 4);
   const int64_t i = (int64_t)(blockIdx.x - (other ? blocks : 0)) * 256 + threadIdx.x;
   if (i >= (int64_t)g.M * quads) return;
@@ -34,7 +35,7 @@ __global__ __launch_bounds__(256) void gemm_join_kernel(JoinJob first, JoinJob s
 #pragma unroll
     for (int q = 0; q < 4; ++q) z[q] += v[q];
   }
-  by_act(g.act, [&](auto act) { epilogue4<decltype(act)::value>(g, m, n, g.N, z); });
+  by_act(g.act, [&](auto act) { epilogue4<decltype(act)::value>(g, add, m, n, g.N, z); });
 }
 
 // Few rows (M <= 16, both operands K contiguous): bound by reading w once, and one CU
@@ -95,7 +96,7 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void gemm_skinny_kernel(GemmArgs
   }
   const int n = n0 + 4 * gr;
   if (l16 >= g.M || n >= n1) return;
-  by_act(g.act, [&](auto act) { epilogue4<decltype(act)::value>(g, l16, n, n1, z); });
+  by_act(g.act, [&](auto act) { epilogue4<decltype(act)::value>(g, g.add, l16, n, n1, z); });
 }
 
 // Lays one or two operands out anew, the first with `blocks` workgroups of 256 threads and the
@@ -125,8 +126,65 @@ __device__ __forceinline__ void pad_rows(const PadJobs& p, int b, int tid) {
 
 __global__ __launch_bounds__(256) void pad_rows_kernel(PadJobs p) { pad_rows(p, blockIdx.x, threadIdx.x); }
 
+// peaks[g] = the bits of the largest finite |dy| in a workgroup's part, for the scale of an fp16
+// dz.  grid ceil(N / 512) * units, block (64, 4), over the rows as in linear_dz_kernel, and behind
+// them the workgroups that lay operands out anew, so that those do not wait for it.
+constexpr int kMaxPeaks = 1024;
+template <class DT>
+__global__ __launch_bounds__(256) void linear_peak_kernel(const typename DT::S* __restrict__ dy, int64_t lddy,
+                                                          uint32_t* __restrict__ peaks, int M, int N, int units,
+                                                          int rows, PadJobs pad) {
+  __shared__ uint32_t top[4];
+  const int wide = (N + 511) / 512, bx = blockIdx.x % wide, unit = blockIdx.x / wide, y = threadIdx.y;
+  if (unit >= units) return pad_rows(pad, blockIdx.x - wide * units, y * 64 + threadIdx.x);
+  const int n = (bx * 64 + threadIdx.x) * 8, cols = min(8, N - n);  // <= 0: none
+  const int m1 = min(M, (unit + 1) * rows);
+  uint32_t best = 0;
+  if (cols > 0) {
+#pragma unroll 4
+    for (int m = unit * rows + y; m < m1; m += 4) {
+      float d[8];
+      load8<DT>(dy + (int64_t)m * lddy + n, cols, d);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const uint32_t b = __float_as_uint(d[q]) & 0x7fffffffu;
+        best = b < 0x7f800000u && b > best ? b : best;
+      }
+    }
+  }
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) best = max(best, (uint32_t)__shfl_xor((int)best, off));
+  if (threadIdx.x == 0) top[y] = best;
+  __syncthreads();
+  if (threadIdx.x == 0 && y == 0) peaks[blockIdx.x] = max(max(top[0], top[1]), max(top[2], top[3]));
+}
+
+// The power of two that takes a bound of the finite |dz|, 1.13 |add| max |dy| (no activation's
+// slope is larger), into [2^14, 2^15).  Between 2^-126 and 2^126, so that its reciprocal is as
+// exact; past those no result fits fp16.  By a whole workgroup of 256.
+__device__ __forceinline__ float dz_scale(const uint32_t* __restrict__ peaks, int count, float add) {
+  __shared__ uint32_t top[4];
+  const int tid = threadIdx.y * 64 + threadIdx.x;
+  uint32_t best = 0;
+#pragma unroll
+  for (int i = 0; i < kMaxPeaks; i += 256)
+    if (i + tid < count) best = max(best, peaks[i + tid]);
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) best = max(best, (uint32_t)__shfl_xor((int)best, off));
+  if (threadIdx.x == 0) top[threadIdx.y] = best;
+  __syncthreads();
+  best = max(max(top[0], top[1]), max(top[2], top[3]));
+  const double bound = 1.13 * fabs((double)add) * __uint_as_float(best);  // inside FP64's range
+  if (bound == 0.0) return 1.f;
+  const int e = (int)(__builtin_bit_cast(uint64_t, bound) >> 52) - 1022;  // bound < 2^e
+  return __uint_as_float((uint32_t)(min(max(15 - e, -126), 126) + 127) << 23);
+}
+
 // dz[m, n] = add dy act'(z), rounded to the products' 16-bit type (the rounding that a
-// gradient kept between two layers has anyway); part[u][n] = the unit's sum of the
+// gradient kept between two layers has anyway).  A gradient may well lie below fp16's range or
+// above: there dz is held times dz_scale's power of two, whose reciprocal goes to *unscale and
+// into the products' results, so that an element is off by half a step, or by 2^-39 of the
+// bound, whatever their size.  part[u][n] = the unit's sum of the unscaled,
 // unrounded dz; dres = keep dy.  grid ceil(N / 512) * units, block (64, 4): thread (c, r)
 // takes 8 columns in rows r, r + 4, ... of the unit.  Behind them the workgroups that lay the
 // products' other operands out anew, which would leave most of the card idle in a launch of
@@ -136,8 +194,9 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(PadJobs p) { pad_rows(p, 
 template <class DT, class T>
 __global__ __launch_bounds__(256) void linear_dz_kernel(const typename DT::S* __restrict__ dy, int64_t lddy,
                                                         const typename T::S* __restrict__ z, int64_t ldz, int act,
-                                                        float keep, float add, typename T::S* __restrict__ dz,
-                                                        int64_t lddz, float* __restrict__ part,
+                                                        float keep, float add, const uint32_t* __restrict__ peaks,
+                                                        int peak_count, float* __restrict__ unscale,
+                                                        typename T::S* __restrict__ dz, int64_t lddz, float* __restrict__ part,
                                                         typename DT::S* __restrict__ dres, int64_t lddres, int M, int N,
                                                         int units, int rows, PadJobs pad) {
   __shared__ float sums[4][64][8];
@@ -146,6 +205,13 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(const typename DT::S* __
   const int n = (bx * 64 + threadIdx.x) * 8, y = threadIdx.y;
   const int cols = min(8, N - n);  // <= 0: none
   const int m1 = min(M, (unit + 1) * rows);
+  [[maybe_unused]] float up = 1.f;
+  if constexpr (std::is_same_v<T, F16>) {
+    if (dz) {
+      up = dz_scale(peaks, peak_count, add);
+      if (blockIdx.x == 0 && threadIdx.x == 0 && y == 0) *unscale = 1.f / up;
+    }
+  }
   float s[8] = {};
   if (cols > 0) {
     by_act(act, [&](auto a) {
@@ -162,6 +228,10 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(const typename DT::S* __
           d[q] *= keep;
         }
         if (dres) store8<DT>(dres + (int64_t)m * lddres + n, cols, d);
+        if constexpr (std::is_same_v<T, F16>) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) v[q] *= up;
+        }
         if (dz) store8<T>(dz + (int64_t)m * lddz + n, 8, v);
       }
     });
@@ -423,23 +493,40 @@ hipError_t launch_gemm_pair(const GemmArgs& dx, const GemmPlan& px, const GemmAr
   return e != hipSuccess ? e : launch_join({dx, sx}, {dw, sw}, st);
 }
 
+size_t linear_peak_bytes() { return kMaxPeaks * sizeof(uint32_t); }
+
 // Rows of partial sums of dbias: a unit of linear_dz_kernel has 4 rows (one to each row of
 // its threads) until there are 256 units.  At 16 rows GELU's arithmetic alone took 10 us
 // of [517, 1003].
 int linear_dz_units(int M) { return M < 8 ? 1 : M / 4 < 256 ? M / 4 : 256; }
 
 hipError_t launch_linear_dz(const void* dy, int dy_type, int64_t lddy, const void* z, int64_t ldz, int act, float keep,
-                            float add, uint16_t* dz, int64_t lddz, int type, float* part, void* dres, int64_t lddres,
-                            int M, int N, const PadJob& first, const PadJob& second, hipStream_t st) {
-  const int units = linear_dz_units(M), rows = ceil_div(M, units);
-  const PadJobs pad = pad_jobs(first, second);
+                            float add, uint32_t* peaks, float* unscale, uint16_t* dz, int64_t lddz, int type,
+                            float* part, void* dres, int64_t lddres, int M, int N, const PadJob& first,
+                            const PadJob& second, hipStream_t st) {
+  const int units = linear_dz_units(M), rows = ceil_div(M, units), wide = ceil_div(N, 512);
+  PadJobs pad = pad_jobs(first, second);
+  int peak_count = 0;
+  if (dz && type == kElemF16) {
+    const int few = units * wide <= kMaxPeaks ? units : kMaxPeaks / wide;  // wide <= 512
+    peak_count = few * wide;
+    auto peak = [&](auto dt) {
+      using DT = decltype(dt);
+      hipLaunchKernelGGL((linear_peak_kernel<DT>), dim3(peak_count + pad.total), dim3(64, 4), 0, st,
+                         static_cast<const typename DT::S*>(dy), lddy, peaks, M, N, few, ceil_div(M, few), pad);
+    };
+    dy_type == kElemF32 ? peak(F32{}) : peak(F16{});
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    pad = PadJobs{};
+  }
   auto go = [&](auto dt, auto t) {
     using DT = decltype(dt);
     using T = decltype(t);
-    hipLaunchKernelGGL((linear_dz_kernel<DT, T>), dim3(ceil_div(N, 512) * units + pad.total), dim3(64, 4), 0, st,
+    hipLaunchKernelGGL((linear_dz_kernel<DT, T>), dim3(wide * units + pad.total), dim3(64, 4), 0, st,
                        static_cast<const typename DT::S*>(dy), lddy, static_cast<const typename T::S*>(z), ldz, act,
-                       keep, add, dz, lddz, part, static_cast<typename DT::S*>(dres), lddres, M, N, units, rows,
-                       pad);
+                       keep, add, peaks, peak_count, unscale, dz, lddz, part, static_cast<typename DT::S*>(dres),
+                       lddres, M, N, units, rows, pad);
   };
   if (type == kElemF16)
     dy_type == kElemF32 ? go(F32{}, F16{}) : go(F16{}, F16{});

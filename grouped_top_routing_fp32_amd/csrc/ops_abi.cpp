@@ -25,9 +25,11 @@ hipError_t launch_route_backward(const float* scores, const int32_t* ids, const 
                                  const int32_t* off, float alpha, const float* dloss, const int32_t* counts,
                                  float* dlogits, int T, int E, int K, hipStream_t st);
 int linear_dz_units(int M);
+size_t linear_peak_bytes();
 hipError_t launch_linear_dz(const void* dy, int dy_type, int64_t lddy, const void* z, int64_t ldz, int act, float keep,
-                            float add, uint16_t* dz, int64_t lddz, int type, float* part, void* dres, int64_t lddres,
-                            int M, int N, const PadJob& first, const PadJob& second, hipStream_t st);
+                            float add, uint32_t* peaks, float* unscale, uint16_t* dz, int64_t lddz, int type,
+                            float* part, void* dres, int64_t lddres, int M, int N, const PadJob& first,
+                            const PadJob& second, hipStream_t st);
 }  // namespace beam
 
 namespace {
@@ -70,15 +72,17 @@ int check_linear(int32_t rows, int32_t cols, int32_t inner) {
 
 bool act_ok(int act) { return act >= BEAM_MOE_ACT_NONE && act <= BEAM_MOE_ACT_GELU; }
 
-// Workspace of the backward pass: dz, the partial sums of dbias, w and x where they are
-// laid out anew, then the partial sums of the two products, in the same place unless they
+// Workspace of the backward pass: dz, the partial sums of dbias, the inverse of an fp16 dz's
+// scale with the maxima that give it, w and x where they are laid out anew, then the partial sums of the two products, in the same place unless they
 // run in one launch.  Where dz is dy itself its place stays unused; the size does not depend on it.
 struct BackwardPlan {
-  size_t off_dz, off_part, off_w, off_x, off_gemm, total;
+  size_t off_dz, off_part, off_scale, off_w, off_x, off_gemm, total;
   int64_t lddz;
   bool copy_w, copy_x;
   beam::GemmPlan dx, dw;
 };
+
+constexpr size_t kScaleBytes = 256;  // before the maxima
 
 BackwardPlan backward_plan(int32_t rows, int32_t cols, int32_t inner, int64_t ldx, int64_t ldw) {
   BackwardPlan p;
@@ -88,7 +92,8 @@ BackwardPlan backward_plan(int32_t rows, int32_t cols, int32_t inner, int64_t ld
   beam::plan_gradients(rows, cols, inner, &p.dx, &p.dw);
   p.off_dz = 0;
   p.off_part = align_up(beam::padded_bytes(rows, cols));
-  p.off_w = p.off_part + align_up((size_t)beam::linear_dz_units(rows) * cols * sizeof(float));
+  p.off_scale = p.off_part + align_up((size_t)beam::linear_dz_units(rows) * cols * sizeof(float));
+  p.off_w = p.off_scale + kScaleBytes + align_up(beam::linear_peak_bytes());
   p.off_x = p.off_w + align_up(p.copy_w ? beam::padded_bytes(cols, inner) : 0);
   p.off_gemm = p.off_x + align_up(p.copy_x ? beam::padded_bytes(rows, inner) : 0);
   p.total = p.off_gemm + (p.dx.paired                   ? p.dx.total + p.dw.total
@@ -264,14 +269,17 @@ int beam_moe_linear_backward(int32_t rows, int32_t cols, int32_t inner, int type
     x = jx.dst;
     ldx = beam::up8(inner);
   }
+  float* unscale = dz && type == BEAM_MOE_F16 && rows > 0 ? at<float>(ws, p.off_scale) : nullptr;
   rc = hip_status(rows > 0 && (dz || part || dres)
-                      ? beam::launch_linear_dz(dy, dy_type, lddy, pre, ldpre, act, keep, add, dz, p.lddz, type, part,
-                                               dres, lddres, rows, cols, jw, jx, st)
+                      ? beam::launch_linear_dz(dy, dy_type, lddy, pre, ldpre, act, keep, add,
+                                               at<uint32_t>(ws, p.off_scale + kScaleBytes), unscale, dz, p.lddz, type,
+                                               part, dres, lddres, rows, cols, jw, jx, st)
                       : beam::launch_pad(jw, jx, st));
   if (rc != BEAM_MOE_OK) return rc;
   beam::GemmArgs gx{}, gw{};
   gx.type = gx.out_type = gw.type = gw.out_type = type;
   gx.add = gw.add = 1.f;
+  gx.add_at = gw.add_at = unscale;
   gx.a = gw.a = same ? dy : dz;
   gx.lda = gw.lda = same ? lddy : p.lddz;
   gx.b = w;

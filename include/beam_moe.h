@@ -437,8 +437,12 @@ int beam_moe_linear(int32_t rows, int32_t cols, int32_t inner, int type, const v
  *   dx     [rows, inner] of `type`, dw [cols, inner] of `type`, dbias [cols] fp32,
  *          dres [rows, cols] of dy_type: each NULL = not wanted, one at least wanted;
  *          x is needed for dw and w for dx (else NULL)
- * dz enters the two products rounded to `type` (dbias sums it unrounded), so in fp16
- * a dz past 65504 becomes an infinity there.  When rows = 0, dw and dbias are zeros. */
+ * dz enters the two products rounded to `type`: half a step of each element, 2^-8 of it in
+ * bf16 and 2^-11 in fp16 (dbias sums it unrounded; where dz is dy itself, act none, add 1 and
+ * dy of `type`, nothing is rounded).  In fp16 dz is held times a power of two taken from
+ * the largest finite |dy|, which the results are divided by, so that gradients of any size go
+ * through: what lies 2^28 times and more below 1.13 |add| max |dy| is rounded to 2^-39 of that.
+ * When rows = 0, dw and dbias are zeros. */
 int beam_moe_linear_backward(int32_t rows, int32_t cols, int32_t inner, int type, const void* dy, int dy_type,
                              int64_t lddy, const void* x, int64_t ldx, const void* w, int64_t ldw, const void* pre,
                              int64_t ldpre, int act, float keep, float add, void* dx, int64_t lddx, void* dw,

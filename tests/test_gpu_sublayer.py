@@ -728,6 +728,115 @@ def test_linear_backward_together(M, N, K, act, dt, pad):
     assert torch.equal(fw.beam_moe_linear_backward(dy, x, None, pre, act=act, want_dx=False)[1], dw)
 
 
+def _dz_check(dy, x, w, pre, act, add, out):
+    """fp16: dz is scaled by the power of two that takes b = 1.13 |add| max |dy| (no slope is larger) into [2^14, 2^15),
+    and rounded: half a step of each term, or 2^-25 of fp16's least subnormal, which is at most 2^-39 b."""
+    d = add * dy.double()
+    if act != "none":
+        d = d * _slope(pre, act)
+    a = d.abs()
+    ez = (_step(x) + 16 * U) * a + 2.0 ** -39 * 1.13 * abs(add) * float(dy.double().abs().max())
+    if act != "none":
+        ez = ez + 8 * U * abs(add) * dy.double().abs()  # slopes near zero are differences of order 1
+    dx, dw, db = out
+    M, N = dy.shape
+    if dx is not None:
+        _near(dx, d @ w.double(), (_depth(N) * GEMM_UP * a + ez) @ w.double().abs(), "dx")
+    if dw is not None:
+        _near(dw, d.t() @ x.double(), (_depth(M) * GEMM_UP * a + ez).t() @ x.double().abs(), "dw")
+    if db is not None:
+        depth = math.ceil(M / 64) + 64 + 24
+        _near(db, d.sum(0), (depth * U * a + 16 * U * a + 8 * U * dy.double().abs() * abs(add)).sum(0), "dbias")
+
+
+# both products together in 64- and 128-row tiles, split or not, and in 256-row tiles by themselves
+RANGE_SHAPES = [(1, 9, 16), (33, 100, 136), (517, 1003, 777), (60, 2500, 2505), (1000, 300, 5000), (2000, 4000, 2560),
+                (3300, 3336, 136), (8192, 136, 264)]
+
+
+@pytest.mark.parametrize("M,N,K", RANGE_SHAPES)
+@pytest.mark.parametrize("size,add,weights", [(1e-6, 1.0, 2.0 ** 10), (1e-7, 1.0, 2.0 ** 11), (2e-8, 0.577, 2.0 ** 11),
+                                              (1e-12, 1e5, 2.0 ** 11), (1e-30, 1.5e23, 2.0 ** 11), (1e6, 1.0, 2.0 ** -14)])
+def test_linear_backward_keeps_small_and_large_gradients_in_fp16(M, N, K, size, add, weights):
+    """FP32 gradients that fp16 cannot hold, or only as subnormals, with weights and inputs for which the results can
+    be held: dx, dw and dbias of one call agree with 64 bits alike."""
+    _say("linear_backward range", M, N, K, size, add)
+    g = _gen(M + N + K)
+    x, w = _randn(g, (M, K), F16, weights, 5), _randn(g, (N, K), F16, weights)
+    dy, pre = _randn(g, (M, N), F32, size, 3), _randn(g, (M, N), F16, 1.5)
+    for act in ("none", "gelu"):
+        p = pre if act != "none" else None
+        dx, dw, db = fw.beam_moe_linear_backward(dy, x, w, p, act=act, add=add)
+        _dz_check(dy, x, w, p, act, add, (dx, dw, db))
+        assert torch.equal(fw.beam_moe_linear_backward(dy, None, w, p, act=act, add=add, want_dw=False)[0], dx)
+        assert torch.equal(fw.beam_moe_linear_backward(dy, x, None, p, act=act, add=add, want_dx=False)[1], dw)
+
+
+@pytest.mark.parametrize("M,N,K", [(517, 1003, 777), (8192, 136, 264)])
+def test_linear_backward_of_small_fp16_gradients(M, N, K):
+    """fp16 dy near its least subnormal: dz = add dy act' lies below it and still counts."""
+    _say("linear_backward small fp16", M, N, K)
+    g = _gen(M)
+    x, w = _randn(g, (M, K), F16, 2.0 ** 11), _randn(g, (N, K), F16, 2.0 ** 11)
+    dy, pre = _randn(g, (M, N), F16, 2.0 ** -21), _randn(g, (M, N), F16, 1.5)
+    assert (dy != 0).any()
+    for act, add in (("silu", 0.1), ("relu", 0.3), ("none", 0.01)):
+        p = pre if act != "none" else None
+        _dz_check(dy, x, w, p, act, add, fw.beam_moe_linear_backward(dy, x, w, p, act=act, add=add))
+
+
+def test_linear_backward_gradients_far_apart_in_fp16():
+    """One gradient far above the others; infinities and NaN, which touch their own row and column alone and have no
+    part in the scale; gradients and factors of zero."""
+    _say("linear_backward far apart")
+    g = _gen(21)
+    M, N, K = 300, 264, 136
+    x, w = _randn(g, (M, K), F16, 16.0), _randn(g, (N, K), F16, 16.0)
+    dy = _randn(g, (M, N), F32, 1e-4)
+    dy[7, 9] = 50.0
+    _dz_check(dy, x, w, None, "none", 1.0, fw.beam_moe_linear_backward(dy, x, w))
+    dy[5] = 0.0
+    clean = fw.beam_moe_linear_backward(dy, x, w)
+    for bad in (float("inf"), float("-inf"), float("nan")):
+        d = dy.clone()
+        d[5, 3] = bad
+        dx, dw, db = fw.beam_moe_linear_backward(d, x, w)
+        rows, cols = torch.arange(M, device=DEV) != 5, torch.arange(N, device=DEV) != 3
+        assert torch.equal(dx[rows], clean[0][rows]) and not dx[5].isfinite().any()
+        assert torch.equal(dw[cols], clean[1][cols]) and not dw[3].isfinite().any()
+        assert torch.equal(db[cols], clean[2][cols]) and not db[3].isfinite()
+    for d, add in ((torch.zeros_like(dy), 1.0), (dy, 0.0)):
+        assert all(not t.any() for t in fw.beam_moe_linear_backward(d, x, w, add=add))
+
+
+def test_linear_backward_scale_of_replayed_gradients():
+    """The scale is the replayed call's own: gradients of other sizes in the captured buffers, and two graphs in turn."""
+    _say("linear_backward replayed scale")
+    g = _gen(22)
+    M, N, K = 517, 264, 136
+    x, w, pre = _randn(g, (M, K), F16, 256.0), _randn(g, (N, K), F16, 256.0), _randn(g, (M, N), F16, 1.5)
+    dys = [_randn(g, (M, N), F32, s) for s in (1e-7, 1.0, 1e-5)]
+    want = [fw.beam_moe_linear_backward(d, x, w, pre, act="silu") for d in dys]
+    bufs, graphs, outs = [], [], []
+    for i in (0, 1):
+        bufs.append(dys[i].clone())
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            fw.beam_moe_linear_backward(bufs[i], x, w, pre, act="silu")
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            outs.append(fw.beam_moe_linear_backward(bufs[i], x, w, pre, act="silu"))
+    for i, j in ((0, 0), (1, 1), (0, 2), (1, 0), (0, 1), (1, 2)):
+        bufs[i].copy_(dys[j])
+        graphs[i].replay()
+        eager = fw.beam_moe_linear_backward(dys[2 - j], x, w, pre, act="silu")
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs[i], want[j]))
+        assert all(torch.equal(a, b) for a, b in zip(eager, want[2 - j]))
+
+
 def test_linear_backward_parts():
     _say("linear_backward parts")
     g = _gen(4)
