@@ -134,18 +134,21 @@ __device__ __forceinline__ float act_f32(float z) {
   return z;
 }
 
-// d act / dz
+// d act / dz.  The factor z is held within +-128, where what it multiplies is 0 or takes the
+// rest to 0, so that an infinite z (a pre past fp16's range) has the slope's limit, 0 or 1, and
+// not 0 times infinity.  NaN comes through sigmoid or distribution function.
 template <int ACT>
 __device__ __forceinline__ float act_slope_f32(float z) {
+  const float f = __builtin_amdgcn_fmed3f(z, -128.f, 128.f);
   if constexpr (ACT == kActRelu) return z > 0.f ? 1.f : 0.f;
   if constexpr (ACT == kActSilu) {
     const float s = sigmoid_f32(z);
-    return s * (1.f + z * (1.f - s));
+    return s * (1.f + f * (1.f - s));
   }
   if constexpr (ACT == kActGelu) {
     float e;
     const float cdf = normal_cdf(z, e);
-    return fmaf(z * 0.39894228040143268f, e, cdf);
+    return fmaf(f * 0.39894228040143268f, e, cdf);
   }
   return 1.f;
 }

@@ -434,6 +434,7 @@ int beam_moe_linear(int32_t rows, int32_t cols, int32_t inner, int type, const v
  *   dy     [rows, cols] of dy_type: `type` or BEAM_MOE_F32
  *   pre    [rows, cols] of `type` as beam_moe_linear wrote it; not read (and may be NULL)
  *          when act is BEAM_MOE_ACT_NONE
+ *          (where it is infinite, as z past 65504 is in fp16, act' is its limit, 0 or 1)
  *   dx     [rows, inner] of `type`, dw [cols, inner] of `type`, dbias [cols] fp32,
  *          dres [rows, cols] of dy_type: each NULL = not wanted, one at least wanted;
  *          x is needed for dw and w for dx (else NULL)

@@ -670,6 +670,30 @@ def _slope(z, act):
     return torch.autograd.grad(ACTS[act](z).sum(), z)[0]
 
 
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu"])
+@pytest.mark.parametrize("dt", [BF16, F16])
+def test_slopes_at_infinite_pre(act, dt):
+    """An fp16 pre past 65504 is stored as an infinity while y, in FP32, is finite: the slope there is its limit, 0 or 1,
+    as it is from |z| = 110 on.  NaN stays NaN."""
+    _say("slopes at infinite pre", act, dt)
+    z = torch.tensor([7e4, -7e4, 6e4, -6e4, 1.0, float("nan"), 3e38, -3e38], device=DEV)
+    x, w = torch.zeros((3, 16), dtype=dt, device=DEV), torch.ones((8, 16), dtype=dt, device=DEV)
+    y, pre = fw.beam_moe_linear(x, w, z, act=act, out_dtype=F32, want_pre=True)
+    if dt == F16:
+        assert pre[0, 0] == float("inf") and pre[0, 1] == float("-inf")
+    x.fill_(1.0)
+    dy = torch.ones((3, 8), device=DEV)
+    dx, dw, db = fw.beam_moe_linear_backward(dy, x, w, pre, act=act)
+    for i, slope in ((0, 1.0), (1, 0.0), (2, 1.0), (3, 0.0), (6, 1.0), (7, 0.0)):
+        assert y[:, i].isfinite().all() and db[i] == 3 * slope and (dw[i] == 3 * slope).all(), i
+    if act == "relu":
+        assert db[5] == 0  # NaN > 0 does not hold
+    else:
+        assert db[5].isnan() and dw[5].isnan().all() and dx.isnan().all()
+    dx, _, _ = fw.beam_moe_linear_backward(dy[:, :4], x, w[:4], pre[:, :4], act=act)
+    assert (dx == 2).all()
+
+
 def _linear_back_check(dy, x, w, pre, act, keep, add, out):
     """dz is rounded to the products' type: half a step of each term, at worst all one way; then the sums.
     With no activation and add = 1, dz is dy, and in dy's type exact."""
