@@ -8,6 +8,7 @@
 // of the forward product, dz in dx) or the output's (w in dx, both in dw); products
 // run on 16-bit MFMA with FP32 accumulation; the epilogue is FP32 and rounds once to
 // the output's type.
+#include <algorithm>
 #include <type_traits>
 
 #include "linear.h"
@@ -260,11 +261,13 @@ constexpr int kSkinnyRows = 16;
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
+constexpr int kMaxSplits = 16;
+
 // Splits of a K of `stages` for `tiles` workgroups where `room` of them run at once.
 int splits_of(int tiles, int stages, int room) {
   int s = tiles > 0 && stages >= 24 ? room / tiles : 1;
   s = s < stages / 8 ? s : stages / 8;
-  s = s < 16 ? s : 16;
+  s = s < kMaxSplits ? s : kMaxSplits;
   return s > 1 ? s : 1;
 }
 
@@ -292,19 +295,20 @@ GemmPlan plan_tiles(int M, int N, int K) {
   // [8192, 2560] x [2560, 2560], 1.25 rounds and 2.5: 137 and 118; [8192, 1024] x [5120,
   // 1024], 2.5 and 5: 112 and 106, but 220 and 240 with K 2560).  128-row tiles split K until
   // two workgroups a CU have work, in at least 8 stages each; under 24 stages the join costs
-  // what a split gains.  64-row tiles where 128-row ones, split or not, make no more than a workgroup a CU
-  // ([2048, 1472] x [1024, 1472], 128 of those, 15.2 us against 21.4; [4096, 1024] x [1024,
-  // 1024], 256, 16.1 against 17.3; but [2048, 1024] x [2560, 1024], 320, 23.7 against 20.3,
-  // and [512, 5120] x [2560, 5120], 80 split nine times, 42 against 28), and for one or two
-  // stages, where the result's stores are most of the work ([3000, 128] x [3000, 128] 12.7
-  // us against 15.7).
+  // what a split gains.  64-row tiles where 128-row ones, in as many splits as K allows, make no
+  // more than a workgroup a CU ([2048, 1472] x [1024, 1472], 128 of those, 15.2 us against 21.4;
+  // [4096, 1024] x [1024, 1024], 256, 16.1 against 17.3; [300, 16384] x [300, 16384], 9 in 16
+  // splits, 19.4 against 23.2; [512, 9216] x [512, 9216], 16 in 16, 19.7 against 22.5, but 38.4
+  // against 35.3 with K 32768; [2048, 1024] x [2560, 1024], 320, 23.7 against 20.3; [512, 5120] x
+  // [2560, 5120], 80 in six, 42 against 28), and for one or two stages, where the result's stores
+  // are most of the work ([3000, 128] x [3000, 128] 12.7 us against 15.7).
   const int stages = ceil_div(K, kBK);
   const int t256 = ceil_div(M, 256) * ceil_div(N, 256), t128 = ceil_div(M, 128) * ceil_div(N, 128);
   auto fill = [](int64_t n, int round) { return (double)n / (double)((n + round - 1) / round * round); };
   auto splits = [&](int tiles) { return splits_of(tiles, stages, 2 * kCUs); };
   if (t128 > 1 << 20)  // so large a grid of smaller tiles would pass 2^32 threads
     p.tile = 256;
-  else if (stages <= 2 || (int64_t)t128 * (stages >= 24 ? stages / 8 + 1 : 1) <= kCUs)
+  else if (stages <= 2 || (int64_t)t128 * (stages >= 24 ? std::min(stages / 8 + 1, kMaxSplits) : 1) <= kCUs)
     p.tile = 64;
   else
     p.tile = fill(t256, kCUs) >= (stages <= 24 ? 0.85 : 0.8) * fill((int64_t)t128 * splits(t128), 2 * kCUs) ? 256 : 128;

@@ -611,6 +611,18 @@ def test_linear_rows_off_16_bytes(M, N, K, pad, dt):
     _linear_check(x[:, : K // 8 * 8], w[:, : K // 8 * 8], None, "none", None, 1.0, 1.0, z)
 
 
+# small results with a long K, split as often as it allows, in 64- and 128-row tiles
+@pytest.mark.parametrize("M,N,K", [(100, 100, 65536), (300, 300, 16384), (512, 512, 9216), (640, 512, 9216),
+                                   (17, 2049, 8200)])
+@pytest.mark.parametrize("dt", [BF16, F16])
+def test_linear_long_k(M, N, K, dt):
+    _say("linear long K", M, N, K, dt)
+    g = _gen(M + K)
+    x, w, bias = _randn(g, (M, K), dt), _randn(g, (N, K), dt, K ** -0.5), _randn(g, (N,))
+    y, pre = fw.beam_moe_linear(x, w, bias, act="gelu", out_dtype=F32, want_pre=True)
+    _linear_check(x, w, bias, "gelu", None, 1.0, 1.0, y, pre)
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 40, 64), (5, 70, 65), (70, 70, 65), (300, 264, 128)])
 def test_linear_in_place_padding_and_nan(M, N, K):
     _say("linear in place", M, N, K)

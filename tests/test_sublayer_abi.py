@@ -132,6 +132,14 @@ def test_workspace_queries_refuse_what_the_calls_refuse():
         binding._scratch(none, None, torch.device("cpu"), "x")
 
 
+def test_workspace_of_a_small_result_with_a_long_k():
+    """16 tiles of 128 rows fill no more than the CUs however K is split: 64-row tiles, split until two workgroups a CU
+    have work, eight times for 64 of them."""
+    lib = binding.load_library()
+    assert lib.beam_moe_linear_workspace_bytes(512, 512, 9216, 9216, 9216) == 8 * 512 * 512 * 4
+    assert lib.beam_moe_linear_workspace_bytes(640, 512, 9216, 9216, 9216) == 16 * 640 * 512 * 4
+
+
 def test_zero_rows_is_a_no_op_where_every_output_is_empty():
     assert NORM(rows=0, x=None, y=None, gamma=None, beta=None, mean=None, rstd=None) == OK
     assert NORM_BACK(rows=0, dy=None, x=None, mean=None, rstd=None, gamma=None, dgamma=None, dbeta=None) == OK
