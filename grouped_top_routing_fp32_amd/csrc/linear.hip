@@ -465,13 +465,17 @@ void plan_gradients(int rows, int cols, int inner, GemmPlan* dx, GemmPlan* dw) {
     }
   }
   // Where one takes 256-row tiles, which run one to a CU for 1.7 of a 128-row tile's stages (see
-  // plan_tiles), both stay as they are unless together they end first by this count: [2000,
-  // 2560] x [4000, 2560] 114.6 us by themselves, 89.3 together, [4096, 5120] x [5120, 5120] 474
-  // and 433 (0.94 of it), but [8192, 5120] x [2560, 5120] 433 and 449 (0.98).
+  // plan_tiles), both stay as they are unless together they end first by this count, which is
+  // good to some 10%: of 23 sizes with 1000 rows and more and cols and inner from 512 on those
+  // that counted 0.90 to 0.94 of alone were 0 to 14% faster together and those at 0.945 to 0.99 1
+  // to 4% slower, while of 28 with 200 to 700 rows, or cols or inner of 64 to 200, those at 0.94
+  // to 0.97 were 24% faster to 3% slower ([2000, 2560] x [4000, 2560], 0.78, 114.6 us by themselves,
+  // 89.3 together; [4096, 5120] x [5120, 5120], 0.936, 474 and 433; [35712, 64] x [512, 64], 47.9
+  // and 38.9; [8192, 5120] x [2560, 5120], 0.977, 433 and 449).
   if (dx->tile == 256 || dw->tile == 256) {
     auto alone = [&](const GemmPlan& p, int m) {
       const int64_t n = (int64_t)ceil_div(m, p.tile) * ceil_div(inner, p.tile) * p.splits;
-      const int64_t room = p.tile == 256 ? kCUs : p.tile == 128 ? 2 * kCUs : 8 * kCUs;
+      const int64_t room = p.tile == 256 ? kCUs : p.tile == 128 ? 2 * kCUs : 5 * kCUs;  // as LDS holds
       return (double)((n + room - 1) / room) * (p.k_per_split / kBK) * (p.tile == 256 ? 1.7 : 1.) + join(p.splits, m);
     };
     if (best > 0.97 * (alone(*dx, rows) + alone(*dw, cols) + 4.)) return;

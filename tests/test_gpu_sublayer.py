@@ -764,6 +764,20 @@ def test_linear_backward_together(M, N, K, act, dt, pad):
     assert torch.equal(fw.beam_moe_linear_backward(dy, x, None, pre, act=act, want_dx=False)[1], dw)
 
 
+# many rows and a small dw, K of dw split often: both in 64-row tiles, dx in 256-row tiles and dw in 64-row ones, both
+# in 128-row tiles
+@pytest.mark.parametrize("M,N,K", [(10176, 832, 192), (18048, 192, 512), (19392, 192, 768), (15000, 65, 1727)])
+@pytest.mark.parametrize("dt", [BF16, F16])
+def test_linear_backward_of_many_rows(M, N, K, dt):
+    _say("linear_backward of many rows", M, N, K, dt)
+    g = _gen(M + N + K)
+    x, w, dy, pre = (_randn(g, s, dt) for s in ((M, K), (N, K), (M, N), (M, N)))
+    dx, dw, db = fw.beam_moe_linear_backward(dy, x, w, pre, act="silu")
+    _linear_back_check(dy, x, w, pre, "silu", 1.0, 1.0, (dx, dw, db, None))
+    again = fw.beam_moe_linear_backward(dy, x, w, pre, act="silu")
+    assert all(torch.equal(p, q) for p, q in zip(again, (dx, dw, db)))
+
+
 def _dz_check(dy, x, w, pre, act, add, out):
     """fp16: dz is scaled by the power of two that takes b = 1.13 |add| max |dy| (no slope is larger) into [2^14, 2^15),
     and rounded: half a step of each term, or 2^-25 of fp16's least subnormal, which is at most 2^-39 b."""
