@@ -258,6 +258,37 @@ def test_layer_norm_gradient_against_differences():
     assert (curve <= 1e-2 * (d * exact).sum(1).abs() / (2 * h) + 1e-2).all()
 
 
+@pytest.mark.parametrize("rows,cols", [(5, 333), (3, 2560)])
+def test_layer_norm_gradient_against_differences_with_64_bit_curvature(rows, cols):
+    """The kernel's difference quotient against its own gradient, where nothing in the bound comes from that
+    gradient: the forward outputs' roundings over the step, dx's own, and the difference of quotient and slope of the
+    formula in 64 bits."""
+    _say("layer_norm differences, 64-bit curvature", rows, cols)
+    g = _gen(rows + cols)
+    x, v, dy = (_randn(g, (rows, cols)) for _ in range(3))
+    gamma = 1 + _randn(g, (cols,), F32, 0.2)
+    _, mean, rstd = fw.beam_moe_layer_norm(x, gamma)
+    dx, _, _ = fw.beam_moe_layer_norm_backward(dy, x, mean, rstd, gamma)
+    h = 2.0 ** -5
+    xp, xm = x + h * v, x - h * v
+    yp, ym = (fw.beam_moe_layer_norm(t, gamma)[0].double() for t in (xp, xm))
+    (rp, _, _, hp), (rm, _, _, hm) = (_norm_ref(t, gamma, None, 1e-5) for t in (xp, xm))
+    _, m64, r64, _ = _norm_ref(x, gamma, None, 1e-5)
+    rdx, _, _, hat, gg = _norm_back_ref(dy, x, m64, r64, gamma)
+    d, moved = dy.double(), (xp.double() - xm.double()) / (2 * h)
+    quot, slope = (d * (yp - ym)).sum(1) / (2 * h), (dx.double() * moved).sum(1)
+    curve = ((d * (rp - rm)).sum(1) / (2 * h) - (rdx * moved).sum(1)).abs()
+    # as in the checks of y and dx; dx takes mean and rstd rounded to FP32 besides, 64 and 40 u of them
+    gd = gamma.double().abs()
+    ey = sum(U * (gd * (64 + 48 * k.abs()) + 4 * y.abs()) + U * y.abs() for k, y in ((hp, rp), (hm, rm)))
+    a, b = gg.abs().mean(1, keepdim=True), (gg * hat).abs().mean(1, keepdim=True)
+    ex = U * r64[:, None] * (6 * gg.abs() + 70 * a + hat.abs() * 76 * b) + U * rdx.abs()
+    ex = ex + U * r64[:, None] * (40 * (gg.abs() + a + 3 * hat.abs() * b) + 64 * (b + hat.abs() * a))
+    bound = (d.abs() * ey).sum(1) / (2 * h) + (ex * moved.abs()).sum(1) + curve
+    assert ((quot - slope).abs() <= bound).all(), (quot, slope, bound)
+    assert (bound <= 0.05 * (rdx * moved).norm(dim=1) * cols ** 0.5).all()  # a bound that says something
+
+
 # --------------------------------------------------------------------------
 # balance loss and the router's gradient
 # --------------------------------------------------------------------------
