@@ -18,7 +18,8 @@ namespace beam {
 constexpr int kBalMaxE = 256;
 // Up to here one workgroup per sequence does everything, in one launch: on the GPU 4.0 us
 // for 64 tokens against 7.1 in two launches, 7.7 against 7.8 for 250, 12.4 against 8.2 for
-// 512, where the second launch still takes 4 us longer to issue.
+// 512, where the second launch still takes 4 us longer to issue.  (In a captured graph, which
+// issues for nothing, two launches would be the faster from some 260 tokens on.)
 constexpr int kBalSmallT = 512;
 constexpr int kBalSmallThreads = 1024;
 constexpr int kBalUnitThreads = 512;

@@ -19,8 +19,11 @@ namespace beam {
 constexpr int kLnMaxThreads = 1024;
 constexpr int kLnMaxWaves = kLnMaxThreads / 64;
 // Up to here the backward pass is one launch: with 1021 rows of 2561 columns in bf16 10.6 us
-// on the GPU, 12.8 in two launches, with 256 rows of 5120 6.3 and 12.0, with 1500 rows of 5120
-// in fp32 22.8 and 20.9; the second launch takes the host 4 us besides.
+// on the GPU, 12.8 in two launches, with 1024 rows of 512 5.8 and 9.2, with 256 rows of 5120
+// 6.3 and 12.0, with 512 rows of 16384 in fp32 31.5 and 35.5, with 1500 rows of 5120 in fp32
+// 22.8 and 20.9; the second launch takes the host 4 us besides.  With 1024 rows of 8192 columns
+// and more, read twice, it is within 12% either way (16384 in fp32 68.6 and 61.1, in bf16 31.5
+// and 33.0).
 constexpr int kLnFewRows = 1024;
 constexpr int kLnFewCols = 32;  // of a workgroup that adds columns
 constexpr int kLnMaxJoin = 4096;  // columns of rows that share a workgroup with others
@@ -117,7 +120,8 @@ __global__ __launch_bounds__(kLnMaxThreads) void layer_norm_kernel(
 // then those blocks * blockDim.y further on; a thread's columns stay the same from
 // row to row, so it sums their dgamma and dbeta in registers.  At the end the teams add
 // up in LDS, in order, and the workgroup writes one row of part [2][blocks][H], which
-// column_sums_kernel adds up: no atomics, so the sums' order is fixed.
+// column_sums_kernel adds up: no atomics, so the sums' order is fixed.  Above 8192 columns, two
+// chunks a thread, FP32 dy spills up to 7 registers.
 template <class DT, class XT, int NCH, bool TAIL, bool SUMS>
 __device__ __forceinline__ void backward_rows(
     const typename DT::S* __restrict__ dy, int64_t lddy, const typename XT::S* __restrict__ x, int64_t ldx,
@@ -458,12 +462,12 @@ hipError_t launch_layer_norm_backward(const void* dy, int dy_type, int64_t lddy,
         hipLaunchKernelGGL((layer_norm_backward_kernel<DT, XT, decltype(n)::value, decltype(tail)::value>),
                            dim3(units), dim3(s.team, teams), 0, st, static_cast<const typename DT::S*>(dy), lddy,
                            static_cast<const typename XT::S*>(x), ldx, mean, rstd, gamma,
-                           static_cast<typename XT::S*>(dx), lddx, sums ? part : nullptr, T, H);
+                           static_cast<typename XT::S*>(dx), lddx, part, T, H);
         return hipGetLastError();
       });
     });
   });
-  if (e != hipSuccess || !sums) return e;
+  if (e != hipSuccess) return e;
   return launch_column_sums(part, dgamma, dbeta, units, H, st);
 }
 

@@ -335,7 +335,9 @@ enum {
  *   y            [rows, cols] out, of any element type
  *   mean, rstd   [rows] fp32 out, what the backward pass reads; NULL = not written
  * 1 <= cols <= 16384, 0 <= rows <= 2^21 (0: nothing is written).  The statistics
- * do not cancel where the mean is far from zero. */
+ * do not cancel where the mean is far from zero.  They are sums in FP32: a row whose
+ * squares (x - mean)^2 add up past its range, from spreads of some 2^57 on, has
+ * rstd = 0 and y = beta. */
 int beam_moe_layer_norm(int32_t rows, int32_t cols, const void* x, int x_type, int64_t ldx, const float* gamma,
                         const float* beta, float eps, void* y, int y_type, int64_t ldy, float* mean, float* rstd,
                         void* stream);
