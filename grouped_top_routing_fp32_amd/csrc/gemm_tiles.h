@@ -385,9 +385,8 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(GemmArgs g, int mt, i
 }
 
 // dx = dz w and dw = dz^T x in one launch, where neither fills the card alone.  Those
-// with the longer K come first.  (In 256-row tiles nothing is gained: 429 us either way at [8192, 5120] x
-// [2560, 5120], where the matrix cores' power is the bound and idle CUs leave the others more
-// of it.)
+// with the longer K come first.  (In 256-row tiles nothing is gained: 429 us either way at [8192,
+// 5120] x [2560, 5120], 640 and 200 tiles, although fewer CUs idle.)
 template <bool HALF, int TILE>
 __global__ __launch_bounds__(256) void gemm_pair_kernel(GemmArgs dx, GemmSplit sx, GemmArgs dw, GemmSplit sw) {
   __shared__ __align__(1024) uint16_t ring[kRing<TILE, TILE>];
