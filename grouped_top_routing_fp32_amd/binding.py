@@ -10,7 +10,8 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
-from typing import Optional
+from array import array
+from typing import NamedTuple, Optional, Sequence
 
 import torch
 
@@ -34,7 +35,9 @@ EXPORTED = ("beam_moe_workspace_bytes", "beam_moe_route_workspace_bytes", "beam_
             "beam_moe_residual_forward_fp8", "beam_moe_layer_norm", "beam_moe_layer_norm_backward_workspace_bytes",
             "beam_moe_layer_norm_backward", "beam_moe_balance_loss_workspace_bytes", "beam_moe_balance_loss",
             "beam_moe_route_backward", "beam_moe_linear_workspace_bytes", "beam_moe_linear_backward_workspace_bytes",
-            "beam_moe_linear", "beam_moe_linear_backward", "beam_moe_stream_rows", "beam_moe_timing_enable",
+            "beam_moe_linear", "beam_moe_linear_backward", "beam_moe_grad_norm_workspace_bytes",
+            "beam_moe_grad_norm", "beam_moe_clip_grads", "beam_moe_quantize_mxfp4", "beam_moe_dequantize_mxfp4",
+            "beam_moe_stream_rows", "beam_moe_timing_enable",
             "beam_moe_timing_read", "beam_moe_stage_name", "beam_moe_status_str")
 
 SIZE_MAX = 2 ** 64 - 1
@@ -109,7 +112,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             ("beam_moe_linear", ci, [i32, i32, i32, ci, vp, i64, vp, i64, vp, ci, vp, i64, f32, f32, vp, ci, i64, vp,
                                      i64, vp, sz, vp]),
             ("beam_moe_linear_backward", ci, [i32, i32, i32, ci, vp, ci, i64, vp, i64, vp, i64, vp, i64, ci, f32, f32,
-                                              vp, i64, vp, i64, vp, vp, i64, vp, sz, vp])):
+                                              vp, i64, vp, i64, vp, vp, i64, vp, sz, vp]),
+            ("beam_moe_grad_norm_workspace_bytes", sz, [i32]),
+            ("beam_moe_grad_norm", ci, [i32, vp, vp, vp, f32, vp, vp, sz, vp]),
+            ("beam_moe_clip_grads", ci, [i32, vp, vp, vp, f32, f32, f32, vp, vp, vp, vp, vp, sz, vp]),
+            ("beam_moe_quantize_mxfp4", ci, [i32, i32, vp, ci, i64, vp, i64, vp, i64, vp]),
+            ("beam_moe_dequantize_mxfp4", ci, [i32, i32, vp, i64, vp, i64, vp, ci, i64, vp])):
         getattr(lib, fn).argtypes = args
         getattr(lib, fn).restype = res
     lib.beam_moe_stream_rows.argtypes = [pd, i32, ctypes.c_int]
@@ -732,6 +740,138 @@ def beam_moe_linear_backward(dy: torch.Tensor, x: Optional[torch.Tensor], w: Opt
             db.data_ptr() if want_dbias else None, dres.data_ptr() if want_dres else None, N, wp, wn, st),
             "beam_moe_linear_backward")
     return (dx, dw, db, dres) if want_dres else (dx, dw, db)
+
+
+# --------------------------------------------------------------------------
+# a dense gated sublayer, trained and served: clipping, 4-bit floating point
+# --------------------------------------------------------------------------
+def _dense(t: torch.Tensor) -> bool:
+    """Whether t's elements fill one stretch of memory: contiguous, or a matrix's transpose."""
+    return t.is_contiguous() or (t.dim() == 2 and t.t().is_contiguous())
+
+
+def _list_of(tensors: Sequence[torch.Tensor], name: str):
+    """(tensors, device, addresses, types, sizes) of a list of gradients; the last three as C arrays."""
+    ts = tensors if isinstance(tensors, (list, tuple)) else list(tensors)
+    if not ts:
+        raise ValueError(f"{name} must hold at least one tensor")
+    dev = ts[0].device
+    types = array("i")
+    sizes = array("q")
+    at = array("Q")
+    for t in ts:
+        kind = ELEM_TYPES.get(t.dtype)
+        if kind is None or t.device != dev or not _dense(t):
+            raise ValueError(f"{name} must be dense tensors of one of {_FLOATS} on {dev}, got {t.dtype} with strides "
+                             f"{t.stride()} on {t.device}")
+        types.append(kind)
+        sizes.append(t.numel())
+        at.append(t.data_ptr())
+    if dev.type != "cuda":
+        raise ValueError(f"{name} must be device tensors")
+    return ts, dev, at, types, sizes
+
+
+def _addr(a: array) -> int:
+    return a.buffer_info()[0]
+
+
+def beam_moe_grad_norm(grads: Sequence[torch.Tensor], *, scale: float = 1.0, ws: Optional[torch.Tensor] = None,
+                       stream=None) -> torch.Tensor:
+    """The norm of all gradients, times |scale|, as a fp32 scalar on the device. grads: tensors of bf16, fp16 or
+    fp32 in any mixture, each dense."""
+    ts, dev, at, types, sizes = _list_of(grads, "grads")
+    lib = load_library()
+    with _On(dev, stream) as st:
+        norm = torch.empty((), dtype=_F32, device=dev)
+        wp, wn, _keep = _scratch(lib.beam_moe_grad_norm_workspace_bytes(len(ts)), ws, dev, "beam_moe_grad_norm")
+        _check(lib.beam_moe_grad_norm(len(ts), _addr(at), _addr(types), _addr(sizes), scale, norm.data_ptr(), wp, wn,
+                                      st), "beam_moe_grad_norm")
+    return norm
+
+
+def beam_moe_clip_grads(grads: Sequence[torch.Tensor], max_norm: float, *, scale: float = 1.0, eps: float = 1e-6,
+                        norm: Optional[torch.Tensor] = None, out: Optional[Sequence[torch.Tensor]] = None,
+                        ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """g * scale * min(1, max_norm / (norm + eps)) for all gradients, in place or, with out, into tensors of the
+    same shapes and strides and any of the types. The norm is that of all gradients times |scale|, or the given fp32
+    scalar. Returns the norm (before clipping)."""
+    ts, dev, at, types, sizes = _list_of(grads, "grads")
+    ot, okinds = None, None
+    if out is not None:
+        os_, odev, ot, okinds, _ = _list_of(out, "out")
+        if odev != dev or len(os_) != len(ts) or any(a.shape != b.shape or a.stride() != b.stride()
+                                                     for a, b in zip(ts, os_)):
+            raise ValueError("out must hold a tensor of each gradient's shape and strides, on its device")
+    if norm is not None and (norm.numel() != 1 or norm.dtype != _F32 or norm.device != dev):
+        raise ValueError(f"norm must be one fp32 element on {dev}")
+    lib = load_library()
+    with _On(dev, stream) as st:
+        wp, wn, _keep = None, 0, None
+        given = norm
+        if given is None:
+            norm = torch.empty((), dtype=_F32, device=dev)
+            wp, wn, _keep = _scratch(lib.beam_moe_grad_norm_workspace_bytes(len(ts)), ws, dev, "beam_moe_clip_grads")
+        _check(lib.beam_moe_clip_grads(
+            len(ts), _addr(at), _addr(types), _addr(sizes), scale, max_norm, eps,
+            None if given is None else given.data_ptr(), None if ot is None else _addr(ot),
+            None if okinds is None else _addr(okinds), norm.data_ptr() if given is None else None, wp, wn, st),
+            "beam_moe_clip_grads")
+    return norm
+
+
+class Mxfp4(NamedTuple):
+    """A matrix in microscaled 4-bit floating point: codes [rows, 16 * ceil(cols / 32)] uint8, two to a byte, first
+    the low half, and scales [rows, ceil(cols / 32)] uint8, 2^(scale - 127). Rows may be strided (codes by 16 bytes)."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+
+_U8 = (torch.uint8,)
+
+
+def _mx(q, name: str, rows: int, blocks: int, dev) -> tuple:
+    """Checks codes and scales of `rows` rows; returns both row strides."""
+    codes, scales = q
+    return (_rows(codes, f"{name}'s codes", _U8, (rows, 16 * blocks), dev),
+            _rows(scales, f"{name}'s scales", _U8, (rows, blocks), dev))
+
+
+def beam_moe_quantize_mxfp4(x: torch.Tensor, *, out: Optional[Mxfp4] = None, stream=None) -> Mxfp4:
+    """x [T, H] (bf16, fp16 or fp32; rows may be strided) in microscaled 4-bit floating point."""
+    T, H, dev = _mat(x, "x")
+    ldx = _rows(x, "x", _FLOATS, (T, H), dev)
+    blocks = (H + 31) // 32
+    with _On(dev, stream) as st:
+        if out is None:
+            out = Mxfp4(torch.empty(T, 16 * blocks, dtype=torch.uint8, device=dev),
+                        torch.empty(T, blocks, dtype=torch.uint8, device=dev))
+            ldc, lds = 16 * blocks, blocks
+        else:
+            ldc, lds = _mx(out, "out", T, blocks, dev)
+        codes, scales = out
+        _check(load_library().beam_moe_quantize_mxfp4(T, H, x.data_ptr(), ELEM_TYPES[x.dtype], ldx, codes.data_ptr(),
+                                                      ldc, scales.data_ptr(), lds, st), "beam_moe_quantize_mxfp4")
+    return out
+
+
+def beam_moe_dequantize_mxfp4(q: Mxfp4, cols: Optional[int] = None, *, out_dtype: Optional[torch.dtype] = None,
+                              out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The values of q = (codes, scales), [T, cols] in out_dtype (default bf16). cols defaults to all columns of the
+    codes; fewer leave the last block's filling out."""
+    codes, _ = q
+    T, width, dev = _mat(codes, "codes")
+    blocks = width // 16
+    ldc, lds = _mx(q, "q", T, blocks, dev)
+    H = 32 * blocks if cols is None else cols
+    if not 32 * (blocks - 1) < H <= 32 * blocks:
+        raise ValueError(f"cols must be in the last of the {blocks} blocks of 32, got {H}")
+    with _On(dev, stream) as st:
+        out, ldy = _result(out, out_dtype, torch.bfloat16, _FLOATS, (T, H), dev)
+        _check(load_library().beam_moe_dequantize_mxfp4(T, H, codes.data_ptr(), ldc, q[1].data_ptr(), lds,
+                                                        out.data_ptr(), ELEM_TYPES[out.dtype], ldy, st),
+               "beam_moe_dequantize_mxfp4")
+    return out
 
 
 # --------------------------------------------------------------------------

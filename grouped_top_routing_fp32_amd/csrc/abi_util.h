@@ -36,6 +36,13 @@ inline int check_optional(std::initializer_list<const void*> ptrs) {
 
 inline int hip_status(hipError_t e) { return e == hipSuccess ? BEAM_MOE_OK : BEAM_MOE_ERR_HIP; }
 
+constexpr int64_t kMaxLd = int64_t(1) << 40;  // row offsets stay far inside 64 bits
+
+inline bool type_ok(int t) { return t == BEAM_MOE_BF16 || t == BEAM_MOE_F16 || t == BEAM_MOE_F32; }
+inline bool half_type(int t) { return t == BEAM_MOE_BF16 || t == BEAM_MOE_F16; }
+inline bool act_ok(int act) { return act >= BEAM_MOE_ACT_NONE && act <= BEAM_MOE_ACT_GELU; }
+inline bool ld_ok(int64_t ld, int64_t cols) { return ld >= cols && ld <= kMaxLd; }
+
 // The block's dims and batch size (abi.cpp).
 int check_block(const beam_moe_dims* d, int32_t T);
 

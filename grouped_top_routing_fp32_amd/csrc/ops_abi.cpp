@@ -34,23 +34,22 @@ hipError_t launch_linear_dz(const void* dy, int dy_type, int64_t lddy, const voi
 
 namespace {
 
+using beam::act_ok;
 using beam::align_up;
 using beam::aligned16;
 using beam::at;
 using beam::check_optional;
 using beam::check_ptrs;
+using beam::half_type;
 using beam::hip_status;
+using beam::ld_ok;
+using beam::type_ok;
 
 constexpr int32_t kMaxNormRows = 1 << 21;   // the grid's threads fit 32 bits
 constexpr int32_t kMaxGradTokens = 1 << 25;
 constexpr int32_t kMaxSeqs = 1 << 20;
 constexpr int32_t kMaxLinearRows = 1 << 20;
 constexpr int32_t kMaxLinearCols = 1 << 18;
-constexpr int64_t kMaxLd = int64_t(1) << 40;  // row offsets stay far inside 64 bits
-
-bool type_ok(int t) { return t == BEAM_MOE_BF16 || t == BEAM_MOE_F16 || t == BEAM_MOE_F32; }
-bool half_type(int t) { return t == BEAM_MOE_BF16 || t == BEAM_MOE_F16; }
-bool ld_ok(int64_t ld, int64_t cols) { return ld >= cols && ld <= kMaxLd; }
 
 int check_norm(int32_t rows, int32_t cols) {
   if (rows < 0) return BEAM_MOE_ERR_INVALID_ARG;
@@ -69,8 +68,6 @@ int check_linear(int32_t rows, int32_t cols, int32_t inner) {
     return BEAM_MOE_ERR_UNSUPPORTED;
   return BEAM_MOE_OK;
 }
-
-bool act_ok(int act) { return act >= BEAM_MOE_ACT_NONE && act <= BEAM_MOE_ACT_GELU; }
 
 // Workspace of the backward pass: dz, the partial sums of dbias, the inverse of an fp16 dz's
 // scale with the maxima that give it, w and x where they are laid out anew, then the partial sums of the two products, in the same place unless they

@@ -452,6 +452,66 @@ int beam_moe_linear_backward(int32_t rows, int32_t cols, int32_t inner, int type
                              int64_t lddw, float* dbias, void* dres, int64_t lddres, void* ws, size_t ws_bytes,
                              void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators of a dense gated sublayer, trained and served.  The conventions of
+ * the section above hold.
+ * ------------------------------------------------------------------------- */
+
+/* Workspace of beam_moe_grad_norm and beam_moe_clip_grads for `count` tensors.
+ * Returns SIZE_MAX for unsupported counts. */
+size_t beam_moe_grad_norm_workspace_bytes(int32_t count);
+
+/* The norm of all gradients of a step, as of one long vector:
+ *   norm = |scale| * sqrt(sum over all tensors of g^2)
+ *   grads   [count] device pointers (an array on the host, read before the call returns), each
+ *           aligned to its element; NULL where the size is 0
+ *   types   [count] element types BEAM_MOE_BF16, _F16 or _F32 (host)
+ *   sizes   [count] elements, 0 .. 2^40 (host); 2^44 in all
+ *   scale   finite; the reciprocal of a loss scale or of a number of accumulated steps
+ *   norm    fp32 out, one element on the device
+ *   ws      of beam_moe_grad_norm_workspace_bytes(count)
+ * Squares are summed in FP64: neither they nor their sum overflow or vanish.  0 <= count <= 2^16;
+ * the norm of no elements is 0. */
+int beam_moe_grad_norm(int32_t count, const void* const* grads, const int32_t* types, const int64_t* sizes, float scale,
+                       float* norm, void* ws, size_t ws_bytes, void* stream);
+
+/* Clipping by the norm of all gradients, and their scaling:
+ *   out = g * (scale * min(1, max_norm / (norm + eps)))
+ * The factor is rounded to FP32, the product to out's type.  The arguments of beam_moe_grad_norm, and
+ *   max_norm   finite, >= 0
+ *   eps        finite, > 0
+ *   norm_in    one fp32 on the device to take as the norm (of gradients that are spread over
+ *              processes, say), NULL = the norm of `grads` as beam_moe_grad_norm gives it
+ *   outs       [count] device pointers (host array), aligned to their element, NULL = in place; outs[i] may be
+ *              grads[i] with the same type, and lies apart from every other gradient and output
+ *   out_types  [count] element types of outs (host), NULL = the gradients' own
+ *   norm       fp32 out: the norm taken, before clipping; NULL = not written
+ *   ws         not needed with norm_in
+ * Outputs that overlap, or gradients that occur twice in place, are refused.  Where the norm is infinite the
+ * finite gradients are 0 and the infinite ones NaN; where it is NaN, all are. */
+int beam_moe_clip_grads(int32_t count, const void* const* grads, const int32_t* types, const int64_t* sizes, float scale,
+                        float max_norm, float eps, const float* norm_in, void* const* outs, const int32_t* out_types,
+                        float* norm, void* ws, size_t ws_bytes, void* stream);
+
+/* Microscaled 4-bit floating point (OCP MX v1.0, MXFP4): each row's elements in blocks of 32, the
+ * last one filled up with zeros; a block has 16 bytes of E2M1 codes, two to a byte with the first in the low
+ * half, and one E8M0 scale byte e, 2^(e - 127), 255 for NaN.  From values:
+ *   e = 127 + floor(log2(largest magnitude of the block)) - 2, at least 0,
+ *   code = x / 2^(e - 127) to the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6, ties to the even code, 6 at most
+ * A block of zeros, and one of FP32 subnormals, has e = 0; one that holds an infinity or NaN has e = 255 and
+ * zero codes, and reads back as NaN.
+ *   x       [rows, cols] of any element type
+ *   codes   [rows, 16 * ceil(cols / 32)] bytes out, ldc its row stride in bytes, a multiple of 16
+ *   scales  [rows, ceil(cols / 32)] bytes out, lds its row stride in bytes
+ * 0 <= rows <= 2^20, 1 <= cols <= 2^18. */
+int beam_moe_quantize_mxfp4(int32_t rows, int32_t cols, const void* x, int x_type, int64_t ldx, uint8_t* codes,
+                            int64_t ldc, uint8_t* scales, int64_t lds, void* stream);
+
+/* The values of such codes, y [rows, cols] out of any element type (rounded to it once; exact in FP32, and
+ * in the others where they hold the value). */
+int beam_moe_dequantize_mxfp4(int32_t rows, int32_t cols, const uint8_t* codes, int64_t ldc, const uint8_t* scales,
+                              int64_t lds, void* y, int y_type, int64_t ldy, void* stream);
+
 /* Static string for a status code. */
 const char* beam_moe_status_str(int status);
 

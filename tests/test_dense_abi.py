@@ -1,0 +1,111 @@
+"""Host-side validation of the operators of a dense gated sublayer (gradient norm and clipping, microscaled 4-bit
+floating point, the gated projections): every rejected call returns before any device work.  CPU only."""
+import ctypes
+
+import pytest
+import torch
+
+from grouped_top_routing_fp32_amd import binding
+from test_sublayer_abi import BAD, BF16, F16, F32, FAKE, ODD, OK, UNSUP, WS, Call
+
+A = [ctypes.c_void_p((k + 1) << 24) for k in range(8)]     # apart from each other, never dereferenced
+
+
+def ptrs(*p):
+    return (ctypes.c_void_p * len(p))(*[q.value if q is not None else None for q in p])
+
+
+def ints(*v):
+    return (ctypes.c_int32 * len(v))(*v)
+
+
+def sizes(*v):
+    return (ctypes.c_int64 * len(v))(*v)
+
+
+NORM = Call("beam_moe_grad_norm", count=2, grads=ptrs(A[0], A[1]), types=ints(BF16, F32), sizes=sizes(5, 7), scale=1.0,
+            norm=FAKE, ws=FAKE, ws_bytes=1 << 30, stream=None)
+CLIP = Call("beam_moe_clip_grads", count=2, grads=ptrs(A[0], A[1]), types=ints(BF16, F32), sizes=sizes(5, 7), scale=1.0,
+            max_norm=1.0, eps=1e-6, norm_in=None, outs=ptrs(A[2], A[3]), out_types=ints(F32, F32), norm=FAKE, ws=FAKE,
+            ws_bytes=1 << 30, stream=None)
+QUANT = Call("beam_moe_quantize_mxfp4", rows=4, cols=70, x=FAKE, x_type=BF16, ldx=70, codes=FAKE, ldc=48, scales=FAKE,
+             lds=3, stream=None)
+DEQUANT = Call("beam_moe_dequantize_mxfp4", rows=4, cols=70, codes=FAKE, ldc=48, scales=FAKE, lds=3, y=FAKE,
+               y_type=BF16, ldy=70, stream=None)
+
+
+@pytest.mark.parametrize("call, required, optional", [
+    (NORM, ("norm",), ()), (CLIP, (), ("norm", "norm_in")), (QUANT, ("x", "codes", "scales"), ()),
+    (DEQUANT, ("codes", "scales", "y"), ()),
+], ids=lambda v: v.fn if isinstance(v, Call) else "")
+def test_pointers(call, required, optional):
+    for name in required:
+        assert call(**{name: None}) == BAD, name
+    for name in required + optional:
+        assert call(**{name: ODD}) == BAD, name
+
+
+@pytest.mark.parametrize("call, bad", [
+    (c, b) for c in (NORM, CLIP) for b in (
+        dict(count=-1), dict(grads=None), dict(types=None), dict(sizes=None), dict(types=ints(BF16, 3)),
+        dict(sizes=sizes(5, -1)), dict(grads=ptrs(A[0], None)), dict(scale=float("nan")), dict(scale=float("inf")),
+        dict(grads=ptrs(ctypes.c_void_p(A[0].value + 1), A[1])), dict(grads=ptrs(A[0], ctypes.c_void_p(A[1].value + 2))))
+] + [
+    (CLIP, dict(max_norm=-1.0)), (CLIP, dict(max_norm=float("inf"))), (CLIP, dict(max_norm=float("nan"))),
+    (CLIP, dict(eps=0.0)), (CLIP, dict(eps=-1e-6)), (CLIP, dict(eps=float("nan"))), (CLIP, dict(outs=None)),
+    (CLIP, dict(out_types=ints(F32, 9))), (CLIP, dict(outs=ptrs(A[2], None))),
+    (CLIP, dict(outs=ptrs(ctypes.c_void_p(A[2].value + 2), A[3]))),
+    # outputs that overlap each other, another gradient, or their own of another type
+    (CLIP, dict(outs=ptrs(A[2], A[2]))), (CLIP, dict(outs=ptrs(A[2], ctypes.c_void_p(A[2].value + 16)))),
+    (CLIP, dict(outs=ptrs(A[1], A[2]))), (CLIP, dict(outs=ptrs(A[2], ctypes.c_void_p(A[0].value + 8)))),
+    (CLIP, dict(outs=ptrs(A[0], A[3]))), (CLIP, dict(outs=ptrs(A[2], ctypes.c_void_p(A[1].value + 4)))),
+    (CLIP, dict(grads=ptrs(A[0], A[0]), types=ints(BF16, BF16), outs=None, out_types=None)),
+    (QUANT, dict(rows=-1)), (QUANT, dict(x_type=3)), (QUANT, dict(ldx=69)), (QUANT, dict(ldc=32)),
+    (QUANT, dict(ldc=56)), (QUANT, dict(lds=2)), (QUANT, dict(lds=1 << 41)),
+    (DEQUANT, dict(rows=-1)), (DEQUANT, dict(y_type=-1)), (DEQUANT, dict(ldy=69)), (DEQUANT, dict(ldc=40)),
+    (DEQUANT, dict(lds=2)),
+], ids=lambda v: v.fn if isinstance(v, Call) else "-".join(v) if isinstance(v, dict) else "")
+def test_invalid_arguments(call, bad):
+    assert call(**bad) == BAD
+
+
+@pytest.mark.parametrize("call, big", [
+    (NORM, dict(count=(1 << 16) + 1)), (CLIP, dict(count=(1 << 16) + 1)), (NORM, dict(sizes=sizes(5, (1 << 40) + 1))),
+    (QUANT, dict(rows=(1 << 20) + 1)), (QUANT, dict(cols=(1 << 18) + 1)), (QUANT, dict(cols=0)),
+    (DEQUANT, dict(rows=(1 << 20) + 1)), (DEQUANT, dict(cols=(1 << 18) + 1)), (DEQUANT, dict(cols=0)),
+], ids=lambda v: v.fn if isinstance(v, Call) else "-".join(v) if isinstance(v, dict) else "")
+def test_unsupported_sizes(call, big):
+    assert call(**big) == UNSUP
+
+
+def test_too_many_elements_in_all():
+    n = 17
+    args = dict(count=n, grads=ptrs(*[A[0]] * n), types=ints(*[BF16] * n), sizes=sizes(*[1 << 40] * n))
+    assert NORM(**args) == UNSUP and CLIP(**args) == UNSUP
+
+
+def test_workspaces():
+    lib = binding.load_library()
+    need = lib.beam_moe_grad_norm_workspace_bytes(2)
+    assert 0 < need < 1 << 20
+    assert lib.beam_moe_grad_norm_workspace_bytes(-1) == lib.beam_moe_grad_norm_workspace_bytes((1 << 16) + 1) \
+        == binding.SIZE_MAX
+    for call in (NORM, CLIP):
+        assert call(ws=None) == WS and call(ws=ODD) == WS and call(ws_bytes=need - 1) == WS
+
+
+def test_no_rows():
+    for call in (QUANT, DEQUANT):
+        assert call(rows=0) == OK
+
+
+def test_binding_refuses_what_is_not_on_the_device():
+    for grads in ([], [torch.zeros(3)], [torch.zeros(3, dtype=torch.int32)], [torch.zeros(3, 4)[:, ::2]]):
+        with pytest.raises(ValueError):
+            binding.beam_moe_grad_norm(grads)
+        with pytest.raises(ValueError):
+            binding.beam_moe_clip_grads(grads, 1.0)
+    with pytest.raises(ValueError):
+        binding.beam_moe_quantize_mxfp4(torch.zeros(3, 4))
+    with pytest.raises(ValueError):
+        binding.beam_moe_dequantize_mxfp4((torch.zeros(3, 16, dtype=torch.uint8), torch.zeros(3, 1, dtype=torch.uint8)))
