@@ -35,7 +35,9 @@ EXPORTED = ("beam_moe_workspace_bytes", "beam_moe_route_workspace_bytes", "beam_
             "beam_moe_residual_forward_fp8", "beam_moe_layer_norm", "beam_moe_layer_norm_backward_workspace_bytes",
             "beam_moe_layer_norm_backward", "beam_moe_balance_loss_workspace_bytes", "beam_moe_balance_loss",
             "beam_moe_route_backward", "beam_moe_linear_workspace_bytes", "beam_moe_linear_backward_workspace_bytes",
-            "beam_moe_linear", "beam_moe_linear_backward", "beam_moe_grad_norm_workspace_bytes",
+            "beam_moe_linear", "beam_moe_linear_backward", "beam_moe_gated_linear_workspace_bytes",
+            "beam_moe_gated_linear_backward_workspace_bytes", "beam_moe_gated_linear",
+            "beam_moe_gated_linear_backward", "beam_moe_grad_norm_workspace_bytes",
             "beam_moe_grad_norm", "beam_moe_clip_grads", "beam_moe_quantize_mxfp4", "beam_moe_dequantize_mxfp4",
             "beam_moe_stream_rows", "beam_moe_timing_enable",
             "beam_moe_timing_read", "beam_moe_stage_name", "beam_moe_status_str")
@@ -113,6 +115,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                      i64, vp, sz, vp]),
             ("beam_moe_linear_backward", ci, [i32, i32, i32, ci, vp, ci, i64, vp, i64, vp, i64, vp, i64, ci, f32, f32,
                                               vp, i64, vp, i64, vp, vp, i64, vp, sz, vp]),
+            ("beam_moe_gated_linear_workspace_bytes", sz, [i32, i32, i32, i64, i64, i64]),
+            ("beam_moe_gated_linear_backward_workspace_bytes", sz, [i32, i32, i32, i64, i64, i64]),
+            ("beam_moe_gated_linear", ci, [i32, i32, i32, ci, vp, i64, vp, i64, vp, i64, vp, vp, ci, vp, ci, i64, vp,
+                                           i64, vp, i64, vp, sz, vp]),
+            ("beam_moe_gated_linear_backward", ci, [i32, i32, i32, ci, vp, ci, i64, vp, i64, vp, i64, vp, i64, vp, i64,
+                                                    vp, i64, ci, vp, i64, vp, i64, vp, i64, vp, vp, vp, sz, vp]),
             ("beam_moe_grad_norm_workspace_bytes", sz, [i32]),
             ("beam_moe_grad_norm", ci, [i32, vp, vp, vp, f32, vp, vp, sz, vp]),
             ("beam_moe_clip_grads", ci, [i32, vp, vp, vp, f32, f32, f32, vp, vp, vp, vp, vp, sz, vp]),
@@ -743,8 +751,74 @@ def beam_moe_linear_backward(dy: torch.Tensor, x: Optional[torch.Tensor], w: Opt
 
 
 # --------------------------------------------------------------------------
-# a dense gated sublayer, trained and served: clipping, 4-bit floating point
+# a dense gated sublayer, trained and served: projections, clipping, 4-bit floating point
 # --------------------------------------------------------------------------
+def beam_moe_gated_linear(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
+                          bias_gate: Optional[torch.Tensor] = None, bias_up: Optional[torch.Tensor] = None, *,
+                          act: str = "silu", out_dtype: Optional[torch.dtype] = None,
+                          out: Optional[torch.Tensor] = None, want_pre: bool = False,
+                          ws: Optional[torch.Tensor] = None, stream=None):
+    """h = act(x w_gate^T + bias_gate) * (x w_up^T + bias_up) for x [M, K], both weights [N, K] in bf16 or fp16 (rows
+    may be strided), biases [N] fp32. h is of out_dtype (x's type, or fp32). Returns h, or (h, pre_gate, pre_up) with
+    want_pre: both arguments [M, N] of x's type are what the backward pass reads."""
+    M, K, dev = _mat(x, "x")
+    if w_gate.dim() != 2:
+        raise ValueError("w_gate must be a matrix")
+    N, dt = w_gate.shape[0], x.dtype
+    ldx, ldg = _rows(x, "x", _HALF, (M, K), dev), _rows(w_gate, "w_gate", (dt,), (N, K), dev)
+    ldu = _rows(w_up, "w_up", (dt,), (N, K), dev)
+    bg, bu = _vec(bias_gate, "bias_gate", _F32, (N,), dev), _vec(bias_up, "bias_up", _F32, (N,), dev)
+    a = _act(act)
+    with _On(dev, stream) as st:
+        out, ldh = _result(out, out_dtype, dt, (dt, _F32), (M, N), dev)
+        pg = torch.empty(M, N, dtype=dt, device=dev) if want_pre else None
+        pu = torch.empty_like(pg) if want_pre else None
+        wp, wn, _keep = _scratch(_linear_ws("beam_moe_gated_linear_workspace_bytes", M, N, K, ldx, ldg, ldu), ws, dev,
+                                 "beam_moe_gated_linear")
+        _check(load_library().beam_moe_gated_linear(
+            M, N, K, ELEM_TYPES[dt], x.data_ptr(), ldx, w_gate.data_ptr(), ldg, w_up.data_ptr(), ldu, bg, bu, a,
+            out.data_ptr(), ELEM_TYPES[out.dtype], ldh, pg.data_ptr() if want_pre else None, N,
+            pu.data_ptr() if want_pre else None, N, wp, wn, st), "beam_moe_gated_linear")
+    return (out, pg, pu) if want_pre else out
+
+
+def beam_moe_gated_linear_backward(dh: torch.Tensor, x: Optional[torch.Tensor], w_gate: Optional[torch.Tensor],
+                                   w_up: Optional[torch.Tensor], pre_gate: torch.Tensor, pre_up: torch.Tensor, *,
+                                   act: str = "silu", want_dx: bool = True, want_dw: bool = True,
+                                   want_dbias: bool = True, ws: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of beam_moe_gated_linear from dh [M, N] (x's type or fp32) and both of its pre. Returns (dx, dw_gate,
+    dw_up, dbias_gate, dbias_up), None for those not wanted. x may be None without want_dw, both weights without
+    want_dx; one of them is needed for the width."""
+    if want_dw and x is None or want_dx and (w_gate is None or w_up is None) or x is None and w_gate is None:
+        raise ValueError("x is needed for dw, both weights for dx, and x or w_gate for the width")
+    M, N, dev = _mat(dh, "dh")
+    K, dt = (x if x is not None else w_gate).shape[-1], (x if x is not None else w_gate).dtype
+    if dt not in _HALF:
+        raise ValueError(f"x and the weights must be one of {_HALF}, got {dt}")
+    ldx = K if x is None else _rows(x, "x", _HALF, (M, K), dev)
+    ldg = K if w_gate is None else _rows(w_gate, "w_gate", (dt,), (N, K), dev)
+    ldu = K if w_up is None else _rows(w_up, "w_up", (dt,), (N, K), dev)
+    lddh = _rows(dh, "dh", (dt, _F32), (M, N), dev)
+    ldpg, ldpu = _rows(pre_gate, "pre_gate", (dt,), (M, N), dev), _rows(pre_up, "pre_up", (dt,), (M, N), dev)
+    a = _act(act)
+    with _On(dev, stream) as st:
+        dx = torch.empty(M, K, dtype=dt, device=dev) if want_dx else None
+        dwg = torch.empty(N, K, dtype=dt, device=dev) if want_dw else None
+        dwu = torch.empty_like(dwg) if want_dw else None
+        dbg = torch.empty(N, dtype=_F32, device=dev) if want_dbias else None
+        dbu = torch.empty_like(dbg) if want_dbias else None
+        wp, wn, _keep = _scratch(_linear_ws("beam_moe_gated_linear_backward_workspace_bytes", M, N, K, ldx, ldg, ldu),
+                                 ws, dev, "beam_moe_gated_linear_backward")
+        _check(load_library().beam_moe_gated_linear_backward(
+            M, N, K, ELEM_TYPES[dt], dh.data_ptr(), ELEM_TYPES[dh.dtype], lddh, None if x is None else x.data_ptr(),
+            ldx, None if w_gate is None else w_gate.data_ptr(), ldg, None if w_up is None else w_up.data_ptr(), ldu,
+            pre_gate.data_ptr(), ldpg, pre_up.data_ptr(), ldpu, a, dx.data_ptr() if want_dx else None, K,
+            dwg.data_ptr() if want_dw else None, K, dwu.data_ptr() if want_dw else None, K,
+            dbg.data_ptr() if want_dbias else None, dbu.data_ptr() if want_dbias else None, wp, wn, st),
+            "beam_moe_gated_linear_backward")
+    return dx, dwg, dwu, dbg, dbu
+
+
 def _dense(t: torch.Tensor) -> bool:
     """Whether t's elements fill one stretch of memory: contiguous, or a matrix's transpose."""
     return t.is_contiguous() or (t.dim() == 2 and t.t().is_contiguous())

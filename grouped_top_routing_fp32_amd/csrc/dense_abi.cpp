@@ -1,20 +1,25 @@
-// C ABI of the operators of a dense gated sublayer, trained and served (the norm of all gradients and their
-// clipping, microscaled 4-bit floating point): argument validation, workspace carving and
-// kernel launches on the caller's stream.  The operations and conventions are stated in include/beam_moe.h.
+// C ABI of the operators of a dense gated sublayer, trained and served (the gated projections and their
+// gradients, the norm of all gradients and their clipping, microscaled 4-bit floating point): argument validation,
+// workspace carving and kernel launches on the caller's stream.  The operations and conventions are stated in include/beam_moe.h.
 #include <algorithm>
 #include <cmath>
 #include <new>
 #include <vector>
 
 #include "abi_util.h"
+#include "gated.h"
 #include "grads.h"
 #include "mxfp4.h"
 
 namespace {
 
+using beam::act_ok;
+using beam::align_up;
 using beam::aligned16;
+using beam::at;
 using beam::check_optional;
 using beam::check_ptrs;
+using beam::half_type;
 using beam::hip_status;
 using beam::ld_ok;
 using beam::type_ok;
@@ -75,9 +80,182 @@ bool mx_rows_ok(int64_t cols, int64_t ldc, int64_t lds) {
   return ldc % 16 == 0 && ld_ok(ldc, 16 * blocks) && ld_ok(lds, blocks);
 }
 
+constexpr int32_t kMaxGatedRows = 1 << 20;
+constexpr int32_t kMaxGatedCols = 1 << 17;  // both projections' are those of one product
+constexpr int32_t kMaxGatedInner = 1 << 18;
+
+int check_gated(int32_t rows, int32_t cols, int32_t inner) {
+  if (rows < 0) return BEAM_MOE_ERR_INVALID_ARG;
+  return rows > kMaxGatedRows || cols < 1 || cols > kMaxGatedCols || inner < 1 || inner > kMaxGatedInner
+             ? BEAM_MOE_ERR_UNSUPPORTED
+             : BEAM_MOE_OK;
+}
+
+// Workspace of the gated backward pass: both dz, the partial sums of the bias gradients, the inverse of an fp16
+// dz's scale with the maxima that give it, the operands that are laid out anew, then the partial sums of the two
+// products, in the same place unless they run in one launch.
+struct GatedBackwardPlan {
+  size_t off_part, off_scale, off_gate, off_up, off_x, off_gemm, total;
+  bool copy_gate, copy_up, copy_x;
+  beam::GemmPlan dx, dw;
+};
+
+constexpr size_t kScaleBytes = 256;  // before the maxima
+
+GatedBackwardPlan gated_backward_plan(int32_t rows, int32_t cols, int32_t inner, int64_t ldx, int64_t ldg, int64_t ldu) {
+  GatedBackwardPlan p;
+  const int wide = 2 * beam::gated_half(cols);
+  p.copy_gate = !beam::regular_rows(ldg, inner);
+  p.copy_up = !beam::regular_rows(ldu, inner);
+  p.copy_x = !beam::regular_rows(ldx, inner);
+  beam::plan_gradients(rows, wide, inner, &p.dx, &p.dw);
+  p.off_part = align_up((size_t)rows * wide * 2);
+  p.off_scale = p.off_part + align_up((size_t)beam::gated_dz_units(rows) * 2 * cols * sizeof(float));
+  p.off_gate = p.off_scale + kScaleBytes + align_up(beam::gated_peak_bytes());
+  p.off_up = p.off_gate + align_up(p.copy_gate ? beam::padded_bytes(cols, inner) : 0);
+  p.off_x = p.off_up + align_up(p.copy_up ? beam::padded_bytes(cols, inner) : 0);
+  p.off_gemm = p.off_x + align_up(p.copy_x ? beam::padded_bytes(rows, inner) : 0);
+  p.total = p.off_gemm + (p.dx.paired ? p.dx.total + p.dw.total : std::max(p.dx.total, p.dw.total));
+  return p;
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t beam_moe_gated_linear_workspace_bytes(int32_t rows, int32_t cols, int32_t inner, int64_t ldx, int64_t ldg,
+                                             int64_t ldu) {
+  if (check_gated(rows, cols, inner) != BEAM_MOE_OK || !ld_ok(ldx, inner) || !ld_ok(ldg, inner) || !ld_ok(ldu, inner))
+    return SIZE_MAX;
+  return beam::plan_gated(rows, cols, inner, ldx, ldg, ldu).total;
+}
+
+int beam_moe_gated_linear(int32_t rows, int32_t cols, int32_t inner, int type, const void* x, int64_t ldx,
+                          const void* w_gate, int64_t ldg, const void* w_up, int64_t ldu, const float* bias_gate,
+                          const float* bias_up, int act, void* h, int h_type, int64_t ldh, void* pre_gate,
+                          int64_t ldpg, void* pre_up, int64_t ldpu, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_gated(rows, cols, inner);
+  if (rc != BEAM_MOE_OK) return rc;
+  if (!half_type(type) || (h_type != type && h_type != BEAM_MOE_F32) || !act_ok(act)) return BEAM_MOE_ERR_INVALID_ARG;
+  if (rows == 0) return BEAM_MOE_OK;
+  if (!ld_ok(ldx, inner) || !ld_ok(ldg, inner) || !ld_ok(ldu, inner) || !ld_ok(ldh, cols) ||
+      (pre_gate && !ld_ok(ldpg, cols)) || (pre_up && !ld_ok(ldpu, cols)))
+    return BEAM_MOE_ERR_INVALID_ARG;
+  if ((rc = check_ptrs({x, w_gate, w_up, h})) != BEAM_MOE_OK) return rc;
+  if ((rc = check_optional({bias_gate, bias_up, pre_gate, pre_up})) != BEAM_MOE_OK) return rc;
+  const beam::GatedPlan plan = beam::plan_gated(rows, cols, inner, ldx, ldg, ldu);
+  if (plan.total && (!ws || !aligned16(ws) || ws_bytes < plan.total)) return BEAM_MOE_ERR_WORKSPACE;
+  beam::GatedArgs g{};
+  g.a = x;
+  g.lda = ldx;
+  g.b = w_gate;
+  g.ldb = ldg;
+  g.b2 = w_up;
+  g.ldb2 = ldu;
+  g.M = rows;
+  g.N = cols;
+  g.K = inner;
+  g.type = type;
+  g.bias = bias_gate;
+  g.bias2 = bias_up;
+  g.act = act;
+  g.out = h;
+  g.out_type = h_type;
+  g.ldo = ldh;
+  g.pre = pre_gate;
+  g.ldp = ldpg;
+  g.pre2 = pre_up;
+  g.ldp2 = ldpu;
+  return hip_status(beam::launch_gated(g, plan, ws, static_cast<hipStream_t>(stream)));
+}
+
+size_t beam_moe_gated_linear_backward_workspace_bytes(int32_t rows, int32_t cols, int32_t inner, int64_t ldx,
+                                                      int64_t ldg, int64_t ldu) {
+  if (check_gated(rows, cols, inner) != BEAM_MOE_OK || !ld_ok(ldx, inner) || !ld_ok(ldg, inner) || !ld_ok(ldu, inner))
+    return SIZE_MAX;
+  return gated_backward_plan(rows, cols, inner, ldx, ldg, ldu).total;
+}
+
+int beam_moe_gated_linear_backward(int32_t rows, int32_t cols, int32_t inner, int type, const void* dh, int dh_type,
+                                   int64_t lddh, const void* x, int64_t ldx, const void* w_gate, int64_t ldg,
+                                   const void* w_up, int64_t ldu, const void* pre_gate, int64_t ldpg,
+                                   const void* pre_up, int64_t ldpu, int act, void* dx, int64_t lddx, void* dw_gate,
+                                   int64_t lddwg, void* dw_up, int64_t lddwu, float* dbias_gate, float* dbias_up,
+                                   void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_gated(rows, cols, inner);
+  if (rc != BEAM_MOE_OK) return rc;
+  if (!half_type(type) || (dh_type != type && dh_type != BEAM_MOE_F32) || !act_ok(act) || !dw_gate != !dw_up ||
+      !dbias_gate != !dbias_up || (!dx && !dw_gate && !dbias_gate))
+    return BEAM_MOE_ERR_INVALID_ARG;
+  if ((rc = check_optional({x, w_gate, w_up, dx, dw_gate, dw_up, dbias_gate, dbias_up})) != BEAM_MOE_OK) return rc;
+  if ((dx && !ld_ok(lddx, inner)) || (dw_gate && (!ld_ok(lddwg, inner) || !ld_ok(lddwu, inner))))
+    return BEAM_MOE_ERR_INVALID_ARG;
+  if (rows > 0) {
+    if ((rc = check_ptrs({dh, pre_gate, pre_up})) != BEAM_MOE_OK) return rc;
+    if ((dx && (!w_gate || !w_up)) || (dw_gate && !x) || !ld_ok(lddh, cols) || !ld_ok(ldpg, cols) ||
+        !ld_ok(ldpu, cols) || (x && !ld_ok(ldx, inner)) || (w_gate && !ld_ok(ldg, inner)) || (w_up && !ld_ok(ldu, inner)))
+      return BEAM_MOE_ERR_INVALID_ARG;
+  }
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const GatedBackwardPlan p =
+      gated_backward_plan(rows, cols, inner, x ? ldx : inner, w_gate ? ldg : inner, w_up ? ldu : inner);
+  if (rows > 0 && (!ws || !aligned16(ws) || ws_bytes < p.total)) return BEAM_MOE_ERR_WORKSPACE;
+  const int half = beam::gated_half(cols), units = rows > 0 ? beam::gated_dz_units(rows) : 0;
+  float* part = dbias_gate ? at<float>(ws, p.off_part) : nullptr;
+  const bool products = dx || dw_gate, scaled = products && type == BEAM_MOE_F16 && rows > 0;
+  float* unscale = scaled ? at<float>(ws, p.off_scale) : nullptr;
+  uint16_t* dz = products ? at<uint16_t>(ws, 0) : nullptr;
+  beam::PadJob jg{}, ju{}, jx{};
+  auto copy = [&](beam::PadJob& j, const void*& m, int64_t& ld, int n, size_t off) {
+    j = {m, ld, n, inner, at<void*>(ws, off)};
+    m = j.dst;
+    ld = beam::up8(inner);
+  };
+  if (rows > 0) {
+    if (dx && p.copy_gate) copy(jg, w_gate, ldg, cols, p.off_gate);
+    if (dx && p.copy_up) copy(ju, w_up, ldu, cols, p.off_up);
+    if (dw_gate && p.copy_x) copy(jx, x, ldx, rows, p.off_x);
+    if ((rc = hip_status(beam::launch_pad(jg, ju, st))) != BEAM_MOE_OK) return rc;
+    if ((rc = hip_status(beam::launch_pad(jx, {}, st))) != BEAM_MOE_OK) return rc;
+    beam::GatedDz d{dh,   dh_type, lddh, pre_gate, pre_up, ldpg, ldpu, act, type, at<uint32_t>(ws, p.off_scale + kScaleBytes),
+                    unscale, dz, part, rows, cols};
+    if ((rc = hip_status(beam::launch_gated_dz(d, st))) != BEAM_MOE_OK) return rc;
+  }
+  beam::GatedArgs gx{}, gw{};
+  gx.type = gx.out_type = gw.type = gw.out_type = type;
+  gx.add = gw.add = 1.f;
+  gx.add_at = gw.add_at = unscale;
+  gx.a = gw.a = dz;
+  gx.lda = gw.lda = 2 * half;
+  gx.half = gw.half = half;
+  gx.valid = gw.valid = cols;
+  gx.b = w_gate;
+  gx.ldb = ldg;
+  gx.b2 = w_up;
+  gx.ldb2 = ldu;
+  gx.bt = true;
+  gx.M = rows;
+  gx.N = inner;
+  gx.K = 2 * half;
+  gx.out = rows > 0 ? dx : nullptr;
+  gx.ldo = lddx;
+  gw.b = x;
+  gw.ldb = ldx;
+  gw.at = gw.bt = true;
+  gw.M = 2 * half;
+  gw.N = inner;
+  gw.K = rows;
+  gw.out = dw_gate;
+  gw.ldo = lddwg;
+  gw.out2 = dw_up;
+  gw.ldo2 = lddwu;
+  const beam::SumJob sums{part, dbias_gate, units, 2 * cols, dbias_up};
+  if (gx.out)
+    gx.sums = sums;
+  else if (dbias_gate && (rc = hip_status(beam::launch_gated_sums(sums, st))) != BEAM_MOE_OK)
+    return rc;
+  return hip_status(beam::launch_gated_gradients(gx, p.dx, gw, p.dw, at<void>(ws, p.off_gemm), st));
+}
 
 size_t beam_moe_grad_norm_workspace_bytes(int32_t count) {
   if (count < 0 || count > kMaxGrads) return SIZE_MAX;

@@ -1,4 +1,4 @@
-// The tiled MFMA product of linear.hip, instantiated once for each 16-bit type.
+// The tiled MFMA product of linear.hip and gated.hip, instantiated once for each 16-bit type.
 #pragma once
 
 #include <type_traits>
@@ -57,6 +57,20 @@ struct Side {
         src[q] = static_cast<const uint16_t*>(base) + (int64_t)min(i0 + r, ni - 1) * ld + k0 + 8 * c;
     }
     step = TR ? kBK * ld : kBK;
+  }
+
+  // Rows of two matrices of ni rows each, 16 of the first and then 16 of the second in turn, R / 2 of
+  // both from row i0 on.  A copy's 8 rows are of one of them.
+  __device__ __forceinline__ void init_pair(const void* first, int64_t ld1, const void* second, int64_t ld2, int i0,
+                                            int ni, int k0, int wave, int lane) {
+    static_assert(!TR, "rows of K alone");
+#pragma unroll
+    for (int q = 0; q < kCopies; ++q) {
+      const int r = row(q, wave, lane), c = chunk(r, lane), i = min(i0 + (r >> 5) * 16 + (r & 15), ni - 1);
+      const bool other = r & 16;
+      src[q] = static_cast<const uint16_t*>(other ? second : first) + (int64_t)i * (other ? ld2 : ld1) + k0 + 8 * c;
+    }
+    step = kBK;
   }
 
   // Copies a stage of which `left` K remain and moves on to the next.
@@ -133,14 +147,93 @@ __device__ __forceinline__ int xcd_lin(int b, int total) {
 // start of step t and waited for at its end; they are issued and waited for by hand
 // (the compiler's own tracking drains them at every loop head).
 // The mfma's first operand is B's: a lane then holds four consecutive columns of a row.
+// GatedArgs: the products of a gated layer.  Forward, a tile's B rows are those of both weights in turn, BN / 2
+// columns of the result; in dx, K runs over the first half's columns and then the second's; in dw, the
+// result's rows are the first half's and then the second's.
 // lin is the tile's place in the order of all of them, split after split; ring holds
 // kRing<BM, BN> elements of LDS.
 template <int BM, int BN>
 constexpr int kRing = 2 * (BM + BN) * kBK;
 
-template <bool HALF, bool AT, bool BT, int BM, int BN, int WM, int WN, bool EPI, bool REGS = false>
-__device__ __forceinline__ void gemm_tile(uint16_t* ring, GemmArgs g, int mt, int nt, int lin, int k_per_split,
+// Result and, in training, both arguments of a gated layer from a tile's sums, or the sums themselves where K is
+// split.  A lane holds gate and up of the same elements, so the product is formed in registers, and one
+// plane of BM x BN / 2 FP32 at a time goes through the ring to leave in whole lines.
+template <bool HALF, int BM, int BN, int WM, int WN>
+__device__ __forceinline__ void gated_epilogue(uint16_t* ring, const GatedArgs& g, f32x4 (&acc)[BM / WM / 16][BN / WN / 16],
+                                               int m0, int n0, int split, float* __restrict__ part, int64_t ldpart) {
+  constexpr int NW = WM * WN, FI = BM / WM / 16, FP = BN / WN / 32;  // pairs of fragments
+  constexpr int kQuads = BN / 8, kRowsAtOnce = 64 * NW / kQuads, kMask = kQuads < 16 ? kQuads - 1 : 15;
+  static_assert(BM * BN * 2 <= kRing<BM, BN> * 2, "a plane fits the ring");
+  f32x4* plane = reinterpret_cast<f32x4*>(ring);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const int c0 = wn * (BN / WN) / 8 + (lane >> 4), r0 = wm * (BM / WM) + (lane & 15);  // quad and row of this lane
+  const int qn = tid % kQuads, qr = tid / kQuads, n = n0 + 4 * qn;
+  const int rmax = n < g.N ? min(BM, g.M - m0) : 0;
+  // value(i, j) to `to`, an array of `type` whose row m0 starts at `row0`
+  auto put = [&](auto value, void* to, int type, int64_t row0, int64_t ld, int end) __attribute__((always_inline)) {
+    __syncthreads();  // everyone is done with the stages, or with the last plane
+#pragma unroll
+    for (int i = 0; i < FI; ++i)
+#pragma unroll
+      for (int j = 0; j < FP; ++j) {
+        const int r = r0 + 16 * i, c = c0 + 4 * j;
+        plane[r * kQuads + (c ^ (r & kMask))] = value(i, j);
+      }
+    __syncthreads();
+#pragma unroll 4
+    for (int r = qr; r < rmax; r += kRowsAtOnce) {
+      const f32x4 v = plane[r * kQuads + (qn ^ (r & kMask))];
+      const int64_t at = row0 + r * ld + n;
+      if (n + 4 <= end) {
+        store_elem4(to, at, type, v);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (n + q < end) store_elem(to, at + q, type, v[q]);
+      }
+    }
+  };
+  if (part) {  // ldpart holds both halves, each a multiple of four columns
+    const int64_t row0 = ((int64_t)split * g.M + m0) * ldpart;
+    const int end = (int)(ldpart / 2);
+    put([&](int i, int j) { return acc[i][2 * j]; }, part, kElemF32, row0, ldpart, end);
+    put([&](int i, int j) { return acc[i][2 * j + 1]; }, part + ldpart / 2, kElemF32, row0, ldpart, end);
+    return;
+  }
+  auto bias = [&](const float* b, int which) __attribute__((always_inline)) {
+    if (!b) return;
+#pragma unroll
+    for (int j = 0; j < FP; ++j) {
+      const int at = n0 + 4 * (c0 + 4 * j);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float v = at + q < g.N ? b[at + q] : 0.f;
+#pragma unroll
+        for (int i = 0; i < FI; ++i) acc[i][2 * j + which][q] += v;
+      }
+    }
+  };
+  bias(g.bias, 0);
+  bias(g.bias2, 1);
+  by_act(g.act, [&](auto act) __attribute__((always_inline)) {
+    put(
+        [&](int i, int j) __attribute__((always_inline)) {
+          f32x4 v;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[q] = act_f32<decltype(act)::value>(acc[i][2 * j][q]) * acc[i][2 * j + 1][q];
+          return v;
+        },
+        g.out, g.out_type, m0 * g.ldo, g.ldo, g.N);
+  });
+  if (g.pre) put([&](int i, int j) { return acc[i][2 * j]; }, g.pre, g.type, m0 * g.ldp, g.ldp, g.N);
+  if (g.pre2) put([&](int i, int j) { return acc[i][2 * j + 1]; }, g.pre2, g.type, m0 * g.ldp2, g.ldp2, g.N);
+}
+
+template <bool HALF, bool AT, bool BT, int BM, int BN, int WM, int WN, bool EPI, bool REGS = false, class G = GemmArgs>
+__device__ __forceinline__ void gemm_tile(uint16_t* ring, G g, int mt, int nt, int lin, int k_per_split,
                                           float* __restrict__ part, int64_t ldpart) {
+  constexpr bool kGated = std::is_same_v<G, GatedArgs>;
   constexpr int NW = WM * WN, FI = BM / WM / 16, FJ = BN / WN / 16;
   constexpr int kSlot = (BM + BN) * kBK;
   lds_u16* lds = (lds_u16*)ring;
@@ -149,17 +242,29 @@ __device__ __forceinline__ void gemm_tile(uint16_t* ring, GemmArgs g, int mt, in
   const int tiles = mt * nt;
   const int split = lin / tiles, t = lin % tiles;
   const int group = t / (8 * nt), in = t % (8 * nt), rows = min(8, mt - 8 * group);
-  const int m0 = (8 * group + in % rows) * BM, n0 = in / rows * BN;
+  const int m0 = (8 * group + in % rows) * BM, n0 = in / rows * (kGated && EPI ? BN / 2 : BN);
   const int k0 = split * k_per_split, k1 = min(g.K, k0 + k_per_split);
 
   Side<AT, BM, NW> sa;
   Side<BT, BN, NW> sb;
   sa.init(g.a, g.lda, m0, g.M, k0, wave, lane);
-  sb.init(g.b, g.ldb, n0, g.N, k0, wave, lane);
+  if constexpr (kGated && EPI)
+    sb.init_pair(g.b, g.ldb, g.b2, g.ldb2, n0, g.N, k0, wave, lane);
+  else if constexpr (kGated && !AT)
+    sb.init(g.b, g.ldb, n0, g.N, min(k0, g.half - kBK), wave, lane);  // of the first half; the second's follows
+  else
+    sb.init(g.b, g.ldb, n0, g.N, k0, wave, lane);
   f32x4 acc[FI][FJ] = {};
-  auto issue = [&](int slot, int left) {
+  auto issue = [&](int slot, int t) {
+    const int left = k1 - k0 - t * kBK;
     sa.issue(lds + slot * kSlot, left, wave, lane);
-    sb.issue(lds + slot * kSlot + BM * kBK, left, wave, lane);
+    if constexpr (kGated && !EPI && !AT) {
+      const int k = k0 + t * kBK, in_half = k < g.half ? k : k - g.half;
+      if (k == g.half || (t == 0 && k > g.half)) sb.init(g.b2, g.ldb2, n0, g.N, in_half, wave, lane);
+      sb.issue(lds + slot * kSlot + BM * kBK, g.valid - in_half, wave, lane);
+    } else {
+      sb.issue(lds + slot * kSlot + BM * kBK, left, wave, lane);
+    }
   };
   auto compute = [&](int slot) __attribute__((always_inline)) {
     const lds_u16* A = lds + slot * kSlot;
@@ -232,13 +337,18 @@ __device__ __forceinline__ void gemm_tile(uint16_t* ring, GemmArgs g, int mt, in
       }
     }
   } else {
-    if (stages > 0) issue(0, k1 - k0);
+    if (stages > 0) issue(0, 0);
     for (int st = 0; st < stages; ++st) {
       __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
       barrier();
-      if (st + 1 < stages) issue((st + 1) & 1, k1 - k0 - (st + 1) * kBK);
+      if (st + 1 < stages) issue((st + 1) & 1, st + 1);
       compute(st & 1);
     }
+  }
+
+  if constexpr (kGated && EPI) {
+    gated_epilogue<HALF, BM, BN, WM, WN>(ring, g, acc, m0, n0, split, part, ldpart);
+    return;
   }
 
   // Epilogue through LDS: FP32 sums in the ring (WM / kPasses wave rows at a time), then
@@ -353,29 +463,10 @@ __device__ __forceinline__ void gemm_tile(uint16_t* ring, GemmArgs g, int mt, in
   }
 }
 
-// The column sums that run beside dx's product, in workgroups behind its tiles: b's are those
-// of 16 columns, thread (c, g) adds the rows g, g + 16, ... of column c, and a column's 16
-// sums are added in order, in FP64.  As a launch of their own they take 3 to 5 us, mostly
-// latency.
-__device__ __forceinline__ void sum_columns(float* s, const SumJob& j, int b) {
-  const int tid = threadIdx.x, c = tid & 15, h = b * 16 + c;
-  float v = 0.f;
-  if (tid < 256 && h < j.cols)
-#pragma unroll 16
-    for (int u = tid >> 4; u < j.units; u += 16) v += j.part[(int64_t)u * j.cols + h];
-  s[tid] = v;
-  __syncthreads();
-  if (tid < 16 && h < j.cols) {
-    double a = 0.0;
-#pragma unroll
-    for (int g = 0; g < 16; ++g) a += s[16 * g + c];
-    j.out[h] = (float)a;
-  }
-}
 inline int sum_groups(const SumJob& j) { return j.out ? (j.cols + 15) / 16 : 0; }
 
-template <bool HALF, bool AT, bool BT, int BM, int BN, int WM, int WN, bool EPI, bool REGS = false>
-__global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(GemmArgs g, int mt, int nt, int total, int k_per_split,
+template <bool HALF, bool AT, bool BT, int BM, int BN, int WM, int WN, bool EPI, bool REGS = false, class G = GemmArgs>
+__global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(G g, int mt, int nt, int total, int k_per_split,
                                                             float* __restrict__ part, int64_t ldpart) {
   __shared__ __align__(1024) uint16_t ring[kRing<BM, BN>];
   if constexpr (BT && !AT)
@@ -387,8 +478,8 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(GemmArgs g, int mt, i
 // dx = dz w and dw = dz^T x in one launch, where neither fills the card alone.  Those
 // with the longer K come first.  (In 256-row tiles nothing is gained: 429 us either way at [8192,
 // 5120] x [2560, 5120], 640 and 200 tiles, although fewer CUs idle.)
-template <bool HALF, int TILE>
-__global__ __launch_bounds__(256) void gemm_pair_kernel(GemmArgs dx, GemmSplit sx, GemmArgs dw, GemmSplit sw) {
+template <bool HALF, int TILE, class G>
+__global__ __launch_bounds__(256) void gemm_pair_kernel(G dx, GemmSplit sx, G dw, GemmSplit sw) {
   __shared__ __align__(1024) uint16_t ring[kRing<TILE, TILE>];
   const int mx = (dx.M + TILE - 1) / TILE, nx = (dx.N + TILE - 1) / TILE;
   const int mw = (dw.M + TILE - 1) / TILE, nw = (dw.N + TILE - 1) / TILE;
@@ -405,20 +496,20 @@ __global__ __launch_bounds__(256) void gemm_pair_kernel(GemmArgs dx, GemmSplit s
     sum_columns(reinterpret_cast<float*>(ring), dx.sums, b - first - second);
 }
 
-template <bool HALF, int TILE>
-hipError_t launch_gemm_pair(const GemmArgs& dx, const GemmSplit& sx, const GemmArgs& dw, const GemmSplit& sw,
-                            hipStream_t st) {
+template <bool HALF, int TILE, class G>
+hipError_t launch_gemm_pair(const G& dx, const GemmSplit& sx, const G& dw, const GemmSplit& sw, hipStream_t st) {
   auto tiles = [](const GemmArgs& g) { return ((g.M + TILE - 1) / TILE) * ((g.N + TILE - 1) / TILE); };
-  hipLaunchKernelGGL((gemm_pair_kernel<HALF, TILE>),
+  hipLaunchKernelGGL((gemm_pair_kernel<HALF, TILE, G>),
                      dim3(tiles(dx) * sx.splits + tiles(dw) * sw.splits + sum_groups(dx.sums)), dim3(256), 0, st, dx,
                      sx, dw, sw);
   return hipGetLastError();
 }
 
 // Launches the tiles of g's layout (A transposed implies B transposed).
-template <bool HALF>
-hipError_t launch_gemm_tiles(const GemmArgs& g, const GemmSplit& s, int tile, hipStream_t st) {
-  const int mt = (g.M + tile - 1) / tile, nt = (g.N + tile - 1) / tile;
+template <bool HALF, class G>
+hipError_t launch_gemm_tiles(const G& g, const GemmSplit& s, int tile, hipStream_t st) {
+  const int wide = std::is_same_v<G, GatedArgs> && !g.bt ? tile / 2 : tile;  // columns
+  const int mt = (g.M + tile - 1) / tile, nt = (g.N + wide - 1) / wide;
   const int total = mt * nt * s.splits;
   const dim3 grid(total + sum_groups(g.sums));
   auto go = [&](auto kernel, int threads) {
@@ -426,21 +517,21 @@ hipError_t launch_gemm_tiles(const GemmArgs& g, const GemmSplit& s, int tile, hi
     return hipGetLastError();
   };
   if (tile == 256) {
-    if (!g.at && !g.bt) return go(gemm_kernel<HALF, false, false, 256, 256, 4, 2, true>, 512);
-    if (!g.at) return go(gemm_kernel<HALF, false, true, 256, 256, 4, 2, false>, 512);
-    return go(gemm_kernel<HALF, true, true, 256, 256, 4, 2, false>, 512);
+    if (!g.at && !g.bt) return go(gemm_kernel<HALF, false, false, 256, 256, 4, 2, true, false, G>, 512);
+    if (!g.at) return go(gemm_kernel<HALF, false, true, 256, 256, 4, 2, false, false, G>, 512);
+    return go(gemm_kernel<HALF, true, true, 256, 256, 4, 2, false, false, G>, 512);
   }
   if (g.regs)  // neither operand transposed
-    return tile == 128 ? go(gemm_kernel<HALF, false, false, 128, 128, 2, 2, true, true>, 256)
-                       : go(gemm_kernel<HALF, false, false, 64, 64, 2, 2, true, true>, 256);
+    return tile == 128 ? go(gemm_kernel<HALF, false, false, 128, 128, 2, 2, true, true, G>, 256)
+                       : go(gemm_kernel<HALF, false, false, 64, 64, 2, 2, true, true, G>, 256);
   if (tile == 128) {
-    if (!g.at && !g.bt) return go(gemm_kernel<HALF, false, false, 128, 128, 2, 2, true>, 256);
-    if (!g.at) return go(gemm_kernel<HALF, false, true, 128, 128, 2, 2, false>, 256);
-    return go(gemm_kernel<HALF, true, true, 128, 128, 2, 2, false>, 256);
+    if (!g.at && !g.bt) return go(gemm_kernel<HALF, false, false, 128, 128, 2, 2, true, false, G>, 256);
+    if (!g.at) return go(gemm_kernel<HALF, false, true, 128, 128, 2, 2, false, false, G>, 256);
+    return go(gemm_kernel<HALF, true, true, 128, 128, 2, 2, false, false, G>, 256);
   }
-  if (!g.at && !g.bt) return go(gemm_kernel<HALF, false, false, 64, 64, 2, 2, true>, 256);
-  if (!g.at) return go(gemm_kernel<HALF, false, true, 64, 64, 2, 2, false>, 256);
-  return go(gemm_kernel<HALF, true, true, 64, 64, 2, 2, false>, 256);
+  if (!g.at && !g.bt) return go(gemm_kernel<HALF, false, false, 64, 64, 2, 2, true, false, G>, 256);
+  if (!g.at) return go(gemm_kernel<HALF, false, true, 64, 64, 2, 2, false, false, G>, 256);
+  return go(gemm_kernel<HALF, true, true, 64, 64, 2, 2, false, false, G>, 256);
 }
 
 }  // namespace beam

@@ -16,6 +16,13 @@ struct SumJob {
   const float* part;
   float* out;
   int units, cols;
+  float* out2;  // the sums of the second half of the columns; null: all go to out
+  __device__ void put(int h, float v) const {
+    if (out2 && 2 * h >= cols)
+      out2[h - cols / 2] = v;
+    else
+      out[h] = v;
+  }
 };
 
 // out[m, n] = keep res[m, n] + add act(sum_k a(m, k) b(n, k) + bias[n]), pre[m, n] = the
@@ -43,6 +50,28 @@ struct GemmArgs {
   SumJob sums;  // runs beside a product of transposed b alone (dx)
 };
 
+// The products of a gated layer.  Forward: b and b2 are both weights, the result act(a b + bias) (a b2 + bias2),
+// N its columns, pre and pre2 the two sums.  dx = dz_gate w_gate + dz_up w_up: a holds `half` columns (a multiple of
+// 64, zeros past the `valid` of them that are a weight's rows) of dz_gate and then of dz_up, K is 2 half.
+// dw: a transposed is the same, out the first half's rows and out2 the second's, `valid` of each.
+struct GatedArgs : GemmArgs {
+  const void* b2;
+  int64_t ldb2;
+  const float* bias2;
+  void* pre2;
+  int64_t ldp2;
+  void* out2;
+  int64_t ldo2;
+  int half, valid;
+};
+
+// Up to here the skinny kernel: 2560 columns, K 5120: 10.4 us at 16 rows against 12.7 in
+// tiles; a form of it for 32 rows took 15.9 against 12.8.
+constexpr int kSkinnyRows = 16;
+constexpr int kSkinnyWaves = 16;
+// Workgroups that look for the largest element of an fp16 gradient, at most.
+constexpr int kMaxPeaks = 1024;
+
 // How a product runs: which kernel, and the workspace it needs (bytes from its start).
 struct GemmPlan {
   enum Kind { kSkinny, kTiles } kind;
@@ -61,7 +90,9 @@ struct GemmSplit {
   int splits, k_per_split;
 };
 // Operand shapes and leading dimensions decide alone, so a size query and its call agree.
+GemmPlan plan_tiles(int M, int N, int K);  // rows are whole chunks on 16 bytes
 GemmPlan plan_linear(int M, int N, int K, int64_t ldx, int64_t ldw);
+GemmSplit split_of(const GemmPlan& p, int N, char* base);
 hipError_t launch_gemm(const GemmArgs& g, const GemmPlan& p, void* ws, hipStream_t st);
 // Both gradients' products, planned together.  Where they are paired (run in one launch) their workspaces lie one
 // behind the other, dx's first, else in the same place.
@@ -77,6 +108,7 @@ struct PadJob {
   int rows, cols;  // rows 0: nothing to do
   void* dst;
 };
+inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 inline int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
 // Whether the tiled kernel's copies can take rows as they are: whole chunks of 8 elements on 16 bytes.
 inline bool regular_rows(int64_t ld, int cols) { return ld % 8 == 0 && cols % 8 == 0; }
@@ -84,6 +116,12 @@ inline size_t padded_bytes(int rows, int cols) { return (size_t)rows * up8(cols)
 hipError_t launch_pad(const PadJob& first, const PadJob& second, hipStream_t st);
 hipError_t launch_gemm_bf16(const GemmArgs& g, const GemmSplit& s, int tile, hipStream_t st);
 hipError_t launch_gemm_f16(const GemmArgs& g, const GemmSplit& s, int tile, hipStream_t st);
+hipError_t launch_gated_bf16(const GatedArgs& g, const GemmSplit& s, int tile, hipStream_t st);
+hipError_t launch_gated_f16(const GatedArgs& g, const GemmSplit& s, int tile, hipStream_t st);
+hipError_t launch_gated_pair_bf16(const GatedArgs& dx, const GemmSplit& sx, const GatedArgs& dw, const GemmSplit& sw,
+                                  int tile, hipStream_t st);
+hipError_t launch_gated_pair_f16(const GatedArgs& dx, const GemmSplit& sx, const GatedArgs& dw, const GemmSplit& sw,
+                                 int tile, hipStream_t st);
 hipError_t launch_gemm_pair_bf16(const GemmArgs& dx, const GemmSplit& sx, const GemmArgs& dw, const GemmSplit& sw,
                                  int tile, hipStream_t st);
 hipError_t launch_gemm_pair_f16(const GemmArgs& dx, const GemmSplit& sx, const GemmArgs& dw, const GemmSplit& sw,
@@ -202,6 +240,59 @@ __device__ __forceinline__ void store_elem4(void* p, int64_t i, int type, f32x4 
   *reinterpret_cast<u32x2_any*>(static_cast<uint16_t*>(p) + i) = u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
 }
 
+// The power of two that takes a bound of the finite |dz|, `times` the largest of the values whose
+// bits are in peaks, into [2^14, 2^15).  Between 2^-126 and 2^126, so that its reciprocal is as
+// exact; past those no result fits fp16.  By a whole workgroup of 256.
+__device__ __forceinline__ float dz_scale(const uint32_t* __restrict__ peaks, int count, double times) {
+  __shared__ uint32_t top[4];
+  const int tid = threadIdx.y * 64 + threadIdx.x;
+  uint32_t best = 0;
+#pragma unroll
+  for (int i = 0; i < kMaxPeaks; i += 256)
+    if (i + tid < count) best = max(best, peaks[i + tid]);
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) best = max(best, (uint32_t)__shfl_xor((int)best, off));
+  if (threadIdx.x == 0) top[threadIdx.y] = best;
+  __syncthreads();
+  best = max(max(top[0], top[1]), max(top[2], top[3]));
+  const double bound = times * __uint_as_float(best);  // inside FP64's range
+  if (bound == 0.0) return 1.f;
+  const int e = (int)(__builtin_bit_cast(uint64_t, bound) >> 52) - 1022;  // bound < 2^e
+  return __uint_as_float((uint32_t)(min(max(15 - e, -126), 126) + 127) << 23);
+}
+
+// Eight elements of a row of K from k on, zeros past K.
+__device__ __forceinline__ u32x4 chunk_of_row(const uint16_t* row, int k, int K) {
+  u32x4 v = {0u, 0u, 0u, 0u};
+  if (k + 8 <= K) {
+    v = *reinterpret_cast<const u32x4_any*>(row + k);
+  } else if (k < K) {
+    Raw8<F16> part;  // the bits alone matter
+    part.load_part(row + k, K - k);
+    v = part.w[0];
+  }
+  return v;
+}
+
+// The column sums that run beside dx's product, in workgroups behind its tiles: b's are those
+// of 16 columns, thread (c, g) adds the rows g, g + 16, ... of column c, and a column's 16
+// sums are added in order, in FP64.  As a launch of their own they take 3 to 5 us, mostly
+// latency.
+__device__ __forceinline__ void sum_columns(float* s, const SumJob& j, int b) {
+  const int tid = threadIdx.x, c = tid & 15, h = b * 16 + c;
+  float v = 0.f;
+  if (tid < 256 && h < j.cols)
+#pragma unroll 16
+    for (int u = tid >> 4; u < j.units; u += 16) v += j.part[(int64_t)u * j.cols + h];
+  s[tid] = v;
+  __syncthreads();
+  if (tid < 16 && h < j.cols) {
+    double a = 0.0;
+#pragma unroll
+    for (int g = 0; g < 16; ++g) a += s[16 * g + c];
+    j.put(h, (float)a);
+  }
+}
 // A product's `add`; read once, before its results.
 __device__ __forceinline__ float add_of(const GemmArgs& g) { return g.add_at ? *g.add_at : g.add; }
 
@@ -242,6 +333,22 @@ __device__ __forceinline__ void epilogue4(const GemmArgs& g, float add, int m, i
 }
 
 // The same of a gradient, which has the sums alone.
+__device__ __forceinline__ void gradient4(const GemmArgs& g, float add, int m, int n, f32x4 z);
+
+// A gated layer's: rows of dw belong to either weight, those of dz's filling to none.
+__device__ __forceinline__ void gradient4(const GatedArgs& g, float add, int m, int n, f32x4 z) {
+  GemmArgs of = g;
+  if (g.at) {
+    if (m >= g.half) {
+      m -= g.half;
+      of.out = g.out2;
+      of.ldo = g.ldo2;
+    }
+    if (m >= g.valid) return;
+  }
+  gradient4(of, add, m, n, z);
+}
+
 __device__ __forceinline__ void gradient4(const GemmArgs& g, float add, int m, int n, f32x4 z) {
 #pragma unroll
   for (int q = 0; q < 4; ++q) z[q] *= add;

@@ -45,8 +45,6 @@ __global__ __launch_bounds__(256) void gemm_join_kernel(JoinJob first, JoinJob s
 // pieces of 128, straight from memory into MFMA operands (a wave reads 256 contiguous
 // bytes of a row of w; operand rows past cols repeat the last), and their sums are joined
 // in LDS in wave order.
-constexpr int kSkinnyWaves = 16;
-
 template <bool HALF>
 __global__ __launch_bounds__(64 * kSkinnyWaves) void gemm_skinny_kernel(GemmArgs g, int cols) {
   __shared__ f32x4 sum[kSkinnyWaves][64];
@@ -54,17 +52,7 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void gemm_skinny_kernel(GemmArgs
   const int n0 = blockIdx.x * cols, n1 = min(g.N, n0 + cols);
   const uint16_t* wrow = static_cast<const uint16_t*>(g.b) + (int64_t)min(n0 + l16, n1 - 1) * g.ldb;
   const uint16_t* xrow = static_cast<const uint16_t*>(g.a) + (int64_t)min(l16, g.M - 1) * g.lda;
-  auto chunk = [&](const uint16_t* row, int k) {  // 8 elements from k, 0 past K
-    u32x4 v = {0u, 0u, 0u, 0u};
-    if (k + 8 <= g.K) {
-      v = *reinterpret_cast<const u32x4_any*>(row + k);
-    } else if (k < g.K) {
-      Raw8<F16> part;  // the bits alone matter
-      part.load_part(row + k, g.K - k);
-      v = part.w[0];
-    }
-    return v;
-  };
+  auto chunk = [&](const uint16_t* row, int k) { return chunk_of_row(row, k, g.K); };
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
   // whole pieces without a test, so that all of their loads are in flight together
   int k = 128 * wave;
@@ -130,7 +118,6 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(PadJobs p) { pad_rows(p, 
 // peaks[g] = the bits of the largest finite |dy| in a workgroup's part, for the scale of an fp16
 // dz.  grid ceil(N / 512) * units, block (64, 4), over the rows as in linear_dz_kernel, and behind
 // them the workgroups that lay operands out anew, so that those do not wait for it.
-constexpr int kMaxPeaks = 1024;
 template <class DT>
 __global__ __launch_bounds__(256) void linear_peak_kernel(const typename DT::S* __restrict__ dy, int64_t lddy,
                                                           uint32_t* __restrict__ peaks, int M, int N, int units,
@@ -158,27 +145,6 @@ __global__ __launch_bounds__(256) void linear_peak_kernel(const typename DT::S* 
   if (threadIdx.x == 0) top[y] = best;
   __syncthreads();
   if (threadIdx.x == 0 && y == 0) peaks[blockIdx.x] = max(max(top[0], top[1]), max(top[2], top[3]));
-}
-
-// The power of two that takes a bound of the finite |dz|, 1.13 |add| max |dy| (no activation's
-// slope is larger), into [2^14, 2^15).  Between 2^-126 and 2^126, so that its reciprocal is as
-// exact; past those no result fits fp16.  By a whole workgroup of 256.
-__device__ __forceinline__ float dz_scale(const uint32_t* __restrict__ peaks, int count, float add) {
-  __shared__ uint32_t top[4];
-  const int tid = threadIdx.y * 64 + threadIdx.x;
-  uint32_t best = 0;
-#pragma unroll
-  for (int i = 0; i < kMaxPeaks; i += 256)
-    if (i + tid < count) best = max(best, peaks[i + tid]);
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) best = max(best, (uint32_t)__shfl_xor((int)best, off));
-  if (threadIdx.x == 0) top[threadIdx.y] = best;
-  __syncthreads();
-  best = max(max(top[0], top[1]), max(top[2], top[3]));
-  const double bound = 1.13 * fabs((double)add) * __uint_as_float(best);  // inside FP64's range
-  if (bound == 0.0) return 1.f;
-  const int e = (int)(__builtin_bit_cast(uint64_t, bound) >> 52) - 1022;  // bound < 2^e
-  return __uint_as_float((uint32_t)(min(max(15 - e, -126), 126) + 127) << 23);
 }
 
 // dz[m, n] = add dy act'(z), rounded to the products' 16-bit type (the rounding that a
@@ -209,7 +175,7 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(const typename DT::S* __
   [[maybe_unused]] float up = 1.f;
   if constexpr (std::is_same_v<T, F16>) {
     if (dz) {
-      up = dz_scale(peaks, peak_count, add);
+      up = dz_scale(peaks, peak_count, 1.13 * fabs((double)add));  // no activation's slope is larger than 1.13
       if (blockIdx.x == 0 && threadIdx.x == 0 && y == 0) *unscale = 1.f / up;
     }
   }
@@ -255,10 +221,7 @@ namespace {
 
 constexpr int kBK = 64;  // K per stage of the tiled kernel
 constexpr int kCUs = 256;
-// Up to here the skinny kernel: 2560 columns, K 5120: 10.4 us at 16 rows against 12.7 in
-// tiles; a form of it for 32 rows took 15.9 against 12.8.
-constexpr int kSkinnyRows = 16;
-size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 constexpr int kMaxSplits = 16;
@@ -283,6 +246,8 @@ void split_plan(GemmPlan& p, int s, int K) {
 size_t split_bytes(const GemmPlan& p, int M, int N) {
   return p.splits > 1 ? up256((size_t)p.splits * M * ((N + 3) / 4 * 4) * sizeof(float)) : 0;
 }
+
+}  // namespace
 
 // A product of operands whose rows are whole chunks on 16 bytes.
 GemmPlan plan_tiles(int M, int N, int K) {
@@ -316,7 +281,6 @@ GemmPlan plan_tiles(int M, int N, int K) {
   p.total = split_bytes(p, M, N);
   return p;
 }
-}  // namespace
 
 GemmPlan plan_linear(int M, int N, int K, int64_t ldx, int64_t ldw) {
   if (M <= kSkinnyRows) return GemmPlan{};  // kSkinny
@@ -357,8 +321,8 @@ hipError_t launch_skinny(const GemmArgs& g, hipStream_t st) {
 
 }  // namespace
 
-static GemmSplit split_of(const GemmArgs& g, const GemmPlan& p, char* base) {
-  return {p.splits > 1 ? reinterpret_cast<float*>(base + p.off_part) : nullptr, (g.N + 3) / 4 * 4, p.splits,
+GemmSplit split_of(const GemmPlan& p, int N, char* base) {
+  return {p.splits > 1 ? reinterpret_cast<float*>(base + p.off_part) : nullptr, (N + 3) / 4 * 4, p.splits,
           p.k_per_split};
 }
 
@@ -405,7 +369,7 @@ hipError_t launch_gemm(const GemmArgs& args, const GemmPlan& p, void* ws, hipStr
   if ((e = launch_pad(ja, jb, st)) != hipSuccess) return e;
   if (p.kind == GemmPlan::kSkinny) return launch_skinny(g, st);
   g.regs = p.regs;
-  const GemmSplit s = split_of(g, p, base);
+  const GemmSplit s = split_of(p, g.N, base);
   e = g.type == kElemF16 ? launch_gemm_f16(g, s, p.tile, st) : launch_gemm_bf16(g, s, p.tile, st);
   return e != hipSuccess ? e : launch_join({g, s}, {}, st);
 }
@@ -495,7 +459,7 @@ hipError_t launch_gemm_pair(const GemmArgs& dx, const GemmPlan& px, const GemmAr
     return e != hipSuccess ? e : launch_gemm(dw, pw, ws, st);
   }
   char* base = static_cast<char*>(ws);
-  const GemmSplit sx = split_of(dx, px, base), sw = split_of(dw, pw, base + px.total);
+  const GemmSplit sx = split_of(px, dx.N, base), sw = split_of(pw, dw.N, base + px.total);
   const hipError_t e = dx.type == kElemF16 ? launch_gemm_pair_f16(dx, sx, dw, sw, px.tile, st)
                                            : launch_gemm_pair_bf16(dx, sx, dw, sw, px.tile, st);
   return e != hipSuccess ? e : launch_join({dx, sx}, {dw, sw}, st);

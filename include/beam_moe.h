@@ -457,6 +457,47 @@ int beam_moe_linear_backward(int32_t rows, int32_t cols, int32_t inner, int type
  * the section above hold.
  * ------------------------------------------------------------------------- */
 
+/* Workspace of beam_moe_gated_linear and beam_moe_gated_linear_backward; the leading dimensions are
+ * those of the call.  Return SIZE_MAX for unsupported sizes. */
+size_t beam_moe_gated_linear_workspace_bytes(int32_t rows, int32_t cols, int32_t inner, int64_t ldx, int64_t ldg,
+                                             int64_t ldu);
+size_t beam_moe_gated_linear_backward_workspace_bytes(int32_t rows, int32_t cols, int32_t inner, int64_t ldx,
+                                                      int64_t ldg, int64_t ldu);
+
+/* The two projections of a gated layer with activation and product (with act BEAM_MOE_ACT_SILU the first half of a
+ * SwiGLU sublayer, whose down projection is beam_moe_linear):
+ *   zg = x w_gate^T + bias_gate,  zu = x w_up^T + bias_up,  h = act(zg) * zu
+ *   x             [rows, inner], w_gate and w_up [cols, inner] of `type` (BEAM_MOE_BF16 or _F16)
+ *   bias_gate, bias_up   [cols] fp32, NULL = none
+ *   act           BEAM_MOE_ACT_*
+ *   h             [rows, cols] out, of h_type: `type` or BEAM_MOE_F32
+ *   pre_gate, pre_up   [rows, cols] out, of `type`: zg and zu, what the backward pass reads; NULL = not written
+ * h is formed from the unrounded zg and zu.  0 <= rows <= 2^20, 1 <= cols <= 2^17, 1 <= inner <= 2^18. */
+int beam_moe_gated_linear(int32_t rows, int32_t cols, int32_t inner, int type, const void* x, int64_t ldx,
+                          const void* w_gate, int64_t ldg, const void* w_up, int64_t ldu, const float* bias_gate,
+                          const float* bias_up, int act, void* h, int h_type, int64_t ldh, void* pre_gate,
+                          int64_t ldpg, void* pre_up, int64_t ldpu, void* ws, size_t ws_bytes, void* stream);
+
+/* Its gradients:
+ *   dzg = dh * zu * act'(zg),  dzu = dh * act(zg),
+ *   dx = dzg w_gate + dzu w_up,  dw_gate = dzg^T x,  dw_up = dzu^T x,
+ *   dbias_gate = sum over rows of dzg,  dbias_up = sum over rows of dzu
+ *   dh       [rows, cols] of dh_type: `type` or BEAM_MOE_F32
+ *   pre_gate, pre_up   [rows, cols] of `type` as beam_moe_gated_linear wrote them
+ *   dx       [rows, inner] of `type`; NULL = not wanted
+ *   dw_gate, dw_up       [cols, inner] of `type`, both or neither
+ *   dbias_gate, dbias_up [cols] fp32, both or neither
+ * One at least is wanted; x is needed for dw_gate and dw_up, both weights for dx (else NULL).  dzg and dzu enter
+ * the products rounded to `type`, in fp16 times a power of two taken from the largest finite one of them, which the
+ * results are divided by: what lies 2^28 times and more below it is rounded to 2^-39 of it.  The bias gradients sum
+ * them unrounded.  When rows = 0, dw_gate, dw_up and both bias gradients are zeros. */
+int beam_moe_gated_linear_backward(int32_t rows, int32_t cols, int32_t inner, int type, const void* dh, int dh_type,
+                                   int64_t lddh, const void* x, int64_t ldx, const void* w_gate, int64_t ldg,
+                                   const void* w_up, int64_t ldu, const void* pre_gate, int64_t ldpg,
+                                   const void* pre_up, int64_t ldpu, int act, void* dx, int64_t lddx, void* dw_gate,
+                                   int64_t lddwg, void* dw_up, int64_t lddwu, float* dbias_gate, float* dbias_up,
+                                   void* ws, size_t ws_bytes, void* stream);
+
 /* Workspace of beam_moe_grad_norm and beam_moe_clip_grads for `count` tensors.
  * Returns SIZE_MAX for unsupported counts. */
 size_t beam_moe_grad_norm_workspace_bytes(int32_t count);

@@ -23,6 +23,13 @@ def sizes(*v):
     return (ctypes.c_int64 * len(v))(*v)
 
 
+GATED = Call("beam_moe_gated_linear", rows=40, cols=10, inner=12, type=BF16, x=FAKE, ldx=12, w_gate=FAKE, ldg=12,
+             w_up=FAKE, ldu=12, bias_gate=FAKE, bias_up=FAKE, act=2, h=FAKE, h_type=F32, ldh=10, pre_gate=FAKE, ldpg=10,
+             pre_up=FAKE, ldpu=10, ws=FAKE, ws_bytes=1 << 40, stream=None)
+GATED_BACK = Call("beam_moe_gated_linear_backward", rows=4, cols=10, inner=12, type=F16, dh=FAKE, dh_type=F32, lddh=10,
+                  x=FAKE, ldx=12, w_gate=FAKE, ldg=12, w_up=FAKE, ldu=12, pre_gate=FAKE, ldpg=10, pre_up=FAKE, ldpu=10,
+                  act=2, dx=FAKE, lddx=12, dw_gate=FAKE, lddwg=12, dw_up=FAKE, lddwu=12, dbias_gate=FAKE,
+                  dbias_up=FAKE, ws=FAKE, ws_bytes=1 << 40, stream=None)
 NORM = Call("beam_moe_grad_norm", count=2, grads=ptrs(A[0], A[1]), types=ints(BF16, F32), sizes=sizes(5, 7), scale=1.0,
             norm=FAKE, ws=FAKE, ws_bytes=1 << 30, stream=None)
 CLIP = Call("beam_moe_clip_grads", count=2, grads=ptrs(A[0], A[1]), types=ints(BF16, F32), sizes=sizes(5, 7), scale=1.0,
@@ -37,6 +44,9 @@ DEQUANT = Call("beam_moe_dequantize_mxfp4", rows=4, cols=70, codes=FAKE, ldc=48,
 @pytest.mark.parametrize("call, required, optional", [
     (NORM, ("norm",), ()), (CLIP, (), ("norm", "norm_in")), (QUANT, ("x", "codes", "scales"), ()),
     (DEQUANT, ("codes", "scales", "y"), ()),
+    (GATED, ("x", "w_gate", "w_up", "h"), ("bias_gate", "bias_up", "pre_gate", "pre_up")),
+    (GATED_BACK, ("dh", "pre_gate", "pre_up"), ("x", "w_gate", "w_up", "dx", "dw_gate", "dw_up", "dbias_gate",
+                                                "dbias_up")),
 ], ids=lambda v: v.fn if isinstance(v, Call) else "")
 def test_pointers(call, required, optional):
     for name in required:
@@ -64,6 +74,16 @@ def test_pointers(call, required, optional):
     (QUANT, dict(ldc=56)), (QUANT, dict(lds=2)), (QUANT, dict(lds=1 << 41)),
     (DEQUANT, dict(rows=-1)), (DEQUANT, dict(y_type=-1)), (DEQUANT, dict(ldy=69)), (DEQUANT, dict(ldc=40)),
     (DEQUANT, dict(lds=2)),
+    (GATED, dict(rows=-1)), (GATED, dict(type=F32)), (GATED, dict(h_type=F16)), (GATED, dict(act=4)),
+    (GATED, dict(act=-1)), (GATED, dict(ldx=11)), (GATED, dict(ldg=11)), (GATED, dict(ldu=11)), (GATED, dict(ldh=9)),
+    (GATED, dict(ldpg=9)), (GATED, dict(ldpu=9)), (GATED, dict(ldx=1 << 41)),
+    (GATED_BACK, dict(rows=-1)), (GATED_BACK, dict(type=F32)), (GATED_BACK, dict(dh_type=BF16)),
+    (GATED_BACK, dict(act=9)), (GATED_BACK, dict(dw_gate=None)), (GATED_BACK, dict(dw_up=None)),
+    (GATED_BACK, dict(dbias_gate=None)), (GATED_BACK, dict(dbias_up=None)), (GATED_BACK, dict(x=None)),
+    (GATED_BACK, dict(w_gate=None)), (GATED_BACK, dict(w_up=None)), (GATED_BACK, dict(lddh=9)),
+    (GATED_BACK, dict(ldx=11)), (GATED_BACK, dict(ldg=11)), (GATED_BACK, dict(ldu=11)), (GATED_BACK, dict(ldpg=9)),
+    (GATED_BACK, dict(ldpu=9)), (GATED_BACK, dict(lddx=11)), (GATED_BACK, dict(lddwg=11)), (GATED_BACK, dict(lddwu=11)),
+    (GATED_BACK, dict(dx=None, dw_gate=None, dw_up=None, dbias_gate=None, dbias_up=None)),
 ], ids=lambda v: v.fn if isinstance(v, Call) else "-".join(v) if isinstance(v, dict) else "")
 def test_invalid_arguments(call, bad):
     assert call(**bad) == BAD
@@ -73,6 +93,9 @@ def test_invalid_arguments(call, bad):
     (NORM, dict(count=(1 << 16) + 1)), (CLIP, dict(count=(1 << 16) + 1)), (NORM, dict(sizes=sizes(5, (1 << 40) + 1))),
     (QUANT, dict(rows=(1 << 20) + 1)), (QUANT, dict(cols=(1 << 18) + 1)), (QUANT, dict(cols=0)),
     (DEQUANT, dict(rows=(1 << 20) + 1)), (DEQUANT, dict(cols=(1 << 18) + 1)), (DEQUANT, dict(cols=0)),
+] + [
+    (c, b) for c in (GATED, GATED_BACK) for b in (dict(rows=(1 << 20) + 1), dict(cols=(1 << 17) + 1), dict(cols=0),
+                                                  dict(inner=(1 << 18) + 1), dict(inner=0))
 ], ids=lambda v: v.fn if isinstance(v, Call) else "-".join(v) if isinstance(v, dict) else "")
 def test_unsupported_sizes(call, big):
     assert call(**big) == UNSUP
@@ -94,8 +117,28 @@ def test_workspaces():
         assert call(ws=None) == WS and call(ws=ODD) == WS and call(ws_bytes=need - 1) == WS
 
 
+def test_gated_workspaces():
+    lib = binding.load_library()
+    need = lib.beam_moe_gated_linear_workspace_bytes
+    assert need(16, 1000, 1000, 1000, 1000, 1000) == 0       # few rows
+    assert need(8192, 2560, 5120, 5120, 5120, 5120) == 0     # whole tiles
+    assert need(64, 2560, 5120, 5120, 5120, 5120) > 0        # split
+    assert need(-1, 8, 8, 8, 8, 8) == need(8, 8, 8, 7, 8, 8) == need(8, 8, 8, 8, 8, 7) == need(8, 0, 8, 8, 8, 8) \
+        == binding.SIZE_MAX
+    n = need(64, 2560, 5120, 5120, 5120, 5120)
+    sizes_ = dict(rows=64, cols=2560, inner=5120, ldx=5120, ldg=5120, ldu=5120, ldh=2560, ldpg=2560, ldpu=2560)
+    for bad in (dict(ws=None), dict(ws=ODD), dict(ws_bytes=n - 1)):
+        assert GATED(**sizes_, **bad) == WS
+    back = lib.beam_moe_gated_linear_backward_workspace_bytes
+    n = back(4, 10, 12, 12, 12, 12)
+    assert 0 < n < 1 << 20
+    assert back(-1, 8, 8, 8, 8, 8) == back(8, 8, 8, 8, 7, 8) == binding.SIZE_MAX
+    for bad in (dict(ws=None), dict(ws=ODD), dict(ws_bytes=n - 1)):
+        assert GATED_BACK(**bad) == WS
+
+
 def test_no_rows():
-    for call in (QUANT, DEQUANT):
+    for call in (QUANT, DEQUANT, GATED):
         assert call(rows=0) == OK
 
 

@@ -368,3 +368,345 @@ def test_mxfp4_offsets_past_32_bits():
     for r in (0, rows - 1):
         assert torch.equal(y[r], fw.beam_moe_dequantize_mxfp4((q.codes[r:r + 1], q.scales[r:r + 1]))[0])
     assert (y[1] == 0).all()
+
+
+# --------------------------------------------------------------------------
+# the gated projections
+# --------------------------------------------------------------------------
+ACTS = {"none": lambda z: z, "relu": torch.relu, "silu": torch.nn.functional.silu, "gelu": torch.nn.functional.gelu}
+GEMM_UP = 2.0 ** -23  # a step inside the matrix core may cut instead of round
+
+
+def _depth(K):
+    """Additions that a product meets: its own group of 32, then one per group (whatever the split)."""
+    return 32 + K / 32 + 40
+
+
+def _slope(z, act):
+    z = z.double().requires_grad_(True)
+    return torch.autograd.grad(ACTS[act](z).sum(), z)[0]
+
+
+def _gated_inputs(M, N, K, dt, pad=0, bias=True, seed=0):
+    g = _gen(M * 3 + N * 5 + K + seed)
+    x, wg, wu = _randn(g, (M, K), dt, 1.0, pad), _randn(g, (N, K), dt, K ** -0.5, pad), _randn(g, (N, K), dt, K ** -0.5)
+    return g, x, wg, wu, _randn(g, (N,)) if bias else None, _randn(g, (N,)) if bias else None
+
+
+def _gated_check(x, wg, wu, bg, bu, act, h, zg=None, zu=None):
+    """Sums of depth d; act is good to 8 u of |z| + 1 and its slope stays below 1.13; the product adds a step."""
+    def arg(w, b):
+        z, mag = x.double() @ w.double().t(), x.double().abs() @ w.double().abs().t()
+        if b is not None:
+            z, mag = z + b.double(), mag + b.double().abs()
+        return z, _depth(x.shape[1]) * GEMM_UP * mag
+    (rg, eg), (ru, eu) = arg(wg, bg), arg(wu, bu)
+    if zg is not None:
+        _near(zg, rg, eg, "pre_gate")
+        _near(zu, ru, eu, "pre_up")
+    a = ACTS[act](rg)
+    ea = 1.13 * eg + 8 * U * (rg.abs() + (act != "none"))
+    _near(h, a * ru, ea * (ru.abs() + eu) + a.abs() * eu + 2 * U * (a * ru).abs(), "h")
+
+
+# the last are large enough for 256-row tiles
+GATED_SHAPES = [(1, 1, 1), (1, 64, 64), (1, 100, 1000), (2, 2560, 512), (3, 17, 5), (7, 33, 2049), (16, 256, 128),
+                (17, 48, 96), (33, 1000, 136), (64, 512, 2560), (65, 130, 72), (100, 64, 7), (129, 257, 65),
+                (255, 96, 520), (256, 256, 64), (300, 513, 1024), (257, 264, 192), (520, 1040, 328), (1000, 1032, 2048),
+                (2100, 1280, 1280)]
+
+
+@pytest.mark.parametrize("M,N,K", GATED_SHAPES)
+@pytest.mark.parametrize("dt", [BF16, F16])
+def test_gated_linear(M, N, K, dt):
+    for act, yt, bias, pad in (("silu", dt, False, 0), ("gelu", F32, True, 0), ("relu", dt, True, 8),
+                               ("silu", dt, True, 3), ("none", F32, False, 1)):
+        _say("gated", M, N, K, dt, act, yt, bias, pad)
+        _, x, wg, wu, bg, bu = _gated_inputs(M, N, K, dt, pad, bias)
+        h, zg, zu = fw.beam_moe_gated_linear(x, wg, wu, bg, bu, act=act, out_dtype=yt, want_pre=True)
+        _gated_check(x, wg, wu, bg, bu, act, h, zg, zu)
+        assert torch.equal(fw.beam_moe_gated_linear(x, wg, wu, bg, bu, act=act, out_dtype=yt), h)
+
+
+@pytest.mark.parametrize("M,N,K", [(100, 50, 65536), (300, 150, 16384), (512, 256, 9216), (20, 100, 2050)])
+@pytest.mark.parametrize("dt", [BF16, F16])
+def test_gated_linear_long_k(M, N, K, dt):
+    _say("gated long K", M, N, K, dt)
+    _, x, wg, wu, bg, bu = _gated_inputs(M, N, K, dt)
+    h, zg, zu = fw.beam_moe_gated_linear(x, wg, wu, bg, bu, want_pre=True)
+    _gated_check(x, wg, wu, bg, bu, "silu", h, zg, zu)
+
+
+def test_gated_linear_of_one_fused_weight():
+    """Both weights as halves of one matrix, or as its alternate rows."""
+    _say("gated fused weight")
+    for M in (5, 200):
+        g = _gen(M)
+        x, w = _randn(g, (M, 136), BF16), _randn(g, (300, 136), BF16, 0.1)
+        for wg, wu in ((w[:150], w[150:]), (w[0::2], w[1::2])):
+            h = fw.beam_moe_gated_linear(x, wg, wu)
+            assert torch.equal(h, fw.beam_moe_gated_linear(x, wg.contiguous(), wu.contiguous()))
+            _gated_check(x, wg, wu, None, None, "silu", h)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 40, 64), (5, 70, 65), (70, 70, 65), (300, 264, 128)])
+def test_gated_linear_padding_and_nan(M, N, K):
+    """What lies behind the rows of h stays; a NaN row of x stays in its row."""
+    _say("gated padding", M, N, K)
+    _, x, wg, wu, bg, bu = _gated_inputs(M, N, K, BF16, 8)
+    buf = torch.full((M, N + 9), 7.0, dtype=BF16, device=DEV)
+    want = fw.beam_moe_gated_linear(x, wg, wu, bg, bu)
+    fw.beam_moe_gated_linear(x, wg, wu, bg, bu, out=buf[:, :N])
+    assert torch.equal(buf[:, :N], want) and (buf[:, N:] == 7.0).all()
+    x = x.clone()
+    x[M // 2, K // 2] = NAN
+    got = fw.beam_moe_gated_linear(x, wg, wu, bg, bu)
+    assert got[M // 2].isnan().all()
+    keep = torch.arange(M, device=DEV) != M // 2
+    assert torch.equal(got[keep], want[keep])
+
+
+def test_gated_linear_of_no_rows():
+    _say("gated no rows")
+    x, w = torch.empty(0, 64, dtype=BF16, device=DEV), torch.ones(40, 64, dtype=BF16, device=DEV)
+    assert fw.beam_moe_gated_linear(x, w, w).shape == (0, 40)
+    z = torch.empty(0, 40, dtype=BF16, device=DEV)
+    dx, dwg, dwu, dbg, dbu = fw.beam_moe_gated_linear_backward(z, x, w, w, z, z)
+    assert dx.shape == (0, 64) and all(t.shape[0] == 40 and not t.any() for t in (dwg, dwu, dbg, dbu))
+
+
+def _gated_back_check(dh, x, wg, wu, zg, zu, act, out):
+    """dz is rounded to the products' type: half a step of each term, at worst all one way, or in fp16, where the
+    largest lies in [2^14, 2^15) of its scale, 2^-25 of it, at most 2^-39 of the largest; then the sums. Slopes near zero
+    are differences of order 1."""
+    d, g, u = dh.double(), zg.double(), zu.double()
+    M, N = dh.shape
+    dg, du = d * u * _slope(zg, act), d * ACTS[act](g)
+    off = _step(x) + 24 * U
+    top = 2.0 ** -39 * float(torch.maximum(dg.abs().max(), du.abs().max())) if x.dtype == F16 else 0.0
+    near = 8 * U * (act != "none") * d.abs()
+    eg, eu = off * dg.abs() + near * u.abs() + top, off * du.abs() + near * (g.abs() + 1) + top
+    dx, dwg, dwu, dbg, dbu = out
+    if dx is not None:
+        w, v = wg.double(), wu.double()
+        dep = _depth(2 * N) * GEMM_UP
+        _near(dx, dg @ w + du @ v, (dep * dg.abs() + eg) @ w.abs() + (dep * du.abs() + eu) @ v.abs(), "dx")
+    if dwg is not None:
+        dep = _depth(M) * GEMM_UP
+        ax = x.double().abs()
+        _near(dwg, dg.t() @ x.double(), (dep * dg.abs() + eg).t() @ ax, "dw_gate")
+        _near(dwu, du.t() @ x.double(), (dep * du.abs() + eu).t() @ ax, "dw_up")
+    if dbg is not None:
+        dep = (math.ceil(M / 64) + 64 + 24 + 24) * U
+        _near(dbg, dg.sum(0), (dep * dg.abs() + near * u.abs()).sum(0), "dbias_gate")
+        _near(dbu, du.sum(0), (dep * du.abs() + near * (g.abs() + 1)).sum(0), "dbias_up")
+
+
+LARGE_BACK = [(1000, 520, 2048), (3300, 1700, 136), (3300, 100, 3336), (200, 1650, 3336), (4096, 1024, 1280)]
+
+
+@pytest.mark.parametrize("M,N,K", GATED_SHAPES + LARGE_BACK)
+@pytest.mark.parametrize("dt", [BF16, F16])
+def test_gated_linear_backward(M, N, K, dt):
+    for act, yt, pad in (("silu", dt, 0), ("gelu", F32, 8), ("relu", dt, 3), ("none", F32, 1)):
+        _say("gated_backward", M, N, K, dt, act, yt, pad)
+        g, x, wg, wu, _, _ = _gated_inputs(M, N, K, dt, pad)
+        dh, zg, zu = _randn(g, (M, N), yt, 1.0, pad), _randn(g, (M, N), dt, 1.0, pad), _randn(g, (M, N), dt)
+        out = fw.beam_moe_gated_linear_backward(dh, x, wg, wu, zg, zu, act=act)
+        _gated_back_check(dh, x, wg, wu, zg, zu, act, out)
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+def test_gated_linear_backward_parts(dt):
+    """Each result by itself has the bits that it has among all."""
+    for M, N, K in ((70, 130, 72), (517, 203, 777), (3300, 1700, 136)):
+        _say("gated_backward parts", M, N, K, dt)
+        g, x, wg, wu, _, _ = _gated_inputs(M, N, K, dt)
+        dh, zg, zu = (_randn(g, (M, N), dt) for _ in range(3))
+        dx, dwg, dwu, dbg, dbu = fw.beam_moe_gated_linear_backward(dh, x, wg, wu, zg, zu)
+        _gated_back_check(dh, x, wg, wu, zg, zu, "silu", (dx, dwg, dwu, dbg, dbu))
+        only = fw.beam_moe_gated_linear_backward(dh, x, None, None, zg, zu, want_dx=False)
+        assert only[0] is None
+        _gated_back_check(dh, x, None, None, zg, zu, "silu", only)
+        only = fw.beam_moe_gated_linear_backward(dh, None, wg, wu, zg, zu, want_dw=False, want_dbias=False)
+        assert only[1:] == (None,) * 4
+        _gated_back_check(dh, torch.empty(M, K, dtype=dt), wg, wu, zg, zu, "silu", only)
+        only = fw.beam_moe_gated_linear_backward(dh, x, None, None, zg, zu, want_dx=False, want_dw=False)
+        assert torch.equal(only[3], dbg) and torch.equal(only[4], dbu)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 9, 16), (33, 100, 136), (517, 203, 777), (3300, 1700, 136)])
+@pytest.mark.parametrize("size,weights", [(1e-7, 2.0 ** 11), (1e-12, 2.0 ** 11), (1e6, 2.0 ** -14)])
+def test_gated_backward_keeps_small_and_large_gradients_in_fp16(M, N, K, size, weights):
+    """FP32 gradients that fp16 cannot hold, with weights and inputs for which the results can be held."""
+    _say("gated_backward range", M, N, K, size)
+    g = _gen(M + N + K)
+    x, wg, wu = (_randn(g, s, F16, weights) for s in ((M, K), (N, K), (N, K)))
+    dh, zg, zu = _randn(g, (M, N), F32, size, 3), _randn(g, (M, N), F16, 1.5), _randn(g, (M, N), F16, 1.5)
+    for act in ("silu", "gelu"):
+        out = fw.beam_moe_gated_linear_backward(dh, x, wg, wu, zg, zu, act=act)
+        _gated_back_check(dh, x, wg, wu, zg, zu, act, out)
+
+
+def test_gated_backward_nan_and_infinite_gradients_in_fp16():
+    """They touch their own row of dx and their own row of dw alone, and have no part in the scale."""
+    _say("gated_backward nan")
+    M, N, K = 90, 70, 136
+    g, x, wg, wu, _, _ = _gated_inputs(M, N, K, F16)
+    dh, zg, zu = (_randn(g, (M, N), F16) for _ in range(3))
+    clean = fw.beam_moe_gated_linear_backward(dh, x, wg, wu, zg, zu)
+    # what the poisoned elements would have been the scale of stays
+    assert dh[3, 5].abs() < dh.abs().max() and dh[40, 6].abs() < dh.abs().max()
+    dh = dh.clone()
+    dh[3, 5], dh[40, 6] = NAN, INF
+    dx, dwg, dwu, dbg, dbu = fw.beam_moe_gated_linear_backward(dh, x, wg, wu, zg, zu)
+    rows = torch.ones(M, dtype=torch.bool, device=DEV)
+    rows[[3, 40]] = False
+    cols = torch.ones(N, dtype=torch.bool, device=DEV)
+    cols[[5, 6]] = False
+    assert torch.equal(dx[rows], clean[0][rows]) and not dx[~rows].isfinite().any()
+    for got, was in ((dwg, clean[1]), (dwu, clean[2]), (dbg, clean[3]), (dbu, clean[4])):
+        assert torch.equal(got[cols], was[cols]) and not got[~cols].isfinite().any()
+
+
+def test_gated_gradient_against_differences():
+    """Differences of the call itself in FP32 outputs: with loss L = sum(h r), (L(x + t v) - L(x - t v)) / 2t against
+    dx . v and the like. x holds multiples of 2^-6 and t v too, so both arguments are exact in bf16. h is off by
+    40 u of its magnitudes, the third derivative of silu(a) b along the line by at most 3 of |v w|^3 / 6 t^2."""
+    _say("gated differences")
+    M, N, K, t = 6, 40, 32, 2.0 ** -4
+    g = _gen(77)
+    grid = lambda s, top: torch.randint(-top, top + 1, s, generator=g, device=DEV).to(BF16) / 64  # noqa: E731
+    x, wg, wu = grid((M, K), 64), grid((N, K), 32), grid((N, K), 32)
+    r = _randn(g, (M, N))
+    h, zg, zu = fw.beam_moe_gated_linear(x, wg, wu, out_dtype=F32, want_pre=True)
+    dx, dwg, dwu, _, _ = fw.beam_moe_gated_linear_backward(r, x, wg, wu, zg, zu)
+
+    def loss(x, wg, wu):
+        return float((fw.beam_moe_gated_linear(x, wg, wu, out_dtype=F32).double() * r.double()).sum())
+
+    size = float((h.double().abs() * r.double().abs()).sum())
+    for k, (arg, grad) in enumerate(((x, dx), (wg, dwg), (wu, dwu))):
+        v = torch.randint(-1, 2, arg.shape, generator=g, device=DEV).to(BF16)
+        ends = [[a if i != k else (a.float() + s * t * v.float()).to(BF16) for i, a in enumerate((x, wg, wu))]
+                for s in (1, -1)]
+        assert all(torch.equal(e[k].float(), arg.float() + s * t * v.float()) for e, s in zip(ends, (1, -1)))
+        quot = (loss(*ends[0]) - loss(*ends[1])) / (2 * t)
+        slope = float((grad.double() * v.double()).sum())
+        xd, vd = x.double().abs(), v.double().abs()
+        # |d zg|, |d zu| along v
+        if k == 0:
+            ag, au = vd @ wg.double().abs().t(), vd @ wu.double().abs().t()
+        elif k == 1:
+            ag, au = xd @ vd.t(), torch.zeros(M, N, device=DEV, dtype=torch.float64)
+        else:
+            ag, au = torch.zeros(M, N, device=DEV, dtype=torch.float64), xd @ vd.t()
+        # |silu''| <= 1/2, |silu'''| <= 0.31
+        third = ((0.31 * ag ** 3 * zu.double().abs() + 3 * 0.5 * ag ** 2 * au) * r.double().abs()).sum()
+        # pre, both dz and the gradient itself are rounded to bf16: at most eight half steps of what they are made of
+        made = ((1.1 * ag * zu.double().abs() + au * zg.double().abs()) * r.double().abs()).sum()
+        tol = 8 * 2.0 ** -8 * float(made) + float(third) * t * t / 6 + 40 * U * size / t * 4
+        assert abs(quot - slope) <= tol, (k, quot, slope, tol)
+        assert tol < 0.2 * max(abs(slope), float(made) / 3), (k, tol, slope)
+
+
+def _gated_step_inputs(seed, T=192, H=512, F=328):
+    g = _gen(seed)
+    return dict(stream=_randn(g, (T, H), F32, 2.0), gamma=1 + _randn(g, (H,), F32, 0.1), beta=_randn(g, (H,), F32, 0.1),
+                wg=_randn(g, (F, H), BF16, H ** -0.5), wu=_randn(g, (F, H), BF16, H ** -0.5),
+                bg=_randn(g, (F,), F32, 0.1), bu=_randn(g, (F,), F32, 0.1), wd=_randn(g, (H, F), BF16, F ** -0.5),
+                dout=_randn(g, (T, H), F32))
+
+
+def _gated_step(s, max_norm=1.0, step=3):
+    """A dense gated sublayer (norm, gated projections, down onto the stream) forward and back to the stream and every
+    weight, and all weights' gradients clipped into 32 bits."""
+    keep, add = math.sqrt((step - 1) / step), math.sqrt(1 / step)
+    x, mean, rstd = fw.beam_moe_layer_norm(s["stream"], s["gamma"], s["beta"], out_dtype=BF16)
+    h, zg, zu = fw.beam_moe_gated_linear(x, s["wg"], s["wu"], s["bg"], s["bu"], want_pre=True)
+    out = fw.beam_moe_linear(h, s["wd"], residual=s["stream"], keep=keep, add=add, out_dtype=F32)
+    dh, dwd, _, dstream = fw.beam_moe_linear_backward(s["dout"], h, s["wd"], keep=keep, add=add, want_dbias=False,
+                                                      want_dres=True)
+    dx, dwg, dwu, dbg, dbu = fw.beam_moe_gated_linear_backward(dh, x, s["wg"], s["wu"], zg, zu)
+    dnorm, dgamma, dbeta = fw.beam_moe_layer_norm_backward(dx, s["stream"], mean, rstd, s["gamma"])
+    grads = dict(gamma=dgamma, beta=dbeta, wg=dwg, wu=dwu, bg=dbg, bu=dbu, wd=dwd)
+    clipped = {k: torch.empty_like(v, dtype=F32) for k, v in grads.items()}
+    norm = fw.beam_moe_clip_grads(list(grads.values()), max_norm, out=list(clipped.values()))
+    return dict(out=out, dstream=dstream + dnorm, norm=norm, **clipped)
+
+
+def _gated_step_ref(s, max_norm=1.0, step=3):
+    f = {k: v.double().requires_grad_(True) for k, v in s.items() if k != "dout"}
+    x = torch.nn.functional.layer_norm(f["stream"], (f["stream"].shape[1],), f["gamma"], f["beta"], 1e-5)
+    h = torch.nn.functional.silu(x @ f["wg"].t() + f["bg"]) * (x @ f["wu"].t() + f["bu"])
+    out = math.sqrt((step - 1) / step) * f["stream"] + math.sqrt(1 / step) * (h @ f["wd"].t())
+    grads = dict(zip(f, torch.autograd.grad((out * s["dout"].double()).sum(), list(f.values()))))
+    dstream = grads.pop("stream")
+    norm = torch.stack([(v * v).sum() for v in grads.values()]).sum().sqrt()
+    c = min(1.0, max_norm / (float(norm) + 1e-6))
+    return dict(out=out.detach(), dstream=dstream, norm=norm, **{k: v * c for k, v in grads.items()})
+
+
+def test_training_step_of_a_gated_sublayer():
+    """The whole run against 64-bit autograd. Rounding a tensor to bf16 changes it by at most eps / 2 of its 2-norm; at
+    most eight such roundings (x, h, both pre, dh, both dz, dx) lie on any path to a result, and random matrices
+    of these shapes pass a relative error on with a factor of order one: 16 half steps in all, and as much again
+    for the norm that every clipped gradient is divided by."""
+    _say("gated training step")
+    s = _gated_step_inputs(1)
+    got, want = _gated_step(s), _gated_step_ref(s)
+    torch.cuda.synchronize()
+    assert float(want["norm"]) > 2.0
+    for k, v in want.items():
+        err = float((got[k].double() - v).norm() / v.norm())
+        assert err <= (16 if k in ("out", "dstream", "norm") else 32) * 2.0 ** -9, (k, err)
+
+
+def test_gated_sublayer_on_two_streams_at_once():
+    _say("gated two streams")
+    a, b = _gated_step_inputs(2), _gated_step_inputs(3)
+    alone = [_gated_step(v) for v in (a, b)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        got = []
+        for v, st in zip((a, b), streams):
+            st.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(st):
+                got.append(_gated_step(v))
+        torch.cuda.synchronize()
+        for x, y in zip(alone, got):
+            assert all(torch.equal(x[k], y[k]) for k in x)
+
+
+def test_gated_sublayer_captured_and_replayed():
+    _say("gated graph")
+    for T in (8, 192):
+        s = _gated_step_inputs(4, T)
+        _gated_step(s)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = _gated_step(s)
+        for k in range(4):
+            s["stream"].copy_(_gated_step_inputs(10 + k, T)["stream"])
+            s["wg"].mul_(1.0 + 0.25 * (k % 2))
+            graph.replay()
+            torch.cuda.synchronize()
+            eager = _gated_step(s)
+            torch.cuda.synchronize()
+            assert all(torch.equal(got[n], eager[n]) for n in got)
+
+
+def test_gated_linear_offsets_past_32_bits():
+    _say("gated offsets")
+    M, N, K = 40000, 100, 64
+    ld = 60000
+    buf = torch.zeros(M, ld, dtype=BF16, device=DEV)       # 2.4e9 elements
+    x, h = buf[:, :K], buf[:, K + 8:K + 8 + N]
+    g = _gen(6)
+    wg, wu = _randn(g, (N, K), BF16, 0.1), _randn(g, (N, K), BF16, 0.1)
+    x[-300:] = _randn(g, (300, K), BF16)
+    fw.beam_moe_gated_linear(x, wg, wu, out=h)
+    _gated_check(x[-300:], wg, wu, None, None, "silu", h[-300:])
+    assert not h[:100].any()
