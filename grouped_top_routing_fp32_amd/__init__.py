@@ -14,8 +14,8 @@ _EXPORTS = ("beam_moe_route", "beam_moe_select", "beam_moe_dispatch", "beam_moe_
             "beam_moe_layer_norm_backward", "beam_moe_balance_loss", "beam_moe_route_backward", "beam_moe_linear",
             "beam_moe_linear_backward", "beam_moe_gated_linear", "beam_moe_gated_linear_backward",
             "beam_moe_grad_norm", "beam_moe_clip_grads", "beam_moe_quantize_mxfp4", "beam_moe_dequantize_mxfp4",
-            "Mxfp4", "beam_moe_workspace_bytes", "beam_moe_status_str", "Dims",
-            "BeamMoeError", "load_library")
+            "beam_moe_linear_mxfp4", "Mxfp4", "beam_moe_workspace_bytes", "beam_moe_status_str",
+            "Dims", "BeamMoeError", "load_library")
 
 
 def __getattr__(name):

@@ -39,12 +39,12 @@ EXPORTED = ("beam_moe_workspace_bytes", "beam_moe_route_workspace_bytes", "beam_
             "beam_moe_gated_linear_backward_workspace_bytes", "beam_moe_gated_linear",
             "beam_moe_gated_linear_backward", "beam_moe_grad_norm_workspace_bytes",
             "beam_moe_grad_norm", "beam_moe_clip_grads", "beam_moe_quantize_mxfp4", "beam_moe_dequantize_mxfp4",
-            "beam_moe_stream_rows", "beam_moe_timing_enable",
+            "beam_moe_linear_mxfp4_workspace_bytes", "beam_moe_linear_mxfp4", "beam_moe_stream_rows", "beam_moe_timing_enable",
             "beam_moe_timing_read", "beam_moe_stage_name", "beam_moe_status_str")
 
 SIZE_MAX = 2 ** 64 - 1
 
-BEAM_MOE_BF16, BEAM_MOE_F16, BEAM_MOE_F32 = 0, 1, 2
+BEAM_MOE_BF16, BEAM_MOE_F16, BEAM_MOE_F32, BEAM_MOE_MXFP4 = 0, 1, 2, 3
 ELEM_TYPES = {torch.bfloat16: BEAM_MOE_BF16, torch.float16: BEAM_MOE_F16, torch.float32: BEAM_MOE_F32}
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 
@@ -125,7 +125,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             ("beam_moe_grad_norm", ci, [i32, vp, vp, vp, f32, vp, vp, sz, vp]),
             ("beam_moe_clip_grads", ci, [i32, vp, vp, vp, f32, f32, f32, vp, vp, vp, vp, vp, sz, vp]),
             ("beam_moe_quantize_mxfp4", ci, [i32, i32, vp, ci, i64, vp, i64, vp, i64, vp]),
-            ("beam_moe_dequantize_mxfp4", ci, [i32, i32, vp, i64, vp, i64, vp, ci, i64, vp])):
+            ("beam_moe_dequantize_mxfp4", ci, [i32, i32, vp, i64, vp, i64, vp, ci, i64, vp]),
+            ("beam_moe_linear_mxfp4_workspace_bytes", sz, [i32, i32, i32, ci, i64]),
+            ("beam_moe_linear_mxfp4", ci, [i32, i32, i32, ci, vp, i64, vp, i64, vp, i64, vp, i64, vp, ci, vp, i64, f32,
+                                           f32, vp, ci, i64, vp, sz, vp])):
         getattr(lib, fn).argtypes = args
         getattr(lib, fn).restype = res
     lib.beam_moe_stream_rows.argtypes = [pd, i32, ctypes.c_int]
@@ -945,6 +948,43 @@ def beam_moe_dequantize_mxfp4(q: Mxfp4, cols: Optional[int] = None, *, out_dtype
         _check(load_library().beam_moe_dequantize_mxfp4(T, H, codes.data_ptr(), ldc, q[1].data_ptr(), lds,
                                                         out.data_ptr(), ELEM_TYPES[out.dtype], ldy, st),
                "beam_moe_dequantize_mxfp4")
+    return out
+
+
+def beam_moe_linear_mxfp4(x, w: Mxfp4, bias: Optional[torch.Tensor] = None, *, act: str = "none",
+                          residual: Optional[torch.Tensor] = None, keep: float = 1.0, add: float = 1.0,
+                          out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None,
+                          ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y = keep * residual + add * act(x w^T + bias) for w = (codes, scales) of [N, K] in microscaled 4-bit floating
+    point and x [M, K] in bf16 or fp16 (rows may be strided), or such a pair itself. y is of out_dtype (x's type or
+    fp32; any of the three, bf16 by default, for a pair), as residual is; out may be residual itself."""
+    four = not isinstance(x, torch.Tensor)
+    codes, scales = w
+    if codes.dim() != 2:
+        raise ValueError("w's codes must be a matrix")
+    N = codes.shape[0]
+    if four:
+        M, width, dev = _mat(x[0], "x's codes")
+        K, blocks = 2 * width, width // 16
+        ldx, ldxs = _mx(x, "x", M, blocks, dev)
+        xt, default, types = BEAM_MOE_MXFP4, torch.bfloat16, _FLOATS
+        xp, xsp = x[0].data_ptr(), x[1].data_ptr()
+    else:
+        M, K, dev = _mat(x, "x")
+        blocks = (K + 31) // 32
+        ldx, ldxs, default, types = _rows(x, "x", _HALF, (M, K), dev), 0, x.dtype, (x.dtype, _F32)
+        xt, xp, xsp = ELEM_TYPES[x.dtype], x.data_ptr(), None
+    ldw, ldws = _mx(w, "w", N, blocks, dev)
+    b, a = _vec(bias, "bias", _F32, (N,), dev), _act(act)
+    with _On(dev, stream) as st:
+        out, ldy = _result(out, out_dtype, default, types, (M, N), dev)
+        ldr = 0 if residual is None else _rows(residual, "residual", (out.dtype,), (M, N), dev)
+        wp, wn, _keep = _scratch(_linear_ws("beam_moe_linear_mxfp4_workspace_bytes", M, N, K, xt, ldx), ws, dev,
+                                 "beam_moe_linear_mxfp4")
+        _check(load_library().beam_moe_linear_mxfp4(
+            M, N, K, xt, xp, ldx, xsp, ldxs, codes.data_ptr(), ldw, scales.data_ptr(), ldws, b, a,
+            None if residual is None else residual.data_ptr(), ldr, keep, add, out.data_ptr(), ELEM_TYPES[out.dtype],
+            ldy, wp, wn, st), "beam_moe_linear_mxfp4")
     return out
 
 

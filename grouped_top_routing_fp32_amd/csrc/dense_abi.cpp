@@ -80,6 +80,11 @@ bool mx_rows_ok(int64_t cols, int64_t ldc, int64_t lds) {
   return ldc % 16 == 0 && ld_ok(ldc, 16 * blocks) && ld_ok(lds, blocks);
 }
 
+int check_mx_linear(int32_t rows, int32_t cols, int32_t inner) {
+  if (rows < 0) return BEAM_MOE_ERR_INVALID_ARG;
+  return cols < 1 || cols > kMaxMxCols ? BEAM_MOE_ERR_UNSUPPORTED : check_mx(rows, inner);
+}
+
 constexpr int32_t kMaxGatedRows = 1 << 20;
 constexpr int32_t kMaxGatedCols = 1 << 17;  // both projections' are those of one product
 constexpr int32_t kMaxGatedInner = 1 << 18;
@@ -330,6 +335,60 @@ int beam_moe_dequantize_mxfp4(int32_t rows, int32_t cols, const uint8_t* codes, 
   if ((rc = check_ptrs({codes, scales, y})) != BEAM_MOE_OK) return rc;
   return hip_status(beam::launch_dequantize_mx(codes, ldc, scales, lds, y, y_type, ldy, rows, cols,
                                                static_cast<hipStream_t>(stream)));
+}
+
+size_t beam_moe_linear_mxfp4_workspace_bytes(int32_t rows, int32_t cols, int32_t inner, int x_type, int64_t ldx) {
+  const bool four = x_type == BEAM_MOE_MXFP4;
+  if (check_mx_linear(rows, cols, inner) != BEAM_MOE_OK || !(four || half_type(x_type)) ||
+      !ld_ok(ldx, four ? 16 * beam::mx_blocks(inner) : inner))
+    return SIZE_MAX;
+  return beam::plan_mx(rows, cols, inner, four, ldx).total;
+}
+
+int beam_moe_linear_mxfp4(int32_t rows, int32_t cols, int32_t inner, int x_type, const void* x, int64_t ldx,
+                          const uint8_t* x_scales, int64_t ldxs, const uint8_t* w, int64_t ldw, const uint8_t* w_scales,
+                          int64_t ldws, const float* bias, int act, const void* res, int64_t ldr, float keep, float add,
+                          void* y, int y_type, int64_t ldy, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_mx_linear(rows, cols, inner);
+  if (rc != BEAM_MOE_OK) return rc;
+  const bool four = x_type == BEAM_MOE_MXFP4;
+  if (!(four || half_type(x_type)) || !(four ? type_ok(y_type) : y_type == x_type || y_type == BEAM_MOE_F32) ||
+      !act_ok(act) || !std::isfinite(keep) || !std::isfinite(add))
+    return BEAM_MOE_ERR_INVALID_ARG;
+  if (rows == 0) return BEAM_MOE_OK;
+  if (!(four ? mx_rows_ok(inner, ldx, ldxs) : ld_ok(ldx, inner)) || !mx_rows_ok(inner, ldw, ldws) ||
+      !ld_ok(ldy, cols) || (res && !ld_ok(ldr, cols)) || (res == y && ldr != ldy))
+    return BEAM_MOE_ERR_INVALID_ARG;
+  if ((rc = check_ptrs({x, w, w_scales, y})) != BEAM_MOE_OK) return rc;
+  if (four && (rc = check_ptrs({x_scales})) != BEAM_MOE_OK) return rc;
+  if ((rc = check_optional({bias, res})) != BEAM_MOE_OK) return rc;
+  const beam::MxPlan plan = beam::plan_mx(rows, cols, inner, four, ldx);
+  if (plan.total && (!ws || !aligned16(ws) || ws_bytes < plan.total)) return BEAM_MOE_ERR_WORKSPACE;
+  beam::MxLinear a{};
+  a.four = four;
+  a.x = x;
+  a.ldx = ldx;
+  a.x_scales = x_scales;
+  a.ldxs = ldxs;
+  a.w = w;
+  a.ldw = ldw;
+  a.w_scales = w_scales;
+  a.ldws = ldws;
+  beam::GemmArgs& g = a.g;
+  g.M = rows;
+  g.N = cols;
+  g.K = inner;
+  g.type = !four ? x_type : y_type == BEAM_MOE_F16 ? BEAM_MOE_F16 : BEAM_MOE_BF16;
+  g.bias = bias;
+  g.act = act;
+  g.res = res;
+  g.ldr = ldr;
+  g.keep = keep;
+  g.add = add;
+  g.out = y;
+  g.out_type = y_type;
+  g.ldo = ldy;
+  return hip_status(beam::launch_linear_mx(a, plan, ws, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

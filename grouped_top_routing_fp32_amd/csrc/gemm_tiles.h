@@ -1,7 +1,8 @@
-// The tiled MFMA product of linear.hip and gated.hip, instantiated once for each 16-bit type.
+// The tiled MFMA product of linear.hip, gated.hip and mx_linear.hip, instantiated once for each 16-bit type.
 #pragma once
 
 #include <type_traits>
+#include <utility>
 
 #include "linear.h"
 
@@ -132,6 +133,48 @@ struct Side {
   }
 };
 
+// The scales of a stage of 4-bit operands: 8 blocks (256 codes, 128 bytes as kBK 16-bit elements are) of R rows.  The byte of
+// block 4 s + g of row r lies at (r / 64, g, r % 16, s, r / 16 % 4), so that a lane (row l % 16, block
+// l / 16 of each four) has those of 64 rows in 8 bytes, and the matrix instruction picks a byte of a word.
+template <int R>
+struct ScaleStage {
+  static constexpr int kBytes = R * 8;
+  typedef __attribute__((address_space(3))) uint8_t lds_u8;
+  typedef u32x2 u32x2_byte __attribute__((aligned(1)));
+  // Blocks b .. b + 7 of a row of `blocks`; 0 past them, where the codes are 0 too.
+  static __device__ __forceinline__ u32x2 load(const uint8_t* row, int b, int blocks) {
+    if (b + 8 <= blocks) return *reinterpret_cast<const u32x2_byte*>(row + b);
+    u32x2 v = {0u, 0u};
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (b + q < blocks) v[q / 4] |= (uint32_t)row[b + q] << (8 * (q % 4));
+    return v;
+  }
+  static __device__ __forceinline__ void store(lds_u8* stage, int r, u32x2 v) {
+    lds_u8* p = stage + (r >> 6) * 512 + (r & 15) * 8 + ((r >> 4) & 3);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) p[(q % 4) * 128 + (q / 4) * 4] = (uint8_t)(v[q / 4] >> (8 * (q % 4)));
+  }
+  // The words (s = 0, 1) of rows r0 .. r0 + 63, or the upper half of them moved down where r0 is off 64 by 32.
+  static __device__ __forceinline__ u32x2 words(const lds_u8* stage, int r0, int lane) {
+    u32x2 v = *(const __attribute__((address_space(3))) u32x2*)(stage + (r0 >> 6) * 512 + (lane >> 4) * 128 + (lane & 15) * 8);
+    const int down = r0 & 32 ? 16 : 0;
+    v[0] >>= down;
+    v[1] >>= down;
+    return v;
+  }
+};
+
+// f(integral_constant<int, 0>) .. f(integral_constant<int, N - 1>)
+template <class F, int... I>
+__device__ __forceinline__ void for_each_of(F& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void static_for(F f) {
+  for_each_of(f, std::make_integer_sequence<int, N>{});
+}
+
 // XCD-aware order: workgroup b runs on XCD b % 8; each XCD takes a contiguous range.
 __device__ __forceinline__ int xcd_lin(int b, int total) {
   const int full = total & ~7;
@@ -154,6 +197,9 @@ __device__ __forceinline__ int xcd_lin(int b, int total) {
 // kRing<BM, BN> elements of LDS.
 template <int BM, int BN>
 constexpr int kRing = 2 * (BM + BN) * kBK;
+// and behind them, for 4-bit operands, two stages of scales
+template <int BM, int BN, class G>
+constexpr int kRingOf = kRing<BM, BN> + (std::is_same_v<G, MxArgs> ? ScaleStage<BM + BN>::kBytes : 0);
 
 // Result and, in training, both arguments of a gated layer from a tile's sums, or the sums themselves where K is
 // split.  A lane holds gate and up of the same elements, so the product is formed in registers, and one
@@ -233,7 +279,7 @@ __device__ __forceinline__ void gated_epilogue(uint16_t* ring, const GatedArgs& 
 template <bool HALF, bool AT, bool BT, int BM, int BN, int WM, int WN, bool EPI, bool REGS = false, class G = GemmArgs>
 __device__ __forceinline__ void gemm_tile(uint16_t* ring, G g, int mt, int nt, int lin, int k_per_split,
                                           float* __restrict__ part, int64_t ldpart) {
-  constexpr bool kGated = std::is_same_v<G, GatedArgs>;
+  constexpr bool kGated = std::is_same_v<G, GatedArgs>, kMx = std::is_same_v<G, MxArgs>;
   constexpr int NW = WM * WN, FI = BM / WM / 16, FJ = BN / WN / 16;
   constexpr int kSlot = (BM + BN) * kBK;
   lds_u16* lds = (lds_u16*)ring;
@@ -266,6 +312,23 @@ __device__ __forceinline__ void gemm_tile(uint16_t* ring, G g, int mt, int nt, i
       sb.issue(lds + slot * kSlot + BM * kBK, left, wave, lane);
     }
   };
+  // 4-bit operands: a thread has a row's scales of a stage, requested a step before they go to LDS
+  using Scales = ScaleStage<BM + BN>;
+  using lds_u8 = typename Scales::lds_u8;
+  [[maybe_unused]] lds_u8* scales = (lds_u8*)(lds + 2 * kSlot);
+  [[maybe_unused]] const uint8_t* scale_row = nullptr;
+  [[maybe_unused]] u32x2 next_scales = {0u, 0u};
+  [[maybe_unused]] auto load_scales = [&](int t) __attribute__((always_inline)) {
+    if constexpr (kMx)
+      if (tid < BM + BN && k0 + t * kBK < k1) next_scales = Scales::load(scale_row, (k0 + t * kBK) / 8, g.K / 8);
+  };
+  [[maybe_unused]] auto store_scales = [&](int slot) __attribute__((always_inline)) {
+    if constexpr (kMx)
+      if (tid < BM + BN) Scales::store(scales + slot * Scales::kBytes, tid, next_scales);
+  };
+  if constexpr (kMx)
+    scale_row = tid < BM ? g.sa + (int64_t)min(m0 + tid, g.M - 1) * g.ldsa
+                         : g.sb + (int64_t)min(n0 + tid - BM, g.N - 1) * g.ldsb;
   auto compute = [&](int slot) __attribute__((always_inline)) {
     const lds_u16* A = lds + slot * kSlot;
     const lds_u16* B = A + BM * kBK;
@@ -276,6 +339,23 @@ __device__ __forceinline__ void gemm_tile(uint16_t* ring, G g, int mt, int nt, i
       for (int j = 0; j < FJ; ++j) fb[s][j] = Side<BT, BN, NW>::frag(B, wn * (BN / WN) + 16 * j, s, lane);
 #pragma unroll
       for (int i = 0; i < FI; ++i) fa[s][i] = Side<AT, BM, NW>::frag(A, wm * (BM / WM) + 16 * i, s, lane);
+    }
+    if constexpr (kMx) {
+      const lds_u8* stage = scales + slot * Scales::kBytes;
+      u32x2 wa[(FI + 3) / 4], wb[(FJ + 3) / 4];
+#pragma unroll
+      for (int i = 0; i < (FI + 3) / 4; ++i) wa[i] = Scales::words(stage, wm * (BM / WM) + 64 * i, lane);
+#pragma unroll
+      for (int j = 0; j < (FJ + 3) / 4; ++j) wb[j] = Scales::words(stage, BM + wn * (BN / WN) + 64 * j, lane);
+      static_for<2>([&](auto s) __attribute__((always_inline)) {
+        static_for<FI>([&](auto i) __attribute__((always_inline)) {
+          static_for<FJ>([&](auto j) __attribute__((always_inline)) {
+            acc[i][j] = mfma_mx<j % 4, i % 4>(fb[s][j], fa[s][i], acc[i][j], wb[j / 4][decltype(s)::value],
+                                                       wa[i / 4][decltype(s)::value]);
+          });
+        });
+      });
+      return;
     }
 #pragma unroll
     for (int s = 0; s < 2; ++s)
@@ -337,11 +417,18 @@ __device__ __forceinline__ void gemm_tile(uint16_t* ring, G g, int mt, int nt, i
       }
     }
   } else {
+    load_scales(0);
     if (stages > 0) issue(0, 0);
+    store_scales(0);
+    load_scales(1);
     for (int st = 0; st < stages; ++st) {
       __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
       barrier();
-      if (st + 1 < stages) issue((st + 1) & 1, st + 1);
+      if (st + 1 < stages) {
+        store_scales((st + 1) & 1);
+        load_scales(st + 2);
+        issue((st + 1) & 1, st + 1);
+      }
       compute(st & 1);
     }
   }
@@ -468,7 +555,7 @@ inline int sum_groups(const SumJob& j) { return j.out ? (j.cols + 15) / 16 : 0; 
 template <bool HALF, bool AT, bool BT, int BM, int BN, int WM, int WN, bool EPI, bool REGS = false, class G = GemmArgs>
 __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(G g, int mt, int nt, int total, int k_per_split,
                                                             float* __restrict__ part, int64_t ldpart) {
-  __shared__ __align__(1024) uint16_t ring[kRing<BM, BN>];
+  __shared__ __align__(1024) uint16_t ring[kRingOf<BM, BN, G>];
   if constexpr (BT && !AT)
     if ((int)blockIdx.x >= total) return sum_columns(reinterpret_cast<float*>(ring), g.sums, blockIdx.x - total);
   gemm_tile<HALF, AT, BT, BM, BN, WM, WN, EPI, REGS>(ring, g, mt, nt, xcd_lin(blockIdx.x, total), k_per_split, part,

@@ -65,6 +65,13 @@ struct GatedArgs : GemmArgs {
   int half, valid;
 };
 
+// The product of two operands in microscaled 4 bits, both K contiguous: a, b, their leading dimensions and K count
+// units of 16 bits, four codes each; K is whole blocks of 8 units.  A row has a scale byte to a block.
+struct MxArgs : GemmArgs {
+  const uint8_t *sa, *sb;
+  int64_t ldsa, ldsb;
+};
+
 // Up to here the skinny kernel: 2560 columns, K 5120: 10.4 us at 16 rows against 12.7 in
 // tiles; a form of it for 32 rows took 15.9 against 12.8.
 constexpr int kSkinnyRows = 16;
@@ -93,6 +100,7 @@ struct GemmSplit {
 GemmPlan plan_tiles(int M, int N, int K);  // rows are whole chunks on 16 bytes
 GemmPlan plan_linear(int M, int N, int K, int64_t ldx, int64_t ldw);
 GemmSplit split_of(const GemmPlan& p, int N, char* base);
+hipError_t launch_join_one(const GemmArgs& g, const GemmSplit& s, hipStream_t st);  // where it was split
 hipError_t launch_gemm(const GemmArgs& g, const GemmPlan& p, void* ws, hipStream_t st);
 // Both gradients' products, planned together.  Where they are paired (run in one launch) their workspaces lie one
 // behind the other, dx's first, else in the same place.
@@ -116,6 +124,8 @@ inline size_t padded_bytes(int rows, int cols) { return (size_t)rows * up8(cols)
 hipError_t launch_pad(const PadJob& first, const PadJob& second, hipStream_t st);
 hipError_t launch_gemm_bf16(const GemmArgs& g, const GemmSplit& s, int tile, hipStream_t st);
 hipError_t launch_gemm_f16(const GemmArgs& g, const GemmSplit& s, int tile, hipStream_t st);
+// `half`: a result of 16 bits is fp16, not bf16.
+hipError_t launch_mx_tiles(const MxArgs& g, const GemmSplit& s, int tile, bool half, hipStream_t st);
 hipError_t launch_gated_bf16(const GatedArgs& g, const GemmSplit& s, int tile, hipStream_t st);
 hipError_t launch_gated_f16(const GatedArgs& g, const GemmSplit& s, int tile, hipStream_t st);
 hipError_t launch_gated_pair_bf16(const GatedArgs& dx, const GemmSplit& sx, const GatedArgs& dw, const GemmSplit& sw,
@@ -130,6 +140,17 @@ hipError_t launch_gemm_pair_f16(const GemmArgs& dx, const GemmSplit& sx, const G
 template <bool HALF>
 __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
   return HALF ? mfma16x16x32_f16(a, b, c) : mfma16x16x32(a, b, c);
+}
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+// 16 x 16 outputs from 128 codes of each row, a block of 32 to a lane; SA and SB pick the scale's byte.
+template <int SA, int SB>
+__device__ __forceinline__ f32x4 mfma_mx(u32x4 a, u32x4 b, f32x4 c, uint32_t sa, uint32_t sb) {
+  const i32x8 wa = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+  const i32x8 wb = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+  constexpr int kE2M1 = 4;
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wa, wb, c, kE2M1, kE2M1, SA, (int)sa, SB, (int)sb);
 }
 
 // 1 / (1 + e^-z) from the hardware base-2 exponential and reciprocal, about 1 ulp each.

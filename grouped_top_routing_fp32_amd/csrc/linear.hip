@@ -335,6 +335,8 @@ static hipError_t launch_join(const JoinJob& first, const JoinJob& second, hipSt
   return hipGetLastError();
 }
 
+hipError_t launch_join_one(const GemmArgs& g, const GemmSplit& s, hipStream_t st) { return launch_join({g, s}, {}, st); }
+
 static PadJobs pad_jobs(const PadJob& first, const PadJob& second) {
   auto blocks = [](const PadJob& j) {
     const int64_t n = (j.rows * (up8(j.cols) / 8) + 255) / 256;

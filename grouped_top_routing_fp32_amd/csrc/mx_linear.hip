@@ -1,0 +1,152 @@
+// A matrix product with weights, or both operands, in microscaled 4 bits, with bias, activation and residual in its
+// epilogue (gfx950).
+//
+//   y = keep res + add act(x w^T + bias)
+//
+// Few rows are bound by reading w, a quarter of its 16-bit bytes: one kernel takes codes and scales straight from
+// memory.  With both operands in 4 bits the tiled product runs on scaled matrix instructions, four times the
+// 16-bit rate for the same bytes in LDS.  With x of 16 bits more rows take w as x's type, laid out once in the
+// workspace, and the plain product.
+#include <algorithm>
+
+#include "mxfp4.h"
+
+namespace beam {
+namespace {
+
+int ceil_div(int a, int b) { return (a + b - 1) / b; }
+constexpr int kCUs = 256;
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
+// Eight codes as eight 16-bit values.
+template <bool HALF>
+__device__ __forceinline__ u32x4 codes_to_16(uint32_t c, float s) {
+  if constexpr (HALF)
+    return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, 0)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, 1)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, 2)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, 3))};
+  else
+    return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 0)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 1)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 2)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 3))};
+}
+
+// Few rows (M <= 16).  A workgroup takes `cols` <= 16 columns and its 16 waves share K in pieces of 128: a lane
+// (row l % 16, block l / 16) takes one block of 32 codes, 16 bytes, and its scale.  With x of 16 bits the
+// products' K runs over the four blocks' first 8 elements, then their second 8, and so on, which is the same
+// sum.  The waves' sums are joined in LDS in wave order.
+template <bool HALF, bool FOUR>
+__global__ __launch_bounds__(64 * kSkinnyWaves) void mx_skinny_kernel(MxLinear a, int cols) {
+  __shared__ f32x4 sum[kSkinnyWaves][64];
+  const GemmArgs& g = a.g;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, gr = lane >> 4;
+  const int n0 = blockIdx.x * cols, n1 = min(g.N, n0 + cols), row = min(n0 + l16, n1 - 1), xr = min(l16, g.M - 1);
+  const uint8_t* wrow = a.w + row * a.ldw;
+  const uint8_t* wscale = a.w_scales + row * a.ldws;
+  const uint16_t* xrow = static_cast<const uint16_t*>(a.x) + xr * a.ldx;
+  const uint8_t* xcodes = static_cast<const uint8_t*>(a.x) + xr * a.ldx;
+  const uint8_t* xscale = FOUR ? a.x_scales + xr * a.ldxs : nullptr;
+  const int blocks = (g.K + kMxBlock - 1) / kMxBlock;
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  for (int b = 4 * wave + gr; b - gr < blocks; b += 4 * kSkinnyWaves) {
+    u32x4 w = {0u, 0u, 0u, 0u};
+    uint32_t ws = 0, xs = 0;
+    u32x4 x[4] = {};
+    if (b < blocks) {
+      w = ldg16(wrow + 16 * b);
+      ws = wscale[b];
+      if constexpr (FOUR) {
+        x[0] = ldg16(xcodes + 16 * b);
+        xs = xscale[b];
+      } else {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) x[s] = chunk_of_row(xrow, 32 * b + 8 * s, g.K);
+      }
+    }
+    if constexpr (FOUR) {
+      acc = mfma_mx<0, 0>(w, x[0], acc, ws, xs);
+    } else {
+      const float scale = mx_scale(ws);
+#pragma unroll
+      for (int s = 0; s < 4; ++s) acc = mfma<HALF>(codes_to_16<HALF>(w[s], scale), x[s], acc);
+    }
+  }
+  sum[wave][lane] = acc;
+  __syncthreads();
+  if (wave > 0) return;
+  f32x4 z = acc;
+#pragma unroll
+  for (int w = 1; w < kSkinnyWaves; ++w) {
+    const f32x4 v = sum[w][lane];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) z[q] += v[q];
+  }
+  const int n = n0 + 4 * gr;
+  if (l16 >= g.M || n >= n1) return;
+  by_act(g.act, [&](auto act) { epilogue4<decltype(act)::value>(g, g.add, l16, n, n1, z); });
+}
+
+}  // namespace
+
+MxPlan plan_mx(int M, int N, int K, bool four, int64_t ldx) {
+  MxPlan p{};
+  if (M <= kSkinnyRows) return p;
+  const int blocks = (int)mx_blocks(K);
+  if (four) {
+    p.gemm = plan_tiles(M, N, 8 * blocks);  // units of four codes
+    p.total = p.gemm.total;
+    return p;
+  }
+  p.copy_x = !regular_rows(ldx, K);
+  p.gemm = plan_tiles(M, N, (int)up8(K));
+  p.off_w = p.copy_x ? up256(padded_bytes(M, K)) : 0;
+  p.off_gemm = p.off_w + up256((size_t)N * blocks * kMxBlock * 2);
+  p.total = p.off_gemm + p.gemm.total;
+  return p;
+}
+
+hipError_t launch_linear_mx(const MxLinear& a, const MxPlan& p, void* ws, hipStream_t st) {
+  const int blocks = (int)mx_blocks(a.g.K);
+  const bool half = a.g.type == kElemF16;
+  char* base = static_cast<char*>(ws);
+  if (p.gemm.kind == GemmPlan::kSkinny) {
+    const int rounds = ceil_div(a.g.N, 16 * kCUs), cols = std::max(4, ceil_div(a.g.N, rounds * kCUs));
+    auto go = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, dim3(ceil_div(a.g.N, cols)), dim3(64 * kSkinnyWaves), 0, st, a, cols);
+      return hipGetLastError();
+    };
+    if (a.four) return go(mx_skinny_kernel<false, true>);
+    return half ? go(mx_skinny_kernel<true, false>) : go(mx_skinny_kernel<false, false>);
+  }
+  hipError_t e;
+  if (a.four) {
+    MxArgs g{a.g, a.x_scales, a.w_scales, a.ldxs, a.ldws};
+    g.a = a.x;
+    g.lda = a.ldx / 2;
+    g.b = a.w;
+    g.ldb = a.ldw / 2;
+    g.K = 8 * blocks;
+    const GemmSplit s = split_of(p.gemm, g.N, base);
+    e = launch_mx_tiles(g, s, p.gemm.tile, half, st);
+    return e != hipSuccess ? e : launch_join_one(g, s, st);
+  }
+  GemmArgs g = a.g;
+  g.a = a.x;
+  g.lda = a.ldx;
+  if (p.copy_x) {
+    const PadJob j{a.x, a.ldx, g.M, g.K, base};
+    if ((e = launch_pad(j, {}, st)) != hipSuccess) return e;
+    g.a = j.dst;
+    g.lda = up8(g.K);
+  }
+  g.b = base + p.off_w;
+  g.ldb = blocks * kMxBlock;
+  g.K = (int)up8(g.K);
+  e = launch_dequantize_mx(a.w, a.ldw, a.w_scales, a.ldws, base + p.off_w, g.type, g.ldb, g.N, blocks * kMxBlock, st);
+  return e != hipSuccess ? e : launch_gemm(g, p.gemm, base + p.off_gemm, st);
+}
+
+}  // namespace beam

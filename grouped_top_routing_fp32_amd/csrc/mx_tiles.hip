@@ -1,0 +1,21 @@
+// The tiled product of 4-bit operands (gfx950).
+#include "gemm_tiles.h"
+
+namespace beam {
+
+hipError_t launch_mx_tiles(const MxArgs& g, const GemmSplit& s, int tile, bool half, hipStream_t st) {
+  const int mt = (g.M + tile - 1) / tile, nt = (g.N + tile - 1) / tile, total = mt * nt * s.splits;
+  auto go = [&](auto kernel, int threads) {
+    hipLaunchKernelGGL(kernel, dim3(total), dim3(threads), 0, st, g, mt, nt, total, s.k_per_split, s.part, s.ld);
+    return hipGetLastError();
+  };
+  auto of = [&](auto h) {
+    constexpr bool kHalf = decltype(h)::value;
+    if (tile == 256) return go(gemm_kernel<kHalf, false, false, 256, 256, 4, 2, true, false, MxArgs>, 512);
+    if (tile == 128) return go(gemm_kernel<kHalf, false, false, 128, 128, 2, 2, true, false, MxArgs>, 256);
+    return go(gemm_kernel<kHalf, false, false, 64, 64, 2, 2, true, false, MxArgs>, 256);
+  };
+  return half ? of(std::true_type{}) : of(std::false_type{});
+}
+
+}  // namespace beam

@@ -4,7 +4,7 @@
 // to a byte, the first in the low half.  A scale byte e stands for 2^(e - 127), 255 for NaN.
 #pragma once
 
-#include "elem.h"
+#include "linear.h"
 
 namespace beam {
 
@@ -13,10 +13,9 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 inline int64_t mx_blocks(int64_t cols) { return (cols + kMxBlock - 1) / kMxBlock; }
 
-// A scale byte as FP32: its exponent field; 2^-127 is subnormal.
-__device__ __forceinline__ float mx_scale(uint32_t e) {
-  return __uint_as_float(e == 255u ? 0x7fc00000u : e == 0u ? 0x00400000u : e << 23);
-}
+// A scale byte as the FP32 that the converting instructions take.  They read its exponent field alone: 0 is
+// 2^-127 to them, and 255 makes every result NaN.
+__device__ __forceinline__ float mx_scale(uint32_t e) { return __uint_as_float(e << 23); }
 
 // The scale byte of a block whose largest magnitude has the bits `top` (FP32): 2^(floor(log2) - 2),
 // so that the largest lies in [4, 8) of it.  Subnormals are floored to FP32's least normal.  An infinity or NaN
@@ -30,5 +29,26 @@ hipError_t launch_quantize_mx(const void* x, int type, int64_t ldx, uint8_t* cod
                               int64_t lds, int rows, int cols, hipStream_t st);
 hipError_t launch_dequantize_mx(const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds, void* y, int type,
                                 int64_t ldy, int rows, int cols, hipStream_t st);
+
+// y = keep res + add act(x w^T + bias), w in 4 bits; x of one of the 16-bit types, or in 4 bits too.
+struct MxLinear {
+  GemmArgs g;                // M, N, K and the epilogue; type is the 16-bit type of x, or of a 16-bit result
+  bool four;                 // x is codes
+  const void* x;
+  int64_t ldx;               // elements; codes: bytes
+  const uint8_t* x_scales;
+  int64_t ldxs;
+  const uint8_t* w;
+  int64_t ldw;               // bytes
+  const uint8_t* w_scales;
+  int64_t ldws;
+};
+struct MxPlan {
+  GemmPlan gemm;
+  bool copy_x;               // x is laid out anew in the workspace, and w as x's type behind it
+  size_t off_w, off_gemm, total;
+};
+MxPlan plan_mx(int M, int N, int K, bool four, int64_t ldx);
+hipError_t launch_linear_mx(const MxLinear& a, const MxPlan& p, void* ws, hipStream_t st);
 
 }  // namespace beam

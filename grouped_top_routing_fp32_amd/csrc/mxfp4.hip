@@ -38,7 +38,7 @@ __device__ __forceinline__ void from_codes(uint32_t c, uint32_t e, float* v) {
   const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 2), f = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 3);
   const float r[8] = {a[0], a[1], b[0], b[1], d[0], d[1], f[0], f[1]};
 #pragma unroll
-  for (int q = 0; q < 8; ++q) v[q] = e == 255u ? s : r[q];
+  for (int q = 0; q < 8; ++q) v[q] = r[q];
 }
 
 // A workgroup's 256 threads are `wide` (a power of two, from 4 on) along a row and the rest down the

@@ -319,7 +319,12 @@ int beam_moe_stream_rows(const beam_moe_dims* dims, int32_t T, int fp8);
  *   norm, a token of the router's gradient or a row of a product that holds
  *   one does not touch the others (column sums hold all rows).
  * ------------------------------------------------------------------------- */
-enum { BEAM_MOE_BF16 = 0, BEAM_MOE_F16 = 1, BEAM_MOE_F32 = 2 };
+enum {
+  BEAM_MOE_BF16 = 0,
+  BEAM_MOE_F16 = 1,
+  BEAM_MOE_F32 = 2,
+  BEAM_MOE_MXFP4 = 3 /* beam_moe_linear_mxfp4's x alone */
+};
 enum {
   BEAM_MOE_ACT_NONE = 0,
   BEAM_MOE_ACT_RELU = 1, /* z < 0 ? 0 : z, slope 0 at 0 */
@@ -552,6 +557,26 @@ int beam_moe_quantize_mxfp4(int32_t rows, int32_t cols, const void* x, int x_typ
  * in the others where they hold the value). */
 int beam_moe_dequantize_mxfp4(int32_t rows, int32_t cols, const uint8_t* codes, int64_t ldc, const uint8_t* scales,
                               int64_t lds, void* y, int y_type, int64_t ldy, void* stream);
+
+/* Workspace of beam_moe_linear_mxfp4.  Returns SIZE_MAX for unsupported sizes. */
+size_t beam_moe_linear_mxfp4_workspace_bytes(int32_t rows, int32_t cols, int32_t inner, int x_type, int64_t ldx);
+
+/* beam_moe_linear with weights in MXFP4, and x in a 16-bit type or in MXFP4 as well:
+ *   z = x w^T + bias,  y = keep * res + add * act(z)
+ *   x_type    BEAM_MOE_BF16, _F16, or BEAM_MOE_MXFP4: then x are codes, ldx their row stride in bytes, and
+ *             x_scales, ldxs their scales (NULL, 0 else)
+ *   x         [rows, inner]
+ *   w, w_scales   codes and scales of [cols, inner], row strides ldw (a multiple of 16) and ldws in bytes
+ *   y_type    x's type or BEAM_MOE_F32; any element type where x is in MXFP4
+ *   bias, act, res, keep, add, y   as in beam_moe_linear
+ * Codes past inner in the last block are 0.  With a 16-bit x the weights are taken as values of its type, which
+ * holds them exactly where their scales lie in 2 .. 252 (bf16) or 104 .. 140 (fp16).  Products are exact and summed in
+ * FP32; a scale of NaN makes its row's, or its column's, results NaN.
+ * 0 <= rows <= 2^20, 1 <= cols, inner <= 2^18. */
+int beam_moe_linear_mxfp4(int32_t rows, int32_t cols, int32_t inner, int x_type, const void* x, int64_t ldx,
+                          const uint8_t* x_scales, int64_t ldxs, const uint8_t* w, int64_t ldw, const uint8_t* w_scales,
+                          int64_t ldws, const float* bias, int act, const void* res, int64_t ldr, float keep, float add,
+                          void* y, int y_type, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
 
 /* Static string for a status code. */
 const char* beam_moe_status_str(int status);

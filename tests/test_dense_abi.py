@@ -40,10 +40,18 @@ QUANT = Call("beam_moe_quantize_mxfp4", rows=4, cols=70, x=FAKE, x_type=BF16, ld
 DEQUANT = Call("beam_moe_dequantize_mxfp4", rows=4, cols=70, codes=FAKE, ldc=48, scales=FAKE, lds=3, y=FAKE,
                y_type=BF16, ldy=70, stream=None)
 
+MX = binding.BEAM_MOE_MXFP4
+MX_LINEAR = Call("beam_moe_linear_mxfp4", rows=4, cols=10, inner=70, x_type=BF16, x=FAKE, ldx=70, x_scales=None, ldxs=0,
+                 w=FAKE, ldw=48, w_scales=FAKE, ldws=3, bias=FAKE, act=1, res=FAKE, ldr=10, keep=0.5, add=0.5,
+                 y=ctypes.c_void_p(2 << 20), y_type=F32, ldy=10, ws=FAKE, ws_bytes=1 << 40, stream=None)
+MX_BOTH = Call("beam_moe_linear_mxfp4", **{**MX_LINEAR.defaults, "x_type": MX, "ldx": 48, "x_scales": FAKE, "ldxs": 3})
+
 
 @pytest.mark.parametrize("call, required, optional", [
     (NORM, ("norm",), ()), (CLIP, (), ("norm", "norm_in")), (QUANT, ("x", "codes", "scales"), ()),
     (DEQUANT, ("codes", "scales", "y"), ()),
+    (MX_LINEAR, ("x", "w", "w_scales", "y"), ("bias", "res")),
+    (MX_BOTH, ("x", "x_scales", "w", "w_scales", "y"), ("bias", "res")),
     (GATED, ("x", "w_gate", "w_up", "h"), ("bias_gate", "bias_up", "pre_gate", "pre_up")),
     (GATED_BACK, ("dh", "pre_gate", "pre_up"), ("x", "w_gate", "w_up", "dx", "dw_gate", "dw_up", "dbias_gate",
                                                 "dbias_up")),
@@ -74,6 +82,14 @@ def test_pointers(call, required, optional):
     (QUANT, dict(ldc=56)), (QUANT, dict(lds=2)), (QUANT, dict(lds=1 << 41)),
     (DEQUANT, dict(rows=-1)), (DEQUANT, dict(y_type=-1)), (DEQUANT, dict(ldy=69)), (DEQUANT, dict(ldc=40)),
     (DEQUANT, dict(lds=2)),
+    (MX_LINEAR, dict(x_type=F32)), (MX_LINEAR, dict(x_type=4)), (MX_LINEAR, dict(y_type=F16)),
+    (MX_LINEAR, dict(ldx=69)), (MX_BOTH, dict(y_type=3)), (MX_BOTH, dict(ldx=32)), (MX_BOTH, dict(ldx=56)),
+    (MX_BOTH, dict(ldxs=2)),
+] + [
+    (c, b) for c in (MX_LINEAR, MX_BOTH) for b in (
+        dict(rows=-1), dict(act=4), dict(act=-1), dict(keep=float("nan")), dict(add=float("inf")), dict(ldw=32),
+        dict(ldw=56), dict(ldws=2), dict(ldy=9), dict(ldr=9), dict(y=FAKE, ldy=11), dict(ldw=1 << 41))
+] + [
     (GATED, dict(rows=-1)), (GATED, dict(type=F32)), (GATED, dict(h_type=F16)), (GATED, dict(act=4)),
     (GATED, dict(act=-1)), (GATED, dict(ldx=11)), (GATED, dict(ldg=11)), (GATED, dict(ldu=11)), (GATED, dict(ldh=9)),
     (GATED, dict(ldpg=9)), (GATED, dict(ldpu=9)), (GATED, dict(ldx=1 << 41)),
@@ -93,6 +109,9 @@ def test_invalid_arguments(call, bad):
     (NORM, dict(count=(1 << 16) + 1)), (CLIP, dict(count=(1 << 16) + 1)), (NORM, dict(sizes=sizes(5, (1 << 40) + 1))),
     (QUANT, dict(rows=(1 << 20) + 1)), (QUANT, dict(cols=(1 << 18) + 1)), (QUANT, dict(cols=0)),
     (DEQUANT, dict(rows=(1 << 20) + 1)), (DEQUANT, dict(cols=(1 << 18) + 1)), (DEQUANT, dict(cols=0)),
+] + [
+    (c, b) for c in (MX_LINEAR, MX_BOTH) for b in (dict(rows=(1 << 20) + 1), dict(cols=(1 << 18) + 1), dict(cols=0),
+                                                   dict(inner=(1 << 18) + 1), dict(inner=0))
 ] + [
     (c, b) for c in (GATED, GATED_BACK) for b in (dict(rows=(1 << 20) + 1), dict(cols=(1 << 17) + 1), dict(cols=0),
                                                   dict(inner=(1 << 18) + 1), dict(inner=0))
@@ -137,8 +156,20 @@ def test_gated_workspaces():
         assert GATED_BACK(**bad) == WS
 
 
+def test_mx_workspaces():
+    need = binding.load_library().beam_moe_linear_mxfp4_workspace_bytes
+    assert need(16, 1000, 1000, BF16, 1000) == 0 and need(16, 1000, 1000, MX, 512) == 0
+    assert need(8192, 2560, 5120, MX, 2560) == 0
+    assert need(64, 2560, 5120, BF16, 5120) >= 2560 * 5120 * 2
+    assert need(-1, 8, 8, BF16, 8) == need(8, 8, 8, BF16, 7) == need(8, 8, 8, MX, 8) == need(8, 8, 8, F32, 8) \
+        == need(8, 0, 8, BF16, 8) == binding.SIZE_MAX
+    n = need(64, 10, 70, BF16, 70)
+    for bad in (dict(ws=None), dict(ws=ODD), dict(ws_bytes=n - 1)):
+        assert MX_LINEAR(rows=64, **bad) == WS
+
+
 def test_no_rows():
-    for call in (QUANT, DEQUANT, GATED):
+    for call in (QUANT, DEQUANT, GATED, MX_LINEAR, MX_BOTH):
         assert call(rows=0) == OK
 
 

@@ -710,3 +710,161 @@ def test_gated_linear_offsets_past_32_bits():
     fw.beam_moe_gated_linear(x, wg, wu, out=h)
     _gated_check(x[-300:], wg, wu, None, None, "silu", h[-300:])
     assert not h[:100].any()
+
+
+# --------------------------------------------------------------------------
+# the product of 4-bit operands
+# --------------------------------------------------------------------------
+def _mx_weights(g, N, K, pad=0, spread=2):
+    """Random codes and scales of a deviation of about K^-1/2, zero codes past K; rows in wider buffers with pad."""
+    blocks = -(-K // 32)
+    code = torch.randint(0, 16, (N, 32 * blocks), generator=g, device=DEV)
+    code[:, K:] = 0
+    mid = 127 - round(0.5 * math.log2(K)) - 2
+    codes = torch.full((N, 16 * blocks + 16 * pad), 0x77, dtype=torch.uint8, device=DEV)
+    codes[:, : 16 * blocks] = _pack(code)
+    scales = torch.full((N, blocks + pad), 255, dtype=torch.uint8, device=DEV)
+    scales[:, :blocks] = torch.randint(mid - spread, mid + spread + 1, (N, blocks), generator=g, device=DEV)
+    return fw.Mxfp4(codes[:, : 16 * blocks], scales[:, :blocks])
+
+
+def _mx_values(q, K):
+    code = torch.stack([q.codes & 15, q.codes >> 4], 2).view(q.codes.shape[0], -1).long()
+    size = torch.tensor(VALUES, dtype=torch.float64, device=DEV)
+    v = torch.cat([size, -size])[code].view(code.shape[0], -1, 32)
+    scale = torch.exp2(q.scales.double() - 127)
+    scale[q.scales == 255] = NAN
+    return (v * scale[..., None]).view(code.shape[0], -1)[:, :K]
+
+
+def _mx_linear_check(x, w, bias, act, res, keep, add, y):
+    """x and w [.., K] in 64 bits; products are exact, sums of depth d, the activation as in the gated product's."""
+    z, mag = x @ w.t(), x.abs() @ w.abs().t()
+    if bias is not None:
+        z, mag = z + bias.double(), mag + bias.double().abs()
+    ry = add * ACTS[act](z)
+    extra = 0.0
+    if res is not None:
+        ry, extra = ry + keep * res.double(), 2 * U * (keep * res.double()).abs()
+    # a matrix instruction adds up to 128 products; 32 + K / 32 + 40 covers them and the splits
+    dz = (128 + _depth(x.shape[1])) * GEMM_UP * mag
+    _near(y, ry, abs(add) * (1.13 * dz + 8 * U * (z.abs() + (act != "none"))) + 2 * U * ry.abs() + extra, "y")
+
+
+MX_LINEAR = [(1, 1, 1), (1, 64, 64), (1, 100, 1000), (2, 2560, 512), (3, 17, 5), (7, 33, 2049), (16, 256, 128),
+             (17, 48, 96), (33, 1000, 136), (64, 512, 2560), (65, 130, 72), (100, 64, 7), (129, 257, 65), (255, 96, 520),
+             (256, 256, 64), (300, 513, 1024), (257, 264, 192), (520, 1040, 328), (1000, 1032, 2048), (2100, 2560, 1280),
+             (3300, 3336, 136), (100, 100, 65536), (300, 300, 16384), (2048, 2100, 8200)]
+
+
+@pytest.mark.parametrize("M,N,K", MX_LINEAR)
+@pytest.mark.parametrize("dt", [BF16, F16])
+def test_linear_mxfp4(M, N, K, dt):
+    """x in 16 bits."""
+    g = _gen(M * 3 + N * 5 + K)
+    for act, yt, res, pad in (("none", dt, False, 0), ("silu", F32, True, 0), ("gelu", dt, True, 8), ("relu", dt, False, 3)):
+        _say("linear_mxfp4", M, N, K, dt, act, yt, res, pad)
+        x, w = _randn(g, (M, K), dt, 1.0, pad), _mx_weights(g, N, K, pad)
+        bias = _randn(g, (N,)) if act != "relu" else None
+        r = _randn(g, (M, N), yt, 1.0, pad) if res else None
+        keep, add = (math.sqrt(2 / 3), math.sqrt(1 / 3)) if res else (1.0, 1.0)
+        y = fw.beam_moe_linear_mxfp4(x, w, bias, act=act, residual=r, keep=keep, add=add, out_dtype=yt)
+        _mx_linear_check(x.double(), _mx_values(w, K), bias, act, r, keep, add, y)
+
+
+@pytest.mark.parametrize("M,N,K", MX_LINEAR)
+def test_linear_mxfp4_of_two(M, N, K):
+    """Both operands in 4 bits."""
+    g = _gen(M * 3 + N * 5 + K + 1)
+    for act, yt, res, pad in (("none", BF16, False, 0), ("silu", F32, True, 0), ("gelu", F16, True, 1),
+                              ("relu", F16, False, 3), ("none", F32, False, 0)):
+        _say("linear_mxfp4 of two", M, N, K, act, yt, res, pad)
+        x, w = _mx_weights(g, M, K, pad, 3), _mx_weights(g, N, K, pad)
+        bias = _randn(g, (N,)) if act != "relu" else None
+        r = _randn(g, (M, N), yt, 1.0, pad) if res else None
+        keep, add = (math.sqrt(2 / 3), math.sqrt(1 / 3)) if res else (1.0, 1.0)
+        y = fw.beam_moe_linear_mxfp4(x, w, bias, act=act, residual=r, keep=keep, add=add, out_dtype=yt)
+        _mx_linear_check(_mx_values(x, K), _mx_values(w, K), bias, act, r, keep, add, y)
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 40, 100), (70, 90, 1003), (300, 264, 128)])
+def test_linear_mxfp4_places(M, N, K):
+    """Each block of K by itself: one code of x and of w set, every other zero, so that a wrong block, scale or order
+    shows whatever the values; scales differ in every block."""
+    _say("linear_mxfp4 places", M, N, K)
+    blocks = -(-K // 32)
+    g = _gen(K)
+    xs = torch.randint(100, 150, (M, blocks), generator=g, device=DEV).to(torch.uint8)
+    ws = torch.randint(100, 150, (N, blocks), generator=g, device=DEV).to(torch.uint8)
+    for k in sorted({0, 1, 31, 32, K // 2, K - 1}):
+        code = torch.zeros(max(M, N), 32 * blocks, dtype=torch.int64, device=DEV)
+        code[:, k] = torch.randint(1, 16, (max(M, N),), generator=g, device=DEV)
+        x, w = fw.Mxfp4(_pack(code[:M]), xs), fw.Mxfp4(_pack(code[:N].flip(0)), ws)
+        want = _mx_values(x, K) @ _mx_values(w, K).t()
+        assert torch.equal(fw.beam_moe_linear_mxfp4(x, w, out_dtype=F32).double(), want)
+        got = fw.beam_moe_linear_mxfp4(_mx_values(x, K).to(BF16), w, out_dtype=F32)
+        assert torch.equal(got.double(), want)
+
+
+@pytest.mark.parametrize("M", [5, 70, 300])
+def test_linear_mxfp4_in_place_padding_and_nan(M):
+    _say("linear_mxfp4 places and nan", M)
+    N, K = 70, 100
+    g = _gen(M)
+    w, x = _mx_weights(g, N, K, 1), _randn(g, (M, K), BF16)
+    q = fw.beam_moe_quantize_mxfp4(x)
+    for a in (x, q):
+        buf = torch.full((M, N + 9), 7.0, device=DEV)
+        buf[:, :N] = _randn(g, (M, N))
+        want = fw.beam_moe_linear_mxfp4(a, w, residual=buf[:, :N], keep=0.5, out_dtype=F32)
+        fw.beam_moe_linear_mxfp4(a, w, residual=buf[:, :N], keep=0.5, out=buf[:, :N])
+        assert torch.equal(buf[:, :N], want) and (buf[:, N:] == 7.0).all()
+        assert torch.equal(fw.beam_moe_linear_mxfp4(a, w), fw.beam_moe_linear_mxfp4(a, w))
+    # NaN of one row of x, and of one block of one column of w
+    want = fw.beam_moe_linear_mxfp4(q, w)
+    q.scales[M // 2, 1] = 255
+    got = fw.beam_moe_linear_mxfp4(q, w)
+    rows = torch.arange(M, device=DEV) != M // 2
+    assert torch.equal(got[rows], want[rows]) and got[M // 2].isnan().all()
+    want = fw.beam_moe_linear_mxfp4(x, w)
+    w.scales[9, 2] = 255
+    cols = torch.arange(N, device=DEV) != 9
+    for a, was in ((x, want), (q, got)):
+        got = fw.beam_moe_linear_mxfp4(a, w)
+        assert torch.equal(got[:, cols].nan_to_num(), was[:, cols].nan_to_num()) and got[:, 9].isnan().all()
+
+
+def test_linear_mxfp4_scales_at_the_ends():
+    """Scales at the ends of their range: 2^-127 times 2^127, and products that leave FP32 in neither direction."""
+    _say("linear_mxfp4 ends")
+    for M in (4, 40):
+        K, N = 64, 48
+        g = _gen(M)
+        code = torch.randint(0, 16, (max(M, N), K), generator=g, device=DEV)
+        for xs, ws in ((0, 254), (254, 0), (1, 250), (0, 127), (127, 127), (100, 10)):
+            x = fw.Mxfp4(_pack(code[:M]), torch.full((M, 2), xs, dtype=torch.uint8, device=DEV))
+            w = fw.Mxfp4(_pack(code[:N]), torch.full((N, 2), ws, dtype=torch.uint8, device=DEV))
+            vx, vw = _mx_values(x, K), _mx_values(w, K)
+            y = fw.beam_moe_linear_mxfp4(x, w, out_dtype=F32)
+            _near(y, vx @ vw.t(), 200 * GEMM_UP * (vx.abs() @ vw.abs().t()) + 64 * 2.0 ** -149)
+
+
+def test_serving_a_gated_sublayer_in_four_bits():
+    """The sublayer of the training step with its weights quantised once: both projections of the quantised weights,
+    the activation and the product, and the down projection onto the stream, against 64 bits on the same quantised
+    weights. Four roundings to bf16 lie on the way (norm, gate, up, h)."""
+    _say("serving in four bits")
+    for T in (1, 9, 192):
+        s = _gated_step_inputs(1, T)
+        q = {k: fw.beam_moe_quantize_mxfp4(s[k]) for k in ("wg", "wu", "wd")}
+        x, _, _ = fw.beam_moe_layer_norm(s["stream"], s["gamma"], s["beta"], out_dtype=BF16)
+        gate = fw.beam_moe_linear_mxfp4(x, q["wg"], s["bg"], act="silu")
+        up = fw.beam_moe_linear_mxfp4(x, q["wu"], s["bu"])
+        out = fw.beam_moe_linear_mxfp4(gate * up, q["wd"], residual=s["stream"], keep=0.8, add=0.6, out_dtype=F32)
+        w = {k: fw.beam_moe_dequantize_mxfp4(v, s[k].shape[1], out_dtype=F32).double() for k, v in q.items()}
+        xr = torch.nn.functional.layer_norm(s["stream"].double(), (s["stream"].shape[1],), s["gamma"].double(),
+                                            s["beta"].double(), 1e-5)
+        h = torch.nn.functional.silu(xr @ w["wg"].t() + s["bg"].double()) * (xr @ w["wu"].t() + s["bu"].double())
+        want = 0.8 * s["stream"].double() + 0.6 * (h @ w["wd"].t())
+        err = float((out.double() - want).norm() / want.norm())
+        assert err <= 8 * 2.0 ** -9, (T, err)
