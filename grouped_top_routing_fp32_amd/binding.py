@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 from array import array
 from typing import NamedTuple, Optional, Sequence
@@ -585,6 +586,7 @@ def _linear_ws(fn: str, *sizes: int) -> int:
 
 
 _FLOATS = tuple(ELEM_TYPES)
+_FLOAT_SET = frozenset(ELEM_TYPES)
 _F32 = torch.float32
 
 
@@ -822,31 +824,36 @@ def beam_moe_gated_linear_backward(dh: torch.Tensor, x: Optional[torch.Tensor], 
     return dx, dwg, dwu, dbg, dbu
 
 
+_Tensor = torch.Tensor
+_dtype_of = operator.attrgetter("dtype")
+
+
 def _dense(t: torch.Tensor) -> bool:
     """Whether t's elements fill one stretch of memory: contiguous, or a matrix's transpose."""
     return t.is_contiguous() or (t.dim() == 2 and t.t().is_contiguous())
 
 
 def _list_of(tensors: Sequence[torch.Tensor], name: str):
-    """(tensors, device, addresses, types, sizes) of a list of gradients; the last three as C arrays."""
+    """(tensors, device, addresses, types, sizes, all contiguous) of a list of gradients, addresses, types and sizes
+    as C arrays. Each attribute in a pass of its own: half the time of a loop over the tensors (0.2 us a tensor)."""
     ts = tensors if isinstance(tensors, (list, tuple)) else list(tensors)
     if not ts:
         raise ValueError(f"{name} must hold at least one tensor")
-    dev = ts[0].device
-    types = array("i")
-    sizes = array("q")
-    at = array("Q")
-    for t in ts:
-        kind = ELEM_TYPES.get(t.dtype)
-        if kind is None or t.device != dev or not _dense(t):
-            raise ValueError(f"{name} must be dense tensors of one of {_FLOATS} on {dev}, got {t.dtype} with strides "
-                             f"{t.stride()} on {t.device}")
-        types.append(kind)
-        sizes.append(t.numel())
-        at.append(t.data_ptr())
-    if dev.type != "cuda":
-        raise ValueError(f"{name} must be device tensors")
-    return ts, dev, at, types, sizes
+    kinds = set(map(_dtype_of, ts))
+    if not kinds <= _FLOAT_SET:
+        raise ValueError(f"{name} must be of {_FLOATS}, got {kinds - _FLOAT_SET}")
+    devices = set(map(_Tensor.get_device, ts))
+    if len(devices) > 1 or -1 in devices:
+        raise ValueError(f"{name} must be tensors on one device")
+    straight = all(map(_Tensor.is_contiguous, ts))
+    if not straight and not all(map(_dense, ts)):
+        raise ValueError(f"{name} must be dense tensors (contiguous, or a matrix's transpose)")
+    if len(kinds) == 1:
+        types = array("i", (ELEM_TYPES[ts[0].dtype],)) * len(ts)
+    else:
+        types = array("i", [ELEM_TYPES[k] for k in map(_dtype_of, ts)])
+    return (ts, ts[0].device, array("Q", map(_Tensor.data_ptr, ts)), types, array("q", map(_Tensor.numel, ts)),
+            straight)
 
 
 def _addr(a: array) -> int:
@@ -857,7 +864,7 @@ def beam_moe_grad_norm(grads: Sequence[torch.Tensor], *, scale: float = 1.0, ws:
                        stream=None) -> torch.Tensor:
     """The norm of all gradients, times |scale|, as a fp32 scalar on the device. grads: tensors of bf16, fp16 or
     fp32 in any mixture, each dense."""
-    ts, dev, at, types, sizes = _list_of(grads, "grads")
+    ts, dev, at, types, sizes, _ = _list_of(grads, "grads")
     lib = load_library()
     with _On(dev, stream) as st:
         norm = torch.empty((), dtype=_F32, device=dev)
@@ -870,25 +877,25 @@ def beam_moe_grad_norm(grads: Sequence[torch.Tensor], *, scale: float = 1.0, ws:
 def beam_moe_clip_grads(grads: Sequence[torch.Tensor], max_norm: float, *, scale: float = 1.0, eps: float = 1e-6,
                         norm: Optional[torch.Tensor] = None, out: Optional[Sequence[torch.Tensor]] = None,
                         ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """g * scale * min(1, max_norm / (norm + eps)) for all gradients, in place or, with out, into tensors of the
-    same shapes and strides and any of the types. The norm is that of all gradients times |scale|, or the given fp32
-    scalar. Returns the norm (before clipping)."""
-    ts, dev, at, types, sizes = _list_of(grads, "grads")
+    """g * scale * min(1, max_norm / (norm + eps)) for all gradients, in place or, with out, into as many tensors of
+    any of the types: contiguous ones of as many elements (views of a flat buffer, say), and the same shape and strides
+    where a gradient is not contiguous. The norm is that of all gradients times |scale|, or the given fp32 scalar.
+    Returns the norm (before clipping)."""
+    ts, dev, at, types, sizes, straight = _list_of(grads, "grads")
     ot, okinds = None, None
     if out is not None:
-        os_, odev, ot, okinds, _ = _list_of(out, "out")
-        if odev != dev or len(os_) != len(ts) or any(a.shape != b.shape or a.stride() != b.stride()
-                                                     for a, b in zip(ts, os_)):
-            raise ValueError("out must hold a tensor of each gradient's shape and strides, on its device")
+        os_, odev, ot, okinds, osizes, ostraight = _list_of(out, "out")
+        if odev != dev or osizes != sizes or not (straight and ostraight) and any(
+                a.shape != b.shape or a.stride() != b.stride() for a, b in zip(ts, os_)):
+            raise ValueError("out must hold a tensor of each gradient's size, on its device")
     if norm is not None and (norm.numel() != 1 or norm.dtype != _F32 or norm.device != dev):
         raise ValueError(f"norm must be one fp32 element on {dev}")
     lib = load_library()
     with _On(dev, stream) as st:
-        wp, wn, _keep = None, 0, None
         given = norm
         if given is None:
             norm = torch.empty((), dtype=_F32, device=dev)
-            wp, wn, _keep = _scratch(lib.beam_moe_grad_norm_workspace_bytes(len(ts)), ws, dev, "beam_moe_clip_grads")
+        wp, wn, _keep = _scratch(lib.beam_moe_grad_norm_workspace_bytes(len(ts)), ws, dev, "beam_moe_clip_grads")
         _check(lib.beam_moe_clip_grads(
             len(ts), _addr(at), _addr(types), _addr(sizes), scale, max_norm, eps,
             None if given is None else given.data_ptr(), None if ot is None else _addr(ot),

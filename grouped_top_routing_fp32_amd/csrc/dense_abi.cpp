@@ -26,7 +26,7 @@ using beam::type_ok;
 
 constexpr int32_t kMaxGrads = 1 << 16;
 constexpr int64_t kMaxGradSize = int64_t(1) << 40;
-constexpr int64_t kMaxGradTotal = int64_t(1) << 44;  // chunks fit 32 bits
+constexpr int64_t kMaxGradTotal = int64_t(1) << 42;  // chunks fit 32 bits
 constexpr int32_t kMaxMxRows = 1 << 20;
 constexpr int32_t kMaxMxCols = 1 << 18;
 
@@ -50,21 +50,42 @@ int check_grads(int32_t count, const void* const* grads, const int32_t* types, c
 bool apart(const std::vector<beam::GradTensor>& t) {
   struct Span {
     uintptr_t a, b;
-    int64_t of;  // a gradient's index, or ~ an output's
+    bool out;
   };
+  auto grad = [](const beam::GradTensor& k) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(k.p);
+    return Span{p, p + k.n * elem_bytes(k.type), false};
+  };
+  auto out = [](const beam::GradTensor& k) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(k.out);
+    return Span{p, p + k.n * elem_bytes(k.out_type), true};
+  };
+  auto replaced = [](const beam::GradTensor& k) { return k.p == k.out && k.type == k.out_type; };
+  // outputs in order, and no gradient among them, as with a flat buffer: no sorting
+  uintptr_t first = UINTPTR_MAX, last = 0;
+  bool ordered = true;
+  for (const auto& k : t) {
+    const Span o = out(k);
+    ordered = ordered && o.a >= last;
+    first = std::min(first, o.a);
+    last = std::max(last, o.b);
+  }
+  if (ordered && std::none_of(t.begin(), t.end(), [&](const beam::GradTensor& k) {
+        const Span g = grad(k);
+        return !replaced(k) && g.a < last && g.b > first;
+      }))
+    return true;
   std::vector<Span> spans;
   spans.reserve(2 * t.size());
-  for (size_t i = 0; i < t.size(); ++i) {
-    if (t[i].n == 0) continue;
-    const uintptr_t p = reinterpret_cast<uintptr_t>(t[i].p), o = reinterpret_cast<uintptr_t>(t[i].out);
-    spans.push_back({o, o + t[i].n * elem_bytes(t[i].out_type), ~(int64_t)i});
-    if (p != o || t[i].type != t[i].out_type) spans.push_back({p, p + t[i].n * elem_bytes(t[i].type), (int64_t)i});
+  for (const auto& k : t) {
+    spans.push_back(out(k));
+    if (!replaced(k)) spans.push_back(grad(k));
   }
   std::sort(spans.begin(), spans.end(), [](const Span& x, const Span& y) { return x.a < y.a; });
   uintptr_t out_end = 0, grad_end = 0;  // of what lies before
   for (const Span& s : spans) {
-    if (s.a < out_end || (s.of < 0 && s.a < grad_end)) return false;
-    uintptr_t& end = s.of < 0 ? out_end : grad_end;
+    if (s.a < out_end || (s.out && s.a < grad_end)) return false;
+    uintptr_t& end = s.out ? out_end : grad_end;
     end = std::max(end, s.b);
   }
   return true;
@@ -264,7 +285,7 @@ int beam_moe_gated_linear_backward(int32_t rows, int32_t cols, int32_t inner, in
 
 size_t beam_moe_grad_norm_workspace_bytes(int32_t count) {
   if (count < 0 || count > kMaxGrads) return SIZE_MAX;
-  return beam::grad_partials(count) * sizeof(double);
+  return beam::grad_workspace(count);
 }
 
 int beam_moe_grad_norm(int32_t count, const void* const* grads, const int32_t* types, const int64_t* sizes, float scale,
@@ -275,10 +296,11 @@ int beam_moe_grad_norm(int32_t count, const void* const* grads, const int32_t* t
   if ((rc = check_ptrs({norm})) != BEAM_MOE_OK) return rc;
   if (!ws || !aligned16(ws) || ws_bytes < beam_moe_grad_norm_workspace_bytes(count)) return BEAM_MOE_ERR_WORKSPACE;
   try {
-    std::vector<beam::GradTensor> t(count);
-    for (int32_t i = 0; i < count; ++i) t[i] = {grads[i], nullptr, sizes[i], types[i], types[i]};
-    return hip_status(beam::launch_grad_norm(t.data(), count, scale, static_cast<double*>(ws), norm,
-                                             static_cast<hipStream_t>(stream)));
+    std::vector<beam::GradTensor> t;
+    t.reserve(count);
+    for (int32_t i = 0; i < count; ++i)
+      if (sizes[i] > 0) t.push_back({grads[i], nullptr, sizes[i], 0u, (uint8_t)types[i], (uint8_t)types[i]});
+    return hip_status(beam::launch_grad_norm(t.data(), (int)t.size(), scale, ws, norm, static_cast<hipStream_t>(stream)));
   } catch (const std::bad_alloc&) {
     return BEAM_MOE_ERR_UNSUPPORTED;
   }
@@ -293,21 +315,21 @@ int beam_moe_clip_grads(int32_t count, const void* const* grads, const int32_t* 
     return BEAM_MOE_ERR_INVALID_ARG;
   if (out_types && !outs) return BEAM_MOE_ERR_INVALID_ARG;
   if ((rc = check_optional({norm_in, norm})) != BEAM_MOE_OK) return rc;
-  if (!norm_in && (!ws || !aligned16(ws) || ws_bytes < beam_moe_grad_norm_workspace_bytes(count)))
-    return BEAM_MOE_ERR_WORKSPACE;
+  if (!ws || !aligned16(ws) || ws_bytes < beam_moe_grad_norm_workspace_bytes(count)) return BEAM_MOE_ERR_WORKSPACE;
   try {
-    std::vector<beam::GradTensor> t(count);
+    std::vector<beam::GradTensor> t;
+    t.reserve(count);
     for (int32_t i = 0; i < count; ++i) {
-      t[i] = {grads[i], outs ? outs[i] : const_cast<void*>(grads[i]), sizes[i], types[i],
-              out_types ? out_types[i] : types[i]};
-      if (!type_ok(t[i].out_type)) return BEAM_MOE_ERR_INVALID_ARG;
-      if (t[i].n > 0 && (!t[i].out || reinterpret_cast<uintptr_t>(t[i].out) % elem_bytes(t[i].out_type) != 0))
-        return BEAM_MOE_ERR_INVALID_ARG;
+      void* out = outs ? outs[i] : const_cast<void*>(grads[i]);
+      const int type = out_types ? out_types[i] : types[i];
+      if (!type_ok(type)) return BEAM_MOE_ERR_INVALID_ARG;
+      if (sizes[i] == 0) continue;
+      if (!out || reinterpret_cast<uintptr_t>(out) % elem_bytes(type) != 0) return BEAM_MOE_ERR_INVALID_ARG;
+      t.push_back({grads[i], out, sizes[i], 0u, (uint8_t)types[i], (uint8_t)type});
     }
     if (!apart(t)) return BEAM_MOE_ERR_INVALID_ARG;
     const beam::ClipArgs a{scale, max_norm, eps, norm_in, norm};
-    return hip_status(beam::launch_clip_grads(t.data(), count, a, static_cast<double*>(ws),
-                                              static_cast<hipStream_t>(stream)));
+    return hip_status(beam::launch_clip_grads(t.data(), (int)t.size(), a, ws, static_cast<hipStream_t>(stream)));
   } catch (const std::bad_alloc&) {
     return BEAM_MOE_ERR_UNSUPPORTED;
   }

@@ -10,8 +10,10 @@ struct GradTensor {
   const void* p;
   void* out;
   int64_t n;
-  int type, out_type;
+  uint32_t end;  // chunks of the list up to this tensor's last; the launches set it
+  uint8_t type, out_type;
 };
+static_assert(sizeof(GradTensor) == 32, "a table's entry");
 
 // Every element's gradient counts `scale` times.  norm_in null: the norm is computed.
 struct ClipArgs {
@@ -20,11 +22,11 @@ struct ClipArgs {
   float* norm;  // null: not written
 };
 
-// Partial sums that the norm of `count` tensors needs.
-int grad_partials(int count);
-// norm = |scale| sqrt(sum of squares)
-hipError_t launch_grad_norm(const GradTensor* t, int count, double scale, double* part, float* norm, hipStream_t st);
+// Workspace of both calls for `count` tensors.
+size_t grad_workspace(int count);
+// norm = |scale| sqrt(sum of squares).  Tensors without elements are left out of the list before.
+hipError_t launch_grad_norm(GradTensor* t, int count, double scale, void* ws, float* norm, hipStream_t st);
 // out = g scale min(1, max_norm / (norm + eps))
-hipError_t launch_clip_grads(const GradTensor* t, int count, const ClipArgs& a, double* part, hipStream_t st);
+hipError_t launch_clip_grads(GradTensor* t, int count, const ClipArgs& a, void* ws, hipStream_t st);
 
 }  // namespace beam

@@ -4,38 +4,43 @@
 //
 // Bound by HBM: every gradient is read for the norm and again for its scaling.  Squares are summed in FP64, where
 // neither they nor their sum leave the range whatever the gradients' size, at two more instructions an element that
-// the memory hides.  A launch takes as many tensors as its arguments hold, so no table is copied to the device
-// and a captured launch keeps its own.  A workgroup takes chunks of the list in turn; the order of every
-// sum depends on the sizes alone.
+// the memory hides.  The list is cut into chunks, and each workgroup takes an equal stretch of them; the order of
+// every sum depends on the sizes alone.  The table of tensors comes with a launch's arguments where it fits them,
+// else small launches lay it down in the workspace first, so that a captured launch keeps its own.
+#include <algorithm>
+
 #include "grads.h"
 
 namespace beam {
 namespace {
 
-constexpr int kPerLaunch = 120;   // tensors whose table fits a launch's 4 KB of arguments
-constexpr int kChunk = 8192;      // elements
-constexpr int kUnits = 1024;      // workgroups that share the chunks, about: four to a CU
+constexpr int kPerLaunch = 112;  // tensors that fit a launch's 4 KB of arguments
+constexpr int kChunk = 2048;     // elements: eight to a thread
+constexpr int kUnits = 1024;     // workgroups, and partial sums, at most: sixteen waves a CU
+// Up to here one launch does it all: every workgroup adds up all squares by itself, or, where results replace
+// gradients that others still read, there is one alone.
+constexpr int64_t kAloneApart = 32768, kAloneInPlace = 16384;
 
 struct GradTable {
-  const void* p[kPerLaunch];
-  void* out[kPerLaunch];
-  int64_t n[kPerLaunch];
-  uint32_t end[kPerLaunch];  // chunks up to this tensor's last
-  uint8_t type[kPerLaunch], out_type[kPerLaunch];
+  GradTensor t[kPerLaunch];
   int count;
-  uint32_t chunks;
 };
-static_assert(sizeof(GradTable) <= 3800, "room for the other arguments");
+static_assert(sizeof(GradTable) <= 3600, "room for the other arguments");
 
-// Sum over the workgroup's threads, for all of them.
-__device__ __forceinline__ double block_sum(double v, double* s) {
+__global__ __launch_bounds__(128) void grad_table_kernel(GradTable part, GradTensor* __restrict__ to) {
+  if ((int)threadIdx.x < part.count) to[threadIdx.x] = part.t[threadIdx.x];
+}
+
+// Sum over the workgroup's threads, for all of them; s holds a value of each wave.
+template <class V>
+__device__ __forceinline__ V block_sum(V v, V* s) {
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);
   const int waves = blockDim.x >> 6;
   __syncthreads();
   if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
   __syncthreads();
-  double a = 0.0;
+  V a = 0;
   for (int w = 0; w < waves; ++w) a += s[w];
   return a;
 }
@@ -46,18 +51,18 @@ __device__ __forceinline__ double sum_partials(const double* part, int n, double
   return block_sum(v, s);
 }
 
-// f(tensor, first element, elements) for each chunk of this workgroup.
+// f(tensor, first element, end) for the stretches of the list's chunks from c0 to c1.  The first tensor is found by
+// all threads together, each looking at its share of the table: one latency whatever its length.
 template <class F>
-__device__ __forceinline__ void chunks_of(const GradTable& t, F f) {
-  for (uint32_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
-    int lo = 0, hi = t.count - 1;
-    while (lo < hi) {  // the first tensor that ends behind c
-      const int mid = (lo + hi) / 2;
-      if (t.end[mid] > c) hi = mid;
-      else lo = mid + 1;
-    }
-    const int64_t i0 = (int64_t)(c - (lo ? t.end[lo - 1] : 0u)) * kChunk;
-    f(lo, i0, (int)min((int64_t)kChunk, t.n[lo] - i0));
+__device__ __forceinline__ void stretch(const GradTensor* t, int count, uint32_t c0, uint32_t c1, int* s, F f) {
+  if (c0 >= c1) return;
+  int before = 0;
+  for (int i = threadIdx.x; i < count; i += blockDim.x) before += t[i].end <= c0;
+  int k = __builtin_amdgcn_readfirstlane(block_sum(before, s));
+  for (uint32_t c = c0; c < c1; ++k) {
+    const uint32_t start = k ? t[k - 1].end : 0u, stop = min(c1, t[k].end);
+    f(t[k], (int64_t)(c - start) * kChunk, min(t[k].n, (int64_t)(stop - start) * kChunk));
+    c = stop;
   }
 }
 
@@ -68,23 +73,89 @@ __device__ __forceinline__ void by_type(int type, F f) {
   else f(BF16{});
 }
 
-__global__ __launch_bounds__(256) void grad_squares_kernel(GradTable t, double* __restrict__ part) {
-  __shared__ double s[4];
-  double sum = 0.0;
-  chunks_of(t, [&](int k, int64_t i0, int n) {
-    by_type(t.type[k], [&](auto type) {
-      using T = decltype(type);
-      const typename T::S* p = static_cast<const typename T::S*>(t.p[k]) + i0;
-#pragma unroll 4
-      for (int i = threadIdx.x * 8; i < n; i += 256 * 8) {
-        float v[8];
-        load8<T>(p + i, n - i, v);
+// g(first of eight elements, how many, the eight) for a thread's share of i0 .. i1, four loads in flight.
+template <class T, class G>
+__device__ __forceinline__ void eights(const typename T::S* p, int64_t i0, int64_t i1, G g) {
+  const int64_t across = (int64_t)blockDim.x * 8;
+  int64_t i = i0 + (int64_t)threadIdx.x * 8;
+  for (; i + 3 * across + 8 <= i1; i += 4 * across) {
+    Raw8<T> r[4];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) sum = fma((double)v[q], (double)v[q], sum);
-      }
+    for (int u = 0; u < 4; ++u) r[u].load(p + i + u * across);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) g(i + u * across, 8, r[u]);
+  }
+  for (; i < i1; i += across) {
+    const int n = (int)min((int64_t)8, i1 - i);
+    Raw8<T> r;
+    if (n == 8)
+      r.load(p + i);
+    else
+      r.load_part(p + i, n);
+    g(i, n, r);
+  }
+}
+
+__device__ __forceinline__ double squares(const GradTensor* t, int count, uint32_t c0, uint32_t c1, int* s) {
+  double sum = 0.0;
+  stretch(t, count, c0, c1, s, [&](const GradTensor& k, int64_t i0, int64_t i1) {
+    by_type(k.type, [&](auto type) {
+      using T = decltype(type);
+      eights<T>(static_cast<const typename T::S*>(k.p), i0, i1, [&](int64_t, int, const Raw8<T>& r) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) sum = fma((double)r[q], (double)r[q], sum);
+      });
     });
   });
-  sum = block_sum(sum, s);
+  return sum;
+}
+
+__device__ __forceinline__ void scaled(const GradTensor* t, int count, uint32_t c0, uint32_t c1, int* s, float f) {
+  stretch(t, count, c0, c1, s, [&](const GradTensor& k, int64_t i0, int64_t i1) {
+    if (f == 1.f && k.p == k.out) return;  // as they are
+    by_type(k.type, [&](auto type) {
+      by_type(k.out_type, [&](auto out_type) {
+        using T = decltype(type);
+        using O = decltype(out_type);
+        typename O::S* o = static_cast<typename O::S*>(k.out);
+        eights<T>(static_cast<const typename T::S*>(k.p), i0, i1, [&](int64_t i, int n, const Raw8<T>& r) {
+          float v[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) v[q] = r[q] * f;
+          store8<O>(o + i, n, v);
+        });
+      });
+    });
+  });
+}
+
+__device__ __forceinline__ float factor(const ClipArgs& a, double norm) {
+  const double c = a.max_norm / (norm + a.eps);
+  return (float)(a.scale * (c > 1.0 ? 1.0 : c));  // NaN stays NaN
+}
+
+// This workgroup's stretch of the chunks.
+__device__ __forceinline__ uint32_t cut(uint32_t chunks, uint32_t b) {
+  return (uint32_t)((uint64_t)chunks * b / gridDim.x);
+}
+
+// The table, from the launch's arguments or the workspace.
+struct Inline {
+  GradTable t;
+  __device__ const GradTensor* table() const { return t.t; }
+};
+struct Laid {
+  const GradTensor* t;
+  __device__ const GradTensor* table() const { return t; }
+};
+
+template <class L>
+__global__ __launch_bounds__(256) void grad_squares_kernel(L list, int count, uint32_t chunks,
+                                                           double* __restrict__ part) {
+  __shared__ double s[4];
+  __shared__ int si[4];
+  const double sum = block_sum(
+      squares(list.table(), count, cut(chunks, blockIdx.x), cut(chunks, blockIdx.x + 1), si), s);
   if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
 
@@ -96,100 +167,114 @@ __global__ __launch_bounds__(256) void grad_norm_kernel(const double* __restrict
 }
 
 // Every workgroup adds the partial sums by itself, so that no launch stands between the norm and the scaling.
-__global__ __launch_bounds__(256) void clip_grads_kernel(GradTable t, ClipArgs a, const double* __restrict__ part,
-                                                         int parts) {
+template <class L>
+__global__ __launch_bounds__(256) void clip_grads_kernel(L list, int count, uint32_t chunks, ClipArgs a,
+                                                         const double* __restrict__ part, int parts) {
   __shared__ double s[4];
+  __shared__ int si[4];
   const double norm = a.norm_in ? (double)*a.norm_in : fabs(a.scale) * sqrt(sum_partials(part, parts, s));
   if (a.norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = (float)norm;
-  const double c = a.max_norm / (norm + a.eps);
-  const float f = (float)(a.scale * (c > 1.0 ? 1.0 : c));  // NaN stays NaN
-  chunks_of(t, [&](int k, int64_t i0, int n) {
-    if (f == 1.f && t.p[k] == t.out[k]) return;  // as they are
-    by_type(t.type[k], [&](auto type) {
-      by_type(t.out_type[k], [&](auto out_type) {
-        using T = decltype(type);
-        using O = decltype(out_type);
-        const typename T::S* p = static_cast<const typename T::S*>(t.p[k]) + i0;
-        typename O::S* o = static_cast<typename O::S*>(t.out[k]) + i0;
-#pragma unroll 4
-        for (int i = threadIdx.x * 8; i < n; i += 256 * 8) {
-          float v[8];
-          load8<T>(p + i, n - i, v);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) v[q] *= f;
-          store8<O>(o + i, n - i, v);
-        }
-      });
-    });
-  });
+  scaled(list.table(), count, cut(chunks, blockIdx.x), cut(chunks, blockIdx.x + 1), si, factor(a, norm));
 }
 
-uint32_t chunks(int64_t n) { return (uint32_t)((n + kChunk - 1) / kChunk); }
+// All of it in one launch; write: whether there are results besides the norm.
+__global__ __launch_bounds__(512) void clip_alone_kernel(Inline list, int count, uint32_t chunks, ClipArgs a,
+                                                         bool write) {
+  __shared__ double s[8];
+  __shared__ int si[8];
+  const double norm = fabs(a.scale) * sqrt(block_sum(squares(list.table(), count, 0, chunks, si), s));
+  if (a.norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = (float)norm;
+  if (!write) return;
+  // the reads of a gradient come before its result's stores: a barrier of block_sum lies between
+  scaled(list.table(), count, cut(chunks, blockIdx.x), cut(chunks, blockIdx.x + 1), si, factor(a, norm));
+}
 
-// f(table, workgroups) for each launch's share of the list; stops at the first error.
-template <class F>
-hipError_t each_launch(const GradTensor* t, int count, F f) {
-  uint64_t total = 0;
-  for (int i = 0; i < count; ++i) total += chunks(t[i].n);
-  for (int i = 0; i < count;) {
-    GradTable g{};
-    for (; i < count && g.count < kPerLaunch; ++i) {
-      if (t[i].n == 0) continue;
-      const int k = g.count++;
-      g.p[k] = t[i].p;
-      g.out[k] = t[i].out;
-      g.n[k] = t[i].n;
-      g.type[k] = (uint8_t)t[i].type;
-      g.out_type[k] = (uint8_t)t[i].out_type;
-      g.end[k] = g.chunks += chunks(t[i].n);
-    }
-    if (g.count == 0) break;
-    const uint32_t units = (uint32_t)(total <= kUnits ? g.chunks : (g.chunks * (uint64_t)kUnits + total - 1) / total);
-    const hipError_t e = f(g, (int)units);
+struct List {
+  const GradTensor* laid;  // in the workspace; null: `all` goes with the launch
+  Inline all;
+  int count;
+  uint32_t chunks;
+  int units;
+  double* part;
+};
+
+size_t table_bytes(int count) { return count > kPerLaunch ? (size_t)count * sizeof(GradTensor) : 0; }
+
+hipError_t prepare(List& l, GradTensor* t, int count, void* ws, hipStream_t st) {
+  l.count = count;
+  l.chunks = 0;
+  for (int i = 0; i < count; ++i) t[i].end = l.chunks += (uint32_t)((t[i].n + kChunk - 1) / kChunk);
+  l.units = (int)std::min<uint32_t>(l.chunks, kUnits);
+  l.laid = nullptr;
+  l.part = reinterpret_cast<double*>(static_cast<char*>(ws) + table_bytes(count));
+  if (count <= kPerLaunch) {
+    std::copy(t, t + count, l.all.t.t);
+    return hipSuccess;
+  }
+  l.laid = static_cast<GradTensor*>(ws);
+  for (int i = 0; i < count; i += kPerLaunch) {
+    GradTable& g = l.all.t;
+    g.count = std::min(count - i, kPerLaunch);
+    std::copy(t + i, t + i + g.count, g.t);
+    hipLaunchKernelGGL(grad_table_kernel, dim3(1), dim3(128), 0, st, g, static_cast<GradTensor*>(ws) + i);
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
 
-hipError_t launch_squares(const GradTensor* t, int count, double* part, int* parts, hipStream_t st) {
-  *parts = 0;
-  return each_launch(t, count, [&](const GradTable& g, int units) {
-    hipLaunchKernelGGL(grad_squares_kernel, dim3(units), dim3(256), 0, st, g, part + *parts);
-    *parts += units;
-    return hipGetLastError();
-  });
+hipError_t launch_squares(const List& l, hipStream_t st) {
+  if (l.laid)
+    hipLaunchKernelGGL(grad_squares_kernel<Laid>, dim3(l.units), dim3(256), 0, st, Laid{l.laid}, l.count, l.chunks,
+                       l.part);
+  else
+    hipLaunchKernelGGL(grad_squares_kernel<Inline>, dim3(l.units), dim3(256), 0, st, l.all, l.count, l.chunks, l.part);
+  return hipGetLastError();
+}
+
+int64_t elements(const GradTensor* t, int count) {
+  int64_t n = 0;
+  for (int i = 0; i < count; ++i) n += t[i].n;
+  return n;
+}
+
+hipError_t launch_alone(const List& l, const ClipArgs& a, bool write, int groups, hipStream_t st) {
+  hipLaunchKernelGGL(clip_alone_kernel, dim3(groups), dim3(512), 0, st, l.all, l.count, l.chunks, a, write);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-// The shares of kUnits are rounded up, one more to a launch at most.
-int grad_partials(int count) { return kUnits + (count + kPerLaunch - 1) / kPerLaunch; }
+size_t grad_workspace(int count) { return table_bytes(count) + kUnits * sizeof(double); }
 
-hipError_t launch_grad_norm(const GradTensor* t, int count, double scale, double* part, float* norm, hipStream_t st) {
-  int parts = 0;
-  const hipError_t e = launch_squares(t, count, part, &parts, st);
+hipError_t launch_grad_norm(GradTensor* t, int count, double scale, void* ws, float* norm, hipStream_t st) {
+  List l;
+  hipError_t e = prepare(l, t, count, ws, st);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(grad_norm_kernel, dim3(1), dim3(256), 0, st, part, parts, scale, norm);
+  if (!l.laid && elements(t, count) <= kAloneInPlace)
+    return launch_alone(l, {scale, 0.0, 1.0, nullptr, norm}, false, 1, st);
+  if ((e = launch_squares(l, st)) != hipSuccess) return e;
+  hipLaunchKernelGGL(grad_norm_kernel, dim3(1), dim3(256), 0, st, l.part, l.units, scale, norm);
   return hipGetLastError();
 }
 
-hipError_t launch_clip_grads(const GradTensor* t, int count, const ClipArgs& args, double* part, hipStream_t st) {
-  int parts = 0;
-  if (!args.norm_in) {
-    const hipError_t e = launch_squares(t, count, part, &parts, st);
-    if (e != hipSuccess) return e;
+hipError_t launch_clip_grads(GradTensor* t, int count, const ClipArgs& a, void* ws, hipStream_t st) {
+  List l;
+  hipError_t e = prepare(l, t, count, ws, st);
+  if (e != hipSuccess) return e;
+  if (!l.laid && !a.norm_in) {
+    const bool in_place = std::any_of(t, t + count, [](const GradTensor& k) { return k.p == k.out; });
+    if (elements(t, count) <= (in_place ? kAloneInPlace : kAloneApart))
+      return launch_alone(l, a, true, in_place || l.chunks == 0 ? 1 : (int)l.chunks, st);
   }
-  ClipArgs a = args;
-  bool any = false;
-  const hipError_t e = each_launch(t, count, [&](const GradTable& g, int units) {
-    hipLaunchKernelGGL(clip_grads_kernel, dim3(units), dim3(256), 0, st, g, a, part, parts);
-    a.norm = nullptr;
-    any = true;
-    return hipGetLastError();
-  });
-  if (e != hipSuccess || any || !a.norm) return e;
-  // no element at all
-  hipLaunchKernelGGL(clip_grads_kernel, dim3(1), dim3(256), 0, st, GradTable{}, a, part, 0);
+  if (!a.norm_in && (e = launch_squares(l, st)) != hipSuccess) return e;
+  if (l.chunks == 0) return hipSuccess;  // nothing to scale by a given norm
+  if (l.laid)
+    hipLaunchKernelGGL(clip_grads_kernel<Laid>, dim3(l.units), dim3(256), 0, st, Laid{l.laid}, l.count, l.chunks, a,
+                       l.part, l.units);
+  else
+    hipLaunchKernelGGL(clip_grads_kernel<Inline>, dim3(l.units), dim3(256), 0, st, l.all, l.count, l.chunks, a, l.part,
+                       l.units);
   return hipGetLastError();
 }
 

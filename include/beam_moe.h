@@ -512,7 +512,7 @@ size_t beam_moe_grad_norm_workspace_bytes(int32_t count);
  *   grads   [count] device pointers (an array on the host, read before the call returns), each
  *           aligned to its element; NULL where the size is 0
  *   types   [count] element types BEAM_MOE_BF16, _F16 or _F32 (host)
- *   sizes   [count] elements, 0 .. 2^40 (host); 2^44 in all
+ *   sizes   [count] elements, 0 .. 2^40 (host); 2^42 in all
  *   scale   finite; the reciprocal of a loss scale or of a number of accumulated steps
  *   norm    fp32 out, one element on the device
  *   ws      of beam_moe_grad_norm_workspace_bytes(count)
@@ -532,7 +532,6 @@ int beam_moe_grad_norm(int32_t count, const void* const* grads, const int32_t* t
  *              grads[i] with the same type, and lies apart from every other gradient and output
  *   out_types  [count] element types of outs (host), NULL = the gradients' own
  *   norm       fp32 out: the norm taken, before clipping; NULL = not written
- *   ws         not needed with norm_in
  * Outputs that overlap, or gradients that occur twice in place, are refused.  Where the norm is infinite the
  * finite gradients are 0 and the infinite ones NaN; where it is NaN, all are. */
 int beam_moe_clip_grads(int32_t count, const void* const* grads, const int32_t* types, const int64_t* sizes, float scale,

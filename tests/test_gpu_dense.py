@@ -79,7 +79,8 @@ def _clip_check(got, grads, f):
         _near(a, want, 2.0 * U * want.abs() + 2.0 ** -149, a.dtype)
 
 
-SIZES = [[1], [7, 1, 0, 33], [8192, 8193, 8191], [100000, 3, 65537], [5] * 300, [1000 + 13 * i for i in range(130)]]
+SIZES = [[1], [7, 1, 0, 33], [8192, 8193, 8191], [100000, 3, 65537], [5] * 300, [1000 + 13 * i for i in range(130)],
+         [16384], [16385], [32768], [30000, 2769], [40] * 112, [40] * 113, [300000, 2, 2047, 2048, 2049] * 50]
 MIXES = [(BF16,), (F16,), (F32,), (BF16, F32), (F16, F32, BF16)]
 
 
@@ -145,6 +146,17 @@ def test_clip_grads_shapes_and_transposes():
     out = [torch.empty_like(t) for t in copies]
     fw.beam_moe_clip_grads(copies, 1.0, out=out)
     assert all(torch.equal(a, b) for a, b in zip(out, grads))
+
+
+def test_clip_grads_partly_in_place():
+    _say("clip partly in place")
+    for n in (300, 9000):
+        grads = _grads(n, [n, 70, n], (F32, BF16, BF16))
+        copies = [t.clone() for t in grads]
+        out = [grads[0], torch.empty(70, device=DEV), grads[2]]
+        fw.beam_moe_clip_grads(grads, 1.0, out=out)
+        _clip_check(out, copies, _factor(copies, 1.0))
+        assert torch.equal(grads[1], copies[1])
 
 
 def test_clip_grads_by_a_given_norm():
