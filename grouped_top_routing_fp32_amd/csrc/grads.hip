@@ -51,18 +51,20 @@ __device__ __forceinline__ double sum_partials(const double* part, int n, double
   return block_sum(v, s);
 }
 
-// f(tensor, first element, end) for the stretches of the list's chunks from c0 to c1.  The first tensor is found by
-// all threads together, each looking at its share of the table: one latency whatever its length.
-template <class F>
+// f(tensor, first element, end) for the stretches of the list's chunks from c0 to c1, or from c1 back to c0.  The first
+// tensor is found by all threads together, each looking at its share of the table: one latency whatever its length.
+template <bool BACK, class F>
 __device__ __forceinline__ void stretch(const GradTensor* t, int count, uint32_t c0, uint32_t c1, int* s, F f) {
   if (c0 >= c1) return;
+  const uint32_t from = BACK ? c1 - 1 : c0;
   int before = 0;
-  for (int i = threadIdx.x; i < count; i += blockDim.x) before += t[i].end <= c0;
+  for (int i = threadIdx.x; i < count; i += blockDim.x) before += t[i].end <= from;
   int k = __builtin_amdgcn_readfirstlane(block_sum(before, s));
-  for (uint32_t c = c0; c < c1; ++k) {
-    const uint32_t start = k ? t[k - 1].end : 0u, stop = min(c1, t[k].end);
-    f(t[k], (int64_t)(c - start) * kChunk, min(t[k].n, (int64_t)(stop - start) * kChunk));
-    c = stop;
+  for (uint32_t c = BACK ? c1 : c0; BACK ? c > c0 : c < c1; BACK ? --k : ++k) {
+    const uint32_t start = k ? t[k - 1].end : 0u;
+    const uint32_t a = BACK ? max(c0, start) : c, b = BACK ? c : min(c1, t[k].end);
+    f(t[k], (int64_t)(a - start) * kChunk, min(t[k].n, (int64_t)(b - start) * kChunk));
+    c = BACK ? a : b;
   }
 }
 
@@ -73,35 +75,41 @@ __device__ __forceinline__ void by_type(int type, F f) {
   else f(BF16{});
 }
 
-// g(first of eight elements, how many, the eight) for a thread's share of i0 .. i1, four loads in flight.
-template <class T, class G>
+// g(first of eight elements, how many, the eight) for a thread's share of i0 .. i1, four loads in flight, from the
+// first on or from the last back.
+template <class T, bool BACK, class G>
 __device__ __forceinline__ void eights(const typename T::S* p, int64_t i0, int64_t i1, G g) {
   const int64_t across = (int64_t)blockDim.x * 8;
-  int64_t i = i0 + (int64_t)threadIdx.x * 8;
-  for (; i + 3 * across + 8 <= i1; i += 4 * across) {
+  const int64_t whole = (i1 - i0) / (4 * across), mid = i0 + whole * 4 * across;  // four full rounds at a time, and the rest
+  auto rest = [&]() __attribute__((always_inline)) {
+    for (int64_t i = mid + (int64_t)threadIdx.x * 8; i < i1; i += across) {
+      const int n = (int)min((int64_t)8, i1 - i);
+      Raw8<T> r;
+      if (n == 8)
+        r.load(p + i);
+      else
+        r.load_part(p + i, n);
+      g(i, n, r);
+    }
+  };
+  if (BACK) rest();
+  for (int64_t w = 0; w < whole; ++w) {
+    const int64_t i = i0 + (BACK ? whole - 1 - w : w) * 4 * across + (int64_t)threadIdx.x * 8;
     Raw8<T> r[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) r[u].load(p + i + u * across);
 #pragma unroll
     for (int u = 0; u < 4; ++u) g(i + u * across, 8, r[u]);
   }
-  for (; i < i1; i += across) {
-    const int n = (int)min((int64_t)8, i1 - i);
-    Raw8<T> r;
-    if (n == 8)
-      r.load(p + i);
-    else
-      r.load_part(p + i, n);
-    g(i, n, r);
-  }
+  if (!BACK) rest();
 }
 
 __device__ __forceinline__ double squares(const GradTensor* t, int count, uint32_t c0, uint32_t c1, int* s) {
   double sum = 0.0;
-  stretch(t, count, c0, c1, s, [&](const GradTensor& k, int64_t i0, int64_t i1) {
+  stretch<false>(t, count, c0, c1, s, [&](const GradTensor& k, int64_t i0, int64_t i1) {
     by_type(k.type, [&](auto type) {
       using T = decltype(type);
-      eights<T>(static_cast<const typename T::S*>(k.p), i0, i1, [&](int64_t, int, const Raw8<T>& r) {
+      eights<T, false>(static_cast<const typename T::S*>(k.p), i0, i1, [&](int64_t, int, const Raw8<T>& r) {
 #pragma unroll
         for (int q = 0; q < 8; ++q) sum = fma((double)r[q], (double)r[q], sum);
       });
@@ -111,14 +119,14 @@ __device__ __forceinline__ double squares(const GradTensor* t, int count, uint32
 }
 
 __device__ __forceinline__ void scaled(const GradTensor* t, int count, uint32_t c0, uint32_t c1, int* s, float f) {
-  stretch(t, count, c0, c1, s, [&](const GradTensor& k, int64_t i0, int64_t i1) {
+  stretch<true>(t, count, c0, c1, s, [&](const GradTensor& k, int64_t i0, int64_t i1) {
     if (f == 1.f && k.p == k.out) return;  // as they are
     by_type(k.type, [&](auto type) {
       by_type(k.out_type, [&](auto out_type) {
         using T = decltype(type);
         using O = decltype(out_type);
         typename O::S* o = static_cast<typename O::S*>(k.out);
-        eights<T>(static_cast<const typename T::S*>(k.p), i0, i1, [&](int64_t i, int n, const Raw8<T>& r) {
+        eights<T, true>(static_cast<const typename T::S*>(k.p), i0, i1, [&](int64_t i, int n, const Raw8<T>& r) {
           float v[8];
 #pragma unroll
           for (int q = 0; q < 8; ++q) v[q] = r[q] * f;
@@ -177,16 +185,58 @@ __global__ __launch_bounds__(256) void clip_grads_kernel(L list, int count, uint
   scaled(list.table(), count, cut(chunks, blockIdx.x), cut(chunks, blockIdx.x + 1), si, factor(a, norm));
 }
 
-// All of it in one launch; write: whether there are results besides the norm.
-__global__ __launch_bounds__(512) void clip_alone_kernel(Inline list, int count, uint32_t chunks, ClipArgs a,
-                                                         bool write) {
-  __shared__ double s[8];
-  __shared__ int si[8];
-  const double norm = fabs(a.scale) * sqrt(block_sum(squares(list.table(), count, 0, chunks, si), s));
+// All of it in one launch of few chunks, one to a wave at a time, so that their latencies run beside each other;
+// write: whether there are results besides the norm.
+constexpr int kAloneWaves = 16;
+__global__ __launch_bounds__(64 * kAloneWaves) void clip_alone_kernel(Inline list, int count, uint32_t chunks, ClipArgs a,
+                                                                      bool write) {
+  __shared__ double s[kAloneWaves];
+  const GradTensor* t = list.table();
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // f(tensor, first element, eight of them and how many), a quarter of chunk c at a time
+  auto chunk = [&](uint32_t c, auto f) __attribute__((always_inline)) {
+    static_assert(kPerLaunch <= 128, "two entries to a lane");
+    const int k = __popcll(__ballot(lane < count && t[lane].end <= c)) +
+                  __popcll(__ballot(lane + 64 < count && t[lane + 64 < count ? lane + 64 : 0].end <= c));
+    const GradTensor& e = t[k];
+    const int64_t i0 = (int64_t)(c - (k ? t[k - 1].end : 0u)) * kChunk;
+    by_type(e.type, [&](auto type) {
+      using T = decltype(type);
+      const typename T::S* p = static_cast<const typename T::S*>(e.p);
+      Raw8<T> r[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int64_t i = i0 + u * 512 + lane * 8, n = e.n - i;
+        if (n >= 8)
+          r[u].load(p + i);
+        else
+          r[u].load_part(p + i, (int)max(n, (int64_t)0));
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) f(e, i0 + u * 512 + lane * 8, r[u]);
+    });
+  };
+  double sum = 0.0;
+  for (uint32_t c = wave; c < chunks; c += kAloneWaves)
+    chunk(c, [&](const GradTensor&, int64_t, const auto& r) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) sum = fma((double)r[q], (double)r[q], sum);
+    });
+  const double norm = fabs(a.scale) * sqrt(block_sum(sum, s));  // all reads lie before its barriers
   if (a.norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = (float)norm;
+  const float f = factor(a, norm);
   if (!write) return;
-  // the reads of a gradient come before its result's stores: a barrier of block_sum lies between
-  scaled(list.table(), count, cut(chunks, blockIdx.x), cut(chunks, blockIdx.x + 1), si, factor(a, norm));
+  for (uint32_t c = blockIdx.x * kAloneWaves + wave; c < chunks; c += gridDim.x * kAloneWaves)
+    chunk(c, [&](const GradTensor& e, int64_t i, const auto& r) {
+      if (i >= e.n || (f == 1.f && e.p == e.out)) return;
+      by_type(e.out_type, [&](auto out_type) {
+        using O = decltype(out_type);
+        float v[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = r[q] * f;
+        store8<O>(static_cast<typename O::S*>(e.out) + i, (int)min((int64_t)8, e.n - i), v);
+      });
+    });
 }
 
 struct List {
@@ -239,7 +289,7 @@ int64_t elements(const GradTensor* t, int count) {
 }
 
 hipError_t launch_alone(const List& l, const ClipArgs& a, bool write, int groups, hipStream_t st) {
-  hipLaunchKernelGGL(clip_alone_kernel, dim3(groups), dim3(512), 0, st, l.all, l.count, l.chunks, a, write);
+  hipLaunchKernelGGL(clip_alone_kernel, dim3(groups), dim3(64 * kAloneWaves), 0, st, l.all, l.count, l.chunks, a, write);
   return hipGetLastError();
 }
 
@@ -265,7 +315,7 @@ hipError_t launch_clip_grads(GradTensor* t, int count, const ClipArgs& a, void* 
   if (!l.laid && !a.norm_in) {
     const bool in_place = std::any_of(t, t + count, [](const GradTensor& k) { return k.p == k.out; });
     if (elements(t, count) <= (in_place ? kAloneInPlace : kAloneApart))
-      return launch_alone(l, a, true, in_place || l.chunks == 0 ? 1 : (int)l.chunks, st);
+      return launch_alone(l, a, true, in_place ? 1 : std::max(1, (int)(l.chunks + kAloneWaves - 1) / kAloneWaves), st);
   }
   if (!a.norm_in && (e = launch_squares(l, st)) != hipSuccess) return e;
   if (l.chunks == 0) return hipSuccess;  // nothing to scale by a given norm
