@@ -241,11 +241,9 @@ int beam_moe_gated_linear_backward(int32_t rows, int32_t cols, int32_t inner, in
     if (dx && p.copy_gate) copy(jg, w_gate, ldg, cols, p.off_gate);
     if (dx && p.copy_up) copy(ju, w_up, ldu, cols, p.off_up);
     if (dw_gate && p.copy_x) copy(jx, x, ldx, rows, p.off_x);
-    if ((rc = hip_status(beam::launch_pad(jg, ju, st))) != BEAM_MOE_OK) return rc;
-    if ((rc = hip_status(beam::launch_pad(jx, {}, st))) != BEAM_MOE_OK) return rc;
-    beam::GatedDz d{dh,   dh_type, lddh, pre_gate, pre_up, ldpg, ldpu, act, type, at<uint32_t>(ws, p.off_scale + kScaleBytes),
-                    unscale, dz, part, rows, cols};
-    if ((rc = hip_status(beam::launch_gated_dz(d, st))) != BEAM_MOE_OK) return rc;
+    const beam::GatedDz d{dh,   dh_type, lddh, pre_gate, pre_up, ldpg, ldpu, act, type,
+                          at<uint32_t>(ws, p.off_scale + kScaleBytes), unscale, dz, part, rows, cols};
+    if ((rc = hip_status(beam::launch_gated_dz(d, beam::pad_jobs(jg, ju, jx), st))) != BEAM_MOE_OK) return rc;
   }
   beam::GatedArgs gx{}, gw{};
   gx.type = gx.out_type = gw.type = gw.out_type = type;

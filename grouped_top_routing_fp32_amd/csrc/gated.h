@@ -31,7 +31,8 @@ struct GatedDz {
   float* part;   // [units][2 N]; null: not wanted
   int M, N;
 };
-hipError_t launch_gated_dz(const GatedDz& d, hipStream_t st);
+// With them the operands that have to be laid out anew.
+hipError_t launch_gated_dz(const GatedDz& d, PadJobs pad, hipStream_t st);
 // The bias gradients by themselves (beside dx's product they need no launch).
 hipError_t launch_gated_sums(const SumJob& j, hipStream_t st);
 // Both products of the backward pass, or one (the other's out null), as planned by plan_gradients.

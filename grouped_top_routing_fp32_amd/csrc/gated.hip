@@ -158,11 +158,12 @@ __device__ __forceinline__ void gated_slopes(const float* d, const float* zg, co
 }
 
 // peaks[b] = the bits of the largest finite |dzg| or |dzu| in a workgroup's part, for the scale of an fp16 dz.  Grid
-// and rows as in gated_dz_kernel.
+// and rows as in gated_dz_kernel; behind them the workgroups that lay operands out anew, so that those do not wait.
 template <class DT, class T>
-__global__ __launch_bounds__(256) void gated_peak_kernel(GatedDz a, int units, int rows) {
+__global__ __launch_bounds__(256) void gated_peak_kernel(GatedDz a, int units, int rows, PadJobs pad) {
   __shared__ uint32_t top[4];
   const int wide = ceil_div(a.N, 512), bx = blockIdx.x % wide, unit = blockIdx.x / wide, y = threadIdx.y;
+  if (unit >= units) return pad_rows(pad, blockIdx.x - wide * units, y * 64 + threadIdx.x);
   const int n = (bx * 64 + threadIdx.x) * 8, cols = min(8, a.N - n);  // <= 0: none
   const int m1 = min(a.M, (unit + 1) * rows);
   uint32_t best = 0;
@@ -195,10 +196,11 @@ __global__ __launch_bounds__(256) void gated_peak_kernel(GatedDz a, int units, i
 // power of two, as the plain product's is.  grid ceil(N / 512) * units, block (64, 4): thread (c, r) takes 8
 // columns in rows r, r + 4, ... of the unit.  Bound by HBM.
 template <class DT, class T>
-__global__ __launch_bounds__(256) void gated_dz_kernel(GatedDz a, int peak_count, int units, int rows) {
+__global__ __launch_bounds__(256) void gated_dz_kernel(GatedDz a, int peak_count, int units, int rows, PadJobs pad) {
   __shared__ float sums[4][64][8];
   const int half = gated_half(a.N), wide = ceil_div(half, 512);
   const int bx = blockIdx.x % wide, unit = blockIdx.x / wide, y = threadIdx.y;
+  if (unit >= units) return pad_rows(pad, blockIdx.x - wide * units, y * 64 + threadIdx.x);
   const int n = (bx * 64 + threadIdx.x) * 8, cols = min(8, a.N - n);  // <= 0: none
   const int m1 = min(a.M, (unit + 1) * rows);
   [[maybe_unused]] float up = 1.f;
@@ -277,6 +279,11 @@ GatedPlan plan_gated(int M, int N, int K, int64_t ldx, int64_t ldg, int64_t ldu)
   p.copy_x = !regular_rows(ldx, K);
   p.copy_gate = !regular_rows(ldg, K);
   p.copy_up = !regular_rows(ldu, K);
+  if ((p.copy_x || p.copy_gate || p.copy_up) &&
+      few_tiles(p.gemm, (int64_t)ceil_div(M, p.gemm.tile) * ceil_div(2 * N, p.gemm.tile), K)) {
+    p.copy_x = p.copy_gate = p.copy_up = false;
+    p.gemm.regs = true;
+  }
   p.off_gate = p.copy_x ? up256(padded_bytes(M, K)) : 0;
   p.off_up = p.off_gate + (p.copy_gate ? up256(padded_bytes(N, K)) : 0);
   p.off_gemm = p.off_up + (p.copy_up ? up256(padded_bytes(N, K)) : 0);
@@ -299,7 +306,7 @@ hipError_t launch_gated(const GatedArgs& args, const GatedPlan& p, void* ws, hip
   if (p.copy_x) copy(jx, g.a, g.lda, g.M, 0);
   if (p.copy_gate) copy(jg, g.b, g.ldb, g.N, p.off_gate);
   if (p.copy_up) copy(ju, g.b2, g.ldb2, g.N, p.off_up);
-  if ((e = launch_pad(jx, jg, st)) != hipSuccess || (e = launch_pad(ju, {}, st)) != hipSuccess) return e;
+  if ((e = launch_pad(jx, jg, ju, st)) != hipSuccess) return e;
   if (p.gemm.kind == GemmPlan::kSkinny) {
     // as many columns as share the weights evenly among the CUs
     const int rounds = ceil_div(g.N, 16 * kCUs), cols = std::max(4, ceil_div(g.N, rounds * kCUs));
@@ -307,6 +314,7 @@ hipError_t launch_gated(const GatedArgs& args, const GatedPlan& p, void* ws, hip
                        dim3(ceil_div(g.N, cols)), dim3(64 * kSkinnyWaves), 0, st, g, cols);
     return hipGetLastError();
   }
+  g.regs = p.gemm.regs;
   const GemmSplit s = split_of(p.gemm, 2 * ((g.N + 3) / 4 * 4), base + p.off_gemm);
   e = launch_tiles(g, s, p.gemm.tile, st);
   if (e != hipSuccess || !s.part) return e;
@@ -318,7 +326,7 @@ size_t gated_peak_bytes() { return kMaxPeaks * sizeof(uint32_t); }
 
 int gated_dz_units(int M) { return M < 8 ? 1 : M / 4 < 256 ? M / 4 : 256; }
 
-hipError_t launch_gated_dz(const GatedDz& d, hipStream_t st) {
+hipError_t launch_gated_dz(const GatedDz& d, PadJobs pad, hipStream_t st) {
   const int units = gated_dz_units(d.M), rows = ceil_div(d.M, units);
   const int wide = ceil_div(gated_half(d.N), 512), wide_peaks = ceil_div(d.N, 512);
   int few = 0;
@@ -327,13 +335,14 @@ hipError_t launch_gated_dz(const GatedDz& d, hipStream_t st) {
     using T = decltype(t);
     if (d.dz && std::is_same_v<T, F16>) {
       few = units * wide_peaks <= kMaxPeaks ? units : kMaxPeaks / wide_peaks;  // wide_peaks <= 256
-      hipLaunchKernelGGL((gated_peak_kernel<DT, T>), dim3(few * wide_peaks), dim3(64, 4), 0, st, d, few,
-                         ceil_div(d.M, few));
+      hipLaunchKernelGGL((gated_peak_kernel<DT, T>), dim3(few * wide_peaks + pad.total()), dim3(64, 4), 0, st, d, few,
+                         ceil_div(d.M, few), pad);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
+      pad = PadJobs{};
     }
-    hipLaunchKernelGGL((gated_dz_kernel<DT, T>), dim3(wide * units), dim3(64, 4), 0, st, d, few * wide_peaks, units,
-                       rows);
+    hipLaunchKernelGGL((gated_dz_kernel<DT, T>), dim3(wide * units + pad.total()), dim3(64, 4), 0, st, d, few * wide_peaks,
+                       units, rows, pad);
     return hipGetLastError();
   };
   if (d.type == kElemF16) return d.dh_type == kElemF32 ? go(F32{}, F16{}) : go(F16{}, F16{});

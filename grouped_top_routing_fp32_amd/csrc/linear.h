@@ -98,6 +98,13 @@ struct GemmSplit {
 };
 // Operand shapes and leading dimensions decide alone, so a size query and its call agree.
 GemmPlan plan_tiles(int M, int N, int K);  // rows are whole chunks on 16 bytes
+// Whether rows that are no whole chunks go through registers: where that costs less than laying them
+// out anew, a launch and their bytes twice.  [500, 640] x [1000, 640] 8.0 us against 10.6,
+// [8000, 1401] x [300, 1401], 625 x 22 stages of 64-row tiles, 26.3 against 30.9, but [4000,
+// 1401] x [1000, 1401], 1008 x 22, 38.0 against 30.5, and [8000, 100] x [2500, 100], 5000 x
+// 2, 30.8 against 24.1; [500, 5003] x [2500, 5003], 80 128-row tiles, 34.6 against 39.7, but
+// [1000, 2560] x [2500, 2560], 160, 33.0 against 31.7.
+bool few_tiles(const GemmPlan& p, int64_t tiles, int K);
 GemmPlan plan_linear(int M, int N, int K, int64_t ldx, int64_t ldw);
 GemmSplit split_of(const GemmPlan& p, int N, char* base);
 hipError_t launch_join_one(const GemmArgs& g, const GemmSplit& s, hipStream_t st);  // where it was split
@@ -120,8 +127,16 @@ inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 inline int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
 // Whether the tiled kernel's copies can take rows as they are: whole chunks of 8 elements on 16 bytes.
 inline bool regular_rows(int64_t ld, int cols) { return ld % 8 == 0 && cols % 8 == 0; }
+// Up to three operands to be laid out anew in one launch, or in workgroups of 256 threads behind another's: those from
+// start[k] to start[k + 1] - 1 have job k.
+struct PadJobs {
+  PadJob job[3];
+  int start[4];
+  __host__ __device__ int total() const { return start[3]; }
+};
+PadJobs pad_jobs(const PadJob& first, const PadJob& second, const PadJob& third);
 inline size_t padded_bytes(int rows, int cols) { return (size_t)rows * up8(cols) * 2; }
-hipError_t launch_pad(const PadJob& first, const PadJob& second, hipStream_t st);
+hipError_t launch_pad(const PadJob& first, const PadJob& second, const PadJob& third, hipStream_t st);
 hipError_t launch_gemm_bf16(const GemmArgs& g, const GemmSplit& s, int tile, hipStream_t st);
 hipError_t launch_gemm_f16(const GemmArgs& g, const GemmSplit& s, int tile, hipStream_t st);
 // `half`: a result of 16 bits is fp16, not bf16.
@@ -280,6 +295,26 @@ __device__ __forceinline__ float dz_scale(const uint32_t* __restrict__ peaks, in
   if (bound == 0.0) return 1.f;
   const int e = (int)(__builtin_bit_cast(uint64_t, bound) >> 52) - 1022;  // bound < 2^e
   return __uint_as_float((uint32_t)(min(max(15 - e, -126), 126) + 127) << 23);
+}
+
+// b is the workgroup's place among the jobs'.
+__device__ __forceinline__ void pad_rows(const PadJobs& p, int b, int tid) {
+  const int k = (b >= p.start[1]) + (b >= p.start[2]);
+  const PadJob j = k == 0 ? p.job[0] : k == 1 ? p.job[1] : p.job[2];
+  const int first = k == 0 ? 0 : k == 1 ? p.start[1] : p.start[2];
+  const int64_t threads = 256 * (int64_t)((k == 0 ? p.start[1] : k == 1 ? p.start[2] : p.start[3]) - first);
+  const int chunks = (j.cols + 7) / 8;
+  const int64_t n = (int64_t)j.rows * chunks;
+  for (int64_t i = (int64_t)(b - first) * 256 + tid; i < n; i += threads) {
+    const int r = (int)(i / chunks), c = (int)(i % chunks) * 8;
+    const uint16_t* s = static_cast<const uint16_t*>(j.src) + (int64_t)r * j.ld + c;
+    Raw8<F16> v;  // the bits alone matter
+    if (c + 8 <= j.cols)
+      v.load(s);
+    else
+      v.load_part(s, j.cols - c);
+    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(j.dst) + 8 * i) = v.w[0];
+  }
 }
 
 // Eight elements of a row of K from k on, zeros past K.

@@ -88,31 +88,6 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void gemm_skinny_kernel(GemmArgs
   by_act(g.act, [&](auto act) { epilogue4<decltype(act)::value>(g, g.add, l16, n, n1, z); });
 }
 
-// Lays one or two operands out anew, the first with `blocks` workgroups of 256 threads and the
-// second with the rest: one launch for what a product or both gradients need.  b is the
-// workgroup's place among `total`.
-struct PadJobs {
-  PadJob first, second;
-  int blocks, total;
-};
-__device__ __forceinline__ void pad_rows(const PadJobs& p, int b, int tid) {
-  const bool other = b >= p.blocks;
-  const PadJob j = other ? p.second : p.first;
-  const int64_t threads = 256 * (int64_t)(other ? p.total - p.blocks : p.blocks);
-  const int chunks = (j.cols + 7) / 8;
-  const int64_t n = (int64_t)j.rows * chunks;
-  for (int64_t i = (int64_t)(b - (other ? p.blocks : 0)) * 256 + tid; i < n; i += threads) {
-    const int r = (int)(i / chunks), c = (int)(i % chunks) * 8;
-    const uint16_t* s = static_cast<const uint16_t*>(j.src) + (int64_t)r * j.ld + c;
-    Raw8<F16> v;  // the bits alone matter
-    if (c + 8 <= j.cols)
-      v.load(s);
-    else
-      v.load_part(s, j.cols - c);
-    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(j.dst) + 8 * i) = v.w[0];
-  }
-}
-
 __global__ __launch_bounds__(256) void pad_rows_kernel(PadJobs p) { pad_rows(p, blockIdx.x, threadIdx.x); }
 
 // peaks[g] = the bits of the largest finite |dy| in a workgroup's part, for the scale of an fp16
@@ -282,21 +257,16 @@ GemmPlan plan_tiles(int M, int N, int K) {
   return p;
 }
 
+bool few_tiles(const GemmPlan& p, int64_t tiles, int K) {
+  return p.tile == 64 ? tiles <= 4 * kCUs && tiles * ceil_div(K, kBK) <= 56 * kCUs : p.tile == 128 && tiles <= kCUs / 2;
+}
+
 GemmPlan plan_linear(int M, int N, int K, int64_t ldx, int64_t ldw) {
   if (M <= kSkinnyRows) return GemmPlan{};  // kSkinny
   GemmPlan p = plan_tiles(M, N, K);
   p.copy_a = !regular_rows(ldx, K);
   p.copy_b = !regular_rows(ldw, K);
-  // Rows that are no whole chunks go through registers where that costs less than laying them
-  // out anew, a launch and their bytes twice: [500, 640] x [1000, 640] 8.0 us against 10.6,
-  // [8000, 1401] x [300, 1401], 625 x 22 stages of 64-row tiles, 26.3 against 30.9, but [4000,
-  // 1401] x [1000, 1401], 1008 x 22, 38.0 against 30.5, and [8000, 100] x [2500, 100], 5000 x
-  // 2, 30.8 against 24.1; [500, 5003] x [2500, 5003], 80 128-row tiles, 34.6 against 39.7, but
-  // [1000, 2560] x [2500, 2560], 160, 33.0 against 31.7.
-  const int64_t tiles = (int64_t)ceil_div(M, p.tile) * ceil_div(N, p.tile);
-  const bool few = p.tile == 64 ? tiles <= 4 * kCUs && tiles * ceil_div(K, kBK) <= 56 * kCUs
-                                : p.tile == 128 && tiles <= kCUs / 2;
-  if (few && (p.copy_a || p.copy_b)) {
+  if ((p.copy_a || p.copy_b) && few_tiles(p, (int64_t)ceil_div(M, p.tile) * ceil_div(N, p.tile), K)) {
     p.copy_a = p.copy_b = false;
     p.regs = true;
   }
@@ -337,19 +307,20 @@ static hipError_t launch_join(const JoinJob& first, const JoinJob& second, hipSt
 
 hipError_t launch_join_one(const GemmArgs& g, const GemmSplit& s, hipStream_t st) { return launch_join({g, s}, {}, st); }
 
-static PadJobs pad_jobs(const PadJob& first, const PadJob& second) {
-  auto blocks = [](const PadJob& j) {
+PadJobs pad_jobs(const PadJob& first, const PadJob& second, const PadJob& third) {
+  PadJobs p{{first, second, third}, {}};
+  for (int k = 0; k < 3; ++k) {
+    const PadJob& j = p.job[k];
     const int64_t n = (j.rows * (up8(j.cols) / 8) + 255) / 256;
-    return (int)(n < (1 << 20) ? n : 1 << 20);
-  };
-  const int a = blocks(first), b = blocks(second);
-  return {first, second, a, a + b};
+    p.start[k + 1] = p.start[k] + (int)(n < (1 << 20) ? n : 1 << 20);
+  }
+  return p;
 }
 
-hipError_t launch_pad(const PadJob& first, const PadJob& second, hipStream_t st) {
-  const PadJobs p = pad_jobs(first, second);
-  if (p.total == 0) return hipSuccess;
-  hipLaunchKernelGGL(pad_rows_kernel, dim3(p.total), dim3(256), 0, st, p);
+hipError_t launch_pad(const PadJob& first, const PadJob& second, const PadJob& third, hipStream_t st) {
+  const PadJobs p = pad_jobs(first, second, third);
+  if (p.total() == 0) return hipSuccess;
+  hipLaunchKernelGGL(pad_rows_kernel, dim3(p.total()), dim3(256), 0, st, p);
   return hipGetLastError();
 }
 
@@ -368,7 +339,7 @@ hipError_t launch_gemm(const GemmArgs& args, const GemmPlan& p, void* ws, hipStr
     g.b = jb.dst;
     g.ldb = up8(g.K);
   }
-  if ((e = launch_pad(ja, jb, st)) != hipSuccess) return e;
+  if ((e = launch_pad(ja, jb, {}, st)) != hipSuccess) return e;
   if (p.kind == GemmPlan::kSkinny) return launch_skinny(g, st);
   g.regs = p.regs;
   const GemmSplit s = split_of(p, g.N, base);
@@ -479,14 +450,14 @@ hipError_t launch_linear_dz(const void* dy, int dy_type, int64_t lddy, const voi
                             float* part, void* dres, int64_t lddres, int M, int N, const PadJob& first,
                             const PadJob& second, hipStream_t st) {
   const int units = linear_dz_units(M), rows = ceil_div(M, units), wide = ceil_div(N, 512);
-  PadJobs pad = pad_jobs(first, second);
+  PadJobs pad = pad_jobs(first, second, {});
   int peak_count = 0;
   if (dz && type == kElemF16) {
     const int few = units * wide <= kMaxPeaks ? units : kMaxPeaks / wide;  // wide <= 512
     peak_count = few * wide;
     auto peak = [&](auto dt) {
       using DT = decltype(dt);
-      hipLaunchKernelGGL((linear_peak_kernel<DT>), dim3(peak_count + pad.total), dim3(64, 4), 0, st,
+      hipLaunchKernelGGL((linear_peak_kernel<DT>), dim3(peak_count + pad.total()), dim3(64, 4), 0, st,
                          static_cast<const typename DT::S*>(dy), lddy, peaks, M, N, few, ceil_div(M, few), pad);
     };
     dy_type == kElemF32 ? peak(F32{}) : peak(F16{});
@@ -497,7 +468,7 @@ hipError_t launch_linear_dz(const void* dy, int dy_type, int64_t lddy, const voi
   auto go = [&](auto dt, auto t) {
     using DT = decltype(dt);
     using T = decltype(t);
-    hipLaunchKernelGGL((linear_dz_kernel<DT, T>), dim3(wide * units + pad.total), dim3(64, 4), 0, st,
+    hipLaunchKernelGGL((linear_dz_kernel<DT, T>), dim3(wide * units + pad.total()), dim3(64, 4), 0, st,
                        static_cast<const typename DT::S*>(dy), lddy, static_cast<const typename T::S*>(z), ldz, act,
                        keep, add, peaks, peak_count, unscale, dz, lddz, part, static_cast<typename DT::S*>(dres),
                        lddres, M, N, units, rows, pad);

@@ -138,7 +138,7 @@ hipError_t launch_linear_mx(const MxLinear& a, const MxPlan& p, void* ws, hipStr
   g.lda = a.ldx;
   if (p.copy_x) {
     const PadJob j{a.x, a.ldx, g.M, g.K, base};
-    if ((e = launch_pad(j, {}, st)) != hipSuccess) return e;
+    if ((e = launch_pad(j, {}, {}, st)) != hipSuccess) return e;
     g.a = j.dst;
     g.lda = up8(g.K);
   }

@@ -271,7 +271,7 @@ int beam_moe_linear_backward(int32_t rows, int32_t cols, int32_t inner, int type
                       ? beam::launch_linear_dz(dy, dy_type, lddy, pre, ldpre, act, keep, add,
                                                at<uint32_t>(ws, p.off_scale + kScaleBytes), unscale, dz, p.lddz, type,
                                                part, dres, lddres, rows, cols, jw, jx, st)
-                      : beam::launch_pad(jw, jx, st));
+                      : beam::launch_pad(jw, jx, {}, st));
   if (rc != BEAM_MOE_OK) return rc;
   beam::GemmArgs gx{}, gw{};
   gx.type = gx.out_type = gw.type = gw.out_type = type;
