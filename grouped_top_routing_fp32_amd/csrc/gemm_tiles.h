@@ -175,6 +175,49 @@ __device__ __forceinline__ void static_for(F f) {
   for_each_of(f, std::make_integer_sequence<int, N>{});
 }
 
+// B's side of a tile from 4-bit codes: rows of K as Side's, eight codes and their scale to a lane and copy, converted
+// on their way into LDS.
+template <bool HALF, int R, int NW>
+struct CodeSide {
+  using Rows = Side<false, R, NW>;
+  static constexpr int kCopies = Rows::kCopies;
+  struct Eight {
+    uint32_t codes, scale;
+  };
+  const uint8_t *codes[kCopies], *scales[kCopies];
+  __device__ __forceinline__ void init(const CodeArgs& g, int i0, int k0, int wave, int lane) {
+#pragma unroll
+    for (int q = 0; q < kCopies; ++q) {
+      const int r = Rows::row(q, wave, lane), k = k0 + 8 * Rows::chunk(r, lane);
+      const int64_t row = min(i0 + r, g.N - 1);
+      codes[q] = static_cast<const uint8_t*>(g.b) + row * g.ldb + k / 2;
+      scales[q] = g.sb + row * g.ldsb + k / 32;
+    }
+  }
+  __device__ __forceinline__ void load(Eight* regs, int left, int wave, int lane) {
+#pragma unroll
+    for (int q = 0; q < kCopies; ++q) {
+      regs[q] = {0u, 0u};
+      if (8 * Rows::chunk(Rows::row(q, wave, lane), lane) < left)
+        regs[q] = {*reinterpret_cast<const uint32_t*>(codes[q]), *scales[q]};
+      codes[q] += kBK / 2;
+      scales[q] += kBK / 32;
+    }
+  }
+  static __device__ __forceinline__ void store(lds_u16* slot, const Eight* regs, int wave, int lane) {
+    u32x4 v[kCopies];
+#pragma unroll
+    for (int q = 0; q < kCopies; ++q) v[q] = codes_to_16<HALF>(regs[q].codes, mx_scale(regs[q].scale));
+    Rows::store(slot, v, wave, lane);
+  }
+};
+
+struct Chunks {
+  using Eight = u32x4;
+};
+__device__ __forceinline__ int codes_end(const CodeArgs& g) { return g.blocks * 32; }
+__device__ __forceinline__ int codes_end(const GemmArgs& g) { return g.K; }
+
 // XCD-aware order: workgroup b runs on XCD b % 8; each XCD takes a contiguous range.
 __device__ __forceinline__ int xcd_lin(int b, int total) {
   const int full = total & ~7;
@@ -280,6 +323,7 @@ template <bool HALF, bool AT, bool BT, int BM, int BN, int WM, int WN, bool EPI,
 __device__ __forceinline__ void gemm_tile(uint16_t* ring, G g, int mt, int nt, int lin, int k_per_split,
                                           float* __restrict__ part, int64_t ldpart) {
   constexpr bool kGated = std::is_same_v<G, GatedArgs>, kMx = std::is_same_v<G, MxArgs>;
+  constexpr bool kCodes = std::is_same_v<G, CodeArgs>;
   constexpr int NW = WM * WN, FI = BM / WM / 16, FJ = BN / WN / 16;
   constexpr int kSlot = (BM + BN) * kBK;
   lds_u16* lds = (lds_u16*)ring;
@@ -292,9 +336,11 @@ __device__ __forceinline__ void gemm_tile(uint16_t* ring, G g, int mt, int nt, i
   const int k0 = split * k_per_split, k1 = min(g.K, k0 + k_per_split);
 
   Side<AT, BM, NW> sa;
-  Side<BT, BN, NW> sb;
+  std::conditional_t<kCodes, CodeSide<HALF, BN, NW>, Side<BT, BN, NW>> sb;
   sa.init(g.a, g.lda, m0, g.M, k0, wave, lane);
-  if constexpr (kGated && EPI)
+  if constexpr (kCodes)
+    sb.init(g, n0, k0, wave, lane);
+  else if constexpr (kGated && EPI)
     sb.init_pair(g.b, g.ldb, g.b2, g.ldb2, n0, g.N, k0, wave, lane);
   else if constexpr (kGated && !AT)
     sb.init(g.b, g.ldb, n0, g.N, min(k0, g.half - kBK), wave, lane);  // of the first half; the second's follows
@@ -304,7 +350,8 @@ __device__ __forceinline__ void gemm_tile(uint16_t* ring, G g, int mt, int nt, i
   auto issue = [&](int slot, int t) {
     const int left = k1 - k0 - t * kBK;
     sa.issue(lds + slot * kSlot, left, wave, lane);
-    if constexpr (kGated && !EPI && !AT) {
+    if constexpr (kCodes) {
+    } else if constexpr (kGated && !EPI && !AT) {
       const int k = k0 + t * kBK, in_half = k < g.half ? k : k - g.half;
       if (k == g.half || (t == 0 && k > g.half)) sb.init(g.b2, g.ldb2, n0, g.N, in_half, wave, lane);
       sb.issue(lds + slot * kSlot + BM * kBK, g.valid - in_half, wave, lane);
@@ -374,13 +421,17 @@ __device__ __forceinline__ void gemm_tile(uint16_t* ring, G g, int mt, int nt, i
   const int stages = (k1 - k0 + kBK - 1) / kBK;  // 0 when K is 0
   if constexpr (REGS) {
     using SA = Side<AT, BM, NW>;
-    using SB = Side<BT, BN, NW>;
+    using SB = decltype(sb);
+    using Eight = typename std::conditional_t<kCodes, CodeSide<HALF, BN, NW>, Chunks>::Eight;
     constexpr int kSets = BM == 64 ? 2 : 1;  // two of 128-row tiles spill
-    u32x4 ra[kSets][SA::kCopies], rb[kSets][SB::kCopies];
+    u32x4 ra[kSets][SA::kCopies];
+    Eight rb[kSets][SB::kCopies];
+    // codes fill whole blocks of 32; x has zeros past its own end
+    const int kb = kCodes ? min(codes_end(g) - k0, k_per_split) : k1 - k0;
     auto load = [&](auto set, int t) __attribute__((always_inline)) {
       if (t >= stages) return;
       sa.load(ra[set], k1 - k0 - t * kBK, wave, lane);
-      sb.load(rb[set], k1 - k0 - t * kBK, wave, lane);
+      sb.load(rb[set], kb - t * kBK, wave, lane);
     };
     auto store = [&](auto set, int t) __attribute__((always_inline)) {
       if (t >= stages) return;

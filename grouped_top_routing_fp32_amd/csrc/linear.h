@@ -72,6 +72,14 @@ struct MxArgs : GemmArgs {
   int64_t ldsa, ldsb;
 };
 
+// The product of 16-bit rows with weights in microscaled 4 bits: b are the codes, ldb their row stride in bytes, and a
+// row has `blocks` of 32 codes and as many scales.  Operands go through registers.
+struct CodeArgs : GemmArgs {
+  const uint8_t* sb;
+  int64_t ldsb;
+  int blocks;
+};
+
 // Up to here the skinny kernel: 2560 columns, K 5120: 10.4 us at 16 rows against 12.7 in
 // tiles; a form of it for 32 rows took 15.9 against 12.8.
 constexpr int kSkinnyRows = 16;
@@ -140,6 +148,7 @@ hipError_t launch_pad(const PadJob& first, const PadJob& second, const PadJob& t
 hipError_t launch_gemm_bf16(const GemmArgs& g, const GemmSplit& s, int tile, hipStream_t st);
 hipError_t launch_gemm_f16(const GemmArgs& g, const GemmSplit& s, int tile, hipStream_t st);
 // `half`: a result of 16 bits is fp16, not bf16.
+hipError_t launch_code_tiles(const CodeArgs& g, const GemmSplit& s, int tile, hipStream_t st);  // 128 or 64
 hipError_t launch_mx_tiles(const MxArgs& g, const GemmSplit& s, int tile, bool half, hipStream_t st);
 hipError_t launch_gated_bf16(const GatedArgs& g, const GemmSplit& s, int tile, hipStream_t st);
 hipError_t launch_gated_f16(const GatedArgs& g, const GemmSplit& s, int tile, hipStream_t st);
@@ -166,6 +175,25 @@ __device__ __forceinline__ f32x4 mfma_mx(u32x4 a, u32x4 b, f32x4 c, uint32_t sa,
   const i32x8 wb = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
   constexpr int kE2M1 = 4;
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wa, wb, c, kE2M1, kE2M1, SA, (int)sa, SB, (int)sb);
+}
+
+// A scale byte of 32 codes as the FP32 that the converting instructions take.  They read its exponent field alone: 0
+// is 2^-127 to them, and 255 makes every result NaN.
+__device__ __forceinline__ float mx_scale(uint32_t e) { return __uint_as_float(e << 23); }
+
+// Eight codes as eight 16-bit values.
+template <bool HALF>
+__device__ __forceinline__ u32x4 codes_to_16(uint32_t c, float s) {
+  if constexpr (HALF)
+    return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, 0)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, 1)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, 2)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, 3))};
+  else
+    return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 0)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 1)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 2)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 3))};
 }
 
 // 1 / (1 + e^-z) from the hardware base-2 exponential and reciprocal, about 1 ulp each.

@@ -5,8 +5,8 @@
 //
 // Few rows are bound by reading w, a quarter of its 16-bit bytes: one kernel takes codes and scales straight from
 // memory.  With both operands in 4 bits the tiled product runs on scaled matrix instructions, four times the
-// 16-bit rate for the same bytes in LDS.  With x of 16 bits more rows take w as x's type, laid out once in the
-// workspace, and the plain product.
+// 16-bit rate for the same bytes in LDS.  With x of 16 bits, products of few tiles turn codes into x's type on
+// their way into LDS; larger ones lay w out as x's type in the workspace first and run the plain product.
 #include <algorithm>
 
 #include "mxfp4.h"
@@ -16,24 +16,6 @@ namespace {
 
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 constexpr int kCUs = 256;
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-
-// Eight codes as eight 16-bit values.
-template <bool HALF>
-__device__ __forceinline__ u32x4 codes_to_16(uint32_t c, float s) {
-  if constexpr (HALF)
-    return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, 0)),
-                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, 1)),
-                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, 2)),
-                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, 3))};
-  else
-    return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 0)),
-                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 1)),
-                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 2)),
-                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 3))};
-}
-
 // Few rows (M <= 16).  A workgroup takes `cols` <= 16 columns and its 16 waves share K in pieces of 128: a lane
 // (row l % 16, block l / 16) takes one block of 32 codes, 16 bytes, and its scale.  With x of 16 bits the
 // products' K runs over the four blocks' first 8 elements, then their second 8, and so on, which is the same
@@ -100,8 +82,13 @@ MxPlan plan_mx(int M, int N, int K, bool four, int64_t ldx) {
     p.total = p.gemm.total;
     return p;
   }
-  p.copy_x = !regular_rows(ldx, K);
   p.gemm = plan_tiles(M, N, (int)up8(K));
+  p.fused = few_tiles(p.gemm, (int64_t)ceil_div(M, p.gemm.tile) * ceil_div(N, p.gemm.tile), K);
+  if (p.fused) {
+    p.total = p.gemm.total;
+    return p;
+  }
+  p.copy_x = !regular_rows(ldx, K);
   p.off_w = p.copy_x ? up256(padded_bytes(M, K)) : 0;
   p.off_gemm = p.off_w + up256((size_t)N * blocks * kMxBlock * 2);
   p.total = p.off_gemm + p.gemm.total;
@@ -131,6 +118,16 @@ hipError_t launch_linear_mx(const MxLinear& a, const MxPlan& p, void* ws, hipStr
     g.K = 8 * blocks;
     const GemmSplit s = split_of(p.gemm, g.N, base);
     e = launch_mx_tiles(g, s, p.gemm.tile, half, st);
+    return e != hipSuccess ? e : launch_join_one(g, s, st);
+  }
+  if (p.fused) {
+    CodeArgs g{a.g, a.w_scales, a.ldws, blocks};
+    g.a = a.x;
+    g.lda = a.ldx;
+    g.b = a.w;
+    g.ldb = a.ldw;
+    const GemmSplit s = split_of(p.gemm, g.N, base);
+    e = launch_code_tiles(g, s, p.gemm.tile, st);
     return e != hipSuccess ? e : launch_join_one(g, s, st);
   }
   GemmArgs g = a.g;

@@ -13,10 +13,6 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 inline int64_t mx_blocks(int64_t cols) { return (cols + kMxBlock - 1) / kMxBlock; }
 
-// A scale byte as the FP32 that the converting instructions take.  They read its exponent field alone: 0 is
-// 2^-127 to them, and 255 makes every result NaN.
-__device__ __forceinline__ float mx_scale(uint32_t e) { return __uint_as_float(e << 23); }
-
 // The scale byte of a block whose largest magnitude has the bits `top` (FP32): 2^(floor(log2) - 2),
 // so that the largest lies in [4, 8) of it.  Subnormals are floored to FP32's least normal.  An infinity or NaN
 // among the 32 makes it NaN.
@@ -45,6 +41,7 @@ struct MxLinear {
 };
 struct MxPlan {
   GemmPlan gemm;
+  bool fused;                // codes become x's type on their way into LDS; else:
   bool copy_x;               // x is laid out anew in the workspace, and w as x's type behind it
   size_t off_w, off_gemm, total;
 };
