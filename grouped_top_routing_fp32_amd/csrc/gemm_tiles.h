@@ -140,20 +140,22 @@ template <int R>
 struct ScaleStage {
   static constexpr int kBytes = R * 8;
   typedef __attribute__((address_space(3))) uint8_t lds_u8;
-  typedef u32x2 u32x2_byte __attribute__((aligned(1)));
-  // Blocks b .. b + 7 of a row of `blocks`; 0 past them, where the codes are 0 too.
-  static __device__ __forceinline__ u32x2 load(const uint8_t* row, int b, int blocks) {
-    if (b + 8 <= blocks) return *reinterpret_cast<const u32x2_byte*>(row + b);
-    u32x2 v = {0u, 0u};
+  typedef uint64_t u64_byte __attribute__((aligned(1)));
+  // Blocks b .. b + 7 of a row of `blocks`.  Past the row's end they are 0, where the codes are 0 too: there the row's
+  // last eight are requested, and moved down when they are stored.
+  static __device__ __forceinline__ uint64_t load(const uint8_t* row, int b, int blocks) {
+    if (blocks >= 8) return *reinterpret_cast<const u64_byte*>(row + min(b, blocks - 8));
+    uint64_t v = 0;
 #pragma unroll
     for (int q = 0; q < 8; ++q)
-      if (b + q < blocks) v[q / 4] |= (uint32_t)row[b + q] << (8 * (q % 4));
+      if (q < blocks) v |= (uint64_t)row[q] << (8 * q);
     return v;
   }
-  static __device__ __forceinline__ void store(lds_u8* stage, int r, u32x2 v) {
+  static __device__ __forceinline__ void store(lds_u8* stage, int r, uint64_t v, int b, int blocks) {
+    if (blocks >= 8) v >>= 8 * max(b + 8 - blocks, 0);
     lds_u8* p = stage + (r >> 6) * 512 + (r & 15) * 8 + ((r >> 4) & 3);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) p[(q % 4) * 128 + (q / 4) * 4] = (uint8_t)(v[q / 4] >> (8 * (q % 4)));
+    for (int q = 0; q < 8; ++q) p[(q % 4) * 128 + (q / 4) * 4] = (uint8_t)(v >> (8 * q));
   }
   // The words (s = 0, 1) of rows r0 .. r0 + 63, or the upper half of them moved down where r0 is off 64 by 32.
   static __device__ __forceinline__ u32x2 words(const lds_u8* stage, int r0, int lane) {
@@ -364,14 +366,15 @@ __device__ __forceinline__ void gemm_tile(uint16_t* ring, G g, int mt, int nt, i
   using lds_u8 = typename Scales::lds_u8;
   [[maybe_unused]] lds_u8* scales = (lds_u8*)(lds + 2 * kSlot);
   [[maybe_unused]] const uint8_t* scale_row = nullptr;
-  [[maybe_unused]] u32x2 next_scales = {0u, 0u};
+  [[maybe_unused]] uint64_t next_scales = 0;
   [[maybe_unused]] auto load_scales = [&](int t) __attribute__((always_inline)) {
     if constexpr (kMx)
       if (tid < BM + BN && k0 + t * kBK < k1) next_scales = Scales::load(scale_row, (k0 + t * kBK) / 8, g.K / 8);
   };
-  [[maybe_unused]] auto store_scales = [&](int slot) __attribute__((always_inline)) {
+  [[maybe_unused]] auto store_scales = [&](int t) __attribute__((always_inline)) {
     if constexpr (kMx)
-      if (tid < BM + BN) Scales::store(scales + slot * Scales::kBytes, tid, next_scales);
+      if (tid < BM + BN)
+        Scales::store(scales + (t & 1) * Scales::kBytes, tid, next_scales, (k0 + t * kBK) / 8, g.K / 8);
   };
   if constexpr (kMx)
     scale_row = tid < BM ? g.sa + (int64_t)min(m0 + tid, g.M - 1) * g.ldsa
@@ -476,7 +479,7 @@ __device__ __forceinline__ void gemm_tile(uint16_t* ring, G g, int mt, int nt, i
       __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
       barrier();
       if (st + 1 < stages) {
-        store_scales((st + 1) & 1);
+        store_scales(st + 1);
         load_scales(st + 2);
         issue((st + 1) & 1, st + 1);
       }
