@@ -127,7 +127,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             ("beam_moe_clip_grads", ci, [i32, vp, vp, vp, f32, f32, f32, vp, vp, vp, vp, vp, sz, vp]),
             ("beam_moe_quantize_mxfp4", ci, [i32, i32, vp, ci, i64, vp, i64, vp, i64, vp]),
             ("beam_moe_dequantize_mxfp4", ci, [i32, i32, vp, i64, vp, i64, vp, ci, i64, vp]),
-            ("beam_moe_linear_mxfp4_workspace_bytes", sz, [i32, i32, i32, ci, i64]),
+            ("beam_moe_linear_mxfp4_workspace_bytes", sz, [i32, i32, i32, ci, i64, i64]),
             ("beam_moe_linear_mxfp4", ci, [i32, i32, i32, ci, vp, i64, vp, i64, vp, i64, vp, i64, vp, ci, vp, i64, f32,
                                            f32, vp, ci, i64, vp, sz, vp])):
         getattr(lib, fn).argtypes = args
@@ -986,7 +986,7 @@ def beam_moe_linear_mxfp4(x, w: Mxfp4, bias: Optional[torch.Tensor] = None, *, a
     with _On(dev, stream) as st:
         out, ldy = _result(out, out_dtype, default, types, (M, N), dev)
         ldr = 0 if residual is None else _rows(residual, "residual", (out.dtype,), (M, N), dev)
-        wp, wn, _keep = _scratch(_linear_ws("beam_moe_linear_mxfp4_workspace_bytes", M, N, K, xt, ldx), ws, dev,
+        wp, wn, _keep = _scratch(_linear_ws("beam_moe_linear_mxfp4_workspace_bytes", M, N, K, xt, ldx, ldw), ws, dev,
                                  "beam_moe_linear_mxfp4")
         _check(load_library().beam_moe_linear_mxfp4(
             M, N, K, xt, xp, ldx, xsp, ldxs, codes.data_ptr(), ldw, scales.data_ptr(), ldws, b, a,

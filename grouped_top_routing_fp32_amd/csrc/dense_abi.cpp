@@ -357,12 +357,13 @@ int beam_moe_dequantize_mxfp4(int32_t rows, int32_t cols, const uint8_t* codes, 
                                                static_cast<hipStream_t>(stream)));
 }
 
-size_t beam_moe_linear_mxfp4_workspace_bytes(int32_t rows, int32_t cols, int32_t inner, int x_type, int64_t ldx) {
+size_t beam_moe_linear_mxfp4_workspace_bytes(int32_t rows, int32_t cols, int32_t inner, int x_type, int64_t ldx,
+                                             int64_t ldw) {
   const bool four = x_type == BEAM_MOE_MXFP4;
   if (check_mx_linear(rows, cols, inner) != BEAM_MOE_OK || !(four || half_type(x_type)) ||
-      !ld_ok(ldx, four ? 16 * beam::mx_blocks(inner) : inner))
+      !ld_ok(ldx, four ? 16 * beam::mx_blocks(inner) : inner) || !ld_ok(ldw, 16 * beam::mx_blocks(inner)))
     return SIZE_MAX;
-  return beam::plan_mx(rows, cols, inner, four, ldx).total;
+  return beam::plan_mx(rows, cols, inner, four, ldx, ldw).total;
 }
 
 int beam_moe_linear_mxfp4(int32_t rows, int32_t cols, int32_t inner, int x_type, const void* x, int64_t ldx,
@@ -382,7 +383,7 @@ int beam_moe_linear_mxfp4(int32_t rows, int32_t cols, int32_t inner, int x_type,
   if ((rc = check_ptrs({x, w, w_scales, y})) != BEAM_MOE_OK) return rc;
   if (four && (rc = check_ptrs({x_scales})) != BEAM_MOE_OK) return rc;
   if ((rc = check_optional({bias, res})) != BEAM_MOE_OK) return rc;
-  const beam::MxPlan plan = beam::plan_mx(rows, cols, inner, four, ldx);
+  const beam::MxPlan plan = beam::plan_mx(rows, cols, inner, four, ldx, ldw);
   if (plan.total && (!ws || !aligned16(ws) || ws_bytes < plan.total)) return BEAM_MOE_ERR_WORKSPACE;
   beam::MxLinear a{};
   a.four = four;

@@ -147,9 +147,13 @@ inline size_t padded_bytes(int rows, int cols) { return (size_t)rows * up8(cols)
 hipError_t launch_pad(const PadJob& first, const PadJob& second, const PadJob& third, hipStream_t st);
 hipError_t launch_gemm_bf16(const GemmArgs& g, const GemmSplit& s, int tile, hipStream_t st);
 hipError_t launch_gemm_f16(const GemmArgs& g, const GemmSplit& s, int tile, hipStream_t st);
-// `half`: a result of 16 bits is fp16, not bf16.
-hipError_t launch_code_tiles(const CodeArgs& g, const GemmSplit& s, int tile, hipStream_t st);  // 128 or 64
+// In tiles of 128 or 64.
+hipError_t launch_code_tiles(const CodeArgs& g, const GemmSplit& s, int tile, hipStream_t st);
+// The same; `half`: a result of 16 bits is fp16, not bf16.
 hipError_t launch_mx_tiles(const MxArgs& g, const GemmSplit& s, int tile, bool half, hipStream_t st);
+// In 256-row tiles, with the scales laid out in ws; 256 rows of either operand span less than 2^31 bytes.
+size_t mx_stream_bytes(int M, int N, int K);
+hipError_t launch_mx_stream(const MxArgs& g, void* ws, hipStream_t st);
 hipError_t launch_gated_bf16(const GatedArgs& g, const GemmSplit& s, int tile, hipStream_t st);
 hipError_t launch_gated_f16(const GatedArgs& g, const GemmSplit& s, int tile, hipStream_t st);
 hipError_t launch_gated_pair_bf16(const GatedArgs& dx, const GemmSplit& sx, const GatedArgs& dw, const GemmSplit& sw,

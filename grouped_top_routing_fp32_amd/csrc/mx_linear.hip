@@ -8,6 +8,7 @@
 // 16-bit rate for the same bytes in LDS.  With x of 16 bits, products of few tiles turn codes into x's type on
 // their way into LDS; larger ones lay w out as x's type in the workspace first and run the plain product.
 #include <algorithm>
+#include <cmath>
 
 #include "mxfp4.h"
 
@@ -71,14 +72,37 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void mx_skinny_kernel(MxLinear a
   by_act(g.act, [&](auto act) { epilogue4<decltype(act)::value>(g, g.add, l16, n, n1, z); });
 }
 
+// Two operands in 4 bits, K of `units` of four codes.  A long K of few tiles is split as any product's.  Else the
+// tile with the least of these estimates, in microseconds with S the stages of K; they meet 21 shapes of 256 to 16384
+// rows, 512 to 5120 columns and K of 200 to 5120 to some 15%, and nearer where the choice is close:
+// - 64: t (0.003 + 0.0013 S) + 3 ([512, 5120] x [5120, 5120], 640 tiles, 20.2 us; 22.6 in 128-row tiles, 41.9 in 256)
+// - 128: rounds of 512 tiles of 4 + 1.45 S, + 3 ([2000, 2000] x [3000, 2000], 384 tiles, 19.8; 21.8 and 28.0)
+// - 256: rounds of 256 tiles of 5.5 + 1.9 S, + 6.5, the scales' launch among it ([16384, 2560] x [5120, 2560], 1280
+//   tiles, 132 us; 180 in 128-row tiles; [2048, 5120] x [5120, 5120], 160 tiles, 48.8 and 54.6, but [8192, 5120] x
+//   [1024, 5120], 128, 46.5 and 38.2)
+GemmPlan plan_mx_tiles(int M, int N, int units, bool wide_rows) {
+  GemmPlan p = plan_tiles(M, N, units);
+  if (p.splits > 1) return p;
+  const double S = ceil_div(units, 64);
+  auto tiles = [&](int t) { return (double)ceil_div(M, t) * ceil_div(N, t); };
+  const double small = tiles(64) * (0.003 + 0.0013 * S) + 3.;
+  const double middle = std::ceil(tiles(128) / 512) * (4. + 1.45 * S) + 3.;
+  const double large = std::ceil(tiles(256) / 256) * (5.5 + 1.9 * S) + 6.5;
+  p.tile = !wide_rows && large <= std::min(small, middle) ? 256 : small <= middle ? 64 : 128;
+  if (tiles(64) > 1 << 20) p.tile = wide_rows ? 128 : 256;  // threads of a grid fit 32 bits
+  p.total = p.tile == 256 ? mx_stream_bytes(M, N, units) : 0;
+  return p;
+}
+
 }  // namespace
 
-MxPlan plan_mx(int M, int N, int K, bool four, int64_t ldx) {
+MxPlan plan_mx(int M, int N, int K, bool four, int64_t ldx, int64_t ldw) {
   MxPlan p{};
   if (M <= kSkinnyRows) return p;
   const int blocks = (int)mx_blocks(K);
   if (four) {
-    p.gemm = plan_tiles(M, N, 8 * blocks);  // units of four codes
+    // 256 rows of an operand span less than 2^31 bytes in the large product
+    p.gemm = plan_mx_tiles(M, N, 8 * blocks, std::max(ldx, ldw) >= int64_t(1) << 23);
     p.total = p.gemm.total;
     return p;
   }
@@ -116,6 +140,7 @@ hipError_t launch_linear_mx(const MxLinear& a, const MxPlan& p, void* ws, hipStr
     g.b = a.w;
     g.ldb = a.ldw / 2;
     g.K = 8 * blocks;
+    if (p.gemm.tile == 256) return launch_mx_stream(g, base, st);
     const GemmSplit s = split_of(p.gemm, g.N, base);
     e = launch_mx_tiles(g, s, p.gemm.tile, half, st);
     return e != hipSuccess ? e : launch_join_one(g, s, st);

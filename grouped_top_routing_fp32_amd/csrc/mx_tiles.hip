@@ -5,15 +5,14 @@ namespace beam {
 
 hipError_t launch_mx_tiles(const MxArgs& g, const GemmSplit& s, int tile, bool half, hipStream_t st) {
   const int mt = (g.M + tile - 1) / tile, nt = (g.N + tile - 1) / tile, total = mt * nt * s.splits;
-  auto go = [&](auto kernel, int threads) {
-    hipLaunchKernelGGL(kernel, dim3(total), dim3(threads), 0, st, g, mt, nt, total, s.k_per_split, s.part, s.ld);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(total), dim3(256), 0, st, g, mt, nt, total, s.k_per_split, s.part, s.ld);
     return hipGetLastError();
   };
   auto of = [&](auto h) {
     constexpr bool kHalf = decltype(h)::value;
-    if (tile == 256) return go(gemm_kernel<kHalf, false, false, 256, 256, 4, 2, true, false, MxArgs>, 512);
-    if (tile == 128) return go(gemm_kernel<kHalf, false, false, 128, 128, 2, 2, true, false, MxArgs>, 256);
-    return go(gemm_kernel<kHalf, false, false, 64, 64, 2, 2, true, false, MxArgs>, 256);
+    if (tile == 128) return go(gemm_kernel<kHalf, false, false, 128, 128, 2, 2, true, false, MxArgs>);
+    return go(gemm_kernel<kHalf, false, false, 64, 64, 2, 2, true, false, MxArgs>);
   };
   return half ? of(std::true_type{}) : of(std::false_type{});
 }

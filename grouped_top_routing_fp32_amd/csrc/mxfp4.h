@@ -45,7 +45,7 @@ struct MxPlan {
   bool copy_x;               // x is laid out anew in the workspace, and w as x's type behind it
   size_t off_w, off_gemm, total;
 };
-MxPlan plan_mx(int M, int N, int K, bool four, int64_t ldx);
+MxPlan plan_mx(int M, int N, int K, bool four, int64_t ldx, int64_t ldw);
 hipError_t launch_linear_mx(const MxLinear& a, const MxPlan& p, void* ws, hipStream_t st);
 
 }  // namespace beam

@@ -557,8 +557,10 @@ int beam_moe_quantize_mxfp4(int32_t rows, int32_t cols, const void* x, int x_typ
 int beam_moe_dequantize_mxfp4(int32_t rows, int32_t cols, const uint8_t* codes, int64_t ldc, const uint8_t* scales,
                               int64_t lds, void* y, int y_type, int64_t ldy, void* stream);
 
-/* Workspace of beam_moe_linear_mxfp4.  Returns SIZE_MAX for unsupported sizes. */
-size_t beam_moe_linear_mxfp4_workspace_bytes(int32_t rows, int32_t cols, int32_t inner, int x_type, int64_t ldx);
+/* Workspace of beam_moe_linear_mxfp4; the leading dimensions are those of the call.  Returns SIZE_MAX for
+ * unsupported sizes. */
+size_t beam_moe_linear_mxfp4_workspace_bytes(int32_t rows, int32_t cols, int32_t inner, int x_type, int64_t ldx,
+                                             int64_t ldw);
 
 /* beam_moe_linear with weights in MXFP4, and x in a 16-bit type or in MXFP4 as well:
  *   z = x w^T + bias,  y = keep * res + add * act(z)

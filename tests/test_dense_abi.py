@@ -158,14 +158,19 @@ def test_gated_workspaces():
 
 def test_mx_workspaces():
     need = binding.load_library().beam_moe_linear_mxfp4_workspace_bytes
-    assert need(16, 1000, 1000, BF16, 1000) == 0 and need(16, 1000, 1000, MX, 512) == 0
-    assert need(8192, 2560, 5120, MX, 2560) == 0
-    assert need(64, 2560, 5120, BF16, 5120) >= 2560 * 5120 * 2
-    assert need(-1, 8, 8, BF16, 8) == need(8, 8, 8, BF16, 7) == need(8, 8, 8, MX, 8) == need(8, 8, 8, F32, 8) \
-        == need(8, 0, 8, BF16, 8) == binding.SIZE_MAX
-    n = need(64, 10, 70, BF16, 70)
+    assert need(16, 1000, 1000, BF16, 1000, 512) == 0 and need(16, 1000, 1000, MX, 512, 512) == 0
+    assert need(300, 300, 1000, MX, 512, 512) == 0
+    # scales laid out by tiles: a byte to a block of 32
+    assert need(8192, 2560, 5120, MX, 2560, 2560) == (8192 + 2560) * 160
+    assert need(8192, 2560, 5120, MX, 2560, 1 << 23) == 0
+    assert need(64, 2560, 5120, BF16, 5120, 2560) > 0                          # split
+    assert need(8192, 2560, 5120, BF16, 5120, 2560) >= 2560 * 5120 * 2         # w as x's type
+    assert need(-1, 8, 8, BF16, 8, 16) == need(8, 8, 8, BF16, 7, 16) == need(8, 8, 8, MX, 8, 16) \
+        == need(8, 8, 8, F32, 8, 16) == need(8, 0, 8, BF16, 8, 16) == need(8, 8, 8, BF16, 8, 8) == binding.SIZE_MAX
+    n = need(8192, 2560, 5120, MX, 2560, 2560)
     for bad in (dict(ws=None), dict(ws=ODD), dict(ws_bytes=n - 1)):
-        assert MX_LINEAR(rows=64, **bad) == WS
+        assert MX_BOTH(rows=8192, cols=2560, inner=5120, ldx=2560, ldxs=160, ldw=2560, ldws=160, ldy=2560, ldr=2560,
+                       **bad) == WS
 
 
 def test_no_rows():
