@@ -249,7 +249,7 @@ __global__ __launch_bounds__(512) void mx_stream_kernel(MxArgs g, int mt, int nt
       constexpr int ACT = decltype(act)::value;
       auto value = [&](int i, int j) __attribute__((always_inline)) {
         f32x4 z = acc[i][j];
-        if (g.bias) {
+        if (g.bias && n + 16 * j + 4 * gr < g.N) {
           const f32x4 b = *reinterpret_cast<const f32x4_any*>(g.bias + n + 16 * j + 4 * gr);
 #pragma unroll
           for (int q = 0; q < 4; ++q) z[q] += b[q];
@@ -260,17 +260,19 @@ __global__ __launch_bounds__(512) void mx_stream_kernel(MxArgs g, int mt, int nt
       };
 #pragma unroll
       for (int i = 0; i < kMxFI; ++i) {
+        const int end = m + 16 * i < g.M ? g.N : 0;  // of the columns that this row stores
         if constexpr (kWide) {
           const int64_t o = (int64_t)(m + 16 * i) * g.ldo + n + 4 * gr, r = (int64_t)(m + 16 * i) * g.ldr + n + 4 * gr;
 #pragma unroll
           for (int j = 0; j < kMxFJ; ++j) {
             f32x4 v = value(i, j);
-            if (g.res) {
+            const bool here = n + 4 * gr + 16 * j < end;
+            if (g.res && here) {
               const f32x4 w = __builtin_nontemporal_load(reinterpret_cast<const f32x4_any*>(res + r + 16 * j));
 #pragma unroll
               for (int q = 0; q < 4; ++q) v[q] += g.keep * w[q];
             }
-            __builtin_nontemporal_store(v, reinterpret_cast<f32x4_any*>(out + o + 16 * j));
+            if (here) __builtin_nontemporal_store(v, reinterpret_cast<f32x4_any*>(out + o + 16 * j));
             fence();
           }
         } else {
@@ -279,8 +281,11 @@ __global__ __launch_bounds__(512) void mx_stream_kernel(MxArgs g, int mt, int nt
 #pragma unroll
           for (int j = 0; j < kMxFJ; j += 2) {
             f32x4 v = value(i, j), w = value(i, j + 1);
+            const bool here = c + 16 * j < end;
             if (g.res) {
-              const u32x4 raw = swap_fragments(*reinterpret_cast<const u32x4_any*>(res + r + 16 * j));
+              u32x4 raw = {0u, 0u, 0u, 0u};
+              if (here) raw = *reinterpret_cast<const u32x4_any*>(res + r + 16 * j);
+              raw = swap_fragments(raw);
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
                 v[q] += g.keep * OT::up((uint16_t)(raw[q / 2] >> (16 * (q % 2))));
@@ -293,13 +298,15 @@ __global__ __launch_bounds__(512) void mx_stream_kernel(MxArgs g, int mt, int nt
               h[q] = OT::down(v[2 * q]) | (uint32_t)OT::down(v[2 * q + 1]) << 16;
               h[2 + q] = OT::down(w[2 * q]) | (uint32_t)OT::down(w[2 * q + 1]) << 16;
             }
-            *reinterpret_cast<u32x4_any*>(out + o + 16 * j) = swap_fragments(h);
+            h = swap_fragments(h);
+            if (here) *reinterpret_cast<u32x4_any*>(out + o + 16 * j) = h;
             fence();
           }
         }
       }
     };
-    if (inside) {
+    // whole chunks of columns, eight to a lane: all but the last tiles of a row of results where N is no multiple
+    if ((p.ni + 1) * kMxT <= g.N || g.N % 8 == 0) {
       by_act(g.act, results);
     } else {
       auto edge = [&](auto act) __attribute__((always_inline)) {

@@ -799,6 +799,56 @@ def test_linear_mxfp4_of_two(M, N, K):
         _mx_linear_check(_mx_values(x, K), _mx_values(w, K), bias, act, r, keep, add, y)
 
 
+# 256-row tiles, whose scales need a workspace: rows and columns that end inside a tile or a chunk of eight, one tile to
+# a workgroup and several, K inside a block, a half and a stage
+MX_LARGE = [(4096, 4096, 512), (3900, 3995, 1003), (3990, 3992, 520), (4000, 3905, 256), (5000, 5003, 300), (9000, 4360, 96),
+            (2500, 5120, 2600)]
+
+
+@pytest.mark.parametrize("M,N,K", MX_LARGE)
+def test_linear_mxfp4_of_two_large(M, N, K):
+    g = _gen(M * 3 + N * 5 + K + 2)
+    for act, yt, res, pad in (("none", BF16, False, 0), ("silu", F32, True, 0), ("gelu", F16, True, 1),
+                              ("relu", BF16, True, 3), ("none", F16, False, 5), ("none", F32, False, 1)):
+        _say("linear_mxfp4 large", M, N, K, act, yt, res, pad)
+        x, w = _mx_weights(g, M, K, pad, 3), _mx_weights(g, N, K, pad)
+        assert fw.load_library().beam_moe_linear_mxfp4_workspace_bytes(M, N, K, 3, x.codes.stride(0),
+                                                                       w.codes.stride(0)) > 0
+        bias = _randn(g, (N,)) if act in ("silu", "gelu") else None
+        r = _randn(g, (M, N), yt, 1.0, pad) if res else None
+        keep, add = (math.sqrt(2 / 3), math.sqrt(1 / 3)) if res else (1.0, 1.0)
+        buf = torch.full((M, N + pad), 7.0, dtype=yt, device=DEV)
+        y = fw.beam_moe_linear_mxfp4(x, w, bias, act=act, residual=r, keep=keep, add=add, out=buf[:, :N])
+        _mx_linear_check(_mx_values(x, K), _mx_values(w, K), bias, act, r, keep, add, y)
+        assert (buf[:, N:] == 7.0).all()
+        again = fw.beam_moe_linear_mxfp4(x, w, bias, act=act, residual=r, keep=keep, add=add, out_dtype=yt)
+        assert torch.equal(again, y)
+
+
+def test_linear_mxfp4_large_nan_and_replay():
+    """A NaN scale in its own row or column alone; captured and replayed beside eager calls."""
+    _say("linear_mxfp4 large nan")
+    M, N, K = 3900, 3995, 300
+    g = _gen(12)
+    x, w = _mx_weights(g, M, K), _mx_weights(g, N, K)
+    want = fw.beam_moe_linear_mxfp4(x, w)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        got = fw.beam_moe_linear_mxfp4(x, w)
+    for k in range(3):
+        x.scales[1000 + k, 9] = 255
+        w.scales[3990 - 300 * k, 0] = 255
+        graph.replay()
+        torch.cuda.synchronize()
+        rows, cols = torch.ones(M, dtype=torch.bool, device=DEV), torch.ones(N, dtype=torch.bool, device=DEV)
+        rows[1000:1001 + k] = False
+        cols[[3990 - 300 * i for i in range(k + 1)]] = False
+        assert torch.equal(got[rows][:, cols], want[rows][:, cols])
+        assert got[~rows].isnan().all() and got[:, ~cols].isnan().all()
+        assert torch.equal(fw.beam_moe_linear_mxfp4(x, w).nan_to_num(), got.nan_to_num())
+
+
 @pytest.mark.parametrize("M,N,K", [(3, 40, 100), (70, 90, 1003), (300, 264, 128)])
 def test_linear_mxfp4_places(M, N, K):
     """Each block of K by itself: one code of x and of w set, every other zero, so that a wrong block, scale or order
