@@ -134,7 +134,7 @@ GatedBackwardPlan gated_backward_plan(int32_t rows, int32_t cols, int32_t inner,
   p.copy_gate = !beam::regular_rows(ldg, inner);
   p.copy_up = !beam::regular_rows(ldu, inner);
   p.copy_x = !beam::regular_rows(ldx, inner);
-  beam::plan_gradients(rows, wide, inner, &p.dx, &p.dw);
+  beam::plan_gated_gradients(rows, cols, inner, &p.dx, &p.dw);
   p.off_part = align_up((size_t)rows * wide * 2);
   p.off_scale = p.off_part + align_up((size_t)beam::gated_dz_units(rows) * 2 * cols * sizeof(float));
   p.off_gate = p.off_scale + kScaleBytes + align_up(beam::gated_peak_bytes());

@@ -16,6 +16,8 @@ struct GatedPlan {
 GatedPlan plan_gated(int M, int N, int K, int64_t ldx, int64_t ldg, int64_t ldu);
 hipError_t launch_gated(const GatedArgs& g, const GatedPlan& p, void* ws, hipStream_t st);
 
+// dx and dw of a gated layer of N columns, planned together.
+void plan_gated_gradients(int rows, int N, int inner, GemmPlan* dx, GemmPlan* dw);
 int gated_dz_units(int M);
 size_t gated_peak_bytes();
 struct GatedDz {
@@ -35,7 +37,7 @@ struct GatedDz {
 hipError_t launch_gated_dz(const GatedDz& d, PadJobs pad, hipStream_t st);
 // The bias gradients by themselves (beside dx's product they need no launch).
 hipError_t launch_gated_sums(const SumJob& j, hipStream_t st);
-// Both products of the backward pass, or one (the other's out null), as planned by plan_gradients.
+// Both products of the backward pass, or one (the other's out null), as planned together.
 hipError_t launch_gated_gradients(const GatedArgs& dx, const GemmPlan& px, const GatedArgs& dw, const GemmPlan& pw,
                                   void* ws, hipStream_t st);
 

@@ -322,6 +322,20 @@ hipError_t launch_gated(const GatedArgs& args, const GatedPlan& p, void* ws, hip
   return hipGetLastError();
 }
 
+void plan_gated_gradients(int rows, int N, int inner, GemmPlan* dx, GemmPlan* dw) {
+  const int wide = 2 * gated_half(N);
+  plan_gradients(rows, wide, inner, dx, dw);
+  if (dx->paired || dx->tile != 256 || dw->tile != 256) return;
+  // 256-row tiles for both: in one launch, those with the longer K first, where together they end sooner by this
+  // count of stages ([8192, 5120] x [2560, 5120], 640 tiles of 80 and 400 of 128, 448 stages against 496, 810 us
+  // against 870; [12712, 4352] x [1664, 4352] 680 against 735; where the counts are near each other so are the times)
+  const int tx = ceil_div(rows, 256) * ceil_div(inner, 256), tw = ceil_div(wide, 256) * ceil_div(inner, 256);
+  const int lx = ceil_div(wide, 64), lw = ceil_div(rows, 64);
+  const int64_t together = lx >= lw ? pair_stages(tx, lx, tw, lw, kCUs) : pair_stages(tw, lw, tx, lx, kCUs);
+  const int64_t apart = (int64_t)ceil_div(tx, kCUs) * lx + (int64_t)ceil_div(tw, kCUs) * lw;
+  dx->paired = dw->paired = (double)together < 0.97 * (double)apart;
+}
+
 size_t gated_peak_bytes() { return kMaxPeaks * sizeof(uint32_t); }
 
 int gated_dz_units(int M) { return M < 8 ? 1 : M / 4 < 256 ? M / 4 : 256; }

@@ -9,6 +9,7 @@ hipError_t launch_gated_bf16(const GatedArgs& g, const GemmSplit& s, int tile, h
 
 hipError_t launch_gated_pair_bf16(const GatedArgs& dx, const GemmSplit& sx, const GatedArgs& dw, const GemmSplit& sw,
                                  int tile, hipStream_t st) {
+  if (tile == 256) return launch_gemm_pair<false, 256>(dx, sx, dw, sw, st);
   return tile == 128 ? launch_gemm_pair<false, 128>(dx, sx, dw, sw, st) : launch_gemm_pair<false, 64>(dx, sx, dw, sw, st);
 }
 

@@ -9,6 +9,7 @@ hipError_t launch_gated_f16(const GatedArgs& g, const GemmSplit& s, int tile, hi
 
 hipError_t launch_gated_pair_f16(const GatedArgs& dx, const GemmSplit& sx, const GatedArgs& dw, const GemmSplit& sw,
                                  int tile, hipStream_t st) {
+  if (tile == 256) return launch_gemm_pair<true, 256>(dx, sx, dw, sw, st);
   return tile == 128 ? launch_gemm_pair<true, 128>(dx, sx, dw, sw, st) : launch_gemm_pair<true, 64>(dx, sx, dw, sw, st);
 }
 

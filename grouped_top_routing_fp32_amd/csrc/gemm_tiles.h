@@ -620,7 +620,8 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(G g, int mt, int nt, 
 // with the longer K come first.  (In 256-row tiles nothing is gained: 429 us either way at [8192,
 // 5120] x [2560, 5120], 640 and 200 tiles, although fewer CUs idle.)
 template <bool HALF, int TILE, class G>
-__global__ __launch_bounds__(256) void gemm_pair_kernel(G dx, GemmSplit sx, G dw, GemmSplit sw) {
+__global__ __launch_bounds__(TILE == 256 ? 512 : 256) void gemm_pair_kernel(G dx, GemmSplit sx, G dw, GemmSplit sw) {
+  constexpr int WM = TILE == 256 ? 4 : 2;
   __shared__ __align__(1024) uint16_t ring[kRing<TILE, TILE>];
   const int mx = (dx.M + TILE - 1) / TILE, nx = (dx.N + TILE - 1) / TILE;
   const int mw = (dw.M + TILE - 1) / TILE, nw = (dw.N + TILE - 1) / TILE;
@@ -628,10 +629,10 @@ __global__ __launch_bounds__(256) void gemm_pair_kernel(G dx, GemmSplit sx, G dw
   int b = blockIdx.x;  // in the order dx, dw, sums
   if (b < first + second && sw.k_per_split > sx.k_per_split) b = b < second ? b + first : b - second;
   if (b < first)
-    gemm_tile<HALF, false, true, TILE, TILE, 2, 2, false>(ring, dx, mx, nx, xcd_lin(b, first), sx.k_per_split,
+    gemm_tile<HALF, false, true, TILE, TILE, WM, 2, false>(ring, dx, mx, nx, xcd_lin(b, first), sx.k_per_split,
                                                           sx.part, sx.ld);
   else if (b < first + second)
-    gemm_tile<HALF, true, true, TILE, TILE, 2, 2, false>(ring, dw, mw, nw, xcd_lin(b - first, second),
+    gemm_tile<HALF, true, true, TILE, TILE, WM, 2, false>(ring, dw, mw, nw, xcd_lin(b - first, second),
                                                          sw.k_per_split, sw.part, sw.ld);
   else
     sum_columns(reinterpret_cast<float*>(ring), dx.sums, b - first - second);
@@ -641,8 +642,8 @@ template <bool HALF, int TILE, class G>
 hipError_t launch_gemm_pair(const G& dx, const GemmSplit& sx, const G& dw, const GemmSplit& sw, hipStream_t st) {
   auto tiles = [](const GemmArgs& g) { return ((g.M + TILE - 1) / TILE) * ((g.N + TILE - 1) / TILE); };
   hipLaunchKernelGGL((gemm_pair_kernel<HALF, TILE, G>),
-                     dim3(tiles(dx) * sx.splits + tiles(dw) * sw.splits + sum_groups(dx.sums)), dim3(256), 0, st, dx,
-                     sx, dw, sw);
+                     dim3(tiles(dx) * sx.splits + tiles(dw) * sw.splits + sum_groups(dx.sums)), dim3(TILE == 256 ? 512 : 256), 0,
+                     st, dx, sx, dw, sw);
   return hipGetLastError();
 }
 

@@ -120,6 +120,9 @@ hipError_t launch_gemm(const GemmArgs& g, const GemmPlan& p, void* ws, hipStream
 // Both gradients' products, planned together.  Where they are paired (run in one launch) their workspaces lie one
 // behind the other, dx's first, else in the same place.
 void plan_gradients(int rows, int cols, int inner, GemmPlan* dx, GemmPlan* dw);
+// Stages until n workgroups of `len` stages each and, started after them, m of l <= len are
+// done, where `room` run at once.
+int64_t pair_stages(int64_t n, int64_t len, int64_t m, int64_t l, int64_t room);
 hipError_t launch_gemm_pair(const GemmArgs& dx, const GemmPlan& px, const GemmArgs& dw, const GemmPlan& pw, void* ws,
                             hipStream_t st);
 hipError_t launch_column_sums(const float* part, float* out0, float* out1, int units, int H, hipStream_t st);

@@ -347,10 +347,7 @@ hipError_t launch_gemm(const GemmArgs& args, const GemmPlan& p, void* ws, hipStr
   return e != hipSuccess ? e : launch_join({g, s}, {}, st);
 }
 
-// Stages until n workgroups of `len` stages each and, started after them, m of l <= len are
-// done, where `room` run at once.
-static int64_t pair_stages(int64_t n, int64_t len, int64_t m, int64_t l) {
-  constexpr int64_t room = 2 * kCUs;
+int64_t pair_stages(int64_t n, int64_t len, int64_t m, int64_t l, int64_t room) {
   const int64_t rounds = n / room * len, late = n % room, soon = room - late;
   if (late == 0) return rounds + (m + room - 1) / room * l;
   // soon places take the m from the start on, the late ones from len on
@@ -386,8 +383,8 @@ void plan_gradients(int rows, int cols, int inner, GemmPlan* dx, GemmPlan* dw) {
   auto join = [&](int s, int m) { return s > 1 ? (double)s * m * inner * 8 / 4e6 : 0.; };
   auto cost = [&](int sx, int sw) {
     const int ax = ceil_div(lx, sx), aw = ceil_div(lw, sw);
-    const int64_t t = ax >= aw ? pair_stages((int64_t)tx * sx, ax, (int64_t)tw * sw, aw)
-                           : pair_stages((int64_t)tw * sw, aw, (int64_t)tx * sx, ax);
+    const int64_t t = ax >= aw ? pair_stages((int64_t)tx * sx, ax, (int64_t)tw * sw, aw, 2 * kCUs)
+                           : pair_stages((int64_t)tw * sw, aw, (int64_t)tx * sx, ax, 2 * kCUs);
     return t + join(sx, rows) + join(sw, cols) + (sx > 1 || sw > 1 ? 3. : 0.);
   };
   constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12};
