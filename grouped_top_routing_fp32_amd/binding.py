@@ -483,6 +483,9 @@ def beam_moe_residual_forward_fp8(dims: Dims, stream_in: torch.Tensor, step: int
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
+# a device tensor is there already: no look at whether CUDA has been set up, which takes 0.25 us
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
 
 class _On:
     """Where a call runs: the tensors' device made current, and the given stream, or that device's
@@ -495,7 +498,7 @@ class _On:
     def __enter__(self) -> int:
         dev, stream = self.dev, self.stream
         if stream is None:
-            if torch.cuda.current_device() != dev.index:
+            if _current_device() != dev.index:
                 self.ctx = torch.cuda.device(dev)
                 self.ctx.__enter__()
             return _raw_stream(dev.index)

@@ -312,7 +312,8 @@ int beam_moe_clip_grads(int32_t count, const void* const* grads, const int32_t* 
   if (!std::isfinite(scale) || !std::isfinite(max_norm) || max_norm < 0.f || !std::isfinite(eps) || !(eps > 0.f))
     return BEAM_MOE_ERR_INVALID_ARG;
   if (out_types && !outs) return BEAM_MOE_ERR_INVALID_ARG;
-  if ((rc = check_optional({norm_in, norm})) != BEAM_MOE_OK) return rc;
+  if ((rc = check_optional({norm})) != BEAM_MOE_OK) return rc;
+  if (reinterpret_cast<uintptr_t>(norm_in) % sizeof(float) != 0) return BEAM_MOE_ERR_INVALID_ARG;
   if (!ws || !aligned16(ws) || ws_bytes < beam_moe_grad_norm_workspace_bytes(count)) return BEAM_MOE_ERR_WORKSPACE;
   try {
     std::vector<beam::GradTensor> t;

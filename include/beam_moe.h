@@ -526,8 +526,8 @@ int beam_moe_grad_norm(int32_t count, const void* const* grads, const int32_t* t
  * The factor is rounded to FP32, the product to out's type.  The arguments of beam_moe_grad_norm, and
  *   max_norm   finite, >= 0
  *   eps        finite, > 0
- *   norm_in    one fp32 on the device to take as the norm (of gradients that are spread over
- *              processes, say), NULL = the norm of `grads` as beam_moe_grad_norm gives it
+ *   norm_in    one fp32 on the device, aligned to 4 bytes, to take as the norm (of gradients that are
+ *              spread over processes, say), NULL = the norm of `grads` as beam_moe_grad_norm gives it
  *   outs       [count] device pointers (host array), aligned to their element, NULL = in place; outs[i] may be
  *              grads[i] with the same type, and lies apart from every other gradient and output
  *   out_types  [count] element types of outs (host), NULL = the gradients' own

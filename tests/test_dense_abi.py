@@ -48,7 +48,7 @@ MX_BOTH = Call("beam_moe_linear_mxfp4", **{**MX_LINEAR.defaults, "x_type": MX, "
 
 
 @pytest.mark.parametrize("call, required, optional", [
-    (NORM, ("norm",), ()), (CLIP, (), ("norm", "norm_in")), (QUANT, ("x", "codes", "scales"), ()),
+    (NORM, ("norm",), ()), (CLIP, (), ("norm",)), (QUANT, ("x", "codes", "scales"), ()),
     (DEQUANT, ("codes", "scales", "y"), ()),
     (MX_LINEAR, ("x", "w", "w_scales", "y"), ("bias", "res")),
     (MX_BOTH, ("x", "x_scales", "w", "w_scales", "y"), ("bias", "res")),
@@ -70,7 +70,7 @@ def test_pointers(call, required, optional):
         dict(grads=ptrs(ctypes.c_void_p(A[0].value + 1), A[1])), dict(grads=ptrs(A[0], ctypes.c_void_p(A[1].value + 2))))
 ] + [
     (CLIP, dict(max_norm=-1.0)), (CLIP, dict(max_norm=float("inf"))), (CLIP, dict(max_norm=float("nan"))),
-    (CLIP, dict(eps=0.0)), (CLIP, dict(eps=-1e-6)), (CLIP, dict(eps=float("nan"))), (CLIP, dict(outs=None)),
+    (CLIP, dict(norm_in=ctypes.c_void_p((1 << 20) + 2))), (CLIP, dict(eps=0.0)), (CLIP, dict(eps=-1e-6)), (CLIP, dict(eps=float("nan"))), (CLIP, dict(outs=None)),
     (CLIP, dict(out_types=ints(F32, 9))), (CLIP, dict(outs=ptrs(A[2], None))),
     (CLIP, dict(outs=ptrs(ctypes.c_void_p(A[2].value + 2), A[3]))),
     # outputs that overlap each other, another gradient, or their own of another type

@@ -162,7 +162,7 @@ def test_clip_grads_partly_in_place():
 def test_clip_grads_by_a_given_norm():
     _say("clip given norm")
     grads = _grads(4, [5000, 70], (F32, BF16))
-    norm = torch.full((), 123.5, device=DEV)
+    norm = torch.full((3,), 123.5, device=DEV)[1]
     out = [torch.empty_like(t) for t in grads]
     assert fw.beam_moe_clip_grads(grads, 2.0, scale=0.5, norm=norm, out=out) is norm
     _clip_check(out, grads, _factor(grads, 2.0, 0.5, norm=123.5))
@@ -514,7 +514,8 @@ def _gated_back_check(dh, x, wg, wu, zg, zu, act, out):
         _near(dbu, du.sum(0), (dep * du.abs() + near * (g.abs() + 1)).sum(0), "dbias_up")
 
 
-LARGE_BACK = [(1000, 520, 2048), (3300, 1700, 136), (3300, 100, 3336), (200, 1650, 3336), (4096, 1024, 1280)]
+LARGE_BACK = [(1000, 520, 2048), (3300, 1700, 136), (3300, 100, 3336), (200, 1650, 3336), (4096, 1024, 1280),
+              (5150, 1029, 5169)]
 
 
 @pytest.mark.parametrize("M,N,K", GATED_SHAPES + LARGE_BACK)
