@@ -20,9 +20,9 @@ ARCH = "gfx950"
 
 SOURCES = ["route.hip", "dispatch.hip", "experts.hip", "grouped_gemm.hip", "residual.hip", "layer_norm.hip",
            "balance.hip", "linear.hip", "gemm_bf16.hip", "gemm_f16.hip", "gated.hip", "gated_bf16.hip",
-           "gated_f16.hip", "grads.hip", "mxfp4.hip", "mx_linear.hip", "mx_tiles.hip", "mx_stream.hip",
-           "mx_stream_bf16.hip", "mx_stream_f16.hip", "mx_stream_f32.hip", "abi.cpp", "ops_abi.cpp",
-           "dense_abi.cpp"]
+           "gated_f16.hip", "gated_stream_bf16.hip", "gated_stream_f16.hip", "grads.hip", "mxfp4.hip",
+           "mx_linear.hip", "mx_tiles.hip", "mx_stream.hip", "mx_stream_bf16.hip", "mx_stream_f16.hip",
+           "mx_stream_f32.hip", "abi.cpp", "ops_abi.cpp", "dense_abi.cpp"]
 
 # Packed FP32 instructions (v_pk_*_f32) are kept out of every kernel.
 DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]

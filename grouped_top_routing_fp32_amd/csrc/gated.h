@@ -10,6 +10,7 @@ __host__ __device__ inline int gated_half(int N) { return (N + 63) / 64 * 64; }
 
 struct GatedPlan {
   GemmPlan gemm;
+  bool stream;                      // the persistent kernel's 256-row tiles
   bool copy_x, copy_gate, copy_up;  // laid out anew in the workspace, in this order
   size_t off_gate, off_up, off_gemm, total;
 };

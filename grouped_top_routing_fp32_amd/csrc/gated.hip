@@ -284,6 +284,7 @@ GatedPlan plan_gated(int M, int N, int K, int64_t ldx, int64_t ldg, int64_t ldu)
     p.copy_x = p.copy_gate = p.copy_up = false;
     p.gemm.regs = true;
   }
+  p.stream = p.gemm.tile == 256 && K % 64 == 0 && std::max({ldx, ldg, ldu}) < int64_t(1) << 22;
   p.off_gate = p.copy_x ? up256(padded_bytes(M, K)) : 0;
   p.off_up = p.off_gate + (p.copy_gate ? up256(padded_bytes(N, K)) : 0);
   p.off_gemm = p.off_up + (p.copy_up ? up256(padded_bytes(N, K)) : 0);
@@ -313,6 +314,10 @@ hipError_t launch_gated(const GatedArgs& args, const GatedPlan& p, void* ws, hip
     hipLaunchKernelGGL(g.type == kElemF16 ? gated_skinny_kernel<true> : gated_skinny_kernel<false>,
                        dim3(ceil_div(g.N, cols)), dim3(64 * kSkinnyWaves), 0, st, g, cols);
     return hipGetLastError();
+  }
+  if (p.stream) {
+    const int mt = ceil_div(g.M, 256), nt = ceil_div(g.N, 128), grid = std::min((mt * nt + 7) / 8 * 8, kCUs);
+    return g.type == kElemF16 ? launch_gated_stream_f16(g, grid, mt, nt, st) : launch_gated_stream_bf16(g, grid, mt, nt, st);
   }
   g.regs = p.gemm.regs;
   const GemmSplit s = split_of(p.gemm, 2 * ((g.N + 3) / 4 * 4), base + p.off_gemm);

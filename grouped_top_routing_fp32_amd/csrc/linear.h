@@ -159,6 +159,9 @@ size_t mx_stream_bytes(int M, int N, int K);
 hipError_t launch_mx_stream(const MxArgs& g, void* ws, hipStream_t st);
 hipError_t launch_gated_bf16(const GatedArgs& g, const GemmSplit& s, int tile, hipStream_t st);
 hipError_t launch_gated_f16(const GatedArgs& g, const GemmSplit& s, int tile, hipStream_t st);
+// A gated layer's forward product in 256-row tiles: K whole stages of 64, strides below 2^22.
+hipError_t launch_gated_stream_bf16(const GatedArgs& g, int grid, int mt, int nt, hipStream_t st);
+hipError_t launch_gated_stream_f16(const GatedArgs& g, int grid, int mt, int nt, hipStream_t st);
 hipError_t launch_gated_pair_bf16(const GatedArgs& dx, const GemmSplit& sx, const GatedArgs& dw, const GemmSplit& sw,
                                   int tile, hipStream_t st);
 hipError_t launch_gated_pair_f16(const GatedArgs& dx, const GemmSplit& sx, const GatedArgs& dw, const GemmSplit& sw,

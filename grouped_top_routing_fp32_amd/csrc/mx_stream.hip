@@ -1,7 +1,7 @@
 // The large product of two operands in microscaled 4 bits (gfx950): the scales' order and the launch.
 #include <algorithm>
 
-#include "mx_stream.h"
+#include "stream.h"
 
 namespace beam {
 namespace {
@@ -21,14 +21,14 @@ __global__ __launch_bounds__(256) void mx_scales_kernel(ScaleJob first, ScaleJob
   const int stages = (blocks + 7) / 8, t = (blockIdx.x - (other ? groups : 0)) * 256 + threadIdx.x;
   if (t >= j.threads) return;
   const int l = t & 15, quarter = (t >> 4) & 3, at = t >> 6, stage = at % stages, tile = at / stages;
-  using Stage = ScaleStage<kMxT>;
+  using Stage = ScaleStage<kT>;
   uint64_t v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int r = min(tile * kMxT + quarter * 64 + 16 * i + l, j.rows - 1);
+    const int r = min(tile * kT + quarter * 64 + 16 * i + l, j.rows - 1);
     v[i] = Stage::load(j.from + r * j.ld, 8 * stage, blocks);
   }
-  uint8_t* to = j.to + (int64_t)at * (kMxScales / 2) + quarter * 512 + l * 8;
+  uint8_t* to = j.to + (int64_t)at * (kScales / 2) + quarter * 512 + l * 8;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (blocks >= 8) v[i] >>= 8 * max(8 * stage + 8 - blocks, 0);
@@ -43,7 +43,7 @@ __global__ __launch_bounds__(256) void mx_scales_kernel(ScaleJob first, ScaleJob
   }
 }
 
-int tiles_of(int n) { return (n + kMxT - 1) / kMxT; }
+int tiles_of(int n) { return (n + kT - 1) / kT; }
 
 }  // namespace
 
@@ -52,14 +52,14 @@ hipError_t launch_mx_stream_f16(const MxArgs& g, int mt, int nt, int grid, hipSt
 hipError_t launch_mx_stream_f32(const MxArgs& g, int mt, int nt, int grid, hipStream_t st);
 
 size_t mx_stream_bytes(int M, int N, int K) {
-  return (size_t)(tiles_of(M) + tiles_of(N)) * ((K + 63) / 64) * (kMxScales / 2);
+  return (size_t)(tiles_of(M) + tiles_of(N)) * ((K + 63) / 64) * (kScales / 2);
 }
 
 hipError_t launch_mx_stream(const MxArgs& args, void* ws, hipStream_t st) {
   MxArgs g = args;
   const int mt = tiles_of(g.M), nt = tiles_of(g.N), blocks = g.K / 8, stages = (blocks + 7) / 8;
   uint8_t* a = static_cast<uint8_t*>(ws);
-  uint8_t* b = a + (int64_t)mt * stages * (kMxScales / 2);
+  uint8_t* b = a + (int64_t)mt * stages * (kScales / 2);
   const ScaleJob ja{g.sa, g.ldsa, g.M, a, mt * stages * 64}, jb{g.sb, g.ldsb, g.N, b, nt * stages * 64};
   const int ga = (ja.threads + 255) / 256, gb = (jb.threads + 255) / 256;
   hipLaunchKernelGGL(mx_scales_kernel, dim3(ga + gb), dim3(256), 0, st, ja, jb, ga, blocks);

@@ -440,6 +440,24 @@ def test_gated_linear(M, N, K, dt):
         assert torch.equal(fw.beam_moe_gated_linear(x, wg, wu, bg, bu, act=act, out_dtype=yt), h)
 
 
+# 256-row tiles with K of whole stages: whole tiles, rows and columns that end inside a tile or a chunk of eight, one tile
+# to a workgroup and several
+@pytest.mark.parametrize("M,N,K", [(4096, 2048, 640), (4000, 2043, 192), (3900, 2040, 320), (8100, 2036, 192),
+                                   (16384, 1024, 256)])
+@pytest.mark.parametrize("dt", [BF16, F16])
+def test_gated_linear_large(M, N, K, dt):
+    for act, yt, bias, pre, pad in (("silu", dt, False, False, 0), ("gelu", F32, True, True, 8),
+                                    ("relu", dt, True, False, 3), ("silu", dt, False, True, 0),
+                                    ("none", F32, False, False, 0)):
+        _say("gated large", M, N, K, dt, act, yt, bias, pre, pad)
+        _, x, wg, wu, bg, bu = _gated_inputs(M, N, K, dt, pad, bias)
+        buf = torch.full((M, N + 8), 7.0, dtype=yt, device=DEV)
+        out = fw.beam_moe_gated_linear(x, wg, wu, bg, bu, act=act, out=buf[:, :N], want_pre=pre)
+        h, zg, zu = out if pre else (out, None, None)
+        _gated_check(x, wg, wu, bg, bu, act, h, zg, zu)
+        assert (buf[:, N:] == 7.0).all()
+
+
 @pytest.mark.parametrize("M,N,K", [(100, 50, 65536), (300, 150, 16384), (512, 256, 9216), (20, 100, 2050)])
 @pytest.mark.parametrize("dt", [BF16, F16])
 def test_gated_linear_long_k(M, N, K, dt):
