@@ -318,13 +318,13 @@ hipError_t launch_clip_grads(GradTensor* t, int count, const ClipArgs& a, void* 
       return launch_alone(l, a, true, in_place ? 1 : std::max(1, (int)(l.chunks + kAloneWaves - 1) / kAloneWaves), st);
   }
   if (!a.norm_in && (e = launch_squares(l, st)) != hipSuccess) return e;
-  if (l.chunks == 0) return hipSuccess;  // nothing to scale by a given norm
+  if (l.chunks == 0 && !a.norm) return hipSuccess;  // nothing to scale by a given norm, nor to write
+  const dim3 grid(std::max(l.units, 1));
   if (l.laid)
-    hipLaunchKernelGGL(clip_grads_kernel<Laid>, dim3(l.units), dim3(256), 0, st, Laid{l.laid}, l.count, l.chunks, a,
-                       l.part, l.units);
-  else
-    hipLaunchKernelGGL(clip_grads_kernel<Inline>, dim3(l.units), dim3(256), 0, st, l.all, l.count, l.chunks, a, l.part,
+    hipLaunchKernelGGL(clip_grads_kernel<Laid>, grid, dim3(256), 0, st, Laid{l.laid}, l.count, l.chunks, a, l.part,
                        l.units);
+  else
+    hipLaunchKernelGGL(clip_grads_kernel<Inline>, grid, dim3(256), 0, st, l.all, l.count, l.chunks, a, l.part, l.units);
   return hipGetLastError();
 }
 

@@ -6,6 +6,7 @@ d u times the sum of magnitudes, and a result stored in type t by at most half a
 (plus half the least subnormal of fp16).
 """
 import math
+from array import array
 
 import pytest
 import torch
@@ -202,6 +203,23 @@ def test_clip_grads_of_nothing():
     assert fw.beam_moe_grad_norm(empty).item() == 0 and fw.beam_moe_clip_grads(empty, 1.0).item() == 0
     zeros = [torch.zeros(100, device=DEV)]
     assert fw.beam_moe_clip_grads(zeros, 0.0).item() == 0 and (zeros[0] == 0).all()
+
+
+@pytest.mark.parametrize("size", [None, 0, 9])
+def test_a_given_norm_is_written_whatever_the_list(size):
+    """The C entry point hands a given norm on, also where the list holds no element."""
+    _say("clip norm handed on", size)
+    lib = fw.load_library()
+    grads = [] if size is None else [torch.ones(size, device=DEV)]
+    at, types, sizes = (array(c, v) for c, v in (("Q", [t.data_ptr() for t in grads]), ("i", [fw.BEAM_MOE_F32] * len(grads)),
+                                                 ("q", [t.numel() for t in grads])))
+    given, norm = torch.full((1,), 8.0, device=DEV), torch.full((4,), NAN, device=DEV)
+    ws = torch.empty(lib.beam_moe_grad_norm_workspace_bytes(len(grads)), dtype=torch.uint8, device=DEV)
+    status = lib.beam_moe_clip_grads(len(grads), at.buffer_info()[0], types.buffer_info()[0], sizes.buffer_info()[0], 1.0,
+                                     4.0, 2.0 ** -40, given.data_ptr(), None, None, norm.data_ptr(), ws.data_ptr(),
+                                     ws.numel(), torch.cuda.current_stream().cuda_stream)
+    assert status == 0 and norm[0].item() == 8.0 and norm[1:].isnan().all()
+    assert all((t == 0.5).all() for t in grads)
 
 
 def test_clip_grads_of_one_tensor_past_32_bits():
