@@ -2,7 +2,8 @@
 counting-sort dispatch, grouped bf16 SwiGLU expert GEMMs and a deterministic
 combine, behind the C-ABI library ``libbeam_moe.so``; and the operators a
 training step or a dense sublayer needs beside it (layer norm, the router's
-balance loss and gradient, linear with bias, activation and residual).
+balance loss and gradient, linear with bias, activation and residual; gated
+projections, gradient clipping and microscaled 4-bit floating point).
 
 The binding is loaded lazily: ``from grouped_top_routing_fp32_amd import
 binding`` (or any of the ``beam_moe_*`` names below) loads the built library

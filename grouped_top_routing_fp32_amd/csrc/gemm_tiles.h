@@ -133,8 +133,8 @@ struct Side {
   }
 };
 
-// The scales of a stage of 4-bit operands: 8 blocks (256 codes, 128 bytes as kBK 16-bit elements are) of R rows.  The byte of
-// block 4 s + g of row r lies at (r / 64, g, r % 16, s, r / 16 % 4), so that a lane (row l % 16, block
+// The scales of a stage of 4-bit operands: 8 blocks (256 codes, 128 bytes as kBK 16-bit elements are) of R rows.
+// The byte of block 4 s + g of row r lies at (r / 64, g, r % 16, s, r / 16 % 4), so that a lane (row l % 16, block
 // l / 16 of each four) has those of 64 rows in 8 bytes, and the matrix instruction picks a byte of a word.
 template <int R>
 struct ScaleStage {
@@ -159,7 +159,8 @@ struct ScaleStage {
   }
   // The words (s = 0, 1) of rows r0 .. r0 + 63, or the upper half of them moved down where r0 is off 64 by 32.
   static __device__ __forceinline__ u32x2 words(const lds_u8* stage, int r0, int lane) {
-    u32x2 v = *(const __attribute__((address_space(3))) u32x2*)(stage + (r0 >> 6) * 512 + (lane >> 4) * 128 + (lane & 15) * 8);
+    const lds_u8* p = stage + (r0 >> 6) * 512 + (lane >> 4) * 128 + (lane & 15) * 8;
+    u32x2 v = *(const __attribute__((address_space(3))) u32x2*)p;
     const int down = r0 & 32 ? 16 : 0;
     v[0] >>= down;
     v[1] >>= down;
@@ -642,8 +643,8 @@ template <bool HALF, int TILE, class G>
 hipError_t launch_gemm_pair(const G& dx, const GemmSplit& sx, const G& dw, const GemmSplit& sw, hipStream_t st) {
   auto tiles = [](const GemmArgs& g) { return ((g.M + TILE - 1) / TILE) * ((g.N + TILE - 1) / TILE); };
   hipLaunchKernelGGL((gemm_pair_kernel<HALF, TILE, G>),
-                     dim3(tiles(dx) * sx.splits + tiles(dw) * sw.splits + sum_groups(dx.sums)), dim3(TILE == 256 ? 512 : 256), 0,
-                     st, dx, sx, dw, sw);
+                     dim3(tiles(dx) * sx.splits + tiles(dw) * sw.splits + sum_groups(dx.sums)),
+                     dim3(TILE == 256 ? 512 : 256), 0, st, dx, sx, dw, sw);
   return hipGetLastError();
 }
 

@@ -4,6 +4,7 @@
 //
 // Bound by HBM.  A lane takes 8 elements, 16 bytes of a 16-bit type, and four lanes a block: the largest
 // magnitude is found among their bits in two DPP moves, and the codes leave as 4 bytes a lane, both in whole lines.
+// [16384, 5120] bf16: to codes 47 to 51 us (212 MB, 4.2 to 4.5 TB/s), back 32 (codes out of the Infinity Cache).
 #include "mxfp4.h"
 
 namespace beam {
