@@ -73,7 +73,7 @@ struct MxArgs : GemmArgs {
 };
 
 // The product of 16-bit rows with weights in microscaled 4 bits: b are the codes, ldb their row stride in bytes, and a
-// row has `blocks` of 32 codes and as many scales.  Operands go through registers.
+// row has `blocks` of 32 codes and as many scales.
 struct CodeArgs : GemmArgs {
   const uint8_t* sb;
   int64_t ldsb;
@@ -150,6 +150,8 @@ inline size_t padded_bytes(int rows, int cols) { return (size_t)rows * up8(cols)
 hipError_t launch_pad(const PadJob& first, const PadJob& second, const PadJob& third, hipStream_t st);
 hipError_t launch_gemm_bf16(const GemmArgs& g, const GemmSplit& s, int tile, hipStream_t st);
 hipError_t launch_gemm_f16(const GemmArgs& g, const GemmSplit& s, int tile, hipStream_t st);
+// In tiles of 64 or 32 rows and 128 columns, K split by 128; rows of a are whole chunks.
+hipError_t launch_code_rows(const CodeArgs& g, const GemmSplit& s, int rows, hipStream_t st);
 // In tiles of 128 or 64.
 hipError_t launch_code_tiles(const CodeArgs& g, const GemmSplit& s, int tile, hipStream_t st);
 // The same; `half`: a result of 16 bits is fp16, not bf16.

@@ -3,13 +3,14 @@
 //
 //   y = keep res + add act(x w^T + bias)
 //
-// Few rows are bound by reading w, a quarter of its 16-bit bytes: one kernel takes codes and scales straight from
-// memory ([1, 5120] x [2560, 5120], 7 MB, 6.5 us, of which some 5 are a launch and one trip to memory).
+// Few rows are bound by reading w, a quarter of its 16-bit bytes: one kernel takes codes and scales straight from memory
+// to registers ([1, 5120] x [2560, 5120], 7 MB, 6.5 us, of which some 5 are a launch and one trip to memory).
 // With both operands in 4 bits the products run on scaled matrix instructions, four times the 16-bit rate for the
 // same bytes in LDS: small ones in the tiled product, large ones in a persistent kernel ([16384, 2560] x [5120,
-// 2560] 149 us, 2.9 PFLOP/s).  With x of 16 bits, products of few tiles turn codes into x's type on their way into
-// LDS ([64, 2560] x [5120, 2560] 11.1 us and 5.0 for the join of the splits; 23.9 with w laid out first); larger ones
-// lay w out as x's type in the workspace first and run the plain product.
+// 2560] 149 us, 2.9 PFLOP/s).  With x of 16 bits, some rows go through tiles that hold codes in LDS and turn them into
+// x's type on their way to the matrix instructions ([64, 2560] x [5120, 2560] 9.8 us and 4.0 for the join of its splits;
+// [64, 5120] x [32768, 5120] 39 us, 2.4 TB/s of codes).  Where rows are no whole chunks, products of few tiles do so on
+// the codes' way into LDS; larger ones lay w out as x's type in the workspace first and run the plain product.
 #include <algorithm>
 #include <cmath>
 
@@ -18,7 +19,10 @@
 namespace beam {
 namespace {
 
-int ceil_div(int a, int b) { return (a + b - 1) / b; }
+template <class A>
+A ceil_div(A a, int b) {
+  return (a + b - 1) / b;
+}
 constexpr int kCUs = 256;
 
 // Few rows (M <= 16).  A workgroup takes `cols` <= 16 columns and its 16 waves share K in pieces of 128: a lane
@@ -98,10 +102,42 @@ GemmPlan plan_mx_tiles(int M, int N, int units, bool wide_rows) {
   return p;
 }
 
+// 16-bit rows in tiles of 64 rows, 32 where there are no more, and 128 columns (launch_code_rows): a workgroup to a CU,
+// rounds of them of 4 us and some 0.75 (0.6 of 32 rows) for each stage of 128 of K, 26 KB (18) at what a CU gets from
+// its L2.  K is split where that saves more than the launch that joins the sums, 4.5 us.  Taken where this estimate is
+// below the other form's:
+// - up to 16 rows the kernel for few, which reads w evenly, 15 bytes a nanosecond and CU, but x once for each 16
+//   columns of a CU ([16, 5120] x [10240, 5120] 22.6 us, 15.8 here; [8, 5120] x [5120, 5120] 11.6 and 12.6; [1, 5120] x
+//   [32768, 5120] 29 both)
+// - above, w turned into 16 bits, in its tiles or in memory, and the product at 1.15 PFLOP/s ([256, 2560] x [5120, 2560]
+//   27.5 us, 18.9 here; [512, 5120] x [2560, 5120] 31 and 33.6; [64, 5120] x [32768, 5120] 161 and 39)
+bool plan_mx_rows(MxPlan* p, int M, int N, int K) {
+  const int rows = M <= 32 ? 32 : 64, stages = ceil_div(K, 128);
+  const int64_t tiles = (int64_t)ceil_div(M, rows) * ceil_div(N, 128);
+  if (tiles > 1 << 20) return false;
+  const double stage = rows == 32 ? 0.6 : 0.75, weights = (double)N * K;
+  int s = tiles <= kCUs ? std::max(1, std::min({kCUs / (int)tiles, stages / 4, 16})) : 1;
+  if ((stages - ceil_div(stages, s)) * stage < 4.5) s = 1;
+  const int per = ceil_div(stages, s);
+  const double here = (double)ceil_div(tiles * s, kCUs) * (4. + stage * per) + (s > 1 ? 5.5 : 1.);
+  const double rounds = ceil_div(N, 16 * kCUs);
+  const double few = 4. + weights * 0.53 / kCUs / 15e3 + rounds * (0.5 + M * (double)K * 2 / 42e3);
+  const double other = 10. + weights * 2.53 / 4.5e6 + weights * M * 2 / 1.15e9;
+  if (here >= (M <= kSkinnyRows ? few : other)) return false;
+  p->rows = rows;
+  p->gemm.kind = GemmPlan::kTiles;
+  p->gemm.k_per_split = per * 128;
+  p->gemm.splits = ceil_div(K, p->gemm.k_per_split);
+  p->gemm.total = p->gemm.splits > 1 ? up256((size_t)p->gemm.splits * M * ((N + 3) / 4 * 4) * sizeof(float)) : 0;
+  p->total = p->gemm.total;
+  return true;
+}
+
 }  // namespace
 
 MxPlan plan_mx(int M, int N, int K, bool four, int64_t ldx, int64_t ldw) {
   MxPlan p{};
+  if (!four && regular_rows(ldx, K) && plan_mx_rows(&p, M, N, K)) return p;
   if (M <= kSkinnyRows) return p;
   const int blocks = (int)mx_blocks(K);
   if (four) {
@@ -149,14 +185,14 @@ hipError_t launch_linear_mx(const MxLinear& a, const MxPlan& p, void* ws, hipStr
     e = launch_mx_tiles(g, s, p.gemm.tile, half, st);
     return e != hipSuccess ? e : launch_join_one(g, s, st);
   }
-  if (p.fused) {
+  if (p.fused || p.rows) {
     CodeArgs g{a.g, a.w_scales, a.ldws, blocks};
     g.a = a.x;
     g.lda = a.ldx;
     g.b = a.w;
     g.ldb = a.ldw;
     const GemmSplit s = split_of(p.gemm, g.N, base);
-    e = launch_code_tiles(g, s, p.gemm.tile, st);
+    e = p.rows ? launch_code_rows(g, s, p.rows, st) : launch_code_tiles(g, s, p.gemm.tile, st);
     return e != hipSuccess ? e : launch_join_one(g, s, st);
   }
   GemmArgs g = a.g;

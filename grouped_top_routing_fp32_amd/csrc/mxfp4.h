@@ -41,6 +41,7 @@ struct MxLinear {
 };
 struct MxPlan {
   GemmPlan gemm;
+  int rows;                  // of launch_code_rows' tiles; 0: not those
   bool fused;                // codes become x's type on their way into LDS; else:
   bool copy_x;               // x is laid out anew in the workspace, and w as x's type behind it
   size_t off_w, off_gemm, total;

@@ -821,6 +821,34 @@ def test_linear_mxfp4(M, N, K, dt):
         _mx_linear_check(x.double(), _mx_values(w, K), bias, act, r, keep, add, y)
 
 
+# one and two row fragments to a wave; parts of K of one stage of 128 up to more than LDS holds, whole and ragged ones
+MX_ROWS = [(17, 129, 4104), (32, 2000, 2048), (24, 40, 16392), (33, 132, 776), (64, 5120, 2560), (100, 1030, 4104),
+           (257, 640, 1160), (384, 2560, 5120), (48, 8192, 1536), (256, 5120, 2560), (63, 126, 128), (1000, 1000, 904),
+           (16, 16384, 2048), (16, 40000, 520), (40, 40000, 1000)]
+
+
+@pytest.mark.parametrize("M,N,K", MX_ROWS)
+@pytest.mark.parametrize("dt", [BF16, F16])
+def test_linear_mxfp4_of_some_rows(M, N, K, dt):
+    """x in 16 bits, rows of whole chunks: padding around every operand, then scales of NaN at both ends of K."""
+    _say("linear_mxfp4 rows", M, N, K, dt)
+    g = _gen(M + N + K)
+    x, w, bias = _randn(g, (M, K), dt, 1.0, 8), _mx_weights(g, N, K, 1), _randn(g, (N,))
+    for act, yt, res in (("none", F32, True), ("gelu", dt, False)):
+        buf = torch.full((M, N + 5), 7.0, device=DEV, dtype=yt)
+        r = _randn(g, (M, N), yt, 1.0, 3) if res else None
+        fw.beam_moe_linear_mxfp4(x, w, bias, act=act, residual=r, keep=0.5, add=0.75, out=buf[:, :N])
+        _mx_linear_check(x.double(), _mx_values(w, K), bias, act, r, 0.5, 0.75, buf[:, :N])
+        assert (buf[:, N:] == 7.0).all()
+    want = fw.beam_moe_linear_mxfp4(x, w)
+    assert torch.equal(want, fw.beam_moe_linear_mxfp4(x, w))
+    w.scales[N // 2, 0] = w.scales[N - 1, -1] = 255
+    got = fw.beam_moe_linear_mxfp4(x, w)
+    bad = torch.zeros(N, dtype=torch.bool, device=DEV)
+    bad[[N // 2, N - 1]] = True
+    assert torch.equal(got[:, ~bad], want[:, ~bad]) and got[:, bad].isnan().all()
+
+
 @pytest.mark.parametrize("M,N,K", MX_LINEAR)
 def test_linear_mxfp4_of_two(M, N, K):
     """Both operands in 4 bits."""
