@@ -114,7 +114,7 @@ GemmPlan plan_mx_tiles(int M, int N, int units, bool wide_rows) {
 bool plan_mx_rows(MxPlan* p, int M, int N, int K) {
   const int rows = M <= 32 ? 32 : 64, stages = ceil_div(K, 128);
   const int64_t tiles = (int64_t)ceil_div(M, rows) * ceil_div(N, 128);
-  if (tiles > 1 << 20) return false;
+  if (tiles < 1 || tiles > 1 << 20) return false;
   const double stage = rows == 32 ? 0.6 : 0.75, weights = (double)N * K;
   int s = tiles <= kCUs ? std::max(1, std::min({kCUs / (int)tiles, stages / 4, 16})) : 1;
   if ((stages - ceil_div(stages, s)) * stage < 4.5) s = 1;

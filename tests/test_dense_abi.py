@@ -188,3 +188,16 @@ def test_binding_refuses_what_is_not_on_the_device():
         binding.beam_moe_quantize_mxfp4(torch.zeros(3, 4))
     with pytest.raises(ValueError):
         binding.beam_moe_dequantize_mxfp4((torch.zeros(3, 16, dtype=torch.uint8), torch.zeros(3, 1, dtype=torch.uint8)))
+
+
+@pytest.mark.parametrize("rows", [0, 1, 16, 17, 1 << 20])
+@pytest.mark.parametrize("cols, inner", [(1, 1), (1, 1 << 18), (1 << 18, 8), (1 << 18, 1 << 18)])
+def test_workspaces_at_the_ends_of_the_sizes(rows, cols, inner):
+    """A size query answers for every size the header allows, no rows among them."""
+    lib = binding.load_library()
+    blocks = (inner + 31) // 32
+    for x_type, ldx in ((BF16, inner), (F16, inner + 1), (MX, 16 * blocks)):
+        assert lib.beam_moe_linear_mxfp4_workspace_bytes(rows, cols, inner, x_type, ldx, 16 * blocks) < 1 << 50
+    cols = min(cols, 1 << 17)
+    for query in (lib.beam_moe_gated_linear_workspace_bytes, lib.beam_moe_gated_linear_backward_workspace_bytes):
+        assert query(rows, cols, inner, inner, inner, inner) < 1 << 50
