@@ -619,7 +619,7 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(G g, int mt, int nt, 
 
 // dx = dz w and dw = dz^T x in one launch, where neither fills the card alone.  Those
 // with the longer K come first.  (In 256-row tiles nothing is gained: 429 us either way at [8192,
-// 5120] x [2560, 5120], 640 and 200 tiles, although fewer CUs idle.)
+// 5120] x [2560, 5120], 640 and 200 tiles, although fewer CUs idle; a gated layer's 640 and 400 do gain.)
 template <bool HALF, int TILE, class G>
 __global__ __launch_bounds__(TILE == 256 ? 512 : 256) void gemm_pair_kernel(G dx, GemmSplit sx, G dw, GemmSplit sw) {
   constexpr int WM = TILE == 256 ? 4 : 2;
