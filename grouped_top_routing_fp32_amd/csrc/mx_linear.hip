@@ -9,8 +9,9 @@
 // same bytes in LDS: small ones in the tiled product, large ones in a persistent kernel ([16384, 2560] x [5120,
 // 2560] 149 us, 2.9 PFLOP/s).  With x of 16 bits, some rows go through tiles that hold codes in LDS and turn them into
 // x's type on their way to the matrix instructions ([64, 2560] x [5120, 2560] 9.8 us and 4.0 for the join of its splits;
-// [64, 5120] x [32768, 5120] 39 us, 2.3 TB/s of codes and scales).  Where rows are no whole chunks, products of few tiles do so on
-// the codes' way into LDS; larger ones lay w out as x's type in the workspace first and run the plain product.
+// [64, 5120] x [32768, 5120] 39 us, 2.3 TB/s of codes and scales).  Where rows are no whole chunks, products of few
+// tiles do so on the codes' way into LDS; larger ones lay w out as x's type in the workspace first and run the plain
+// product.
 #include <algorithm>
 #include <cmath>
 
