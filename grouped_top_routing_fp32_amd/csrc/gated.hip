@@ -148,13 +148,25 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void gated_skinny_kernel(GatedAr
   by_act(g.act, [&](auto act) { gated4<decltype(act)::value>(g, l16, n, n1, ag, au); });
 }
 
-// Eight elements of both gradients.
+// Eight elements of both gradients.  An infinite argument stands for one past the type's range: the activation at it
+// is its limit, and 0 times an infinite argument or activation is 0, as times the finite one.  Where d zu leaves FP32's
+// range the slope, which is small or 0 there, is taken first.  All of these come out infinite or NaN as the formulas stand,
+// and only then are looked at.
 template <int ACT>
 __device__ __forceinline__ void gated_slopes(const float* d, const float* zg, const float* zu, float* dg, float* du) {
+  float odd = 0.f;  // NaN if one is not finite
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
     dg[q] = d[q] * zu[q] * act_slope_f32<ACT>(zg[q]);
     du[q] = d[q] * act_f32<ACT>(zg[q]);
+    odd = fmaf(du[q], 0.f, fmaf(dg[q], 0.f, odd));
+  }
+  if (odd == 0.f) return;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const float p = d[q] * act_slope_f32<ACT>(zg[q]), a = act_limit_f32<ACT>(zg[q]);
+    if (!__builtin_isfinite(dg[q])) dg[q] = p == 0.f && __builtin_isinf(zu[q]) ? 0.f : p * zu[q];
+    du[q] = d[q] == 0.f && __builtin_isinf(a) ? 0.f : d[q] * a;
   }
 }
 

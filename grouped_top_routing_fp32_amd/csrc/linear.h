@@ -249,6 +249,19 @@ __device__ __forceinline__ float act_f32(float z) {
   return z;
 }
 
+// The same with the limit 0 at minus infinity, where SiLU's and GELU's factor z meets a 0: z is held from -128 on, where
+// that factor has been 0 for long (the same bits for every finite z).  NaN comes through sigmoid or distribution function.
+template <int ACT>
+__device__ __forceinline__ float act_limit_f32(float z) {
+  const float f = fmaxf(z, -128.f);
+  if constexpr (ACT == kActSilu) return f * sigmoid_f32(z);
+  if constexpr (ACT == kActGelu) {
+    float e;
+    return f * normal_cdf(z, e);
+  }
+  return act_f32<ACT>(z);
+}
+
 // d act / dz.  The factor z is held within +-128, where what it multiplies is 0 or takes the
 // rest to 0, so that an infinite z (a pre past fp16's range) has the slope's limit, 0 or 1, and
 // not 0 times infinity.  NaN comes through sigmoid or distribution function.

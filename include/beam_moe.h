@@ -489,6 +489,9 @@ int beam_moe_gated_linear(int32_t rows, int32_t cols, int32_t inner, int type, c
  *   dbias_gate = sum over rows of dzg,  dbias_up = sum over rows of dzu
  *   dh       [rows, cols] of dh_type: `type` or BEAM_MOE_F32
  *   pre_gate, pre_up   [rows, cols] of `type` as beam_moe_gated_linear wrote them
+ *            (where one is infinite, as zg or zu past 65504 is in fp16, act and act' are their limits there, and 0
+ *            times it or act of it is 0; what remains of it is infinite, as dzg is of an infinite zu past a gate that
+ *            lets something through)
  *   dx       [rows, inner] of `type`; NULL = not wanted
  *   dw_gate, dw_up       [cols, inner] of `type`, both or neither
  *   dbias_gate, dbias_up [cols] fp32, both or neither

@@ -618,6 +618,77 @@ def test_gated_backward_nan_and_infinite_gradients_in_fp16():
         assert torch.equal(got[cols], was[cols]) and not got[~cols].isfinite().any()
 
 
+@pytest.mark.parametrize("act", list(ACTS))
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("wide", [False, True], ids=["own", "f32"])
+def test_gated_gradients_at_infinite_pre(act, dt, wide):
+    """Every pair of a finite, infinite and NaN argument of either projection. An activation and its slope are their
+    limits at infinity, and 0 times an infinite argument or activation is 0, as times the finite one it stands for."""
+    _say("gated infinite pre", act, dt, wide)
+    vals = torch.tensor([-INF, INF, -200.0, 1.0, 0.0, NAN], dtype=torch.float64, device=DEV)
+    g, u = (t.reshape(-1) for t in torch.meshgrid(vals, vals, indexing="ij"))
+    N, K = g.numel(), 16
+    # at +-200 the forms are within e^-200 of their limits, 2^-280 with the factor 200: rounded to FP32, whose least is
+    # 2^-149, they are the limits. NaN stays
+    big = g.clamp(-200.0, 200.0)
+    a = torch.where(g == INF, g, ACTS[act](big).float().double()) if act != "none" else g
+    slope = torch.where(g.isnan(), torch.zeros_like(g), (g > 0).double()) if act == "relu" else _slope(big, act)
+    slope = slope.float().double()
+    times = lambda p, q: torch.where((p == 0) & q.isinf(), torch.zeros_like(q), p * q)  # noqa: E731
+    x, w = torch.ones(1, K, dtype=dt, device=DEV), torch.ones(N, K, dtype=dt, device=DEV)
+    for d in (1.0, -2.0, 0.0):
+        dh = torch.full((1, N), d, dtype=F32 if wide else dt, device=DEV)
+        zg, zu = g[None].to(dt), u[None].to(dt)
+        wg, wu = times(d * slope, u), times(torch.full_like(a, d), a)
+        dx, dwg, dwu, dbg, dbu = fw.beam_moe_gated_linear_backward(dh, x, w, w, zg, zu, act=act)
+        for got, want, steps in ((dbg, wg, 0), (dbu, wu, 0), (dwg[:, 3], wg, 2), (dwu[:, 3], wu, 2)):
+            assert torch.equal(got.isnan(), want.isnan()), (d, got, want)
+            assert torch.equal(got == INF, want == INF) and torch.equal(got == -INF, want == -INF), (d, got, want)
+            got, want = got[want.isfinite()], want[want.isfinite()]
+            _near(got, want, steps * _step(dx) * want.abs() + 32 * U * abs(d) * (1 + want.abs()))
+        # a row of dx holds what its columns do
+        fine = wg.isfinite() & wu.isfinite()
+        dx, _, _, _, _ = fw.beam_moe_gated_linear_backward(dh[:, fine], x, w[fine], w[fine], zg[:, fine], zu[:, fine],
+                                                           act=act)
+        terms = wg[fine].abs().sum() + wu[fine].abs().sum()
+        _near(dx, (wg[fine].sum() + wu[fine].sum()).expand(1, K), 2 * _step(dx) * terms + 64 * U * (abs(d) * 400 + terms))
+
+
+def test_gated_step_past_the_range_of_fp16():
+    """Arguments past 65504 are stored as infinities while h, in FP32, is finite: a gate far below zero lets no gradient
+    through, whatever stands beside it."""
+    _say("gated past fp16")
+    x, w = torch.zeros(3, 16, dtype=F16, device=DEV), torch.ones(8, 16, dtype=F16, device=DEV)
+    bg = torch.tensor([-7e4, -7e4, -7e4, -3e38, 2.0, 2.0, -7e4, 7e4], device=DEV)
+    bu = torch.tensor([1.0, 7e4, -7e4, 7e4, 0.5, -1.0, 0.0, 0.0], device=DEV)
+    for act in ("relu", "silu", "gelu"):
+        h, zg, zu = fw.beam_moe_gated_linear(x, w, w, bg, bu, act=act, out_dtype=F32, want_pre=True)
+        assert h.isfinite().all() and (h[:, :4] == 0).all() and zg[:, :4].isinf().all() and zu[:, 1:4].isinf().all()
+        for dh in (torch.ones(3, 8, device=DEV), torch.ones(3, 8, dtype=F16, device=DEV)):
+            dx, dwg, dwu, dbg, dbu = fw.beam_moe_gated_linear_backward(dh, x + 1, w, w, zg, zu, act=act)
+            for t in (dwg, dwu, dbg, dbu):
+                assert (t[:4] == 0).all() and t[4:7].isfinite().all()
+            for n in (4, 7):
+                dx, _, _, _, _ = fw.beam_moe_gated_linear_backward(dh[:, :n], x + 1, w[:n], w[:n], zg[:, :n], zu[:, :n],
+                                                                   act=act)
+                assert dx.isfinite().all() and (n > 4 or (dx == 0).all())
+
+
+def test_gated_gradients_whose_products_pass_fp32():
+    """dh times the up argument may leave FP32's range where the gate's slope takes it back."""
+    _say("gated products past fp32")
+    d = torch.tensor([[1e38, -1e38, 3e38, 1e38]], device=DEV)
+    zg = torch.tensor([[-30.0, -40.0, -1000.0, -INF]], dtype=BF16, device=DEV)
+    zu = torch.tensor([[1e3, 1e4, -1e6, 1e3]], dtype=BF16, device=DEV)
+    w, x = torch.full((4, 16), 1e-30, dtype=BF16, device=DEV), torch.ones(1, 16, dtype=BF16, device=DEV)
+    for act in ("relu", "silu"):
+        want = d.double() * zu.double() * _slope(zg.double().clamp_min(-1000.0), act)
+        out = fw.beam_moe_gated_linear_backward(d, x, w, w, zg, zu, act=act)
+        assert all(t.isfinite().all() for t in out)
+        # the exponent of e^-z is rounded at |z| half steps of FP32
+        _near(out[3][None], want, 64 * U * want.abs())
+
+
 def test_gated_gradient_against_differences():
     """Differences of the call itself in FP32 outputs: with loss L = sum(h r), (L(x + t v) - L(x - t v)) / 2t against
     dx . v and the like. x holds multiples of 2^-6 and t v too, so both arguments are exact in bf16. h is off by
