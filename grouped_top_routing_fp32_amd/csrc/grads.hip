@@ -18,10 +18,6 @@ namespace {
 constexpr int kPerLaunch = 112;  // tensors that fit a launch's 4 KB of arguments
 constexpr int kChunk = 2048;     // elements: eight to a thread
 constexpr int kUnits = 1024;     // workgroups, and partial sums, at most: sixteen waves a CU
-// Up to here one launch does it all: every workgroup adds up all squares by itself, or, where results replace
-// gradients that others still read, there is one alone.
-constexpr int64_t kAloneApart = 32768, kAloneInPlace = 16384;
-
 struct GradTable {
   GradTensor t[kPerLaunch];
   int count;
@@ -187,9 +183,12 @@ __global__ __launch_bounds__(256) void clip_grads_kernel(L list, int count, uint
 }
 
 // All of it in one launch of few chunks, one to a wave at a time, so that their latencies run beside each other (30011
-// elements 7.4 us; a chunk to a workgroup at a time took 11);
-// write: whether there are results besides the norm.
+// elements 7.4 us; a chunk to a workgroup at a time took 11): every workgroup adds up all squares by itself, or, where
+// results replace gradients that others still read, there is one alone.  write: whether there are results besides the norm.
 constexpr int kAloneWaves = 16;
+// Up to so many chunks, in place or not, and for the norm by itself, so that the norm is one and the same.  On the GPU, in
+// place, 5.5 us at 16 chunks and 6.6 above against 6.9 in two launches, but 8.9 at 31 (apart 8.3 and 8.2).
+constexpr uint32_t kAlone = 24;
 __global__ __launch_bounds__(64 * kAloneWaves) void clip_alone_kernel(Inline list, int count, uint32_t chunks, ClipArgs a,
                                                                       bool write) {
   __shared__ double s[kAloneWaves];
@@ -284,12 +283,6 @@ hipError_t launch_squares(const List& l, hipStream_t st) {
   return hipGetLastError();
 }
 
-int64_t elements(const GradTensor* t, int count) {
-  int64_t n = 0;
-  for (int i = 0; i < count; ++i) n += t[i].n;
-  return n;
-}
-
 hipError_t launch_alone(const List& l, const ClipArgs& a, bool write, int groups, hipStream_t st) {
   hipLaunchKernelGGL(clip_alone_kernel, dim3(groups), dim3(64 * kAloneWaves), 0, st, l.all, l.count, l.chunks, a, write);
   return hipGetLastError();
@@ -303,7 +296,7 @@ hipError_t launch_grad_norm(GradTensor* t, int count, double scale, void* ws, fl
   List l;
   hipError_t e = prepare(l, t, count, ws, st);
   if (e != hipSuccess) return e;
-  if (!l.laid && elements(t, count) <= kAloneInPlace)
+  if (!l.laid && l.chunks <= kAlone)
     return launch_alone(l, {scale, 0.0, 1.0, nullptr, norm}, false, 1, st);
   if ((e = launch_squares(l, st)) != hipSuccess) return e;
   hipLaunchKernelGGL(grad_norm_kernel, dim3(1), dim3(256), 0, st, l.part, l.units, scale, norm);
@@ -314,10 +307,9 @@ hipError_t launch_clip_grads(GradTensor* t, int count, const ClipArgs& a, void* 
   List l;
   hipError_t e = prepare(l, t, count, ws, st);
   if (e != hipSuccess) return e;
-  if (!l.laid && !a.norm_in) {
+  if (!l.laid && !a.norm_in && l.chunks <= kAlone) {
     const bool in_place = std::any_of(t, t + count, [](const GradTensor& k) { return k.p == k.out; });
-    if (elements(t, count) <= (in_place ? kAloneInPlace : kAloneApart))
-      return launch_alone(l, a, true, in_place ? 1 : std::max(1, (int)(l.chunks + kAloneWaves - 1) / kAloneWaves), st);
+    return launch_alone(l, a, true, in_place ? 1 : std::max(1, (int)(l.chunks + kAloneWaves - 1) / kAloneWaves), st);
   }
   if (!a.norm_in && (e = launch_squares(l, st)) != hipSuccess) return e;
   if (l.chunks == 0 && !a.norm) return hipSuccess;  // nothing to scale by a given norm, nor to write

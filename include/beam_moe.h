@@ -519,8 +519,8 @@ size_t beam_moe_grad_norm_workspace_bytes(int32_t count);
  *   scale   finite; the reciprocal of a loss scale or of a number of accumulated steps
  *   norm    fp32 out, one element on the device
  *   ws      of beam_moe_grad_norm_workspace_bytes(count)
- * Squares are summed in FP64: neither they nor their sum overflow or vanish.  0 <= count <= 2^16;
- * the norm of no elements is 0. */
+ * Squares are summed in FP64: neither they nor their sum overflow or vanish, in an order that depends on the sizes
+ * alone.  0 <= count <= 2^16; the norm of no elements is 0. */
 int beam_moe_grad_norm(int32_t count, const void* const* grads, const int32_t* types, const int64_t* sizes, float scale,
                        float* norm, void* ws, size_t ws_bytes, void* stream);
 

@@ -169,6 +169,23 @@ def test_clip_grads_by_a_given_norm():
     _clip_check(out, grads, _factor(grads, 2.0, 0.5, norm=123.5))
 
 
+def test_the_norm_is_one_whatever_the_call():
+    """Squares whose FP64 sum lies within its own rounding of a border of FP32: 24 of just below 2^-53 count beside the
+    largest or do not, by the order of the sum. Clipping in place, apart and the norm alone agree in every bit."""
+    _say("norm order")
+    c, (b, d) = 2.0 ** -26.5 * 0.99, (3.4526692e-04, 2.1562738e-07)
+    for n in (2048, 16385, 20000, 32768, 40000, 65536, 65537, 140000):
+        g = torch.zeros(n, device=DEV)
+        g[0], g[8], g[16] = 1.0, b, d
+        for i in (512, 1024, 1536):
+            g[i:i + 8] = c
+        norm = fw.beam_moe_grad_norm([g])
+        assert abs(norm.item() - 1.0) <= 2.0 ** -23
+        for grads in ([g.clone()], [g.clone(), torch.zeros(0, device=DEV)]):
+            assert torch.equal(fw.beam_moe_clip_grads(grads, 1.0, out=[torch.empty_like(t) for t in grads]), norm), n
+            assert torch.equal(fw.beam_moe_clip_grads(grads, 1.0), norm), n
+
+
 @pytest.mark.parametrize("dt,size", [(F32, 1e-30), (F32, 1e30), (BF16, 1e-30), (BF16, 1e30), (F16, 2.0 ** -20),
                                      (F16, 1e4)])
 def test_norm_of_tiny_and_huge_gradients(dt, size):
