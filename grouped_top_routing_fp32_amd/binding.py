@@ -889,7 +889,8 @@ def beam_moe_clip_grads(grads: Sequence[torch.Tensor], max_norm: float, *, scale
     if out is not None:
         os_, odev, ot, okinds, osizes, ostraight = _list_of(out, "out")
         if odev != dev or osizes != sizes or not (straight and ostraight) and any(
-                a.shape != b.shape or a.stride() != b.stride() for a, b in zip(ts, os_)):
+                not (a.is_contiguous() and b.is_contiguous()) and (a.shape != b.shape or a.stride() != b.stride())
+                for a, b in zip(ts, os_)):
             raise ValueError("out must hold a tensor of each gradient's size, on its device")
     if norm is not None and (norm.numel() != 1 or norm.dtype != _F32 or norm.device != dev):
         raise ValueError(f"norm must be one fp32 element on {dev}")

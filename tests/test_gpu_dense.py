@@ -149,6 +149,21 @@ def test_clip_grads_shapes_and_transposes():
     assert all(torch.equal(a, b) for a, b in zip(out, grads))
 
 
+def test_clip_grads_of_transposes_beside_a_flat_buffer():
+    """Each output by itself: contiguous ones of as many elements for contiguous gradients, the same strides for others."""
+    _say("clip transposes and flat")
+    g = _gen(11)
+    grads = [_randn(g, (30, 70)), _randn(g, (70, 30)).t(), _randn(g, (2, 3, 5), BF16)]
+    flat = torch.zeros(3000, device=DEV)
+    out = [flat[:2100], torch.empty_like(grads[1]), flat[2200:2230]]
+    fw.beam_moe_clip_grads(grads, 1.0, out=out)
+    _clip_check([o.reshape(t.shape) for o, t in zip(out, grads)], grads, _factor(grads, 1.0))
+    for bad in ([out[0], flat[:2100], out[2]], [out[0], torch.empty(30, 70, device=DEV), out[2]],
+                [torch.empty(70, 30, device=DEV).t(), out[1], out[2]], [flat[:2099], out[1], out[2]]):
+        with pytest.raises(ValueError):
+            fw.beam_moe_clip_grads(grads, 1.0, out=bad)
+
+
 def test_clip_grads_partly_in_place():
     _say("clip partly in place")
     for n in (300, 9000):
