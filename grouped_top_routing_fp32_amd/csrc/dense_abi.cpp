@@ -46,8 +46,9 @@ int check_grads(int32_t count, const void* const* grads, const int32_t* types, c
   return total > kMaxGradTotal ? BEAM_MOE_ERR_UNSUPPORTED : BEAM_MOE_OK;
 }
 
-// Whether every output lies apart from the other outputs and from the other gradients.
-bool apart(const std::vector<beam::GradTensor>& t) {
+// Whether every output lies apart from the other outputs and from the other gradients, the norm that is read apart from
+// the outputs, and the one that is written apart from all.
+bool apart(const std::vector<beam::GradTensor>& t, const float* norm_in, const float* norm) {
   struct Span {
     uintptr_t a, b;
     bool out;
@@ -61,6 +62,14 @@ bool apart(const std::vector<beam::GradTensor>& t) {
     return Span{p, p + k.n * elem_bytes(k.out_type), true};
   };
   auto replaced = [](const beam::GradTensor& k) { return k.p == k.out && k.type == k.out_type; };
+  auto clear = [&](const float* one, bool written) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(one);
+    auto off = [p](const Span& s) { return p + sizeof(float) <= s.a || p >= s.b; };
+    return !one || std::all_of(t.begin(), t.end(), [&](const beam::GradTensor& k) {
+      return off(out(k)) && (!written || off(grad(k)));
+    });
+  };
+  if (!clear(norm_in, false) || !clear(norm, true)) return false;
   // outputs in order, and no gradient among them, as with a flat buffer: no sorting
   uintptr_t first = UINTPTR_MAX, last = 0;
   bool ordered = true;
@@ -326,7 +335,7 @@ int beam_moe_clip_grads(int32_t count, const void* const* grads, const int32_t* 
       if (!out || reinterpret_cast<uintptr_t>(out) % elem_bytes(type) != 0) return BEAM_MOE_ERR_INVALID_ARG;
       t.push_back({grads[i], out, sizes[i], 0u, (uint8_t)types[i], (uint8_t)type});
     }
-    if (!apart(t)) return BEAM_MOE_ERR_INVALID_ARG;
+    if (!apart(t, norm_in, norm)) return BEAM_MOE_ERR_INVALID_ARG;
     const beam::ClipArgs a{scale, max_norm, eps, norm_in, norm};
     return hip_status(beam::launch_clip_grads(t.data(), (int)t.size(), a, ws, static_cast<hipStream_t>(stream)));
   } catch (const std::bad_alloc&) {

@@ -535,7 +535,8 @@ int beam_moe_grad_norm(int32_t count, const void* const* grads, const int32_t* t
  *              grads[i] with the same type, and lies apart from every other gradient and output
  *   out_types  [count] element types of outs (host), NULL = the gradients' own
  *   norm       fp32 out: the norm taken, before clipping; NULL = not written
- * Outputs that overlap, or gradients that occur twice in place, are refused.  Where the norm is infinite the
+ * Outputs that overlap, gradients that occur twice in place, norm_in inside an output and norm inside an output or a
+ * gradient are refused.  Where the norm is infinite the
  * finite gradients are 0 and the infinite ones NaN; where it is NaN, all are. */
 int beam_moe_clip_grads(int32_t count, const void* const* grads, const int32_t* types, const int64_t* sizes, float scale,
                         float max_norm, float eps, const float* norm_in, void* const* outs, const int32_t* out_types,

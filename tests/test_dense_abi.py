@@ -120,6 +120,14 @@ def test_unsupported_sizes(call, big):
     assert call(**big) == UNSUP
 
 
+@pytest.mark.parametrize("bad", [dict(norm_in=A[2]), dict(norm_in=ctypes.c_void_p(A[3].value + 24)),
+                                 dict(outs=None, out_types=None, norm_in=A[1]), dict(norm=A[0]), dict(norm=A[2]),
+                                 dict(norm=ctypes.c_void_p(A[3].value + 16)), dict(outs=None, out_types=None, norm=A[1])])
+def test_norms_inside_the_lists(bad):
+    """A norm that other workgroups overwrite while it is read, or read as a gradient while it is written."""
+    assert CLIP(**bad) == BAD
+
+
 def test_too_many_elements_in_all():
     n = 17
     args = dict(count=n, grads=ptrs(*[A[0]] * n), types=ints(*[BF16] * n), sizes=sizes(*[1 << 40] * n))
