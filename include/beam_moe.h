@@ -536,8 +536,9 @@ int beam_moe_grad_norm(int32_t count, const void* const* grads, const int32_t* t
  *   out_types  [count] element types of outs (host), NULL = the gradients' own
  *   norm       fp32 out: the norm taken, before clipping; NULL = not written
  * Outputs that overlap, gradients that occur twice in place, norm_in inside an output and norm inside an output or a
- * gradient are refused.  Where the norm is infinite the
- * finite gradients are 0 and the infinite ones NaN; where it is NaN, all are. */
+ * gradient are refused.  A norm of finite gradients that is past FP32's range is written as infinity, and they are
+ * clipped by what it is.  Where a gradient or the given norm is infinite, the finite gradients become 0 and the infinite
+ * ones NaN; where one is NaN, all do. */
 int beam_moe_clip_grads(int32_t count, const void* const* grads, const int32_t* types, const int64_t* sizes, float scale,
                         float max_norm, float eps, const float* norm_in, void* const* outs, const int32_t* out_types,
                         float* norm, void* ws, size_t ws_bytes, void* stream);
@@ -551,13 +552,15 @@ int beam_moe_clip_grads(int32_t count, const void* const* grads, const int32_t* 
  * zero codes, and reads back as NaN.
  *   x       [rows, cols] of any element type
  *   codes   [rows, 16 * ceil(cols / 32)] bytes out, ldc its row stride in bytes, a multiple of 16
- *   scales  [rows, ceil(cols / 32)] bytes out, lds its row stride in bytes
+ *   scales  [rows, ceil(cols / 32)] bytes out, lds its row stride in bytes, any; it starts on 16 bytes as
+ *           every array does
  * 0 <= rows <= 2^20, 1 <= cols <= 2^18. */
 int beam_moe_quantize_mxfp4(int32_t rows, int32_t cols, const void* x, int x_type, int64_t ldx, uint8_t* codes,
                             int64_t ldc, uint8_t* scales, int64_t lds, void* stream);
 
-/* The values of such codes, y [rows, cols] out of any element type (rounded to it once; exact in FP32, and
- * in the others where they hold the value). */
+/* The values of such codes, y [rows, cols] out of any element type, rounded to FP32 and then to it: exact in FP32 for
+ * scales up to 252, the largest that the quantisation writes besides 255, and in the others where they hold the value.
+ * A code of 4 or 6 at scale 253, and of 2 to 6 at 254, is past FP32's range and infinite. */
 int beam_moe_dequantize_mxfp4(int32_t rows, int32_t cols, const uint8_t* codes, int64_t ldc, const uint8_t* scales,
                               int64_t lds, void* y, int y_type, int64_t ldy, void* stream);
 

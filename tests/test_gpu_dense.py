@@ -386,6 +386,36 @@ def test_every_code_and_scale():
         assert torch.equal(y[:255], want[:255].to(F32).to(dt)), dt
 
 
+def test_codes_past_the_range_of_fp32():
+    """Values in 64 bits: exact up to scale 252, infinite above where they are 2^128 and more, exact elsewhere; the
+    quantisation writes no scale above 252 but 255."""
+    _say("dequantize ends")
+    scales = torch.arange(250, 255, device=DEV, dtype=torch.uint8)[:, None]
+    codes = torch.arange(16, device=DEV, dtype=torch.uint8)
+    codes = torch.cat([codes[0::2] + 16 * codes[1::2]] * 2)[None].expand(5, 16).contiguous()
+    size = torch.tensor(VALUES, dtype=torch.float64, device=DEV)
+    want = torch.cat([size, -size]).repeat(2)[None] * torch.exp2(scales.double() - 127)
+    past = want.abs() >= 2.0 ** 128
+    assert past.sum(1).tolist() == [0, 0, 0, 8, 16]
+    y = fw.beam_moe_dequantize_mxfp4((codes, scales), out_dtype=F32).double()
+    assert torch.equal(y[~past], want[~past]) and torch.equal(y[past], want[past].sign() * INF)
+    x = torch.tensor([[3.4028234e38, -1.0, 6e-39] + [0.0] * 29], device=DEV)
+    assert fw.beam_moe_quantize_mxfp4(x).scales.item() == 252
+
+
+def test_clip_grads_of_a_norm_past_fp32():
+    """Finite gradients of a norm of some 1.4e40: infinite as FP32, and clipped by its value."""
+    _say("clip past fp32")
+    for n in (20000, 200000):
+        g = torch.full((n,), 1e38, device=DEV)
+        out = [torch.empty_like(g)]
+        assert fw.beam_moe_grad_norm([g]).item() == INF
+        assert fw.beam_moe_clip_grads([g], 1e38, out=out).item() == INF
+        _clip_check(out, [g], 1 / math.sqrt(n))  # the limit is rounded to FP32 as the elements are
+        fw.beam_moe_clip_grads([g], 1e38, norm=torch.full((), INF, device=DEV), out=out)
+        assert not out[0].any()
+
+
 def test_quantize_mxfp4_infinities_and_nan():
     _say("quantize inf nan")
     for dt in (BF16, F16, F32):
