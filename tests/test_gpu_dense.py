@@ -502,6 +502,7 @@ def _gated_check(x, wg, wu, bg, bu, act, h, zg=None, zu=None):
 
 
 # the last are large enough for 256-row tiles
+# in one of the gradients' products; the forward product's are in test_gated_linear_large and GATED_TILES_256
 GATED_SHAPES = [(1, 1, 1), (1, 64, 64), (1, 100, 1000), (2, 2560, 512), (3, 17, 5), (7, 33, 2049), (16, 256, 128),
                 (17, 48, 96), (33, 1000, 136), (64, 512, 2560), (65, 130, 72), (100, 64, 7), (129, 257, 65),
                 (255, 96, 520), (256, 256, 64), (300, 513, 1024), (257, 264, 192), (520, 1040, 328), (1000, 1032, 2048),
@@ -536,6 +537,47 @@ def test_gated_linear_large(M, N, K, dt):
         h, zg, zu = out if pre else (out, None, None)
         _gated_check(x, wg, wu, bg, bu, act, h, zg, zu)
         assert (buf[:, N:] == 7.0).all()
+
+
+# 256-row tiles with K that ends inside a stage: whole and ragged chunks, the last laid out anew; rows and columns that end
+# inside a tile, and whole ones
+GATED_TILES_256 = [(4096, 2048, 328), (4000, 2043, 331), (4096, 2048, 1000), (3900, 2040, 200), (8100, 1021, 777)]
+
+
+@pytest.mark.parametrize("M,N,K", GATED_TILES_256)
+@pytest.mark.parametrize("dt", [BF16, F16])
+def test_gated_linear_large_with_a_ragged_k(M, N, K, dt):
+    for act, yt, bias, pre, pad in (("silu", dt, False, False, 0), ("gelu", F32, True, True, 8),
+                                    ("relu", dt, True, True, 3), ("none", F32, False, False, 0)):
+        _say("gated large ragged", M, N, K, dt, act, yt, bias, pre, pad)
+        _, x, wg, wu, bg, bu = _gated_inputs(M, N, K, dt, pad, bias)
+        buf = torch.full((M, N + 8), 7.0, dtype=yt, device=DEV)
+        out = fw.beam_moe_gated_linear(x, wg, wu, bg, bu, act=act, out=buf[:, :N], want_pre=pre)
+        h, zg, zu = out if pre else (out, None, None)
+        _gated_check(x, wg, wu, bg, bu, act, h, zg, zu)
+        assert (buf[:, N:] == 7.0).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 70, 65), (100, 130, 72), (200, 131, 71), (300, 150, 16384), (4096, 2048, 328),
+                                   (4000, 2043, 192), (4096, 2048, 192)])
+@pytest.mark.parametrize("dt", [BF16, F16])
+def test_gated_linear_pre_into_wider_buffers(M, N, K, dt):
+    """The C entry point's strided pre, each with a stride of its own: the binding's bits, and nothing behind the rows."""
+    _say("gated strided pre", M, N, K, dt)
+    lib = fw.load_library()
+    _, x, wg, wu, bg, bu = _gated_inputs(M, N, K, dt)
+    h, zg, zu = fw.beam_moe_gated_linear(x, wg, wu, bg, bu, want_pre=True)
+    ws = torch.empty(lib.beam_moe_gated_linear_workspace_bytes(M, N, K, K, K, K) + 16, dtype=torch.uint8, device=DEV)
+    for both in ((True, True), (True, False), (False, True)):
+        bufs = [torch.full((M, N + p), 7.0, dtype=dt, device=DEV) for p in (3, 5, 8)]
+        pre = [(b.data_ptr() if w else None, b.shape[1]) for b, w in zip(bufs[1:], both)]
+        status = lib.beam_moe_gated_linear(M, N, K, fw.ELEM_TYPES[dt], x.data_ptr(), K, wg.data_ptr(), K, wu.data_ptr(), K,
+                                           bg.data_ptr(), bu.data_ptr(), fw.ACTIVATIONS["silu"], bufs[0].data_ptr(),
+                                           fw.ELEM_TYPES[dt], N + 3, *pre[0], *pre[1], ws.data_ptr(), ws.numel(),
+                                           torch.cuda.current_stream().cuda_stream)
+        assert status == 0
+        for b, want, wrote in zip(bufs, (h, zg, zu), (True, *both)):
+            assert (b[:, N:] == 7.0).all() and (torch.equal(b[:, :N], want) if wrote else (b == 7.0).all())
 
 
 @pytest.mark.parametrize("M,N,K", [(100, 50, 65536), (300, 150, 16384), (512, 256, 9216), (20, 100, 2050)])
@@ -894,6 +936,42 @@ def test_gated_linear_offsets_past_32_bits():
     assert not h[:100].any()
 
 
+# a row stride in 256-row tiles just inside the persistent kernel's bound, and past it
+@pytest.mark.parametrize("ld", [(1 << 22) - 8, 1 << 22])
+@pytest.mark.parametrize("M,N,K", [(520, 16384, 192), (13056, 640, 192)])
+def test_gated_linear_of_far_rows(M, N, K, ld):
+    """Rows of x, or of both weights, that span more than 2^31 elements."""
+    _say("gated far rows", M, N, K, ld)
+    g, x, wg, wu, bg, bu = _gated_inputs(M, N, K, BF16)
+    far = torch.zeros(min(M, N), ld, dtype=BF16, device=DEV)
+    assert far.numel() > 1 << 31
+    if M < N:
+        far[:, :K] = x
+        x = far[:, :K]
+    else:
+        far[:, :K], far[:, 1 << 21:(1 << 21) + K] = wg, wu
+        wg, wu = far[:, :K], far[:, 1 << 21:(1 << 21) + K]
+    h, zg, zu = fw.beam_moe_gated_linear(x, wg, wu, bg, bu, want_pre=True)
+    _gated_check(x, wg, wu, bg, bu, "silu", h, zg, zu)
+
+
+@pytest.mark.parametrize("M,N,K", [(600, 72, 136), (600, 71, 131)])
+@pytest.mark.parametrize("dt", [BF16, F16])
+def test_gated_linear_backward_of_far_rows(M, N, K, dt):
+    _say("gated backward far rows", M, N, K, dt)
+    g, x, wg, wu, _, _ = _gated_inputs(M, N, K, dt)
+    rows, cols = (torch.zeros(*s, dtype=dt, device=DEV) for s in ((M, 1 << 22), (N, 1 << 25)))
+    assert min(rows.numel(), cols.numel()) > 1 << 31
+    parts = []
+    for k, (buf, t) in enumerate(((rows, _randn(g, (M, N), dt)), (rows, _randn(g, (M, N), dt)), (rows, _randn(g, (M, N), dt)),
+                                  (rows, x), (cols, wg), (cols, wu))):
+        view = buf[:, 4096 * k:4096 * k + t.shape[1]]
+        view.copy_(t)
+        parts.append(view)
+    dh, zg, zu, x, wg, wu = parts
+    _gated_back_check(dh, x, wg, wu, zg, zu, "silu", fw.beam_moe_gated_linear_backward(dh, x, wg, wu, zg, zu))
+
+
 # --------------------------------------------------------------------------
 # the product of 4-bit operands
 # --------------------------------------------------------------------------
@@ -1128,3 +1206,41 @@ def test_serving_a_gated_sublayer_in_four_bits():
         want = 0.8 * s["stream"].double() + 0.6 * (h @ w["wd"].t())
         err = float((out.double() - want).norm() / want.norm())
         assert err <= 8 * 2.0 ** -9, (T, err)
+
+
+# strides of codes just inside the persistent kernel's bound, and past it
+@pytest.mark.parametrize("ld", [(1 << 23) - 16, 1 << 23])
+@pytest.mark.parametrize("M,N,K", [(520, 16384, 2560), (16384, 520, 2560)])
+def test_linear_mxfp4_of_two_with_far_rows(M, N, K, ld):
+    """Codes whose rows span more than 2^32 bytes."""
+    _say("linear_mxfp4 far rows", M, N, K, ld)
+    g = _gen(M + N)
+    x, w = _mx_weights(g, M, K, 0, 3), _mx_weights(g, N, K)
+    far = torch.zeros(min(M, N), ld, dtype=torch.uint8, device=DEV)
+    assert far.numel() > 1 << 32
+    q = x if M < N else w
+    far[:, : K // 2] = q.codes
+    q = fw.Mxfp4(far[:, : K // 2], q.scales)
+    x, w = (q, w) if M < N else (x, q)
+    need = fw.load_library().beam_moe_linear_mxfp4_workspace_bytes(M, N, K, 3, x.codes.stride(0), w.codes.stride(0))
+    assert (need > 0) == (ld < 1 << 23)
+    y = fw.beam_moe_linear_mxfp4(x, w, out_dtype=F32)
+    _mx_linear_check(_mx_values(x, K), _mx_values(w, K), None, "none", None, 1.0, 1.0, y)
+
+
+# the kernel for few rows, tiles that hold codes, codes through registers, and w laid out as x's type
+@pytest.mark.parametrize("M,K", [(8, 2560), (64, 2560), (64, 2557), (3000, 2560)])
+def test_linear_mxfp4_with_far_rows(M, K):
+    """Weights whose codes span more than 2^32 bytes, and rows of x more than 2^31 elements."""
+    N = 520
+    _say("linear_mxfp4 far rows", M, N, K)
+    g = _gen(M + K)
+    w, x0 = _mx_weights(g, N, K), _randn(g, (M, K), BF16)
+    far = torch.zeros(N, 1 << 23, dtype=torch.uint8, device=DEV)
+    wide = torch.zeros(M, -(-(9 << 28) // M // 8) * 8, dtype=BF16, device=DEV)
+    assert far.numel() > 1 << 32 and wide.numel() > 1 << 31
+    far[:, : w.codes.shape[1]] = w.codes
+    wide[:, :K] = x0
+    w = fw.Mxfp4(far[:, : w.codes.shape[1]], w.scales)
+    y = fw.beam_moe_linear_mxfp4(wide[:, :K], w, out_dtype=F32)
+    _mx_linear_check(x0.double(), _mx_values(w, K), None, "none", None, 1.0, 1.0, y)
