@@ -7,7 +7,7 @@
 // to registers ([1, 5120] x [2560, 5120], 7 MB, 6.5 us, of which some 5 are a launch and one trip to memory).
 // With both operands in 4 bits the products run on scaled matrix instructions, four times the 16-bit rate for the
 // same bytes in LDS: small ones in the tiled product, large ones in a persistent kernel ([16384, 2560] x [5120,
-// 2560] 149 us, 2.9 PFLOP/s).  With x of 16 bits, some rows go through tiles that hold codes in LDS and turn them into
+// 2560] 123 to 131 us in calls, 3.3 to 3.5 PFLOP/s).  With x of 16 bits, some rows go through tiles that hold codes in LDS and turn them into
 // x's type on their way to the matrix instructions ([64, 2560] x [5120, 2560] 9.8 us and 4.0 for the join of its splits;
 // [64, 5120] x [32768, 5120] 39 us, 2.3 TB/s of codes and scales).  Where rows are no whole chunks, products of few
 // tiles do so on the codes' way into LDS; larger ones lay w out as x's type in the workspace first and run the plain

@@ -16,9 +16,13 @@
 //   instructions' words, so that a stage's are 4 KB in a row (as they lie, a row's eight bytes to a cache line,
 //   they took a third as long as the codes).
 // - Results leave from registers, and the next tile's first stages are requested before.
-// What bounds it is power: [16384, 2560] x [5120, 2560] in 4 bits takes 149 us, the matrix cores 31% busy at 2.17 GHz, of
-// which the results' stores are 25 to 30 us; at 8192^3 (260 us, 4.2 PFLOP/s; 300 in the tiled product) they are
-// 53% busy at 1.87, and [16384, 5120] x [2560, 5120] of a gated layer in bf16 (670 us, 1280 TFLOP/s) 59% at 1.66.
+// A stage of 4-bit operands takes 1.8 us, and 6 us lie between the last stage of one tile and the first of the next (calls
+// with K of 512 to 10240 at [16384, K] x [5120, K]): twice the 0.94 us of its matrix instructions, so there it is bound by
+// its feeding and, with a short K, by the epilogues.  [16384, 2560] x [5120, 2560] takes 123 to 131 us in calls (3.3 to 3.5
+// PFLOP/s), of which the results' stores are 25 to 30; under the profiler, with inputs out of memory, 149, the matrix cores
+// 31% busy at 2.17 GHz.  The largest products run into power, busy times clock near 1 GHz: 53% at 1.87 GHz at 8192^3 (260
+// us, 4.2 PFLOP/s; 300 in the tiled product), 59% at 1.66 for [16384, 5120] x [2560, 5120] of a gated layer in bf16 (670 us
+// in calls, 1280 TFLOP/s).
 // A tile of a gated layer has 16 rows of one weight and 16 of the other in turn, 128 columns of the result.
 #pragma once
 
